@@ -1,0 +1,316 @@
+"""Layer operators that produce the gradients the optimizer exchanges: layer norm, the linear layer with
+a fused epilogue, and activation checkpoints held in 8 bits, forward and backward.
+
+Thin Python binding over the C ABI in ``include/onebit_layers.h`` (the formulas are stated there); every
+operator runs in the library's CUDA kernels on the current torch stream, or on ``stream``.
+
+Matrices are CUDA tensors whose last dimension is the features and has unit stride.  A 2-D tensor may
+have any row stride (a column slice of a wider buffer); one of more dimensions must be contiguous and
+counts as its leading dimensions' rows.  Gradients come in ``grad_dtype``, the type ``OneBitAdam`` was
+configured with, and may be written into the caller's tensors (``dw=``, ``db=``).
+
+    y = W2 gelu(W1 x + b1) + b2 + x, then layer norm, with 8-bit checkpoints:
+
+    h, z8 = layers.linear(x, w1, b1, layers.ACT_GELU, checkpoint=True)
+    s = layers.linear(h, w2, b2, residual=x)
+    y, mean, rstd, s8 = layers.layer_norm(s, gamma, beta, 1e-12, checkpoint=True)
+    ds, dgamma, dbeta = layers.layer_norm_backward(dy, s8, gamma, mean, rstd)
+    dz, dw2, db2 = layers.linear_backward(ds, z8, w2, layers.ACT_GELU)
+    dx, dw1, db1 = layers.linear_backward(dz, x, w1, add=ds)
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple
+
+import torch
+
+from . import BF16, F16, F32, OK, OneBitError, lib
+
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH = range(4)
+ACTIVATIONS = {"none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH}
+CHECKPOINT_BLOCK = 64  # columns of a row that share one scale
+
+_DTYPE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+
+
+class Checkpoint(NamedTuple):
+    """A matrix in 8 bits: int8 ``codes`` of its shape, fp32 ``scales`` with one value per 64 columns of
+    a row, and the ``dtype`` of the matrix it stands for."""
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+    dtype: torch.dtype
+
+
+class LinearArgs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("w", ctypes.c_void_p), ("ldw", ctypes.c_int64),
+                ("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+                ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64), ("in_", ctypes.c_int64),
+                ("out", ctypes.c_int64), ("dtype", ctypes.c_int32), ("activation", ctypes.c_int32)]
+
+
+class LinearGradArgs(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("w", ctypes.c_void_p),
+                ("ldw", ctypes.c_int64), ("add", ctypes.c_void_p), ("ldadd", ctypes.c_int64),
+                ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64), ("dw", ctypes.c_void_p), ("db", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("in_", ctypes.c_int64), ("out", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("activation", ctypes.c_int32), ("grad_dtype", ctypes.c_int32)]
+
+
+_fn = None
+
+
+def _functions():
+    """The C entries, with their argument types set on first use."""
+    global _fn
+    if _fn is None:
+        L = lib()
+        vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+        sig = {
+            "onebit_checkpoint_compress": [vp, i64, i32, i64, i64, vp, vp, vp],
+            "onebit_checkpoint_restore": [vp, vp, i64, i64, i32, vp, i64, i32, vp],
+            "onebit_layer_norm_forward": [vp, i64, i32, i64, i64, vp, vp, ctypes.c_float, vp, i64, vp, vp, vp, vp, vp],
+            "onebit_layer_norm_backward_workspace": [i64, i64, ctypes.POINTER(sz)],
+            "onebit_layer_norm_backward": [vp, i64, vp, i64, vp, vp, i32, i64, i64, vp, vp, vp, vp, i64, vp, i64, vp, vp,
+                                           i32, vp, sz, vp],
+            "onebit_linear_forward_workspace": [ctypes.POINTER(LinearArgs), ctypes.POINTER(sz)],
+            "onebit_linear_forward": [ctypes.POINTER(LinearArgs), vp, sz, vp],
+            "onebit_linear_backward_workspace": [ctypes.POINTER(LinearGradArgs), ctypes.POINTER(sz)],
+            "onebit_linear_backward": [ctypes.POINTER(LinearGradArgs), vp, sz, vp],
+        }
+        for name, args in sig.items():
+            f = getattr(L, name)
+            f.argtypes = args
+            f.restype = ctypes.c_int
+        L.onebit_layers_last_error.argtypes = []
+        L.onebit_layers_last_error.restype = ctypes.c_char_p
+        _fn = L
+    return _fn
+
+
+def _check(status: int, where: str):
+    if status != OK:
+        raise OneBitError(status, where, _functions().onebit_layers_last_error().decode())
+
+
+def _code(dtype, what: str) -> int:
+    try:
+        return _DTYPE[dtype]
+    except KeyError:
+        raise ValueError(f"{what}: dtype {dtype} is not float32, float16 or bfloat16") from None
+
+
+def _matrix(t, name: str, cols=None, rows=None, dtype=None, device=None):
+    """(rows, columns, row stride) of a tensor whose last dimension is the features."""
+    shape = t.shape
+    if not t.is_cuda or t.dim() < 1:
+        raise ValueError(f"{name}: expected a CUDA tensor of at least one dimension")
+    c = shape[-1]
+    if t.dim() == 2:
+        r = shape[0]
+        ld, unit = t.stride()
+        if (c > 1 and unit != 1) or (r > 1 and ld < c):
+            raise ValueError(f"{name}: the last dimension needs unit stride and rows that do not overlap")
+        if r <= 1 or ld < c:
+            ld = c
+    else:
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: a tensor that is not 2-D must be contiguous")
+        r, ld = (t.numel() // c if c else 0), c
+    if c < 1:
+        raise ValueError(f"{name}: no columns")
+    if cols is not None and c != cols:
+        raise ValueError(f"{name}: expected {cols} columns, got {c}")
+    if rows is not None and r != rows:
+        raise ValueError(f"{name}: expected {rows} rows, got {r}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+    return r, c, ld
+
+
+def _vector(t, name: str, n: int, device, dtype=torch.float32):
+    """Pointer of a contiguous vector of n values (None: 0)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name}: expected {n} contiguous {dtype} values on {device}")
+    return t.data_ptr()
+
+
+def _kept(x, name: str, cols=None, rows=None, dtype=None, device=None):
+    """(x pointer, row stride, codes pointer, scales pointer, rows, columns, dtype, device, shape) of a
+    layer's kept input: a tensor or its Checkpoint."""
+    if not isinstance(x, Checkpoint):
+        r, c, ld = _matrix(x, name, cols, rows, dtype, device)
+        return x.data_ptr(), ld, None, None, r, c, x.dtype, x.device, x.shape
+    if dtype is not None and x.dtype != dtype:
+        raise ValueError(f"{name}: expected a checkpoint of {dtype}, got one of {x.dtype}")
+    codes = x.codes
+    r, c, ld = _matrix(codes, name + ".codes", cols, rows, torch.int8, device)
+    if r > 1 and ld != c:
+        raise ValueError(f"{name}.codes: a checkpoint is contiguous")
+    blocks = -(-c // CHECKPOINT_BLOCK)
+    s = _vector(x.scales, name + ".scales", r * blocks, codes.device)
+    return None, 0, codes.data_ptr(), s, r, c, x.dtype, codes.device, codes.shape
+
+
+class _On:
+    """Runs the body with `stream` current (None: as is), so that its outputs and workspace belong to it."""
+
+    __slots__ = ("ctx",)
+
+    def __init__(self, stream):
+        self.ctx = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _stream(device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _new_checkpoint(shape, dtype, device):
+    blocks = -(-shape[-1] // CHECKPOINT_BLOCK)
+    return Checkpoint(torch.empty(shape, dtype=torch.int8, device=device),
+                      torch.empty((*shape[:-1], blocks), dtype=torch.float32, device=device), dtype)
+
+
+def _workspace(nbytes: int, device):
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def compress(x, stream=None) -> Checkpoint:
+    """The 8-bit checkpoint of x."""
+    rows, cols, ld = _matrix(x, "x")
+    code = _code(x.dtype, "x")
+    with _On(stream):
+        ck = _new_checkpoint(x.shape, x.dtype, x.device)
+        _check(_functions().onebit_checkpoint_compress(x.data_ptr(), ld, code, rows, cols, ck.codes.data_ptr(),
+                                                       ck.scales.data_ptr(), _stream(x.device)),
+               "onebit_checkpoint_compress")
+    return ck
+
+
+def restore(ck: Checkpoint, activation=ACT_NONE, stream=None):
+    """activation(the values a checkpoint stands for), in the checkpoint's dtype."""
+    _, _, codes, scales, rows, cols, dtype, device, shape = _kept(ck, "ck")
+    code = _code(dtype, "ck")
+    with _On(stream):
+        x = torch.empty(shape, dtype=dtype, device=device)
+        _check(_functions().onebit_checkpoint_restore(codes, scales, rows, cols, activation, x.data_ptr(), cols, code,
+                                                      _stream(device)), "onebit_checkpoint_restore")
+    return x
+
+
+def layer_norm(x, gamma, beta, eps=1e-5, checkpoint=False, stream=None):
+    """(y, mean, rstd), and the 8-bit checkpoint of x where asked for."""
+    rows, cols, ld = _matrix(x, "x")
+    code, device = _code(x.dtype, "x"), x.device
+    g, b = _vector(gamma, "gamma", cols, device), _vector(beta, "beta", cols, device)
+    with _On(stream):
+        y = torch.empty(x.shape, dtype=x.dtype, device=device)
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
+        ck = _new_checkpoint(x.shape, x.dtype, device) if checkpoint else None
+        _check(_functions().onebit_layer_norm_forward(
+            x.data_ptr(), ld, code, rows, cols, g, b, eps, y.data_ptr(), cols, mean.data_ptr(), rstd.data_ptr(),
+            ck.codes.data_ptr() if ck else None, ck.scales.data_ptr() if ck else None, _stream(device)),
+            "onebit_layer_norm_forward")
+    return (y, mean, rstd, ck) if checkpoint else (y, mean, rstd)
+
+
+def layer_norm_backward(dy, x, gamma, mean, rstd, add=None, grad_dtype=torch.float32, stream=None):
+    """(dx, dgamma, dbeta) from the layer's input x, a tensor or its Checkpoint; ``add`` joins dx."""
+    rows, cols, lddy = _matrix(dy, "dy")
+    code, gcode, device = _code(dy.dtype, "dy"), _code(grad_dtype, "grad_dtype"), dy.device
+    xp, ldx, codes, scales, *_ = _kept(x, "x", cols, rows, dy.dtype, device)
+    g = _vector(gamma, "gamma", cols, device)
+    mu, rs = _vector(mean, "mean", rows, device), _vector(rstd, "rstd", rows, device)
+    ap, lda = (add.data_ptr(), _matrix(add, "add", cols, rows, dy.dtype, device)[2]) if add is not None else (None, 0)
+    fn, need = _functions(), ctypes.c_size_t()
+    with _On(stream):
+        dx = torch.empty(dy.shape, dtype=dy.dtype, device=device)
+        dgamma = torch.empty(cols, dtype=grad_dtype, device=device)
+        dbeta = torch.empty(cols, dtype=grad_dtype, device=device)
+        _check(fn.onebit_layer_norm_backward_workspace(rows, cols, ctypes.byref(need)),
+               "onebit_layer_norm_backward_workspace")
+        ws = _workspace(need.value, device)
+        _check(fn.onebit_layer_norm_backward(
+            dy.data_ptr(), lddy, xp, ldx, codes, scales, code, rows, cols, g, mu, rs, ap, lda, dx.data_ptr(), cols,
+            dgamma.data_ptr(), dbeta.data_ptr(), gcode, ws.data_ptr() if ws is not None else None, need.value,
+            _stream(device)), "onebit_layer_norm_backward")
+    return dx, dgamma, dbeta
+
+
+def linear(x, w, bias=None, activation=ACT_NONE, residual=None, checkpoint=False, stream=None):
+    """y = activation(x w^T + bias) + residual; with ``checkpoint`` (y, the 8-bit checkpoint of x w^T + bias)."""
+    rows, cols, ldx = _matrix(x, "x")
+    dtype, device = x.dtype, x.device
+    code = _code(dtype, "x")
+    if w.dim() != 2:
+        raise ValueError("w: expected out x in")
+    out, _, ldw = _matrix(w, "w", cols, None, dtype, device)
+    bp = _vector(bias, "bias", out, device)
+    rp, ldr = (residual.data_ptr(), _matrix(residual, "residual", out, rows, dtype, device)[2]) if residual is not None else (None, 0)
+    shape = (*x.shape[:-1], out)
+    fn, need = _functions(), ctypes.c_size_t()
+    with _On(stream):
+        y = torch.empty(shape, dtype=dtype, device=device)
+        ck = _new_checkpoint(shape, dtype, device) if checkpoint else None
+        a = LinearArgs(x.data_ptr(), ldx, w.data_ptr(), ldw, bp, rp, ldr, y.data_ptr(), out,
+                       ck.codes.data_ptr() if ck else None, ck.scales.data_ptr() if ck else None, rows, cols, out, code,
+                       activation)
+        _check(fn.onebit_linear_forward_workspace(a, need), "onebit_linear_forward_workspace")
+        ws = _workspace(need.value, device)
+        _check(fn.onebit_linear_forward(a, ws.data_ptr() if ws is not None else None, need.value, _stream(device)),
+               "onebit_linear_forward")
+    return (y, ck) if checkpoint else y
+
+
+def linear_backward(dy, x, w, activation=ACT_NONE, add=None, grad_dtype=None, dw=None, db=None, need=("dx", "dw", "db"),
+                    stream=None):
+    """(dx, dw, db) of y = activation(x) w^T + bias, given dy: x is the value before the activation that
+    precedes the product (with ACT_NONE the product's input), a tensor or its Checkpoint; ``add`` joins
+    dx.  grad_dtype (default dy's) is the type of dw (out x in) and db; ``dw`` and ``db`` may be the
+    caller's contiguous tensors.  What ``need`` leaves out is None."""
+    rows, out, lddy = _matrix(dy, "dy")
+    dtype, device = dy.dtype, dy.device
+    code = _code(dtype, "dy")
+    grad_dtype = dtype if grad_dtype is None else grad_dtype
+    gcode = _code(grad_dtype, "grad_dtype")
+    if w.dim() != 2:
+        raise ValueError("w: expected out x in")
+    _, cols, ldw = _matrix(w, "w", None, out, dtype, device)
+    xp, ldx, codes, scales = None, 0, None, None
+    if x is not None:
+        xp, ldx, codes, scales, *_ = _kept(x, "x", cols, rows, dtype, device)
+    ap, lda = (add.data_ptr(), _matrix(add, "add", cols, rows, dtype, device)[2]) if add is not None else (None, 0)
+    want_dx, want_dw, want_db = "dx" in need, "dw" in need, "db" in need
+    fn, bytes_ = _functions(), ctypes.c_size_t()
+    with _On(stream):
+        dx = torch.empty((*dy.shape[:-1], cols), dtype=dtype, device=device) if want_dx else None
+        if want_dw and dw is None:
+            dw = torch.empty((out, cols), dtype=grad_dtype, device=device)
+        if want_db and db is None:
+            db = torch.empty(out, dtype=grad_dtype, device=device)
+        a = LinearGradArgs(dy.data_ptr(), lddy, xp, ldx, codes, scales, w.data_ptr(), ldw, ap, lda,
+                           dx.data_ptr() if want_dx else None, cols,
+                           _vector(dw, "dw", out * cols, device, grad_dtype) if want_dw else None,
+                           _vector(db, "db", out, device, grad_dtype) if want_db else None,
+                           rows, cols, out, code, activation, gcode)
+        _check(fn.onebit_linear_backward_workspace(a, bytes_), "onebit_linear_backward_workspace")
+        ws = _workspace(bytes_.value, device)
+        _check(fn.onebit_linear_backward(a, ws.data_ptr() if ws is not None else None, bytes_.value, _stream(device)),
+               "onebit_linear_backward")
+    return dx, (dw if want_dw else None), (db if want_db else None)
