@@ -19,8 +19,10 @@ LIB = os.path.join(HERE, "libonebit_adam.so")
 LIB_CHECKED = os.path.join(HERE, "libonebit_adam_checked.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 
-SOURCES = ["onebit_adam.cu", "onebit_noalloc.cu", "activation_checkpoint.cu", "layer_norm.cu", "linear.cu"]
-HEADERS = ["onebit_kernels.cuh", "layers_common.cuh", os.path.join("..", "..", "include", "onebit_adam.h"),
+SOURCES = ["onebit_adam.cu", "onebit_noalloc.cu", "activation_checkpoint.cu", "layer_norm.cu", "tensor_product.cu",
+           "linear_forward.cu", "linear_backward.cu"]
+HEADERS = ["onebit_kernels.cuh", "layers_common.cuh", "tensor_product.cuh", "linear_common.cuh",
+           os.path.join("..", "..", "include", "onebit_adam.h"),
            os.path.join("..", "..", "include", "onebit_layers.h")]
 
 NVCC_FLAGS = [

@@ -1,0 +1,198 @@
+// linear_backward.cu -- the linear layer's backward pass: dx through the derivative of the activation
+// before the product, dw and db.  See include/onebit_layers.h for the formulas.
+#include "linear_common.cuh"
+
+namespace onebit {
+namespace layers {
+namespace {
+
+// dx = (the product) * act'(v) [+ add] over the partial sums of a cut contraction, and h = act(v)
+template <typename T>
+__global__ void __launch_bounds__(256) k_finish_dx(Partials c, int64_t rows, int cols, Kept<T> v, int act, const T* __restrict__ add,
+                                                   int64_t ldadd, T* __restrict__ dx, int64_t lddx, T* __restrict__ h, int64_t ldh) {
+  const int64_t total = rows * cols;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / cols;
+    const int col = (int)(i - r * cols);
+    float d = c.at(r, col);
+    if (act != ONEBIT_ACT_NONE || h) {
+      const float z = v.at(r, col);
+      d *= act_slope(act, z);
+      if (h) h[r * ldh + col] = from_f<T>(act_value(act, z));
+    }
+    if (add) d += to_f(add[r * ldadd + col]);
+    dx[r * lddx + col] = from_f<T>(d);
+  }
+}
+
+// h = act(v), rounded to the product's operand type, where dx is not computed beside it
+template <typename T>
+__global__ void __launch_bounds__(256) k_operand(Kept<T> v, int64_t rows, int cols, int act, T* __restrict__ h, int64_t ldh) {
+  const int64_t total = rows * cols;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / cols;
+    const int col = (int)(i - r * cols);
+    h[r * ldh + col] = from_f<T>(act_value(act, v.at(r, col)));
+  }
+}
+
+// dw over the partial sums of a cut contraction
+template <typename G>
+__global__ void __launch_bounds__(256) k_finish_dw(Partials c, int64_t rows, int cols, G* __restrict__ dw) {
+  const int64_t total = rows * cols;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / cols;
+    dw[i] = from_f<G>(c.at(r, (int)(i - r * cols)));
+  }
+}
+
+// Column sums: part[chunk][cols] over runs of kRun rows, then their sum in chunk order.
+constexpr int kRun = 128;
+template <typename T>
+__global__ void __launch_bounds__(256) k_colsum_part(const T* __restrict__ dy, int64_t lddy, int64_t rows, int cols,
+                                                     float* __restrict__ part) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= cols) return;
+  for (int64_t ch = blockIdx.y; ch * kRun < rows; ch += gridDim.y) {
+    const int64_t end = (ch + 1) * kRun < rows ? (ch + 1) * kRun : rows;
+    float b = 0.0f;
+    for (int64_t r = ch * kRun; r < end; ++r) b += to_f(dy[r * lddy + c]);
+    part[ch * cols + c] = b;
+  }
+}
+template <typename G>
+__global__ void __launch_bounds__(256) k_colsum_sum(const float* __restrict__ part, int64_t chunks, int cols,
+                                                    G* __restrict__ db) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= cols) return;
+  float b = 0.0f;
+  for (int64_t ch = 0; ch < chunks; ++ch) b += part[ch * cols + c];
+  db[c] = from_f<G>(b);
+}
+
+// Takes the workspace; with `run`, enqueues the work too.
+template <typename T>
+cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, bool run) {
+  const int sms = sm_count();
+  const ProductShape sx{a.rows, a.in, a.out}, sw{a.out, a.in, a.rows};
+  const Kept<T> v{static_cast<const T*>(a.x), a.ldx, a.codes, a.scales, (int)a.in, (int)ceil_div(a.in, kBlock)};
+  const bool computed = a.dw && (a.codes || a.activation != ONEBIT_ACT_NONE);  // act(v) is not in memory yet
+  const int64_t ldh = pad8(a.in);
+  T* h = computed ? ws.take<T>(a.rows * ldh) : nullptr;
+  Operand dy{a.dy, a.lddy};
+  if (a.dx || a.dw) dy = readable(ws, a.dy, a.lddy, a.rows, a.out, s, run);
+  cudaError_t err = cudaSuccess;
+  if (a.dx) {
+    const ProductPlan plan = plan_product(sx, sms);
+    const Operand w = readable(ws, a.w, a.ldw, a.out, a.in, s, run);
+    const Partials part = take_partials(ws, plan, a.rows, a.in);
+    const T* add = static_cast<const T*>(a.add);
+    if (run && plan.splits == 1) {
+      const InputGradEpilogue<T> e{v.x, a.ldx, a.codes, a.scales, v.blocks, add, a.ldadd, static_cast<T*>(a.dx), a.lddx, h, ldh, a.activation,
+                                   vec16(v.x, a.ldx), aligned(a.codes, 16) && a.in % 16 == 0, vec16(add, a.ldadd), vec16(a.dx, a.lddx)};
+      err = run_product<false, true>(a.dtype, dy, w, sx, plan, e, s);
+    } else if (run) {
+      err = run_product<false, true>(a.dtype, dy, w, sx, plan, to_partials(part), s);
+      k_finish_dx<T><<<flat_grid(a.rows * a.in, 256), 256, 0, s>>>(part, a.rows, (int)a.in, v, a.activation, add, a.ldadd,
+                                                                   static_cast<T*>(a.dx), a.lddx, h, ldh);
+    }
+    if (err != cudaSuccess) return err;
+  } else if (computed && run) {
+    k_operand<T><<<flat_grid(a.rows * a.in, 256), 256, 0, s>>>(v, a.rows, (int)a.in, a.activation, h, ldh);
+  }
+  if (a.dw) {
+    const ProductPlan plan = plan_product(sw, sms);
+    const Operand x = computed ? Operand{h, ldh} : readable(ws, a.x, a.ldx, a.rows, a.in, s, run);
+    const Partials part = take_partials(ws, plan, a.out, a.in);
+    if (run)
+      with_grad(a.grad_dtype, a.dw, [&](auto* g) {
+        using G = std::remove_pointer_t<decltype(g)>;
+        if (plan.splits == 1) {
+          const PlainEpilogue<G> e{g, a.in, 0, aligned(g, 16) && a.in % (16 / (int64_t)sizeof(G)) == 0};
+          err = run_product<true, true>(a.dtype, dy, x, sw, plan, e, s);
+        } else {
+          err = run_product<true, true>(a.dtype, dy, x, sw, plan, to_partials(part), s);
+          k_finish_dw<<<flat_grid(a.out * a.in, 256), 256, 0, s>>>(part, a.out, (int)a.in, g);
+        }
+      });
+    if (err != cudaSuccess) return err;
+  }
+  if (a.db) {
+    const int64_t chunks = ceil_div(a.rows, kRun);
+    float* part = ws.take<float>(chunks * a.out);
+    if (run) {
+      const unsigned cgrid = (unsigned)ceil_div(a.out, 256);
+      k_colsum_part<T><<<dim3(cgrid, (unsigned)(chunks < 65535 ? chunks : 65535)), 256, 0, s>>>(static_cast<const T*>(a.dy), a.lddy, a.rows,
+                                                                                                (int)a.out, part);
+      with_grad(a.grad_dtype, a.db, [&](auto* g) { k_colsum_sum<<<cgrid, 256, 0, s>>>(part, chunks, (int)a.out, g); });
+    }
+  }
+  return cudaGetLastError();
+}
+cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, bool run) {
+  return a.dtype == ONEBIT_F16 ? backward<__half>(a, ws, s, run) : backward<__nv_bfloat16>(a, ws, s, run);
+}
+
+onebit_status_t backward_ok(const onebit_linear_grad_t* a) {
+  if (!a) return fail(ONEBIT_ERR_INVALID_ARG, "the arguments are NULL");
+  onebit_status_t st = linear_shape_ok(a->rows, a->in, a->out, a->dtype, a->activation);
+  if (st != ONEBIT_OK) return st;
+  if (!dtype_ok(a->grad_dtype)) return fail(ONEBIT_ERR_INVALID_ARG, "grad_dtype is not one of f32, f16, bf16");
+  if (!a->codes != !a->scales) return fail(ONEBIT_ERR_INVALID_ARG, "a checkpoint needs codes and scales");
+  if (a->x && a->codes) return fail(ONEBIT_ERR_INVALID_ARG, "the input is x or its checkpoint, not both");
+  if (a->lddy < a->out || (a->x && a->ldx < a->in) || (a->dx && (a->ldw < a->in || a->lddx < a->in || (a->add && a->ldadd < a->in))))
+    return fail(ONEBIT_ERR_INVALID_ARG, "a row stride below the columns");
+  if (a->rows > 0) {
+    if ((a->dx || a->dw || a->db) && !a->dy) return fail(ONEBIT_ERR_INVALID_ARG, "a NULL buffer");
+    if (a->dx && !a->w) return fail(ONEBIT_ERR_INVALID_ARG, "dx needs the weight");
+    if ((a->dw || (a->dx && a->activation != ONEBIT_ACT_NONE)) && !a->x && !a->codes)
+      return fail(ONEBIT_ERR_INVALID_ARG, "dw and the activation's derivative need x or its checkpoint");
+  }
+  const uintptr_t g = (uintptr_t)dtype_size(a->grad_dtype);
+  if (!aligned(a->dy, 2) || !aligned(a->x, 2) || !aligned(a->w, 2) || !aligned(a->add, 2) || !aligned(a->dx, 2) ||
+      !aligned(a->scales, 4) || !aligned(a->dw, g) || !aligned(a->db, g))
+    return fail(ONEBIT_ERR_INVALID_ARG, "a buffer is not aligned to its type");
+  return ONEBIT_OK;
+}
+
+}  // namespace
+}  // namespace layers
+}  // namespace onebit
+
+using namespace onebit::layers;
+
+extern "C" onebit_status_t onebit_linear_backward_workspace(const onebit_linear_grad_t* a, size_t* bytes) {
+  onebit_status_t st = backward_ok(a);
+  if (st != ONEBIT_OK) return st;
+  if (!bytes) return fail(ONEBIT_ERR_INVALID_ARG, "bytes is NULL");
+  Space ws{nullptr};
+  if (a->rows > 0) backward(*a, ws, nullptr, false);
+  *bytes = (size_t)ws.used;
+  return ONEBIT_OK;
+}
+
+extern "C" onebit_status_t onebit_linear_backward(const onebit_linear_grad_t* a, void* workspace,
+                                                  size_t workspace_bytes, onebit_stream_t stream) {
+  size_t need = 0;
+  onebit_status_t st = onebit_linear_backward_workspace(a, &need);
+  if (st != ONEBIT_OK) return st;
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+    return fail(ONEBIT_ERR_WORKSPACE, "the workspace is too small or not 256-byte aligned");
+  const int64_t blocks = ceil_div(a->in, kBlock), g = dtype_size(a->grad_dtype);
+  if (!disjoint({matrix(a->dy, a->rows, a->lddy, a->out, 2), matrix(a->x, a->rows, a->ldx, a->in, 2),
+                 span_of(a->codes, a->rows * a->in), span_of(a->scales, a->rows * blocks * 4),
+                 matrix(a->w, a->out, a->ldw, a->in, 2), matrix(a->add, a->rows, a->ldadd, a->in, 2)},
+                {matrix(a->dx, a->rows, a->lddx, a->in, 2), span_of(a->dw, a->out * a->in * g),
+                 span_of(a->db, a->out * g), span_of(workspace, (int64_t)need)}))
+    return fail(ONEBIT_ERR_INVALID_ARG, "an output overlaps another buffer");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (a->rows > 0) {
+    Space ws{static_cast<char*>(workspace)};
+    e = backward(*a, ws, s, true);
+  } else {  // no tokens: the parameters' gradients are 0
+    if (a->dw) e = cudaMemsetAsync(a->dw, 0, (size_t)(a->out * a->in * g), s);
+    if (a->db && e == cudaSuccess) e = cudaMemsetAsync(a->db, 0, (size_t)(a->out * g), s);
+  }
+  return e == cudaSuccess ? ONEBIT_OK : cuda_fail(e, "onebit_linear_backward");
+}

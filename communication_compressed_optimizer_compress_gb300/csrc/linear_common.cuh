@@ -1,0 +1,116 @@
+// linear_common.cuh -- what the linear layer's forward and backward pass share: realigned copies of
+// operands, epilogues over the partial sums of a cut contraction, workspace layout.
+#pragma once
+
+#include "tensor_product.cuh"
+
+namespace onebit {
+namespace layers {
+
+inline int64_t pad256(int64_t b) { return (b + 255) & ~(int64_t)255; }
+inline int64_t pad8(int64_t c) { return (c + 7) & ~(int64_t)7; }
+
+// Can TMA read this matrix as it lies?  (16-byte base, row stride a multiple of 16 bytes)
+inline bool copyable(const void* p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
+inline bool vec16(const void* p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
+
+inline unsigned flat_grid(int64_t total, int threads) {
+  const int64_t most = (int64_t)sm_count() * 8, want = ceil_div(total, threads);
+  return (unsigned)(want < most ? want : most);
+}
+
+// Hands out pieces of the caller's workspace; with a NULL base it only adds them up.
+struct Space {
+  char* base;
+  int64_t used = 0;
+  template <typename T>
+  T* take(int64_t count) {
+    char* p = base ? base + used : nullptr;
+    used += pad256(count * (int64_t)sizeof(T));
+    return reinterpret_cast<T*>(p);
+  }
+};
+
+// Rows of any alignment into rows of ld = pad8(cols) on 16 bytes (the columns past the end are not read).
+static __global__ void __launch_bounds__(256) k_realign(const uint16_t* __restrict__ x, int64_t ldx, int64_t rows, int cols, int64_t ld,
+                                                        uint16_t* __restrict__ out) {
+  const int64_t per = ld / 8, total = rows * per;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / per;
+    const int c = (int)(i - r * per) * 8;
+    uint32_t v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t lo = c + 2 * q < cols ? x[r * ldx + c + 2 * q] : 0, hi = c + 2 * q + 1 < cols ? x[r * ldx + c + 2 * q + 1] : 0;
+      v[q] = lo | hi << 16;
+    }
+    *reinterpret_cast<uint4*>(out + r * ld + c) = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+}
+
+// The operand as TMA can read it: itself, or a realigned copy in the workspace.
+inline Operand readable(Space& ws, const void* p, int64_t ld, int64_t rows, int64_t cols, cudaStream_t s, bool run) {
+  if (copyable(p, ld)) return {p, ld};
+  const int64_t ldc = pad8(cols);
+  uint16_t* c = ws.take<uint16_t>(rows * ldc);
+  if (run)
+    k_realign<<<flat_grid(rows * ldc / 8, 256), 256, 0, s>>>(static_cast<const uint16_t*>(p), ld, rows, (int)cols, ldc, c);
+  return {c, ldc};
+}
+
+// The value before the activation as the backward pass has it: itself, or its 8-bit checkpoint.
+template <typename T>
+struct Kept {
+  const T* x;
+  int64_t ldx;
+  const int8_t* codes;
+  const float* scales;
+  int cols, blocks;
+  __device__ __forceinline__ float at(int64_t r, int c) const {
+    return codes ? value_of<T>(codes[r * cols + c], scales[r * blocks + c / kBlock]) : to_f(x[r * ldx + c]);
+  }
+};
+
+// The partial products of a cut contraction: splits x rows x ld in fp32, added in order.
+struct Partials {
+  const float* p;
+  int64_t ld, split_stride;
+  int splits;
+  __device__ __forceinline__ float at(int64_t r, int c) const {
+    float s = p[r * ld + c];
+    for (int i = 1; i < splits; ++i) s += p[i * split_stride + r * ld + c];
+    return s;
+  }
+};
+inline Partials take_partials(Space& ws, const ProductPlan& plan, int64_t rows, int64_t cols) {
+  Partials q{};
+  if (plan.splits == 1) return q;
+  q.ld = (cols + 3) & ~(int64_t)3;
+  q.split_stride = rows * q.ld;
+  q.splits = plan.splits;
+  q.p = ws.take<float>(q.split_stride * plan.splits);
+  return q;
+}
+inline PlainEpilogue<float> to_partials(const Partials& q) {
+  return PlainEpilogue<float>{const_cast<float*>(q.p), q.ld, q.split_stride, true};
+}
+
+template <typename F>
+void with_grad(int32_t dtype, void* p, F&& f) {
+  if (dtype == ONEBIT_F32) f(static_cast<float*>(p));
+  else if (dtype == ONEBIT_F16) f(static_cast<__half*>(p));
+  else f(static_cast<__nv_bfloat16*>(p));
+}
+
+inline onebit_status_t linear_shape_ok(int64_t rows, int64_t in, int64_t out, int32_t dtype, int32_t act) {
+  if (rows < 0 || in < 1 || out < 1) return fail(ONEBIT_ERR_INVALID_ARG, "rows or widths out of range");
+  if (rows > kMaxRows || in > kMaxCols || out > kMaxCols)
+    return fail(ONEBIT_ERR_UNSUPPORTED, "more than 2^31 rows or a width above 2^24");
+  if (!dtype_ok(dtype)) return fail(ONEBIT_ERR_INVALID_ARG, "dtype is not one of f32, f16, bf16");
+  if (dtype == ONEBIT_F32) return fail(ONEBIT_ERR_UNSUPPORTED, "the linear layer takes f16 or bf16 operands");
+  if (act < ONEBIT_ACT_NONE || act > ONEBIT_ACT_GELU_TANH) return fail(ONEBIT_ERR_INVALID_ARG, "unknown activation");
+  return ONEBIT_OK;
+}
+
+}  // namespace layers
+}  // namespace onebit

@@ -1,0 +1,107 @@
+// linear_forward.cu -- the linear layer's forward pass: matrix product with bias, activation, residual
+// and an 8-bit checkpoint in its epilogue.  See include/onebit_layers.h for the formulas.
+#include "linear_common.cuh"
+
+namespace onebit {
+namespace layers {
+namespace {
+
+// The epilogue over the partial sums of a cut contraction, one warp per 64 columns of a row.
+template <typename T>
+__global__ void __launch_bounds__(256) k_finish_forward(Partials c, int64_t rows, int cols, ForwardEpilogue<T> e) {
+  const int lane = threadIdx.x & 31;
+  const int64_t units = rows * e.blocks, step = (int64_t)gridDim.x * 8;
+  for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < units; u += step) {
+    const int64_t r = u / e.blocks;
+    const int c0 = (int)(u - r * e.blocks) * kBlock + lane;
+    float z[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int col = c0 + 32 * q;
+      z[q] = 0.0f;
+      if (col < cols) {
+        z[q] = c.at(r, col) + (e.bias ? e.bias[col] : 0.0f);
+        float v = act_value(e.act, z[q]);
+        if (e.residual) v += to_f(e.residual[r * e.ldr + col]);
+        e.y[r * e.ldy + col] = from_f<T>(v);
+      }
+    }
+    if (e.codes) {
+      const BlockScale s = block_scale(warp_max_nan(max_nan(fabsf(z[0]), fabsf(z[1]))));
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        if (c0 + 32 * q < cols) e.codes[r * cols + c0 + 32 * q] = (int8_t)code_of(z[q], s.inv);
+      if (lane == 0) e.scales[u] = s.scale;
+    }
+  }
+}
+
+// Takes the workspace; with `run`, enqueues the work too.
+template <typename T>
+cudaError_t forward(const onebit_linear_t& a, Space& ws, cudaStream_t s, bool run) {
+  const ProductShape shape{a.rows, a.out, a.in};
+  const ProductPlan plan = plan_product(shape, sm_count());
+  const Operand x = readable(ws, a.x, a.ldx, a.rows, a.in, s, run), w = readable(ws, a.w, a.ldw, a.out, a.in, s, run);
+  const Partials part = take_partials(ws, plan, a.rows, a.out);
+  if (!run) return cudaSuccess;
+  const ForwardEpilogue<T> e{a.bias, static_cast<const T*>(a.residual), a.ldr, static_cast<T*>(a.y), a.ldy, a.codes, a.scales,
+                             (int)ceil_div(a.out, kBlock), a.activation, aligned(a.bias, 16), vec16(a.residual, a.ldr), vec16(a.y, a.ldy),
+                             aligned(a.codes, 16) && a.out % 16 == 0};
+  if (plan.splits == 1) return run_product<false, false>(a.dtype, x, w, shape, plan, e, s);
+  const cudaError_t err = run_product<false, false>(a.dtype, x, w, shape, plan, to_partials(part), s);
+  if (err != cudaSuccess) return err;
+  k_finish_forward<T><<<flat_grid(a.rows * e.blocks * 32, 256), 256, 0, s>>>(part, a.rows, (int)a.out, e);
+  return cudaGetLastError();
+}
+cudaError_t forward(const onebit_linear_t& a, Space& ws, cudaStream_t s, bool run) {
+  return a.dtype == ONEBIT_F16 ? forward<__half>(a, ws, s, run) : forward<__nv_bfloat16>(a, ws, s, run);
+}
+
+onebit_status_t forward_ok(const onebit_linear_t* a) {
+  if (!a) return fail(ONEBIT_ERR_INVALID_ARG, "the arguments are NULL");
+  onebit_status_t st = linear_shape_ok(a->rows, a->in, a->out, a->dtype, a->activation);
+  if (st != ONEBIT_OK) return st;
+  if (a->ldx < a->in || a->ldw < a->in || a->ldy < a->out || (a->residual && a->ldr < a->out))
+    return fail(ONEBIT_ERR_INVALID_ARG, "a row stride below the columns");
+  if (!a->codes != !a->scales) return fail(ONEBIT_ERR_INVALID_ARG, "a checkpoint needs codes and scales");
+  if (a->rows > 0 && (!a->x || !a->w || !a->y)) return fail(ONEBIT_ERR_INVALID_ARG, "a NULL buffer");
+  if (!aligned(a->x, 2) || !aligned(a->w, 2) || !aligned(a->y, 2) || !aligned(a->residual, 2) || !aligned(a->bias, 4) ||
+      !aligned(a->scales, 4))
+    return fail(ONEBIT_ERR_INVALID_ARG, "a buffer is not aligned to its type");
+  return ONEBIT_OK;
+}
+
+}  // namespace
+}  // namespace layers
+}  // namespace onebit
+
+using namespace onebit::layers;
+
+extern "C" onebit_status_t onebit_linear_forward_workspace(const onebit_linear_t* a, size_t* bytes) {
+  onebit_status_t st = forward_ok(a);
+  if (st != ONEBIT_OK) return st;
+  if (!bytes) return fail(ONEBIT_ERR_INVALID_ARG, "bytes is NULL");
+  Space ws{nullptr};
+  if (a->rows > 0) forward(*a, ws, nullptr, false);
+  *bytes = (size_t)ws.used;
+  return ONEBIT_OK;
+}
+
+extern "C" onebit_status_t onebit_linear_forward(const onebit_linear_t* a, void* workspace, size_t workspace_bytes,
+                                                 onebit_stream_t stream) {
+  size_t need = 0;
+  onebit_status_t st = onebit_linear_forward_workspace(a, &need);
+  if (st != ONEBIT_OK || a->rows == 0) return st;
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+    return fail(ONEBIT_ERR_WORKSPACE, "the workspace is too small or not 256-byte aligned");
+  const int64_t blocks = ceil_div(a->out, kBlock);
+  if (!disjoint({matrix(a->x, a->rows, a->ldx, a->in, 2), matrix(a->w, a->out, a->ldw, a->in, 2),
+                 span_of(a->bias, a->out * 4), matrix(a->residual, a->rows, a->ldr, a->out, 2)},
+                {matrix(a->y, a->rows, a->ldy, a->out, 2), span_of(a->codes, a->rows * a->out),
+                 span_of(a->scales, a->rows * blocks * 4), span_of(workspace, (int64_t)need)}))
+    return fail(ONEBIT_ERR_INVALID_ARG, "an output overlaps another buffer");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Space ws{static_cast<char*>(workspace)};
+  const cudaError_t e = forward(*a, ws, s, true);
+  return e == cudaSuccess ? ONEBIT_OK : cuda_fail(e, "onebit_linear_forward");
+}

@@ -1,0 +1,781 @@
+// tensor_product.cuh -- C[m][n] = sum_k A(m,k) B(n,k) of 16-bit operands on the tensor cores, accumulated
+// in fp32, with an epilogue that turns the fp32 tile into what the caller stores.
+//
+// Each operand lies in memory with its contraction index contiguous ("K-major": A is m rows of k) or
+// with its own index contiguous ("MN-major": A is k rows of m), which covers x w^T (K, K), dy w (K, MN)
+// and dy^T x (MN, MN) without transposing anything.
+//
+// One block (or a pair of blocks on neighbouring SMs) computes a tile of 128 (256) rows by 128 (256)
+// columns at a time.  Warp 0 copies operand slabs of 64 contraction elements into a ring of shared
+// memory stages with TMA; warp 1 issues the tensor-core instructions; eight warps read finished
+// accumulators out of tensor memory and run the epilogue.  Two accumulators alternate, so that the
+// epilogue of one tile runs under the products of the next.  In a pair each block holds half of A's
+// rows and half of B's, and the even block's instructions use both halves: each SM's shared memory
+// then feeds a 256x256 tile with the traffic of a 128x128 one.
+//
+// A product that is stored in fp32 (dw over many tokens, partial sums) is accumulated in chunks of
+// kFoldSlabs slabs, whose sums the epilogue warps add up in registers: the tensor cores' own running
+// sum loses about 2^-26 of its size a step (measured: 1.9e-6 of the result's norm after 2048 terms).
+#pragma once
+
+#include <cuda.h>  // CUtensorMap: types only, the encoder is looked up at run time
+
+#include "layers_common.cuh"
+
+namespace onebit {
+namespace layers {
+
+constexpr int kSlabK = 64;                    // contraction elements per stage: 128 bytes, one swizzle row
+constexpr int kRowsPerBlock = 128;            // rows of each operand that a block holds
+constexpr int kOperandBytes = kRowsPerBlock * kSlabK * 2;
+constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kStages = 5;
+constexpr int kEpilogueWarps = 8;
+constexpr int kProductThreads = 128 + 32 * kEpilogueWarps;
+constexpr int kControlRegs = 40, kEpilogueRegs = 232;  // 56 + 2*224 = 3 * 168, what a block is launched with
+constexpr int kStagingRow = 144;              // 128 bytes and 16 to spread the rows over the banks
+constexpr int kStagingBytes = 32 * kStagingRow;
+constexpr int kBarrierBytes = 256;
+constexpr int kProductSmem = 1024 + kStages * kStageBytes + kEpilogueWarps * kStagingBytes + kBarrierBytes;
+constexpr int kFoldSlabs = 8;                 // slabs that an accumulator of a folded product sums up
+constexpr int kGroupTiles = 8;                // tile rows that are walked together, for the L2
+
+constexpr unsigned kStatusGaveUp = 1u;
+
+struct ProductArgs {
+  CUtensorMap a, b;
+  int64_t m;
+  int32_t n;
+  int32_t slabs;             // of the whole contraction
+  int32_t tiles_m, tiles_n;
+  int32_t splits, split_slabs;
+  uint32_t idesc;
+  uint32_t stall_tx;         // test hook: bytes that every stage waits for and no copy brings (normally 0)
+  unsigned int* status;
+};
+
+// ------------------------------------------------------------------------------------------------
+// PTX
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Address of this block's shared memory word `addr` in the block `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_block(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// One box of a matrix into this block's shared memory; `bar` may be the other block's of a pair.
+template <int CTAS>
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
+  if (CTAS == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map),
+        "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+template <int CTAS>
+__device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t cols) {
+  if (CTAS == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+}
+template <int CTAS>
+__device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
+  if (CTAS == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
+  else
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
+}
+template <int CTAS>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  if (CTAS == 2)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a),
+        "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a),
+        "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+// The barrier (of both blocks of a pair) is arrived at when this thread's instructions so far are done.
+template <int CTAS>
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  if (CTAS == 2)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar), "h"((uint16_t)3)
+        : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// Waits for this warp's loads.  The values pass through the statement, so that nothing that uses them
+// can be moved ahead of it.
+__device__ __forceinline__ void tmem_hold32(float* v) {
+  asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
+}
+__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// 32 columns of the 32 lanes that this warp may read
+__device__ __forceinline__ void tmem_load32(uint32_t addr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+      "%29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
+        "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31])
+      : "r"(addr));
+}
+
+// Shared-memory matrix descriptor: 128-byte swizzle over groups of 8 rows of 128 bytes (1024 bytes).
+// K-major: a row is one m (n) with 64 k; groups of 8 m follow each other (stride 1024), and a step of
+// 16 k is 32 bytes along the row.  MN-major: a row is one k with 64 m; groups of 8 k follow each other
+// (stride 1024), the next 64 m lie one 64-row box (8192 bytes) further, and a step of 16 k is 2048 bytes.
+template <bool MN>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+  const uint64_t lead = MN ? (8192 >> 4) : 1;
+  return (uint64_t)((addr >> 4) & 0x3fff) | lead << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+template <bool MN>
+__device__ __forceinline__ constexpr uint32_t k_step() { return MN ? (2048 >> 4) : (32 >> 4); }
+
+// ------------------------------------------------------------------------------------------------
+// Waits end after about a second: the block's flag is set, every other wait of the block ends too, and
+// the status word says so.
+struct Wait {
+  volatile int* gave_up;
+  unsigned int* status;
+  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+    if (bar_try(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!bar_try(bar, parity)) {
+      if (*gave_up) return false;
+      if (clock64() - t0 > 2000000000ll) {
+        *gave_up = 1;
+        atomicOr(status, kStatusGaveUp);
+        return false;
+      }
+    }
+    return true;
+  }
+};
+
+// ------------------------------------------------------------------------------------------------
+// Rows of 128 bytes between registers (a lane has a row) and memory (eight lanes share a row, so that
+// every access is a whole 128-byte line), through the warp's staging buffer.
+
+template <typename T>
+struct RowStore {  // 128/sizeof(T) columns from col0 on
+  static constexpr int kCols = 128 / sizeof(T);
+  static constexpr int kVec = 16 / sizeof(T);
+  __device__ static __forceinline__ void run(char* staging, const uint32_t (&v)[32], T* p, int64_t ld, int64_t row0, int64_t rows, int col0,
+                                             int cols, bool vec) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      *reinterpret_cast<uint4*>(staging + lane * kStagingRow + j * 16) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    __syncwarp();
+    const int c = (lane & 7) * kVec;
+    if (vec && col0 + kCols <= cols) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = i * 4 + (lane >> 3);
+        if (row0 + r < rows)
+          *reinterpret_cast<uint4*>(p + (row0 + r) * ld + col0 + c) =
+              *reinterpret_cast<const uint4*>(staging + r * kStagingRow + (lane & 7) * 16);
+      }
+    } else {
+      for (int r = 0; r < 32 && row0 + r < rows; ++r)
+        for (int q = lane; q < kCols && col0 + q < cols; q += 32)
+          p[(row0 + r) * ld + col0 + q] = reinterpret_cast<const T*>(staging + r * kStagingRow)[q];
+    }
+    __syncwarp();
+  }
+};
+
+template <typename T>  // a 16-bit type: 64 columns
+__device__ __forceinline__ void load_rows(char* staging, uint32_t (&v)[32], const T* p, int64_t ld, int64_t row0, int64_t rows, int col0, int cols,
+                                          bool vec) {
+  const int lane = threadIdx.x & 31;
+  if (vec && col0 + 64 <= cols) {
+    uint4 t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = i * 4 + (lane >> 3);
+      t[i] = row0 + r < rows ? *reinterpret_cast<const uint4*>(p + (row0 + r) * ld + col0 + (lane & 7) * 8) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      *reinterpret_cast<uint4*>(staging + (i * 4 + (lane >> 3)) * kStagingRow + (lane & 7) * 16) = t[i];
+  } else {
+    for (int r = 0; r < 32; ++r)
+      for (int q = lane; q < 64; q += 32)
+        reinterpret_cast<T*>(staging + r * kStagingRow)[q] = row0 + r < rows && col0 + q < cols ? p[(row0 + r) * ld + col0 + q] : from_f<T>(0.0f);
+  }
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint4 t = *reinterpret_cast<const uint4*>(staging + lane * kStagingRow + j * 16);
+    v[4 * j] = t.x, v[4 * j + 1] = t.y, v[4 * j + 2] = t.z, v[4 * j + 3] = t.w;
+  }
+  __syncwarp();
+}
+
+// 64 codes of a row, packed in 16 words; codes are contiguous rows of `cols`
+constexpr int kCodeRow = 80;
+__device__ __forceinline__ void store_codes(char* staging, const uint32_t (&v)[16], int8_t* p, int64_t row0, int64_t rows, int col0, int cols, bool vec) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<uint4*>(staging + lane * kCodeRow + j * 16) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+  __syncwarp();
+  if (vec && col0 + 64 <= cols) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 8 + (lane >> 2);
+      if (row0 + r < rows)
+        *reinterpret_cast<uint4*>(p + (row0 + r) * cols + col0 + (lane & 3) * 16) = *reinterpret_cast<const uint4*>(staging + r * kCodeRow + (lane & 3) * 16);
+    }
+  } else {
+    for (int r = 0; r < 32 && row0 + r < rows; ++r)
+      for (int q = lane; q < 64 && col0 + q < cols; q += 32) p[(row0 + r) * cols + col0 + q] = (staging + r * kCodeRow)[q];
+  }
+  __syncwarp();
+}
+__device__ __forceinline__ void load_codes(char* staging, uint32_t (&v)[16], const int8_t* p, int64_t row0, int64_t rows, int col0, int cols, bool vec) {
+  const int lane = threadIdx.x & 31;
+  if (vec && col0 + 64 <= cols) {
+    uint4 t[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 8 + (lane >> 2);
+      t[i] = row0 + r < rows ? *reinterpret_cast<const uint4*>(p + (row0 + r) * cols + col0 + (lane & 3) * 16) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(staging + (i * 8 + (lane >> 2)) * kCodeRow + (lane & 3) * 16) = t[i];
+  } else {
+    for (int r = 0; r < 32; ++r)
+      for (int q = lane; q < 64; q += 32) (staging + r * kCodeRow)[q] = row0 + r < rows && col0 + q < cols ? p[(row0 + r) * cols + col0 + q] : 0;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint4 t = *reinterpret_cast<const uint4*>(staging + lane * kCodeRow + j * 16);
+    v[4 * j] = t.x, v[4 * j + 1] = t.y, v[4 * j + 2] = t.z, v[4 * j + 3] = t.w;
+  }
+  __syncwarp();
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t v);
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t v) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+__device__ __forceinline__ float code_at(uint32_t word, int byte) { return (float)(int8_t)(word >> (8 * byte)); }
+
+// ------------------------------------------------------------------------------------------------
+// Epilogues.  run() has 64 columns from col0 on of the 32 rows from row0 on: a lane has row row0 + lane.
+
+template <typename T>
+struct ForwardEpilogue {
+  // y = act(d + bias) + residual, and the 8-bit checkpoint of d + bias
+  static constexpr bool kFold = false;
+  const float* bias;
+  const T* residual;
+  int64_t ldr;
+  T* y;
+  int64_t ldy;
+  int8_t* codes;
+  float* scales;
+  int blocks;
+  int act;
+  bool vec_bias, vec_res, vec_y, vec_codes;
+
+  __device__ __forceinline__ void run(float (&z)[64], int64_t row0, int64_t rows, int col0, int cols, int, char* staging) const {
+    const int64_t row = row0 + (threadIdx.x & 31);
+    if (bias) {
+      if (vec_bias && col0 + 64 <= cols) {
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) {
+          const float4 b = __ldg(reinterpret_cast<const float4*>(bias + col0 + i));
+          z[i] += b.x, z[i + 1] += b.y, z[i + 2] += b.z, z[i + 3] += b.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) z[i] += col0 + i < cols ? __ldg(bias + col0 + i) : 0.0f;
+      }
+    }
+    if (codes) {  // columns past the end have z = 0: their operand rows were filled with zeros
+      float most = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 64; ++i) most = max_nan(most, fabsf(z[i]));
+      const BlockScale s = block_scale(most);
+      uint32_t c[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        c[i] = code_of(z[4 * i], s.inv) | code_of(z[4 * i + 1], s.inv) << 8 | code_of(z[4 * i + 2], s.inv) << 16 | code_of(z[4 * i + 3], s.inv) << 24;
+      if (row < rows) scales[row * blocks + col0 / kBlock] = s.scale;
+      store_codes(staging, c, codes, row0, rows, col0, cols, vec_codes);
+    }
+    uint32_t v[32];
+    if (act == ONEBIT_ACT_RELU) {
+#pragma unroll
+      for (int i = 0; i < 64; ++i) z[i] = act_value(ONEBIT_ACT_RELU, z[i]);
+    } else if (act == ONEBIT_ACT_GELU) {
+#pragma unroll
+      for (int i = 0; i < 64; ++i) z[i] = act_value(ONEBIT_ACT_GELU, z[i]);
+    } else if (act == ONEBIT_ACT_GELU_TANH) {
+#pragma unroll
+      for (int i = 0; i < 64; ++i) z[i] = act_value(ONEBIT_ACT_GELU_TANH, z[i]);
+    }
+    if (residual) {
+      load_rows(staging, v, residual, ldr, row0, rows, col0, cols, vec_res);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float2 r = unpack2<T>(v[i]);
+        z[2 * i] += r.x, z[2 * i + 1] += r.y;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = pack2<T>(z[2 * i], z[2 * i + 1]);
+    RowStore<T>::run(staging, v, y, ldy, row0, rows, col0, cols, vec_y);
+  }
+};
+
+template <typename T>
+struct InputGradEpilogue {
+  // dx = d * act'(v) [+ add], and h = act(v) for the product of dw
+  static constexpr bool kFold = false;
+  const T* x;
+  int64_t ldx;
+  const int8_t* codes;
+  const float* scales;
+  int blocks;
+  const T* add;
+  int64_t ldadd;
+  T* dx;
+  int64_t lddx;
+  T* h;
+  int64_t ldh;
+  int act;
+  bool vec_x, vec_codes, vec_add, vec_dx;
+
+  template <int ACT>
+  __device__ __forceinline__ void slopes(float (&d)[64], uint32_t (&v)[32]) const {  // v: in the kept values, out h
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float2 z = unpack2<T>(v[i]);
+      d[2 * i] *= act_slope(ACT, z.x), d[2 * i + 1] *= act_slope(ACT, z.y);
+      v[i] = pack2<T>(act_value(ACT, z.x), act_value(ACT, z.y));
+    }
+  }
+  template <int ACT>
+  __device__ __forceinline__ void slopes(float (&d)[64], const uint32_t (&c)[16], float s, uint32_t (&v)[32]) const {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float z0 = code_at(c[i / 2], (2 * i) & 3) * s, z1 = code_at(c[i / 2], (2 * i + 1) & 3) * s;
+      d[2 * i] *= act_slope(ACT, z0), d[2 * i + 1] *= act_slope(ACT, z1);
+      v[i] = pack2<T>(act_value(ACT, z0), act_value(ACT, z1));
+    }
+  }
+  __device__ __forceinline__ void run(float (&d)[64], int64_t row0, int64_t rows, int col0, int cols, int, char* staging) const {
+    uint32_t v[32];
+    if (codes && (act != ONEBIT_ACT_NONE || h)) {
+      uint32_t c[16];
+      load_codes(staging, c, codes, row0, rows, col0, cols, vec_codes);
+      const int64_t row = row0 + (threadIdx.x & 31);
+      const float s = row < rows ? __ldg(scales + row * blocks + col0 / kBlock) : 0.0f;
+      if (act == ONEBIT_ACT_NONE) slopes<ONEBIT_ACT_NONE>(d, c, s, v);
+      else if (act == ONEBIT_ACT_RELU) slopes<ONEBIT_ACT_RELU>(d, c, s, v);
+      else if (act == ONEBIT_ACT_GELU) slopes<ONEBIT_ACT_GELU>(d, c, s, v);
+      else slopes<ONEBIT_ACT_GELU_TANH>(d, c, s, v);
+    } else if (act != ONEBIT_ACT_NONE) {
+      load_rows(staging, v, x, ldx, row0, rows, col0, cols, vec_x);
+      if (act == ONEBIT_ACT_RELU) slopes<ONEBIT_ACT_RELU>(d, v);
+      else if (act == ONEBIT_ACT_GELU) slopes<ONEBIT_ACT_GELU>(d, v);
+      else slopes<ONEBIT_ACT_GELU_TANH>(d, v);
+    }
+    if (h) RowStore<T>::run(staging, v, h, ldh, row0, rows, col0, cols, true);
+    if (add) {
+      load_rows(staging, v, add, ldadd, row0, rows, col0, cols, vec_add);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float2 r = unpack2<T>(v[i]);
+        d[2 * i] += r.x, d[2 * i + 1] += r.y;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = pack2<T>(d[2 * i], d[2 * i + 1]);
+    RowStore<T>::run(staging, v, dx, lddx, row0, rows, col0, cols, vec_dx);
+  }
+};
+
+template <typename G>
+struct PlainEpilogue {
+  // the product itself in G; split s of a cut contraction goes to p + s * split_stride
+  static constexpr bool kFold = true;
+  G* p;
+  int64_t ld;
+  int64_t split_stride;
+  bool vec;
+  __device__ __forceinline__ void run(float (&acc)[64], int64_t row0, int64_t rows, int col0, int cols, int split, char* staging) const {
+    G* out = p + split * split_stride;
+    uint32_t v[32];
+    if (sizeof(G) == 4) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(acc[32 * half + i]);
+        RowStore<G>::run(staging, v, out, ld, row0, rows, col0 + 32 * half, cols, vec);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = pack2<std::conditional_t<sizeof(G) == 4, __half, G>>(acc[2 * i], acc[2 * i + 1]);
+      RowStore<G>::run(staging, v, out, ld, row0, rows, col0, cols, vec);
+    }
+  }
+};
+
+// ------------------------------------------------------------------------------------------------
+
+struct Tile {
+  int64_t m0;
+  int n0, split, first, slabs;
+};
+template <int CTAS>
+__device__ __forceinline__ Tile tile_of(const ProductArgs& P, int64_t unit) {
+  constexpr int kM = kRowsPerBlock * CTAS, kN = kRowsPerBlock * CTAS;
+  Tile t;
+  const int64_t tile = unit / P.splits;
+  t.split = (int)(unit - tile * P.splits);
+  // kGroupTiles tile rows side by side, column after column: the tiles in flight share operand slabs in L2
+  const int64_t per = (int64_t)kGroupTiles * P.tiles_n, g = tile / per;
+  const int rows = (int)(P.tiles_m - g * kGroupTiles < kGroupTiles ? P.tiles_m - g * kGroupTiles : kGroupTiles);
+  const int in = (int)(tile - g * per);
+  t.m0 = (g * kGroupTiles + in % rows) * kM;
+  t.n0 = in / rows * kN;
+  t.first = t.split * P.split_slabs;
+  t.slabs = P.slabs - t.first < P.split_slabs ? P.slabs - t.first : P.split_slabs;
+  return t;
+}
+
+template <int CTAS, bool A_MN, bool B_MN, class Epilogue>
+__global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_constant__ ProductArgs P, const __grid_constant__ Epilogue E) {
+  constexpr int kTileN = kRowsPerBlock * CTAS;
+  constexpr int kCols = kTileN / 2;             // columns of an epilogue warp
+  constexpr uint32_t kTmemCols = 2 * kTileN;    // two accumulators
+  extern __shared__ char smem_raw[];
+  char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  char* staging_base = smem + kStages * kStageBytes;
+  char* bars = staging_base + kEpilogueWarps * kStagingBytes;
+  const uint32_t bar0 = smem_addr(bars);
+  auto full = [&](int s) { return bar0 + 8 * s; };
+  auto empty = [&](int s) { return bar0 + 8 * (kStages + s); };
+  auto acc_full = [&](int s) { return bar0 + 8 * (2 * kStages + s); };
+  auto acc_empty = [&](int s) { return bar0 + 8 * (2 * kStages + 2 + s); };
+  const uint32_t drained = bar0 + 8 * (2 * kStages + 4);
+  volatile uint32_t* tmem_ptr = reinterpret_cast<volatile uint32_t*>(bars + 8 * (2 * kStages + 5));
+  volatile int* gave_up = reinterpret_cast<volatile int*>(bars + 8 * (2 * kStages + 6));
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CTAS == 2 ? cluster_rank() : 0;
+  const int64_t units = (int64_t)P.tiles_m * P.tiles_n * P.splits;
+  const int64_t first_unit = blockIdx.x / CTAS, unit_step = gridDim.x / CTAS;
+  const Wait wait{gave_up, P.status};
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) bar_init(full(s), 1), bar_init(empty(s), 1);
+    for (int s = 0; s < 2; ++s) bar_init(acc_full(s), 1), bar_init(acc_empty(s), CTAS * kEpilogueWarps);
+    bar_init(drained, 1);
+    *gave_up = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc<CTAS>(smem_addr((const void*)tmem_ptr), kTmemCols);
+  tmem_fence_before();
+  __syncthreads();
+  if (CTAS == 2) cluster_sync();  // the other block's barriers are ready too
+  tmem_fence_after();
+  const uint32_t tmem = *tmem_ptr;
+
+  // the epilogue warps take the registers that the control warps do not need
+  if (warp >= 4) {
+    // ---- epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpilogueRegs));
+    const int quad = warp & 3, half = (warp - 4) >> 2;
+    char* staging = staging_base + (warp - 4) * kStagingBytes;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + half * kCols;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    // the accumulator is in registers: the next product may write over it
+    auto release = [&] {
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive_cluster(in_block(acc_empty(acc), 0));
+      if ((acc ^= 1) == 0) acc_phase ^= 1;
+    };
+    auto ready = [&] {  // the warp stays whole
+      const bool ok = __all_sync(0xffffffffu, wait(acc_full(acc), acc_phase));
+      tmem_fence_after();
+      return ok;
+    };
+    bool ok = true;
+    for (int64_t u = first_unit; u < units && ok; u += unit_step) {
+      const Tile t = tile_of<CTAS>(P, u);
+      const int64_t row0 = t.m0 + rank * kRowsPerBlock + quad * 32;
+      const int col0 = t.n0 + half * kCols;
+      if (Epilogue::kFold) {
+        float c[kCols / 64][64];
+        for (int k0 = 0; k0 < t.slabs; k0 += kFoldSlabs) {
+          if (!(ok = ready())) break;
+          const uint32_t at = lanes + acc * kTileN;
+          if (k0 == 0) {
+#pragma unroll
+            for (int q = 0; q < kCols; q += 32) tmem_load32(at + q, &c[q / 64][q % 64]);
+            tmem_wait_load();
+#pragma unroll
+            for (int q = 0; q < kCols; q += 32) tmem_hold32(&c[q / 64][q % 64]);
+          } else {
+#pragma unroll
+            for (int q = 0; q < kCols; q += 32) {
+              float v[32];
+              tmem_load32(at + q, v);
+              tmem_wait_load();
+              tmem_hold32(v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) c[q / 64][q % 64 + i] += v[i];
+            }
+          }
+          release();
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int q = 0; q < kCols / 64; ++q)
+          if (row0 < P.m && col0 + 64 * q < P.n) E.run(c[q], row0, P.m, col0 + 64 * q, P.n, t.split, staging);
+      } else {
+        if (!(ok = ready())) break;
+        const uint32_t at = lanes + acc * kTileN;
+#pragma unroll
+        for (int q = 0; q < kCols / 64; ++q) {
+          float c[64];
+          tmem_load32(at + 64 * q, c);
+          tmem_load32(at + 64 * q + 32, c + 32);
+          tmem_wait_load();
+          tmem_hold32(c);
+          tmem_hold32(c + 32);
+          if (q == kCols / 64 - 1) release();
+          if (row0 < P.m && col0 + 64 * q < P.n) E.run(c, row0, P.m, col0 + 64 * q, P.n, t.split, staging);
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
+    if (warp == 0 && lane == 0) {
+      // ---- copies
+      int st = 0;
+      uint32_t phase = 0;
+      int64_t issued = 0;
+      bool ok = true;
+      for (int64_t u = first_unit; u < units && ok; u += unit_step) {
+        const Tile t = tile_of<CTAS>(P, u);
+        const int32_t ma = (int32_t)(t.m0 + rank * kRowsPerBlock), nb = t.n0 + (int)rank * kRowsPerBlock;
+        for (int k = 0; k < t.slabs; ++k) {
+          if (!wait(empty(st), phase ^ 1)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) bar_expect(full(st), CTAS * kStageBytes + P.stall_tx);
+          const uint32_t bar = CTAS == 2 ? in_block(full(st), 0) : full(st);
+          const uint32_t da = smem_addr(smem + st * kStageBytes), db = da + kOperandBytes;
+          const int32_t kk = (t.first + k) * kSlabK;
+          if (A_MN) {
+            copy_box<CTAS>(da, &P.a, ma, kk, bar);
+            copy_box<CTAS>(da + kOperandBytes / 2, &P.a, ma + 64, kk, bar);
+          } else {
+            copy_box<CTAS>(da, &P.a, kk, ma, bar);
+          }
+          if (B_MN) {
+            copy_box<CTAS>(db, &P.b, nb, kk, bar);
+            copy_box<CTAS>(db + kOperandBytes / 2, &P.b, nb + 64, kk, bar);
+          } else {
+            copy_box<CTAS>(db, &P.b, kk, nb, bar);
+          }
+          ++issued;
+          if (++st == kStages) st = 0, phase ^= 1;
+        }
+      }
+      if (!ok && rank == 0) {
+        // gave up: the copies in flight land before the block leaves (a limited wait for each stage's)
+        for (int64_t q = issued > kStages ? issued - kStages : 0; q < issued; ++q) {
+          const long long t0 = clock64();
+          while (!bar_try(full((int)(q % kStages)), (uint32_t)(q / kStages) & 1) && clock64() - t0 < 20000000ll) {
+          }
+        }
+      }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      // ---- products
+      int st = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int64_t u = first_unit; u < units && ok; u += unit_step) {
+        const Tile t = tile_of<CTAS>(P, u);
+        for (int k0 = 0, k1; k0 < t.slabs && ok; k0 = k1) {
+          k1 = Epilogue::kFold && t.slabs - k0 > kFoldSlabs ? k0 + kFoldSlabs : t.slabs;
+          if (!(ok = wait(acc_empty(acc), acc_phase ^ 1))) break;
+          tmem_fence_after();
+          const uint32_t d = tmem + acc * kTileN;
+          for (int k = k0; k < k1; ++k) {
+            if (!(ok = wait(full(st), phase))) break;
+            tmem_fence_after();
+            const uint32_t sa = smem_addr(smem + st * kStageBytes);
+            const uint64_t da = operand_desc<A_MN>(sa), db = operand_desc<B_MN>(sa + kOperandBytes);
+  #pragma unroll
+            for (int q = 0; q < kSlabK / 16; ++q) mma<CTAS>(d, da + q * k_step<A_MN>(), db + q * k_step<B_MN>(), P.idesc, k > k0 || q > 0);
+            mma_commit<CTAS>(empty(st));
+            if (++st == kStages) st = 0, phase ^= 1;
+          }
+          if (!ok) break;
+          mma_commit<CTAS>(acc_full(acc));
+          if ((acc ^= 1) == 0) acc_phase ^= 1;
+        }
+      }
+      // the tensor cores are done with shared and tensor memory before the block frees them
+      mma_commit<CTAS>(drained);
+      const long long t0 = clock64();
+      while (!bar_try(drained, 0) && clock64() - t0 < 2000000000ll) {
+      }
+    }
+  }
+  __syncwarp();
+  tmem_fence_before();
+  __syncthreads();
+  if (CTAS == 2) cluster_sync();  // neither block leaves while the other may still reach into it
+  tmem_fence_after();
+  if (warp == 1) tmem_free<CTAS>(tmem, kTmemCols);
+}
+
+// ------------------------------------------------------------------------------------------------
+// host side
+
+// A row-major matrix of rows x cols 16-bit values, copied in boxes of 64 columns by box_rows rows.  The
+// base lies on 16 bytes and ld is a multiple of 8.
+cudaError_t make_map(CUtensorMap* map, int32_t dtype, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows);
+unsigned int* status_word();   // of the current device (NULL: a CUDA error)
+uint32_t stall_bytes();        // the test hook's
+
+struct ProductShape {
+  int64_t m;
+  int64_t n, k;
+};
+struct ProductPlan {
+  int ctas, splits, split_slabs;
+};
+ProductPlan plan_product(const ProductShape& s, int sms);
+
+struct Operand {
+  const void* p;
+  int64_t ld;
+};
+
+template <int CTAS, bool A_MN, bool B_MN, class Epilogue>
+cudaError_t launch_product(const ProductArgs& P, const Epilogue& E, int sms, cudaStream_t s) {
+  auto* kernel = k_product<CTAS, A_MN, B_MN, Epilogue>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t units = (int64_t)P.tiles_m * P.tiles_n * P.splits, most = sms / CTAS;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((units < most ? units : most) * CTAS));
+  cfg.blockDim = dim3(kProductThreads);
+  cfg.dynamicSmemBytes = kProductSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = CTAS;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P, E);
+}
+
+// C = A B^T by `plan`, through epilogue E.  A: m x k (or k x m with A_MN), B: n x k (or k x n with B_MN).
+template <bool A_MN, bool B_MN, class Epilogue>
+cudaError_t run_product(int32_t dtype, const Operand& a, const Operand& b, const ProductShape& s, const ProductPlan& plan, const Epilogue& E,
+                        cudaStream_t stream) {
+  ProductArgs P{};
+  cudaError_t e = make_map(&P.a, dtype, a.p, A_MN ? s.k : s.m, A_MN ? s.m : s.k, a.ld, A_MN ? 64 : 128);
+  if (e == cudaSuccess) e = make_map(&P.b, dtype, b.p, B_MN ? s.k : s.n, B_MN ? s.n : s.k, b.ld, B_MN ? 64 : 128);
+  if (e != cudaSuccess) return e;
+  P.m = s.m;
+  P.n = (int32_t)s.n;
+  P.slabs = (int32_t)ceil_div(s.k, kSlabK);
+  P.tiles_m = (int32_t)ceil_div(s.m, kRowsPerBlock * plan.ctas);
+  P.tiles_n = (int32_t)ceil_div(s.n, kRowsPerBlock * plan.ctas);
+  P.splits = plan.splits;
+  P.split_slabs = plan.split_slabs;
+  const uint32_t type = dtype == ONEBIT_F16 ? 0u : 1u;  // both operands have the same
+  P.idesc = 1u << 4 | type << 7 | type << 10 | (uint32_t)A_MN << 15 | (uint32_t)B_MN << 16 |
+            (uint32_t)(kRowsPerBlock * plan.ctas / 8) << 17 | (uint32_t)(kRowsPerBlock * plan.ctas / 16) << 24;
+  P.stall_tx = stall_bytes();
+  P.status = status_word();
+  if (!P.status) return cudaErrorUnknown;
+  const int sms = sm_count();
+  return plan.ctas == 2 ? launch_product<2, A_MN, B_MN>(P, E, sms, stream) : launch_product<1, A_MN, B_MN>(P, E, sms, stream);
+}
+
+}  // namespace layers
+}  // namespace onebit

@@ -25,7 +25,7 @@ from typing import NamedTuple
 
 import torch
 
-from . import BF16, F16, F32, OK, OneBitError, lib
+from . import BF16, F16, F32, OK, OneBitError, _stream_ptr, lib
 
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH = range(4)
 ACTIVATIONS = {"none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH}
@@ -80,6 +80,9 @@ def _functions():
             "onebit_linear_forward": [ctypes.POINTER(LinearArgs), vp, sz, vp],
             "onebit_linear_backward_workspace": [ctypes.POINTER(LinearGradArgs), ctypes.POINTER(sz)],
             "onebit_linear_backward": [ctypes.POINTER(LinearGradArgs), vp, sz, vp],
+            "onebit_layers_get_status": [vp],
+            "onebit_layers_clear_status": [vp],
+            "onebit_layers_set_fault_injection": [i32, i64],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -188,6 +191,20 @@ def _new_checkpoint(shape, dtype, device):
 
 def _workspace(nbytes: int, device):
     return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def get_status(stream=None) -> int:
+    """Waits for the stream; OK, or ERR_CUDA when a product gave up waiting for its copies."""
+    return int(_functions().onebit_layers_get_status(_stream_ptr(stream)))
+
+
+def clear_status(stream=None):
+    _check(_functions().onebit_layers_clear_status(_stream_ptr(stream)), "onebit_layers_clear_status")
+
+
+def set_fault_injection(kind: int, value: int = 0):
+    """Test hook of the whole process: FAULT_STALL_COPIES makes the following products' waits run out."""
+    _check(_functions().onebit_layers_set_fault_injection(int(kind), int(value)), "onebit_layers_set_fault_injection")
 
 
 def compress(x, stream=None) -> Checkpoint:

@@ -142,6 +142,19 @@ onebit_status_t onebit_linear_backward_workspace(const onebit_linear_grad_t* a, 
 onebit_status_t onebit_linear_backward(const onebit_linear_grad_t* a, void* workspace, size_t workspace_bytes,
                                        onebit_stream_t stream);
 
+/* ---- Status ----
+ *
+ * Synchronise `stream` and report the device's sticky flag: ONEBIT_OK, or ONEBIT_ERR_CUDA when some
+ * product gave up waiting (about one second) for its own asynchronous copies and stopped early; its
+ * outputs are then not meaningful.  The CUDA context stays usable. */
+onebit_status_t onebit_layers_get_status(onebit_stream_t stream);
+/* Clear the flag (enqueued on `stream`). */
+onebit_status_t onebit_layers_clear_status(onebit_stream_t stream);
+/* Test hook, of the whole process: with ONEBIT_FAULT_STALL_COPIES the products of the following calls
+ * wait for `value` bytes (1..2^19) that no copy delivers, so that their limited waits run out.
+ * ONEBIT_FAULT_NONE turns it off.  Nothing here makes the GPU fault. */
+onebit_status_t onebit_layers_set_fault_injection(int32_t kind, int64_t value);
+
 /* Message of the last call of this header that failed on the calling thread ("" if none). */
 const char* onebit_layers_last_error(void);
 

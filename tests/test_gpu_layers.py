@@ -524,6 +524,30 @@ def test_linear_past_32_bit_offsets():
     _within(back[2], sums, 2e-5 * y.double().abs().sum(0), "db")
 
 
+def test_a_wait_that_runs_out_is_reported():
+    """With the stall hook every product waits for bytes that no copy brings: its waits end after about a
+    second, the status says so, and the next product, with the hook off, is right again."""
+    gen = _gen(17)
+    x, w = _randn(gen, 600, 520, dtype=BF16), _randn(gen, 600, 520, dtype=BF16, scale=0.1)
+    big = _randn(gen, 4096, 256, dtype=BF16), _randn(gen, 4096, 256, dtype=BF16, scale=0.1)
+    want = L.linear(x, w), L.linear(*big)
+    assert L.get_status() == ob.OK
+    L.set_fault_injection(ob.FAULT_STALL_COPIES, 16)
+    try:
+        for a in ((x, w), big):  # both forms: one block a tile, and pairs
+            L.linear(*a)
+            assert L.get_status() == ob.ERR_CUDA
+            L.clear_status()
+            assert L.get_status() == ob.OK
+    finally:
+        L.set_fault_injection(ob.FAULT_NONE)
+    assert torch.equal(L.linear(x, w), want[0]) and torch.equal(L.linear(*big), want[1])
+    assert L.get_status() == ob.OK
+    for kind, value in ((ob.FAULT_STALL_COPIES, 0), (ob.FAULT_STALL_COPIES, 1 << 20), (ob.FAULT_FAIL_ALLOC, 1)):
+        with pytest.raises(ob.OneBitError):
+            L.set_fault_injection(kind, value)
+
+
 # ---------------------------------------------------------------- refusals
 
 
