@@ -38,9 +38,79 @@ int sm_count() {
 
 namespace {
 
+// Both kernels move every byte once and are bound by that.  Wide form: a thread has 16 columns (32 or 64
+// bytes in, 16 bytes of codes out), so that four threads share a scale and find the block's largest
+// magnitude with two shuffles; a block takes runs of about kCkRun elements of whole rows.  It needs rows
+// that start on 16 bytes and a multiple of 16 columns.  Any other matrix takes the narrow form: one warp
+// per 64 columns, a lane with two of them.
 constexpr int kCkThreads = 256;
+constexpr int kCkRun = 16384;
 
-// One warp per block of 64 columns of a row; a lane holds columns lane and lane + 32 of it.
+// Columns and rows of a run: unit u of a run is 16 columns of row u / (4 blocks).
+struct Wide {
+  int64_t rows;
+  int cols, blocks, run_rows;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kCkThreads) k_compress_wide(const T* __restrict__ x, int64_t ldx, Wide w, int8_t* __restrict__ codes,
+                                                              float* __restrict__ scales) {
+  const int per = 4 * w.blocks;
+  const int64_t runs = (w.rows + w.run_rows - 1) / w.run_rows;
+  for (int64_t run = blockIdx.x; run < runs; run += gridDim.x) {
+    const int64_t r0 = run * w.run_rows;
+    const int rows = (int)(w.rows - r0 < w.run_rows ? w.rows - r0 : w.run_rows), units = rows * per;
+    for (int u0 = 0; u0 < units; u0 += kCkThreads) {
+      const int u = u0 + threadIdx.x, r = u / per, g = u - r * per;
+      const bool on = u < units && g * 16 < w.cols;
+      float v[16];
+      float most = 0.0f;
+      if (on) {
+        const T* p = x + (r0 + r) * ldx + g * 16;
+        const Raw8<T> a = load8(p), b = load8(p + 8);
+        expand8(a, v);
+        expand8(b, v + 8);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) most = max_nan(most, fabsf(v[i]));
+      }
+      most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 1));
+      most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 2));
+      if (on) {
+        const BlockScale s = block_scale(most);
+        uint32_t c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = codes4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], s.inv);
+        *reinterpret_cast<uint4*>(codes + (r0 + r) * w.cols + g * 16) = make_uint4(c[0], c[1], c[2], c[3]);
+        if ((g & 3) == 0) scales[(r0 + r) * w.blocks + g / 4] = s.scale;
+      }
+    }
+  }
+}
+
+template <typename T, int ACT>
+__global__ void __launch_bounds__(kCkThreads) k_restore_wide(const int8_t* __restrict__ codes, const float* __restrict__ scales, Wide w,
+                                                             T* __restrict__ x, int64_t ldx) {
+  const int per = w.cols / 16;
+  const int64_t runs = (w.rows + w.run_rows - 1) / w.run_rows;
+  for (int64_t run = blockIdx.x; run < runs; run += gridDim.x) {
+    const int64_t r0 = run * w.run_rows;
+    const int rows = (int)(w.rows - r0 < w.run_rows ? w.rows - r0 : w.run_rows), units = rows * per;
+#pragma unroll 2
+    for (int u = threadIdx.x; u < units; u += kCkThreads) {
+      const int r = u / per, g = u - r * per;
+      const uint4 c = __ldg(reinterpret_cast<const uint4*>(codes + (r0 + r) * w.cols + g * 16));
+      const float s = __ldg(scales + (r0 + r) * w.blocks + g / 4);
+      float v[16];
+      values4<T>(c.x, s, v), values4<T>(c.y, s, v + 4), values4<T>(c.z, s, v + 8), values4<T>(c.w, s, v + 12);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = act_value<ACT>(v[i]);
+      T* p = x + (r0 + r) * ldx + g * 16;
+      store8(p, v);
+      store8(p + 8, v + 8);
+    }
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kCkThreads) k_compress(const T* __restrict__ x, int64_t ldx, int64_t rows, int cols,
                                                          int blocks, int8_t* __restrict__ codes,
@@ -73,9 +143,39 @@ __global__ void __launch_bounds__(kCkThreads) k_restore(const int8_t* __restrict
   }
 }
 
-int ck_grid(int64_t units) {
-  const int64_t most = (int64_t)sm_count() * 8, want = ceil_div(units, kCkThreads / 32);
-  return (int)(want < most ? want : most);
+bool wide_ok(const void* x, int64_t ldx, int32_t dtype, int64_t cols, const int8_t* codes) {
+  return aligned(x, 16) && (ldx * dtype_size(dtype)) % 16 == 0 && cols % 16 == 0 && aligned(codes, 16);
+}
+unsigned ck_grid(int64_t units) {
+  const int64_t most = (int64_t)sm_count() * 8;
+  return (unsigned)(units < most ? units : most);
+}
+
+template <typename T>
+void compress(const void* x, int64_t ldx, int32_t dtype, int64_t rows, int cols, int8_t* codes, float* scales, cudaStream_t s) {
+  const int blocks = (int)ceil_div(cols, kBlock);
+  const T* p = static_cast<const T*>(x);
+  if (wide_ok(x, ldx, dtype, cols, codes)) {
+    const Wide w{rows, cols, blocks, cols < kCkRun ? kCkRun / cols : 1};
+    k_compress_wide<T><<<ck_grid(ceil_div(rows, w.run_rows)), kCkThreads, 0, s>>>(p, ldx, w, codes, scales);
+  } else {
+    k_compress<T><<<ck_grid(ceil_div(rows * blocks, kCkThreads / 32)), kCkThreads, 0, s>>>(p, ldx, rows, cols, blocks, codes, scales);
+  }
+}
+template <typename T>
+void restore(const int8_t* codes, const float* scales, int64_t rows, int cols, int act, void* x, int64_t ldx, int32_t dtype, cudaStream_t s) {
+  const int blocks = (int)ceil_div(cols, kBlock);
+  T* p = static_cast<T*>(x);
+  if (wide_ok(x, ldx, dtype, cols, codes)) {
+    const Wide w{rows, cols, blocks, cols < kCkRun ? kCkRun / cols : 1};
+    const unsigned grid = ck_grid(ceil_div(rows, w.run_rows));
+    if (act == ONEBIT_ACT_NONE) k_restore_wide<T, ONEBIT_ACT_NONE><<<grid, kCkThreads, 0, s>>>(codes, scales, w, p, ldx);
+    else if (act == ONEBIT_ACT_RELU) k_restore_wide<T, ONEBIT_ACT_RELU><<<grid, kCkThreads, 0, s>>>(codes, scales, w, p, ldx);
+    else if (act == ONEBIT_ACT_GELU) k_restore_wide<T, ONEBIT_ACT_GELU><<<grid, kCkThreads, 0, s>>>(codes, scales, w, p, ldx);
+    else k_restore_wide<T, ONEBIT_ACT_GELU_TANH><<<grid, kCkThreads, 0, s>>>(codes, scales, w, p, ldx);
+  } else {
+    k_restore<T><<<ck_grid(ceil_div(rows * blocks, kCkThreads / 32)), kCkThreads, 0, s>>>(codes, scales, rows, cols, blocks, act, p, ldx);
+  }
 }
 
 }  // namespace
@@ -106,13 +206,9 @@ extern "C" onebit_status_t onebit_checkpoint_compress(const void* x, int64_t ldx
   if (!disjoint({matrix(x, rows, ldx, cols, dtype_size(dtype))}, {span_of(codes, rows * cols), span_of(scales, rows * blocks * 4)}))
     return fail(ONEBIT_ERR_INVALID_ARG, "an output overlaps another buffer");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int grid = ck_grid(rows * blocks);
-  if (dtype == ONEBIT_F32)
-    k_compress<<<grid, kCkThreads, 0, s>>>(static_cast<const float*>(x), ldx, rows, (int)cols, (int)blocks, codes, scales);
-  else if (dtype == ONEBIT_F16)
-    k_compress<<<grid, kCkThreads, 0, s>>>(static_cast<const __half*>(x), ldx, rows, (int)cols, (int)blocks, codes, scales);
-  else
-    k_compress<<<grid, kCkThreads, 0, s>>>(static_cast<const __nv_bfloat16*>(x), ldx, rows, (int)cols, (int)blocks, codes, scales);
+  if (dtype == ONEBIT_F32) compress<float>(x, ldx, dtype, rows, (int)cols, codes, scales, s);
+  else if (dtype == ONEBIT_F16) compress<__half>(x, ldx, dtype, rows, (int)cols, codes, scales, s);
+  else compress<__nv_bfloat16>(x, ldx, dtype, rows, (int)cols, codes, scales, s);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? ONEBIT_OK : cuda_fail(e, "onebit_checkpoint_compress");
 }
@@ -129,13 +225,9 @@ extern "C" onebit_status_t onebit_checkpoint_restore(const int8_t* codes, const 
   if (!disjoint({span_of(codes, rows * cols), span_of(scales, rows * blocks * 4)}, {matrix(x, rows, ldx, cols, dtype_size(dtype))}))
     return fail(ONEBIT_ERR_INVALID_ARG, "the output overlaps an input");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int grid = ck_grid(rows * blocks);
-  if (dtype == ONEBIT_F32)
-    k_restore<<<grid, kCkThreads, 0, s>>>(codes, scales, rows, (int)cols, (int)blocks, activation, static_cast<float*>(x), ldx);
-  else if (dtype == ONEBIT_F16)
-    k_restore<<<grid, kCkThreads, 0, s>>>(codes, scales, rows, (int)cols, (int)blocks, activation, static_cast<__half*>(x), ldx);
-  else
-    k_restore<<<grid, kCkThreads, 0, s>>>(codes, scales, rows, (int)cols, (int)blocks, activation, static_cast<__nv_bfloat16*>(x), ldx);
+  if (dtype == ONEBIT_F32) restore<float>(codes, scales, rows, (int)cols, activation, x, ldx, dtype, s);
+  else if (dtype == ONEBIT_F16) restore<__half>(codes, scales, rows, (int)cols, activation, x, ldx, dtype, s);
+  else restore<__nv_bfloat16>(codes, scales, rows, (int)cols, activation, x, ldx, dtype, s);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? ONEBIT_OK : cuda_fail(e, "onebit_checkpoint_restore");
 }

@@ -308,18 +308,6 @@ __device__ __forceinline__ void load_codes(char* staging, uint32_t (&v)[16], con
 }
 
 template <typename T>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi);
-template <>
-__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <>
-__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <typename T>
 __device__ __forceinline__ float2 unpack2(uint32_t v);
 template <>
 __device__ __forceinline__ float2 unpack2<__half>(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
@@ -327,7 +315,6 @@ template <>
 __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t v) {
   return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
-__device__ __forceinline__ float code_at(uint32_t word, int byte) { return (float)(int8_t)(word >> (8 * byte)); }
 
 // ------------------------------------------------------------------------------------------------
 // Epilogues.  run() has 64 columns from col0 on of the 32 rows from row0 on: a lane has row row0 + lane.
@@ -369,20 +356,20 @@ struct ForwardEpilogue {
       uint32_t c[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        c[i] = code_of(z[4 * i], s.inv) | code_of(z[4 * i + 1], s.inv) << 8 | code_of(z[4 * i + 2], s.inv) << 16 | code_of(z[4 * i + 3], s.inv) << 24;
+        c[i] = codes4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3], s.inv);
       if (row < rows) scales[row * blocks + col0 / kBlock] = s.scale;
       store_codes(staging, c, codes, row0, rows, col0, cols, vec_codes);
     }
     uint32_t v[32];
     if (act == ONEBIT_ACT_RELU) {
 #pragma unroll
-      for (int i = 0; i < 64; ++i) z[i] = act_value(ONEBIT_ACT_RELU, z[i]);
+      for (int i = 0; i < 64; ++i) z[i] = act_value<ONEBIT_ACT_RELU>(z[i]);
     } else if (act == ONEBIT_ACT_GELU) {
 #pragma unroll
-      for (int i = 0; i < 64; ++i) z[i] = act_value(ONEBIT_ACT_GELU, z[i]);
+      for (int i = 0; i < 64; ++i) z[i] = act_value<ONEBIT_ACT_GELU>(z[i]);
     } else if (act == ONEBIT_ACT_GELU_TANH) {
 #pragma unroll
-      for (int i = 0; i < 64; ++i) z[i] = act_value(ONEBIT_ACT_GELU_TANH, z[i]);
+      for (int i = 0; i < 64; ++i) z[i] = act_value<ONEBIT_ACT_GELU_TANH>(z[i]);
     }
     if (residual) {
       load_rows(staging, v, residual, ldr, row0, rows, col0, cols, vec_res);
@@ -421,17 +408,23 @@ struct InputGradEpilogue {
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
       const float2 z = unpack2<T>(v[i]);
-      d[2 * i] *= act_slope(ACT, z.x), d[2 * i + 1] *= act_slope(ACT, z.y);
-      v[i] = pack2<T>(act_value(ACT, z.x), act_value(ACT, z.y));
+      const ActPair p = act_pair<ACT, true, true>(z.x), q = act_pair<ACT, true, true>(z.y);
+      d[2 * i] *= p.slope, d[2 * i + 1] *= q.slope;
+      v[i] = pack2<T>(p.value, q.value);
     }
   }
   template <int ACT>
   __device__ __forceinline__ void slopes(float (&d)[64], const uint32_t (&c)[16], float s, uint32_t (&v)[32]) const {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float z0 = code_at(c[i / 2], (2 * i) & 3) * s, z1 = code_at(c[i / 2], (2 * i + 1) & 3) * s;
-      d[2 * i] *= act_slope(ACT, z0), d[2 * i + 1] *= act_slope(ACT, z1);
-      v[i] = pack2<T>(act_value(ACT, z0), act_value(ACT, z1));
+    for (int i = 0; i < 16; ++i) {
+      float z[4];
+      values4<T>(c[i], s, z);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const ActPair p = act_pair<ACT, true, true>(z[2 * j]), q = act_pair<ACT, true, true>(z[2 * j + 1]);
+        d[4 * i + 2 * j] *= p.slope, d[4 * i + 2 * j + 1] *= q.slope;
+        v[2 * i + j] = pack2<T>(p.value, q.value);
+      }
     }
   }
   __device__ __forceinline__ void run(float (&d)[64], int64_t row0, int64_t rows, int col0, int cols, int, char* staging) const {
