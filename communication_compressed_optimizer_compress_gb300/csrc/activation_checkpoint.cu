@@ -2,6 +2,7 @@
 // columns of a row.  See include/onebit_layers.h for the formulas.
 #include <stdio.h>
 
+#include <atomic>
 #include <string>
 
 #include "layers_common.cuh"
@@ -29,10 +30,12 @@ onebit_status_t cuda_fail(cudaError_t e, const char* where) {
 const char* error_text() { return t_error.c_str(); }
 
 int sm_count() {
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      n < 1)
-    return 1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 1;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 1;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

@@ -10,7 +10,7 @@ namespace {
 
 // Both passes are bound by the bytes of the rows.  A row is held in registers between its statistics and
 // its output, so that it is read once: TPR threads have a row, a thread CH groups of eight columns (and
-// the same columns of every row that it meets, so that gamma and beta stay in registers too).  Widths are
+// the same columns of every row that it meets, so that the parameters' gradients add up in registers too).  Widths are
 // served by the narrowest of the forms below; a wider row than the widest takes the re-reading kernels.
 //
 // In the wide form (VEC: rows on 16 bytes, a multiple of eight columns) a group is eight columns that lie
@@ -70,6 +70,22 @@ __device__ __forceinline__ void store_group(T* p, int t, int j, int cols, const 
   }
 }
 
+// gamma or beta of a group, 0 past the end: from L1, where it stays for every row
+template <int TPR, bool VEC>
+__device__ __forceinline__ void param_group(const float* p, int t, int j, int cols, float* f) {
+  if (VEC) {
+    const int c = Columns<TPR, true>::at(t, j, 0);
+    const Raw8<float> r = c < cols ? load8(p + c) : Raw8<float>{};
+    expand8(r, f);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int c = Columns<TPR, false>::at(t, j, e);
+      f[e] = c < cols ? __ldg(p + c) : 0.0f;
+    }
+  }
+}
+
 // Sums over the TPR threads of a row, the same order on every call; every thread gets them.  `red` has
 // room for two sets, used alternately, so that one barrier a call is enough.
 template <int TPR, int N>
@@ -110,22 +126,13 @@ template <int TPR>
 constexpr int kForwardThreads = TPR < 128 ? 128 : TPR;
 
 template <typename T, int TPR, int CH, bool VEC>
-__global__ void __launch_bounds__(kForwardThreads<TPR>, CH > 1 ? 1 : 1536 / kForwardThreads<TPR>) k_ln_forward(const ForwardArgs A) {
+__global__ void __launch_bounds__(kForwardThreads<TPR>, (CH > 1 ? TPR < 512 ? 768 : 512 : 1536) / kForwardThreads<TPR>) k_ln_forward(const ForwardArgs A) {
   constexpr int kGroups = kForwardThreads<TPR> / TPR;
   using Col = Columns<TPR, VEC>;
   __shared__ float red[2][32];
   const int t = threadIdx.x % TPR;
   const int64_t first = (int64_t)blockIdx.x * kGroups + threadIdx.x / TPR, step = (int64_t)gridDim.x * kGroups;
   int turn = 0;
-  float g[CH][8], b[CH][8];
-#pragma unroll
-  for (int j = 0; j < CH; ++j)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = Col::at(t, j, e);
-      g[j][e] = c < A.cols ? __ldg(A.gamma + c) : 0.0f;
-      b[j][e] = c < A.cols ? __ldg(A.beta + c) : 0.0f;
-    }
   RowInput<T, TPR, CH, VEC> in;
   if (first < A.rows) in.load(static_cast<const T*>(A.x) + first * A.ldx, t, A.cols);
   for (int64_t r = first; r < A.rows; r += step) {
@@ -186,9 +193,11 @@ __global__ void __launch_bounds__(kForwardThreads<TPR>, CH > 1 ? 1 : 1536 / kFor
     }
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      float y[8];
+      float y[8], g[8], b[8];
+      param_group<TPR, VEC>(A.gamma, t, j, A.cols, g);
+      param_group<TPR, VEC>(A.beta, t, j, A.cols, b);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = fmaf((x[j][e] - mean) * rstd, g[j][e], b[j][e]);
+      for (int e = 0; e < 8; ++e) y[e] = fmaf((x[j][e] - mean) * rstd, g[e], b[e]);
       store_group<T, TPR, VEC>(static_cast<T*>(A.y) + r * A.ldy, t, j, A.cols, y);
     }
   }
@@ -274,21 +283,19 @@ __global__ void __launch_bounds__(kBackThreads<TPR>, TPR < 256 ? 3 : 1) k_ln_bac
   const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
   const int64_t first = (int64_t)blockIdx.x * kGroups + group, step = (int64_t)gridDim.x * kGroups;
   int turn = 0;
-  float gamma[CH][8], dg[CH][8], db[CH][8];
+  launch_next();
+  float dg[CH][8], db[CH][8];
 #pragma unroll
   for (int j = 0; j < CH; ++j)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = Col::at(t, j, e);
-      gamma[j][e] = c < A.cols ? __ldg(A.gamma + c) : 0.0f;
-      dg[j][e] = db[j][e] = 0.0f;
-    }
+    for (int e = 0; e < 8; ++e) dg[j][e] = db[j][e] = 0.0f;
   KeptRow<T, TPR, CH, VEC, CODES> kept;
-  RowInput<T, TPR, CH, VEC> dyin;
+  RowInput<T, TPR, CH, VEC> dyin, addin, addnow;
   float mu = 0.0f, rs = 0.0f;
   auto load = [&](int64_t r) {
     kept.load(A, r, t);
     dyin.load(static_cast<const T*>(A.dy) + r * A.lddy, t, A.cols);
+    if (A.add) addin.load(static_cast<const T*>(A.add) + r * A.ldadd, t, A.cols);
     mu = __ldg(A.mean + r);
     rs = __ldg(A.rstd + r);
   };
@@ -299,6 +306,8 @@ __global__ void __launch_bounds__(kBackThreads<TPR>, TPR < 256 ? 3 : 1) k_ln_bac
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
+      float gamma[8];
+      param_group<TPR, VEC>(A.gamma, t, j, A.cols, gamma);
       kept.expand(j, xh[j]);
       dyin.expand(j, d[j]);
 #pragma unroll
@@ -307,13 +316,12 @@ __global__ void __launch_bounds__(kBackThreads<TPR>, TPR < 256 ? 3 : 1) k_ln_bac
         xh[j][e] = (xh[j][e] - mu) * rstd;
         dg[j][e] = fmaf(d[j][e], xh[j][e], dg[j][e]);
         db[j][e] += d[j][e];
-        d[j][e] *= gamma[j][e];
+        d[j][e] *= gamma[e];
         s[0] += d[j][e];
         s[1] = fmaf(d[j][e], xh[j][e], s[1]);
       }
     }
-    RowInput<T, TPR, CH, VEC> addin;
-    if (A.add) addin.load(static_cast<const T*>(A.add) + r * A.ldadd, t, A.cols);
+    if (A.add) addnow = addin;
     if (r + step < A.rows) load(r + step);  // under this row's sums
     row_sums<TPR>(s, red[group], turn, 1 + group);
     s[0] *= A.inv_cols;
@@ -325,7 +333,7 @@ __global__ void __launch_bounds__(kBackThreads<TPR>, TPR < 256 ? 3 : 1) k_ln_bac
       for (int e = 0; e < 8; ++e) o[e] = rstd * (d[j][e] - s[0] - xh[j][e] * s[1]);
       if (A.add) {
         float a[8];
-        addin.expand(j, a);
+        addnow.expand(j, a);
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] += a[e];
       }
@@ -455,30 +463,6 @@ __global__ void __launch_bounds__(kLnThreads) k_ln_param_wide(const BackwardArgs
   p[A.cols + c] = b;
 }
 
-// dgamma and dbeta: the blocks' shares, added in order.  A block has 32 of the 2*cols columns, eight
-// threads to each.
-template <typename G>
-__global__ void __launch_bounds__(256) k_ln_param_sum(const float* __restrict__ part, int parts, int cols, G* __restrict__ dgamma,
-                                                      G* __restrict__ dbeta) {
-  __shared__ float red[8][33];
-  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * 32 + lane, width = 2 * (int64_t)cols;
-  float s = 0.0f;
-  if (c < width) {
-#pragma unroll 8
-    for (int p = row; p < parts; p += 8) s += __ldg(part + p * width + c);
-  }
-  red[row][lane] = s;
-  __syncthreads();
-  if (row == 0 && c < width) {
-    float v = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v += red[i][lane];
-    if (c < cols) dgamma[c] = from_f<G>(v);
-    else dbeta[c - cols] = from_f<G>(v);
-  }
-}
-
 unsigned at_most(int64_t want, int64_t per_sm) {
   const int64_t most = (int64_t)sm_count() * per_sm;
   return (unsigned)(want < most ? want : most);
@@ -495,8 +479,8 @@ void launch_forward(const ForwardArgs& a, cudaStream_t s) {
   };
   using std::integral_constant;
   if (a.cols <= 256) go(integral_constant<int, 32>{}, integral_constant<int, 1>{}, 12);
-  else if (a.cols <= 1024) go(integral_constant<int, 128>{}, integral_constant<int, 1>{}, 12);
-  else if (a.cols <= 4096) go(integral_constant<int, 512>{}, integral_constant<int, 1>{}, 3);
+  else if (a.cols <= 1024) go(integral_constant<int, 32>{}, integral_constant<int, 4>{}, 6);
+  else if (a.cols <= 4096) go(integral_constant<int, 128>{}, integral_constant<int, 4>{}, 6);
   else if (a.cols <= kForwardCols) go(integral_constant<int, 512>{}, integral_constant<int, 4>{}, 1);
   else k_ln_forward_wide<T><<<at_most(a.rows, 8), kLnThreads, 0, s>>>(a);
 }
@@ -533,14 +517,8 @@ cudaError_t launch_backward(const BackwardArgs& a, cudaStream_t s) {
     if (a.codes) launch_backward<T, false, true>(a, parts, s);
     else launch_backward<T, false, false>(a, parts, s);
   }
-  auto sum = [&](auto* g) {
-    using G = std::remove_pointer_t<decltype(g)>;
-    k_ln_param_sum<G><<<(unsigned)ceil_div(2 * (int64_t)a.cols, 32), 256, 0, s>>>(a.part, parts, a.cols, static_cast<G*>(a.dgamma), static_cast<G*>(a.dbeta));
-  };
-  if (a.grad_dtype == ONEBIT_F32) sum((float*)nullptr);
-  else if (a.grad_dtype == ONEBIT_F16) sum((__half*)nullptr);
-  else sum((__nv_bfloat16*)nullptr);
-  return cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? sum_parts(a.grad_dtype, a.part, parts, 2 * (int64_t)a.cols, a.cols, a.dgamma, a.dbeta, s) : e;
 }
 
 onebit_status_t shape_ok(int64_t rows, int64_t cols) {

@@ -223,6 +223,39 @@ __device__ __forceinline__ float warp_max_nan(float v) {
 }
 
 // ------------------------------------------------------------------------------------------------
+// Kernels of one call follow each other with programmatic launches: the next kernel's blocks may start
+// when every block of the one before has started (and there is room), and wait where they need its
+// results.  A kernel that does not need them still waits before it ends, so that the end of a call's last
+// kernel is the end of them all.
+__device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Sums of `parts` partial rows of `width` fp32 columns, in a fixed order; columns below `split` go to lo,
+// the others to hi.  A block has 32 columns, 32 threads to each.
+constexpr int kSumRows = 32;
+template <typename G>
+static __global__ void __launch_bounds__(32 * kSumRows) k_sum_parts(const float* __restrict__ part, int64_t parts, int64_t width, int64_t split,
+                                                                    G* __restrict__ lo, G* __restrict__ hi) {
+  __shared__ float red[kSumRows][33];
+  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  wait_previous();
+  float s = 0.0f;
+  if (c < width) {
+#pragma unroll 8
+    for (int64_t p = row; p < parts; p += kSumRows) s += part[p * width + c];
+  }
+  red[row][lane] = s;
+  __syncthreads();
+  const float t = warp_sum(red[lane][row]);  // column `row` of the block's 32
+  const int64_t o = (int64_t)blockIdx.x * 32 + row;
+  if (lane == 0 && o < width) {
+    if (o < split) lo[o] = from_f<G>(t);
+    else hi[o - split] = from_f<G>(t);
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
 // host side
 
 // Records a message for onebit_layers_last_error() and returns the status.
@@ -256,6 +289,30 @@ inline bool disjoint(std::initializer_list<Span> in, std::initializer_list<Span>
 }
 inline bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <typename... Params, typename... Args>
+inline cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+template <typename G>
+inline cudaError_t sum_parts(const float* part, int64_t parts, int64_t width, int64_t split, void* lo, void* hi, cudaStream_t s) {
+  return launch_after(k_sum_parts<G>, dim3((unsigned)ceil_div(width, 32)), 32 * kSumRows, s, part, parts, width, split, static_cast<G*>(lo),
+                      static_cast<G*>(hi));
+}
+inline cudaError_t sum_parts(int32_t dtype, const float* part, int64_t parts, int64_t width, int64_t split, void* lo, void* hi, cudaStream_t s) {
+  return dtype == ONEBIT_F32   ? sum_parts<float>(part, parts, width, split, lo, hi, s)
+         : dtype == ONEBIT_F16 ? sum_parts<__half>(part, parts, width, split, lo, hi, s)
+                               : sum_parts<__nv_bfloat16>(part, parts, width, split, lo, hi, s);
+}
 
 // Widths and row counts beyond these have no use on one device; within them every element offset
 // fits 63 bits and every tile index 31.

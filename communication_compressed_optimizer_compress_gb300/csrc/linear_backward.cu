@@ -46,28 +46,49 @@ __global__ void __launch_bounds__(256) k_finish_dw(Partials c, int64_t rows, int
   }
 }
 
-// Column sums: part[chunk][cols] over runs of kRun rows, then their sum in chunk order.
-constexpr int kRun = 128;
-template <typename T>
-__global__ void __launch_bounds__(256) k_colsum_part(const T* __restrict__ dy, int64_t lddy, int64_t rows, int cols,
+// Column sums of dy over runs of kRun rows: a block has 256 columns, eight threads (one of each warp) to
+// every eight columns.  Behind a product of the same call it starts at once and reads dy on the SMs that
+// the product's tiles leave idle (dy was complete before the product began); one block then waits for the
+// product, so that this kernel ends after it.  As the call's first kernel it waits before it reads.
+constexpr int kRun = 512;
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) k_colsum_part(const T* __restrict__ dy, int64_t lddy, int64_t rows, int cols, bool wait_first,
                                                      float* __restrict__ part) {
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= cols) return;
-  for (int64_t ch = blockIdx.y; ch * kRun < rows; ch += gridDim.y) {
-    const int64_t end = (ch + 1) * kRun < rows ? (ch + 1) * kRun : rows;
-    float b = 0.0f;
-    for (int64_t r = ch * kRun; r < end; ++r) b += to_f(dy[r * lddy + c]);
-    part[ch * cols + c] = b;
+  __shared__ float red[8][256];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.x * 256;
+  launch_next();
+  if (wait_first) wait_previous();
+  for (int64_t run = blockIdx.y; run * kRun < rows; run += gridDim.y) {
+    const int64_t end = (run + 1) * kRun < rows ? (run + 1) * kRun : rows;
+    float s[8] = {};
+    if (VEC) {  // columns c0 + 8 lane ..
+      if (c0 + lane * 8 < cols) {
+#pragma unroll 8
+        for (int64_t r = run * kRun + warp; r < end; r += 8) {
+          float v[8];
+          expand8(load8(dy + r * lddy + c0 + lane * 8), v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s[i] += v[i];
+        }
+      }
+    } else {  // columns c0 + lane + 32 i
+#pragma unroll 4
+      for (int64_t r = run * kRun + warp; r < end; r += 8)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c0 + lane + 32 * i < cols) s[i] += to_f(dy[r * lddy + c0 + lane + 32 * i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) red[warp][VEC ? i * 32 + lane : lane + 32 * i] = s[i];
+    __syncthreads();
+    const int t = threadIdx.x, c = c0 + (VEC ? (t & 31) * 8 + t / 32 : t);
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) v += red[w][t];
+    if (c < cols) part[run * cols + c] = v;
+    __syncthreads();
   }
-}
-template <typename G>
-__global__ void __launch_bounds__(256) k_colsum_sum(const float* __restrict__ part, int64_t chunks, int cols,
-                                                    G* __restrict__ db) {
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= cols) return;
-  float b = 0.0f;
-  for (int64_t ch = 0; ch < chunks; ++ch) b += part[ch * cols + c];
-  db[c] = from_f<G>(b);
+  if (!wait_first && blockIdx.x == 0 && blockIdx.y == 0) wait_previous();
 }
 
 // Takes the workspace; with `run`, enqueues the work too.
@@ -121,10 +142,15 @@ cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, b
     const int64_t chunks = ceil_div(a.rows, kRun);
     float* part = ws.take<float>(chunks * a.out);
     if (run) {
-      const unsigned cgrid = (unsigned)ceil_div(a.out, 256);
-      k_colsum_part<T><<<dim3(cgrid, (unsigned)(chunks < 65535 ? chunks : 65535)), 256, 0, s>>>(static_cast<const T*>(a.dy), a.lddy, a.rows,
-                                                                                                (int)a.out, part);
-      with_grad(a.grad_dtype, a.db, [&](auto* g) { k_colsum_sum<<<cgrid, 256, 0, s>>>(part, chunks, (int)a.out, g); });
+      const T* p = static_cast<const T*>(dy.p);
+      const dim3 grid((unsigned)ceil_div(a.out, 256), (unsigned)(chunks < 65535 ? chunks : 65535));
+      const bool first = !a.dx && !a.dw;
+      // eight columns at a time where the last eight lie inside the row (a realigned copy is padded to them)
+      err = vec16(p, dy.ld) && (a.out % 8 == 0 || p != a.dy)
+                ? launch_after(k_colsum_part<T, true>, grid, 256, s, p, dy.ld, a.rows, (int)a.out, first, part)
+                : launch_after(k_colsum_part<T, false>, grid, 256, s, p, dy.ld, a.rows, (int)a.out, first, part);
+      if (err == cudaSuccess) err = sum_parts(a.grad_dtype, part, chunks, a.out, a.out, a.db, nullptr, s);
+      if (err != cudaSuccess) return err;
     }
   }
   return cudaGetLastError();

@@ -20,6 +20,8 @@
 
 #include <cuda.h>  // CUtensorMap: types only, the encoder is looked up at run time
 
+#include <atomic>
+
 #include "layers_common.cuh"
 
 namespace onebit {
@@ -217,18 +219,20 @@ struct RowStore {  // 128/sizeof(T) columns from col0 on
       *reinterpret_cast<uint4*>(staging + lane * kStagingRow + j * 16) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
     __syncwarp();
     const int c = (lane & 7) * kVec;
-    if (vec && col0 + kCols <= cols) {
+    if (vec && (col0 + kCols <= cols || cols % kVec == 0)) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int r = i * 4 + (lane >> 3);
-        if (row0 + r < rows)
+        if (row0 + r < rows && col0 + c < cols)
           *reinterpret_cast<uint4*>(p + (row0 + r) * ld + col0 + c) =
               *reinterpret_cast<const uint4*>(staging + r * kStagingRow + (lane & 7) * 16);
       }
     } else {
-      for (int r = 0; r < 32 && row0 + r < rows; ++r)
-        for (int q = lane; q < kCols && col0 + q < cols; q += 32)
-          p[(row0 + r) * ld + col0 + q] = reinterpret_cast<const T*>(staging + r * kStagingRow)[q];
+#pragma unroll 8
+      for (int r = 0; r < 32; ++r)
+#pragma unroll
+        for (int q = lane; q < kCols; q += 32)
+          if (row0 + r < rows && col0 + q < cols) p[(row0 + r) * ld + col0 + q] = reinterpret_cast<const T*>(staging + r * kStagingRow)[q];
     }
     __syncwarp();
   }
@@ -238,20 +242,27 @@ template <typename T>  // a 16-bit type: 64 columns
 __device__ __forceinline__ void load_rows(char* staging, uint32_t (&v)[32], const T* p, int64_t ld, int64_t row0, int64_t rows, int col0, int cols,
                                           bool vec) {
   const int lane = threadIdx.x & 31;
-  if (vec && col0 + 64 <= cols) {
+  if (vec && (col0 + 64 <= cols || cols % 8 == 0)) {
     uint4 t[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int r = i * 4 + (lane >> 3);
-      t[i] = row0 + r < rows ? *reinterpret_cast<const uint4*>(p + (row0 + r) * ld + col0 + (lane & 7) * 8) : make_uint4(0, 0, 0, 0);
+      t[i] = row0 + r < rows && col0 + (lane & 7) * 8 < cols ? *reinterpret_cast<const uint4*>(p + (row0 + r) * ld + col0 + (lane & 7) * 8) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       *reinterpret_cast<uint4*>(staging + (i * 4 + (lane >> 3)) * kStagingRow + (lane & 7) * 16) = t[i];
   } else {
-    for (int r = 0; r < 32; ++r)
-      for (int q = lane; q < 64; q += 32)
-        reinterpret_cast<T*>(staging + r * kStagingRow)[q] = row0 + r < rows && col0 + q < cols ? p[(row0 + r) * ld + col0 + q] : from_f<T>(0.0f);
+    for (int r0 = 0; r0 < 32; r0 += 8) {  // sixteen loads in flight
+      T t[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int r = r0 + i / 2, q = lane + 32 * (i & 1);
+        t[i] = row0 + r < rows && col0 + q < cols ? p[(row0 + r) * ld + col0 + q] : from_f<T>(0.0f);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) reinterpret_cast<T*>(staging + (r0 + i / 2) * kStagingRow)[lane + 32 * (i & 1)] = t[i];
+    }
   }
   __syncwarp();
 #pragma unroll
@@ -270,33 +281,44 @@ __device__ __forceinline__ void store_codes(char* staging, const uint32_t (&v)[1
   for (int j = 0; j < 4; ++j)
     *reinterpret_cast<uint4*>(staging + lane * kCodeRow + j * 16) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
   __syncwarp();
-  if (vec && col0 + 64 <= cols) {
+  if (vec) {  // cols is a multiple of 16
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = i * 8 + (lane >> 2);
-      if (row0 + r < rows)
+      if (row0 + r < rows && col0 + (lane & 3) * 16 < cols)
         *reinterpret_cast<uint4*>(p + (row0 + r) * cols + col0 + (lane & 3) * 16) = *reinterpret_cast<const uint4*>(staging + r * kCodeRow + (lane & 3) * 16);
     }
   } else {
-    for (int r = 0; r < 32 && row0 + r < rows; ++r)
-      for (int q = lane; q < 64 && col0 + q < cols; q += 32) p[(row0 + r) * cols + col0 + q] = (staging + r * kCodeRow)[q];
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r)
+#pragma unroll
+      for (int q = lane; q < 64; q += 32)
+        if (row0 + r < rows && col0 + q < cols) p[(row0 + r) * cols + col0 + q] = (staging + r * kCodeRow)[q];
   }
   __syncwarp();
 }
 __device__ __forceinline__ void load_codes(char* staging, uint32_t (&v)[16], const int8_t* p, int64_t row0, int64_t rows, int col0, int cols, bool vec) {
   const int lane = threadIdx.x & 31;
-  if (vec && col0 + 64 <= cols) {
+  if (vec) {
     uint4 t[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = i * 8 + (lane >> 2);
-      t[i] = row0 + r < rows ? *reinterpret_cast<const uint4*>(p + (row0 + r) * cols + col0 + (lane & 3) * 16) : make_uint4(0, 0, 0, 0);
+      t[i] = row0 + r < rows && col0 + (lane & 3) * 16 < cols ? *reinterpret_cast<const uint4*>(p + (row0 + r) * cols + col0 + (lane & 3) * 16) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(staging + (i * 8 + (lane >> 2)) * kCodeRow + (lane & 3) * 16) = t[i];
   } else {
-    for (int r = 0; r < 32; ++r)
-      for (int q = lane; q < 64; q += 32) (staging + r * kCodeRow)[q] = row0 + r < rows && col0 + q < cols ? p[(row0 + r) * cols + col0 + q] : 0;
+    for (int r0 = 0; r0 < 32; r0 += 8) {
+      int8_t t[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int r = r0 + i / 2, q = lane + 32 * (i & 1);
+        t[i] = row0 + r < rows && col0 + q < cols ? p[(row0 + r) * cols + col0 + q] : (int8_t)0;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) (staging + (r0 + i / 2) * kCodeRow)[lane + 32 * (i & 1)] = t[i];
+    }
   }
   __syncwarp();
 #pragma unroll
@@ -545,6 +567,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
   if (CTAS == 2) cluster_sync();  // the other block's barriers are ready too
   tmem_fence_after();
   const uint32_t tmem = *tmem_ptr;
+  launch_next();
 
   // the epilogue warps take the registers that the control warps do not need
   if (warp >= 4) {
@@ -728,8 +751,16 @@ struct Operand {
 template <int CTAS, bool A_MN, bool B_MN, class Epilogue>
 cudaError_t launch_product(const ProductArgs& P, const Epilogue& E, int sms, cudaStream_t s) {
   auto* kernel = k_product<CTAS, A_MN, B_MN, Epilogue>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem);
+  static std::atomic<uint64_t> ready{0};  // devices on which this kernel may use its shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
   const int64_t units = (int64_t)P.tiles_m * P.tiles_n * P.splits, most = sms / CTAS;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((units < most ? units : most) * CTAS));

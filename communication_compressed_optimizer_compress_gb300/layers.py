@@ -108,28 +108,26 @@ def _code(dtype, what: str) -> int:
 
 def _matrix(t, name: str, cols=None, rows=None, dtype=None, device=None):
     """(rows, columns, row stride) of a tensor whose last dimension is the features."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
     shape = t.shape
-    if not t.is_cuda or t.dim() < 1:
-        raise ValueError(f"{name}: expected a CUDA tensor of at least one dimension")
-    c = shape[-1]
-    if t.dim() == 2:
-        r = shape[0]
+    if len(shape) == 2:
+        r, c = shape
         ld, unit = t.stride()
-        if (c > 1 and unit != 1) or (r > 1 and ld < c):
+        if (unit != 1 and c > 1) or (ld < c and r > 1):
             raise ValueError(f"{name}: the last dimension needs unit stride and rows that do not overlap")
         if r <= 1 or ld < c:
             ld = c
     else:
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: a tensor that is not 2-D must be contiguous")
-        r, ld = (t.numel() // c if c else 0), c
+        if not shape or not t.is_contiguous():
+            raise ValueError(f"{name}: a tensor that is not 2-D must be contiguous, of at least one dimension")
+        c = ld = shape[-1]
+        r = t.numel() // c if c else 0
     if c < 1:
         raise ValueError(f"{name}: no columns")
-    if cols is not None and c != cols:
-        raise ValueError(f"{name}: expected {cols} columns, got {c}")
-    if rows is not None and r != rows:
-        raise ValueError(f"{name}: expected {rows} rows, got {r}")
-    if dtype is not None and t.dtype != dtype:
+    if (cols is not None and c != cols) or (rows is not None and r != rows):
+        raise ValueError(f"{name}: expected {rows if rows is not None else r} x {cols if cols is not None else c}, got {r} x {c}")
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     if device is not None and t.device != device:
         raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
@@ -137,10 +135,10 @@ def _matrix(t, name: str, cols=None, rows=None, dtype=None, device=None):
 
 
 def _vector(t, name: str, n: int, device, dtype=torch.float32):
-    """Pointer of a contiguous vector of n values (None: 0)."""
+    """Pointer of a contiguous vector of n values (None: none)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or t.device != device:
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name}: expected {n} contiguous {dtype} values on {device}")
     return t.data_ptr()
 
@@ -162,25 +160,28 @@ def _kept(x, name: str, cols=None, rows=None, dtype=None, device=None):
     return None, 0, codes.data_ptr(), s, r, c, x.dtype, codes.device, codes.shape
 
 
-class _On:
-    """Runs the body with `stream` current (None: as is), so that its outputs and workspace belong to it."""
+def _on(stream):
+    """Makes `stream` current (None: as is), so that outputs and workspaces belong to the stream that writes
+    them."""
+    return _HERE if stream is None else torch.cuda.stream(stream)
 
-    __slots__ = ("ctx",)
 
-    def __init__(self, stream):
-        self.ctx = None if stream is None else torch.cuda.stream(stream)
+class _Here:
+    __slots__ = ()
 
     def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
+        pass
 
     def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+        pass
+
+
+_HERE = _Here()
 
 
 def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    """The handle of the device's current stream (without making a Stream object, most of a small call)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _new_checkpoint(shape, dtype, device):
@@ -211,7 +212,7 @@ def compress(x, stream=None) -> Checkpoint:
     """The 8-bit checkpoint of x."""
     rows, cols, ld = _matrix(x, "x")
     code = _code(x.dtype, "x")
-    with _On(stream):
+    with _on(stream):
         ck = _new_checkpoint(x.shape, x.dtype, x.device)
         _check(_functions().onebit_checkpoint_compress(x.data_ptr(), ld, code, rows, cols, ck.codes.data_ptr(),
                                                        ck.scales.data_ptr(), _stream(x.device)),
@@ -223,7 +224,7 @@ def restore(ck: Checkpoint, activation=ACT_NONE, stream=None):
     """activation(the values a checkpoint stands for), in the checkpoint's dtype."""
     _, _, codes, scales, rows, cols, dtype, device, shape = _kept(ck, "ck")
     code = _code(dtype, "ck")
-    with _On(stream):
+    with _on(stream):
         x = torch.empty(shape, dtype=dtype, device=device)
         _check(_functions().onebit_checkpoint_restore(codes, scales, rows, cols, activation, x.data_ptr(), cols, code,
                                                       _stream(device)), "onebit_checkpoint_restore")
@@ -235,10 +236,10 @@ def layer_norm(x, gamma, beta, eps=1e-5, checkpoint=False, stream=None):
     rows, cols, ld = _matrix(x, "x")
     code, device = _code(x.dtype, "x"), x.device
     g, b = _vector(gamma, "gamma", cols, device), _vector(beta, "beta", cols, device)
-    with _On(stream):
-        y = torch.empty(x.shape, dtype=x.dtype, device=device)
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
+    with _on(stream):
+        y = x.new_empty(x.shape)
+        mean = gamma.new_empty(x.shape[:-1])
+        rstd = gamma.new_empty(x.shape[:-1])
         ck = _new_checkpoint(x.shape, x.dtype, device) if checkpoint else None
         _check(_functions().onebit_layer_norm_forward(
             x.data_ptr(), ld, code, rows, cols, g, b, eps, y.data_ptr(), cols, mean.data_ptr(), rstd.data_ptr(),
@@ -256,8 +257,8 @@ def layer_norm_backward(dy, x, gamma, mean, rstd, add=None, grad_dtype=torch.flo
     mu, rs = _vector(mean, "mean", rows, device), _vector(rstd, "rstd", rows, device)
     ap, lda = (add.data_ptr(), _matrix(add, "add", cols, rows, dy.dtype, device)[2]) if add is not None else (None, 0)
     fn, need = _functions(), ctypes.c_size_t()
-    with _On(stream):
-        dx = torch.empty(dy.shape, dtype=dy.dtype, device=device)
+    with _on(stream):
+        dx = dy.new_empty(dy.shape)
         dgamma = torch.empty(cols, dtype=grad_dtype, device=device)
         dbeta = torch.empty(cols, dtype=grad_dtype, device=device)
         _check(fn.onebit_layer_norm_backward_workspace(rows, cols, ctypes.byref(need)),
@@ -282,8 +283,8 @@ def linear(x, w, bias=None, activation=ACT_NONE, residual=None, checkpoint=False
     rp, ldr = (residual.data_ptr(), _matrix(residual, "residual", out, rows, dtype, device)[2]) if residual is not None else (None, 0)
     shape = (*x.shape[:-1], out)
     fn, need = _functions(), ctypes.c_size_t()
-    with _On(stream):
-        y = torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream):
+        y = x.new_empty(shape)
         ck = _new_checkpoint(shape, dtype, device) if checkpoint else None
         a = LinearArgs(x.data_ptr(), ldx, w.data_ptr(), ldw, bp, rp, ldr, y.data_ptr(), out,
                        ck.codes.data_ptr() if ck else None, ck.scales.data_ptr() if ck else None, rows, cols, out, code,
@@ -315,8 +316,8 @@ def linear_backward(dy, x, w, activation=ACT_NONE, add=None, grad_dtype=None, dw
     ap, lda = (add.data_ptr(), _matrix(add, "add", cols, rows, dtype, device)[2]) if add is not None else (None, 0)
     want_dx, want_dw, want_db = "dx" in need, "dw" in need, "db" in need
     fn, bytes_ = _functions(), ctypes.c_size_t()
-    with _On(stream):
-        dx = torch.empty((*dy.shape[:-1], cols), dtype=dtype, device=device) if want_dx else None
+    with _on(stream):
+        dx = dy.new_empty((*dy.shape[:-1], cols)) if want_dx else None
         if want_dw and dw is None:
             dw = torch.empty((out, cols), dtype=grad_dtype, device=device)
         if want_db and db is None:
