@@ -66,15 +66,15 @@ __global__ void __launch_bounds__(kCkThreads) k_compress_wide(const T* __restric
     for (int u0 = 0; u0 < units; u0 += kCkThreads) {
       const int u = u0 + threadIdx.x, r = u / per, g = u - r * per;
       const bool on = u < units && g * 16 < w.cols;
-      float v[16];
+      f2 v[8];
       float most = 0.0f;
       if (on) {
         const T* p = x + (r0 + r) * ldx + g * 16;
         const Raw8<T> a = load8(p), b = load8(p + 8);
         expand8(a, v);
-        expand8(b, v + 8);
+        expand8(b, v + 4);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) most = max_nan(most, fabsf(v[i]));
+        for (int i = 0; i < 8; ++i) most = max_abs(most, v[i]);
       }
       most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 1));
       most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 2));
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kCkThreads) k_compress_wide(const T* __restric
         const BlockScale s = block_scale(most);
         uint32_t c[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = codes4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], s.inv);
+        for (int i = 0; i < 4; ++i) c[i] = codes4(v[2 * i], v[2 * i + 1], s.inv);
         *reinterpret_cast<uint4*>(codes + (r0 + r) * w.cols + g * 16) = make_uint4(c[0], c[1], c[2], c[3]);
         if ((g & 3) == 0) scales[(r0 + r) * w.blocks + g / 4] = s.scale;
       }
@@ -103,13 +103,13 @@ __global__ void __launch_bounds__(kCkThreads) k_restore_wide(const int8_t* __res
       const int r = u / per, g = u - r * per;
       const uint4 c = __ldg(reinterpret_cast<const uint4*>(codes + (r0 + r) * w.cols + g * 16));
       const float s = __ldg(scales + (r0 + r) * w.blocks + g / 4);
-      float v[16];
-      values4<T>(c.x, s, v), values4<T>(c.y, s, v + 4), values4<T>(c.z, s, v + 8), values4<T>(c.w, s, v + 12);
+      f2 v[8];
+      values4<T>(c.x, s, v), values4<T>(c.y, s, v + 2), values4<T>(c.z, s, v + 4), values4<T>(c.w, s, v + 6);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = act_value<ACT>(v[i]);
+      for (int i = 0; i < 8; ++i) v[i] = act2<ACT>(v[i]);
       T* p = x + (r0 + r) * ldx + g * 16;
       store8(p, v);
-      store8(p + 8, v + 8);
+      store8(p + 8, v + 4);
     }
   }
 }

@@ -37,7 +37,7 @@ struct RowInput<T, TPR, CH, true> {
       else raw[j] = Raw8<T>{};
     }
   }
-  __device__ __forceinline__ void expand(int j, float* f) const { expand8(raw[j], f); }
+  __device__ __forceinline__ void expand(int j, f2* f) const { expand8(raw[j], f); }
 };
 template <typename T, int TPR, int CH>
 struct RowInput<T, TPR, CH, false> {
@@ -51,37 +51,39 @@ struct RowInput<T, TPR, CH, false> {
         raw[j][e] = c < cols ? p[c] : from_f<T>(0.0f);
       }
   }
-  __device__ __forceinline__ void expand(int j, float* f) const {
+  __device__ __forceinline__ void expand(int j, f2* f) const {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = to_f(raw[j][e]);
+    for (int e = 0; e < 4; ++e) f[e] = pair(to_f(raw[j][2 * e]), to_f(raw[j][2 * e + 1]));
   }
 };
 template <typename T, int TPR, bool VEC>
-__device__ __forceinline__ void store_group(T* p, int t, int j, int cols, const float* f) {
+__device__ __forceinline__ void store_group(T* p, int t, int j, int cols, const f2* f) {
   if (VEC) {
     const int c = Columns<TPR, true>::at(t, j, 0);
     if (c < cols) store8(p + c, f);
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = Columns<TPR, false>::at(t, j, e);
-      if (c < cols) p[c] = from_f<T>(f[e]);
+    for (int e = 0; e < 4; ++e) {  // columns c and c + 32
+      const int c = Columns<TPR, false>::at(t, j, 2 * e);
+      const float2 h = halves(f[e]);
+      if (c < cols) p[c] = from_f<T>(h.x);
+      if (c + 32 < cols) p[c + 32] = from_f<T>(h.y);
     }
   }
 }
 
 // gamma or beta of a group, 0 past the end: from L1, where it stays for every row
 template <int TPR, bool VEC>
-__device__ __forceinline__ void param_group(const float* p, int t, int j, int cols, float* f) {
+__device__ __forceinline__ void param_group(const float* p, int t, int j, int cols, f2* f) {
   if (VEC) {
     const int c = Columns<TPR, true>::at(t, j, 0);
     const Raw8<float> r = c < cols ? load8(p + c) : Raw8<float>{};
     expand8(r, f);
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = Columns<TPR, false>::at(t, j, e);
-      f[e] = c < cols ? __ldg(p + c) : 0.0f;
+    for (int e = 0; e < 4; ++e) {
+      const int c = Columns<TPR, false>::at(t, j, 2 * e);
+      f[e] = pair(c < cols ? __ldg(p + c) : 0.0f, c + 32 < cols ? __ldg(p + c + 32) : 0.0f);
     }
   }
 }
@@ -125,81 +127,122 @@ struct ForwardArgs {
 template <int TPR>
 constexpr int kForwardThreads = TPR < 128 ? 128 : TPR;
 
-template <typename T, int TPR, int CH, bool VEC>
-__global__ void __launch_bounds__(kForwardThreads<TPR>, (CH > 1 ? TPR < 512 ? 768 : 512 : 1536) / kForwardThreads<TPR>) k_ln_forward(const ForwardArgs A) {
+// NR rows at a time: their sums go through the shuffles and the barrier together, and gamma and beta are
+// read (from L1) once for them.  Bound by instruction issue first and by DRAM next: fewer threads with more
+// columns each pay the fixed cost of a row less often.  16384 x 1024 bf16 with the checkpoint: one block of
+// 128 threads a row 28 us, a warp a row 26 us (gamma and beta took 62% of the L1's cycles).
+template <typename T, int TPR, int CH, int NR, bool VEC>
+__global__ void __launch_bounds__(kForwardThreads<TPR>, (TPR < 256 ? 640 : 512) / kForwardThreads<TPR>) k_ln_forward(const ForwardArgs A) {
   constexpr int kGroups = kForwardThreads<TPR> / TPR;
   using Col = Columns<TPR, VEC>;
-  __shared__ float red[2][32];
-  const int t = threadIdx.x % TPR;
-  const int64_t first = (int64_t)blockIdx.x * kGroups + threadIdx.x / TPR, step = (int64_t)gridDim.x * kGroups;
+  __shared__ float red[kGroups][2][NR * 32];
+  const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
+  const int64_t first = ((int64_t)blockIdx.x * kGroups + group) * NR, step = (int64_t)gridDim.x * kGroups * NR;
   int turn = 0;
-  RowInput<T, TPR, CH, VEC> in;
-  if (first < A.rows) in.load(static_cast<const T*>(A.x) + first * A.ldx, t, A.cols);
+  RowInput<T, TPR, CH, VEC> in[NR];
+  const T* px = static_cast<const T*>(A.x) + first * A.ldx;
+  T* py = static_cast<T*>(A.y) + first * A.ldy;
+  auto load = [&](int64_t r) {
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+      if (r + n < A.rows) in[n].load(px + n * A.ldx, t, A.cols);
+  };
+  load(first);
   for (int64_t r = first; r < A.rows; r += step) {
-    float x[CH][8];
+    f2 x[NR][CH][4];
+    float mean[NR], rstd[NR];
 #pragma unroll
-    for (int j = 0; j < CH; ++j) in.expand(j, x[j]);
-    if (r + step < A.rows) in.load(static_cast<const T*>(A.x) + (r + step) * A.ldx, t, A.cols);  // under this row's work
-    float s[1] = {0.0f};
+    for (int n = 0; n < NR; ++n)
 #pragma unroll
-    for (int j = 0; j < CH; ++j)
+      for (int j = 0; j < CH; ++j) in[n].expand(j, x[n][j]);
+    px += step * A.ldx;
+    load(r + step);  // under these rows' work
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[0] += x[j][e];
-    row_sums<TPR>(s, red, turn, 1);
-    const float mean = s[0] * A.inv_cols;
-    s[0] = 0.0f;
+    for (int n = 0; n < NR; ++n) {
+      f2 s = 0;
 #pragma unroll
-    for (int j = 0; j < CH; ++j)
+      for (int j = 0; j < CH; ++j)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float d = Col::at(t, j, e) < A.cols ? x[j][e] - mean : 0.0f;
-        s[0] = fmaf(d, d, s[0]);
-      }
-    row_sums<TPR>(s, red, turn, 1);
-    const float rstd = 1.0f / sqrtf(fmaf(s[0], A.inv_cols, A.eps));
-    if (t == 0) {
-      A.mean[r] = mean;
-      A.rstd[r] = rstd;
+        for (int e = 0; e < 4; ++e) s = add2(s, x[n][j][e]);
+      mean[n] = sum_of(s);
     }
+    row_sums<TPR>(mean, red[group], turn, 1 + group);
     if (A.codes) {
-      int8_t* codes = A.codes + r * A.cols;
-      float* scales = A.scales + r * A.blocks;
 #pragma unroll
-      for (int j = 0; j < CH; ++j) {
-        if (VEC) {  // a block is eight neighbouring lanes
-          const int c = Col::at(t, j, 0);
-          float most = 0.0f;
+      for (int n = 0; n < NR; ++n) {
+        if (r + n >= A.rows) continue;
+        int8_t* codes = A.codes + (r + n) * A.cols;
+        float* scales = A.scales + (r + n) * A.blocks;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) most = max_nan(most, fabsf(x[j][e]));
+        for (int j = 0; j < CH; ++j) {
+          const f2* v = x[n][j];
+          if (VEC) {  // a block is eight neighbouring lanes
+            const int c = Col::at(t, j, 0);
+            float most = 0.0f;
 #pragma unroll
-          for (int o = 1; o < 8; o *= 2) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
-          const BlockScale q = block_scale(most);
-          if (c < A.cols) {
-            *reinterpret_cast<uint2*>(codes + c) = make_uint2(codes4(x[j][0], x[j][1], x[j][2], x[j][3], q.inv), codes4(x[j][4], x[j][5], x[j][6], x[j][7], q.inv));
-            if ((t & 7) == 0) scales[c / kBlock] = q.scale;
-          }
-        } else {  // a block is two columns of every lane
+            for (int e = 0; e < 4; ++e) most = max_abs(most, v[e]);
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const int c = Col::at(t, j, e), c0 = c - (t & 31);
-            if (c0 >= A.cols) continue;
-            const BlockScale q = block_scale(warp_max_nan(max_nan(fabsf(x[j][e]), fabsf(x[j][e + 1]))));
-            if (c < A.cols) codes[c] = (int8_t)code_of(x[j][e], q.inv);
-            if (c + 32 < A.cols) codes[c + 32] = (int8_t)code_of(x[j][e + 1], q.inv);
-            if ((t & 31) == 0) scales[c0 / kBlock] = q.scale;
+            for (int o = 1; o < 8; o *= 2) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
+            const BlockScale q = block_scale(most);
+            if (c < A.cols) {
+              *reinterpret_cast<uint2*>(codes + c) = make_uint2(codes4(v[0], v[1], q.inv), codes4(v[2], v[3], q.inv));
+              if ((t & 7) == 0) scales[c / kBlock] = q.scale;
+            }
+          } else {  // a block is two columns of every lane
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int c = Col::at(t, j, 2 * e), c0 = c - (t & 31);
+              if (c0 >= A.cols) continue;
+              const BlockScale q = block_scale(warp_max_nan(max_abs(0.0f, v[e])));
+              const float2 h = halves(v[e]);
+              if (c < A.cols) codes[c] = (int8_t)code_of(h.x, q.inv);
+              if (c + 32 < A.cols) codes[c + 32] = (int8_t)code_of(h.y, q.inv);
+              if ((t & 31) == 0) scales[c0 / kBlock] = q.scale;
+            }
           }
         }
       }
     }
+    // from here on x is its distance from the mean
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      mean[n] *= A.inv_cols;
+      f2 s = 0;
+#pragma unroll
+      for (int j = 0; j < CH; ++j) {
+        const f2 shift = VEC && Col::at(t, j, 0) >= A.cols ? 0 : splat(-mean[n]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int c = Col::at(t, j, 2 * e);
+          x[n][j][e] = add2(x[n][j][e], VEC ? shift : pair(c < A.cols ? -mean[n] : 0.0f, c + 32 < A.cols ? -mean[n] : 0.0f));
+          s = fma2(x[n][j][e], x[n][j][e], s);
+        }
+      }
+      rstd[n] = sum_of(s);
+    }
+    row_sums<TPR>(rstd, red[group], turn, 1 + group);
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      rstd[n] = rsqrtf(fmaf(rstd[n], A.inv_cols, A.eps));
+      if (t == 0 && r + n < A.rows) {
+        A.mean[r + n] = mean[n];
+        A.rstd[r + n] = rstd[n];
+      }
+    }
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      float y[8], g[8], b[8];
+      f2 g[4], b[4];
       param_group<TPR, VEC>(A.gamma, t, j, A.cols, g);
       param_group<TPR, VEC>(A.beta, t, j, A.cols, b);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = fmaf((x[j][e] - mean) * rstd, g[e], b[e]);
-      store_group<T, TPR, VEC>(static_cast<T*>(A.y) + r * A.ldy, t, j, A.cols, y);
+      for (int n = 0; n < NR; ++n) {
+        f2 y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = fma2(mul2(x[n][j][e], splat(rstd[n])), g[e], b[e]);
+        if (r + n < A.rows) store_group<T, TPR, VEC>(py + n * A.ldy, t, j, A.cols, y);
+      }
     }
+    py += step * A.ldy;
   }
 }
 
@@ -226,119 +269,157 @@ struct BackwardArgs {
 template <int TPR>
 constexpr int kBackThreads = TPR < 256 ? 256 : TPR;
 
-// The kept input of one thread's columns: values, or codes with the scale of their block.
+// The kept input of one thread's columns: values, or codes with the scale of their block.  normal() gives
+// the normalised values x rstd - mean rstd, one operation each.
 template <typename T, int TPR, int CH, bool VEC, bool CODES>
 struct KeptRow;
 template <typename T, int TPR, int CH, bool VEC>
 struct KeptRow<T, TPR, CH, VEC, false> {
   RowInput<T, TPR, CH, VEC> in;
-  __device__ __forceinline__ void load(const BackwardArgs& A, int64_t r, int t) { in.load(static_cast<const T*>(A.x) + r * A.ldx, t, A.cols); }
-  __device__ __forceinline__ void expand(int j, float* f) const { in.expand(j, f); }
+  const T* p;
+  int64_t step;
+  __device__ __forceinline__ KeptRow(const BackwardArgs& A, int64_t first, int64_t rows) : p(static_cast<const T*>(A.x) + first * A.ldx), step(rows * A.ldx) {}
+  __device__ __forceinline__ void load(int t, int cols) {
+    in.load(p, t, cols);
+    p += step;
+  }
+  __device__ __forceinline__ void normal(int j, float rstd, float shift, f2* f) const {
+    in.expand(j, f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = fma2(f[e], splat(rstd), splat(shift));
+  }
 };
 template <typename T, int TPR, int CH>
 struct KeptRow<T, TPR, CH, true, true> {
   uint2 raw[CH];
   float scale[CH];
-  __device__ __forceinline__ void load(const BackwardArgs& A, int64_t r, int t) {
+  const int8_t* p;
+  const float* q;
+  int64_t step, qstep;
+  __device__ __forceinline__ KeptRow(const BackwardArgs& A, int64_t first, int64_t rows)
+      : p(A.codes + first * A.cols), q(A.scales + first * A.blocks), step(rows * A.cols), qstep(rows * A.blocks) {}
+  __device__ __forceinline__ void load(int t, int cols) {
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
       const int c = Columns<TPR, true>::at(t, j, 0);
-      raw[j] = c < A.cols ? __ldg(reinterpret_cast<const uint2*>(A.codes + r * A.cols + c)) : make_uint2(0, 0);
-      scale[j] = c < A.cols ? __ldg(A.scales + r * A.blocks + c / kBlock) : 0.0f;
+      raw[j] = c < cols ? __ldg(reinterpret_cast<const uint2*>(p + c)) : make_uint2(0, 0);
+      scale[j] = c < cols ? __ldg(q + c / kBlock) : 0.0f;
     }
+    p += step;
+    q += qstep;
   }
-  __device__ __forceinline__ void expand(int j, float* f) const {
-    values4<T>(raw[j].x, scale[j], f);
-    values4<T>(raw[j].y, scale[j], f + 4);
+  __device__ __forceinline__ void normal(int j, float rstd, float shift, f2* f) const {
+    const float s = scale[j] * rstd;
+    const uint32_t lo = raw[j].x ^ 0x80808080u, hi = raw[j].y ^ 0x80808080u;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = fma2(codes_f(e < 2 ? lo : hi, 2 * (e & 1)), splat(s), splat(shift));
   }
 };
 template <typename T, int TPR, int CH>
 struct KeptRow<T, TPR, CH, false, true> {
   int8_t raw[CH][8];
   float scale[CH][4];
-  __device__ __forceinline__ void load(const BackwardArgs& A, int64_t r, int t) {
+  const int8_t* p;
+  const float* q;
+  int64_t step, qstep;
+  __device__ __forceinline__ KeptRow(const BackwardArgs& A, int64_t first, int64_t rows)
+      : p(A.codes + first * A.cols), q(A.scales + first * A.blocks), step(rows * A.cols), qstep(rows * A.blocks) {}
+  __device__ __forceinline__ void load(int t, int cols) {
 #pragma unroll
     for (int j = 0; j < CH; ++j)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int c = Columns<TPR, false>::at(t, j, e);
-        raw[j][e] = c < A.cols ? A.codes[r * A.cols + c] : (int8_t)0;
-        if ((e & 1) == 0) scale[j][e / 2] = c < A.cols ? A.scales[r * A.blocks + c / kBlock] : 0.0f;
+        raw[j][e] = c < cols ? p[c] : (int8_t)0;
+        if ((e & 1) == 0) scale[j][e / 2] = c < cols ? q[c / kBlock] : 0.0f;
       }
+    p += step;
+    q += qstep;
   }
-  __device__ __forceinline__ void expand(int j, float* f) const {
+  __device__ __forceinline__ void normal(int j, float rstd, float shift, f2* f) const {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = value_of<T>(raw[j][e], scale[j][e / 2]);
+    for (int e = 0; e < 4; ++e)
+      f[e] = fma2(pair((float)raw[j][2 * e], (float)raw[j][2 * e + 1]), splat(scale[j][e] * rstd), splat(shift));
   }
 };
 
 // dx of every row, and this block's share of dgamma and dbeta.  Each thread adds up its own columns over
-// the rows that it meets; at the end the block's row groups are joined in shared memory, in order.
+// the rows that it meets; at the end the block's row groups are joined in shared memory, in order.  Bound by
+// instruction issue with four warps to a row of 1024 columns (62% of the slots, 1370 instructions a row,
+// 29.6 us at 16384 rows from the checkpoint with `add`), so two warps have it, sixteen columns a thread.
 template <typename T, int TPR, int CH, bool VEC, bool CODES>
-__global__ void __launch_bounds__(kBackThreads<TPR>, TPR < 256 ? 3 : 1) k_ln_backward(const BackwardArgs A) {
+__global__ void __launch_bounds__(kBackThreads<TPR>, 512 / kBackThreads<TPR>) k_ln_backward(const BackwardArgs A) {
   constexpr int kGroups = kBackThreads<TPR> / TPR;
   using Col = Columns<TPR, VEC>;
   __shared__ float red[kGroups][2][2 * 32];
-  __shared__ float join[kGroups == 1 ? 1 : 2 * TPR * CH * 8];
+  __shared__ f2 join[kGroups == 1 ? 1 : 2 * TPR * CH * 4];
   const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
   const int64_t first = (int64_t)blockIdx.x * kGroups + group, step = (int64_t)gridDim.x * kGroups;
   int turn = 0;
   launch_next();
-  float dg[CH][8], db[CH][8];
+  f2 dg[CH][4], db[CH][4];
 #pragma unroll
   for (int j = 0; j < CH; ++j)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dg[j][e] = db[j][e] = 0.0f;
-  KeptRow<T, TPR, CH, VEC, CODES> kept;
-  RowInput<T, TPR, CH, VEC> dyin, addin, addnow;
+    for (int e = 0; e < 4; ++e) dg[j][e] = db[j][e] = 0;
+  KeptRow<T, TPR, CH, VEC, CODES> kept(A, first, step);
+  RowInput<T, TPR, CH, VEC> dyin, addin;
+  const T *pdy = static_cast<const T*>(A.dy) + first * A.lddy, *padd = static_cast<const T*>(A.add) + (A.add ? first * A.ldadd : 0);
+  T* pdx = static_cast<T*>(A.dx) + first * A.lddx;
   float mu = 0.0f, rs = 0.0f;
   auto load = [&](int64_t r) {
-    kept.load(A, r, t);
-    dyin.load(static_cast<const T*>(A.dy) + r * A.lddy, t, A.cols);
-    if (A.add) addin.load(static_cast<const T*>(A.add) + r * A.ldadd, t, A.cols);
+    kept.load(t, A.cols);
+    dyin.load(pdy, t, A.cols);
+    pdy += step * A.lddy;
     mu = __ldg(A.mean + r);
     rs = __ldg(A.rstd + r);
   };
-  if (first < A.rows) load(first);
+  auto load_add = [&] {
+    addin.load(padd, t, A.cols);
+    padd += step * A.ldadd;
+  };
+  if (first < A.rows) {
+    load(first);
+    if (A.add) load_add();
+  }
   for (int64_t r = first; r < A.rows; r += step) {
-    float xh[CH][8], d[CH][8];
-    const float rstd = rs;
-    float s[2] = {0.0f, 0.0f};
+    f2 xh[CH][4], d[CH][4], s0 = 0, s1 = 0;
+    const float rstd = rs, shift = -mu * rs;
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      float gamma[8];
+      f2 gamma[4];
       param_group<TPR, VEC>(A.gamma, t, j, A.cols, gamma);
-      kept.expand(j, xh[j]);
+      kept.normal(j, rstd, shift, xh[j]);
       dyin.expand(j, d[j]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < 4; ++e) {
         // columns past the end have dy = gamma = 0 and add nothing
-        xh[j][e] = (xh[j][e] - mu) * rstd;
-        dg[j][e] = fmaf(d[j][e], xh[j][e], dg[j][e]);
-        db[j][e] += d[j][e];
-        d[j][e] *= gamma[e];
-        s[0] += d[j][e];
-        s[1] = fmaf(d[j][e], xh[j][e], s[1]);
+        dg[j][e] = fma2(d[j][e], xh[j][e], dg[j][e]);
+        db[j][e] = add2(db[j][e], d[j][e]);
+        d[j][e] = mul2(d[j][e], gamma[e]);
+        s0 = add2(s0, d[j][e]);
+        s1 = fma2(d[j][e], xh[j][e], s1);
       }
     }
-    if (A.add) addnow = addin;
+    float s[2] = {sum_of(s0), sum_of(s1)};
     if (r + step < A.rows) load(r + step);  // under this row's sums
     row_sums<TPR>(s, red[group], turn, 1 + group);
-    s[0] *= A.inv_cols;
-    s[1] *= A.inv_cols;
+    const f2 c0 = splat(-s[0] * A.inv_cols * rstd), c1 = splat(-s[1] * A.inv_cols * rstd);
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      float o[8];
+      f2 o[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = rstd * (d[j][e] - s[0] - xh[j][e] * s[1]);
+      for (int e = 0; e < 4; ++e) o[e] = fma2(xh[j][e], c1, fma2(d[j][e], splat(rstd), c0));
       if (A.add) {
-        float a[8];
-        addnow.expand(j, a);
+        f2 a[4];
+        addin.expand(j, a);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] += a[e];
+        for (int e = 0; e < 4; ++e) o[e] = add2(o[e], a[e]);
       }
-      store_group<T, TPR, VEC>(static_cast<T*>(A.dx) + r * A.lddx, t, j, A.cols, o);
+      store_group<T, TPR, VEC>(pdx, t, j, A.cols, o);
     }
+    pdx += step * A.lddx;
+    if (A.add && r + step < A.rows) load_add();
   }
   if (kGroups > 1) {
     for (int q = 0; q < kGroups; ++q) {
@@ -347,10 +428,10 @@ __global__ void __launch_bounds__(kBackThreads<TPR>, TPR < 256 ? 3 : 1) k_ln_bac
 #pragma unroll
         for (int j = 0; j < CH; ++j)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int i = (j * 8 + e) * TPR + t;
-            join[i] = q ? join[i] + dg[j][e] : dg[j][e];
-            join[TPR * CH * 8 + i] = q ? join[TPR * CH * 8 + i] + db[j][e] : db[j][e];
+          for (int e = 0; e < 4; ++e) {
+            const int i = (j * 4 + e) * TPR + t, k = TPR * CH * 4 + i;
+            join[i] = q ? add2(join[i], dg[j][e]) : dg[j][e];
+            join[k] = q ? add2(join[k], db[j][e]) : db[j][e];
           }
       }
     }
@@ -361,12 +442,11 @@ __global__ void __launch_bounds__(kBackThreads<TPR>, TPR < 256 ? 3 : 1) k_ln_bac
 #pragma unroll
     for (int j = 0; j < CH; ++j)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int c = Col::at(t, j, e), i = (j * 8 + e) * TPR + t;
-        if (c < A.cols) {
-          p[c] = kGroups > 1 ? join[i] : dg[j][e];
-          p[A.cols + c] = kGroups > 1 ? join[TPR * CH * 8 + i] : db[j][e];
-        }
+      for (int e = 0; e < 4; ++e) {
+        const int i = (j * 4 + e) * TPR + t, c = Col::at(t, j, 2 * e), c1 = Col::at(t, j, 2 * e + 1);
+        const float2 g = halves(kGroups > 1 ? join[i] : dg[j][e]), b = halves(kGroups > 1 ? join[TPR * CH * 4 + i] : db[j][e]);
+        if (c < A.cols) p[c] = g.x, p[A.cols + c] = b.x;
+        if (c1 < A.cols) p[c1] = g.y, p[A.cols + c1] = b.y;
       }
   }
 }
@@ -399,7 +479,7 @@ __global__ void __launch_bounds__(kLnThreads) k_ln_forward_wide(const ForwardArg
       const float d = to_f(xr[c]) - mean;
       s = fmaf(d, d, s);
     }
-    const float rstd = 1.0f / sqrtf(fmaf(block_sum(s, red), A.inv_cols, A.eps));
+    const float rstd = rsqrtf(fmaf(block_sum(s, red), A.inv_cols, A.eps));
     for (int c = threadIdx.x; c < A.cols; c += kLnThreads)
       yr[c] = from_f<T>(fmaf((to_f(xr[c]) - mean) * rstd, A.gamma[c], A.beta[c]));
     if (threadIdx.x == 0) {
@@ -473,15 +553,18 @@ constexpr int kForwardCols = 512 * 4 * 8, kBackwardCols = 512 * 2 * 8;
 
 template <typename T, bool VEC>
 void launch_forward(const ForwardArgs& a, cudaStream_t s) {
-  auto go = [&](auto tpr, auto ch, int per_sm) {
-    constexpr int kTpr = decltype(tpr)::value, kCh = decltype(ch)::value, kThreads = kForwardThreads<kTpr>;
-    k_ln_forward<T, kTpr, kCh, VEC><<<at_most(ceil_div(a.rows, kThreads / kTpr), per_sm), kThreads, 0, s>>>(a);
+  auto go = [&](auto tpr, auto ch, auto nr, int per_sm) {
+    constexpr int kTpr = decltype(tpr)::value, kCh = decltype(ch)::value, kNr = decltype(nr)::value, kThreads = kForwardThreads<kTpr>;
+    k_ln_forward<T, kTpr, kCh, kNr, VEC><<<at_most(ceil_div(a.rows, kThreads / kTpr * kNr), per_sm), kThreads, 0, s>>>(a);
   };
   using std::integral_constant;
-  if (a.cols <= 256) go(integral_constant<int, 32>{}, integral_constant<int, 1>{}, 12);
-  else if (a.cols <= 1024) go(integral_constant<int, 32>{}, integral_constant<int, 4>{}, 6);
-  else if (a.cols <= 4096) go(integral_constant<int, 128>{}, integral_constant<int, 4>{}, 6);
-  else if (a.cols <= kForwardCols) go(integral_constant<int, 512>{}, integral_constant<int, 4>{}, 1);
+  using One = integral_constant<int, 1>;
+  using Two = integral_constant<int, 2>;
+  if (a.cols <= 256) go(integral_constant<int, 32>{}, One{}, Two{}, 5);
+  else if (a.cols <= 1024) go(integral_constant<int, 64>{}, Two{}, Two{}, 5);
+  else if (a.cols <= 2048) go(integral_constant<int, 128>{}, Two{}, Two{}, 5);
+  else if (a.cols <= 4096) go(integral_constant<int, 256>{}, Two{}, Two{}, 2);
+  else if (a.cols <= kForwardCols) go(integral_constant<int, 512>{}, integral_constant<int, 4>{}, One{}, 1);
   else k_ln_forward_wide<T><<<at_most(a.rows, 8), kLnThreads, 0, s>>>(a);
 }
 
@@ -489,15 +572,16 @@ void launch_forward(const ForwardArgs& a, cudaStream_t s) {
 int backward_parts(int64_t rows, int64_t cols) {
   if (rows == 0) return 0;
   if (cols > kBackwardCols) return (int)ceil_div(rows, ceil_div(rows, 64));
-  const int tpr = cols <= 256 ? 32 : cols <= 1024 ? 128 : 512;
-  return (int)at_most(ceil_div(rows, tpr < 256 ? 256 / tpr : 1), tpr < 256 ? 3 : 1);
+  const int groups = cols <= 256 ? 8 : cols <= 1024 ? 4 : cols <= 2048 ? 2 : 1;
+  return (int)at_most(ceil_div(rows, groups), cols <= 4096 ? 2 : 1);
 }
 
 template <typename T, bool VEC, bool CODES>
 void launch_backward(const BackwardArgs& a, int parts, cudaStream_t s) {
   if (a.cols <= 256) k_ln_backward<T, 32, 1, VEC, CODES><<<parts, kBackThreads<32>, 0, s>>>(a);
-  else if (a.cols <= 1024) k_ln_backward<T, 128, 1, VEC, CODES><<<parts, kBackThreads<128>, 0, s>>>(a);
-  else if (a.cols <= 4096) k_ln_backward<T, 512, 1, VEC, CODES><<<parts, kBackThreads<512>, 0, s>>>(a);
+  else if (a.cols <= 1024) k_ln_backward<T, 64, 2, VEC, CODES><<<parts, kBackThreads<64>, 0, s>>>(a);
+  else if (a.cols <= 2048) k_ln_backward<T, 128, 2, VEC, CODES><<<parts, kBackThreads<128>, 0, s>>>(a);
+  else if (a.cols <= 4096) k_ln_backward<T, 256, 2, VEC, CODES><<<parts, kBackThreads<256>, 0, s>>>(a);
   else k_ln_backward<T, 512, 2, VEC, CODES><<<parts, kBackThreads<512>, 0, s>>>(a);
 }
 

@@ -32,25 +32,57 @@ template <>
 __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
 // ------------------------------------------------------------------------------------------------
-// Activations and their derivatives, fp32.
-//
-// Phi(z), the normal distribution function, by Hastings' rational approximation (Abramowitz and Stegun
-// 7.1.26): with a = |z| and t = 1/(1 + 0.3275911 a/sqrt(2)), 1 - Phi(a) = t (c1 + t (c2 + t (c3 + t (c4 +
-// t c5)))) exp(-a^2/2) to 7.5e-8.  It needs the exponential that the derivative needs too, one reciprocal
-// and no branch: 16 instructions for gelu, 21 for gelu and its derivative together (the library's erff and
-// expf: 47).  Beyond |z| = 40 the tail is 0 in fp32; the clamp there keeps infinities from meeting zeros,
-// and passes NaN on.
-//
-// The tanh form is z times the logistic function of 2 sqrt(2/pi) (z + 0.044715 z^3).
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+// Two fp32 values in a register pair: one instruction adds, multiplies or fuses both.  The streaming
+// kernels and the products' epilogues are close to the issue limit, so their arithmetic goes by pairs.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pair(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
   return r;
 }
+__device__ __forceinline__ f2 splat(float x) { return pair(x, x); }
+__device__ __forceinline__ float2 halves(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float sum_of(f2 v) {
+  const float2 h = halves(v);
+  return h.x + h.y;
+}
+
 // the larger of two values, NaN if either is NaN
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// the largest of m and two magnitudes, NaN if any is NaN
+__device__ __forceinline__ float max_abs(float m, f2 v) {
+  const float2 h = halves(v);
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(h.x), "f"(h.y));
+  return r;
+}
+// z with its magnitude held to at most 40; NaN stays NaN
+__device__ __forceinline__ float held(float z) {
+  float r;
+  asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(z), "f"(40.0f));
   return r;
 }
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -63,49 +95,77 @@ __device__ __forceinline__ float rcp_fast(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-struct ActPair {
-  float value, slope;
-};
+
+// ------------------------------------------------------------------------------------------------
+// Activations and their derivatives, fp32, two at a time.
+//
+// Phi(z), the normal distribution function, by Hastings' rational approximation (Abramowitz and Stegun
+// 7.1.26): with a = |z| and t = 1/(1 + 0.3275911 a/sqrt(2)), 1 - Phi(a) = t (c1 + t (c2 + t (c3 + t (c4 +
+// t c5)))) exp(-a^2/2) to 7.5e-8.  It needs the exponential that the derivative needs too, one reciprocal
+// and no branch.  Beyond |z| = 40 the tail is 0 in fp32; holding z there keeps infinities from meeting
+// zeros, and passes NaN on.
+//
+// The tanh form is z times the logistic function of 2 sqrt(2/pi) (z + 0.044715 z^3).
 template <int ACT, bool VALUE, bool SLOPE>
-__device__ __forceinline__ ActPair act_pair(float z) {
-  ActPair p{z, 1.0f};
-  if (ACT == ONEBIT_ACT_RELU) {
-    if (VALUE) p.value = max_nan(z, 0.0f);
-    if (SLOPE) p.slope = z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
-  } else if (ACT == ONEBIT_ACT_GELU) {
-    const float a = min_nan(fabsf(z), 40.0f);
-    const float e = exp2_fast(a * a * -0.72134752f);  // -1/(2 ln 2)
-    const float t = rcp_fast(fmaf(a, 0.23164190f, 1.0f));
-    float q = fmaf(t, 0.53070271f, -0.72657601f);
-    q = fmaf(t, q, 0.71070687f);
-    q = fmaf(t, q, -0.14224837f);
-    q = fmaf(t, q, 0.12741480f);
-    const float tail = q * t * e;
-    if (VALUE) p.value = fmaf(-a, tail, fmaxf(z, 0.0f));
-    if (SLOPE) p.slope = 0.5f + copysignf(fmaf(a * 0.39894228f, e, 0.5f - tail), z);
-  } else if (ACT == ONEBIT_ACT_GELU_TANH) {
-    const float c = SLOPE ? min_nan(max_nan(z, -40.0f), 40.0f) : max_nan(z, -40.0f);
-    const float zz = c * c;
-    // -2 sqrt(2/pi) / ln 2 = -2.3022082
-    const float s = rcp_fast(1.0f + exp2_fast(c * fmaf(zz, -0.10294324f, -2.3022082f)));
-    if (VALUE) p.value = (SLOPE ? max_nan(z, -40.0f) : c) * s;
-    if (SLOPE) p.slope = fmaf(c * s * (1.0f - s), fmaf(zz, 0.21406445f, 1.5957691f), s);
+__device__ __forceinline__ void activate(f2 z2, f2& value, f2& slope) {
+  if (ACT == ONEBIT_ACT_NONE) {
+    value = z2;
+    slope = splat(1.0f);
+    return;
   }
-  return p;
+  const float2 z = halves(z2);
+  if (ACT == ONEBIT_ACT_RELU) {
+    if (VALUE) value = pair(max_nan(z.x, 0.0f), max_nan(z.y, 0.0f));
+    if (SLOPE) slope = pair(z.x > 0.0f ? 1.0f : (z.x != z.x ? z.x : 0.0f), z.y > 0.0f ? 1.0f : (z.y != z.y ? z.y : 0.0f));
+    return;
+  }
+  const float2 c = make_float2(held(z.x), held(z.y));
+  const f2 c2 = pair(c.x, c.y), zz = mul2(c2, c2);
+  if (ACT == ONEBIT_ACT_GELU) {
+    const float2 g = halves(mul2(zz, splat(-0.72134752f)));  // -1/(2 ln 2)
+    const f2 e = pair(exp2_fast(g.x), exp2_fast(g.y));
+    const f2 t = pair(rcp_fast(fmaf(fabsf(c.x), 0.23164190f, 1.0f)), rcp_fast(fmaf(fabsf(c.y), 0.23164190f, 1.0f)));
+    f2 q = fma2(t, splat(0.53070271f), splat(-0.72657601f));
+    q = fma2(t, q, splat(0.71070687f));
+    q = fma2(t, q, splat(-0.14224837f));
+    q = fma2(t, q, splat(0.12741480f));
+    const f2 tail2 = mul2(mul2(q, t), e);
+    if (VALUE) {
+      const float2 tail = halves(tail2);
+      value = pair(fmaf(-fabsf(c.x), tail.x, fmaxf(z.x, 0.0f)), fmaf(-fabsf(c.y), tail.y, fmaxf(z.y, 0.0f)));
+    }
+    if (SLOPE) {
+      const float2 m = halves(fma2(tail2, splat(-1.0f), splat(0.5f)));
+      slope = fma2(c2, mul2(e, splat(0.39894228f)), add2(pair(copysignf(m.x, c.x), copysignf(m.y, c.y)), splat(0.5f)));
+    }
+  } else {
+    // -2 sqrt(2/pi) / ln 2 = -2.3022082
+    const float2 g = halves(mul2(c2, fma2(zz, splat(-0.10294324f), splat(-2.3022082f))));
+    const float2 u = halves(add2(pair(exp2_fast(g.x), exp2_fast(g.y)), splat(1.0f)));
+    const f2 s = pair(rcp_fast(u.x), rcp_fast(u.y));
+    if (VALUE) value = mul2(pair(max_nan(z.x, -40.0f), max_nan(z.y, -40.0f)), s);
+    if (SLOPE) slope = fma2(mul2(mul2(c2, s), fma2(s, splat(-1.0f), splat(1.0f))), fma2(zz, splat(0.21406445f), splat(1.5957691f)), s);
+  }
 }
 template <int ACT>
-__device__ __forceinline__ float act_value(float z) { return act_pair<ACT, true, false>(z).value; }
-template <int ACT>
-__device__ __forceinline__ float act_slope(float z) { return act_pair<ACT, false, true>(z).slope; }
+__device__ __forceinline__ f2 act2(f2 z) {
+  f2 v, s;
+  activate<ACT, true, false>(z, v, s);
+  return v;
+}
+// one value, for the kernels off the hot paths
 __device__ __forceinline__ float act_value(int act, float z) {
-  return act == ONEBIT_ACT_GELU ? act_value<ONEBIT_ACT_GELU>(z)
-         : act == ONEBIT_ACT_RELU ? act_value<ONEBIT_ACT_RELU>(z)
-         : act == ONEBIT_ACT_GELU_TANH ? act_value<ONEBIT_ACT_GELU_TANH>(z) : z;
+  const f2 p = splat(z);
+  return halves(act == ONEBIT_ACT_GELU ? act2<ONEBIT_ACT_GELU>(p)
+                : act == ONEBIT_ACT_RELU ? act2<ONEBIT_ACT_RELU>(p)
+                : act == ONEBIT_ACT_GELU_TANH ? act2<ONEBIT_ACT_GELU_TANH>(p) : p).x;
 }
 __device__ __forceinline__ float act_slope(int act, float z) {
-  return act == ONEBIT_ACT_GELU ? act_slope<ONEBIT_ACT_GELU>(z)
-         : act == ONEBIT_ACT_RELU ? act_slope<ONEBIT_ACT_RELU>(z)
-         : act == ONEBIT_ACT_GELU_TANH ? act_slope<ONEBIT_ACT_GELU_TANH>(z) : 1.0f;
+  f2 v, s = splat(1.0f);
+  if (act == ONEBIT_ACT_GELU) activate<ONEBIT_ACT_GELU, false, true>(splat(z), v, s);
+  else if (act == ONEBIT_ACT_RELU) activate<ONEBIT_ACT_RELU, false, true>(splat(z), v, s);
+  else if (act == ONEBIT_ACT_GELU_TANH) activate<ONEBIT_ACT_GELU_TANH, false, true>(splat(z), v, s);
+  return halves(s).x;
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -115,10 +175,19 @@ struct BlockScale {
   float scale;  // what a code is multiplied by
   float inv;    // what a value is multiplied by before it is rounded to a code
 };
+// Both quotients by one correction of an approximate one (Markstein 1990): q += r (n - d q), which leaves
+// them within an ulp.  A division of the language is several times as long, and every eight columns of a
+// layer norm's row need two.
 __device__ __forceinline__ BlockScale block_scale(float most) {
   if (!(most <= 3.4028234663852886e38f)) return {CUDART_NAN_F, 0.0f};
-  if (most < 7.52316384526264e-37f) return {0.0f, 0.0f};  // 2^-120: 127/most stays finite above it
-  return {__fdiv_rn(most, 127.0f), __fdiv_rn(127.0f, most)};
+  if (most < 7.52316384526264e-37f) return {0.0f, 0.0f};  // 2^-120
+  const float q = most * 0.0078740157f;
+  const float scale = fmaf(fmaf(q, -127.0f, most), 0.0078740157f, q);
+  // far from where the reciprocal or the quotient would leave the normal range
+  const bool big = most > 1.8446744e19f;
+  const float d = big ? most * 5.4210109e-20f : most, r = rcp_fast(d), p = r * 127.0f;
+  const float inv = fmaf(fmaf(p, -d, 127.0f), r, p);
+  return {scale, big ? inv * 5.4210109e-20f : inv};
 }
 // code of one value, in the low byte: adding 1.5*2^23 leaves the nearest integer (ties to even) in
 // the low bits of the sum.  A block with inv = 0 that holds inf or NaN (inf*0) gets code 0.
@@ -132,26 +201,33 @@ __device__ __forceinline__ float value_of(int code, float scale) {
   const float v = __fmul_rn((float)code, scale);
   return sizeof(T) == 4 && isinf(v) ? copysignf(3.4028234663852886e38f, v) : v;
 }
-// A code as fp32, exactly: the byte, made unsigned, becomes the low bits of 2^23, from which 2^23 + 128
-// is taken away (a byte permute and an addition; the conversion unit does a quarter as many).
-__device__ __forceinline__ float code_f(uint32_t biased_word, int byte) {
-  return __uint_as_float(__byte_perm(biased_word, 0x4b000000u, 0x7650 + byte)) - 8388736.0f;
+// Codes as fp32, exactly: a byte, made unsigned, becomes the low bits of 2^23, from which 2^23 + 128 is
+// taken away (a byte permute and half an addition; the conversion unit does a quarter as many).
+__device__ __forceinline__ f2 codes_f(uint32_t biased, int byte) {  // two bytes from `byte` on, XORed with 0x80
+  return add2(pair(__uint_as_float(__byte_perm(biased, 0x4b000000u, 0x7650 + byte)), __uint_as_float(__byte_perm(biased, 0x4b000000u, 0x7651 + byte))),
+              splat(-8388736.0f));
 }
-// four codes of a word, which the caller has XORed with 0x80808080
+// what the four codes of a word stand for
 template <typename T>
-__device__ __forceinline__ void values4(uint32_t word, float scale, float* v) {
+__device__ __forceinline__ void values4(uint32_t word, float scale, f2* v) {
   word ^= 0x80808080u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[i] = __fmul_rn(code_f(word, i), scale);
-    if (sizeof(T) == 4 && isinf(v[i])) v[i] = copysignf(3.4028234663852886e38f, v[i]);
+  for (int i = 0; i < 2; ++i) {
+    v[i] = mul2(codes_f(word, 2 * i), splat(scale));
+    if (sizeof(T) == 4) {
+      float2 h = halves(v[i]);
+      if (isinf(h.x)) h.x = copysignf(3.4028234663852886e38f, h.x);
+      if (isinf(h.y)) h.y = copysignf(3.4028234663852886e38f, h.y);
+      v[i] = pair(h.x, h.y);
+    }
   }
 }
-// four values to a word of codes; inv is 0 only for blocks whose codes are all 0
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float inv) {
-  const uint32_t x = __float_as_uint(__fadd_rn(__fmul_rn(a, inv), 12582912.0f)), y = __float_as_uint(__fadd_rn(__fmul_rn(b, inv), 12582912.0f));
-  const uint32_t z = __float_as_uint(__fadd_rn(__fmul_rn(c, inv), 12582912.0f)), w = __float_as_uint(__fadd_rn(__fmul_rn(d, inv), 12582912.0f));
-  const uint32_t r = __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
+// four values to a word of codes; inv is 0 only for blocks whose codes are all 0.  The product is rounded
+// before 1.5*2^23 is added, as in code_of().
+__device__ __forceinline__ uint32_t codes4(f2 ab, f2 cd, float inv) {
+  const float2 x = halves(add2(mul2(ab, splat(inv)), splat(12582912.0f))), y = halves(add2(mul2(cd, splat(inv)), splat(12582912.0f)));
+  const uint32_t r = __byte_perm(__byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x0040),
+                                 __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x0040), 0x5410);
   return inv == 0.0f ? 0u : r;  // inf and NaN times 0 would leave other bits
 }
 
@@ -168,45 +244,50 @@ __device__ __forceinline__ Raw8<T> load8(const T* p) {
   for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
   return r;
 }
-__device__ __forceinline__ void expand8(const Raw8<float>& r, float* f) {
+__device__ __forceinline__ void expand8(const Raw8<float>& r, f2* f) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    f[4 * i] = __uint_as_float(r.v[i].x), f[4 * i + 1] = __uint_as_float(r.v[i].y);
-    f[4 * i + 2] = __uint_as_float(r.v[i].z), f[4 * i + 3] = __uint_as_float(r.v[i].w);
+    f[2 * i] = pair(__uint_as_float(r.v[i].x), __uint_as_float(r.v[i].y));
+    f[2 * i + 1] = pair(__uint_as_float(r.v[i].z), __uint_as_float(r.v[i].w));
   }
-}
-__device__ __forceinline__ void expand8(const Raw8<__half>& r, float* f) {
-  const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    f[2 * i] = h.x, f[2 * i + 1] = h.y;
-  }
-}
-__device__ __forceinline__ void expand8(const Raw8<__nv_bfloat16>& r, float* f) {
-  const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
 }
 template <typename T>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+__device__ __forceinline__ f2 widen(uint32_t v);  // two 16-bit values
 template <>
-__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
+__device__ __forceinline__ f2 widen<__half>(uint32_t v) {
+  const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&v));
+  return pair(h.x, h.y);
+}
+template <>
+__device__ __forceinline__ f2 widen<__nv_bfloat16>(uint32_t v) {
+  return pair(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+template <typename T>
+__device__ __forceinline__ void expand8(const Raw8<T>& r, f2* f) {
+  f[0] = widen<T>(r.v[0].x), f[1] = widen<T>(r.v[0].y), f[2] = widen<T>(r.v[0].z), f[3] = widen<T>(r.v[0].w);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t narrow(f2 v);  // two values, rounded
+template <>
+__device__ __forceinline__ uint32_t narrow<__half>(f2 v) {
+  const float2 f = halves(v);
+  const __half2 h = __floats2half2_rn(f.x, f.y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 template <>
-__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+__device__ __forceinline__ uint32_t narrow<__nv_bfloat16>(f2 v) {
+  const float2 f = halves(v);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ void store8(float* p, const float* f) {
-  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+__device__ __forceinline__ void store8(float* p, const f2* f) {
+  const float2 a = halves(f[0]), b = halves(f[1]), c = halves(f[2]), d = halves(f[3]);
+  *reinterpret_cast<float4*>(p) = make_float4(a.x, a.y, b.x, b.y);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(c.x, c.y, d.x, d.y);
 }
 template <typename T>
-__device__ __forceinline__ void store8(T* p, const float* f) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
+__device__ __forceinline__ void store8(T* p, const f2* f) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(narrow<T>(f[0]), narrow<T>(f[1]), narrow<T>(f[2]), narrow<T>(f[3]));
 }
 
 // ------------------------------------------------------------------------------------------------

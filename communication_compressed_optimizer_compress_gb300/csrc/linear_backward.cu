@@ -65,10 +65,13 @@ __global__ void __launch_bounds__(256) k_colsum_part(const T* __restrict__ dy, i
       if (c0 + lane * 8 < cols) {
 #pragma unroll 8
         for (int64_t r = run * kRun + warp; r < end; r += 8) {
-          float v[8];
+          f2 v[4];
           expand8(load8(dy + r * lddy + c0 + lane * 8), v);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) s[i] += v[i];
+          for (int i = 0; i < 4; ++i) {
+            const float2 h = halves(v[i]);
+            s[2 * i] += h.x, s[2 * i + 1] += h.y;
+          }
         }
       }
     } else {  // columns c0 + lane + 32 i

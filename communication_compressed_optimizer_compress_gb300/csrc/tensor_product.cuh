@@ -156,7 +156,7 @@ __device__ __forceinline__ void tmem_hold32(float* v) {
   asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
 }
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-// 32 columns of the 32 lanes that this warp may read
+// 32 columns of the 32 lanes that this warp may read, as fp32 pairs
 __device__ __forceinline__ void tmem_load32(uint32_t addr, float* v) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
   asm volatile(
@@ -329,17 +329,9 @@ __device__ __forceinline__ void load_codes(char* staging, uint32_t (&v)[16], con
   __syncwarp();
 }
 
-template <typename T>
-__device__ __forceinline__ float2 unpack2(uint32_t v);
-template <>
-__device__ __forceinline__ float2 unpack2<__half>(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
-template <>
-__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t v) {
-  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
-}
-
 // ------------------------------------------------------------------------------------------------
-// Epilogues.  run() has 64 columns from col0 on of the 32 rows from row0 on: a lane has row row0 + lane.
+// Epilogues.  run() has 64 columns from col0 on of the 32 rows from row0 on: a lane has row row0 + lane, in
+// 32 pairs.
 
 template <typename T>
 struct ForwardEpilogue {
@@ -356,53 +348,48 @@ struct ForwardEpilogue {
   int act;
   bool vec_bias, vec_res, vec_y, vec_codes;
 
-  __device__ __forceinline__ void run(float (&z)[64], int64_t row0, int64_t rows, int col0, int cols, int, char* staging) const {
+  template <int ACT>
+  __device__ __forceinline__ void finish(f2 (&z)[32], uint32_t (&v)[32]) const {  // v: in the residual, out y
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const f2 a = act2<ACT>(z[i]);
+      v[i] = narrow<T>(residual ? add2(a, widen<T>(v[i])) : a);
+    }
+  }
+  __device__ __forceinline__ void run(f2 (&z)[32], int64_t row0, int64_t rows, int col0, int cols, int, char* staging) const {
     const int64_t row = row0 + (threadIdx.x & 31);
     if (bias) {
       if (vec_bias && col0 + 64 <= cols) {
 #pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          const float4 b = __ldg(reinterpret_cast<const float4*>(bias + col0 + i));
-          z[i] += b.x, z[i + 1] += b.y, z[i + 2] += b.z, z[i + 3] += b.w;
+        for (int i = 0; i < 16; ++i) {
+          const float4 b = __ldg(reinterpret_cast<const float4*>(bias + col0) + i);
+          z[2 * i] = add2(z[2 * i], pair(b.x, b.y)), z[2 * i + 1] = add2(z[2 * i + 1], pair(b.z, b.w));
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 64; ++i) z[i] += col0 + i < cols ? __ldg(bias + col0 + i) : 0.0f;
+        for (int i = 0; i < 32; ++i) {
+          const int c = col0 + 2 * i;
+          z[i] = add2(z[i], pair(c < cols ? __ldg(bias + c) : 0.0f, c + 1 < cols ? __ldg(bias + c + 1) : 0.0f));
+        }
       }
     }
     if (codes) {  // columns past the end have z = 0: their operand rows were filled with zeros
       float most = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 64; ++i) most = max_nan(most, fabsf(z[i]));
+      for (int i = 0; i < 32; ++i) most = max_abs(most, z[i]);
       const BlockScale s = block_scale(most);
       uint32_t c[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        c[i] = codes4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3], s.inv);
+      for (int i = 0; i < 16; ++i) c[i] = codes4(z[2 * i], z[2 * i + 1], s.inv);
       if (row < rows) scales[row * blocks + col0 / kBlock] = s.scale;
       store_codes(staging, c, codes, row0, rows, col0, cols, vec_codes);
     }
     uint32_t v[32];
-    if (act == ONEBIT_ACT_RELU) {
-#pragma unroll
-      for (int i = 0; i < 64; ++i) z[i] = act_value<ONEBIT_ACT_RELU>(z[i]);
-    } else if (act == ONEBIT_ACT_GELU) {
-#pragma unroll
-      for (int i = 0; i < 64; ++i) z[i] = act_value<ONEBIT_ACT_GELU>(z[i]);
-    } else if (act == ONEBIT_ACT_GELU_TANH) {
-#pragma unroll
-      for (int i = 0; i < 64; ++i) z[i] = act_value<ONEBIT_ACT_GELU_TANH>(z[i]);
-    }
-    if (residual) {
-      load_rows(staging, v, residual, ldr, row0, rows, col0, cols, vec_res);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float2 r = unpack2<T>(v[i]);
-        z[2 * i] += r.x, z[2 * i + 1] += r.y;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = pack2<T>(z[2 * i], z[2 * i + 1]);
+    if (residual) load_rows(staging, v, residual, ldr, row0, rows, col0, cols, vec_res);
+    if (act == ONEBIT_ACT_NONE) finish<ONEBIT_ACT_NONE>(z, v);
+    else if (act == ONEBIT_ACT_RELU) finish<ONEBIT_ACT_RELU>(z, v);
+    else if (act == ONEBIT_ACT_GELU) finish<ONEBIT_ACT_GELU>(z, v);
+    else finish<ONEBIT_ACT_GELU_TANH>(z, v);
     RowStore<T>::run(staging, v, y, ldy, row0, rows, col0, cols, vec_y);
   }
 };
@@ -426,30 +413,31 @@ struct InputGradEpilogue {
   bool vec_x, vec_codes, vec_add, vec_dx;
 
   template <int ACT>
-  __device__ __forceinline__ void slopes(float (&d)[64], uint32_t (&v)[32]) const {  // v: in the kept values, out h
+  __device__ __forceinline__ void slopes(f2 (&d)[32], uint32_t (&v)[32]) const {  // v: in the kept values, out h
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-      const float2 z = unpack2<T>(v[i]);
-      const ActPair p = act_pair<ACT, true, true>(z.x), q = act_pair<ACT, true, true>(z.y);
-      d[2 * i] *= p.slope, d[2 * i + 1] *= q.slope;
-      v[i] = pack2<T>(p.value, q.value);
+      f2 a, s;
+      activate<ACT, true, true>(widen<T>(v[i]), a, s);
+      d[i] = mul2(d[i], s);
+      v[i] = narrow<T>(a);
     }
   }
   template <int ACT>
-  __device__ __forceinline__ void slopes(float (&d)[64], const uint32_t (&c)[16], float s, uint32_t (&v)[32]) const {
+  __device__ __forceinline__ void slopes(f2 (&d)[32], const uint32_t (&c)[16], float scale, uint32_t (&v)[32]) const {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      float z[4];
-      values4<T>(c[i], s, z);
+      f2 z[2];
+      values4<T>(c[i], scale, z);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const ActPair p = act_pair<ACT, true, true>(z[2 * j]), q = act_pair<ACT, true, true>(z[2 * j + 1]);
-        d[4 * i + 2 * j] *= p.slope, d[4 * i + 2 * j + 1] *= q.slope;
-        v[2 * i + j] = pack2<T>(p.value, q.value);
+        f2 a, s;
+        activate<ACT, true, true>(z[j], a, s);
+        if (ACT != ONEBIT_ACT_NONE) d[2 * i + j] = mul2(d[2 * i + j], s);
+        v[2 * i + j] = narrow<T>(a);
       }
     }
   }
-  __device__ __forceinline__ void run(float (&d)[64], int64_t row0, int64_t rows, int col0, int cols, int, char* staging) const {
+  __device__ __forceinline__ void run(f2 (&d)[32], int64_t row0, int64_t rows, int col0, int cols, int, char* staging) const {
     uint32_t v[32];
     if (codes && (act != ONEBIT_ACT_NONE || h)) {
       uint32_t c[16];
@@ -470,13 +458,10 @@ struct InputGradEpilogue {
     if (add) {
       load_rows(staging, v, add, ldadd, row0, rows, col0, cols, vec_add);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float2 r = unpack2<T>(v[i]);
-        d[2 * i] += r.x, d[2 * i + 1] += r.y;
-      }
+      for (int i = 0; i < 32; ++i) d[i] = add2(d[i], widen<T>(v[i]));
     }
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = pack2<T>(d[2 * i], d[2 * i + 1]);
+    for (int i = 0; i < 32; ++i) v[i] = narrow<T>(d[i]);
     RowStore<T>::run(staging, v, dx, lddx, row0, rows, col0, cols, vec_dx);
   }
 };
@@ -489,19 +474,22 @@ struct PlainEpilogue {
   int64_t ld;
   int64_t split_stride;
   bool vec;
-  __device__ __forceinline__ void run(float (&acc)[64], int64_t row0, int64_t rows, int col0, int cols, int split, char* staging) const {
+  __device__ __forceinline__ void run(f2 (&d)[32], int64_t row0, int64_t rows, int col0, int cols, int split, char* staging) const {
     G* out = p + split * split_stride;
     uint32_t v[32];
     if (sizeof(G) == 4) {
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(acc[32 * half + i]);
+        for (int i = 0; i < 16; ++i) {
+          const float2 f = halves(d[16 * half + i]);
+          v[2 * i] = __float_as_uint(f.x), v[2 * i + 1] = __float_as_uint(f.y);
+        }
         RowStore<G>::run(staging, v, out, ld, row0, rows, col0 + 32 * half, cols, vec);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = pack2<std::conditional_t<sizeof(G) == 4, __half, G>>(acc[2 * i], acc[2 * i + 1]);
+      for (int i = 0; i < 32; ++i) v[i] = narrow<std::conditional_t<sizeof(G) == 4, __half, G>>(d[i]);
       RowStore<G>::run(staging, v, out, ld, row0, rows, col0, cols, vec);
     }
   }
@@ -596,16 +584,20 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
       const int64_t row0 = t.m0 + rank * kRowsPerBlock + quad * 32;
       const int col0 = t.n0 + half * kCols;
       if (Epilogue::kFold) {
-        float c[kCols / 64][64];
+        f2 c[kCols / 64][32];
         for (int k0 = 0; k0 < t.slabs; k0 += kFoldSlabs) {
           if (!(ok = ready())) break;
           const uint32_t at = lanes + acc * kTileN;
           if (k0 == 0) {
 #pragma unroll
-            for (int q = 0; q < kCols; q += 32) tmem_load32(at + q, &c[q / 64][q % 64]);
-            tmem_wait_load();
+            for (int q = 0; q < kCols; q += 32) {
+              float v[32];
+              tmem_load32(at + q, v);
+              tmem_wait_load();
+              tmem_hold32(v);
 #pragma unroll
-            for (int q = 0; q < kCols; q += 32) tmem_hold32(&c[q / 64][q % 64]);
+              for (int i = 0; i < 16; ++i) c[q / 64][q % 64 / 2 + i] = pair(v[2 * i], v[2 * i + 1]);
+            }
           } else {
 #pragma unroll
             for (int q = 0; q < kCols; q += 32) {
@@ -614,7 +606,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
               tmem_wait_load();
               tmem_hold32(v);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) c[q / 64][q % 64 + i] += v[i];
+              for (int i = 0; i < 16; ++i) c[q / 64][q % 64 / 2 + i] = add2(c[q / 64][q % 64 / 2 + i], pair(v[2 * i], v[2 * i + 1]));
             }
           }
           release();
@@ -628,12 +620,15 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
         const uint32_t at = lanes + acc * kTileN;
 #pragma unroll
         for (int q = 0; q < kCols / 64; ++q) {
-          float c[64];
-          tmem_load32(at + 64 * q, c);
-          tmem_load32(at + 64 * q + 32, c + 32);
+          float raw[64];
+          tmem_load32(at + 64 * q, raw);
+          tmem_load32(at + 64 * q + 32, raw + 32);
           tmem_wait_load();
-          tmem_hold32(c);
-          tmem_hold32(c + 32);
+          tmem_hold32(raw);
+          tmem_hold32(raw + 32);
+          f2 c[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) c[i] = pair(raw[2 * i], raw[2 * i + 1]);
           if (q == kCols / 64 - 1) release();
           if (row0 < P.m && col0 + 64 * q < P.n) E.run(c, row0, P.m, col0 + 64 * q, P.n, t.split, staging);
         }

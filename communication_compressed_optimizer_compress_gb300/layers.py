@@ -144,11 +144,11 @@ def _vector(t, name: str, n: int, device, dtype=torch.float32):
 
 
 def _kept(x, name: str, cols=None, rows=None, dtype=None, device=None):
-    """(x pointer, row stride, codes pointer, scales pointer, rows, columns, dtype, device, shape) of a
+    """(x pointer, row stride, codes pointer, scales pointer, rows, columns, dtype, device) of a
     layer's kept input: a tensor or its Checkpoint."""
     if not isinstance(x, Checkpoint):
         r, c, ld = _matrix(x, name, cols, rows, dtype, device)
-        return x.data_ptr(), ld, None, None, r, c, x.dtype, x.device, x.shape
+        return x.data_ptr(), ld, None, None, r, c, x.dtype, x.device
     if dtype is not None and x.dtype != dtype:
         raise ValueError(f"{name}: expected a checkpoint of {dtype}, got one of {x.dtype}")
     codes = x.codes
@@ -157,7 +157,7 @@ def _kept(x, name: str, cols=None, rows=None, dtype=None, device=None):
         raise ValueError(f"{name}.codes: a checkpoint is contiguous")
     blocks = -(-c // CHECKPOINT_BLOCK)
     s = _vector(x.scales, name + ".scales", r * blocks, codes.device)
-    return None, 0, codes.data_ptr(), s, r, c, x.dtype, codes.device, codes.shape
+    return None, 0, codes.data_ptr(), s, r, c, x.dtype, codes.device
 
 
 def _on(stream):
@@ -184,10 +184,27 @@ def _stream(device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _new_checkpoint(shape, dtype, device):
-    blocks = -(-shape[-1] // CHECKPOINT_BLOCK)
-    return Checkpoint(torch.empty(shape, dtype=torch.int8, device=device),
-                      torch.empty((*shape[:-1], blocks), dtype=torch.float32, device=device), dtype)
+# Outputs.  An allocation is most of what a small call costs the host, and one from plain integers costs
+# half of one from a shape, so the 2-D case is written out.
+def _like(t):
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def _rows_of(t, rows, device):
+    """One fp32 value per row of t."""
+    return torch.empty(rows if t.dim() == 2 else t.shape[:-1], device=device, dtype=torch.float32)
+
+
+def _rows_by(t, rows, cols, dtype, device):
+    """t's rows with `cols` columns."""
+    if t.dim() == 2:
+        return torch.empty(rows, cols, dtype=dtype, device=device)
+    return torch.empty((*t.shape[:-1], cols), dtype=dtype, device=device)
+
+
+def _new_checkpoint(t, rows, cols, dtype, device):
+    return Checkpoint(_rows_by(t, rows, cols, torch.int8, device),
+                      _rows_by(t, rows, -(-cols // CHECKPOINT_BLOCK), torch.float32, device), dtype)
 
 
 def _workspace(nbytes: int, device):
@@ -213,7 +230,7 @@ def compress(x, stream=None) -> Checkpoint:
     rows, cols, ld = _matrix(x, "x")
     code = _code(x.dtype, "x")
     with _on(stream):
-        ck = _new_checkpoint(x.shape, x.dtype, x.device)
+        ck = _new_checkpoint(x, rows, cols, x.dtype, x.device)
         _check(_functions().onebit_checkpoint_compress(x.data_ptr(), ld, code, rows, cols, ck.codes.data_ptr(),
                                                        ck.scales.data_ptr(), _stream(x.device)),
                "onebit_checkpoint_compress")
@@ -222,10 +239,10 @@ def compress(x, stream=None) -> Checkpoint:
 
 def restore(ck: Checkpoint, activation=ACT_NONE, stream=None):
     """activation(the values a checkpoint stands for), in the checkpoint's dtype."""
-    _, _, codes, scales, rows, cols, dtype, device, shape = _kept(ck, "ck")
+    _, _, codes, scales, rows, cols, dtype, device = _kept(ck, "ck")
     code = _code(dtype, "ck")
     with _on(stream):
-        x = torch.empty(shape, dtype=dtype, device=device)
+        x = torch.empty_like(ck.codes, dtype=dtype)
         _check(_functions().onebit_checkpoint_restore(codes, scales, rows, cols, activation, x.data_ptr(), cols, code,
                                                       _stream(device)), "onebit_checkpoint_restore")
     return x
@@ -237,10 +254,9 @@ def layer_norm(x, gamma, beta, eps=1e-5, checkpoint=False, stream=None):
     code, device = _code(x.dtype, "x"), x.device
     g, b = _vector(gamma, "gamma", cols, device), _vector(beta, "beta", cols, device)
     with _on(stream):
-        y = x.new_empty(x.shape)
-        mean = gamma.new_empty(x.shape[:-1])
-        rstd = gamma.new_empty(x.shape[:-1])
-        ck = _new_checkpoint(x.shape, x.dtype, device) if checkpoint else None
+        y = _like(x)
+        mean, rstd = _rows_of(x, rows, device), _rows_of(x, rows, device)
+        ck = _new_checkpoint(x, rows, cols, x.dtype, device) if checkpoint else None
         _check(_functions().onebit_layer_norm_forward(
             x.data_ptr(), ld, code, rows, cols, g, b, eps, y.data_ptr(), cols, mean.data_ptr(), rstd.data_ptr(),
             ck.codes.data_ptr() if ck else None, ck.scales.data_ptr() if ck else None, _stream(device)),
@@ -258,7 +274,7 @@ def layer_norm_backward(dy, x, gamma, mean, rstd, add=None, grad_dtype=torch.flo
     ap, lda = (add.data_ptr(), _matrix(add, "add", cols, rows, dy.dtype, device)[2]) if add is not None else (None, 0)
     fn, need = _functions(), ctypes.c_size_t()
     with _on(stream):
-        dx = dy.new_empty(dy.shape)
+        dx = _like(dy)
         dgamma = torch.empty(cols, dtype=grad_dtype, device=device)
         dbeta = torch.empty(cols, dtype=grad_dtype, device=device)
         _check(fn.onebit_layer_norm_backward_workspace(rows, cols, ctypes.byref(need)),
@@ -281,11 +297,10 @@ def linear(x, w, bias=None, activation=ACT_NONE, residual=None, checkpoint=False
     out, _, ldw = _matrix(w, "w", cols, None, dtype, device)
     bp = _vector(bias, "bias", out, device)
     rp, ldr = (residual.data_ptr(), _matrix(residual, "residual", out, rows, dtype, device)[2]) if residual is not None else (None, 0)
-    shape = (*x.shape[:-1], out)
     fn, need = _functions(), ctypes.c_size_t()
     with _on(stream):
-        y = x.new_empty(shape)
-        ck = _new_checkpoint(shape, dtype, device) if checkpoint else None
+        y = _rows_by(x, rows, out, dtype, device)
+        ck = _new_checkpoint(x, rows, out, dtype, device) if checkpoint else None
         a = LinearArgs(x.data_ptr(), ldx, w.data_ptr(), ldw, bp, rp, ldr, y.data_ptr(), out,
                        ck.codes.data_ptr() if ck else None, ck.scales.data_ptr() if ck else None, rows, cols, out, code,
                        activation)
@@ -317,7 +332,7 @@ def linear_backward(dy, x, w, activation=ACT_NONE, add=None, grad_dtype=None, dw
     want_dx, want_dw, want_db = "dx" in need, "dw" in need, "db" in need
     fn, bytes_ = _functions(), ctypes.c_size_t()
     with _on(stream):
-        dx = dy.new_empty((*dy.shape[:-1], cols)) if want_dx else None
+        dx = _rows_by(dy, rows, cols, dtype, device) if want_dx else None
         if want_dw and dw is None:
             dw = torch.empty((out, cols), dtype=grad_dtype, device=device)
         if want_db and db is None:
