@@ -94,6 +94,7 @@ template <typename T, int ACT>
 __global__ void __launch_bounds__(kCkThreads) k_restore_wide(const int8_t* __restrict__ codes, const float* __restrict__ scales, Wide w,
                                                              T* __restrict__ x, int64_t ldx) {
   const int per = w.cols / 16;
+  const ActConsts k = literal_consts<ACT>();
   const int64_t runs = (w.rows + w.run_rows - 1) / w.run_rows;
   for (int64_t run = blockIdx.x; run < runs; run += gridDim.x) {
     const int64_t r0 = run * w.run_rows;
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(kCkThreads) k_restore_wide(const int8_t* __res
       f2 v[8];
       values4<T>(c.x, s, v), values4<T>(c.y, s, v + 2), values4<T>(c.z, s, v + 4), values4<T>(c.w, s, v + 6);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = act2<ACT>(v[i]);
+      for (int i = 0; i < 8; ++i) v[i] = act2<ACT>(k, v[i]);
       T* p = x + (r0 + r) * ldx + g * 16;
       store8(p, v);
       store8(p + 8, v + 4);

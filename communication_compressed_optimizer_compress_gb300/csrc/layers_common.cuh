@@ -79,8 +79,13 @@ __device__ __forceinline__ float max_abs(float m, f2 v) {
   asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(h.x), "f"(h.y));
   return r;
 }
-// z with its magnitude held to at most 40; NaN stays NaN
-__device__ __forceinline__ float held(float z) {
+// |z| held to at most 6, and z itself to a magnitude of at most 40; NaN stays NaN
+__device__ __forceinline__ float magnitude6(float z) {
+  float r;
+  asm("min.NaN.abs.f32 %0, %1, %2, %2;" : "=f"(r) : "f"(z), "f"(6.0f));
+  return r;
+}
+__device__ __forceinline__ float held40(float z) {
   float r;
   asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(z), "f"(40.0f));
   return r;
@@ -99,15 +104,41 @@ __device__ __forceinline__ float rcp_fast(float x) {
 // ------------------------------------------------------------------------------------------------
 // Activations and their derivatives, fp32, two at a time.
 //
-// Phi(z), the normal distribution function, by Hastings' rational approximation (Abramowitz and Stegun
-// 7.1.26): with a = |z| and t = 1/(1 + 0.3275911 a/sqrt(2)), 1 - Phi(a) = t (c1 + t (c2 + t (c3 + t (c4 +
-// t c5)))) exp(-a^2/2) to 7.5e-8.  It needs the exponential that the derivative needs too, one reciprocal
-// and no branch.  Beyond |z| = 40 the tail is 0 in fp32; holding z there keeps infinities from meeting
-// zeros, and passes NaN on.
+// gelu(z) = max(z, 0) - a (1 - Phi(a)), a = |z|.  log2(1 - Phi(a)) is a smooth, nearly quadratic function, so
+// the tail is one exponential of a polynomial: degree 6, fitted here on [0, 6] by least squares with the
+// weights of gelu's own error, raised where it was largest until it levelled out.  It leaves gelu within
+// 3.8e-7 and Phi within 2e-7 in fp32, for 14 instructions a pair (a rational form with its reciprocal and
+// second exponential: 22).  Beyond 6 the product a (1 - Phi(a)) is 6e-9 and stays there.  The derivative
+// Phi(z) + z phi(z) = 1/2 + sign(z) (1/2 - tail + a phi(a)) needs one exponential more.
 //
 // The tanh form is z times the logistic function of 2 sqrt(2/pi) (z + 0.044715 z^3).
+//
+// The constants come as register pairs: as literals they would be set up again for each pair, which was
+// a third of the instructions of the products' epilogues.
+constexpr int kActConsts = 10;
+struct ActConsts {
+  f2 k[kActConsts];
+};
+__host__ __device__ constexpr float act_const(int act, int i) {
+  constexpr float gelu[kActConsts] = {-0.9999995231628418f, -1.151128888130188f, -0.45901408791542053f, -0.05307028442621231f, 0.007853773422539234f,
+                                      -0.0006991532281972468f, 2.503262112441007e-05f,
+                                      -0.72134752f,  // -1/(2 ln 2)
+                                      0.39894228f,   // 1/sqrt(2 pi)
+                                      0.5f};
+  // -2 sqrt(2/pi) / ln 2 times 0.044715 and 1; 2 sqrt(2/pi) times 3 * 0.044715 and 1
+  constexpr float tanh[kActConsts] = {-0.10294324f, -2.3022082f, 1.0f, 0.21406445f, 1.5957691f};
+  return act == ONEBIT_ACT_GELU ? gelu[i] : act == ONEBIT_ACT_GELU_TANH ? tanh[i] : 0.0f;
+}
+template <int ACT>
+__device__ __forceinline__ ActConsts literal_consts() {
+  ActConsts c;
+#pragma unroll
+  for (int i = 0; i < kActConsts; ++i) c.k[i] = splat(act_const(ACT, i));
+  return c;
+}
 template <int ACT, bool VALUE, bool SLOPE>
-__device__ __forceinline__ void activate(f2 z2, f2& value, f2& slope) {
+__device__ __forceinline__ void activate(const ActConsts& c, f2 z2, f2& value, f2& slope) {
+  const f2* k = c.k;
   if (ACT == ONEBIT_ACT_NONE) {
     value = z2;
     slope = splat(1.0f);
@@ -117,56 +148,51 @@ __device__ __forceinline__ void activate(f2 z2, f2& value, f2& slope) {
   if (ACT == ONEBIT_ACT_RELU) {
     if (VALUE) value = pair(max_nan(z.x, 0.0f), max_nan(z.y, 0.0f));
     if (SLOPE) slope = pair(z.x > 0.0f ? 1.0f : (z.x != z.x ? z.x : 0.0f), z.y > 0.0f ? 1.0f : (z.y != z.y ? z.y : 0.0f));
-    return;
-  }
-  const float2 c = make_float2(held(z.x), held(z.y));
-  const f2 c2 = pair(c.x, c.y), zz = mul2(c2, c2);
-  if (ACT == ONEBIT_ACT_GELU) {
-    const float2 g = halves(mul2(zz, splat(-0.72134752f)));  // -1/(2 ln 2)
-    const f2 e = pair(exp2_fast(g.x), exp2_fast(g.y));
-    const f2 t = pair(rcp_fast(fmaf(fabsf(c.x), 0.23164190f, 1.0f)), rcp_fast(fmaf(fabsf(c.y), 0.23164190f, 1.0f)));
-    f2 q = fma2(t, splat(0.53070271f), splat(-0.72657601f));
-    q = fma2(t, q, splat(0.71070687f));
-    q = fma2(t, q, splat(-0.14224837f));
-    q = fma2(t, q, splat(0.12741480f));
-    const f2 tail2 = mul2(mul2(q, t), e);
-    if (VALUE) {
-      const float2 tail = halves(tail2);
-      value = pair(fmaf(-fabsf(c.x), tail.x, fmaxf(z.x, 0.0f)), fmaf(-fabsf(c.y), tail.y, fmaxf(z.y, 0.0f)));
-    }
+  } else if (ACT == ONEBIT_ACT_GELU) {
+    const float2 a = make_float2(magnitude6(z.x), magnitude6(z.y));
+    const f2 a2 = pair(a.x, a.y);
+    f2 p = k[6];
+#pragma unroll
+    for (int i = 5; i >= 0; --i) p = fma2(p, a2, k[i]);
+    const float2 l = halves(p), tail = make_float2(exp2_fast(l.x), exp2_fast(l.y));
+    if (VALUE) value = pair(fmaf(-a.x, tail.x, fmaxf(z.x, 0.0f)), fmaf(-a.y, tail.y, fmaxf(z.y, 0.0f)));
     if (SLOPE) {
-      const float2 m = halves(fma2(tail2, splat(-1.0f), splat(0.5f)));
-      slope = fma2(c2, mul2(e, splat(0.39894228f)), add2(pair(copysignf(m.x, c.x), copysignf(m.y, c.y)), splat(0.5f)));
+      const float2 g = halves(mul2(mul2(a2, a2), k[7]));
+      const float2 m = halves(fma2(mul2(a2, k[8]), pair(exp2_fast(g.x), exp2_fast(g.y)), add2(k[9], pair(-tail.x, -tail.y))));
+      slope = add2(pair(copysignf(m.x, z.x), copysignf(m.y, z.y)), k[9]);
     }
   } else {
-    // -2 sqrt(2/pi) / ln 2 = -2.3022082
-    const float2 g = halves(mul2(c2, fma2(zz, splat(-0.10294324f), splat(-2.3022082f))));
-    const float2 u = halves(add2(pair(exp2_fast(g.x), exp2_fast(g.y)), splat(1.0f)));
+    const f2 c2 = pair(held40(z.x), held40(z.y)), zz = mul2(c2, c2);
+    const float2 g = halves(mul2(c2, fma2(zz, k[0], k[1])));
+    const float2 u = halves(add2(pair(exp2_fast(g.x), exp2_fast(g.y)), k[2]));
     const f2 s = pair(rcp_fast(u.x), rcp_fast(u.y));
     if (VALUE) value = mul2(pair(max_nan(z.x, -40.0f), max_nan(z.y, -40.0f)), s);
-    if (SLOPE) slope = fma2(mul2(mul2(c2, s), fma2(s, splat(-1.0f), splat(1.0f))), fma2(zz, splat(0.21406445f), splat(1.5957691f)), s);
+    if (SLOPE) {
+      const float2 h = halves(s);
+      slope = fma2(mul2(mul2(c2, s), add2(k[2], pair(-h.x, -h.y))), fma2(zz, k[3], k[4]), s);
+    }
   }
 }
 template <int ACT>
-__device__ __forceinline__ f2 act2(f2 z) {
+__device__ __forceinline__ f2 act2(const ActConsts& c, f2 z) {
   f2 v, s;
-  activate<ACT, true, false>(z, v, s);
+  activate<ACT, true, false>(c, z, v, s);
   return v;
 }
 // one value, for the kernels off the hot paths
-__device__ __forceinline__ float act_value(int act, float z) {
-  const f2 p = splat(z);
-  return halves(act == ONEBIT_ACT_GELU ? act2<ONEBIT_ACT_GELU>(p)
-                : act == ONEBIT_ACT_RELU ? act2<ONEBIT_ACT_RELU>(p)
-                : act == ONEBIT_ACT_GELU_TANH ? act2<ONEBIT_ACT_GELU_TANH>(p) : p).x;
+template <int ACT>
+__device__ __forceinline__ float2 act_one(float z) {  // value and slope
+  f2 v = splat(z), s = splat(1.0f);
+  activate<ACT, true, true>(literal_consts<ACT>(), splat(z), v, s);
+  return make_float2(halves(v).x, halves(s).x);
 }
-__device__ __forceinline__ float act_slope(int act, float z) {
-  f2 v, s = splat(1.0f);
-  if (act == ONEBIT_ACT_GELU) activate<ONEBIT_ACT_GELU, false, true>(splat(z), v, s);
-  else if (act == ONEBIT_ACT_RELU) activate<ONEBIT_ACT_RELU, false, true>(splat(z), v, s);
-  else if (act == ONEBIT_ACT_GELU_TANH) activate<ONEBIT_ACT_GELU_TANH, false, true>(splat(z), v, s);
-  return halves(s).x;
+__device__ __forceinline__ float2 act_both(int act, float z) {
+  return act == ONEBIT_ACT_GELU ? act_one<ONEBIT_ACT_GELU>(z)
+         : act == ONEBIT_ACT_RELU ? act_one<ONEBIT_ACT_RELU>(z)
+         : act == ONEBIT_ACT_GELU_TANH ? act_one<ONEBIT_ACT_GELU_TANH>(z) : make_float2(z, 1.0f);
 }
+__device__ __forceinline__ float act_value(int act, float z) { return act_both(act, z).x; }
+__device__ __forceinline__ float act_slope(int act, float z) { return act_both(act, z).y; }
 
 // ------------------------------------------------------------------------------------------------
 // the 8-bit checkpoint's rounding.  `most` is the block's largest |x| (NaN or infinite if the block

@@ -16,9 +16,9 @@ __global__ void __launch_bounds__(256) k_finish_dx(Partials c, int64_t rows, int
     const int col = (int)(i - r * cols);
     float d = c.at(r, col);
     if (act != ONEBIT_ACT_NONE || h) {
-      const float z = v.at(r, col);
-      d *= act_slope(act, z);
-      if (h) h[r * ldh + col] = from_f<T>(act_value(act, z));
+      const float2 p = act_both(act, v.at(r, col));
+      d *= p.y;
+      if (h) h[r * ldh + col] = from_f<T>(p.x);
     }
     if (add) d += to_f(add[r * ldadd + col]);
     dx[r * lddx + col] = from_f<T>(d);

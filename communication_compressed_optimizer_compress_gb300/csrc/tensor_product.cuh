@@ -32,13 +32,17 @@ constexpr int kRowsPerBlock = 128;            // rows of each operand that a blo
 constexpr int kOperandBytes = kRowsPerBlock * kSlabK * 2;
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kStages = 5;
-constexpr int kEpilogueWarps = 8;
-constexpr int kProductThreads = 128 + 32 * kEpilogueWarps;
-constexpr int kControlRegs = 40, kEpilogueRegs = 232;  // 56 + 2*224 = 3 * 168, what a block is launched with
-constexpr int kStagingRow = 144;              // 128 bytes and 16 to spread the rows over the banks
+template <int CTAS>
+constexpr int kEpilogueWarps = 8 * CTAS;      // 128 rows are 4 quarters of the tensor memory; 64 columns a warp
+template <int CTAS>
+constexpr int kProductThreads = 128 + 32 * kEpilogueWarps<CTAS>;
+// A pair's block is launched with 640 * 96 registers; 128 * 56 + 512 * 104 of them are used.
+constexpr int kControlRegs = 56, kEpilogueRegs = 104;
+constexpr int kStagingRow = 80;               // 64 bytes and 16 to spread the rows over the banks
 constexpr int kStagingBytes = 32 * kStagingRow;
 constexpr int kBarrierBytes = 256;
-constexpr int kProductSmem = 1024 + kStages * kStageBytes + kEpilogueWarps * kStagingBytes + kBarrierBytes;
+template <int CTAS>
+constexpr int kProductSmem = 1024 + kStages * kStageBytes + kEpilogueWarps<CTAS> * kStagingBytes + kBarrierBytes + kActConsts * 8;
 constexpr int kFoldSlabs = 8;                 // slabs that an accumulator of a folded product sums up
 constexpr int kGroupTiles = 8;                // tile rows that are walked together, for the L2
 
@@ -66,8 +70,10 @@ __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
+// What this arrival announces is that loads from tensor memory are done, which tcgen05.wait has seen to: no
+// memory has to be released with it.
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -150,6 +156,16 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
 }
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// 16 columns, for the folding sums
+__device__ __forceinline__ void tmem_load16(uint32_t addr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(addr));
+}
+__device__ __forceinline__ void tmem_hold16(float* v) {
+  asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
+}
 // Waits for this warp's loads.  The values pass through the statement, so that nothing that uses them
 // can be moved ahead of it.
 __device__ __forceinline__ void tmem_hold32(float* v) {
@@ -204,125 +220,115 @@ struct Wait {
 };
 
 // ------------------------------------------------------------------------------------------------
-// Rows of 128 bytes between registers (a lane has a row) and memory (eight lanes share a row, so that
-// every access is a whole 128-byte line), through the warp's staging buffer.
+// Rows of 64 bytes between registers (a lane has a row) and memory (four lanes share a row, so that every
+// access is whole sectors), through the warp's staging buffer.
 
 template <typename T>
-struct RowStore {  // 128/sizeof(T) columns from col0 on
-  static constexpr int kCols = 128 / sizeof(T);
-  static constexpr int kVec = 16 / sizeof(T);
-  __device__ static __forceinline__ void run(char* staging, const uint32_t (&v)[32], T* p, int64_t ld, int64_t row0, int64_t rows, int col0,
-                                             int cols, bool vec) {
-    const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void store_rows(char* staging, const uint32_t (&v)[16], T* p, int64_t ld, int64_t row0, int64_t rows, int col0, int cols,
+                                           bool vec) {
+  constexpr int kCols = 64 / sizeof(T), kVec = 16 / sizeof(T);
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      *reinterpret_cast<uint4*>(staging + lane * kStagingRow + j * 16) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-    __syncwarp();
-    const int c = (lane & 7) * kVec;
-    if (vec && (col0 + kCols <= cols || cols % kVec == 0)) {
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<uint4*>(staging + lane * kStagingRow + j * 16) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+  __syncwarp();
+  const int c = col0 + (lane & 3) * kVec;
+  if (vec && (col0 + kCols <= cols || cols % kVec == 0)) {
+    T* q = p + (row0 + (lane >> 2)) * ld + c;
+    const char* from = staging + (lane >> 2) * kStagingRow + (lane & 3) * 16;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = i * 4 + (lane >> 3);
-        if (row0 + r < rows && col0 + c < cols)
-          *reinterpret_cast<uint4*>(p + (row0 + r) * ld + col0 + c) =
-              *reinterpret_cast<const uint4*>(staging + r * kStagingRow + (lane & 7) * 16);
-      }
-    } else {
+    for (int i = 0; i < 4; ++i)
+      if (row0 + i * 8 + (lane >> 2) < rows && c < cols) *reinterpret_cast<uint4*>(q + i * 8 * ld) = *reinterpret_cast<const uint4*>(from + i * 8 * kStagingRow);
+  } else {
+    constexpr int kPer = 32 / kCols;  // rows at a time
+    const int q = lane % kCols;
 #pragma unroll 8
-      for (int r = 0; r < 32; ++r)
-#pragma unroll
-        for (int q = lane; q < kCols; q += 32)
-          if (row0 + r < rows && col0 + q < cols) p[(row0 + r) * ld + col0 + q] = reinterpret_cast<const T*>(staging + r * kStagingRow)[q];
+    for (int i = 0; i < 32; i += kPer) {
+      const int r = i + lane / kCols;
+      if (row0 + r < rows && col0 + q < cols) p[(row0 + r) * ld + col0 + q] = reinterpret_cast<const T*>(staging + r * kStagingRow)[q];
     }
-    __syncwarp();
   }
-};
+  __syncwarp();
+}
 
-template <typename T>  // a 16-bit type: 64 columns
-__device__ __forceinline__ void load_rows(char* staging, uint32_t (&v)[32], const T* p, int64_t ld, int64_t row0, int64_t rows, int col0, int cols,
+template <typename T>  // a 16-bit type: 32 columns
+__device__ __forceinline__ void load_rows(char* staging, uint32_t (&v)[16], const T* p, int64_t ld, int64_t row0, int64_t rows, int col0, int cols,
                                           bool vec) {
   const int lane = threadIdx.x & 31;
-  if (vec && (col0 + 64 <= cols || cols % 8 == 0)) {
-    uint4 t[8];
+  if (vec && (col0 + 32 <= cols || cols % 8 == 0)) {
+    const int c = col0 + (lane & 3) * 8;
+    const T* q = p + (row0 + (lane >> 2)) * ld + c;
+    uint4 t[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = i * 4 + (lane >> 3);
-      t[i] = row0 + r < rows && col0 + (lane & 7) * 8 < cols ? *reinterpret_cast<const uint4*>(p + (row0 + r) * ld + col0 + (lane & 7) * 8) : make_uint4(0, 0, 0, 0);
-    }
+    for (int i = 0; i < 4; ++i)
+      t[i] = row0 + i * 8 + (lane >> 2) < rows && c < cols ? *reinterpret_cast<const uint4*>(q + i * 8 * ld) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      *reinterpret_cast<uint4*>(staging + (i * 4 + (lane >> 3)) * kStagingRow + (lane & 7) * 16) = t[i];
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(staging + (i * 8 + (lane >> 2)) * kStagingRow + (lane & 3) * 16) = t[i];
   } else {
-    for (int r0 = 0; r0 < 32; r0 += 8) {  // sixteen loads in flight
+    for (int r0 = 0; r0 < 32; r0 += 16) {  // sixteen loads in flight
       T t[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int r = r0 + i / 2, q = lane + 32 * (i & 1);
-        t[i] = row0 + r < rows && col0 + q < cols ? p[(row0 + r) * ld + col0 + q] : from_f<T>(0.0f);
-      }
+      for (int i = 0; i < 16; ++i) t[i] = row0 + r0 + i < rows && col0 + lane < cols ? p[(row0 + r0 + i) * ld + col0 + lane] : from_f<T>(0.0f);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) reinterpret_cast<T*>(staging + (r0 + i / 2) * kStagingRow)[lane + 32 * (i & 1)] = t[i];
+      for (int i = 0; i < 16; ++i) reinterpret_cast<T*>(staging + (r0 + i) * kStagingRow)[lane] = t[i];
     }
   }
   __syncwarp();
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < 4; ++j) {
     const uint4 t = *reinterpret_cast<const uint4*>(staging + lane * kStagingRow + j * 16);
     v[4 * j] = t.x, v[4 * j + 1] = t.y, v[4 * j + 2] = t.z, v[4 * j + 3] = t.w;
   }
   __syncwarp();
 }
 
-// 64 codes of a row, packed in 16 words; codes are contiguous rows of `cols`
-constexpr int kCodeRow = 80;
-__device__ __forceinline__ void store_codes(char* staging, const uint32_t (&v)[16], int8_t* p, int64_t row0, int64_t rows, int col0, int cols, bool vec) {
+// 32 codes of a row, packed in 8 words; codes are contiguous rows of `cols`
+constexpr int kCodeRow = 48;
+__device__ __forceinline__ void store_codes(char* staging, const uint32_t (&v)[8], int8_t* p, int64_t row0, int64_t rows, int col0, int cols, bool vec) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+  for (int j = 0; j < 2; ++j)
     *reinterpret_cast<uint4*>(staging + lane * kCodeRow + j * 16) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
   __syncwarp();
   if (vec) {  // cols is a multiple of 16
+    const int c = col0 + (lane & 1) * 16;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = i * 8 + (lane >> 2);
-      if (row0 + r < rows && col0 + (lane & 3) * 16 < cols)
-        *reinterpret_cast<uint4*>(p + (row0 + r) * cols + col0 + (lane & 3) * 16) = *reinterpret_cast<const uint4*>(staging + r * kCodeRow + (lane & 3) * 16);
+    for (int i = 0; i < 2; ++i) {
+      const int r = i * 16 + (lane >> 1);
+      if (row0 + r < rows && c < cols)
+        *reinterpret_cast<uint4*>(p + (row0 + r) * cols + c) = *reinterpret_cast<const uint4*>(staging + r * kCodeRow + (lane & 1) * 16);
     }
   } else {
 #pragma unroll 8
     for (int r = 0; r < 32; ++r)
-#pragma unroll
-      for (int q = lane; q < 64; q += 32)
-        if (row0 + r < rows && col0 + q < cols) p[(row0 + r) * cols + col0 + q] = (staging + r * kCodeRow)[q];
+      if (row0 + r < rows && col0 + lane < cols) p[(row0 + r) * cols + col0 + lane] = (staging + r * kCodeRow)[lane];
   }
   __syncwarp();
 }
-__device__ __forceinline__ void load_codes(char* staging, uint32_t (&v)[16], const int8_t* p, int64_t row0, int64_t rows, int col0, int cols, bool vec) {
+__device__ __forceinline__ void load_codes(char* staging, uint32_t (&v)[8], const int8_t* p, int64_t row0, int64_t rows, int col0, int cols, bool vec) {
   const int lane = threadIdx.x & 31;
   if (vec) {
-    uint4 t[4];
+    const int c = col0 + (lane & 1) * 16;
+    uint4 t[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = i * 8 + (lane >> 2);
-      t[i] = row0 + r < rows && col0 + (lane & 3) * 16 < cols ? *reinterpret_cast<const uint4*>(p + (row0 + r) * cols + col0 + (lane & 3) * 16) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 2; ++i) {
+      const int r = i * 16 + (lane >> 1);
+      t[i] = row0 + r < rows && c < cols ? *reinterpret_cast<const uint4*>(p + (row0 + r) * cols + c) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(staging + (i * 8 + (lane >> 2)) * kCodeRow + (lane & 3) * 16) = t[i];
+    for (int i = 0; i < 2; ++i) *reinterpret_cast<uint4*>(staging + (i * 16 + (lane >> 1)) * kCodeRow + (lane & 1) * 16) = t[i];
   } else {
-    for (int r0 = 0; r0 < 32; r0 += 8) {
+    for (int r0 = 0; r0 < 32; r0 += 16) {
       int8_t t[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int r = r0 + i / 2, q = lane + 32 * (i & 1);
-        t[i] = row0 + r < rows && col0 + q < cols ? p[(row0 + r) * cols + col0 + q] : (int8_t)0;
-      }
+      for (int i = 0; i < 16; ++i) t[i] = row0 + r0 + i < rows && col0 + lane < cols ? p[(row0 + r0 + i) * cols + col0 + lane] : (int8_t)0;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) (staging + (r0 + i / 2) * kCodeRow)[lane + 32 * (i & 1)] = t[i];
+      for (int i = 0; i < 16; ++i) (staging + (r0 + i) * kCodeRow)[lane] = t[i];
     }
   }
   __syncwarp();
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < 2; ++j) {
     const uint4 t = *reinterpret_cast<const uint4*>(staging + lane * kCodeRow + j * 16);
     v[4 * j] = t.x, v[4 * j + 1] = t.y, v[4 * j + 2] = t.z, v[4 * j + 3] = t.w;
   }
@@ -330,8 +336,10 @@ __device__ __forceinline__ void load_codes(char* staging, uint32_t (&v)[16], con
 }
 
 // ------------------------------------------------------------------------------------------------
-// Epilogues.  run() has 64 columns from col0 on of the 32 rows from row0 on: a lane has row row0 + lane, in
-// 32 pairs.
+// Epilogues.  A lane has row row0 + lane.  run() of the fused ones reads the warp's 64 columns from col0 on
+// out of tensor memory, 32 at a time, by load(half, pairs), and calls release() after the last read: a rolled
+// loop over the halves, with few registers and little code, lets sixteen warps run side by side (eight warps
+// with all 64 columns in registers: 2.2 times the time at 9728 x 1024 x 4096 with gelu and checkpoint).
 
 template <typename T>
 struct ForwardEpilogue {
@@ -348,49 +356,71 @@ struct ForwardEpilogue {
   int act;
   bool vec_bias, vec_res, vec_y, vec_codes;
 
-  template <int ACT>
-  __device__ __forceinline__ void finish(f2 (&z)[32], uint32_t (&v)[32]) const {  // v: in the residual, out y
+  __device__ __forceinline__ void add_bias(f2 (&z)[16], int col0, int cols) const {
+    if (!bias) return;
+    if (vec_bias && col0 + 32 <= cols) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const f2 a = act2<ACT>(z[i]);
+      for (int i = 0; i < 8; ++i) {
+        const float4 b = __ldg(reinterpret_cast<const float4*>(bias + col0) + i);
+        z[2 * i] = add2(z[2 * i], pair(b.x, b.y)), z[2 * i + 1] = add2(z[2 * i + 1], pair(b.z, b.w));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int c = col0 + 2 * i;
+        z[i] = add2(z[i], pair(c < cols ? __ldg(bias + c) : 0.0f, c + 1 < cols ? __ldg(bias + c + 1) : 0.0f));
+      }
+    }
+  }
+  template <int ACT>
+  __device__ __forceinline__ void finish(const ActConsts& k, f2 (&z)[16], uint32_t (&v)[16]) const {  // v: in the residual, out y
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const f2 a = act2<ACT>(k, z[i]);
       v[i] = narrow<T>(residual ? add2(a, widen<T>(v[i])) : a);
     }
   }
-  __device__ __forceinline__ void run(f2 (&z)[32], int64_t row0, int64_t rows, int col0, int cols, int, char* staging) const {
-    const int64_t row = row0 + (threadIdx.x & 31);
-    if (bias) {
-      if (vec_bias && col0 + 64 <= cols) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float4 b = __ldg(reinterpret_cast<const float4*>(bias + col0) + i);
-          z[2 * i] = add2(z[2 * i], pair(b.x, b.y)), z[2 * i + 1] = add2(z[2 * i + 1], pair(b.z, b.w));
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const int c = col0 + 2 * i;
-          z[i] = add2(z[i], pair(c < cols ? __ldg(bias + c) : 0.0f, c + 1 < cols ? __ldg(bias + c + 1) : 0.0f));
-        }
-      }
-    }
+  template <class Load, class Release>
+  __device__ __forceinline__ void run(Load&& load, Release&& release, const ActConsts& k, int64_t row0, int64_t rows, int col0, int cols,
+                                      char* staging) const {
+    float inv = 0.0f;
     if (codes) {  // columns past the end have z = 0: their operand rows were filled with zeros
       float most = 0.0f;
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        f2 z[16];
+        load(half, z);
+        add_bias(z, col0 + 32 * half, cols);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) most = max_abs(most, z[i]);
+        for (int i = 0; i < 16; ++i) most = max_abs(most, z[i]);
+      }
       const BlockScale s = block_scale(most);
-      uint32_t c[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) c[i] = codes4(z[2 * i], z[2 * i + 1], s.inv);
+      const int64_t row = row0 + (threadIdx.x & 31);
       if (row < rows) scales[row * blocks + col0 / kBlock] = s.scale;
-      store_codes(staging, c, codes, row0, rows, col0, cols, vec_codes);
+      inv = s.inv;
     }
-    uint32_t v[32];
-    if (residual) load_rows(staging, v, residual, ldr, row0, rows, col0, cols, vec_res);
-    if (act == ONEBIT_ACT_NONE) finish<ONEBIT_ACT_NONE>(z, v);
-    else if (act == ONEBIT_ACT_RELU) finish<ONEBIT_ACT_RELU>(z, v);
-    else if (act == ONEBIT_ACT_GELU) finish<ONEBIT_ACT_GELU>(z, v);
-    else finish<ONEBIT_ACT_GELU_TANH>(z, v);
-    RowStore<T>::run(staging, v, y, ldy, row0, rows, col0, cols, vec_y);
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      f2 z[16];
+      uint32_t v[16];
+      load(half, z);
+      if (half) release();
+      const int c0 = col0 + 32 * half;
+      if (c0 >= cols) continue;
+      add_bias(z, c0, cols);
+      if (codes) {
+        uint32_t c[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = codes4(z[2 * i], z[2 * i + 1], inv);
+        store_codes(staging, c, codes, row0, rows, c0, cols, vec_codes);
+      }
+      if (residual) load_rows(staging, v, residual, ldr, row0, rows, c0, cols, vec_res);
+      if (act == ONEBIT_ACT_NONE) finish<ONEBIT_ACT_NONE>(k, z, v);
+      else if (act == ONEBIT_ACT_RELU) finish<ONEBIT_ACT_RELU>(k, z, v);
+      else if (act == ONEBIT_ACT_GELU) finish<ONEBIT_ACT_GELU>(k, z, v);
+      else finish<ONEBIT_ACT_GELU_TANH>(k, z, v);
+      store_rows(staging, v, y, ldy, row0, rows, c0, cols, vec_y);
+    }
   }
 };
 
@@ -412,57 +442,68 @@ struct InputGradEpilogue {
   int act;
   bool vec_x, vec_codes, vec_add, vec_dx;
 
+  // z in: the kept values as 16-bit words; z out: h
   template <int ACT>
-  __device__ __forceinline__ void slopes(f2 (&d)[32], uint32_t (&v)[32]) const {  // v: in the kept values, out h
+  __device__ __forceinline__ void slopes(const ActConsts& k, f2 (&d)[16], uint32_t (&v)[16]) const {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < 16; ++i) {
       f2 a, s;
-      activate<ACT, true, true>(widen<T>(v[i]), a, s);
+      activate<ACT, true, true>(k, widen<T>(v[i]), a, s);
       d[i] = mul2(d[i], s);
       v[i] = narrow<T>(a);
     }
   }
   template <int ACT>
-  __device__ __forceinline__ void slopes(f2 (&d)[32], const uint32_t (&c)[16], float scale, uint32_t (&v)[32]) const {
+  __device__ __forceinline__ void slopes(const ActConsts& k, f2 (&d)[16], const uint32_t (&c)[8], float scale, uint32_t (&v)[16]) const {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < 8; ++i) {
       f2 z[2];
       values4<T>(c[i], scale, z);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         f2 a, s;
-        activate<ACT, true, true>(z[j], a, s);
+        activate<ACT, true, true>(k, z[j], a, s);
         if (ACT != ONEBIT_ACT_NONE) d[2 * i + j] = mul2(d[2 * i + j], s);
         v[2 * i + j] = narrow<T>(a);
       }
     }
   }
-  __device__ __forceinline__ void run(f2 (&d)[32], int64_t row0, int64_t rows, int col0, int cols, int, char* staging) const {
-    uint32_t v[32];
-    if (codes && (act != ONEBIT_ACT_NONE || h)) {
-      uint32_t c[16];
-      load_codes(staging, c, codes, row0, rows, col0, cols, vec_codes);
-      const int64_t row = row0 + (threadIdx.x & 31);
-      const float s = row < rows ? __ldg(scales + row * blocks + col0 / kBlock) : 0.0f;
-      if (act == ONEBIT_ACT_NONE) slopes<ONEBIT_ACT_NONE>(d, c, s, v);
-      else if (act == ONEBIT_ACT_RELU) slopes<ONEBIT_ACT_RELU>(d, c, s, v);
-      else if (act == ONEBIT_ACT_GELU) slopes<ONEBIT_ACT_GELU>(d, c, s, v);
-      else slopes<ONEBIT_ACT_GELU_TANH>(d, c, s, v);
-    } else if (act != ONEBIT_ACT_NONE) {
-      load_rows(staging, v, x, ldx, row0, rows, col0, cols, vec_x);
-      if (act == ONEBIT_ACT_RELU) slopes<ONEBIT_ACT_RELU>(d, v);
-      else if (act == ONEBIT_ACT_GELU) slopes<ONEBIT_ACT_GELU>(d, v);
-      else slopes<ONEBIT_ACT_GELU_TANH>(d, v);
-    }
-    if (h) RowStore<T>::run(staging, v, h, ldh, row0, rows, col0, cols, true);
-    if (add) {
-      load_rows(staging, v, add, ldadd, row0, rows, col0, cols, vec_add);
+  template <class Load, class Release>
+  __device__ __forceinline__ void run(Load&& load, Release&& release, const ActConsts& k, int64_t row0, int64_t rows, int col0, int cols,
+                                      char* staging) const {
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      f2 d[16];
+      uint32_t v[16];
+      load(half, d);
+      if (half) release();
+      const int c0 = col0 + 32 * half;
+      if (c0 >= cols) continue;
+      if (codes && (act != ONEBIT_ACT_NONE || h)) {
+        uint32_t c[8];
+        load_codes(staging, c, codes, row0, rows, c0, cols, vec_codes);
+        const int64_t row = row0 + (threadIdx.x & 31);
+        const float s = row < rows ? __ldg(scales + row * blocks + col0 / kBlock) : 0.0f;
+        if (act == ONEBIT_ACT_NONE) slopes<ONEBIT_ACT_NONE>(k, d, c, s, v);
+        else if (act == ONEBIT_ACT_RELU) slopes<ONEBIT_ACT_RELU>(k, d, c, s, v);
+        else if (act == ONEBIT_ACT_GELU) slopes<ONEBIT_ACT_GELU>(k, d, c, s, v);
+        else slopes<ONEBIT_ACT_GELU_TANH>(k, d, c, s, v);
+      } else if (act != ONEBIT_ACT_NONE) {
+        load_rows(staging, v, x, ldx, row0, rows, c0, cols, vec_x);
+        if (act == ONEBIT_ACT_RELU) slopes<ONEBIT_ACT_RELU>(k, d, v);
+        else if (act == ONEBIT_ACT_GELU) slopes<ONEBIT_ACT_GELU>(k, d, v);
+        else slopes<ONEBIT_ACT_GELU_TANH>(k, d, v);
+      }
+      if (h) store_rows(staging, v, h, ldh, row0, rows, c0, cols, true);
+      if (add) {
+        load_rows(staging, v, add, ldadd, row0, rows, c0, cols, vec_add);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) d[i] = add2(d[i], widen<T>(v[i]));
-    }
+        for (int i = 0; i < 16; ++i) d[i] = add2(d[i], widen<T>(v[i]));
+      }
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = narrow<T>(d[i]);
-    RowStore<T>::run(staging, v, dx, lddx, row0, rows, col0, cols, vec_dx);
+      for (int i = 0; i < 16; ++i) v[i] = narrow<T>(d[i]);
+      store_rows(staging, v, dx, lddx, row0, rows, c0, cols, vec_dx);
+    }
   }
 };
 
@@ -470,27 +511,28 @@ template <typename G>
 struct PlainEpilogue {
   // the product itself in G; split s of a cut contraction goes to p + s * split_stride
   static constexpr bool kFold = true;
+  static constexpr int act = ONEBIT_ACT_NONE;
   G* p;
   int64_t ld;
   int64_t split_stride;
   bool vec;
-  __device__ __forceinline__ void run(f2 (&d)[32], int64_t row0, int64_t rows, int col0, int cols, int split, char* staging) const {
+  __device__ __forceinline__ void run(f2 (&d)[16], int64_t row0, int64_t rows, int col0, int cols, int split, char* staging) const {
     G* out = p + split * split_stride;
-    uint32_t v[32];
+    uint32_t v[16];
     if (sizeof(G) == 4) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
+      for (int q = 0; q < 2; ++q) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 f = halves(d[16 * half + i]);
+        for (int i = 0; i < 8; ++i) {
+          const float2 f = halves(d[8 * q + i]);
           v[2 * i] = __float_as_uint(f.x), v[2 * i + 1] = __float_as_uint(f.y);
         }
-        RowStore<G>::run(staging, v, out, ld, row0, rows, col0 + 32 * half, cols, vec);
+        store_rows(staging, v, out, ld, row0, rows, col0 + 16 * q, cols, vec);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = narrow<std::conditional_t<sizeof(G) == 4, __half, G>>(d[i]);
-      RowStore<G>::run(staging, v, out, ld, row0, rows, col0, cols, vec);
+      for (int i = 0; i < 16; ++i) v[i] = narrow<std::conditional_t<sizeof(G) == 4, __half, G>>(d[i]);
+      store_rows(staging, v, out, ld, row0, rows, col0, cols, vec);
     }
   }
 };
@@ -519,14 +561,14 @@ __device__ __forceinline__ Tile tile_of(const ProductArgs& P, int64_t unit) {
 }
 
 template <int CTAS, bool A_MN, bool B_MN, class Epilogue>
-__global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_constant__ ProductArgs P, const __grid_constant__ Epilogue E) {
+__global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __grid_constant__ ProductArgs P, const __grid_constant__ Epilogue E) {
   constexpr int kTileN = kRowsPerBlock * CTAS;
-  constexpr int kCols = kTileN / 2;             // columns of an epilogue warp
   constexpr uint32_t kTmemCols = 2 * kTileN;    // two accumulators
   extern __shared__ char smem_raw[];
   char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   char* staging_base = smem + kStages * kStageBytes;
-  char* bars = staging_base + kEpilogueWarps * kStagingBytes;
+  char* bars = staging_base + kEpilogueWarps<CTAS> * kStagingBytes;
+  f2* consts = reinterpret_cast<f2*>(bars + kBarrierBytes);
   const uint32_t bar0 = smem_addr(bars);
   auto full = [&](int s) { return bar0 + 8 * s; };
   auto empty = [&](int s) { return bar0 + 8 * (kStages + s); };
@@ -544,9 +586,12 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) bar_init(full(s), 1), bar_init(empty(s), 1);
-    for (int s = 0; s < 2; ++s) bar_init(acc_full(s), 1), bar_init(acc_empty(s), CTAS * kEpilogueWarps);
+    for (int s = 0; s < 2; ++s) bar_init(acc_full(s), 1), bar_init(acc_empty(s), CTAS * kEpilogueWarps<CTAS>);
     bar_init(drained, 1);
     *gave_up = 0;
+#pragma unroll
+    for (int i = 0; i < kActConsts; ++i)
+      consts[i] = splat(E.act == ONEBIT_ACT_GELU ? act_const(ONEBIT_ACT_GELU, i) : act_const(ONEBIT_ACT_GELU_TANH, i));
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc<CTAS>(smem_addr((const void*)tmem_ptr), kTmemCols);
@@ -557,16 +602,19 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
   const uint32_t tmem = *tmem_ptr;
   launch_next();
 
-  // the epilogue warps take the registers that the control warps do not need
+  // a pair's epilogue warps take the registers that its control warps do not need
   if (warp >= 4) {
     // ---- epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpilogueRegs));
-    const int quad = warp & 3, half = (warp - 4) >> 2;
+    if (CTAS == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpilogueRegs));
+    const int quad = warp & 3, group = (warp - 4) >> 2;
     char* staging = staging_base + (warp - 4) * kStagingBytes;
-    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + half * kCols;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + group * 64;
+    ActConsts k;
+#pragma unroll
+    for (int i = 0; i < kActConsts; ++i) k.k[i] = *const_cast<volatile f2*>(consts + i);
     int acc = 0;
     uint32_t acc_phase = 0;
-    // the accumulator is in registers: the next product may write over it
+    // the accumulator has been read: the next product may write over it
     auto release = [&] {
       tmem_fence_before();
       __syncwarp();
@@ -582,60 +630,48 @@ __global__ void __launch_bounds__(kProductThreads, 1) k_product(const __grid_con
     for (int64_t u = first_unit; u < units && ok; u += unit_step) {
       const Tile t = tile_of<CTAS>(P, u);
       const int64_t row0 = t.m0 + rank * kRowsPerBlock + quad * 32;
-      const int col0 = t.n0 + half * kCols;
-      if (Epilogue::kFold) {
-        f2 c[kCols / 64][32];
+      const int col0 = t.n0 + group * 64;
+      const bool inside = row0 < P.m && col0 < P.n;
+      if constexpr (Epilogue::kFold) {
+        f2 c[2][16];
         for (int k0 = 0; k0 < t.slabs; k0 += kFoldSlabs) {
           if (!(ok = ready())) break;
           const uint32_t at = lanes + acc * kTileN;
-          if (k0 == 0) {
 #pragma unroll
-            for (int q = 0; q < kCols; q += 32) {
-              float v[32];
-              tmem_load32(at + q, v);
-              tmem_wait_load();
-              tmem_hold32(v);
+          for (int q = 0; q < 4; ++q) {
+            float v[16];
+            tmem_load16(at + 16 * q, v);
+            tmem_wait_load();
+            tmem_hold16(v);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) c[q / 64][q % 64 / 2 + i] = pair(v[2 * i], v[2 * i + 1]);
-            }
-          } else {
-#pragma unroll
-            for (int q = 0; q < kCols; q += 32) {
-              float v[32];
-              tmem_load32(at + q, v);
-              tmem_wait_load();
-              tmem_hold32(v);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) c[q / 64][q % 64 / 2 + i] = add2(c[q / 64][q % 64 / 2 + i], pair(v[2 * i], v[2 * i + 1]));
+            for (int i = 0; i < 8; ++i) {
+              f2& s = c[q / 2][q % 2 * 8 + i];
+              s = k0 ? add2(s, pair(v[2 * i], v[2 * i + 1])) : pair(v[2 * i], v[2 * i + 1]);
             }
           }
           release();
         }
         if (!ok) break;
 #pragma unroll
-        for (int q = 0; q < kCols / 64; ++q)
-          if (row0 < P.m && col0 + 64 * q < P.n) E.run(c[q], row0, P.m, col0 + 64 * q, P.n, t.split, staging);
+        for (int q = 0; q < 2; ++q)
+          if (inside && col0 + 32 * q < P.n) E.run(c[q], row0, P.m, col0 + 32 * q, P.n, t.split, staging);
       } else {
         if (!(ok = ready())) break;
         const uint32_t at = lanes + acc * kTileN;
-#pragma unroll
-        for (int q = 0; q < kCols / 64; ++q) {
-          float raw[64];
-          tmem_load32(at + 64 * q, raw);
-          tmem_load32(at + 64 * q + 32, raw + 32);
+        auto load = [&](int half, f2(&z)[16]) {
+          float v[32];
+          tmem_load32(at + 32 * half, v);
           tmem_wait_load();
-          tmem_hold32(raw);
-          tmem_hold32(raw + 32);
-          f2 c[32];
+          tmem_hold32(v);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) c[i] = pair(raw[2 * i], raw[2 * i + 1]);
-          if (q == kCols / 64 - 1) release();
-          if (row0 < P.m && col0 + 64 * q < P.n) E.run(c, row0, P.m, col0 + 64 * q, P.n, t.split, staging);
-        }
+          for (int i = 0; i < 16; ++i) z[i] = pair(v[2 * i], v[2 * i + 1]);
+        };
+        if (inside) E.run(load, release, k, row0, P.m, col0, P.n, staging);
+        else release();
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
+    if (CTAS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
     if (warp == 0 && lane == 0) {
       // ---- copies
       int st = 0;
@@ -752,15 +788,15 @@ cudaError_t launch_product(const ProductArgs& P, const Epilogue& E, int sms, cud
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem<CTAS>);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
   const int64_t units = (int64_t)P.tiles_m * P.tiles_n * P.splits, most = sms / CTAS;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((units < most ? units : most) * CTAS));
-  cfg.blockDim = dim3(kProductThreads);
-  cfg.dynamicSmemBytes = kProductSmem;
+  cfg.blockDim = dim3(kProductThreads<CTAS>);
+  cfg.dynamicSmemBytes = kProductSmem<CTAS>;
   cfg.stream = s;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
