@@ -112,11 +112,25 @@ cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, b
     const Partials part = take_partials(ws, plan, a.rows, a.in);
     const T* add = static_cast<const T*>(a.add);
     if (run && plan.splits == 1) {
-      const InputGradEpilogue<T> e{v.x, a.ldx, a.codes, a.scales, v.blocks, add, a.ldadd, static_cast<T*>(a.dx), a.lddx, h, ldh, a.activation,
-                                   vec16(v.x, a.ldx), aligned(a.codes, 16) && a.in % 16 == 0, vec16(add, a.ldadd), vec16(a.dx, a.lddx)};
-      err = run_product<false, true>(a.dtype, dy, w, sx, plan, e, s);
+      InputGradEpilogue<T> e{};
+      e.x = v.x;
+      e.ldx = a.ldx;
+      e.codes = a.codes;
+      e.scales = a.scales;
+      e.blocks = v.blocks;
+      e.add = add;
+      e.ldadd = a.ldadd;
+      e.act = a.activation;
+      e.vec_x = vec16(v.x, a.ldx);
+      e.vec_codes = aligned(a.codes, 16) && a.in % 16 == 0;
+      e.vec_add = vec16(add, a.ldadd);
+      err = make_output(&e.dx, static_cast<T*>(a.dx), a.rows, a.in, a.lddx);
+      if (err == cudaSuccess) err = make_output(&e.h, h, a.rows, a.in, ldh);
+      if (err == cudaSuccess) err = run_product<false, true>(a.dtype, dy, w, sx, plan, e, s);
     } else if (run) {
-      err = run_product<false, true>(a.dtype, dy, w, sx, plan, to_partials(part), s);
+      PlainEpilogue<float> to{};
+      err = to_partials(&to, part, a.in);
+      if (err == cudaSuccess) err = run_product<false, true>(a.dtype, dy, w, sx, plan, to, s);
       k_finish_dx<T><<<flat_grid(a.rows * a.in, 256), 256, 0, s>>>(part, a.rows, (int)a.in, v, a.activation, add, a.ldadd,
                                                                    static_cast<T*>(a.dx), a.lddx, h, ldh);
     }
@@ -132,10 +146,13 @@ cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, b
       with_grad(a.grad_dtype, a.dw, [&](auto* g) {
         using G = std::remove_pointer_t<decltype(g)>;
         if (plan.splits == 1) {
-          const PlainEpilogue<G> e{g, a.in, 0, aligned(g, 16) && a.in % (16 / (int64_t)sizeof(G)) == 0};
-          err = run_product<true, true>(a.dtype, dy, x, sw, plan, e, s);
+          PlainEpilogue<G> e{};
+          err = make_output(&e.out, g, a.out, a.in, a.in);
+          if (err == cudaSuccess) err = run_product<true, true>(a.dtype, dy, x, sw, plan, e, s);
         } else {
-          err = run_product<true, true>(a.dtype, dy, x, sw, plan, to_partials(part), s);
+          PlainEpilogue<float> to{};
+          err = to_partials(&to, part, a.in);
+          if (err == cudaSuccess) err = run_product<true, true>(a.dtype, dy, x, sw, plan, to, s);
           k_finish_dw<<<flat_grid(a.out * a.in, 256), 256, 0, s>>>(part, a.out, (int)a.in, g);
         }
       });

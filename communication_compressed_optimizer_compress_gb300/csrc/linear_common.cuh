@@ -86,13 +86,15 @@ inline Partials take_partials(Space& ws, const ProductPlan& plan, int64_t rows, 
   Partials q{};
   if (plan.splits == 1) return q;
   q.ld = (cols + 3) & ~(int64_t)3;
-  q.split_stride = rows * q.ld;
+  q.split_stride = ((rows + 31) & ~(int64_t)31) * q.ld;
   q.splits = plan.splits;
   q.p = ws.take<float>(q.split_stride * plan.splits);
   return q;
 }
-inline PlainEpilogue<float> to_partials(const Partials& q) {
-  return PlainEpilogue<float>{const_cast<float*>(q.p), q.ld, q.split_stride, true};
+// Each split's tile rows are a multiple of the store boxes' (32): a box never reaches into the next split.
+inline cudaError_t to_partials(PlainEpilogue<float>* e, const Partials& q, int64_t cols) {
+  e->split_rows = q.split_stride / q.ld;
+  return make_output(&e->out, const_cast<float*>(q.p), e->split_rows * q.splits, cols, q.ld);
 }
 
 template <typename F>

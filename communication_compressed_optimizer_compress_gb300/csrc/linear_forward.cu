@@ -8,7 +8,7 @@ namespace {
 
 // The epilogue over the partial sums of a cut contraction, one warp per 64 columns of a row.
 template <typename T>
-__global__ void __launch_bounds__(256) k_finish_forward(Partials c, int64_t rows, int cols, ForwardEpilogue<T> e) {
+__global__ void __launch_bounds__(256) k_finish_forward(Partials c, int64_t rows, int cols, const __grid_constant__ ForwardEpilogue<T> e) {
   const int lane = threadIdx.x & 31;
   const int64_t units = rows * e.blocks, step = (int64_t)gridDim.x * 8;
   for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < units; u += step) {
@@ -23,14 +23,14 @@ __global__ void __launch_bounds__(256) k_finish_forward(Partials c, int64_t rows
         z[q] = c.at(r, col) + (e.bias ? e.bias[col] : 0.0f);
         float v = act_value(e.act, z[q]);
         if (e.residual) v += to_f(e.residual[r * e.ldr + col]);
-        e.y[r * e.ldy + col] = from_f<T>(v);
+        e.y.p[r * e.y.ld + col] = from_f<T>(v);
       }
     }
-    if (e.codes) {
+    if (e.scales) {
       const BlockScale s = block_scale(warp_max_nan(max_nan(fabsf(z[0]), fabsf(z[1]))));
 #pragma unroll
       for (int q = 0; q < 2; ++q)
-        if (c0 + 32 * q < cols) e.codes[r * cols + c0 + 32 * q] = (int8_t)code_of(z[q], s.inv);
+        if (c0 + 32 * q < cols) e.codes.p[r * cols + c0 + 32 * q] = (int8_t)code_of(z[q], s.inv);
       if (lane == 0) e.scales[u] = s.scale;
     }
   }
@@ -44,11 +44,22 @@ cudaError_t forward(const onebit_linear_t& a, Space& ws, cudaStream_t s, bool ru
   const Operand x = readable(ws, a.x, a.ldx, a.rows, a.in, s, run), w = readable(ws, a.w, a.ldw, a.out, a.in, s, run);
   const Partials part = take_partials(ws, plan, a.rows, a.out);
   if (!run) return cudaSuccess;
-  const ForwardEpilogue<T> e{a.bias, static_cast<const T*>(a.residual), a.ldr, static_cast<T*>(a.y), a.ldy, a.codes, a.scales,
-                             (int)ceil_div(a.out, kBlock), a.activation, aligned(a.bias, 16), vec16(a.residual, a.ldr), vec16(a.y, a.ldy),
-                             aligned(a.codes, 16) && a.out % 16 == 0};
+  ForwardEpilogue<T> e{};
+  e.bias = a.bias;
+  e.residual = static_cast<const T*>(a.residual);
+  e.ldr = a.ldr;
+  e.scales = a.scales;
+  e.blocks = (int)ceil_div(a.out, kBlock);
+  e.act = a.activation;
+  e.vec_bias = aligned(a.bias, 16);
+  e.vec_res = vec16(a.residual, a.ldr);
+  cudaError_t err = make_output(&e.y, static_cast<T*>(a.y), a.rows, a.out, a.ldy);
+  if (err == cudaSuccess) err = make_output(&e.codes, a.codes, a.rows, a.out, a.out);
+  if (err != cudaSuccess) return err;
   if (plan.splits == 1) return run_product<false, false>(a.dtype, x, w, shape, plan, e, s);
-  const cudaError_t err = run_product<false, false>(a.dtype, x, w, shape, plan, to_partials(part), s);
+  PlainEpilogue<float> to{};
+  err = to_partials(&to, part, a.out);
+  if (err == cudaSuccess) err = run_product<false, false>(a.dtype, x, w, shape, plan, to, s);
   if (err != cudaSuccess) return err;
   k_finish_forward<T><<<flat_grid(a.rows * e.blocks * 32, 256), 256, 0, s>>>(part, a.rows, (int)a.out, e);
   return cudaGetLastError();

@@ -45,6 +45,20 @@ cudaError_t make_map(CUtensorMap* map, int32_t dtype, const void* p, int64_t row
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t make_output_map(CUtensorMap* map, int size, const void* p, int64_t rows, int64_t cols, int64_t ld) {
+  const Encode encode = encoder();
+  if (!encode) return cudaErrorNotSupported;
+  // bits only: the type decides nothing but its size
+  const CUtensorMapDataType type = size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : size == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT32;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(ld * size)};
+  const cuuint32_t box[2] = {size == 1 ? 32u : 64u / size, 32u}, step[2] = {1, 1};
+  const CUresult r = encode(map, type, 2, const_cast<void*>(p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            size == 1 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 unsigned int* status_word() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
@@ -69,7 +83,7 @@ ProductPlan plan_product(const ProductShape& s, int sms) {
   double least = 1e300;
   for (int ctas = 1; ctas <= 2; ++ctas) {
     const int64_t tiles = ceil_div(s.m, kRowsPerBlock * ctas) * ceil_div(s.n, kRowsPerBlock * ctas), slots = sms / ctas > 0 ? sms / ctas : 1;
-    for (int64_t want = 1; want <= 16 && (want == 1 || slabs >= 4 * want); ++want) {
+    for (int64_t want = 1; want <= 16 && (want == 1 || (slabs >= 4 * want && s.m * want < (int64_t)1 << 30)); ++want) {
       const int64_t per = ceil_div(slabs, want), splits = ceil_div(slabs, per);
       if (per > 1024 && want < 16) continue;  // one accumulator sums at most 65536 terms, where it can be helped
       const double waves = (double)ceil_div(tiles * splits, slots);

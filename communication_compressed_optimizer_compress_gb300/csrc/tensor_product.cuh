@@ -38,11 +38,15 @@ template <int CTAS>
 constexpr int kProductThreads = 128 + 32 * kEpilogueWarps<CTAS>;
 // A pair's block is launched with 640 * 96 registers; 128 * 56 + 512 * 104 of them are used.
 constexpr int kControlRegs = 56, kEpilogueRegs = 104;
-constexpr int kStagingRow = 80;               // 64 bytes and 16 to spread the rows over the banks
-constexpr int kStagingBytes = 32 * kStagingRow;
+// A warp's staging buffer: 32 rows of 64 bytes (2048, swizzled, what TMA stores; padded to 80 bytes a row
+// where single elements are stored), and behind it 32 rows of 32 codes.
+constexpr int kStagingRow = 80;
+constexpr int kCodeStaging = 32 * kStagingRow;
+constexpr int kStagingBytes = kCodeStaging + 1024;
 constexpr int kBarrierBytes = 256;
 template <int CTAS>
 constexpr int kProductSmem = 1024 + kStages * kStageBytes + kEpilogueWarps<CTAS> * kStagingBytes + kBarrierBytes + kActConsts * 8;
+static_assert(kStagingBytes % 512 == 0, "the swizzle's period");
 constexpr int kFoldSlabs = 8;                 // slabs that an accumulator of a folded product sums up
 constexpr int kGroupTiles = 8;                // tile rows that are walked together, for the L2
 
@@ -55,6 +59,7 @@ struct ProductArgs {
   int32_t slabs;             // of the whole contraction
   int32_t tiles_m, tiles_n;
   int32_t splits, split_slabs;
+  uint32_t units;            // tiles times splits
   uint32_t idesc;
   uint32_t stall_tx;         // test hook: bytes that every stage waits for and no copy brings (normally 0)
   unsigned int* status;
@@ -78,7 +83,7 @@ __device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(bar), "r"(parity)
       : "memory");
@@ -131,19 +136,6 @@ __device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
   else
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
 }
-template <int CTAS>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-  if (CTAS == 2)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a),
-        "l"(b), "r"(idesc), "r"((uint32_t)add)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a),
-        "l"(b), "r"(idesc), "r"((uint32_t)add)
-        : "memory");
-}
 // The barrier (of both blocks of a pair) is arrived at when this thread's instructions so far are done.
 template <int CTAS>
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
@@ -190,13 +182,36 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float* v) {
 // K-major: a row is one m (n) with 64 k; groups of 8 m follow each other (stride 1024), and a step of
 // 16 k is 32 bytes along the row.  MN-major: a row is one k with 64 m; groups of 8 k follow each other
 // (stride 1024), the next 64 m lie one 64-row box (8192 bytes) further, and a step of 16 k is 2048 bytes.
+// The low word holds the address and the leading stride, the high word is the same for all.
 template <bool MN>
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
-  const uint64_t lead = MN ? (8192 >> 4) : 1;
-  return (uint64_t)((addr >> 4) & 0x3fff) | lead << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+__device__ __forceinline__ uint32_t operand_desc(uint32_t addr) {
+  return (addr >> 4 & 0x3fff) | (MN ? 8192u >> 4 : 1u) << 16;
 }
+constexpr uint32_t kDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
 template <bool MN>
-__device__ __forceinline__ constexpr uint32_t k_step() { return MN ? (2048 >> 4) : (32 >> 4); }
+constexpr uint32_t kStep16 = MN ? 2048 >> 4 : 32 >> 4;
+
+// The products of one slab: four steps of 16.  The thread that issues them has about 500 clocks a slab
+// before the tensor cores run dry, beside four busy warps of its scheduler, so the loop around this is kept
+// to a few instructions.
+template <int CTAS, bool A_MN, bool B_MN>
+__device__ __forceinline__ void mma_slab(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+#pragma unroll
+  for (int q = 0; q < kSlabK / 16; ++q) {
+    if (CTAS == 2)
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+          "tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+          "r"(a + q * kStep16<A_MN>), "r"(b + q * kStep16<B_MN>), "r"(idesc), "r"((uint32_t)(add || q > 0)), "r"(kDescHigh)
+          : "memory");
+    else
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+          "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+          "r"(a + q * kStep16<A_MN>), "r"(b + q * kStep16<B_MN>), "r"(idesc), "r"((uint32_t)(add || q > 0)), "r"(kDescHigh)
+          : "memory");
+  }
+}
 
 // ------------------------------------------------------------------------------------------------
 // Waits end after about a second: the block's flag is set, every other wait of the block ends too, and
@@ -223,30 +238,56 @@ struct Wait {
 // Rows of 64 bytes between registers (a lane has a row) and memory (four lanes share a row, so that every
 // access is whole sectors), through the warp's staging buffer.
 
+// Before a staging buffer is written again: the warp's stores out of it have read it.
+__device__ __forceinline__ void staging_free() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
+}
+// The warp's staged box to a matrix, by one lane; what lies outside the matrix is left out.
+__device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y) {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y), "r"(src) : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+}
+
+// A matrix that an epilogue writes: by TMA where its rows start on 16 bytes, element by element elsewhere.
 template <typename T>
-__device__ __forceinline__ void store_rows(char* staging, const uint32_t (&v)[16], T* p, int64_t ld, int64_t row0, int64_t rows, int col0, int cols,
-                                           bool vec) {
-  constexpr int kCols = 64 / sizeof(T), kVec = 16 / sizeof(T);
+struct Output {
+  CUtensorMap map;
+  T* p;
+  int64_t ld;
+  bool by_tma;
+};
+
+// 64 bytes of a lane's row.  (With ordinary stores the way through shared memory and back to registers
+// took most of an epilogue's time, as it shares the SM's shared-memory bandwidth with the products.)
+template <typename T>
+__device__ __forceinline__ void store_rows(char* staging, const uint32_t (&v)[16], const Output<T>& out, int64_t row0, int64_t rows, int col0, int cols) {
+  constexpr int kCols = 64 / sizeof(T);
   const int lane = threadIdx.x & 31;
+  staging_free();
+  if (out.by_tma) {
+    char* row = staging + lane * 64;
+    const int swap = lane >> 1 & 3;  // 64-byte swizzle: 16-byte chunk j of row r lies at j ^ (r / 2 % 4)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<uint4*>(row + (j ^ swap) * 16) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    store_box(&out.map, smem_addr(staging), col0, (int32_t)row0);
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     *reinterpret_cast<uint4*>(staging + lane * kStagingRow + j * 16) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
   __syncwarp();
-  const int c = col0 + (lane & 3) * kVec;
-  if (vec && (col0 + kCols <= cols || cols % kVec == 0)) {
-    T* q = p + (row0 + (lane >> 2)) * ld + c;
-    const char* from = staging + (lane >> 2) * kStagingRow + (lane & 3) * 16;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (row0 + i * 8 + (lane >> 2) < rows && c < cols) *reinterpret_cast<uint4*>(q + i * 8 * ld) = *reinterpret_cast<const uint4*>(from + i * 8 * kStagingRow);
-  } else {
-    constexpr int kPer = 32 / kCols;  // rows at a time
-    const int q = lane % kCols;
+  constexpr int kPer = 32 / kCols;  // rows at a time
+  const int q = lane % kCols;
 #pragma unroll 8
-    for (int i = 0; i < 32; i += kPer) {
-      const int r = i + lane / kCols;
-      if (row0 + r < rows && col0 + q < cols) p[(row0 + r) * ld + col0 + q] = reinterpret_cast<const T*>(staging + r * kStagingRow)[q];
-    }
+  for (int i = 0; i < 32; i += kPer) {
+    const int r = i + lane / kCols;
+    if (row0 + r < rows && col0 + q < cols) out.p[(row0 + r) * out.ld + col0 + q] = reinterpret_cast<const T*>(staging + r * kStagingRow)[q];
   }
   __syncwarp();
 }
@@ -255,6 +296,7 @@ template <typename T>  // a 16-bit type: 32 columns
 __device__ __forceinline__ void load_rows(char* staging, uint32_t (&v)[16], const T* p, int64_t ld, int64_t row0, int64_t rows, int col0, int cols,
                                           bool vec) {
   const int lane = threadIdx.x & 31;
+  staging_free();
   if (vec && (col0 + 32 <= cols || cols % 8 == 0)) {
     const int c = col0 + (lane & 3) * 8;
     const T* q = p + (row0 + (lane >> 2)) * ld + c;
@@ -284,29 +326,30 @@ __device__ __forceinline__ void load_rows(char* staging, uint32_t (&v)[16], cons
 
 // 32 codes of a row, packed in 8 words; codes are contiguous rows of `cols`
 constexpr int kCodeRow = 48;
-__device__ __forceinline__ void store_codes(char* staging, const uint32_t (&v)[8], int8_t* p, int64_t row0, int64_t rows, int col0, int cols, bool vec) {
+__device__ __forceinline__ void store_codes(char* staging, const uint32_t (&v)[8], const Output<int8_t>& out, int64_t row0, int64_t rows, int col0, int cols) {
   const int lane = threadIdx.x & 31;
+  staging_free();
+  if (out.by_tma) {
+    char* row = staging + kCodeStaging + lane * 32;
+    const int swap = lane >> 2 & 1;  // 32-byte swizzle: chunk j of row r lies at j ^ (r / 4 % 2)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      *reinterpret_cast<uint4*>(row + (j ^ swap) * 16) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    store_box(&out.map, smem_addr(staging + kCodeStaging), col0, (int32_t)row0);
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < 2; ++j)
     *reinterpret_cast<uint4*>(staging + lane * kCodeRow + j * 16) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
   __syncwarp();
-  if (vec) {  // cols is a multiple of 16
-    const int c = col0 + (lane & 1) * 16;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = i * 16 + (lane >> 1);
-      if (row0 + r < rows && c < cols)
-        *reinterpret_cast<uint4*>(p + (row0 + r) * cols + c) = *reinterpret_cast<const uint4*>(staging + r * kCodeRow + (lane & 1) * 16);
-    }
-  } else {
 #pragma unroll 8
-    for (int r = 0; r < 32; ++r)
-      if (row0 + r < rows && col0 + lane < cols) p[(row0 + r) * cols + col0 + lane] = (staging + r * kCodeRow)[lane];
-  }
+  for (int r = 0; r < 32; ++r)
+    if (row0 + r < rows && col0 + lane < cols) out.p[(row0 + r) * cols + col0 + lane] = (staging + r * kCodeRow)[lane];
   __syncwarp();
 }
 __device__ __forceinline__ void load_codes(char* staging, uint32_t (&v)[8], const int8_t* p, int64_t row0, int64_t rows, int col0, int cols, bool vec) {
   const int lane = threadIdx.x & 31;
+  staging_free();
   if (vec) {
     const int c = col0 + (lane & 1) * 16;
     uint4 t[2];
@@ -348,13 +391,12 @@ struct ForwardEpilogue {
   const float* bias;
   const T* residual;
   int64_t ldr;
-  T* y;
-  int64_t ldy;
-  int8_t* codes;
-  float* scales;
+  Output<T> y;
+  Output<int8_t> codes;
+  float* scales;  // NULL: no checkpoint
   int blocks;
   int act;
-  bool vec_bias, vec_res, vec_y, vec_codes;
+  bool vec_bias, vec_res;
 
   __device__ __forceinline__ void add_bias(f2 (&z)[16], int col0, int cols) const {
     if (!bias) return;
@@ -384,7 +426,7 @@ struct ForwardEpilogue {
   __device__ __forceinline__ void run(Load&& load, Release&& release, const ActConsts& k, int64_t row0, int64_t rows, int col0, int cols,
                                       char* staging) const {
     float inv = 0.0f;
-    if (codes) {  // columns past the end have z = 0: their operand rows were filled with zeros
+    if (scales) {  // columns past the end have z = 0: their operand rows were filled with zeros
       float most = 0.0f;
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
@@ -408,18 +450,18 @@ struct ForwardEpilogue {
       const int c0 = col0 + 32 * half;
       if (c0 >= cols) continue;
       add_bias(z, c0, cols);
-      if (codes) {
+      if (scales) {
         uint32_t c[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) c[i] = codes4(z[2 * i], z[2 * i + 1], inv);
-        store_codes(staging, c, codes, row0, rows, c0, cols, vec_codes);
+        store_codes(staging, c, codes, row0, rows, c0, cols);
       }
       if (residual) load_rows(staging, v, residual, ldr, row0, rows, c0, cols, vec_res);
       if (act == ONEBIT_ACT_NONE) finish<ONEBIT_ACT_NONE>(k, z, v);
       else if (act == ONEBIT_ACT_RELU) finish<ONEBIT_ACT_RELU>(k, z, v);
       else if (act == ONEBIT_ACT_GELU) finish<ONEBIT_ACT_GELU>(k, z, v);
       else finish<ONEBIT_ACT_GELU_TANH>(k, z, v);
-      store_rows(staging, v, y, ldy, row0, rows, c0, cols, vec_y);
+      store_rows(staging, v, y, row0, rows, c0, cols);
     }
   }
 };
@@ -435,12 +477,9 @@ struct InputGradEpilogue {
   int blocks;
   const T* add;
   int64_t ldadd;
-  T* dx;
-  int64_t lddx;
-  T* h;
-  int64_t ldh;
+  Output<T> dx, h;  // h.p NULL: not wanted
   int act;
-  bool vec_x, vec_codes, vec_add, vec_dx;
+  bool vec_x, vec_codes, vec_add;
 
   // z in: the kept values as 16-bit words; z out: h
   template <int ACT>
@@ -479,7 +518,7 @@ struct InputGradEpilogue {
       if (half) release();
       const int c0 = col0 + 32 * half;
       if (c0 >= cols) continue;
-      if (codes && (act != ONEBIT_ACT_NONE || h)) {
+      if (codes && (act != ONEBIT_ACT_NONE || h.p)) {
         uint32_t c[8];
         load_codes(staging, c, codes, row0, rows, c0, cols, vec_codes);
         const int64_t row = row0 + (threadIdx.x & 31);
@@ -494,7 +533,7 @@ struct InputGradEpilogue {
         else if (act == ONEBIT_ACT_GELU) slopes<ONEBIT_ACT_GELU>(k, d, v);
         else slopes<ONEBIT_ACT_GELU_TANH>(k, d, v);
       }
-      if (h) store_rows(staging, v, h, ldh, row0, rows, c0, cols, true);
+      if (h.p) store_rows(staging, v, h, row0, rows, c0, cols);
       if (add) {
         load_rows(staging, v, add, ldadd, row0, rows, c0, cols, vec_add);
 #pragma unroll
@@ -502,22 +541,21 @@ struct InputGradEpilogue {
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = narrow<T>(d[i]);
-      store_rows(staging, v, dx, lddx, row0, rows, c0, cols, vec_dx);
+      store_rows(staging, v, dx, row0, rows, c0, cols);
     }
   }
 };
 
 template <typename G>
 struct PlainEpilogue {
-  // the product itself in G; split s of a cut contraction goes to p + s * split_stride
+  // the product itself in G; split s of a cut contraction goes to rows s * split_rows and on
   static constexpr bool kFold = true;
   static constexpr int act = ONEBIT_ACT_NONE;
-  G* p;
-  int64_t ld;
-  int64_t split_stride;
-  bool vec;
+  Output<G> out;
+  int64_t split_rows;
   __device__ __forceinline__ void run(f2 (&d)[16], int64_t row0, int64_t rows, int col0, int cols, int split, char* staging) const {
-    G* out = p + split * split_stride;
+    // a split's rows past its own end would fall into the next one's
+    const int64_t at = row0 + split * split_rows, end = split * split_rows + rows;
     uint32_t v[16];
     if (sizeof(G) == 4) {
 #pragma unroll
@@ -527,12 +565,12 @@ struct PlainEpilogue {
           const float2 f = halves(d[8 * q + i]);
           v[2 * i] = __float_as_uint(f.x), v[2 * i + 1] = __float_as_uint(f.y);
         }
-        store_rows(staging, v, out, ld, row0, rows, col0 + 16 * q, cols, vec);
+        if (col0 + 16 * q < cols) store_rows(staging, v, out, at, end, col0 + 16 * q, cols);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = narrow<std::conditional_t<sizeof(G) == 4, __half, G>>(d[i]);
-      store_rows(staging, v, out, ld, row0, rows, col0, cols, vec);
+      store_rows(staging, v, out, at, end, col0, cols);
     }
   }
 };
@@ -543,20 +581,23 @@ struct Tile {
   int64_t m0;
   int n0, split, first, slabs;
 };
+__device__ __forceinline__ int slabs_of(const ProductArgs& P, int split) {
+  const int left = P.slabs - split * P.split_slabs;
+  return left < P.split_slabs ? left : P.split_slabs;
+}
 template <int CTAS>
-__device__ __forceinline__ Tile tile_of(const ProductArgs& P, int64_t unit) {
+__device__ __forceinline__ Tile tile_of(const ProductArgs& P, uint32_t unit) {
   constexpr int kM = kRowsPerBlock * CTAS, kN = kRowsPerBlock * CTAS;
   Tile t;
-  const int64_t tile = unit / P.splits;
+  const uint32_t tile = P.splits == 1 ? unit : unit / P.splits;
   t.split = (int)(unit - tile * P.splits);
   // kGroupTiles tile rows side by side, column after column: the tiles in flight share operand slabs in L2
-  const int64_t per = (int64_t)kGroupTiles * P.tiles_n, g = tile / per;
-  const int rows = (int)(P.tiles_m - g * kGroupTiles < kGroupTiles ? P.tiles_m - g * kGroupTiles : kGroupTiles);
-  const int in = (int)(tile - g * per);
-  t.m0 = (g * kGroupTiles + in % rows) * kM;
-  t.n0 = in / rows * kN;
+  const uint32_t per = (uint32_t)kGroupTiles * P.tiles_n, g = tile / per, m = g * kGroupTiles;
+  const uint32_t rows = P.tiles_m - m < kGroupTiles ? P.tiles_m - m : kGroupTiles, in = tile - g * per, col = in / rows;
+  t.m0 = (int64_t)(m + in - col * rows) * kM;
+  t.n0 = (int)col * kN;
   t.first = t.split * P.split_slabs;
-  t.slabs = P.slabs - t.first < P.split_slabs ? P.slabs - t.first : P.split_slabs;
+  t.slabs = slabs_of(P, t.split);
   return t;
 }
 
@@ -580,8 +621,7 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CTAS == 2 ? cluster_rank() : 0;
-  const int64_t units = (int64_t)P.tiles_m * P.tiles_n * P.splits;
-  const int64_t first_unit = blockIdx.x / CTAS, unit_step = gridDim.x / CTAS;
+  const uint32_t units = P.units, first_unit = blockIdx.x / CTAS, unit_step = gridDim.x / CTAS;
   const Wait wait{gave_up, P.status};
 
   if (threadIdx.x == 0) {
@@ -627,7 +667,7 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
       return ok;
     };
     bool ok = true;
-    for (int64_t u = first_unit; u < units && ok; u += unit_step) {
+    for (uint32_t u = first_unit; u < units && ok; u += unit_step) {
       const Tile t = tile_of<CTAS>(P, u);
       const int64_t row0 = t.m0 + rank * kRowsPerBlock + quad * 32;
       const int col0 = t.n0 + group * 64;
@@ -670,6 +710,7 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
         else release();
       }
     }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the stores have landed
   } else {
     if (CTAS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
     if (warp == 0 && lane == 0) {
@@ -678,10 +719,13 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
       uint32_t phase = 0;
       int64_t issued = 0;
       bool ok = true;
-      for (int64_t u = first_unit; u < units && ok; u += unit_step) {
-        const Tile t = tile_of<CTAS>(P, u);
+      Tile next = tile_of<CTAS>(P, first_unit);
+      for (uint32_t u = first_unit; u < units && ok; u += unit_step) {
+        const Tile t = next;
         const int32_t ma = (int32_t)(t.m0 + rank * kRowsPerBlock), nb = t.n0 + (int)rank * kRowsPerBlock;
         for (int k = 0; k < t.slabs; ++k) {
+          // the next tile's divisions under this tile's copies: at its start they would leave the ring empty
+          if (k == 1 || t.slabs == 1) next = tile_of<CTAS>(P, u + unit_step);
           if (!wait(empty(st), phase ^ 1)) {
             ok = false;
             break;
@@ -716,23 +760,22 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
       }
     } else if (warp == 1 && lane == 0 && rank == 0) {
       // ---- products
+      const uint32_t desc_a = operand_desc<A_MN>(smem_addr(smem)), desc_b = operand_desc<B_MN>(smem_addr(smem) + kOperandBytes);
       int st = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      for (int64_t u = first_unit; u < units && ok; u += unit_step) {
-        const Tile t = tile_of<CTAS>(P, u);
-        for (int k0 = 0, k1; k0 < t.slabs && ok; k0 = k1) {
-          k1 = Epilogue::kFold && t.slabs - k0 > kFoldSlabs ? k0 + kFoldSlabs : t.slabs;
+      for (uint32_t u = first_unit; u < units && ok; u += unit_step) {
+        // nothing but the number of slabs, and that without a division where it is always the same: the tensor
+        // cores run dry while this thread computes
+        const int slabs = P.splits == 1 ? P.slabs : slabs_of(P, (int)(u % P.splits));
+        for (int k0 = 0, k1; k0 < slabs && ok; k0 = k1) {
+          k1 = Epilogue::kFold && slabs - k0 > kFoldSlabs ? k0 + kFoldSlabs : slabs;
           if (!(ok = wait(acc_empty(acc), acc_phase ^ 1))) break;
           tmem_fence_after();
           const uint32_t d = tmem + acc * kTileN;
           for (int k = k0; k < k1; ++k) {
             if (!(ok = wait(full(st), phase))) break;
-            tmem_fence_after();
-            const uint32_t sa = smem_addr(smem + st * kStageBytes);
-            const uint64_t da = operand_desc<A_MN>(sa), db = operand_desc<B_MN>(sa + kOperandBytes);
-  #pragma unroll
-            for (int q = 0; q < kSlabK / 16; ++q) mma<CTAS>(d, da + q * k_step<A_MN>(), db + q * k_step<B_MN>(), P.idesc, k > k0 || q > 0);
+            mma_slab<CTAS, A_MN, B_MN>(d, desc_a + st * (kStageBytes >> 4), desc_b + st * (kStageBytes >> 4), P.idesc, k > k0);
             mma_commit<CTAS>(empty(st));
             if (++st == kStages) st = 0, phase ^= 1;
           }
@@ -762,6 +805,17 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
 // A row-major matrix of rows x cols 16-bit values, copied in boxes of 64 columns by box_rows rows.  The
 // base lies on 16 bytes and ld is a multiple of 8.
 cudaError_t make_map(CUtensorMap* map, int32_t dtype, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows);
+// An output matrix of elements of `size` bytes (1: codes), stored in boxes of 32 rows of 64 bytes (codes: 32).
+cudaError_t make_output_map(CUtensorMap* map, int size, const void* p, int64_t rows, int64_t cols, int64_t ld);
+template <typename T>
+cudaError_t make_output(Output<T>* out, T* p, int64_t rows, int64_t cols, int64_t ld) {
+  *out = Output<T>{};
+  out->p = p;
+  out->ld = ld;
+  if (!p || !aligned(p, 16) || ld * (int64_t)sizeof(T) % 16 != 0) return cudaSuccess;
+  out->by_tma = true;
+  return make_output_map(&out->map, (int)sizeof(T), p, rows, cols, ld);
+}
 unsigned int* status_word();   // of the current device (NULL: a CUDA error)
 uint32_t stall_bytes();        // the test hook's
 
@@ -792,7 +846,7 @@ cudaError_t launch_product(const ProductArgs& P, const Epilogue& E, int sms, cud
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  const int64_t units = (int64_t)P.tiles_m * P.tiles_n * P.splits, most = sms / CTAS;
+  const int64_t units = P.units, most = sms / CTAS;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((units < most ? units : most) * CTAS));
   cfg.blockDim = dim3(kProductThreads<CTAS>);
@@ -822,6 +876,9 @@ cudaError_t run_product(int32_t dtype, const Operand& a, const Operand& b, const
   P.tiles_n = (int32_t)ceil_div(s.n, kRowsPerBlock * plan.ctas);
   P.splits = plan.splits;
   P.split_slabs = plan.split_slabs;
+  const int64_t units = (int64_t)P.tiles_m * P.tiles_n * P.splits;
+  if (units >= (int64_t)1 << 31) return cudaErrorNotSupported;
+  P.units = (uint32_t)units;
   const uint32_t type = dtype == ONEBIT_F16 ? 0u : 1u;  // both operands have the same
   P.idesc = 1u << 4 | type << 7 | type << 10 | (uint32_t)A_MN << 15 | (uint32_t)B_MN << 16 |
             (uint32_t)(kRowsPerBlock * plan.ctas / 8) << 17 | (uint32_t)(kRowsPerBlock * plan.ctas / 16) << 24;
