@@ -51,7 +51,6 @@ cudaError_t forward(const onebit_linear_t& a, Space& ws, cudaStream_t s, bool ru
   e.scales = a.scales;
   e.blocks = (int)ceil_div(a.out, kBlock);
   e.act = a.activation;
-  e.vec_bias = aligned(a.bias, 16);
   e.vec_res = vec16(a.residual, a.ldr);
   cudaError_t err = make_output(&e.y, static_cast<T*>(a.y), a.rows, a.out, a.ldy);
   if (err == cudaSuccess) err = make_output(&e.codes, a.codes, a.rows, a.out, a.out);

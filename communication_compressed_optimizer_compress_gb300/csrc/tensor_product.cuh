@@ -39,10 +39,11 @@ constexpr int kProductThreads = 128 + 32 * kEpilogueWarps<CTAS>;
 // A pair's block is launched with 640 * 96 registers; 128 * 56 + 512 * 104 of them are used.
 constexpr int kControlRegs = 56, kEpilogueRegs = 104;
 // A warp's staging buffer: 32 rows of 64 bytes (2048, swizzled, what TMA stores; padded to 80 bytes a row
-// where single elements are stored), and behind it 32 rows of 32 codes.
+// where single elements are stored), behind it 32 rows of 32 codes, and 64 columns' bias.
 constexpr int kStagingRow = 80;
 constexpr int kCodeStaging = 32 * kStagingRow;
-constexpr int kStagingBytes = kCodeStaging + 1024;
+constexpr int kBiasStaging = kCodeStaging + 1024;
+constexpr int kStagingBytes = kBiasStaging + 512;
 constexpr int kBarrierBytes = 256;
 template <int CTAS>
 constexpr int kProductSmem = 1024 + kStages * kStageBytes + kEpilogueWarps<CTAS> * kStagingBytes + kBarrierBytes + kActConsts * 8;
@@ -384,6 +385,16 @@ __device__ __forceinline__ void load_codes(char* staging, uint32_t (&v)[8], cons
 // loop over the halves, with few registers and little code, lets sixteen warps run side by side (eight warps
 // with all 64 columns in registers: 2.2 times the time at 9728 x 1024 x 4096 with gelu and checkpoint).
 
+// The activation's constants, read once for 32 columns (volatile: as literals, or kept longer than that, they
+// cost more registers or instructions than these few loads).
+template <int ACT>
+__device__ __forceinline__ ActConsts shared_consts(const f2* consts) {
+  ActConsts k;
+#pragma unroll
+  for (int i = 0; i < kActConsts; ++i) k.k[i] = ACT == ONEBIT_ACT_GELU || ACT == ONEBIT_ACT_GELU_TANH ? *const_cast<volatile const f2*>(consts + i) : 0;
+  return k;
+}
+
 template <typename T>
 struct ForwardEpilogue {
   // y = act(d + bias) + residual, and the 8-bit checkpoint of d + bias
@@ -396,26 +407,28 @@ struct ForwardEpilogue {
   float* scales;  // NULL: no checkpoint
   int blocks;
   int act;
-  bool vec_bias, vec_res;
+  bool vec_res;
 
-  __device__ __forceinline__ void add_bias(f2 (&z)[16], int col0, int cols) const {
+  // the warp's 64 columns of the bias, before the product is waited for: two a lane
+  __device__ __forceinline__ void prepare(int col0, int cols, char* staging) const {
     if (!bias) return;
-    if (vec_bias && col0 + 32 <= cols) {
+    const int c = col0 + 2 * (threadIdx.x & 31);
+    const f2 b = pair(c < cols ? __ldg(bias + c) : 0.0f, c + 1 < cols ? __ldg(bias + c + 1) : 0.0f);
+    reinterpret_cast<f2*>(staging + kBiasStaging)[threadIdx.x & 31] = b;
+    __syncwarp();
+  }
+  __device__ __forceinline__ void add_bias(f2 (&z)[16], int half, const char* staging) const {
+    if (!bias) return;
+    const ulonglong2* b = reinterpret_cast<const ulonglong2*>(staging + kBiasStaging + 128 * half);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 b = __ldg(reinterpret_cast<const float4*>(bias + col0) + i);
-        z[2 * i] = add2(z[2 * i], pair(b.x, b.y)), z[2 * i + 1] = add2(z[2 * i + 1], pair(b.z, b.w));
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int c = col0 + 2 * i;
-        z[i] = add2(z[i], pair(c < cols ? __ldg(bias + c) : 0.0f, c + 1 < cols ? __ldg(bias + c + 1) : 0.0f));
-      }
+    for (int i = 0; i < 8; ++i) {
+      const ulonglong2 v = b[i];
+      z[2 * i] = add2(z[2 * i], v.x), z[2 * i + 1] = add2(z[2 * i + 1], v.y);
     }
   }
   template <int ACT>
-  __device__ __forceinline__ void finish(const ActConsts& k, f2 (&z)[16], uint32_t (&v)[16]) const {  // v: in the residual, out y
+  __device__ __forceinline__ void finish(const f2* consts, f2 (&z)[16], uint32_t (&v)[16]) const {  // v: in the residual, out y
+    const ActConsts k = shared_consts<ACT>(consts);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const f2 a = act2<ACT>(k, z[i]);
@@ -423,7 +436,7 @@ struct ForwardEpilogue {
     }
   }
   template <class Load, class Release>
-  __device__ __forceinline__ void run(Load&& load, Release&& release, const ActConsts& k, int64_t row0, int64_t rows, int col0, int cols,
+  __device__ __forceinline__ void run(Load&& load, Release&& release, const f2* consts, int64_t row0, int64_t rows, int col0, int cols,
                                       char* staging) const {
     float inv = 0.0f;
     if (scales) {  // columns past the end have z = 0: their operand rows were filled with zeros
@@ -432,7 +445,7 @@ struct ForwardEpilogue {
       for (int half = 0; half < 2; ++half) {
         f2 z[16];
         load(half, z);
-        add_bias(z, col0 + 32 * half, cols);
+        add_bias(z, half, staging);
 #pragma unroll
         for (int i = 0; i < 16; ++i) most = max_abs(most, z[i]);
       }
@@ -449,7 +462,7 @@ struct ForwardEpilogue {
       if (half) release();
       const int c0 = col0 + 32 * half;
       if (c0 >= cols) continue;
-      add_bias(z, c0, cols);
+      add_bias(z, half, staging);
       if (scales) {
         uint32_t c[8];
 #pragma unroll
@@ -457,12 +470,13 @@ struct ForwardEpilogue {
         store_codes(staging, c, codes, row0, rows, c0, cols);
       }
       if (residual) load_rows(staging, v, residual, ldr, row0, rows, c0, cols, vec_res);
-      if (act == ONEBIT_ACT_NONE) finish<ONEBIT_ACT_NONE>(k, z, v);
-      else if (act == ONEBIT_ACT_RELU) finish<ONEBIT_ACT_RELU>(k, z, v);
-      else if (act == ONEBIT_ACT_GELU) finish<ONEBIT_ACT_GELU>(k, z, v);
-      else finish<ONEBIT_ACT_GELU_TANH>(k, z, v);
+      if (act == ONEBIT_ACT_NONE) finish<ONEBIT_ACT_NONE>(consts, z, v);
+      else if (act == ONEBIT_ACT_RELU) finish<ONEBIT_ACT_RELU>(consts, z, v);
+      else if (act == ONEBIT_ACT_GELU) finish<ONEBIT_ACT_GELU>(consts, z, v);
+      else finish<ONEBIT_ACT_GELU_TANH>(consts, z, v);
       store_rows(staging, v, y, row0, rows, c0, cols);
     }
+    __syncwarp();  // the bias has been read: prepare() may write the next
   }
 };
 
@@ -481,9 +495,10 @@ struct InputGradEpilogue {
   int act;
   bool vec_x, vec_codes, vec_add;
 
-  // z in: the kept values as 16-bit words; z out: h
+  __device__ __forceinline__ void prepare(int, int, char*) const {}
   template <int ACT>
-  __device__ __forceinline__ void slopes(const ActConsts& k, f2 (&d)[16], uint32_t (&v)[16]) const {
+  __device__ __forceinline__ void slopes(const f2* consts, f2 (&d)[16], uint32_t (&v)[16]) const {
+    const ActConsts k = shared_consts<ACT>(consts);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       f2 a, s;
@@ -493,7 +508,8 @@ struct InputGradEpilogue {
     }
   }
   template <int ACT>
-  __device__ __forceinline__ void slopes(const ActConsts& k, f2 (&d)[16], const uint32_t (&c)[8], float scale, uint32_t (&v)[16]) const {
+  __device__ __forceinline__ void slopes(const f2* consts, f2 (&d)[16], const uint32_t (&c)[8], float scale, uint32_t (&v)[16]) const {
+    const ActConsts k = shared_consts<ACT>(consts);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       f2 z[2];
@@ -508,7 +524,7 @@ struct InputGradEpilogue {
     }
   }
   template <class Load, class Release>
-  __device__ __forceinline__ void run(Load&& load, Release&& release, const ActConsts& k, int64_t row0, int64_t rows, int col0, int cols,
+  __device__ __forceinline__ void run(Load&& load, Release&& release, const f2* consts, int64_t row0, int64_t rows, int col0, int cols,
                                       char* staging) const {
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
@@ -523,15 +539,15 @@ struct InputGradEpilogue {
         load_codes(staging, c, codes, row0, rows, c0, cols, vec_codes);
         const int64_t row = row0 + (threadIdx.x & 31);
         const float s = row < rows ? __ldg(scales + row * blocks + col0 / kBlock) : 0.0f;
-        if (act == ONEBIT_ACT_NONE) slopes<ONEBIT_ACT_NONE>(k, d, c, s, v);
-        else if (act == ONEBIT_ACT_RELU) slopes<ONEBIT_ACT_RELU>(k, d, c, s, v);
-        else if (act == ONEBIT_ACT_GELU) slopes<ONEBIT_ACT_GELU>(k, d, c, s, v);
-        else slopes<ONEBIT_ACT_GELU_TANH>(k, d, c, s, v);
+        if (act == ONEBIT_ACT_NONE) slopes<ONEBIT_ACT_NONE>(consts, d, c, s, v);
+        else if (act == ONEBIT_ACT_RELU) slopes<ONEBIT_ACT_RELU>(consts, d, c, s, v);
+        else if (act == ONEBIT_ACT_GELU) slopes<ONEBIT_ACT_GELU>(consts, d, c, s, v);
+        else slopes<ONEBIT_ACT_GELU_TANH>(consts, d, c, s, v);
       } else if (act != ONEBIT_ACT_NONE) {
         load_rows(staging, v, x, ldx, row0, rows, c0, cols, vec_x);
-        if (act == ONEBIT_ACT_RELU) slopes<ONEBIT_ACT_RELU>(k, d, v);
-        else if (act == ONEBIT_ACT_GELU) slopes<ONEBIT_ACT_GELU>(k, d, v);
-        else slopes<ONEBIT_ACT_GELU_TANH>(k, d, v);
+        if (act == ONEBIT_ACT_RELU) slopes<ONEBIT_ACT_RELU>(consts, d, v);
+        else if (act == ONEBIT_ACT_GELU) slopes<ONEBIT_ACT_GELU>(consts, d, v);
+        else slopes<ONEBIT_ACT_GELU_TANH>(consts, d, v);
       }
       if (h.p) store_rows(staging, v, h, row0, rows, c0, cols);
       if (add) {
@@ -606,7 +622,8 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
   constexpr int kTileN = kRowsPerBlock * CTAS;
   constexpr uint32_t kTmemCols = 2 * kTileN;    // two accumulators
   extern __shared__ char smem_raw[];
-  char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  // (an offset, not a rounded pointer: the compiler has to see that this is shared memory)
+  char* smem = smem_raw + (-(int)smem_addr(smem_raw) & 1023);
   char* staging_base = smem + kStages * kStageBytes;
   char* bars = staging_base + kEpilogueWarps<CTAS> * kStagingBytes;
   f2* consts = reinterpret_cast<f2*>(bars + kBarrierBytes);
@@ -649,9 +666,6 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
     const int quad = warp & 3, group = (warp - 4) >> 2;
     char* staging = staging_base + (warp - 4) * kStagingBytes;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + group * 64;
-    ActConsts k;
-#pragma unroll
-    for (int i = 0; i < kActConsts; ++i) k.k[i] = *const_cast<volatile f2*>(consts + i);
     int acc = 0;
     uint32_t acc_phase = 0;
     // the accumulator has been read: the next product may write over it
@@ -696,6 +710,7 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
         for (int q = 0; q < 2; ++q)
           if (inside && col0 + 32 * q < P.n) E.run(c[q], row0, P.m, col0 + 32 * q, P.n, t.split, staging);
       } else {
+        if (inside) E.prepare(col0, P.n, staging);
         if (!(ok = ready())) break;
         const uint32_t at = lanes + acc * kTileN;
         auto load = [&](int half, f2(&z)[16]) {
@@ -706,7 +721,7 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
 #pragma unroll
           for (int i = 0; i < 16; ++i) z[i] = pair(v[2 * i], v[2 * i + 1]);
         };
-        if (inside) E.run(load, release, k, row0, P.m, col0, P.n, staging);
+        if (inside) E.run(load, release, consts, row0, P.m, col0, P.n, staging);
         else release();
       }
     }
