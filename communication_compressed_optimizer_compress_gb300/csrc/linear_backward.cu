@@ -112,21 +112,38 @@ cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, b
     const Partials part = take_partials(ws, plan, a.rows, a.in);
     const T* add = static_cast<const T*>(a.add);
     if (run && plan.splits == 1) {
-      InputGradEpilogue<T> e{};
-      e.x = v.x;
-      e.ldx = a.ldx;
-      e.codes = a.codes;
-      e.scales = a.scales;
-      e.blocks = v.blocks;
-      e.add = add;
-      e.ldadd = a.ldadd;
-      e.act = a.activation;
-      e.vec_x = vec16(v.x, a.ldx);
-      e.vec_codes = aligned(a.codes, 16) && a.in % 16 == 0;
-      e.vec_add = vec16(add, a.ldadd);
-      err = make_output(&e.dx, static_cast<T*>(a.dx), a.rows, a.in, a.lddx);
-      if (err == cudaSuccess) err = make_output(&e.h, h, a.rows, a.in, ldh);
-      if (err == cudaSuccess) err = run_product<false, true>(a.dtype, dy, w, sx, plan, e, s);
+      const int need = a.codes && (a.activation != ONEBIT_ACT_NONE || h) ? kKeptCodes : a.activation != ONEBIT_ACT_NONE ? kKeptValue : kKeptNone;
+      auto go = [&](auto ctas, auto act, auto kept) {
+        InputGradEpilogue<T, decltype(act)::value, decltype(kept)::value> e{};
+        e.x = make_input<T>(v.x, a.ldx);
+        e.codes = a.codes;
+        e.scales = a.scales;
+        e.blocks = v.blocks;
+        e.add = make_input<T>(add, a.ldadd);
+        e.act = a.activation;
+        e.kept = need;
+        e.wide_codes = aligned(a.codes, 32) && a.in % 32 == 0;
+        e.vec_codes = aligned(a.codes, 16) && a.in % 16 == 0;
+        cudaError_t r = make_output(&e.dx, static_cast<T*>(a.dx), a.rows, a.in, a.lddx);
+        if (r == cudaSuccess) r = make_output(&e.h, h, a.rows, a.in, ldh);
+        return r == cudaSuccess ? run_product_by<decltype(ctas)::value, false, true>(a.dtype, dy, w, sx, plan, e, s) : r;
+      };
+      using std::integral_constant;
+      using Two = integral_constant<int, 2>;
+      auto by_act = [&](auto kept) {
+        switch (a.activation) {
+          case ONEBIT_ACT_RELU: return go(Two{}, integral_constant<int, ONEBIT_ACT_RELU>{}, kept);
+          case ONEBIT_ACT_GELU: return go(Two{}, integral_constant<int, ONEBIT_ACT_GELU>{}, kept);
+          default: return go(Two{}, integral_constant<int, ONEBIT_ACT_GELU_TANH>{}, kept);
+        }
+      };
+      using None = integral_constant<int, ONEBIT_ACT_NONE>;
+      using Codes = integral_constant<int, kKeptCodes>;
+      if (plan.ctas == 1) err = go(integral_constant<int, 1>{}, integral_constant<int, kAny>{}, integral_constant<int, kAny>{});
+      else if (need == kKeptNone) err = go(Two{}, None{}, integral_constant<int, kKeptNone>{});
+      else if (need == kKeptValue) err = by_act(integral_constant<int, kKeptValue>{});
+      else if (a.activation == ONEBIT_ACT_NONE) err = go(Two{}, None{}, Codes{});
+      else err = by_act(Codes{});
     } else if (run) {
       PlainEpilogue<float> to{};
       err = to_partials(&to, part, a.in);

@@ -14,6 +14,11 @@ inline int64_t pad8(int64_t c) { return (c + 7) & ~(int64_t)7; }
 inline bool copyable(const void* p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
 inline bool vec16(const void* p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
 
+template <typename T>
+inline Input16<T> make_input(const void* p, int64_t ld) {
+  return {static_cast<const T*>(p), ld, aligned(p, 32) && ld % 16 == 0, vec16(p, ld)};
+}
+
 inline unsigned flat_grid(int64_t total, int threads) {
   const int64_t most = (int64_t)sm_count() * 8, want = ceil_div(total, threads);
   return (unsigned)(want < most ? want : most);

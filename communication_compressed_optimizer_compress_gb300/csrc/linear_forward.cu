@@ -8,7 +8,7 @@ namespace {
 
 // The epilogue over the partial sums of a cut contraction, one warp per 64 columns of a row.
 template <typename T>
-__global__ void __launch_bounds__(256) k_finish_forward(Partials c, int64_t rows, int cols, const __grid_constant__ ForwardEpilogue<T> e) {
+__global__ void __launch_bounds__(256) k_finish_forward(Partials c, int64_t rows, int cols, const __grid_constant__ ForwardEpilogue<T, kAny> e) {
   const int lane = threadIdx.x & 31;
   const int64_t units = rows * e.blocks, step = (int64_t)gridDim.x * 8;
   for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < units; u += step) {
@@ -22,7 +22,7 @@ __global__ void __launch_bounds__(256) k_finish_forward(Partials c, int64_t rows
       if (col < cols) {
         z[q] = c.at(r, col) + (e.bias ? e.bias[col] : 0.0f);
         float v = act_value(e.act, z[q]);
-        if (e.residual) v += to_f(e.residual[r * e.ldr + col]);
+        if (e.residual.p) v += to_f(e.residual.p[r * e.residual.ld + col]);
         e.y.p[r * e.y.ld + col] = from_f<T>(v);
       }
     }
@@ -44,18 +44,29 @@ cudaError_t forward(const onebit_linear_t& a, Space& ws, cudaStream_t s, bool ru
   const Operand x = readable(ws, a.x, a.ldx, a.rows, a.in, s, run), w = readable(ws, a.w, a.ldw, a.out, a.in, s, run);
   const Partials part = take_partials(ws, plan, a.rows, a.out);
   if (!run) return cudaSuccess;
-  ForwardEpilogue<T> e{};
+  ForwardEpilogue<T, kAny> e{};
   e.bias = a.bias;
-  e.residual = static_cast<const T*>(a.residual);
-  e.ldr = a.ldr;
+  e.residual = make_input<T>(a.residual, a.ldr);
   e.scales = a.scales;
   e.blocks = (int)ceil_div(a.out, kBlock);
   e.act = a.activation;
-  e.vec_res = vec16(a.residual, a.ldr);
   cudaError_t err = make_output(&e.y, static_cast<T*>(a.y), a.rows, a.out, a.ldy);
   if (err == cudaSuccess) err = make_output(&e.codes, a.codes, a.rows, a.out, a.out);
   if (err != cudaSuccess) return err;
-  if (plan.splits == 1) return run_product<false, false>(a.dtype, x, w, shape, plan, e, s);
+  if (plan.splits == 1 && plan.ctas == 1) return run_product_by<1, false, false>(a.dtype, x, w, shape, plan, e, s);
+  if (plan.splits == 1) {
+    auto go = [&](auto act) {
+      ForwardEpilogue<T, decltype(act)::value> f{};
+      f.bias = e.bias, f.residual = e.residual, f.y = e.y, f.codes = e.codes, f.scales = e.scales, f.blocks = e.blocks, f.act = e.act;
+      return run_product_by<2, false, false>(a.dtype, x, w, shape, plan, f, s);
+    };
+    switch (a.activation) {
+      case ONEBIT_ACT_RELU: return go(std::integral_constant<int, ONEBIT_ACT_RELU>{});
+      case ONEBIT_ACT_GELU: return go(std::integral_constant<int, ONEBIT_ACT_GELU>{});
+      case ONEBIT_ACT_GELU_TANH: return go(std::integral_constant<int, ONEBIT_ACT_GELU_TANH>{});
+      default: return go(std::integral_constant<int, ONEBIT_ACT_NONE>{});
+    }
+  }
   PlainEpilogue<float> to{};
   err = to_partials(&to, part, a.out);
   if (err == cudaSuccess) err = run_product<false, false>(a.dtype, x, w, shape, plan, to, s);

@@ -61,6 +61,7 @@ struct ProductArgs {
   int32_t tiles_m, tiles_n;
   int32_t splits, split_slabs;
   uint32_t units;            // tiles times splits
+  uint32_t group_mul, group_shift;  // reciprocal of the tiles in a group of kGroupTiles tile rows
   uint32_t idesc;
   uint32_t stall_tx;         // test hook: bytes that every stage waits for and no copy brings (normally 0)
   unsigned int* status;
@@ -293,6 +294,36 @@ __device__ __forceinline__ void store_rows(char* staging, const uint32_t (&v)[16
   __syncwarp();
 }
 
+// 32 bytes of the lane's own row
+__device__ __forceinline__ void load32(const void* p, uint32_t* v) {
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "l"(p));
+}
+
+// A matrix that an epilogue reads.  Where its rows start on 32 bytes a lane reads its own row, whole sectors at a
+// time, half of its 64 columns ahead: the first before the product is waited for, the second under the first
+// one's arithmetic (through the staging buffer and waited for at once: 2.6 us a tile).
+template <typename T>
+struct Input16 {
+  const T* p;
+  int64_t ld;
+  bool wide;   // rows on 32 bytes
+  bool vec;    // rows on 16 bytes
+
+  __device__ __forceinline__ bool ahead(int64_t row, int64_t rows, int col0, int cols, uint32_t (&v)[16]) const {
+    if (!wide || col0 + 32 > cols) return false;
+    if (row < rows) {
+      load32(p + row * ld + col0, v);
+      load32(p + row * ld + col0 + 16, v + 8);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = 0;
+    }
+    return true;
+  }
+};
+
 template <typename T>  // a 16-bit type: 32 columns
 __device__ __forceinline__ void load_rows(char* staging, uint32_t (&v)[16], const T* p, int64_t ld, int64_t row0, int64_t rows, int col0, int cols,
                                           bool vec) {
@@ -395,22 +426,33 @@ __device__ __forceinline__ ActConsts shared_consts(const f2* consts) {
   return k;
 }
 
-template <typename T>
+// The activation, and what the kept value is, are template parameters of the epilogues of pairs: with them
+// decided at run time inside the loop the register allocation of the alternatives met in copies, 100 to 300 of
+// a unit's 700 to 1700 instructions.  kAny decides at run time (the single blocks of small products).
+constexpr int kAny = -1;
+enum Kept16 { kKeptNone = 0, kKeptValue = 1, kKeptCodes = 2 };
+
+template <typename T, int ACT>
 struct ForwardEpilogue {
   // y = act(d + bias) + residual, and the 8-bit checkpoint of d + bias
   static constexpr bool kFold = false;
+  static constexpr bool kAhead = ACT == ONEBIT_ACT_NONE;  // a residual's first columns are fetched ahead
   const float* bias;
-  const T* residual;
-  int64_t ldr;
+  Input16<T> residual;
   Output<T> y;
   Output<int8_t> codes;
   float* scales;  // NULL: no checkpoint
   int blocks;
   int act;
-  bool vec_res;
 
-  // the warp's 64 columns of the bias, before the product is waited for: two a lane
-  __device__ __forceinline__ void prepare(int col0, int cols, char* staging) const {
+  struct Ahead {
+    uint32_t v[kAhead ? 16 : 1];
+  };
+  // before the product is waited for: the warp's 64 columns of the bias, two a lane, and the residual's first 32
+  __device__ __forceinline__ void prepare(Ahead& a, int64_t row0, int64_t rows, int col0, int cols, char* staging) const {
+    if constexpr (kAhead) {
+      if (residual.p) residual.ahead(row0 + (threadIdx.x & 31), rows, col0, cols, a.v);
+    }
     if (!bias) return;
     const int c = col0 + 2 * (threadIdx.x & 31);
     const f2 b = pair(c < cols ? __ldg(bias + c) : 0.0f, c + 1 < cols ? __ldg(bias + c + 1) : 0.0f);
@@ -426,18 +468,20 @@ struct ForwardEpilogue {
       z[2 * i] = add2(z[2 * i], v.x), z[2 * i + 1] = add2(z[2 * i + 1], v.y);
     }
   }
-  template <int ACT>
+  template <int A>
   __device__ __forceinline__ void finish(const f2* consts, f2 (&z)[16], uint32_t (&v)[16]) const {  // v: in the residual, out y
-    const ActConsts k = shared_consts<ACT>(consts);
+    const ActConsts k = shared_consts<A>(consts);
+    if (residual.p) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const f2 a = act2<ACT>(k, z[i]);
-      v[i] = narrow<T>(residual ? add2(a, widen<T>(v[i])) : a);
+      for (int i = 0; i < 16; ++i) v[i] = narrow<T>(add2(act2<A>(k, z[i]), widen<T>(v[i])));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = narrow<T>(act2<A>(k, z[i]));
     }
   }
   template <class Load, class Release>
-  __device__ __forceinline__ void run(Load&& load, Release&& release, const f2* consts, int64_t row0, int64_t rows, int col0, int cols,
-                                      char* staging) const {
+  __device__ __forceinline__ void run(Ahead& ahead, Load&& load, Release&& release, const f2* consts, int64_t row0, int64_t rows, int col0,
+                                      int cols, char* staging) const {
     float inv = 0.0f;
     if (scales) {  // columns past the end have z = 0: their operand rows were filled with zeros
       float most = 0.0f;
@@ -469,8 +513,19 @@ struct ForwardEpilogue {
         for (int i = 0; i < 8; ++i) c[i] = codes4(z[2 * i], z[2 * i + 1], inv);
         store_codes(staging, c, codes, row0, rows, c0, cols);
       }
-      if (residual) load_rows(staging, v, residual, ldr, row0, rows, c0, cols, vec_res);
-      if (act == ONEBIT_ACT_NONE) finish<ONEBIT_ACT_NONE>(consts, z, v);
+      if (residual.p) {
+        if (kAhead && residual.wide && c0 + 32 <= cols) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = ahead.v[kAhead ? i : 0];
+          if constexpr (kAhead) {
+            if (!half) residual.ahead(row0 + (threadIdx.x & 31), rows, c0 + 32, cols, ahead.v);
+          }
+        } else {
+          load_rows(staging, v, residual.p, residual.ld, row0, rows, c0, cols, residual.vec);
+        }
+      }
+      if constexpr (ACT != kAny) finish<ACT>(consts, z, v);
+      else if (act == ONEBIT_ACT_NONE) finish<ONEBIT_ACT_NONE>(consts, z, v);
       else if (act == ONEBIT_ACT_RELU) finish<ONEBIT_ACT_RELU>(consts, z, v);
       else if (act == ONEBIT_ACT_GELU) finish<ONEBIT_ACT_GELU>(consts, z, v);
       else finish<ONEBIT_ACT_GELU_TANH>(consts, z, v);
@@ -480,80 +535,122 @@ struct ForwardEpilogue {
   }
 };
 
-template <typename T>
+template <typename T, int ACT, int KEPT>
 struct InputGradEpilogue {
   // dx = d * act'(v) [+ add], and h = act(v) for the product of dw
   static constexpr bool kFold = false;
-  const T* x;
-  int64_t ldx;
-  const int8_t* codes;
+  Input16<T> x;          // the value before the activation,
+  const int8_t* codes;   // or its checkpoint
   const float* scales;
   int blocks;
-  const T* add;
-  int64_t ldadd;
+  Input16<T> add;
   Output<T> dx, h;  // h.p NULL: not wanted
   int act;
-  bool vec_x, vec_codes, vec_add;
+  int kept;         // Kept16: what is needed
+  bool wide_codes, vec_codes;
 
-  __device__ __forceinline__ void prepare(int, int, char*) const {}
-  template <int ACT>
-  __device__ __forceinline__ void slopes(const f2* consts, f2 (&d)[16], uint32_t (&v)[16]) const {
-    const ActConsts k = shared_consts<ACT>(consts);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      f2 a, s;
-      activate<ACT, true, true>(k, widen<T>(v[i]), a, s);
-      d[i] = mul2(d[i], s);
-      v[i] = narrow<T>(a);
+  static constexpr bool kAheadCodes = KEPT == kKeptCodes, kAheadRow = KEPT == kKeptValue || KEPT == kKeptNone;
+  struct Ahead {
+    uint32_t c[kAheadCodes ? 8 : 1];
+    uint32_t v[kAheadRow ? 16 : 1];  // x, or add where x is not needed
+  };
+  __device__ __forceinline__ void fetch(Ahead& a, int64_t row, int64_t rows, int c0, int cols) const {
+    if constexpr (kAheadCodes) {
+      if (wide_codes && c0 + 32 <= cols && row < rows) load32(codes + row * cols + c0, a.c);
+    }
+    if constexpr (KEPT == kKeptValue) x.ahead(row, rows, c0, cols, a.v);
+    if constexpr (KEPT == kKeptNone) {
+      if (add.p) add.ahead(row, rows, c0, cols, a.v);
     }
   }
-  template <int ACT>
-  __device__ __forceinline__ void slopes(const f2* consts, f2 (&d)[16], const uint32_t (&c)[8], float scale, uint32_t (&v)[16]) const {
-    const ActConsts k = shared_consts<ACT>(consts);
+  __device__ __forceinline__ void prepare(Ahead& a, int64_t row0, int64_t rows, int col0, int cols, char*) const {
+    fetch(a, row0 + (threadIdx.x & 31), rows, col0, cols);
+  }
+  // z: the kept values; d: times the slope; v: out h
+  template <int A>
+  __device__ __forceinline__ void slopes(const ActConsts& k, f2 z, f2& d, uint32_t& v) const {
+    f2 a, s;
+    activate<A, true, A != ONEBIT_ACT_NONE>(k, z, a, s);
+    if (A != ONEBIT_ACT_NONE) d = mul2(d, s);
+    v = narrow<T>(a);
+  }
+  template <int A>
+  __device__ __forceinline__ void by_value(const f2* consts, f2 (&d)[16], uint32_t (&v)[16]) const {
+    const ActConsts k = shared_consts<A>(consts);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) slopes<A>(k, widen<T>(v[i]), d[i], v[i]);
+  }
+  template <int A>
+  __device__ __forceinline__ void by_codes(const f2* consts, f2 (&d)[16], const uint32_t (&c)[8], float scale, uint32_t (&v)[16]) const {
+    const ActConsts k = shared_consts<A>(consts);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       f2 z[2];
       values4<T>(c[i], scale, z);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        f2 a, s;
-        activate<ACT, true, true>(k, z[j], a, s);
-        if (ACT != ONEBIT_ACT_NONE) d[2 * i + j] = mul2(d[2 * i + j], s);
-        v[2 * i + j] = narrow<T>(a);
-      }
+      slopes<A>(k, z[0], d[2 * i], v[2 * i]);
+      slopes<A>(k, z[1], d[2 * i + 1], v[2 * i + 1]);
     }
   }
   template <class Load, class Release>
-  __device__ __forceinline__ void run(Load&& load, Release&& release, const f2* consts, int64_t row0, int64_t rows, int col0, int cols,
-                                      char* staging) const {
+  __device__ __forceinline__ void run(Ahead& ahead, Load&& load, Release&& release, const f2* consts, int64_t row0, int64_t rows, int col0,
+                                      int cols, char* staging) const {
+    const int64_t row = row0 + (threadIdx.x & 31);
+    const int need = KEPT == kAny ? kept : KEPT;
+    float scale = 0.0f;
+    if (need == kKeptCodes && row < rows) scale = __ldg(scales + row * blocks + col0 / kBlock);
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
+      const int c0 = col0 + 32 * half;
       f2 d[16];
       uint32_t v[16];
       load(half, d);
       if (half) release();
-      const int c0 = col0 + 32 * half;
       if (c0 >= cols) continue;
-      if (codes && (act != ONEBIT_ACT_NONE || h.p)) {
+      const bool whole = c0 + 32 <= cols;
+      if (need == kKeptCodes) {
         uint32_t c[8];
-        load_codes(staging, c, codes, row0, rows, c0, cols, vec_codes);
-        const int64_t row = row0 + (threadIdx.x & 31);
-        const float s = row < rows ? __ldg(scales + row * blocks + col0 / kBlock) : 0.0f;
-        if (act == ONEBIT_ACT_NONE) slopes<ONEBIT_ACT_NONE>(consts, d, c, s, v);
-        else if (act == ONEBIT_ACT_RELU) slopes<ONEBIT_ACT_RELU>(consts, d, c, s, v);
-        else if (act == ONEBIT_ACT_GELU) slopes<ONEBIT_ACT_GELU>(consts, d, c, s, v);
-        else slopes<ONEBIT_ACT_GELU_TANH>(consts, d, c, s, v);
-      } else if (act != ONEBIT_ACT_NONE) {
-        load_rows(staging, v, x, ldx, row0, rows, c0, cols, vec_x);
-        if (act == ONEBIT_ACT_RELU) slopes<ONEBIT_ACT_RELU>(consts, d, v);
-        else if (act == ONEBIT_ACT_GELU) slopes<ONEBIT_ACT_GELU>(consts, d, v);
-        else slopes<ONEBIT_ACT_GELU_TANH>(consts, d, v);
-      }
-      if (h.p) store_rows(staging, v, h, row0, rows, c0, cols);
-      if (add) {
-        load_rows(staging, v, add, ldadd, row0, rows, c0, cols, vec_add);
+        if (kAheadCodes && wide_codes && whole) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) d[i] = add2(d[i], widen<T>(v[i]));
+          for (int i = 0; i < 8; ++i) c[i] = ahead.c[kAheadCodes ? i : 0];
+        } else {
+          load_codes(staging, c, codes, row0, rows, c0, cols, vec_codes);
+        }
+        if constexpr (kAheadCodes) {
+          if (!half) fetch(ahead, row, rows, c0 + 32, cols);
+        }
+        if constexpr (ACT != kAny) by_codes<ACT>(consts, d, c, scale, v);
+        else if (act == ONEBIT_ACT_NONE) by_codes<ONEBIT_ACT_NONE>(consts, d, c, scale, v);
+        else if (act == ONEBIT_ACT_RELU) by_codes<ONEBIT_ACT_RELU>(consts, d, c, scale, v);
+        else if (act == ONEBIT_ACT_GELU) by_codes<ONEBIT_ACT_GELU>(consts, d, c, scale, v);
+        else by_codes<ONEBIT_ACT_GELU_TANH>(consts, d, c, scale, v);
+      } else if (need == kKeptValue) {
+        if (KEPT == kKeptValue && x.wide && whole) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = ahead.v[kAheadRow ? i : 0];
+        } else {
+          load_rows(staging, v, x.p, x.ld, row0, rows, c0, cols, x.vec);
+        }
+        if constexpr (KEPT == kKeptValue) {
+          if (!half) fetch(ahead, row, rows, c0 + 32, cols);
+        }
+        if constexpr (ACT != kAny) by_value<ACT>(consts, d, v);
+        else if (act == ONEBIT_ACT_RELU) by_value<ONEBIT_ACT_RELU>(consts, d, v);
+        else if (act == ONEBIT_ACT_GELU) by_value<ONEBIT_ACT_GELU>(consts, d, v);
+        else by_value<ONEBIT_ACT_GELU_TANH>(consts, d, v);
+      }
+      if (need != kKeptNone && h.p) store_rows(staging, v, h, row0, rows, c0, cols);
+      if (add.p) {
+        if (KEPT == kKeptNone && add.wide && whole) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) d[i] = add2(d[i], widen<T>(ahead.v[kAheadRow ? i : 0]));
+          if constexpr (KEPT == kKeptNone) {
+            if (!half) fetch(ahead, row, rows, c0 + 32, cols);
+          }
+        } else {
+          load_rows(staging, v, add.p, add.ld, row0, rows, c0, cols, add.vec);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) d[i] = add2(d[i], widen<T>(v[i]));
+        }
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = narrow<T>(d[i]);
@@ -607,9 +704,11 @@ __device__ __forceinline__ Tile tile_of(const ProductArgs& P, uint32_t unit) {
   Tile t;
   const uint32_t tile = P.splits == 1 ? unit : unit / P.splits;
   t.split = (int)(unit - tile * P.splits);
-  // kGroupTiles tile rows side by side, column after column: the tiles in flight share operand slabs in L2
-  const uint32_t per = (uint32_t)kGroupTiles * P.tiles_n, g = tile / per, m = g * kGroupTiles;
-  const uint32_t rows = P.tiles_m - m < kGroupTiles ? P.tiles_m - m : kGroupTiles, in = tile - g * per, col = in / rows;
+  // kGroupTiles tile rows side by side, column after column: the tiles in flight share operand slabs in L2.
+  // The division by a group's tiles is a multiplication by its rounded-up reciprocal (exact below 2^31).
+  const uint32_t g = (__umulhi(tile, P.group_mul) + tile) >> P.group_shift, m = g * kGroupTiles;
+  const uint32_t in = tile - m * P.tiles_n, left = P.tiles_m - m;
+  const uint32_t col = left >= kGroupTiles ? in / kGroupTiles : in / left, rows = left >= kGroupTiles ? kGroupTiles : left;
   t.m0 = (int64_t)(m + in - col * rows) * kM;
   t.n0 = (int)col * kN;
   t.first = t.split * P.split_slabs;
@@ -710,7 +809,8 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
         for (int q = 0; q < 2; ++q)
           if (inside && col0 + 32 * q < P.n) E.run(c[q], row0, P.m, col0 + 32 * q, P.n, t.split, staging);
       } else {
-        if (inside) E.prepare(col0, P.n, staging);
+        typename Epilogue::Ahead ahead;
+        if (inside) E.prepare(ahead, row0, P.m, col0, P.n, staging);
         if (!(ok = ready())) break;
         const uint32_t at = lanes + acc * kTileN;
         auto load = [&](int half, f2(&z)[16]) {
@@ -721,7 +821,7 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
 #pragma unroll
           for (int i = 0; i < 16; ++i) z[i] = pair(v[2 * i], v[2 * i + 1]);
         };
-        if (inside) E.run(load, release, consts, row0, P.m, col0, P.n, staging);
+        if (inside) E.run(ahead, load, release, consts, row0, P.m, col0, P.n, staging);
         else release();
       }
     }
@@ -877,9 +977,9 @@ cudaError_t launch_product(const ProductArgs& P, const Epilogue& E, int sms, cud
 }
 
 // C = A B^T by `plan`, through epilogue E.  A: m x k (or k x m with A_MN), B: n x k (or k x n with B_MN).
-template <bool A_MN, bool B_MN, class Epilogue>
-cudaError_t run_product(int32_t dtype, const Operand& a, const Operand& b, const ProductShape& s, const ProductPlan& plan, const Epilogue& E,
-                        cudaStream_t stream) {
+template <int CTAS, bool A_MN, bool B_MN, class Epilogue>
+cudaError_t run_product_by(int32_t dtype, const Operand& a, const Operand& b, const ProductShape& s, const ProductPlan& plan, const Epilogue& E,
+                           cudaStream_t stream) {
   ProductArgs P{};
   cudaError_t e = make_map(&P.a, dtype, a.p, A_MN ? s.k : s.m, A_MN ? s.m : s.k, a.ld, A_MN ? 64 : 128);
   if (e == cudaSuccess) e = make_map(&P.b, dtype, b.p, B_MN ? s.k : s.n, B_MN ? s.n : s.k, b.ld, B_MN ? 64 : 128);
@@ -894,14 +994,21 @@ cudaError_t run_product(int32_t dtype, const Operand& a, const Operand& b, const
   const int64_t units = (int64_t)P.tiles_m * P.tiles_n * P.splits;
   if (units >= (int64_t)1 << 31) return cudaErrorNotSupported;
   P.units = (uint32_t)units;
+  const uint32_t per = (uint32_t)kGroupTiles * (uint32_t)P.tiles_n;  // at least 8
+  P.group_shift = 32 - (uint32_t)__builtin_clz(per - 1);
+  P.group_mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << P.group_shift) - per)) / per + 1);
   const uint32_t type = dtype == ONEBIT_F16 ? 0u : 1u;  // both operands have the same
   P.idesc = 1u << 4 | type << 7 | type << 10 | (uint32_t)A_MN << 15 | (uint32_t)B_MN << 16 |
             (uint32_t)(kRowsPerBlock * plan.ctas / 8) << 17 | (uint32_t)(kRowsPerBlock * plan.ctas / 16) << 24;
   P.stall_tx = stall_bytes();
   P.status = status_word();
   if (!P.status) return cudaErrorUnknown;
-  const int sms = sm_count();
-  return plan.ctas == 2 ? launch_product<2, A_MN, B_MN>(P, E, sms, stream) : launch_product<1, A_MN, B_MN>(P, E, sms, stream);
+  return launch_product<CTAS, A_MN, B_MN>(P, E, sm_count(), stream);
+}
+template <bool A_MN, bool B_MN, class Epilogue>
+cudaError_t run_product(int32_t dtype, const Operand& a, const Operand& b, const ProductShape& s, const ProductPlan& plan, const Epilogue& E,
+                        cudaStream_t stream) {
+  return plan.ctas == 2 ? run_product_by<2, A_MN, B_MN>(dtype, a, b, s, plan, E, stream) : run_product_by<1, A_MN, B_MN>(dtype, a, b, s, plan, E, stream);
 }
 
 }  // namespace layers
