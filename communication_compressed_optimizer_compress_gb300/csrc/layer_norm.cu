@@ -561,7 +561,7 @@ void launch_forward(const ForwardArgs& a, cudaStream_t s) {
   using One = integral_constant<int, 1>;
   using Two = integral_constant<int, 2>;
   if (a.cols <= 256) go(integral_constant<int, 32>{}, One{}, Two{}, 5);
-  else if (a.cols <= 1024) go(integral_constant<int, 64>{}, Two{}, Two{}, 5);
+  else if (a.cols <= 1024) go(integral_constant<int, 32>{}, integral_constant<int, 4>{}, One{}, 5);
   else if (a.cols <= 2048) go(integral_constant<int, 128>{}, Two{}, Two{}, 5);
   else if (a.cols <= 4096) go(integral_constant<int, 256>{}, Two{}, Two{}, 2);
   else if (a.cols <= kForwardCols) go(integral_constant<int, 512>{}, integral_constant<int, 4>{}, One{}, 1);
@@ -572,8 +572,9 @@ void launch_forward(const ForwardArgs& a, cudaStream_t s) {
 int backward_parts(int64_t rows, int64_t cols) {
   if (rows == 0) return 0;
   if (cols > kBackwardCols) return (int)ceil_div(rows, ceil_div(rows, 64));
+  // the wide form's groups and blocks an SM; the narrow form starts at most as many blocks
   const int groups = cols <= 256 ? 8 : cols <= 1024 ? 4 : cols <= 2048 ? 2 : 1;
-  return (int)at_most(ceil_div(rows, groups), cols <= 4096 ? 2 : 1);
+  return (int)at_most(ceil_div(rows, groups), cols <= 256 ? 2 : cols <= 4096 ? 2 : 1);
 }
 
 template <typename T, bool VEC, bool CODES>

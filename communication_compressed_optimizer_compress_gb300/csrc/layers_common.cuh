@@ -209,11 +209,9 @@ __device__ __forceinline__ BlockScale block_scale(float most) {
   if (most < 7.52316384526264e-37f) return {0.0f, 0.0f};  // 2^-120
   const float q = most * 0.0078740157f;
   const float scale = fmaf(fmaf(q, -127.0f, most), 0.0078740157f, q);
-  // far from where the reciprocal or the quotient would leave the normal range
-  const bool big = most > 1.8446744e19f;
-  const float d = big ? most * 5.4210109e-20f : most, r = rcp_fast(d), p = r * 127.0f;
-  const float inv = fmaf(fmaf(p, -d, 127.0f), r, p);
-  return {scale, big ? inv * 5.4210109e-20f : inv};
+  // the reciprocal of most/4: neither it nor a factor below leaves the normal range
+  const float r = rcp_fast(most * 0.25f), p = r * 31.75f;
+  return {scale, fmaf(fmaf(p, -most, 127.0f) * 0.25f, r, p)};
 }
 // code of one value, in the low byte: adding 1.5*2^23 leaves the nearest integer (ties to even) in
 // the low bits of the sum.  A block with inv = 0 that holds inf or NaN (inf*0) gets code 0.
