@@ -70,9 +70,7 @@ __global__ void __launch_bounds__(kCkThreads) k_compress_wide(const T* __restric
       float most = 0.0f;
       if (on) {
         const T* p = x + (r0 + r) * ldx + g * 16;
-        const Raw8<T> a = load8(p), b = load8(p + 8);
-        expand8(a, v);
-        expand8(b, v + 4);
+        load16(p, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) most = max_abs(most, v[i]);
       }
@@ -109,8 +107,7 @@ __global__ void __launch_bounds__(kCkThreads) k_restore_wide(const int8_t* __res
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = act2<ACT>(k, v[i]);
       T* p = x + (r0 + r) * ldx + g * 16;
-      store8(p, v);
-      store8(p + 8, v + 4);
+      store16(p, v);
     }
   }
 }
@@ -148,7 +145,7 @@ __global__ void __launch_bounds__(kCkThreads) k_restore(const int8_t* __restrict
 }
 
 bool wide_ok(const void* x, int64_t ldx, int32_t dtype, int64_t cols, const int8_t* codes) {
-  return aligned(x, 16) && (ldx * dtype_size(dtype)) % 16 == 0 && cols % 16 == 0 && aligned(codes, 16);
+  return aligned(x, 32) && (ldx * dtype_size(dtype)) % 32 == 0 && cols % 16 == 0 && aligned(codes, 16);
 }
 unsigned ck_grid(int64_t units) {
   const int64_t most = (int64_t)sm_count() * 8;

@@ -131,9 +131,10 @@ constexpr int kForwardThreads = TPR < 128 ? 128 : TPR;
 // read (from L1) once for them.  Bound by instruction issue first and by DRAM next: fewer threads with more
 // columns each pay the fixed cost of a row less often.  16384 x 1024 bf16 with the checkpoint: one block of
 // 128 threads a row 28 us, a warp a row 26 us (gamma and beta took 62% of the L1's cycles).
-template <typename T, int TPR, int CH, int NR, bool VEC>
+template <typename T, int TPR, int CH, int NR, bool VEC, bool FULL>
 __global__ void __launch_bounds__(kForwardThreads<TPR>, (TPR < 256 ? 640 : 512) / kForwardThreads<TPR>) k_ln_forward(const ForwardArgs A) {
   constexpr int kGroups = kForwardThreads<TPR> / TPR;
+  const int cols = FULL ? TPR * CH * 8 : A.cols;
   using Col = Columns<TPR, VEC>;
   __shared__ float red[kGroups][2][NR * 32];
   const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(kForwardThreads<TPR>, (TPR < 256 ? 640 : 512) 
   auto load = [&](int64_t r) {
 #pragma unroll
     for (int n = 0; n < NR; ++n)
-      if (r + n < A.rows) in[n].load(px + n * A.ldx, t, A.cols);
+      if (r + n < A.rows) in[n].load(px + n * A.ldx, t, cols);
   };
   load(first);
   for (int64_t r = first; r < A.rows; r += step) {
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(kForwardThreads<TPR>, (TPR < 256 ? 640 : 512) 
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
         if (r + n >= A.rows) continue;
-        int8_t* codes = A.codes + (r + n) * A.cols;
+        int8_t* codes = A.codes + (r + n) * cols;
         float* scales = A.scales + (r + n) * A.blocks;
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(kForwardThreads<TPR>, (TPR < 256 ? 640 : 512) 
 #pragma unroll
             for (int o = 1; o < 8; o *= 2) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
             const BlockScale q = block_scale(most);
-            if (c < A.cols) {
+            if (c < cols) {
               *reinterpret_cast<uint2*>(codes + c) = make_uint2(codes4(v[0], v[1], q.inv), codes4(v[2], v[3], q.inv));
               if ((t & 7) == 0) scales[c / kBlock] = q.scale;
             }
@@ -192,11 +193,11 @@ __global__ void __launch_bounds__(kForwardThreads<TPR>, (TPR < 256 ? 640 : 512) 
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int c = Col::at(t, j, 2 * e), c0 = c - (t & 31);
-              if (c0 >= A.cols) continue;
+              if (c0 >= cols) continue;
               const BlockScale q = block_scale(warp_max_nan(max_abs(0.0f, v[e])));
               const float2 h = halves(v[e]);
-              if (c < A.cols) codes[c] = (int8_t)code_of(h.x, q.inv);
-              if (c + 32 < A.cols) codes[c + 32] = (int8_t)code_of(h.y, q.inv);
+              if (c < cols) codes[c] = (int8_t)code_of(h.x, q.inv);
+              if (c + 32 < cols) codes[c + 32] = (int8_t)code_of(h.y, q.inv);
               if ((t & 31) == 0) scales[c0 / kBlock] = q.scale;
             }
           }
@@ -210,11 +211,11 @@ __global__ void __launch_bounds__(kForwardThreads<TPR>, (TPR < 256 ? 640 : 512) 
       f2 s = 0;
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
-        const f2 shift = VEC && Col::at(t, j, 0) >= A.cols ? 0 : splat(-mean[n]);
+        const f2 shift = VEC && Col::at(t, j, 0) >= cols ? 0 : splat(-mean[n]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int c = Col::at(t, j, 2 * e);
-          x[n][j][e] = add2(x[n][j][e], VEC ? shift : pair(c < A.cols ? -mean[n] : 0.0f, c + 32 < A.cols ? -mean[n] : 0.0f));
+          x[n][j][e] = add2(x[n][j][e], VEC ? shift : pair(c < cols ? -mean[n] : 0.0f, c + 32 < cols ? -mean[n] : 0.0f));
           s = fma2(x[n][j][e], x[n][j][e], s);
         }
       }
@@ -232,14 +233,14 @@ __global__ void __launch_bounds__(kForwardThreads<TPR>, (TPR < 256 ? 640 : 512) 
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
       f2 g[4], b[4];
-      param_group<TPR, VEC>(A.gamma, t, j, A.cols, g);
-      param_group<TPR, VEC>(A.beta, t, j, A.cols, b);
+      param_group<TPR, VEC>(A.gamma, t, j, cols, g);
+      param_group<TPR, VEC>(A.beta, t, j, cols, b);
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
         f2 y[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] = fma2(mul2(x[n][j][e], splat(rstd[n])), g[e], b[e]);
-        if (r + n < A.rows) store_group<T, TPR, VEC>(py + n * A.ldy, t, j, A.cols, y);
+        if (r + n < A.rows) store_group<T, TPR, VEC>(py + n * A.ldy, t, j, cols, y);
       }
     }
     py += step * A.ldy;
@@ -348,8 +349,9 @@ struct KeptRow<T, TPR, CH, false, true> {
 // instruction issue with four warps to a row of 1024 columns (62% of the slots, 1370 instructions a row,
 // 29.6 us at 16384 rows from the checkpoint with `add`), so two warps have it, sixteen columns a thread.
 template <typename T, int TPR, int CH, bool VEC, bool CODES>
-__global__ void __launch_bounds__(kBackThreads<TPR>, 512 / kBackThreads<TPR>) k_ln_backward(const BackwardArgs A) {
+__global__ void __launch_bounds__(kBackThreads<TPR>, (CH == 1 ? 768 : 512) / kBackThreads<TPR>) k_ln_backward(const BackwardArgs A) {
   constexpr int kGroups = kBackThreads<TPR> / TPR;
+  const int cols = A.cols;
   using Col = Columns<TPR, VEC>;
   __shared__ float red[kGroups][2][2 * 32];
   __shared__ f2 join[kGroups == 1 ? 1 : 2 * TPR * CH * 4];
@@ -363,34 +365,36 @@ __global__ void __launch_bounds__(kBackThreads<TPR>, 512 / kBackThreads<TPR>) k_
 #pragma unroll
     for (int e = 0; e < 4; ++e) dg[j][e] = db[j][e] = 0;
   KeptRow<T, TPR, CH, VEC, CODES> kept(A, first, step);
-  RowInput<T, TPR, CH, VEC> dyin, addin;
+  RowInput<T, TPR, CH, VEC> dyin, addin, addnow;
   const T *pdy = static_cast<const T*>(A.dy) + first * A.lddy, *padd = static_cast<const T*>(A.add) + (A.add ? first * A.ldadd : 0);
   T* pdx = static_cast<T*>(A.dx) + first * A.lddx;
   float mu = 0.0f, rs = 0.0f;
   auto load = [&](int64_t r) {
-    kept.load(t, A.cols);
-    dyin.load(pdy, t, A.cols);
+    kept.load(t, cols);
+    dyin.load(pdy, t, cols);
     pdy += step * A.lddy;
+    if (A.add) {
+      addin.load(padd, t, cols);
+      padd += step * A.ldadd;
+    }
     mu = __ldg(A.mean + r);
     rs = __ldg(A.rstd + r);
   };
-  auto load_add = [&] {
-    addin.load(padd, t, A.cols);
-    padd += step * A.ldadd;
-  };
-  if (first < A.rows) {
-    load(first);
-    if (A.add) load_add();
-  }
+  if (first < A.rows) load(first);
   for (int64_t r = first; r < A.rows; r += step) {
     f2 xh[CH][4], d[CH][4], s0 = 0, s1 = 0;
     const float rstd = rs, shift = -mu * rs;
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      f2 gamma[4];
-      param_group<TPR, VEC>(A.gamma, t, j, A.cols, gamma);
       kept.normal(j, rstd, shift, xh[j]);
       dyin.expand(j, d[j]);
+    }
+    addnow = addin;
+    if (r + step < A.rows) load(r + step);  // under this row's work
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      f2 gamma[4];
+      param_group<TPR, VEC>(A.gamma, t, j, cols, gamma);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         // columns past the end have dy = gamma = 0 and add nothing
@@ -402,7 +406,6 @@ __global__ void __launch_bounds__(kBackThreads<TPR>, 512 / kBackThreads<TPR>) k_
       }
     }
     float s[2] = {sum_of(s0), sum_of(s1)};
-    if (r + step < A.rows) load(r + step);  // under this row's sums
     row_sums<TPR>(s, red[group], turn, 1 + group);
     const f2 c0 = splat(-s[0] * A.inv_cols * rstd), c1 = splat(-s[1] * A.inv_cols * rstd);
 #pragma unroll
@@ -412,14 +415,13 @@ __global__ void __launch_bounds__(kBackThreads<TPR>, 512 / kBackThreads<TPR>) k_
       for (int e = 0; e < 4; ++e) o[e] = fma2(xh[j][e], c1, fma2(d[j][e], splat(rstd), c0));
       if (A.add) {
         f2 a[4];
-        addin.expand(j, a);
+        addnow.expand(j, a);
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] = add2(o[e], a[e]);
       }
-      store_group<T, TPR, VEC>(pdx, t, j, A.cols, o);
+      store_group<T, TPR, VEC>(pdx, t, j, cols, o);
     }
     pdx += step * A.lddx;
-    if (A.add && r + step < A.rows) load_add();
   }
   if (kGroups > 1) {
     for (int q = 0; q < kGroups; ++q) {
@@ -438,15 +440,15 @@ __global__ void __launch_bounds__(kBackThreads<TPR>, 512 / kBackThreads<TPR>) k_
     __syncthreads();
   }
   if (group == 0) {
-    float* p = A.part + (int64_t)blockIdx.x * 2 * A.cols;
+    float* p = A.part + (int64_t)blockIdx.x * 2 * cols;
 #pragma unroll
     for (int j = 0; j < CH; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int i = (j * 4 + e) * TPR + t, c = Col::at(t, j, 2 * e), c1 = Col::at(t, j, 2 * e + 1);
         const float2 g = halves(kGroups > 1 ? join[i] : dg[j][e]), b = halves(kGroups > 1 ? join[TPR * CH * 4 + i] : db[j][e]);
-        if (c < A.cols) p[c] = g.x, p[A.cols + c] = b.x;
-        if (c1 < A.cols) p[c1] = g.y, p[A.cols + c1] = b.y;
+        if (c < cols) p[c] = g.x, p[cols + c] = b.x;
+        if (c1 < cols) p[c1] = g.y, p[cols + c1] = b.y;
       }
   }
 }
@@ -555,7 +557,9 @@ template <typename T, bool VEC>
 void launch_forward(const ForwardArgs& a, cudaStream_t s) {
   auto go = [&](auto tpr, auto ch, auto nr, int per_sm) {
     constexpr int kTpr = decltype(tpr)::value, kCh = decltype(ch)::value, kNr = decltype(nr)::value, kThreads = kForwardThreads<kTpr>;
-    k_ln_forward<T, kTpr, kCh, kNr, VEC><<<at_most(ceil_div(a.rows, kThreads / kTpr * kNr), per_sm), kThreads, 0, s>>>(a);
+    const unsigned grid = at_most(ceil_div(a.rows, kThreads / kTpr * kNr), per_sm);
+    if (VEC && a.cols == kTpr * kCh * 8) k_ln_forward<T, kTpr, kCh, kNr, VEC, VEC><<<grid, kThreads, 0, s>>>(a);  // no bounds to test
+    else k_ln_forward<T, kTpr, kCh, kNr, VEC, false><<<grid, kThreads, 0, s>>>(a);
   };
   using std::integral_constant;
   using One = integral_constant<int, 1>;
@@ -568,29 +572,50 @@ void launch_forward(const ForwardArgs& a, cudaStream_t s) {
   else k_ln_forward_wide<T><<<at_most(a.rows, 8), kLnThreads, 0, s>>>(a);
 }
 
+// The backward form for a width: threads a row, groups of eight columns a thread.  Single elements need more
+// registers a column, so the narrow form has one group a thread and twice the threads.
+struct BackwardForm {
+  int tpr, ch;
+};
+BackwardForm backward_form(int64_t cols, bool vec) {
+  if (cols <= 256) return {32, 1};
+  if (cols <= 1024) return vec ? BackwardForm{64, 2} : BackwardForm{128, 1};
+  if (cols <= 2048) return vec ? BackwardForm{128, 2} : BackwardForm{256, 1};
+  if (cols <= 4096) return vec ? BackwardForm{256, 2} : BackwardForm{512, 1};
+  return {512, 2};
+}
 // Blocks of the backward kernel, which are the parts that the parameters' gradients are summed from.
-int backward_parts(int64_t rows, int64_t cols) {
+int backward_parts(int64_t rows, int64_t cols, bool vec) {
   if (rows == 0) return 0;
   if (cols > kBackwardCols) return (int)ceil_div(rows, ceil_div(rows, 64));
-  // the wide form's groups and blocks an SM; the narrow form starts at most as many blocks
-  const int groups = cols <= 256 ? 8 : cols <= 1024 ? 4 : cols <= 2048 ? 2 : 1;
-  return (int)at_most(ceil_div(rows, groups), cols <= 256 ? 2 : cols <= 4096 ? 2 : 1);
+  const BackwardForm f = backward_form(cols, vec);
+  const int threads = f.tpr < 256 ? 256 : f.tpr;
+  const int per_sm = (f.ch == 1 ? 768 : 512) / threads;
+  return (int)at_most(ceil_div(rows, threads / f.tpr), per_sm);
 }
 
 template <typename T, bool VEC, bool CODES>
 void launch_backward(const BackwardArgs& a, int parts, cudaStream_t s) {
-  if (a.cols <= 256) k_ln_backward<T, 32, 1, VEC, CODES><<<parts, kBackThreads<32>, 0, s>>>(a);
-  else if (a.cols <= 1024) k_ln_backward<T, 64, 2, VEC, CODES><<<parts, kBackThreads<64>, 0, s>>>(a);
-  else if (a.cols <= 2048) k_ln_backward<T, 128, 2, VEC, CODES><<<parts, kBackThreads<128>, 0, s>>>(a);
-  else if (a.cols <= 4096) k_ln_backward<T, 256, 2, VEC, CODES><<<parts, kBackThreads<256>, 0, s>>>(a);
-  else k_ln_backward<T, 512, 2, VEC, CODES><<<parts, kBackThreads<512>, 0, s>>>(a);
+  const BackwardForm f = backward_form(a.cols, VEC);
+  auto go = [&](auto tpr, auto ch) {
+    constexpr int kTpr = decltype(tpr)::value, kCh = decltype(ch)::value;
+    k_ln_backward<T, kTpr, kCh, VEC, CODES><<<parts, kBackThreads<kTpr>, 0, s>>>(a);
+  };
+  using std::integral_constant;
+  constexpr int kCh = VEC ? 2 : 1, kWide = VEC ? 1 : 2;
+  using Ch = integral_constant<int, kCh>;
+  if (f.tpr == 32) go(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+  else if (a.cols <= 1024) go(integral_constant<int, 64 * kWide>{}, Ch{});
+  else if (a.cols <= 2048) go(integral_constant<int, 128 * kWide>{}, Ch{});
+  else if (a.cols <= 4096) go(integral_constant<int, 256 * kWide>{}, Ch{});
+  else go(integral_constant<int, 512>{}, integral_constant<int, 2>{});
 }
 
 template <typename T>
 cudaError_t launch_backward(const BackwardArgs& a, cudaStream_t s) {
-  const int parts = backward_parts(a.rows, a.cols);
   auto on16 = [](const void* p, int64_t ld) { return aligned(p, 16) && (ld * (int64_t)sizeof(T)) % 16 == 0; };
   const bool vec = a.cols % 8 == 0 && on16(a.dy, a.lddy) && on16(a.x, a.ldx) && on16(a.add, a.ldadd) && on16(a.dx, a.lddx) && aligned(a.codes, 8);
+  const int parts = backward_parts(a.rows, a.cols, vec);
   if (parts == 0) {  // no rows
   } else if (a.cols > kBackwardCols) {
     k_ln_backward_wide<T><<<at_most(a.rows, 8), kLnThreads, 0, s>>>(a);
@@ -657,7 +682,8 @@ extern "C" onebit_status_t onebit_layer_norm_backward_workspace(int64_t rows, in
   if (!bytes) return fail(ONEBIT_ERR_INVALID_ARG, "bytes is NULL");
   onebit_status_t st = shape_ok(rows, cols);
   if (st != ONEBIT_OK) return st;
-  *bytes = (size_t)((int64_t)backward_parts(rows, cols) * 2 * cols * 4);
+  const int a = backward_parts(rows, cols, false), b = backward_parts(rows, cols, true);
+  *bytes = (size_t)((int64_t)(a > b ? a : b) * 2 * cols * 4);
   return ONEBIT_OK;
 }
 

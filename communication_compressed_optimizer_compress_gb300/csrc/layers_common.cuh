@@ -268,6 +268,17 @@ __device__ __forceinline__ Raw8<T> load8(const T* p) {
   for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
   return r;
 }
+// 32 bytes at once (the address lies on 32): a warp's accesses then cover whole lines
+__device__ __forceinline__ void load32(const void* p, uint32_t* v) {
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void store32(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
+               "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 __device__ __forceinline__ void expand8(const Raw8<float>& r, f2* f) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -312,6 +323,38 @@ __device__ __forceinline__ void store8(float* p, const f2* f) {
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const f2* f) {
   *reinterpret_cast<uint4*>(p) = make_uint4(narrow<T>(f[0]), narrow<T>(f[1]), narrow<T>(f[2]), narrow<T>(f[3]));
+}
+
+// 16 elements on 32 bytes
+template <typename T>
+__device__ __forceinline__ void load16(const T* p, f2* f) {
+  uint32_t v[8];
+#pragma unroll
+  for (int h = 0; h < (int)sizeof(T) / 2; ++h) {
+    load32(p + h * (32 / sizeof(T)), v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (sizeof(T) == 2) f[i] = widen<T>(v[i]);
+      else if (i % 2 == 0) f[4 * h + i / 2] = pair(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store16(T* p, const f2* f) {
+  uint32_t v[8];
+#pragma unroll
+  for (int h = 0; h < (int)sizeof(T) / 2; ++h) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (sizeof(T) == 2) {
+        v[i] = narrow<T>(f[i]);
+      } else if (i % 2 == 0) {
+        const float2 x = halves(f[4 * h + i / 2]);
+        v[i] = __float_as_uint(x.x), v[i + 1] = __float_as_uint(x.y);
+      }
+    }
+    store32(p + h * (32 / sizeof(T)), v);
+  }
 }
 
 // ------------------------------------------------------------------------------------------------

@@ -294,13 +294,6 @@ __device__ __forceinline__ void store_rows(char* staging, const uint32_t (&v)[16
   __syncwarp();
 }
 
-// 32 bytes of the lane's own row
-__device__ __forceinline__ void load32(const void* p, uint32_t* v) {
-  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-               : "l"(p));
-}
-
 // A matrix that an epilogue reads.  Where its rows start on 32 bytes a lane reads its own row, whole sectors at a
 // time, half of its 64 columns ahead: the first before the product is waited for, the second under the first
 // one's arithmetic (through the staging buffer and waited for at once: 2.6 us a tile).
