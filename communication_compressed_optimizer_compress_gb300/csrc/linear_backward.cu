@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(256) k_finish_dw(Partials c, int64_t rows, int
 constexpr int kRun = 512;
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) k_colsum_part(const T* __restrict__ dy, int64_t lddy, int64_t rows, int cols, bool wait_first,
-                                                     float* __restrict__ part) {
+                                                     float* __restrict__ part, void* db, int grad) {
   __shared__ float red[8][256];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.x * 256;
   launch_next();
@@ -88,7 +88,12 @@ __global__ void __launch_bounds__(256) k_colsum_part(const T* __restrict__ dy, i
     float v = 0.0f;
 #pragma unroll
     for (int w = 0; w < 8; ++w) v += red[w][t];
-    if (c < cols) part[run * cols + c] = v;
+    if (c < cols) {
+      if (!db) part[run * cols + c] = v;
+      else if (grad == ONEBIT_F32) static_cast<float*>(db)[c] = v;
+      else if (grad == ONEBIT_F16) static_cast<__half*>(db)[c] = from_f<__half>(v);
+      else static_cast<__nv_bfloat16*>(db)[c] = from_f<__nv_bfloat16>(v);
+    }
     __syncthreads();
   }
   if (!wait_first && blockIdx.x == 0 && blockIdx.y == 0) wait_previous();
@@ -103,12 +108,15 @@ cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, b
   const bool computed = a.dw && (a.codes || a.activation != ONEBIT_ACT_NONE);  // act(v) is not in memory yet
   const int64_t ldh = pad8(a.in);
   T* h = computed ? ws.take<T>(a.rows * ldh) : nullptr;
-  Operand dy{a.dy, a.lddy};
-  if (a.dx || a.dw) dy = readable(ws, a.dy, a.lddy, a.rows, a.out, s, run);
+  Readable copies;
+  Operand dy{a.dy, a.lddy}, w{}, x{h, ldh};
+  if (a.dx || a.dw) dy = copies.take(ws, a.dy, a.lddy, a.rows, a.out);
+  if (a.dx) w = copies.take(ws, a.w, a.ldw, a.out, a.in);
+  if (a.dw && !computed) x = copies.take(ws, a.x, a.ldx, a.rows, a.in);
+  if (run) copies.run(s);
   cudaError_t err = cudaSuccess;
   if (a.dx) {
     const ProductPlan plan = plan_product(sx, sms);
-    const Operand w = readable(ws, a.w, a.ldw, a.out, a.in, s, run);
     const Partials part = take_partials(ws, plan, a.rows, a.in);
     const T* add = static_cast<const T*>(a.add);
     if (run && plan.splits == 1) {
@@ -157,7 +165,6 @@ cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, b
   }
   if (a.dw) {
     const ProductPlan plan = plan_product(sw, sms);
-    const Operand x = computed ? Operand{h, ldh} : readable(ws, a.x, a.ldx, a.rows, a.in, s, run);
     const Partials part = take_partials(ws, plan, a.out, a.in);
     if (run)
       with_grad(a.grad_dtype, a.dw, [&](auto* g) {
@@ -177,16 +184,17 @@ cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, b
   }
   if (a.db) {
     const int64_t chunks = ceil_div(a.rows, kRun);
-    float* part = ws.take<float>(chunks * a.out);
+    float* part = chunks > 1 ? ws.take<float>(chunks * a.out) : nullptr;
+    void* whole = chunks > 1 ? nullptr : a.db;
     if (run) {
       const T* p = static_cast<const T*>(dy.p);
       const dim3 grid((unsigned)ceil_div(a.out, 256), (unsigned)(chunks < 65535 ? chunks : 65535));
       const bool first = !a.dx && !a.dw;
       // eight columns at a time where the last eight lie inside the row (a realigned copy is padded to them)
       err = vec16(p, dy.ld) && (a.out % 8 == 0 || p != a.dy)
-                ? launch_after(k_colsum_part<T, true>, grid, 256, s, p, dy.ld, a.rows, (int)a.out, first, part)
-                : launch_after(k_colsum_part<T, false>, grid, 256, s, p, dy.ld, a.rows, (int)a.out, first, part);
-      if (err == cudaSuccess) err = sum_parts(a.grad_dtype, part, chunks, a.out, a.out, a.db, nullptr, s);
+                ? launch_after(k_colsum_part<T, true>, grid, 256, s, p, dy.ld, a.rows, (int)a.out, first, part, whole, a.grad_dtype)
+                : launch_after(k_colsum_part<T, false>, grid, 256, s, p, dy.ld, a.rows, (int)a.out, first, part, whole, a.grad_dtype);
+      if (err == cudaSuccess && chunks > 1) err = sum_parts(a.grad_dtype, part, chunks, a.out, a.out, a.db, nullptr, s);
       if (err != cudaSuccess) return err;
     }
   }

@@ -36,32 +36,50 @@ struct Space {
   }
 };
 
-// Rows of any alignment into rows of ld = pad8(cols) on 16 bytes (the columns past the end are not read).
-static __global__ void __launch_bounds__(256) k_realign(const uint16_t* __restrict__ x, int64_t ldx, int64_t rows, int cols, int64_t ld,
-                                                        uint16_t* __restrict__ out) {
-  const int64_t per = ld / 8, total = rows * per;
+// Rows of any alignment into rows of ld = pad8(cols) on 16 bytes (the columns past the end are not read).  Up to
+// three matrices in one launch, one to each blockIdx.y.
+struct Realign {
+  const uint16_t* x;
+  int64_t ldx, rows, ld;
+  int cols;
+  uint16_t* out;
+};
+struct Realigns {
+  Realign m[3];
+};
+static __global__ void __launch_bounds__(256) k_realign(const Realigns all) {
+  const Realign& a = all.m[blockIdx.y];
+  const int64_t per = a.ld / 8, total = a.rows * per;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t r = i / per;
     const int c = (int)(i - r * per) * 8;
     uint32_t v[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const uint32_t lo = c + 2 * q < cols ? x[r * ldx + c + 2 * q] : 0, hi = c + 2 * q + 1 < cols ? x[r * ldx + c + 2 * q + 1] : 0;
+      const uint32_t lo = c + 2 * q < a.cols ? a.x[r * a.ldx + c + 2 * q] : 0, hi = c + 2 * q + 1 < a.cols ? a.x[r * a.ldx + c + 2 * q + 1] : 0;
       v[q] = lo | hi << 16;
     }
-    *reinterpret_cast<uint4*>(out + r * ld + c) = make_uint4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<uint4*>(a.out + r * a.ld + c) = make_uint4(v[0], v[1], v[2], v[3]);
   }
 }
 
-// The operand as TMA can read it: itself, or a realigned copy in the workspace.
-inline Operand readable(Space& ws, const void* p, int64_t ld, int64_t rows, int64_t cols, cudaStream_t s, bool run) {
-  if (copyable(p, ld)) return {p, ld};
-  const int64_t ldc = pad8(cols);
-  uint16_t* c = ws.take<uint16_t>(rows * ldc);
-  if (run)
-    k_realign<<<flat_grid(rows * ldc / 8, 256), 256, 0, s>>>(static_cast<const uint16_t*>(p), ld, rows, (int)cols, ldc, c);
-  return {c, ldc};
-}
+// The operands as TMA can read them: themselves, or realigned copies in the workspace, made by run().
+struct Readable {
+  Realigns all{};
+  int n = 0;
+  int64_t most = 0;
+  Operand take(Space& ws, const void* p, int64_t ld, int64_t rows, int64_t cols) {
+    if (copyable(p, ld)) return {p, ld};
+    const int64_t ldc = pad8(cols);
+    uint16_t* c = ws.take<uint16_t>(rows * ldc);
+    all.m[n++] = Realign{static_cast<const uint16_t*>(p), ld, rows, ldc, (int)cols, c};
+    if (rows * ldc / 8 > most) most = rows * ldc / 8;
+    return {c, ldc};
+  }
+  void run(cudaStream_t s) const {
+    if (n) k_realign<<<dim3(flat_grid(most, 256), (unsigned)n), 256, 0, s>>>(all);
+  }
+};
 
 // The value before the activation as the backward pass has it: itself, or its 8-bit checkpoint.
 template <typename T>

@@ -41,9 +41,11 @@ template <typename T>
 cudaError_t forward(const onebit_linear_t& a, Space& ws, cudaStream_t s, bool run) {
   const ProductShape shape{a.rows, a.out, a.in};
   const ProductPlan plan = plan_product(shape, sm_count());
-  const Operand x = readable(ws, a.x, a.ldx, a.rows, a.in, s, run), w = readable(ws, a.w, a.ldw, a.out, a.in, s, run);
+  Readable copies;
+  const Operand x = copies.take(ws, a.x, a.ldx, a.rows, a.in), w = copies.take(ws, a.w, a.ldw, a.out, a.in);
   const Partials part = take_partials(ws, plan, a.rows, a.out);
   if (!run) return cudaSuccess;
+  copies.run(s);
   ForwardEpilogue<T, kAny> e{};
   e.bias = a.bias;
   e.residual = make_input<T>(a.residual, a.ldr);

@@ -25,7 +25,7 @@ from typing import NamedTuple
 
 import torch
 
-from . import BF16, F16, F32, OK, OneBitError, _stream_ptr, lib
+from . import BF16, ERR_WORKSPACE, F16, F32, OK, OneBitError, _stream_ptr, lib
 
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH = range(4)
 ACTIVATIONS = {"none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH}
@@ -160,25 +160,6 @@ def _kept(x, name: str, cols=None, rows=None, dtype=None, device=None):
     return None, 0, codes.data_ptr(), s, r, c, x.dtype, codes.device
 
 
-def _on(stream):
-    """Makes `stream` current (None: as is), so that outputs and workspaces belong to the stream that writes
-    them."""
-    return _HERE if stream is None else torch.cuda.stream(stream)
-
-
-class _Here:
-    __slots__ = ()
-
-    def __enter__(self):
-        pass
-
-    def __exit__(self, *exc):
-        pass
-
-
-_HERE = _Here()
-
-
 def _stream(device) -> int:
     """The handle of the device's current stream (without making a Stream object, most of a small call)."""
     return torch._C._cuda_getCurrentRawStream(device.index)
@@ -225,70 +206,105 @@ def set_fault_injection(kind: int, value: int = 0):
     _check(_functions().onebit_layers_set_fault_injection(int(kind), int(value)), "onebit_layers_set_fault_injection")
 
 
+# Every operator works on the current stream: with `stream` it calls itself with that one current, so that its
+# outputs and workspace belong to the stream that writes them.
+
+
 def compress(x, stream=None) -> Checkpoint:
     """The 8-bit checkpoint of x."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return compress(x)
     rows, cols, ld = _matrix(x, "x")
-    code = _code(x.dtype, "x")
-    with _on(stream):
-        ck = _new_checkpoint(x, rows, cols, x.dtype, x.device)
-        _check(_functions().onebit_checkpoint_compress(x.data_ptr(), ld, code, rows, cols, ck.codes.data_ptr(),
-                                                       ck.scales.data_ptr(), _stream(x.device)),
-               "onebit_checkpoint_compress")
+    code, device = _code(x.dtype, "x"), x.device
+    ck = _new_checkpoint(x, rows, cols, x.dtype, device)
+    st = _functions().onebit_checkpoint_compress(x.data_ptr(), ld, code, rows, cols, ck[0].data_ptr(), ck[1].data_ptr(),
+                                                 _stream(device))
+    if st:
+        _check(st, "onebit_checkpoint_compress")
     return ck
 
 
 def restore(ck: Checkpoint, activation=ACT_NONE, stream=None):
     """activation(the values a checkpoint stands for), in the checkpoint's dtype."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return restore(ck, activation)
     _, _, codes, scales, rows, cols, dtype, device = _kept(ck, "ck")
-    code = _code(dtype, "ck")
-    with _on(stream):
-        x = torch.empty_like(ck.codes, dtype=dtype)
-        _check(_functions().onebit_checkpoint_restore(codes, scales, rows, cols, activation, x.data_ptr(), cols, code,
-                                                      _stream(device)), "onebit_checkpoint_restore")
+    x = torch.empty_like(ck[0], dtype=dtype)
+    st = _functions().onebit_checkpoint_restore(codes, scales, rows, cols, activation, x.data_ptr(), cols, _code(dtype, "ck"),
+                                                _stream(device))
+    if st:
+        _check(st, "onebit_checkpoint_restore")
     return x
 
 
 def layer_norm(x, gamma, beta, eps=1e-5, checkpoint=False, stream=None):
     """(y, mean, rstd), and the 8-bit checkpoint of x where asked for."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return layer_norm(x, gamma, beta, eps, checkpoint)
     rows, cols, ld = _matrix(x, "x")
     code, device = _code(x.dtype, "x"), x.device
     g, b = _vector(gamma, "gamma", cols, device), _vector(beta, "beta", cols, device)
-    with _on(stream):
-        y = _like(x)
-        mean, rstd = _rows_of(x, rows, device), _rows_of(x, rows, device)
-        ck = _new_checkpoint(x, rows, cols, x.dtype, device) if checkpoint else None
-        _check(_functions().onebit_layer_norm_forward(
-            x.data_ptr(), ld, code, rows, cols, g, b, eps, y.data_ptr(), cols, mean.data_ptr(), rstd.data_ptr(),
-            ck.codes.data_ptr() if ck else None, ck.scales.data_ptr() if ck else None, _stream(device)),
-            "onebit_layer_norm_forward")
+    y = _like(x)
+    mean, rstd = _rows_of(x, rows, device), _rows_of(x, rows, device)
+    ck = _new_checkpoint(x, rows, cols, x.dtype, device) if checkpoint else None
+    st = _functions().onebit_layer_norm_forward(
+        x.data_ptr(), ld, code, rows, cols, g, b, eps, y.data_ptr(), cols, mean.data_ptr(), rstd.data_ptr(),
+        ck[0].data_ptr() if checkpoint else None, ck[1].data_ptr() if checkpoint else None, _stream(device))
+    if st:
+        _check(st, "onebit_layer_norm_forward")
     return (y, mean, rstd, ck) if checkpoint else (y, mean, rstd)
 
 
 def layer_norm_backward(dy, x, gamma, mean, rstd, add=None, grad_dtype=torch.float32, stream=None):
     """(dx, dgamma, dbeta) from the layer's input x, a tensor or its Checkpoint; ``add`` joins dx."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return layer_norm_backward(dy, x, gamma, mean, rstd, add, grad_dtype)
     rows, cols, lddy = _matrix(dy, "dy")
-    code, gcode, device = _code(dy.dtype, "dy"), _code(grad_dtype, "grad_dtype"), dy.device
-    xp, ldx, codes, scales, *_ = _kept(x, "x", cols, rows, dy.dtype, device)
+    dtype, device = dy.dtype, dy.device
+    code, gcode = _code(dtype, "dy"), _code(grad_dtype, "grad_dtype")
+    xp, ldx, codes, scales, *_ = _kept(x, "x", cols, rows, dtype, device)
     g = _vector(gamma, "gamma", cols, device)
     mu, rs = _vector(mean, "mean", rows, device), _vector(rstd, "rstd", rows, device)
-    ap, lda = (add.data_ptr(), _matrix(add, "add", cols, rows, dy.dtype, device)[2]) if add is not None else (None, 0)
+    ap, lda = (add.data_ptr(), _matrix(add, "add", cols, rows, dtype, device)[2]) if add is not None else (None, 0)
     fn, need = _functions(), ctypes.c_size_t()
-    with _on(stream):
-        dx = _like(dy)
-        dgamma = torch.empty(cols, dtype=grad_dtype, device=device)
-        dbeta = torch.empty(cols, dtype=grad_dtype, device=device)
-        _check(fn.onebit_layer_norm_backward_workspace(rows, cols, ctypes.byref(need)),
-               "onebit_layer_norm_backward_workspace")
-        ws = _workspace(need.value, device)
-        _check(fn.onebit_layer_norm_backward(
-            dy.data_ptr(), lddy, xp, ldx, codes, scales, code, rows, cols, g, mu, rs, ap, lda, dx.data_ptr(), cols,
-            dgamma.data_ptr(), dbeta.data_ptr(), gcode, ws.data_ptr() if ws is not None else None, need.value,
-            _stream(device)), "onebit_layer_norm_backward")
+    dx = _like(dy)
+    dgamma, dbeta = torch.empty(cols, dtype=grad_dtype, device=device), torch.empty(cols, dtype=grad_dtype, device=device)
+    st = fn.onebit_layer_norm_backward_workspace(rows, cols, need)
+    if st:
+        _check(st, "onebit_layer_norm_backward_workspace")
+    ws = _workspace(need.value, device)
+    st = fn.onebit_layer_norm_backward(
+        dy.data_ptr(), lddy, xp, ldx, codes, scales, code, rows, cols, g, mu, rs, ap, lda, dx.data_ptr(), cols,
+        dgamma.data_ptr(), dbeta.data_ptr(), gcode, ws.data_ptr() if ws is not None else None, need.value, _stream(device))
+    if st:
+        _check(st, "onebit_layer_norm_backward")
     return dx, dgamma, dbeta
+
+
+def _with_workspace(run, size, args, device, where):
+    """Calls run(args, workspace, bytes, stream): without a workspace, which is enough for most calls, and with
+    one where the call says that it needs it (it has enqueued nothing then)."""
+    stream = _stream(device)
+    st = run(args, None, 0, stream)
+    if st == ERR_WORKSPACE:
+        need = ctypes.c_size_t()
+        st = size(args, need)
+        if not st:
+            ws = _workspace(need.value, device)
+            st = run(args, ws.data_ptr(), need.value, stream)
+    if st:
+        _check(st, where)
 
 
 def linear(x, w, bias=None, activation=ACT_NONE, residual=None, checkpoint=False, stream=None):
     """y = activation(x w^T + bias) + residual; with ``checkpoint`` (y, the 8-bit checkpoint of x w^T + bias)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linear(x, w, bias, activation, residual, checkpoint)
     rows, cols, ldx = _matrix(x, "x")
     dtype, device = x.dtype, x.device
     code = _code(dtype, "x")
@@ -297,17 +313,13 @@ def linear(x, w, bias=None, activation=ACT_NONE, residual=None, checkpoint=False
     out, _, ldw = _matrix(w, "w", cols, None, dtype, device)
     bp = _vector(bias, "bias", out, device)
     rp, ldr = (residual.data_ptr(), _matrix(residual, "residual", out, rows, dtype, device)[2]) if residual is not None else (None, 0)
-    fn, need = _functions(), ctypes.c_size_t()
-    with _on(stream):
-        y = _rows_by(x, rows, out, dtype, device)
-        ck = _new_checkpoint(x, rows, out, dtype, device) if checkpoint else None
-        a = LinearArgs(x.data_ptr(), ldx, w.data_ptr(), ldw, bp, rp, ldr, y.data_ptr(), out,
-                       ck.codes.data_ptr() if ck else None, ck.scales.data_ptr() if ck else None, rows, cols, out, code,
-                       activation)
-        _check(fn.onebit_linear_forward_workspace(a, need), "onebit_linear_forward_workspace")
-        ws = _workspace(need.value, device)
-        _check(fn.onebit_linear_forward(a, ws.data_ptr() if ws is not None else None, need.value, _stream(device)),
-               "onebit_linear_forward")
+    y = _rows_by(x, rows, out, dtype, device)
+    ck = _new_checkpoint(x, rows, out, dtype, device) if checkpoint else None
+    a = LinearArgs(x.data_ptr(), ldx, w.data_ptr(), ldw, bp, rp, ldr, y.data_ptr(), out,
+                   ck[0].data_ptr() if checkpoint else None, ck[1].data_ptr() if checkpoint else None, rows, cols, out, code,
+                   activation)
+    fn = _functions()
+    _with_workspace(fn.onebit_linear_forward, fn.onebit_linear_forward_workspace, a, device, "onebit_linear_forward")
     return (y, ck) if checkpoint else y
 
 
@@ -317,6 +329,9 @@ def linear_backward(dy, x, w, activation=ACT_NONE, add=None, grad_dtype=None, dw
     precedes the product (with ACT_NONE the product's input), a tensor or its Checkpoint; ``add`` joins
     dx.  grad_dtype (default dy's) is the type of dw (out x in) and db; ``dw`` and ``db`` may be the
     caller's contiguous tensors.  What ``need`` leaves out is None."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linear_backward(dy, x, w, activation, add, grad_dtype, dw, db, need)
     rows, out, lddy = _matrix(dy, "dy")
     dtype, device = dy.dtype, dy.device
     code = _code(dtype, "dy")
@@ -330,20 +345,18 @@ def linear_backward(dy, x, w, activation=ACT_NONE, add=None, grad_dtype=None, dw
         xp, ldx, codes, scales, *_ = _kept(x, "x", cols, rows, dtype, device)
     ap, lda = (add.data_ptr(), _matrix(add, "add", cols, rows, dtype, device)[2]) if add is not None else (None, 0)
     want_dx, want_dw, want_db = "dx" in need, "dw" in need, "db" in need
-    fn, bytes_ = _functions(), ctypes.c_size_t()
-    with _on(stream):
-        dx = _rows_by(dy, rows, cols, dtype, device) if want_dx else None
-        if want_dw and dw is None:
-            dw = torch.empty((out, cols), dtype=grad_dtype, device=device)
-        if want_db and db is None:
-            db = torch.empty(out, dtype=grad_dtype, device=device)
-        a = LinearGradArgs(dy.data_ptr(), lddy, xp, ldx, codes, scales, w.data_ptr(), ldw, ap, lda,
-                           dx.data_ptr() if want_dx else None, cols,
-                           _vector(dw, "dw", out * cols, device, grad_dtype) if want_dw else None,
-                           _vector(db, "db", out, device, grad_dtype) if want_db else None,
-                           rows, cols, out, code, activation, gcode)
-        _check(fn.onebit_linear_backward_workspace(a, bytes_), "onebit_linear_backward_workspace")
-        ws = _workspace(bytes_.value, device)
-        _check(fn.onebit_linear_backward(a, ws.data_ptr() if ws is not None else None, bytes_.value, _stream(device)),
-               "onebit_linear_backward")
-    return dx, (dw if want_dw else None), (db if want_db else None)
+    dx = _rows_by(dy, rows, cols, dtype, device) if want_dx else None
+    if not want_dw:
+        dw = None
+    elif dw is None:
+        dw = torch.empty(out, cols, dtype=grad_dtype, device=device)
+    if not want_db:
+        db = None
+    elif db is None:
+        db = torch.empty(out, dtype=grad_dtype, device=device)
+    a = LinearGradArgs(dy.data_ptr(), lddy, xp, ldx, codes, scales, w.data_ptr(), ldw, ap, lda,
+                       dx.data_ptr() if want_dx else None, cols, _vector(dw, "dw", out * cols, device, grad_dtype),
+                       _vector(db, "db", out, device, grad_dtype), rows, cols, out, code, activation, gcode)
+    fn = _functions()
+    _with_workspace(fn.onebit_linear_backward, fn.onebit_linear_backward_workspace, a, device, "onebit_linear_backward")
+    return dx, dw, db
