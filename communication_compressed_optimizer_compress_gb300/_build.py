@@ -8,9 +8,12 @@ package loads the checked library when the environment variable ONEBIT_LIBRARY i
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.util
 import os
 import shutil
 import subprocess
+import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -18,6 +21,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libonebit_adam.so")
 LIB_CHECKED = os.path.join(HERE, "libonebit_adam_checked.so")
 BUILD_DIR = os.path.join(HERE, "_build")
+BINDING = os.path.join(HERE, "_layers_binding.so")
 
 SOURCES = ["onebit_adam.cu", "onebit_noalloc.cu", "activation_checkpoint.cu", "layer_norm.cu", "tensor_product.cu",
            "linear_forward.cu", "linear_backward.cu"]
@@ -49,6 +53,36 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_binding(force: bool = False) -> str:
+    """_layers_binding.so: the layer operators' Python entry points in C++ (host code only, against the
+    installed torch)."""
+    src = os.path.join(CSRC, "layers_binding.cpp")
+    header = os.path.join(ROOT, "include", "onebit_layers.h")
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    # built against another torch than the one at hand: built again
+    stamp = os.path.join(BUILD_DIR, "binding_torch")
+    version = os.path.join(torch_dir, "version.py")
+    made_for = open(stamp).read() if os.path.exists(stamp) else ""
+    now = open(version).read() + sys.version
+    if not force and not _stale(BINDING, [src, header, __file__]) and made_for == now:
+        return BINDING
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    inc, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w", "-D_GLIBCXX_USE_CXX11_ABI=1", "-I", inc,
+           "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-I", os.path.join(cuda, "include"),
+           "-I", sysconfig.get_paths()["include"], src, "-o", tmp, "-L", lib, "-ltorch_python", "-ltorch_cuda",
+           "-ltorch_cpu", "-lc10_cuda", "-lc10", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
+    os.replace(tmp, BINDING)
+    with open(stamp, "w") as f:
+        f.write(now)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, checked: bool = False) -> str:
     lib = LIB_CHECKED if checked else LIB
     bdir = os.path.join(BUILD_DIR, "checked") if checked else BUILD_DIR
@@ -71,8 +105,10 @@ def build(force: bool = False, verbose: bool = False, checked: bool = False) -> 
         if verbose:
             print(r.stdout + r.stderr)
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, len(jobs))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
+        binding = ex.submit(build_binding, force)
         list(ex.map(run, jobs))
+        binding.result()
     if force or jobs or _stale(lib, objs):
         tmp = lib + f".tmp{os.getpid()}"
         run([nvcc(), "-gencode", "arch=compute_103a,code=sm_103a", "-shared", "-o", tmp, *objs])

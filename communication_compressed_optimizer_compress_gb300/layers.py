@@ -2,7 +2,9 @@
 a fused epilogue, and activation checkpoints held in 8 bits, forward and backward.
 
 Thin Python binding over the C ABI in ``include/onebit_layers.h`` (the formulas are stated there); every
-operator runs in the library's CUDA kernels on the current torch stream, or on ``stream``.
+operator runs in the library's CUDA kernels on the current torch stream, or on ``stream``.  The common case
+of each (2-D tensors that need no further look) is called through ``_layers_binding`` (C++), everything else,
+and every complaint, comes from here.
 
 Matrices are CUDA tensors whose last dimension is the features and has unit stride.  A 2-D tensor may
 have any row stride (a column slice of a wider buffer); one of more dimensions must be contiguous and
@@ -21,6 +23,8 @@ configured with, and may be written into the caller's tensors (``dw=``, ``db=``)
 from __future__ import annotations
 
 import ctypes
+import importlib.util
+import os
 from typing import NamedTuple
 
 import torch
@@ -61,6 +65,18 @@ class LinearGradArgs(ctypes.Structure):
 
 
 _fn = None
+_layers_binding = None
+
+
+def _load_binding():
+    """The compiled binding.  Raises if it has not been built."""
+    global _layers_binding
+    path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_layers_binding.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'`")
+    spec = importlib.util.spec_from_file_location("_layers_binding", path)
+    _layers_binding = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(_layers_binding)
 
 
 def _functions():
@@ -68,6 +84,7 @@ def _functions():
     global _fn
     if _fn is None:
         L = lib()
+        _load_binding()
         vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         sig = {
             "onebit_checkpoint_compress": [vp, i64, i32, i64, i64, vp, vp, vp],
@@ -90,6 +107,10 @@ def _functions():
             f.restype = ctypes.c_int
         L.onebit_layers_last_error.argtypes = []
         L.onebit_layers_last_error.restype = ctypes.c_char_p
+        names = ("onebit_checkpoint_compress", "onebit_checkpoint_restore", "onebit_layer_norm_forward",
+                 "onebit_layer_norm_backward_workspace", "onebit_layer_norm_backward", "onebit_linear_forward_workspace",
+                 "onebit_linear_forward", "onebit_linear_backward_workspace", "onebit_linear_backward")
+        _layers_binding.setup(tuple(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names), Checkpoint)
         _fn = L
     return _fn
 
@@ -215,6 +236,11 @@ def compress(x, stream=None) -> Checkpoint:
     if stream is not None:
         with torch.cuda.stream(stream):
             return compress(x)
+    if _fn is None:
+        _functions()
+    fast = _layers_binding.compress(x)
+    if fast is not None:
+        return fast
     rows, cols, ld = _matrix(x, "x")
     code, device = _code(x.dtype, "x"), x.device
     ck = _new_checkpoint(x, rows, cols, x.dtype, device)
@@ -230,6 +256,11 @@ def restore(ck: Checkpoint, activation=ACT_NONE, stream=None):
     if stream is not None:
         with torch.cuda.stream(stream):
             return restore(ck, activation)
+    if _fn is None:
+        _functions()
+    fast = _layers_binding.restore(ck, activation)
+    if fast is not None:
+        return fast
     _, _, codes, scales, rows, cols, dtype, device = _kept(ck, "ck")
     x = torch.empty_like(ck[0], dtype=dtype)
     st = _functions().onebit_checkpoint_restore(codes, scales, rows, cols, activation, x.data_ptr(), cols, _code(dtype, "ck"),
@@ -244,6 +275,11 @@ def layer_norm(x, gamma, beta, eps=1e-5, checkpoint=False, stream=None):
     if stream is not None:
         with torch.cuda.stream(stream):
             return layer_norm(x, gamma, beta, eps, checkpoint)
+    if _fn is None:
+        _functions()
+    fast = _layers_binding.layer_norm(x, gamma, beta, eps, checkpoint)
+    if fast is not None:
+        return fast
     rows, cols, ld = _matrix(x, "x")
     code, device = _code(x.dtype, "x"), x.device
     g, b = _vector(gamma, "gamma", cols, device), _vector(beta, "beta", cols, device)
@@ -263,6 +299,11 @@ def layer_norm_backward(dy, x, gamma, mean, rstd, add=None, grad_dtype=torch.flo
     if stream is not None:
         with torch.cuda.stream(stream):
             return layer_norm_backward(dy, x, gamma, mean, rstd, add, grad_dtype)
+    if _fn is None:
+        _functions()
+    fast = _layers_binding.layer_norm_backward(dy, x, gamma, mean, rstd, add, grad_dtype)
+    if fast is not None:
+        return fast
     rows, cols, lddy = _matrix(dy, "dy")
     dtype, device = dy.dtype, dy.device
     code, gcode = _code(dtype, "dy"), _code(grad_dtype, "grad_dtype")
@@ -305,6 +346,11 @@ def linear(x, w, bias=None, activation=ACT_NONE, residual=None, checkpoint=False
     if stream is not None:
         with torch.cuda.stream(stream):
             return linear(x, w, bias, activation, residual, checkpoint)
+    if _fn is None:
+        _functions()
+    fast = _layers_binding.linear(x, w, bias, activation, residual, checkpoint)
+    if fast is not None:
+        return fast
     rows, cols, ldx = _matrix(x, "x")
     dtype, device = x.dtype, x.device
     code = _code(dtype, "x")
@@ -332,6 +378,11 @@ def linear_backward(dy, x, w, activation=ACT_NONE, add=None, grad_dtype=None, dw
     if stream is not None:
         with torch.cuda.stream(stream):
             return linear_backward(dy, x, w, activation, add, grad_dtype, dw, db, need)
+    if _fn is None:
+        _functions()
+    fast = _layers_binding.linear_backward(dy, x, w, activation, add, grad_dtype, dw, db, need)
+    if fast is not None:
+        return fast
     rows, out, lddy = _matrix(dy, "dy")
     dtype, device = dy.dtype, dy.device
     code = _code(dtype, "dy")
