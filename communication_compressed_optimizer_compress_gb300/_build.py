@@ -25,7 +25,7 @@ BINDING = os.path.join(HERE, "_layers_binding.so")
 
 SOURCES = ["onebit_adam.cu", "onebit_noalloc.cu", "activation_checkpoint.cu", "layer_norm.cu", "tensor_product.cu",
            "linear_forward.cu", "linear_backward.cu"]
-HEADERS = ["onebit_kernels.cuh", "layers_common.cuh", "tensor_product.cuh", "linear_common.cuh",
+HEADERS = ["onebit_kernels.cuh", "layers_common.cuh", "tensor_product.cuh", "linear_common.cuh", "few_rows.cuh",
            os.path.join("..", "..", "include", "onebit_adam.h"),
            os.path.join("..", "..", "include", "onebit_layers.h")]
 

@@ -1,6 +1,6 @@
 // linear_forward.cu -- the linear layer's forward pass: matrix product with bias, activation, residual
 // and an 8-bit checkpoint in its epilogue.  See include/onebit_layers.h for the formulas.
-#include "linear_common.cuh"
+#include "few_rows.cuh"
 
 namespace onebit {
 namespace layers {
@@ -39,6 +39,7 @@ __global__ void __launch_bounds__(256) k_finish_forward(Partials c, int64_t rows
 // Takes the workspace; with `run`, enqueues the work too.
 template <typename T>
 cudaError_t forward(const onebit_linear_t& a, Space& ws, cudaStream_t s, bool run) {
+  if (few_rows(a)) return run ? run_few_rows<T>(a, s) : cudaSuccess;
   const ProductShape shape{a.rows, a.out, a.in};
   const ProductPlan plan = plan_product(shape, sm_count());
   Readable copies;
