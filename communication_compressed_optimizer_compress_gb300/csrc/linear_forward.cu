@@ -8,7 +8,7 @@ namespace {
 
 // The epilogue over the partial sums of a cut contraction, one warp per 64 columns of a row.
 template <typename T>
-__global__ void __launch_bounds__(256) k_finish_forward(Partials c, int64_t rows, int cols, const __grid_constant__ ForwardEpilogue<T, kAny> e) {
+__global__ void __launch_bounds__(256) k_finish_forward(Partials c, int64_t rows, int cols, const __grid_constant__ ForwardEpilogue<T, kAny, kAny, kAny> e) {
   const int lane = threadIdx.x & 31;
   const int64_t units = rows * e.blocks, step = (int64_t)gridDim.x * 8;
   for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < units; u += step) {
@@ -47,7 +47,7 @@ cudaError_t forward(const onebit_linear_t& a, Space& ws, cudaStream_t s, bool ru
   const Partials part = take_partials(ws, plan, a.rows, a.out);
   if (!run) return cudaSuccess;
   copies.run(s);
-  ForwardEpilogue<T, kAny> e{};
+  ForwardEpilogue<T, kAny, kAny, kAny> e{};
   e.bias = a.bias;
   e.residual = make_input<T>(a.residual, a.ldr);
   e.scales = a.scales;
@@ -58,17 +58,26 @@ cudaError_t forward(const onebit_linear_t& a, Space& ws, cudaStream_t s, bool ru
   if (err != cudaSuccess) return err;
   if (plan.splits == 1 && plan.ctas == 1) return run_product_by<1, false, false>(a.dtype, x, w, shape, plan, e, s);
   if (plan.splits == 1) {
-    auto go = [&](auto act) {
-      ForwardEpilogue<T, decltype(act)::value> f{};
+    using std::integral_constant;
+    using Any = integral_constant<int, kAny>;
+    auto go = [&](auto act, auto ck, auto res) {
+      ForwardEpilogue<T, decltype(act)::value, decltype(ck)::value, decltype(res)::value> f{};
       f.bias = e.bias, f.residual = e.residual, f.y = e.y, f.codes = e.codes, f.scales = e.scales, f.blocks = e.blocks, f.act = e.act;
       return run_product_by<2, false, false>(a.dtype, x, w, shape, plan, f, s);
     };
-    switch (a.activation) {
-      case ONEBIT_ACT_RELU: return go(std::integral_constant<int, ONEBIT_ACT_RELU>{});
-      case ONEBIT_ACT_GELU: return go(std::integral_constant<int, ONEBIT_ACT_GELU>{});
-      case ONEBIT_ACT_GELU_TANH: return go(std::integral_constant<int, ONEBIT_ACT_GELU_TANH>{});
-      default: return go(std::integral_constant<int, ONEBIT_ACT_NONE>{});
-    }
+    using No = integral_constant<int, 0>;
+    using Yes = integral_constant<int, 1>;
+    using None = integral_constant<int, ONEBIT_ACT_NONE>;
+    if (a.residual) return a.activation == ONEBIT_ACT_NONE && !a.codes ? go(None{}, No{}, Yes{}) : go(Any{}, Any{}, Any{});
+    auto by_act = [&](auto ck) {
+      switch (a.activation) {
+        case ONEBIT_ACT_RELU: return go(integral_constant<int, ONEBIT_ACT_RELU>{}, ck, No{});
+        case ONEBIT_ACT_GELU: return go(integral_constant<int, ONEBIT_ACT_GELU>{}, ck, No{});
+        case ONEBIT_ACT_GELU_TANH: return go(integral_constant<int, ONEBIT_ACT_GELU_TANH>{}, ck, No{});
+        default: return go(None{}, ck, No{});
+      }
+    };
+    return a.codes ? by_act(Yes{}) : by_act(No{});
   }
   PlainEpilogue<float> to{};
   err = to_partials(&to, part, a.out);

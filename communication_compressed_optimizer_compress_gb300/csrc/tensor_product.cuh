@@ -245,12 +245,15 @@ __device__ __forceinline__ void staging_free() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   __syncwarp();
 }
-// The warp's staged box to a matrix, by one lane; what lies outside the matrix is left out.
+// A staged box to a matrix, by one lane; what lies outside the matrix is left out.
+__device__ __forceinline__ void copy_out(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y), "r"(src) : "memory");
+}
 __device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y) {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
   if ((threadIdx.x & 31) == 0) {
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y), "r"(src) : "memory");
+    copy_out(map, src, x, y);
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   }
 }
@@ -264,6 +267,20 @@ struct Output {
   bool by_tma;
 };
 
+template <typename T>
+__device__ __forceinline__ void stage_rows(char* staging, const uint32_t (&v)[16]) {
+  const int lane = threadIdx.x & 31, swap = lane >> 1 & 3;  // 64-byte swizzle: 16-byte chunk j of row r lies at j ^ (r / 2 % 4)
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<uint4*>(staging + lane * 64 + (j ^ swap) * 16) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+}
+__device__ __forceinline__ void stage_codes(char* staging, const uint32_t (&v)[8]) {
+  const int lane = threadIdx.x & 31, swap = lane >> 2 & 1;  // 32-byte swizzle: chunk j of row r lies at j ^ (r / 4 % 2)
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    *reinterpret_cast<uint4*>(staging + kCodeStaging + lane * 32 + (j ^ swap) * 16) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+}
+
 // 64 bytes of a lane's row.  (With ordinary stores the way through shared memory and back to registers
 // took most of an epilogue's time, as it shares the SM's shared-memory bandwidth with the products.)
 template <typename T>
@@ -272,11 +289,7 @@ __device__ __forceinline__ void store_rows(char* staging, const uint32_t (&v)[16
   const int lane = threadIdx.x & 31;
   staging_free();
   if (out.by_tma) {
-    char* row = staging + lane * 64;
-    const int swap = lane >> 1 & 3;  // 64-byte swizzle: 16-byte chunk j of row r lies at j ^ (r / 2 % 4)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<uint4*>(row + (j ^ swap) * 16) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    stage_rows<T>(staging, v);
     store_box(&out.map, smem_addr(staging), col0, (int32_t)row0);
     return;
   }
@@ -355,11 +368,7 @@ __device__ __forceinline__ void store_codes(char* staging, const uint32_t (&v)[8
   const int lane = threadIdx.x & 31;
   staging_free();
   if (out.by_tma) {
-    char* row = staging + kCodeStaging + lane * 32;
-    const int swap = lane >> 2 & 1;  // 32-byte swizzle: chunk j of row r lies at j ^ (r / 4 % 2)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      *reinterpret_cast<uint4*>(row + (j ^ swap) * 16) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    stage_codes(staging, v);
     store_box(&out.map, smem_addr(staging + kCodeStaging), col0, (int32_t)row0);
     return;
   }
@@ -371,6 +380,26 @@ __device__ __forceinline__ void store_codes(char* staging, const uint32_t (&v)[8
   for (int r = 0; r < 32; ++r)
     if (row0 + r < rows && col0 + lane < cols) out.p[(row0 + r) * cols + col0 + lane] = (staging + r * kCodeRow)[lane];
   __syncwarp();
+}
+// y and the codes of 32 columns with one fence between their staging and their copies
+template <typename T>
+__device__ __forceinline__ void store_rows_and_codes(char* staging, const uint32_t (&v)[16], const Output<T>& y, const uint32_t (&c)[8],
+                                                     const Output<int8_t>& codes, int64_t row0, int64_t rows, int col0, int cols) {
+  if (y.by_tma && codes.by_tma) {
+    staging_free();
+    stage_rows<T>(staging, v);
+    stage_codes(staging, c);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+      copy_out(&y.map, smem_addr(staging), col0, (int32_t)row0);
+      copy_out(&codes.map, smem_addr(staging + kCodeStaging), col0, (int32_t)row0);
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+    return;
+  }
+  store_codes(staging, c, codes, row0, rows, col0, cols);
+  store_rows(staging, v, y, row0, rows, col0, cols);
 }
 __device__ __forceinline__ void load_codes(char* staging, uint32_t (&v)[8], const int8_t* p, int64_t row0, int64_t rows, int col0, int cols, bool vec) {
   const int lane = threadIdx.x & 31;
@@ -414,8 +443,11 @@ __device__ __forceinline__ void load_codes(char* staging, uint32_t (&v)[8], cons
 template <int ACT>
 __device__ __forceinline__ ActConsts shared_consts(const f2* consts) {
   ActConsts k;
+  if (ACT == ONEBIT_ACT_GELU || ACT == ONEBIT_ACT_GELU_TANH) {
 #pragma unroll
-  for (int i = 0; i < kActConsts; ++i) k.k[i] = ACT == ONEBIT_ACT_GELU || ACT == ONEBIT_ACT_GELU_TANH ? *const_cast<volatile const f2*>(consts + i) : 0;
+    for (int i = 0; i < kActConsts; i += 2)
+      asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(k.k[i]), "=l"(k.k[i + 1]) : "r"(smem_addr(consts + i)));
+  }
   return k;
 }
 
@@ -425,11 +457,11 @@ __device__ __forceinline__ ActConsts shared_consts(const f2* consts) {
 constexpr int kAny = -1;
 enum Kept16 { kKeptNone = 0, kKeptValue = 1, kKeptCodes = 2 };
 
-template <typename T, int ACT>
+template <typename T, int ACT, int CK, int RES>
 struct ForwardEpilogue {
   // y = act(d + bias) + residual, and the 8-bit checkpoint of d + bias
   static constexpr bool kFold = false;
-  static constexpr bool kAhead = ACT == ONEBIT_ACT_NONE;  // a residual's first columns are fetched ahead
+  static constexpr bool kAhead = ACT == ONEBIT_ACT_NONE && RES == 1;  // a residual's first columns are fetched ahead
   const float* bias;
   Input16<T> residual;
   Output<T> y;
@@ -438,22 +470,22 @@ struct ForwardEpilogue {
   int blocks;
   int act;
 
+  __device__ __forceinline__ bool keeps() const { return CK == kAny ? scales != nullptr : CK == 1; }
+  __device__ __forceinline__ bool adds() const { return RES == kAny ? residual.p != nullptr : RES == 1; }
   struct Ahead {
     uint32_t v[kAhead ? 16 : 1];
   };
-  // before the product is waited for: the warp's 64 columns of the bias, two a lane, and the residual's first 32
+  // before the product is waited for: the warp's 64 columns of the bias, two a lane (without one: zeros, as adding
+  // them is cheaper than both ways meeting behind a branch), and the residual's first 32
   __device__ __forceinline__ void prepare(Ahead& a, int64_t row0, int64_t rows, int col0, int cols, char* staging) const {
-    if constexpr (kAhead) {
-      if (residual.p) residual.ahead(row0 + (threadIdx.x & 31), rows, col0, cols, a.v);
-    }
-    if (!bias) return;
+    if constexpr (kAhead) residual.ahead(row0 + (threadIdx.x & 31), rows, col0, cols, a.v);
     const int c = col0 + 2 * (threadIdx.x & 31);
-    const f2 b = pair(c < cols ? __ldg(bias + c) : 0.0f, c + 1 < cols ? __ldg(bias + c + 1) : 0.0f);
+    f2 b = 0;
+    if (bias) b = pair(c < cols ? __ldg(bias + c) : 0.0f, c + 1 < cols ? __ldg(bias + c + 1) : 0.0f);
     reinterpret_cast<f2*>(staging + kBiasStaging)[threadIdx.x & 31] = b;
     __syncwarp();
   }
   __device__ __forceinline__ void add_bias(f2 (&z)[16], int half, const char* staging) const {
-    if (!bias) return;
     const ulonglong2* b = reinterpret_cast<const ulonglong2*>(staging + kBiasStaging + 128 * half);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -464,7 +496,7 @@ struct ForwardEpilogue {
   template <int A>
   __device__ __forceinline__ void finish(const f2* consts, f2 (&z)[16], uint32_t (&v)[16]) const {  // v: in the residual, out y
     const ActConsts k = shared_consts<A>(consts);
-    if (residual.p) {
+    if (adds()) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = narrow<T>(add2(act2<A>(k, z[i]), widen<T>(v[i])));
     } else {
@@ -476,7 +508,8 @@ struct ForwardEpilogue {
   __device__ __forceinline__ void run(Ahead& ahead, Load&& load, Release&& release, const f2* consts, int64_t row0, int64_t rows, int col0,
                                       int cols, char* staging) const {
     float inv = 0.0f;
-    if (scales) {  // columns past the end have z = 0: their operand rows were filled with zeros
+    bool plain = true;  // no value of the warp's blocks is infinite or NaN
+    if (keeps()) {  // columns past the end have z = 0: their operand rows were filled with zeros
       float most = 0.0f;
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
@@ -490,23 +523,26 @@ struct ForwardEpilogue {
       const int64_t row = row0 + (threadIdx.x & 31);
       if (row < rows) scales[row * blocks + col0 / kBlock] = s.scale;
       inv = s.inv;
+      plain = __all_sync(0xffffffffu, s.scale == s.scale);
     }
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
       f2 z[16];
-      uint32_t v[16];
+      uint32_t v[16], c[8];
       load(half, z);
       if (half) release();
       const int c0 = col0 + 32 * half;
       if (c0 >= cols) continue;
       add_bias(z, half, staging);
-      if (scales) {
-        uint32_t c[8];
+      if (keeps()) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = codes4(z[2 * i], z[2 * i + 1], inv);
-        store_codes(staging, c, codes, row0, rows, c0, cols);
+        for (int i = 0; i < 8; ++i) c[i] = codes4_rounded_once(z[2 * i], z[2 * i + 1], inv);
+        if (!plain && inv == 0.0f) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) c[i] = 0;
+        }
       }
-      if (residual.p) {
+      if (adds()) {
         if (kAhead && residual.wide && c0 + 32 <= cols) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] = ahead.v[kAhead ? i : 0];
@@ -522,7 +558,8 @@ struct ForwardEpilogue {
       else if (act == ONEBIT_ACT_RELU) finish<ONEBIT_ACT_RELU>(consts, z, v);
       else if (act == ONEBIT_ACT_GELU) finish<ONEBIT_ACT_GELU>(consts, z, v);
       else finish<ONEBIT_ACT_GELU_TANH>(consts, z, v);
-      store_rows(staging, v, y, row0, rows, c0, cols);
+      if (keeps()) store_rows_and_codes(staging, v, y, c, codes, row0, rows, c0, cols);
+      else store_rows(staging, v, y, row0, rows, c0, cols);
     }
     __syncwarp();  // the bias has been read: prepare() may write the next
   }
@@ -718,7 +755,7 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
   char* smem = smem_raw + (-(int)smem_addr(smem_raw) & 1023);
   char* staging_base = smem + kStages * kStageBytes;
   char* bars = staging_base + kEpilogueWarps<CTAS> * kStagingBytes;
-  f2* consts = reinterpret_cast<f2*>(bars + kBarrierBytes);
+  f2* consts = reinterpret_cast<f2*>(bars + kBarrierBytes);  // on 16 bytes
   const uint32_t bar0 = smem_addr(bars);
   auto full = [&](int s) { return bar0 + 8 * s; };
   auto empty = [&](int s) { return bar0 + 8 * (kStages + s); };
