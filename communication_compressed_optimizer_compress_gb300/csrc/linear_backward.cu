@@ -134,7 +134,7 @@ cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, b
         e.vec_codes = aligned(a.codes, 16) && a.in % 16 == 0;
         cudaError_t r = make_output(&e.dx, static_cast<T*>(a.dx), a.rows, a.in, a.lddx);
         if (r == cudaSuccess) r = make_output(&e.h, h, a.rows, a.in, ldh);
-        return r == cudaSuccess ? run_product_by<decltype(ctas)::value, false, true>(a.dtype, dy, w, sx, plan, e, s) : r;
+        return r == cudaSuccess ? run_product_by<decltype(ctas)::value, false, true>(a.dtype, dy, w, sx, plan, e, copies.n > 0, s) : r;
       };
       using std::integral_constant;
       using Two = integral_constant<int, 2>;
@@ -155,7 +155,7 @@ cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, b
     } else if (run) {
       PlainEpilogue<float> to{};
       err = to_partials(&to, part, a.in);
-      if (err == cudaSuccess) err = run_product<false, true>(a.dtype, dy, w, sx, plan, to, s);
+      if (err == cudaSuccess) err = run_product<false, true>(a.dtype, dy, w, sx, plan, to, copies.n > 0, s);
       k_finish_dx<T><<<flat_grid(a.rows * a.in, 256), 256, 0, s>>>(part, a.rows, (int)a.in, v, a.activation, add, a.ldadd,
                                                                    static_cast<T*>(a.dx), a.lddx, h, ldh);
     }
@@ -166,17 +166,18 @@ cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, b
   if (a.dw) {
     const ProductPlan plan = plan_product(sw, sms);
     const Partials part = take_partials(ws, plan, a.out, a.in);
+    const bool chained = copies.n > 0 || a.dx || computed;
     if (run)
       with_grad(a.grad_dtype, a.dw, [&](auto* g) {
         using G = std::remove_pointer_t<decltype(g)>;
         if (plan.splits == 1) {
           PlainEpilogue<G> e{};
           err = make_output(&e.out, g, a.out, a.in, a.in);
-          if (err == cudaSuccess) err = run_product<true, true>(a.dtype, dy, x, sw, plan, e, s);
+          if (err == cudaSuccess) err = run_product<true, true>(a.dtype, dy, x, sw, plan, e, chained, s);
         } else {
           PlainEpilogue<float> to{};
           err = to_partials(&to, part, a.in);
-          if (err == cudaSuccess) err = run_product<true, true>(a.dtype, dy, x, sw, plan, to, s);
+          if (err == cudaSuccess) err = run_product<true, true>(a.dtype, dy, x, sw, plan, to, chained, s);
           k_finish_dw<<<flat_grid(a.out * a.in, 256), 256, 0, s>>>(part, a.out, (int)a.in, g);
         }
       });

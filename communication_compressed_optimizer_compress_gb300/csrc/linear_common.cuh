@@ -50,6 +50,7 @@ struct Realigns {
 static __global__ void __launch_bounds__(256) k_realign(const Realigns all) {
   const Realign& a = all.m[blockIdx.y];
   const int64_t per = a.ld / 8, total = a.rows * per;
+  launch_next();
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t r = i / per;
     const int c = (int)(i - r * per) * 8;

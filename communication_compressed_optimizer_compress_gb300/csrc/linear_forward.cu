@@ -56,14 +56,14 @@ cudaError_t forward(const onebit_linear_t& a, Space& ws, cudaStream_t s, bool ru
   cudaError_t err = make_output(&e.y, static_cast<T*>(a.y), a.rows, a.out, a.ldy);
   if (err == cudaSuccess) err = make_output(&e.codes, a.codes, a.rows, a.out, a.out);
   if (err != cudaSuccess) return err;
-  if (plan.splits == 1 && plan.ctas == 1) return run_product_by<1, false, false>(a.dtype, x, w, shape, plan, e, s);
+  if (plan.splits == 1 && plan.ctas == 1) return run_product_by<1, false, false>(a.dtype, x, w, shape, plan, e, copies.n > 0, s);
   if (plan.splits == 1) {
     using std::integral_constant;
     using Any = integral_constant<int, kAny>;
     auto go = [&](auto act, auto ck, auto res) {
       ForwardEpilogue<T, decltype(act)::value, decltype(ck)::value, decltype(res)::value> f{};
       f.bias = e.bias, f.residual = e.residual, f.y = e.y, f.codes = e.codes, f.scales = e.scales, f.blocks = e.blocks, f.act = e.act;
-      return run_product_by<2, false, false>(a.dtype, x, w, shape, plan, f, s);
+      return run_product_by<2, false, false>(a.dtype, x, w, shape, plan, f, copies.n > 0, s);
     };
     using No = integral_constant<int, 0>;
     using Yes = integral_constant<int, 1>;
@@ -81,7 +81,7 @@ cudaError_t forward(const onebit_linear_t& a, Space& ws, cudaStream_t s, bool ru
   }
   PlainEpilogue<float> to{};
   err = to_partials(&to, part, a.out);
-  if (err == cudaSuccess) err = run_product<false, false>(a.dtype, x, w, shape, plan, to, s);
+  if (err == cudaSuccess) err = run_product<false, false>(a.dtype, x, w, shape, plan, to, copies.n > 0, s);
   if (err != cudaSuccess) return err;
   k_finish_forward<T><<<flat_grid(a.rows * e.blocks * 32, 256), 256, 0, s>>>(part, a.rows, (int)a.out, e);
   return cudaGetLastError();
