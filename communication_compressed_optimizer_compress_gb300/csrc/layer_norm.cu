@@ -267,8 +267,15 @@ struct BackwardArgs {
   float* part;  // [block][2][cols]
 };
 
-template <int TPR>
-constexpr int kBackThreads = TPR < 256 ? 256 : TPR;
+// Threads that an SM has registers for (96 a thread, 128 with two groups of columns), in as few blocks as can be: a
+// block leaves one partial sum of each parameter.  (With 768 threads of 80 registers the single-element forms spill:
+// 16384 x 1001 bf16 57.7 us for 44.0.)
+template <int CH>
+constexpr int kBackRoom = CH == 1 ? 640 : 512;
+template <int TPR, int CH>
+constexpr int kBackGroups = kBackRoom<CH> / TPR < 10 ? kBackRoom<CH> / TPR : 10;  // rows at a time
+template <int TPR, int CH>
+constexpr int kBackThreads = TPR * kBackGroups<TPR, CH>;
 
 // The kept input of one thread's columns: values, or codes with the scale of their block.  normal() gives
 // the normalised values x rstd - mean rstd, one operation each.
@@ -349,14 +356,15 @@ struct KeptRow<T, TPR, CH, false, true> {
 // instruction issue with four warps to a row of 1024 columns (62% of the slots, 1370 instructions a row,
 // 29.6 us at 16384 rows from the checkpoint with `add`), so two warps have it, sixteen columns a thread.
 template <typename T, int TPR, int CH, bool VEC, bool CODES>
-__global__ void __launch_bounds__(kBackThreads<TPR>, (CH == 1 ? 768 : 512) / kBackThreads<TPR>) k_ln_backward(const BackwardArgs A) {
-  constexpr int kGroups = kBackThreads<TPR> / TPR;
+__global__ void __launch_bounds__(kBackThreads<TPR, CH>, kBackRoom<CH> / kBackThreads<TPR, CH>) k_ln_backward(const BackwardArgs A) {
+  constexpr int kGroups = kBackGroups<TPR, CH>;
   const int cols = A.cols;
   using Col = Columns<TPR, VEC>;
   __shared__ float red[kGroups][2][2 * 32];
-  __shared__ f2 join[kGroups == 1 ? 1 : 2 * TPR * CH * 4];
+  constexpr int kSums = 2 * CH * 4;  // pairs of sums a thread
+  __shared__ f2 join[kGroups == 1 ? 1 : kGroups / 2 * kSums * TPR];
   const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
-  const int64_t first = (int64_t)blockIdx.x * kGroups + group, step = (int64_t)gridDim.x * kGroups;
+  const int64_t first = (int64_t)group * gridDim.x + blockIdx.x, step = (int64_t)gridDim.x * kGroups;
   int turn = 0;
   launch_next();
   f2 dg[CH][4], db[CH][4];
@@ -423,21 +431,27 @@ __global__ void __launch_bounds__(kBackThreads<TPR>, (CH == 1 ? 768 : 512) / kBa
     }
     pdx += step * A.lddx;
   }
-  if (kGroups > 1) {
-    for (int q = 0; q < kGroups; ++q) {
-      __syncthreads();
-      if (group == q) {
+  // the upper half of the row groups that had rows hand their sums to the lower
+  const int64_t met = (A.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;
+  for (int n = met < kGroups ? (int)met : kGroups; n > 1; n = (n + 1) / 2) {
+    const int low = (n + 1) / 2;
+    f2* const to = join + (group - low) * kSums * TPR + t;
+    const f2* const from = join + group * kSums * TPR + t;
+    __syncthreads();
+    if (group >= low && group < n) {
 #pragma unroll
-        for (int j = 0; j < CH; ++j)
+      for (int j = 0; j < CH; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int i = (j * 4 + e) * TPR + t, k = TPR * CH * 4 + i;
-            join[i] = q ? add2(join[i], dg[j][e]) : dg[j][e];
-            join[k] = q ? add2(join[k], db[j][e]) : db[j][e];
-          }
-      }
+        for (int e = 0; e < 4; ++e) to[(j * 4 + e) * TPR] = dg[j][e], to[(CH * 4 + j * 4 + e) * TPR] = db[j][e];
     }
     __syncthreads();
+    if (group + low < n) {
+#pragma unroll
+      for (int j = 0; j < CH; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          dg[j][e] = add2(dg[j][e], from[(j * 4 + e) * TPR]), db[j][e] = add2(db[j][e], from[(CH * 4 + j * 4 + e) * TPR]);
+    }
   }
   if (group == 0) {
     float* p = A.part + (int64_t)blockIdx.x * 2 * cols;
@@ -445,8 +459,8 @@ __global__ void __launch_bounds__(kBackThreads<TPR>, (CH == 1 ? 768 : 512) / kBa
     for (int j = 0; j < CH; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int i = (j * 4 + e) * TPR + t, c = Col::at(t, j, 2 * e), c1 = Col::at(t, j, 2 * e + 1);
-        const float2 g = halves(kGroups > 1 ? join[i] : dg[j][e]), b = halves(kGroups > 1 ? join[TPR * CH * 4 + i] : db[j][e]);
+        const int c = Col::at(t, j, 2 * e), c1 = Col::at(t, j, 2 * e + 1);
+        const float2 g = halves(dg[j][e]), b = halves(db[j][e]);
         if (c < cols) p[c] = g.x, p[cols + c] = b.x;
         if (c1 < cols) p[c1] = g.y, p[cols + c1] = b.y;
       }
@@ -564,58 +578,86 @@ void launch_forward(const ForwardArgs& a, cudaStream_t s) {
   using std::integral_constant;
   using One = integral_constant<int, 1>;
   using Two = integral_constant<int, 2>;
+  using Four = integral_constant<int, 4>;
+  constexpr bool kLean = VEC && sizeof(T) == 2;
+  // Single elements and fp32 need more registers a column: up to 2048 (wide fp32: 1024) columns a thread has eight and
+  // a row the fewest warps that hold it (4099 x 1155 fp32 by single elements: 9.6 us with 160 threads, 19.8 with 128 and
+  // sixteen columns each; 16384 x 1024 wide fp32: 23.9 with 128, 28.1 with a warp, but 8192 x 2048 28.5 and 24.5).
+  auto up_to_2048 = [&] {
+    if constexpr (kLean) {
+      if (a.cols <= 1024) return go(integral_constant<int, 32>{}, Four{}, One{}, 5);
+    } else {
+      if (a.cols <= 512) return go(integral_constant<int, 64>{}, One{}, Two{}, 5);
+      if (a.cols <= 1024) return go(integral_constant<int, 128>{}, One{}, Two{}, 5);
+    }
+    if constexpr (VEC) {
+      go(integral_constant<int, 128>{}, Two{}, Two{}, 5);
+    } else {
+      if (a.cols <= 1280) go(integral_constant<int, 160>{}, One{}, Two{}, 4);
+      else if (a.cols <= 1536) go(integral_constant<int, 192>{}, One{}, Two{}, 3);
+      else go(integral_constant<int, 256>{}, One{}, Two{}, 2);
+    }
+  };
   if (a.cols <= 256) go(integral_constant<int, 32>{}, One{}, Two{}, 5);
-  else if (a.cols <= 1024) go(integral_constant<int, 32>{}, integral_constant<int, 4>{}, One{}, 5);
-  else if (a.cols <= 2048) go(integral_constant<int, 128>{}, Two{}, Two{}, 5);
+  else if (a.cols <= 2048) up_to_2048();
   else if (a.cols <= 4096) go(integral_constant<int, 256>{}, Two{}, Two{}, 2);
-  else if (a.cols <= kForwardCols) go(integral_constant<int, 512>{}, integral_constant<int, 4>{}, One{}, 1);
+  else if (a.cols <= kForwardCols) go(integral_constant<int, 512>{}, Four{}, One{}, 1);
   else k_ln_forward_wide<T><<<at_most(a.rows, 8), kLnThreads, 0, s>>>(a);
 }
 
-// The backward form for a width: threads a row, groups of eight columns a thread.  Single elements need more
-// registers a column, so the narrow form has one group a thread and twice the threads.
-struct BackwardForm {
-  int tpr, ch;
-};
-BackwardForm backward_form(int64_t cols, bool vec) {
-  if (cols <= 256) return {32, 1};
-  if (cols <= 1024) return vec ? BackwardForm{64, 2} : BackwardForm{128, 1};
-  if (cols <= 2048) return vec ? BackwardForm{128, 2} : BackwardForm{256, 1};
-  if (cols <= 4096) return vec ? BackwardForm{256, 2} : BackwardForm{512, 1};
-  return {512, 2};
+// The backward form for a width: threads a row, groups of eight columns a thread.  In 16 bits, read wide, a row has
+// few threads with two groups each; single elements and fp32 need more registers a column, so there a thread has one
+// group and a row the fewest warps that hold it (16384 x 1024 fp32 with two groups a thread spilled; 4099 x 1155 fp32
+// by single elements 20.8 us with 160 threads a row, 23.3 with 256).
+template <typename T, bool VEC>
+constexpr bool kTwoGroups = VEC && sizeof(T) == 2;
+template <bool TWO, typename F>
+void with_backward_form(int64_t cols, F&& f) {
+  using std::integral_constant;
+  using One = integral_constant<int, 1>;
+  using Two = integral_constant<int, 2>;
+  if (cols <= 256) return f(integral_constant<int, 32>{}, One{});
+  if constexpr (TWO) {
+    if (cols <= 1024) return f(integral_constant<int, 64>{}, Two{});
+    if (cols <= 2048) return f(integral_constant<int, 128>{}, Two{});
+    if (cols <= 4096) return f(integral_constant<int, 256>{}, Two{});
+  } else {
+    if (cols <= 512) return f(integral_constant<int, 64>{}, One{});
+    if (cols <= 1024) return f(integral_constant<int, 128>{}, One{});
+    if (cols <= 1280) return f(integral_constant<int, 160>{}, One{});
+    if (cols <= 1536) return f(integral_constant<int, 192>{}, One{});
+    if (cols <= 2048) return f(integral_constant<int, 256>{}, One{});
+    if (cols <= 3072) return f(integral_constant<int, 384>{}, One{});
+    if (cols <= 4096) return f(integral_constant<int, 512>{}, One{});
+  }
+  f(integral_constant<int, 512>{}, Two{});
 }
 // Blocks of the backward kernel, which are the parts that the parameters' gradients are summed from.
-int backward_parts(int64_t rows, int64_t cols, bool vec) {
+template <bool TWO>
+int backward_parts(int64_t rows, int64_t cols) {
   if (rows == 0) return 0;
   if (cols > kBackwardCols) return (int)ceil_div(rows, ceil_div(rows, 64));
-  const BackwardForm f = backward_form(cols, vec);
-  const int threads = f.tpr < 256 ? 256 : f.tpr;
-  const int per_sm = (f.ch == 1 ? 768 : 512) / threads;
-  return (int)at_most(ceil_div(rows, threads / f.tpr), per_sm);
+  int parts = 0;
+  with_backward_form<TWO>(cols, [&](auto tpr, auto ch) {
+    constexpr int kCh = decltype(ch)::value, kThreads = kBackThreads<decltype(tpr)::value, kCh>;
+    parts = (int)at_most(rows, kBackRoom<kCh> / kThreads);
+  });
+  return parts;
 }
 
 template <typename T, bool VEC, bool CODES>
 void launch_backward(const BackwardArgs& a, int parts, cudaStream_t s) {
-  const BackwardForm f = backward_form(a.cols, VEC);
-  auto go = [&](auto tpr, auto ch) {
+  with_backward_form<kTwoGroups<T, VEC>>(a.cols, [&](auto tpr, auto ch) {
     constexpr int kTpr = decltype(tpr)::value, kCh = decltype(ch)::value;
-    k_ln_backward<T, kTpr, kCh, VEC, CODES><<<parts, kBackThreads<kTpr>, 0, s>>>(a);
-  };
-  using std::integral_constant;
-  constexpr int kCh = VEC ? 2 : 1, kWide = VEC ? 1 : 2;
-  using Ch = integral_constant<int, kCh>;
-  if (f.tpr == 32) go(integral_constant<int, 32>{}, integral_constant<int, 1>{});
-  else if (a.cols <= 1024) go(integral_constant<int, 64 * kWide>{}, Ch{});
-  else if (a.cols <= 2048) go(integral_constant<int, 128 * kWide>{}, Ch{});
-  else if (a.cols <= 4096) go(integral_constant<int, 256 * kWide>{}, Ch{});
-  else go(integral_constant<int, 512>{}, integral_constant<int, 2>{});
+    k_ln_backward<T, kTpr, kCh, VEC, CODES><<<parts, kBackThreads<kTpr, kCh>, 0, s>>>(a);
+  });
 }
 
 template <typename T>
 cudaError_t launch_backward(const BackwardArgs& a, cudaStream_t s) {
   auto on16 = [](const void* p, int64_t ld) { return aligned(p, 16) && (ld * (int64_t)sizeof(T)) % 16 == 0; };
   const bool vec = a.cols % 8 == 0 && on16(a.dy, a.lddy) && on16(a.x, a.ldx) && on16(a.add, a.ldadd) && on16(a.dx, a.lddx) && aligned(a.codes, 8);
-  const int parts = backward_parts(a.rows, a.cols, vec);
+  const int parts = vec ? backward_parts<kTwoGroups<T, true>>(a.rows, a.cols) : backward_parts<false>(a.rows, a.cols);
   if (parts == 0) {  // no rows
   } else if (a.cols > kBackwardCols) {
     k_ln_backward_wide<T><<<at_most(a.rows, 8), kLnThreads, 0, s>>>(a);
@@ -682,7 +724,7 @@ extern "C" onebit_status_t onebit_layer_norm_backward_workspace(int64_t rows, in
   if (!bytes) return fail(ONEBIT_ERR_INVALID_ARG, "bytes is NULL");
   onebit_status_t st = shape_ok(rows, cols);
   if (st != ONEBIT_OK) return st;
-  const int a = backward_parts(rows, cols, false), b = backward_parts(rows, cols, true);
+  const int a = backward_parts<false>(rows, cols), b = backward_parts<true>(rows, cols);
   *bytes = (size_t)((int64_t)(a > b ? a : b) * 2 * cols * 4);
   return ONEBIT_OK;
 }

@@ -388,24 +388,27 @@ __device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.lau
 __device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Sums of `parts` partial rows of `width` fp32 columns, in a fixed order; columns below `split` go to lo,
-// the others to hi.  A block has 32 columns, 32 threads to each.
-constexpr int kSumRows = 32;
-template <typename G>
-static __global__ void __launch_bounds__(32 * kSumRows) k_sum_parts(const float* __restrict__ part, int64_t parts, int64_t width, int64_t split,
-                                                                    G* __restrict__ lo, G* __restrict__ hi) {
-  __shared__ float red[kSumRows][33];
-  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+// the others to hi.  A block of 1024 threads has COLS columns, 16 (two sectors of a row, and twice the threads to
+// a column) where 32 would leave SMs without a block.
+template <typename G, int COLS>
+static __global__ void __launch_bounds__(1024) k_sum_parts(const float* __restrict__ part, int64_t parts, int64_t width, int64_t split,
+                                                           G* __restrict__ lo, G* __restrict__ hi) {
+  constexpr int kRows = 1024 / COLS;
+  __shared__ float red[kRows][COLS + 1];
+  const int col = threadIdx.x % COLS, row = threadIdx.x / COLS;
+  const int64_t c = (int64_t)blockIdx.x * COLS + col;
   wait_previous();
   float s = 0.0f;
   if (c < width) {
 #pragma unroll 8
-    for (int64_t p = row; p < parts; p += kSumRows) s += part[p * width + c];
+    for (int64_t p = row; p < parts; p += kRows) s += part[p * width + c];
   }
-  red[row][lane] = s;
+  red[row][col] = s;
   __syncthreads();
-  const float t = warp_sum(red[lane][row]);  // column `row` of the block's 32
-  const int64_t o = (int64_t)blockIdx.x * 32 + row;
+  const int lane = threadIdx.x & 31, mine = threadIdx.x >> 5;  // a warp's column
+  if (mine >= COLS) return;
+  const float t = warp_sum(COLS == 32 ? red[lane][mine] : red[lane][mine] + red[lane + kRows / 2][mine]);
+  const int64_t o = (int64_t)blockIdx.x * COLS + mine;
   if (lane == 0 && o < width) {
     if (o < split) lo[o] = from_f<G>(t);
     else hi[o - split] = from_f<G>(t);
@@ -462,8 +465,12 @@ inline cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int thread
 }
 template <typename G>
 inline cudaError_t sum_parts(const float* part, int64_t parts, int64_t width, int64_t split, void* lo, void* hi, cudaStream_t s) {
-  return launch_after(k_sum_parts<G>, dim3((unsigned)ceil_div(width, 32)), 32 * kSumRows, s, part, parts, width, split, static_cast<G*>(lo),
-                      static_cast<G*>(hi));
+  auto go = [&](auto cols) {
+    constexpr int kCols = decltype(cols)::value;
+    return launch_after(k_sum_parts<G, kCols>, dim3((unsigned)ceil_div(width, kCols)), 1024, s, part, parts, width, split, static_cast<G*>(lo),
+                        static_cast<G*>(hi));
+  };
+  return ceil_div(width, 32) < sm_count() ? go(std::integral_constant<int, 16>{}) : go(std::integral_constant<int, 32>{});
 }
 inline cudaError_t sum_parts(int32_t dtype, const float* part, int64_t parts, int64_t width, int64_t split, void* lo, void* hi, cudaStream_t s) {
   return dtype == ONEBIT_F32   ? sum_parts<float>(part, parts, width, split, lo, hi, s)
