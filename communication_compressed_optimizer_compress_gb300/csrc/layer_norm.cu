@@ -352,10 +352,12 @@ struct KeptRow<T, TPR, CH, false, true> {
 };
 
 // dx of every row, and this block's share of dgamma and dbeta.  Each thread adds up its own columns over
-// the rows that it meets; at the end the block's row groups are joined in shared memory, in order.  Bound by
+// the rows that it meets; at the end the block's row groups are joined in shared memory, in a fixed order.  Bound by
 // instruction issue with four warps to a row of 1024 columns (62% of the slots, 1370 instructions a row,
-// 29.6 us at 16384 rows from the checkpoint with `add`), so two warps have it, sixteen columns a thread.
-template <typename T, int TPR, int CH, bool VEC, bool CODES>
+// 29.6 us at 16384 rows from the checkpoint with `add`), so two warps have it, sixteen columns a thread: 27.6 us.
+// Single elements wait for their loads, gamma's among them: 4099 x 1155 fp32 21.1 us with gamma read for every
+// row (36% of the issue slots), 16.2 with gamma in registers.
+template <typename T, int TPR, int CH, bool VEC, bool CODES, bool ADD>
 __global__ void __launch_bounds__(kBackThreads<TPR, CH>, kBackRoom<CH> / kBackThreads<TPR, CH>) k_ln_backward(const BackwardArgs A) {
   constexpr int kGroups = kBackGroups<TPR, CH>;
   const int cols = A.cols;
@@ -374,14 +376,14 @@ __global__ void __launch_bounds__(kBackThreads<TPR, CH>, kBackRoom<CH> / kBackTh
     for (int e = 0; e < 4; ++e) dg[j][e] = db[j][e] = 0;
   KeptRow<T, TPR, CH, VEC, CODES> kept(A, first, step);
   RowInput<T, TPR, CH, VEC> dyin, addin, addnow;
-  const T *pdy = static_cast<const T*>(A.dy) + first * A.lddy, *padd = static_cast<const T*>(A.add) + (A.add ? first * A.ldadd : 0);
+  const T *pdy = static_cast<const T*>(A.dy) + first * A.lddy, *padd = static_cast<const T*>(A.add) + (ADD ? first * A.ldadd : 0);
   T* pdx = static_cast<T*>(A.dx) + first * A.lddx;
   float mu = 0.0f, rs = 0.0f;
   auto load = [&](int64_t r) {
     kept.load(t, cols);
     dyin.load(pdy, t, cols);
     pdy += step * A.lddy;
-    if (A.add) {
+    if (ADD) {
       addin.load(padd, t, cols);
       padd += step * A.ldadd;
     }
@@ -389,6 +391,13 @@ __global__ void __launch_bounds__(kBackThreads<TPR, CH>, kBackRoom<CH> / kBackTh
     rs = __ldg(A.rstd + r);
   };
   if (first < A.rows) load(first);
+  // gamma stays in the registers that `add` would need, where there is one group of columns
+  constexpr bool kHold = !ADD && CH == 1;
+  f2 held[kHold ? CH : 1][4];
+  if (kHold) {
+#pragma unroll
+    for (int j = 0; j < CH; ++j) param_group<TPR, VEC>(A.gamma, t, j, cols, held[kHold ? j : 0]);
+  }
   for (int64_t r = first; r < A.rows; r += step) {
     f2 xh[CH][4], d[CH][4], s0 = 0, s1 = 0;
     const float rstd = rs, shift = -mu * rs;
@@ -402,7 +411,12 @@ __global__ void __launch_bounds__(kBackThreads<TPR, CH>, kBackRoom<CH> / kBackTh
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
       f2 gamma[4];
-      param_group<TPR, VEC>(A.gamma, t, j, cols, gamma);
+      if (kHold) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) gamma[e] = held[kHold ? j : 0][e];
+      } else {
+        param_group<TPR, VEC>(A.gamma, t, j, cols, gamma);
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         // columns past the end have dy = gamma = 0 and add nothing
@@ -421,7 +435,7 @@ __global__ void __launch_bounds__(kBackThreads<TPR, CH>, kBackRoom<CH> / kBackTh
       f2 o[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[e] = fma2(xh[j][e], c1, fma2(d[j][e], splat(rstd), c0));
-      if (A.add) {
+      if (ADD) {
         f2 a[4];
         addnow.expand(j, a);
 #pragma unroll
@@ -649,7 +663,8 @@ template <typename T, bool VEC, bool CODES>
 void launch_backward(const BackwardArgs& a, int parts, cudaStream_t s) {
   with_backward_form<kTwoGroups<T, VEC>>(a.cols, [&](auto tpr, auto ch) {
     constexpr int kTpr = decltype(tpr)::value, kCh = decltype(ch)::value;
-    k_ln_backward<T, kTpr, kCh, VEC, CODES><<<parts, kBackThreads<kTpr, kCh>, 0, s>>>(a);
+    if (a.add) k_ln_backward<T, kTpr, kCh, VEC, CODES, true><<<parts, kBackThreads<kTpr, kCh>, 0, s>>>(a);
+    else k_ln_backward<T, kTpr, kCh, VEC, CODES, false><<<parts, kBackThreads<kTpr, kCh>, 0, s>>>(a);
   });
 }
 
