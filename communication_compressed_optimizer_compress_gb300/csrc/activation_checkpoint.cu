@@ -58,6 +58,7 @@ struct Wide {
 template <typename T>
 __global__ void __launch_bounds__(kCkThreads) k_compress_wide(const T* __restrict__ x, int64_t ldx, Wide w, int8_t* __restrict__ codes,
                                                               float* __restrict__ scales) {
+  in_turn();
   const int per = 4 * w.blocks;
   const int64_t runs = (w.rows + w.run_rows - 1) / w.run_rows;
   for (int64_t run = blockIdx.x; run < runs; run += gridDim.x) {
@@ -91,6 +92,7 @@ __global__ void __launch_bounds__(kCkThreads) k_compress_wide(const T* __restric
 template <typename T, int ACT>
 __global__ void __launch_bounds__(kCkThreads) k_restore_wide(const int8_t* __restrict__ codes, const float* __restrict__ scales, Wide w,
                                                              T* __restrict__ x, int64_t ldx) {
+  in_turn();
   const int per = w.cols / 16;
   const ActConsts k = literal_consts<ACT>();
   const int64_t runs = (w.rows + w.run_rows - 1) / w.run_rows;
@@ -116,6 +118,7 @@ template <typename T>
 __global__ void __launch_bounds__(kCkThreads) k_compress(const T* __restrict__ x, int64_t ldx, int64_t rows, int cols,
                                                          int blocks, int8_t* __restrict__ codes,
                                                          float* __restrict__ scales) {
+  in_turn();
   const int lane = threadIdx.x & 31;
   const int64_t units = rows * blocks, step = (int64_t)gridDim.x * (kCkThreads / 32);
   for (int64_t u = (int64_t)blockIdx.x * (kCkThreads / 32) + (threadIdx.x >> 5); u < units; u += step) {
@@ -134,6 +137,7 @@ template <typename T>
 __global__ void __launch_bounds__(kCkThreads) k_restore(const int8_t* __restrict__ codes,
                                                         const float* __restrict__ scales, int64_t rows, int cols,
                                                         int blocks, int act, T* __restrict__ x, int64_t ldx) {
+  in_turn();
   const int lane = threadIdx.x & 31;
   const int64_t units = rows * blocks, step = (int64_t)gridDim.x * (kCkThreads / 32);
   for (int64_t u = (int64_t)blockIdx.x * (kCkThreads / 32) + (threadIdx.x >> 5); u < units; u += step) {
@@ -158,9 +162,9 @@ void compress(const void* x, int64_t ldx, int32_t dtype, int64_t rows, int cols,
   const T* p = static_cast<const T*>(x);
   if (wide_ok(x, ldx, dtype, cols, codes)) {
     const Wide w{rows, cols, blocks, cols < kCkRun ? kCkRun / cols : 1};
-    k_compress_wide<T><<<ck_grid(ceil_div(rows, w.run_rows)), kCkThreads, 0, s>>>(p, ldx, w, codes, scales);
+    launch_after(k_compress_wide<T>, ck_grid(ceil_div(rows, w.run_rows)), kCkThreads, s, p, ldx, w, codes, scales);
   } else {
-    k_compress<T><<<ck_grid(ceil_div(rows * blocks, kCkThreads / 32)), kCkThreads, 0, s>>>(p, ldx, rows, cols, blocks, codes, scales);
+    launch_after(k_compress<T>, ck_grid(ceil_div(rows * blocks, kCkThreads / 32)), kCkThreads, s, p, ldx, rows, cols, blocks, codes, scales);
   }
 }
 template <typename T>
@@ -170,12 +174,12 @@ void restore(const int8_t* codes, const float* scales, int64_t rows, int cols, i
   if (wide_ok(x, ldx, dtype, cols, codes)) {
     const Wide w{rows, cols, blocks, cols < kCkRun ? kCkRun / cols : 1};
     const unsigned grid = ck_grid(ceil_div(rows, w.run_rows));
-    if (act == ONEBIT_ACT_NONE) k_restore_wide<T, ONEBIT_ACT_NONE><<<grid, kCkThreads, 0, s>>>(codes, scales, w, p, ldx);
-    else if (act == ONEBIT_ACT_RELU) k_restore_wide<T, ONEBIT_ACT_RELU><<<grid, kCkThreads, 0, s>>>(codes, scales, w, p, ldx);
-    else if (act == ONEBIT_ACT_GELU) k_restore_wide<T, ONEBIT_ACT_GELU><<<grid, kCkThreads, 0, s>>>(codes, scales, w, p, ldx);
-    else k_restore_wide<T, ONEBIT_ACT_GELU_TANH><<<grid, kCkThreads, 0, s>>>(codes, scales, w, p, ldx);
+    if (act == ONEBIT_ACT_NONE) launch_after(k_restore_wide<T, ONEBIT_ACT_NONE>, grid, kCkThreads, s, codes, scales, w, p, ldx);
+    else if (act == ONEBIT_ACT_RELU) launch_after(k_restore_wide<T, ONEBIT_ACT_RELU>, grid, kCkThreads, s, codes, scales, w, p, ldx);
+    else if (act == ONEBIT_ACT_GELU) launch_after(k_restore_wide<T, ONEBIT_ACT_GELU>, grid, kCkThreads, s, codes, scales, w, p, ldx);
+    else launch_after(k_restore_wide<T, ONEBIT_ACT_GELU_TANH>, grid, kCkThreads, s, codes, scales, w, p, ldx);
   } else {
-    k_restore<T><<<ck_grid(ceil_div(rows * blocks, kCkThreads / 32)), kCkThreads, 0, s>>>(codes, scales, rows, cols, blocks, act, p, ldx);
+    launch_after(k_restore<T>, ck_grid(ceil_div(rows * blocks, kCkThreads / 32)), kCkThreads, s, codes, scales, rows, cols, blocks, act, p, ldx);
   }
 }
 

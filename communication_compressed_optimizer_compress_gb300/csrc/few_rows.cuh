@@ -47,6 +47,7 @@ struct FewRowsArgs {
 // M: sixteen-row halves (1 or 2); G: column groups of eight in a block.
 template <typename T, int M, int G>
 __global__ void __launch_bounds__(kFewThreads) k_few_rows(const FewRowsArgs A) {
+  in_turn();
   constexpr int kSplits = 8 / G, kAhead = 4;
   __shared__ float part[kSplits][M * 16][G * 8 + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp % G, split = warp / G;
@@ -114,7 +115,7 @@ cudaError_t run_few_rows(const onebit_linear_t& a, cudaStream_t s) {
   const int64_t groups = ceil_div(a.out, 8), sms = sm_count();
   auto go = [&](auto m, auto g) {
     constexpr int kM = decltype(m)::value, kG = decltype(g)::value;
-    k_few_rows<T, kM, kG><<<(unsigned)ceil_div(groups, kG), kFewThreads, 0, s>>>(f);
+    launch_after(k_few_rows<T, kM, kG>, (unsigned)ceil_div(groups, kG), kFewThreads, s, f);
   };
   using std::integral_constant;
   auto by_rows = [&](auto g) {

@@ -133,6 +133,7 @@ constexpr int kForwardThreads = TPR < 128 ? 128 : TPR;
 // 128 threads a row 28 us, a warp a row 26 us (gamma and beta took 62% of the L1's cycles).
 template <typename T, int TPR, int CH, int NR, bool VEC, bool FULL>
 __global__ void __launch_bounds__(kForwardThreads<TPR>, (TPR < 256 ? 640 : 512) / kForwardThreads<TPR>) k_ln_forward(const ForwardArgs A) {
+  in_turn();
   constexpr int kGroups = kForwardThreads<TPR> / TPR;
   const int cols = FULL ? TPR * CH * 8 : A.cols;
   using Col = Columns<TPR, VEC>;
@@ -359,6 +360,7 @@ struct KeptRow<T, TPR, CH, false, true> {
 // row (36% of the issue slots), 16.2 with gamma in registers.
 template <typename T, int TPR, int CH, bool VEC, bool CODES, bool ADD>
 __global__ void __launch_bounds__(kBackThreads<TPR, CH>, kBackRoom<CH> / kBackThreads<TPR, CH>) k_ln_backward(const BackwardArgs A) {
+  in_turn();
   constexpr int kGroups = kBackGroups<TPR, CH>;
   const int cols = A.cols;
   using Col = Columns<TPR, VEC>;
@@ -368,7 +370,6 @@ __global__ void __launch_bounds__(kBackThreads<TPR, CH>, kBackRoom<CH> / kBackTh
   const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
   const int64_t first = (int64_t)group * gridDim.x + blockIdx.x, step = (int64_t)gridDim.x * kGroups;
   int turn = 0;
-  launch_next();
   f2 dg[CH][4], db[CH][4];
 #pragma unroll
   for (int j = 0; j < CH; ++j)
@@ -497,6 +498,7 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 
 template <typename T>
 __global__ void __launch_bounds__(kLnThreads) k_ln_forward_wide(const ForwardArgs A) {
+  in_turn();
   __shared__ float red[kLnWarps];
   for (int64_t r = blockIdx.x; r < A.rows; r += gridDim.x) {
     const T* xr = static_cast<const T*>(A.x) + r * A.ldx;
@@ -536,6 +538,7 @@ __device__ __forceinline__ float kept_at(const BackwardArgs& A, int64_t r, int c
 }
 template <typename T>
 __global__ void __launch_bounds__(kLnThreads) k_ln_backward_wide(const BackwardArgs A) {
+  in_turn();
   __shared__ float red[kLnWarps];
   const T *dy = static_cast<const T*>(A.dy), *add = static_cast<const T*>(A.add);
   for (int64_t r = blockIdx.x; r < A.rows; r += gridDim.x) {
@@ -559,6 +562,7 @@ __global__ void __launch_bounds__(kLnThreads) k_ln_backward_wide(const BackwardA
 // this block's rows' share of dgamma and dbeta
 template <typename T>
 __global__ void __launch_bounds__(kLnThreads) k_ln_param_wide(const BackwardArgs A, int64_t run) {
+  in_turn();
   const int c = blockIdx.x * kLnThreads + threadIdx.x;
   if (c >= A.cols) return;
   const int64_t r0 = blockIdx.y * run, r1 = r0 + run < A.rows ? r0 + run : A.rows;
@@ -586,8 +590,8 @@ void launch_forward(const ForwardArgs& a, cudaStream_t s) {
   auto go = [&](auto tpr, auto ch, auto nr, int per_sm) {
     constexpr int kTpr = decltype(tpr)::value, kCh = decltype(ch)::value, kNr = decltype(nr)::value, kThreads = kForwardThreads<kTpr>;
     const unsigned grid = at_most(ceil_div(a.rows, kThreads / kTpr * kNr), per_sm);
-    if (VEC && a.cols == kTpr * kCh * 8) k_ln_forward<T, kTpr, kCh, kNr, VEC, VEC><<<grid, kThreads, 0, s>>>(a);  // no bounds to test
-    else k_ln_forward<T, kTpr, kCh, kNr, VEC, false><<<grid, kThreads, 0, s>>>(a);
+    if (VEC && a.cols == kTpr * kCh * 8) launch_after(k_ln_forward<T, kTpr, kCh, kNr, VEC, VEC>, grid, kThreads, s, a);  // no bounds to test
+    else launch_after(k_ln_forward<T, kTpr, kCh, kNr, VEC, false>, grid, kThreads, s, a);
   };
   using std::integral_constant;
   using One = integral_constant<int, 1>;
@@ -616,7 +620,7 @@ void launch_forward(const ForwardArgs& a, cudaStream_t s) {
   else if (a.cols <= 2048) up_to_2048();
   else if (a.cols <= 4096) go(integral_constant<int, 256>{}, Two{}, Two{}, 2);
   else if (a.cols <= kForwardCols) go(integral_constant<int, 512>{}, Four{}, One{}, 1);
-  else k_ln_forward_wide<T><<<at_most(a.rows, 8), kLnThreads, 0, s>>>(a);
+  else launch_after(k_ln_forward_wide<T>, at_most(a.rows, 8), kLnThreads, s, a);
 }
 
 // The backward form for a width: threads a row, groups of eight columns a thread.  In 16 bits, read wide, a row has
@@ -663,8 +667,8 @@ template <typename T, bool VEC, bool CODES>
 void launch_backward(const BackwardArgs& a, int parts, cudaStream_t s) {
   with_backward_form<kTwoGroups<T, VEC>>(a.cols, [&](auto tpr, auto ch) {
     constexpr int kTpr = decltype(tpr)::value, kCh = decltype(ch)::value;
-    if (a.add) k_ln_backward<T, kTpr, kCh, VEC, CODES, true><<<parts, kBackThreads<kTpr, kCh>, 0, s>>>(a);
-    else k_ln_backward<T, kTpr, kCh, VEC, CODES, false><<<parts, kBackThreads<kTpr, kCh>, 0, s>>>(a);
+    if (a.add) launch_after(k_ln_backward<T, kTpr, kCh, VEC, CODES, true>, parts, kBackThreads<kTpr, kCh>, s, a);
+    else launch_after(k_ln_backward<T, kTpr, kCh, VEC, CODES, false>, parts, kBackThreads<kTpr, kCh>, s, a);
   });
 }
 
@@ -675,8 +679,8 @@ cudaError_t launch_backward(const BackwardArgs& a, cudaStream_t s) {
   const int parts = vec ? backward_parts<kTwoGroups<T, true>>(a.rows, a.cols) : backward_parts<false>(a.rows, a.cols);
   if (parts == 0) {  // no rows
   } else if (a.cols > kBackwardCols) {
-    k_ln_backward_wide<T><<<at_most(a.rows, 8), kLnThreads, 0, s>>>(a);
-    k_ln_param_wide<T><<<dim3((unsigned)ceil_div(a.cols, kLnThreads), (unsigned)parts), kLnThreads, 0, s>>>(a, ceil_div(a.rows, 64));
+    launch_after(k_ln_backward_wide<T>, at_most(a.rows, 8), kLnThreads, s, a);
+    launch_after(k_ln_param_wide<T>, dim3((unsigned)ceil_div(a.cols, kLnThreads), (unsigned)parts), kLnThreads, s, a, ceil_div(a.rows, 64));
   } else if (vec) {
     if (a.codes) launch_backward<T, true, true>(a, parts, s);
     else launch_backward<T, true, false>(a, parts, s);

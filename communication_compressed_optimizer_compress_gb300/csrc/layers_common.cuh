@@ -380,12 +380,19 @@ __device__ __forceinline__ float warp_max_nan(float v) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// Kernels of one call follow each other with programmatic launches: the next kernel's blocks may start
-// when every block of the one before has started (and there is room), and wait where they need its
-// results.  A kernel that does not need them still waits before it ends, so that the end of a call's last
-// kernel is the end of them all.
+// All kernels of the layers are launched programmatically: a kernel's blocks may be brought up when every block of
+// the one before has called launch_next() or ended, beside its last blocks, and wait_previous() holds them until it is
+// complete and what it wrote is visible.  Every kernel begins with in_turn(), before it reads or writes memory (the
+// column sums behind a product do so at their end), so that a kernel is complete only when all before it are, and no
+// kernel comes up before the last but one is complete.  Behind any other kernel this is an ordinary launch.
+// (Calls back to back: linear on 16 rows, 1024 to 4096, 5.0 us for 6.15; layer norm and restore of 16384 x 1024 24.9 for
+// 29.3.)
 __device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void in_turn() {
+  wait_previous();
+  launch_next();
+}
 
 // Sums of `parts` partial rows of `width` fp32 columns, in a fixed order; columns below `split` go to lo,
 // the others to hi.  A block of 1024 threads has COLS columns, 16 (two sectors of a row, and twice the threads to
@@ -397,7 +404,7 @@ static __global__ void __launch_bounds__(1024) k_sum_parts(const float* __restri
   __shared__ float red[kRows][COLS + 1];
   const int col = threadIdx.x % COLS, row = threadIdx.x / COLS;
   const int64_t c = (int64_t)blockIdx.x * COLS + col;
-  wait_previous();
+  in_turn();
   float s = 0.0f;
   if (c < width) {
 #pragma unroll 8

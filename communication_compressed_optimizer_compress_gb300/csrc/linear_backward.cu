@@ -10,6 +10,7 @@ namespace {
 template <typename T>
 __global__ void __launch_bounds__(256) k_finish_dx(Partials c, int64_t rows, int cols, Kept<T> v, int act, const T* __restrict__ add,
                                                    int64_t ldadd, T* __restrict__ dx, int64_t lddx, T* __restrict__ h, int64_t ldh) {
+  in_turn();
   const int64_t total = rows * cols;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t r = i / cols;
@@ -28,6 +29,7 @@ __global__ void __launch_bounds__(256) k_finish_dx(Partials c, int64_t rows, int
 // h = act(v), rounded to the product's operand type, where dx is not computed beside it
 template <typename T>
 __global__ void __launch_bounds__(256) k_operand(Kept<T> v, int64_t rows, int cols, int act, T* __restrict__ h, int64_t ldh) {
+  in_turn();
   const int64_t total = rows * cols;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t r = i / cols;
@@ -39,6 +41,7 @@ __global__ void __launch_bounds__(256) k_operand(Kept<T> v, int64_t rows, int co
 // dw over the partial sums of a cut contraction
 template <typename G>
 __global__ void __launch_bounds__(256) k_finish_dw(Partials c, int64_t rows, int cols, G* __restrict__ dw) {
+  in_turn();
   const int64_t total = rows * cols;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t r = i / cols;
@@ -56,8 +59,7 @@ __global__ void __launch_bounds__(256) k_colsum_part(const T* __restrict__ dy, i
                                                      float* __restrict__ part, void* db, int grad) {
   __shared__ float red[8][256];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.x * 256;
-  launch_next();
-  if (wait_first) wait_previous();
+  if (wait_first) in_turn();
   for (int64_t run = blockIdx.y; run * kRun < rows; run += gridDim.y) {
     const int64_t end = (run + 1) * kRun < rows ? (run + 1) * kRun : rows;
     float s[8] = {};
@@ -96,7 +98,7 @@ __global__ void __launch_bounds__(256) k_colsum_part(const T* __restrict__ dy, i
     }
     __syncthreads();
   }
-  if (!wait_first && blockIdx.x == 0 && blockIdx.y == 0) wait_previous();
+  if (!wait_first && blockIdx.x == 0 && blockIdx.y == 0) in_turn();
 }
 
 // Takes the workspace; with `run`, enqueues the work too.
@@ -113,8 +115,8 @@ cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, b
   if (a.dx || a.dw) dy = copies.take(ws, a.dy, a.lddy, a.rows, a.out);
   if (a.dx) w = copies.take(ws, a.w, a.ldw, a.out, a.in);
   if (a.dw && !computed) x = copies.take(ws, a.x, a.ldx, a.rows, a.in);
-  if (run) copies.run(s);
-  cudaError_t err = cudaSuccess;
+  cudaError_t err = run ? copies.run(s) : cudaSuccess;
+  if (err != cudaSuccess) return err;
   if (a.dx) {
     const ProductPlan plan = plan_product(sx, sms);
     const Partials part = take_partials(ws, plan, a.rows, a.in);
@@ -134,7 +136,7 @@ cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, b
         e.vec_codes = aligned(a.codes, 16) && a.in % 16 == 0;
         cudaError_t r = make_output(&e.dx, static_cast<T*>(a.dx), a.rows, a.in, a.lddx);
         if (r == cudaSuccess) r = make_output(&e.h, h, a.rows, a.in, ldh);
-        return r == cudaSuccess ? run_product_by<decltype(ctas)::value, false, true>(a.dtype, dy, w, sx, plan, e, copies.n > 0, s) : r;
+        return r == cudaSuccess ? run_product_by<decltype(ctas)::value, false, true>(a.dtype, dy, w, sx, plan, e, s) : r;
       };
       using std::integral_constant;
       using Two = integral_constant<int, 2>;
@@ -155,30 +157,29 @@ cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, b
     } else if (run) {
       PlainEpilogue<float> to{};
       err = to_partials(&to, part, a.in);
-      if (err == cudaSuccess) err = run_product<false, true>(a.dtype, dy, w, sx, plan, to, copies.n > 0, s);
-      k_finish_dx<T><<<flat_grid(a.rows * a.in, 256), 256, 0, s>>>(part, a.rows, (int)a.in, v, a.activation, add, a.ldadd,
+      if (err == cudaSuccess) err = run_product<false, true>(a.dtype, dy, w, sx, plan, to, s);
+      launch_after(k_finish_dx<T>, flat_grid(a.rows * a.in, 256), 256, s, part, a.rows, (int)a.in, v, a.activation, add, a.ldadd,
                                                                    static_cast<T*>(a.dx), a.lddx, h, ldh);
     }
     if (err != cudaSuccess) return err;
   } else if (computed && run) {
-    k_operand<T><<<flat_grid(a.rows * a.in, 256), 256, 0, s>>>(v, a.rows, (int)a.in, a.activation, h, ldh);
+    launch_after(k_operand<T>, flat_grid(a.rows * a.in, 256), 256, s, v, a.rows, (int)a.in, a.activation, h, ldh);
   }
   if (a.dw) {
     const ProductPlan plan = plan_product(sw, sms);
     const Partials part = take_partials(ws, plan, a.out, a.in);
-    const bool chained = copies.n > 0 || a.dx || computed;
     if (run)
       with_grad(a.grad_dtype, a.dw, [&](auto* g) {
         using G = std::remove_pointer_t<decltype(g)>;
         if (plan.splits == 1) {
           PlainEpilogue<G> e{};
           err = make_output(&e.out, g, a.out, a.in, a.in);
-          if (err == cudaSuccess) err = run_product<true, true>(a.dtype, dy, x, sw, plan, e, chained, s);
+          if (err == cudaSuccess) err = run_product<true, true>(a.dtype, dy, x, sw, plan, e, s);
         } else {
           PlainEpilogue<float> to{};
           err = to_partials(&to, part, a.in);
-          if (err == cudaSuccess) err = run_product<true, true>(a.dtype, dy, x, sw, plan, to, chained, s);
-          k_finish_dw<<<flat_grid(a.out * a.in, 256), 256, 0, s>>>(part, a.out, (int)a.in, g);
+          if (err == cudaSuccess) err = run_product<true, true>(a.dtype, dy, x, sw, plan, to, s);
+          launch_after(k_finish_dw<G>, flat_grid(a.out * a.in, 256), 256, s, part, a.out, (int)a.in, g);
         }
       });
     if (err != cudaSuccess) return err;

@@ -48,9 +48,9 @@ struct Realigns {
   Realign m[3];
 };
 static __global__ void __launch_bounds__(256) k_realign(const Realigns all) {
+  in_turn();
   const Realign& a = all.m[blockIdx.y];
   const int64_t per = a.ld / 8, total = a.rows * per;
-  launch_next();
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t r = i / per;
     const int c = (int)(i - r * per) * 8;
@@ -77,8 +77,8 @@ struct Readable {
     if (rows * ldc / 8 > most) most = rows * ldc / 8;
     return {c, ldc};
   }
-  void run(cudaStream_t s) const {
-    if (n) k_realign<<<dim3(flat_grid(most, 256), (unsigned)n), 256, 0, s>>>(all);
+  cudaError_t run(cudaStream_t s) const {
+    return n == 0 ? cudaSuccess : launch_after(k_realign, dim3(flat_grid(most, 256), (unsigned)n), 256, s, all);
   }
 };
 

@@ -9,6 +9,7 @@ namespace {
 // The epilogue over the partial sums of a cut contraction, one warp per 64 columns of a row.
 template <typename T>
 __global__ void __launch_bounds__(256) k_finish_forward(Partials c, int64_t rows, int cols, const __grid_constant__ ForwardEpilogue<T, kAny, kAny, kAny> e) {
+  in_turn();
   const int lane = threadIdx.x & 31;
   const int64_t units = rows * e.blocks, step = (int64_t)gridDim.x * 8;
   for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < units; u += step) {
@@ -46,24 +47,25 @@ cudaError_t forward(const onebit_linear_t& a, Space& ws, cudaStream_t s, bool ru
   const Operand x = copies.take(ws, a.x, a.ldx, a.rows, a.in), w = copies.take(ws, a.w, a.ldw, a.out, a.in);
   const Partials part = take_partials(ws, plan, a.rows, a.out);
   if (!run) return cudaSuccess;
-  copies.run(s);
+  cudaError_t err = copies.run(s);
+  if (err != cudaSuccess) return err;
   ForwardEpilogue<T, kAny, kAny, kAny> e{};
   e.bias = a.bias;
   e.residual = make_input<T>(a.residual, a.ldr);
   e.scales = a.scales;
   e.blocks = (int)ceil_div(a.out, kBlock);
   e.act = a.activation;
-  cudaError_t err = make_output(&e.y, static_cast<T*>(a.y), a.rows, a.out, a.ldy);
+  err = make_output(&e.y, static_cast<T*>(a.y), a.rows, a.out, a.ldy);
   if (err == cudaSuccess) err = make_output(&e.codes, a.codes, a.rows, a.out, a.out);
   if (err != cudaSuccess) return err;
-  if (plan.splits == 1 && plan.ctas == 1) return run_product_by<1, false, false>(a.dtype, x, w, shape, plan, e, copies.n > 0, s);
+  if (plan.splits == 1 && plan.ctas == 1) return run_product_by<1, false, false>(a.dtype, x, w, shape, plan, e, s);
   if (plan.splits == 1) {
     using std::integral_constant;
     using Any = integral_constant<int, kAny>;
     auto go = [&](auto act, auto ck, auto res) {
       ForwardEpilogue<T, decltype(act)::value, decltype(ck)::value, decltype(res)::value> f{};
       f.bias = e.bias, f.residual = e.residual, f.y = e.y, f.codes = e.codes, f.scales = e.scales, f.blocks = e.blocks, f.act = e.act;
-      return run_product_by<2, false, false>(a.dtype, x, w, shape, plan, f, copies.n > 0, s);
+      return run_product_by<2, false, false>(a.dtype, x, w, shape, plan, f, s);
     };
     using No = integral_constant<int, 0>;
     using Yes = integral_constant<int, 1>;
@@ -81,9 +83,9 @@ cudaError_t forward(const onebit_linear_t& a, Space& ws, cudaStream_t s, bool ru
   }
   PlainEpilogue<float> to{};
   err = to_partials(&to, part, a.out);
-  if (err == cudaSuccess) err = run_product<false, false>(a.dtype, x, w, shape, plan, to, copies.n > 0, s);
+  if (err == cudaSuccess) err = run_product<false, false>(a.dtype, x, w, shape, plan, to, s);
   if (err != cudaSuccess) return err;
-  k_finish_forward<T><<<flat_grid(a.rows * e.blocks * 32, 256), 256, 0, s>>>(part, a.rows, (int)a.out, e);
+  launch_after(k_finish_forward<T>, flat_grid(a.rows * e.blocks * 32, 256), 256, s, part, a.rows, (int)a.out, e);
   return cudaGetLastError();
 }
 cudaError_t forward(const onebit_linear_t& a, Space& ws, cudaStream_t s, bool run) {

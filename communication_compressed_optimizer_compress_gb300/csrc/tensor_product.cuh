@@ -836,9 +836,7 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
   if (CTAS == 2) cluster_sync();  // the other block's barriers are ready too
   tmem_fence_after();
   const uint32_t tmem = *tmem_ptr;
-  // behind another kernel of the call the setup ran beside its last blocks; nothing it writes is touched before here
-  wait_previous();
-  launch_next();
+  in_turn();  // the setup has run beside the last blocks of the kernel before
 
   // a pair's epilogue warps take the registers that its control warps do not need
   if (warp >= 4) {
@@ -1031,7 +1029,7 @@ struct Operand {
 };
 
 template <int CTAS, bool A_MN, bool B_MN, class Epilogue>
-cudaError_t launch_product(const ProductArgs& P, const Epilogue& E, int sms, bool chained, cudaStream_t s) {
+cudaError_t launch_product(const ProductArgs& P, const Epilogue& E, int sms, cudaStream_t s) {
   auto* kernel = k_product<CTAS, A_MN, B_MN, Epilogue>;
   static std::atomic<uint64_t> ready{0};  // devices on which this kernel may use its shared memory
   int dev = 0;
@@ -1056,15 +1054,14 @@ cudaError_t launch_product(const ProductArgs& P, const Epilogue& E, int sms, boo
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = chained ? 2 : 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, P, E);
 }
 
 // C = A B^T by `plan`, through epilogue E.  A: m x k (or k x m with A_MN), B: n x k (or k x n with B_MN).
-// `chained`: behind a kernel of the same call, whose last blocks this one's setup may run beside.
 template <int CTAS, bool A_MN, bool B_MN, class Epilogue>
 cudaError_t run_product_by(int32_t dtype, const Operand& a, const Operand& b, const ProductShape& s, const ProductPlan& plan, const Epilogue& E,
-                           bool chained, cudaStream_t stream) {
+                           cudaStream_t stream) {
   ProductArgs P{};
   cudaError_t e = make_map(&P.a, dtype, a.p, A_MN ? s.k : s.m, A_MN ? s.m : s.k, a.ld, A_MN ? 64 : 128);
   if (e == cudaSuccess) e = make_map(&P.b, dtype, b.p, B_MN ? s.k : s.n, B_MN ? s.n : s.k, b.ld, B_MN ? 64 : 128);
@@ -1088,13 +1085,13 @@ cudaError_t run_product_by(int32_t dtype, const Operand& a, const Operand& b, co
   P.stall_tx = stall_bytes();
   P.status = status_word();
   if (!P.status) return cudaErrorUnknown;
-  return launch_product<CTAS, A_MN, B_MN>(P, E, sm_count(), chained, stream);
+  return launch_product<CTAS, A_MN, B_MN>(P, E, sm_count(), stream);
 }
 template <bool A_MN, bool B_MN, class Epilogue>
 cudaError_t run_product(int32_t dtype, const Operand& a, const Operand& b, const ProductShape& s, const ProductPlan& plan, const Epilogue& E,
-                        bool chained, cudaStream_t stream) {
-  return plan.ctas == 2 ? run_product_by<2, A_MN, B_MN>(dtype, a, b, s, plan, E, chained, stream)
-                        : run_product_by<1, A_MN, B_MN>(dtype, a, b, s, plan, E, chained, stream);
+                        cudaStream_t stream) {
+  return plan.ctas == 2 ? run_product_by<2, A_MN, B_MN>(dtype, a, b, s, plan, E, stream)
+                        : run_product_by<1, A_MN, B_MN>(dtype, a, b, s, plan, E, stream);
 }
 
 }  // namespace layers

@@ -90,3 +90,62 @@ def test_single_tokens(ff, rows):
     block, x, _, exact, x64 = _block(ff, 256, 1024, rows, torch.bfloat16, 11)
     with torch.no_grad():
         assert _rel(block(x), _formula(exact, x64)) < 3 * 2.0 ** -8
+
+
+def _steps(ff, hidden, inner, rows, n):
+    """n steps that each read what the one before wrote, in the same buffers."""
+    block, x, dy, _, _ = _block(ff, hidden, inner, rows, torch.bfloat16, 21)
+    grads = [torch.empty_like(p) for p in block.parameters()]
+    for _ in range(n):
+        y, kept = block.forward(x)
+        dx = block.backward(dy, kept, grads, torch.float32)
+        x.sub_(dx, alpha=0.5)
+        dy.copy_(y)
+        for p, g in zip(block.parameters(), grads):
+            p.sub_(g, alpha=1e-4)
+        block.weights_changed()
+    return [x, dy] + grads
+
+
+@pytest.mark.parametrize("hidden,inner,rows", [(1024, 4096, 2048), (72, 200, 33), (100, 250, 700), (256, 1024, 16)])
+def test_kernels_that_follow_each_other(ff, monkeypatch, hidden, inner, rows):
+    # a kernel comes up beside the last blocks of the one before: the results are those of kernels one at a time
+    got = _steps(ff, hidden, inner, rows, 8)
+    torch.cuda.synchronize()
+    for name in ("compress", "layer_norm", "layer_norm_backward", "linear", "linear_backward"):
+        def alone(*a, f=getattr(ff.layers, name), **k):
+            torch.cuda.synchronize()
+            r = f(*a, **k)
+            torch.cuda.synchronize()
+            return r
+        monkeypatch.setattr(ff.layers, name, alone)
+    assert all(torch.equal(a, b) for a, b in zip(got, _steps(ff, hidden, inner, rows, 8)))
+
+
+def test_graph_with_a_second_stream(ff):
+    # a captured call behind two streams' work, and one behind a copy
+    block, x, dy, _, _ = _block(ff, 256, 1024, 512, torch.bfloat16, 31)
+    other, kept = x.flip(0), torch.empty_like(x)
+
+    def run(side):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            a = ff.layers.linear(other, block.low1, block.b1)
+        b = ff.layers.linear(x, block.low1, block.b1, ff.layers.ACT_RELU)
+        torch.cuda.current_stream().wait_stream(side)
+        s = ff.layers.linear(b, block.low2, residual=x)
+        kept.copy_(s)
+        return ff.layers.layer_norm(kept, block.gamma, block.beta)[0], ff.layers.linear(a, block.low2)
+
+    want = run(torch.cuda.Stream())
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        got = run(side)
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        kept.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
