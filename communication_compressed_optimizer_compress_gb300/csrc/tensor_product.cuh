@@ -7,8 +7,8 @@
 //
 // One block (or a pair of blocks on neighbouring SMs) computes a tile of 128 (256) rows by 128 (256)
 // columns at a time.  Warp 0 copies operand slabs of 64 contraction elements into a ring of shared
-// memory stages with TMA; warp 1 issues the tensor-core instructions; eight warps read finished
-// accumulators out of tensor memory and run the epilogue.  Two accumulators alternate, so that the
+// memory stages with TMA; warp 1 issues the tensor-core instructions; eight warps (a pair's block:
+// sixteen) read finished accumulators out of tensor memory and run the epilogue.  Two accumulators alternate, so that the
 // epilogue of one tile runs under the products of the next.  In a pair each block holds half of A's
 // rows and half of B's, and the even block's instructions use both halves: each SM's shared memory
 // then feeds a 256x256 tile with the traffic of a 128x128 one.
@@ -316,7 +316,7 @@ __device__ __forceinline__ void store_rows(char* staging, const uint32_t (&v)[16
 
 // A matrix that an epilogue reads.  Where its rows start on 32 bytes a lane reads its own row, whole sectors at a
 // time, half of its 64 columns ahead: the first before the product is waited for, the second under the first
-// one's arithmetic (through the staging buffer and waited for at once: 2.6 us a tile).
+// one's arithmetic (16384 x 1024 x 4096 through gelu' from codes: 117 us, 128 through the staging buffer).
 template <typename T>
 struct Input16 {
   const T* p;
@@ -468,8 +468,9 @@ __device__ __forceinline__ void load_codes(char* staging, uint32_t (&v)[8], cons
 // ------------------------------------------------------------------------------------------------
 // Epilogues.  A lane has row row0 + lane.  run() of the fused ones reads the warp's 64 columns from col0 on
 // out of tensor memory, 32 at a time, by load(half, pairs), and calls release() after the last read: a rolled
-// loop over the halves, with few registers and little code, lets sixteen warps run side by side (eight warps
-// with all 64 columns in registers: 2.2 times the time at 9728 x 1024 x 4096 with gelu and checkpoint).
+// loop over the halves, with few registers and little code, lets sixteen warps run side by side.  (Eight warps of
+// 232 registers that hold all 64 columns are no faster: 8.4 us a pair's tile of 1024 terms with gelu and checkpoint
+// for 8.5, and 9.4 for 9.1 in the input's gradient.)
 
 // The activation's constants, read once for 32 columns (volatile: as literals, or kept longer than that, they
 // cost more registers or instructions than these few loads).
@@ -494,7 +495,6 @@ template <typename T, int ACT, int CK, int RES>
 struct ForwardEpilogue {
   // y = act(d + bias) + residual, and the 8-bit checkpoint of d + bias
   static constexpr bool kFold = false;
-  static constexpr bool kAhead = ACT == ONEBIT_ACT_NONE && RES == 1;  // a residual's first columns are fetched ahead
   const float* bias;
   Input16<T> residual;
   Output<T> y;
@@ -505,24 +505,18 @@ struct ForwardEpilogue {
 
   __device__ __forceinline__ bool keeps() const { return CK == kAny ? scales != nullptr : CK == 1; }
   __device__ __forceinline__ bool adds() const { return RES == kAny ? residual.p != nullptr : RES == 1; }
-  // or brought to the staging buffer while the product runs (1237 x 1001 x 777 in odd rows: 18.3 -> 16.3 us with the
-  // setup beside the realigning kernel)
-  static constexpr bool kStaged = RES == kAny;
-  struct Ahead {
-    uint32_t v[kAhead ? 16 : 1];
-  };
+  struct Ahead {};
   // before the product is waited for: the warp's 64 columns of the bias, two a lane (without one: zeros, as adding
-  // them is cheaper than both ways meeting behind a branch), and the residual's first 32
-  __device__ __forceinline__ void prepare(Ahead& a, int64_t row0, int64_t rows, int col0, int cols, char* staging) const {
-    if constexpr (kAhead) residual.ahead(row0 + (threadIdx.x & 31), rows, col0, cols, a.v);
+  // them is cheaper than both ways meeting behind a branch), and the residual's first 32 to the staging buffer
+  // (1237 x 1001 x 777 in odd rows: 18.3 -> 16.3 us with the setup beside the realigning kernel; ahead in registers it
+  // is no faster: 16384 x 4096 x 1024 98.9 us for 98.1)
+  __device__ __forceinline__ void prepare(Ahead&, int64_t row0, int64_t rows, int col0, int cols, char* staging) const {
     const int c = col0 + 2 * (threadIdx.x & 31);
     f2 b = 0;
     if (bias) b = pair(c < cols ? __ldg(bias + c) : 0.0f, c + 1 < cols ? __ldg(bias + c + 1) : 0.0f);
     reinterpret_cast<f2*>(staging + kBiasStaging)[threadIdx.x & 31] = b;
     __syncwarp();
-    if constexpr (kStaged) {
-      if (adds()) fetch_rows(staging, residual.p, residual.ld, row0, rows, col0, cols, residual.vec);
-    }
+    if (adds()) fetch_rows(staging, residual.p, residual.ld, row0, rows, col0, cols, residual.vec);
   }
   __device__ __forceinline__ void add_bias(f2 (&z)[16], int half, const char* staging) const {
     const ulonglong2* b = reinterpret_cast<const ulonglong2*>(staging + kBiasStaging + 128 * half);
@@ -544,7 +538,7 @@ struct ForwardEpilogue {
     }
   }
   template <class Load, class Release>
-  __device__ __forceinline__ void run(Ahead& ahead, Load&& load, Release&& release, const f2* consts, int64_t row0, int64_t rows, int col0,
+  __device__ __forceinline__ void run(Ahead&, Load&& load, Release&& release, const f2* consts, int64_t row0, int64_t rows, int col0,
                                       int cols, char* staging) const {
     float inv = 0.0f;
     bool plain = true;  // no value of the warp's blocks is infinite or NaN
@@ -582,17 +576,8 @@ struct ForwardEpilogue {
         }
       }
       if (adds()) {
-        if (kAhead && residual.wide && c0 + 32 <= cols) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = ahead.v[kAhead ? i : 0];
-          if constexpr (kAhead) {
-            if (!half) residual.ahead(row0 + (threadIdx.x & 31), rows, c0 + 32, cols, ahead.v);
-          }
-        } else if (kStaged && !half) {
-          take_rows(staging, v);
-        } else {
-          load_rows(staging, v, residual.p, residual.ld, row0, rows, c0, cols, residual.vec);
-        }
+        if (!half) take_rows(staging, v);
+        else load_rows(staging, v, residual.p, residual.ld, row0, rows, c0, cols, residual.vec);
       }
       if constexpr (ACT != kAny) finish<ACT>(consts, z, v);
       else if (act == ONEBIT_ACT_NONE) finish<ONEBIT_ACT_NONE>(consts, z, v);
