@@ -125,14 +125,16 @@ struct ForwardArgs {
 };
 
 template <int TPR>
-constexpr int kForwardThreads = TPR < 128 ? 128 : TPR;
+constexpr int kForwardThreads = TPR < 128 ? 128 / TPR * TPR : TPR;
+template <typename T, int TPR, int CH, bool VEC>
+constexpr int kForwardRoom = VEC && sizeof(T) == 2 && CH == 1 && TPR > 64 ? 1024 : TPR < 256 ? 640 : 512;  // threads an SM
 
-// NR rows at a time: their sums go through the shuffles and the barrier together, and gamma and beta are
-// read (from L1) once for them.  Bound by instruction issue first and by DRAM next: fewer threads with more
-// columns each pay the fixed cost of a row less often.  16384 x 1024 bf16 with the checkpoint: one block of
-// 128 threads a row 28 us, a warp a row 26 us (gamma and beta took 62% of the L1's cycles).
+// NR rows at a time: their sums go through the shuffles and the barrier together.  gamma and beta stay in registers
+// where they fit beside the rows; elsewhere they are read (from L1) once for the NR rows.  16384 x 1024 bf16 with the
+// checkpoint: a warp a row, which reads them for every row, 18.6 us (62% of the L1's cycles), 128 threads a row that hold
+// them 17.2, at 1024 threads an SM (18.5 at 640); 33 rows 2.7 and 2.1 us.
 template <typename T, int TPR, int CH, int NR, bool VEC, bool FULL>
-__global__ void __launch_bounds__(kForwardThreads<TPR>, (TPR < 256 ? 640 : 512) / kForwardThreads<TPR>) k_ln_forward(const ForwardArgs A) {
+__global__ void __launch_bounds__(kForwardThreads<TPR>, kForwardRoom<T, TPR, CH, VEC> / kForwardThreads<TPR>) k_ln_forward(const ForwardArgs A) {
   in_turn();
   constexpr int kGroups = kForwardThreads<TPR> / TPR;
   const int cols = FULL ? TPR * CH * 8 : A.cols;
@@ -150,6 +152,17 @@ __global__ void __launch_bounds__(kForwardThreads<TPR>, (TPR < 256 ? 640 : 512) 
       if (r + n < A.rows) in[n].load(px + n * A.ldx, t, cols);
   };
   load(first);
+  // (in the single-element forms they would spill: 16384 x 1155 bf16 with the checkpoint 60 us for 48.5; in the wide form
+  // of 2048 columns 17.7 for 17.1)
+  constexpr bool kHold = VEC && (CH == 1 || (CH == 2 && TPR == 256 && sizeof(T) == 2));
+  f2 gs[kHold ? CH : 1][4], bs[kHold ? CH : 1][4];
+  if (kHold) {
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      param_group<TPR, VEC>(A.gamma, t, j, cols, gs[kHold ? j : 0]);
+      param_group<TPR, VEC>(A.beta, t, j, cols, bs[kHold ? j : 0]);
+    }
+  }
   for (int64_t r = first; r < A.rows; r += step) {
     f2 x[NR][CH][4];
     float mean[NR], rstd[NR];
@@ -234,8 +247,13 @@ __global__ void __launch_bounds__(kForwardThreads<TPR>, (TPR < 256 ? 640 : 512) 
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
       f2 g[4], b[4];
-      param_group<TPR, VEC>(A.gamma, t, j, cols, g);
-      param_group<TPR, VEC>(A.beta, t, j, cols, b);
+      if (kHold) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) g[e] = gs[kHold ? j : 0][e], b[e] = bs[kHold ? j : 0][e];
+      } else {
+        param_group<TPR, VEC>(A.gamma, t, j, cols, g);
+        param_group<TPR, VEC>(A.beta, t, j, cols, b);
+      }
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
         f2 y[4];
@@ -392,8 +410,8 @@ __global__ void __launch_bounds__(kBackThreads<TPR, CH>, kBackRoom<CH> / kBackTh
     rs = __ldg(A.rstd + r);
   };
   if (first < A.rows) load(first);
-  // gamma stays in the registers that `add` would need, where there is one group of columns
-  constexpr bool kHold = !ADD && CH == 1;
+  // gamma stays in the registers that `add` would need, or that the wide form has with one group of columns
+  constexpr bool kHold = !ADD || (VEC && CH == 1);
   f2 held[kHold ? CH : 1][4];
   if (kHold) {
 #pragma unroll
@@ -603,7 +621,9 @@ void launch_forward(const ForwardArgs& a, cudaStream_t s) {
   // sixteen columns each; 16384 x 1024 wide fp32: 23.9 with 128, 28.1 with a warp, but 8192 x 2048 28.5 and 24.5).
   auto up_to_2048 = [&] {
     if constexpr (kLean) {
-      if (a.cols <= 1024) return go(integral_constant<int, 32>{}, Four{}, One{}, 5);
+      if (a.cols <= 512) return go(integral_constant<int, 32>{}, Four{}, One{}, 5);
+      if (a.cols <= 768) return go(integral_constant<int, 96>{}, One{}, Two{}, 10);
+      if (a.cols <= 1024) return go(integral_constant<int, 128>{}, One{}, Two{}, 8);
     } else {
       if (a.cols <= 512) return go(integral_constant<int, 64>{}, One{}, Two{}, 5);
       if (a.cols <= 1024) return go(integral_constant<int, 128>{}, One{}, Two{}, 5);
@@ -623,8 +643,9 @@ void launch_forward(const ForwardArgs& a, cudaStream_t s) {
   else launch_after(k_ln_forward_wide<T>, at_most(a.rows, 8), kLnThreads, s, a);
 }
 
-// The backward form for a width: threads a row, groups of eight columns a thread.  In 16 bits, read wide, a row has
-// few threads with two groups each; single elements and fp32 need more registers a column, so there a thread has one
+// The backward form for a width: threads a row, groups of eight columns a thread.  In 16 bits, read wide, a row of
+// more than 512 columns has few threads with two groups each (16384 x 1024 bf16 24.6 us, 27.4 with one; x 512 18.7 and
+// 16.8); single elements and fp32 need more registers a column, so there a thread has one
 // group and a row the fewest warps that hold it (16384 x 1024 fp32 with two groups a thread spilled; 4099 x 1155 fp32
 // by single elements 20.8 us with 160 threads a row, 23.3 with 256).
 template <typename T, bool VEC>
@@ -635,12 +656,12 @@ void with_backward_form(int64_t cols, F&& f) {
   using One = integral_constant<int, 1>;
   using Two = integral_constant<int, 2>;
   if (cols <= 256) return f(integral_constant<int, 32>{}, One{});
+  if (cols <= 512) return f(integral_constant<int, 64>{}, One{});
   if constexpr (TWO) {
     if (cols <= 1024) return f(integral_constant<int, 64>{}, Two{});
     if (cols <= 2048) return f(integral_constant<int, 128>{}, Two{});
     if (cols <= 4096) return f(integral_constant<int, 256>{}, Two{});
   } else {
-    if (cols <= 512) return f(integral_constant<int, 64>{}, One{});
     if (cols <= 1024) return f(integral_constant<int, 128>{}, One{});
     if (cols <= 1280) return f(integral_constant<int, 160>{}, One{});
     if (cols <= 1536) return f(integral_constant<int, 192>{}, One{});
