@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kBackThreads<TPR, CH>, kBackRoom<CH> / kBackTh
 #pragma unroll
     for (int e = 0; e < 4; ++e) dg[j][e] = db[j][e] = 0;
   KeptRow<T, TPR, CH, VEC, CODES> kept(A, first, step);
-  RowInput<T, TPR, CH, VEC> dyin, addin, addnow;
+  RowInput<T, TPR, CH, VEC> dyin, addin;
   const T *pdy = static_cast<const T*>(A.dy) + first * A.lddy, *padd = static_cast<const T*>(A.add) + (ADD ? first * A.ldadd : 0);
   T* pdx = static_cast<T*>(A.dx) + first * A.lddx;
   float mu = 0.0f, rs = 0.0f;
@@ -402,16 +402,13 @@ __global__ void __launch_bounds__(kBackThreads<TPR, CH>, kBackRoom<CH> / kBackTh
     kept.load(t, cols);
     dyin.load(pdy, t, cols);
     pdy += step * A.lddy;
-    if (ADD) {
-      addin.load(padd, t, cols);
-      padd += step * A.ldadd;
-    }
     mu = __ldg(A.mean + r);
     rs = __ldg(A.rstd + r);
   };
   if (first < A.rows) load(first);
-  // gamma stays in the registers that `add` would need, or that the wide form has with one group of columns
-  constexpr bool kHold = !ADD || (VEC && CH == 1);
+  // gamma stays in registers, but beside codes and `add` only in the wide form of one group (16384 x 1155 bf16: held
+  // 69.5 us, read for every row 52.0; 16384 x 1024 30.4 and 27.5)
+  constexpr bool kHold = !ADD || !CODES || (VEC && CH == 1);
   f2 held[kHold ? CH : 1][4];
   if (kHold) {
 #pragma unroll
@@ -425,7 +422,10 @@ __global__ void __launch_bounds__(kBackThreads<TPR, CH>, kBackRoom<CH> / kBackTh
       kept.normal(j, rstd, shift, xh[j]);
       dyin.expand(j, d[j]);
     }
-    addnow = addin;
+    if (ADD) {  // needed last: this row's, not ahead
+      addin.load(padd, t, cols);
+      padd += step * A.ldadd;
+    }
     if (r + step < A.rows) load(r + step);  // under this row's work
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(kBackThreads<TPR, CH>, kBackRoom<CH> / kBackTh
       for (int e = 0; e < 4; ++e) o[e] = fma2(xh[j][e], c1, fma2(d[j][e], splat(rstd), c0));
       if (ADD) {
         f2 a[4];
-        addnow.expand(j, a);
+        addin.expand(j, a);
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] = add2(o[e], a[e]);
       }
