@@ -11,18 +11,24 @@ template <typename T>
 __global__ void __launch_bounds__(256) k_finish_dx(Partials c, int64_t rows, int cols, Kept<T> v, int act, const T* __restrict__ add,
                                                    int64_t ldadd, T* __restrict__ dx, int64_t lddx, T* __restrict__ h, int64_t ldh) {
   in_turn();
-  const int64_t total = rows * cols;
+  const int64_t per = c.ld / 4, total = rows * per;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / cols;
-    const int col = (int)(i - r * cols);
-    float d = c.at(r, col);
-    if (act != ONEBIT_ACT_NONE || h) {
-      const float2 p = act_both(act, v.at(r, col));
-      d *= p.y;
-      if (h) h[r * ldh + col] = from_f<T>(p.x);
+    const int64_t r = i / per;
+    const int c0 = (int)(i - r * per) * 4;
+    float d[4];
+    c.at4(r, c0, d);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int col = c0 + q;
+      if (col >= cols) break;
+      if (act != ONEBIT_ACT_NONE || h) {
+        const float2 p = act_both(act, v.at(r, col));
+        d[q] *= p.y;
+        if (h) h[r * ldh + col] = from_f<T>(p.x);
+      }
+      if (add) d[q] += to_f(add[r * ldadd + col]);
+      dx[r * lddx + col] = from_f<T>(d[q]);
     }
-    if (add) d += to_f(add[r * ldadd + col]);
-    dx[r * lddx + col] = from_f<T>(d);
   }
 }
 
@@ -38,14 +44,20 @@ __global__ void __launch_bounds__(256) k_operand(Kept<T> v, int64_t rows, int co
   }
 }
 
-// dw over the partial sums of a cut contraction
+// dw over the partial sums of a cut contraction, four columns a thread
 template <typename G>
 __global__ void __launch_bounds__(256) k_finish_dw(Partials c, int64_t rows, int cols, G* __restrict__ dw) {
   in_turn();
-  const int64_t total = rows * cols;
+  const int64_t per = c.ld / 4, total = rows * per;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / cols;
-    dw[i] = from_f<G>(c.at(r, (int)(i - r * cols)));
+    const int64_t r = i / per;
+    const int c0 = (int)(i - r * per) * 4;
+    float s[4];
+    c.at4(r, c0, s);
+    G* p = dw + r * cols + c0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (c0 + q < cols) p[q] = from_f<G>(s[q]);
   }
 }
 
@@ -158,7 +170,7 @@ cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, b
       PlainEpilogue<float> to{};
       err = to_partials(&to, part, a.in);
       if (err == cudaSuccess) err = run_product<false, true>(a.dtype, dy, w, sx, plan, to, s);
-      launch_after(k_finish_dx<T>, flat_grid(a.rows * a.in, 256), 256, s, part, a.rows, (int)a.in, v, a.activation, add, a.ldadd,
+      launch_after(k_finish_dx<T>, flat_grid(a.rows * (part.ld / 4), 256), 256, s, part, a.rows, (int)a.in, v, a.activation, add, a.ldadd,
                                                                    static_cast<T*>(a.dx), a.lddx, h, ldh);
     }
     if (err != cudaSuccess) return err;
@@ -179,7 +191,7 @@ cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, b
           PlainEpilogue<float> to{};
           err = to_partials(&to, part, a.in);
           if (err == cudaSuccess) err = run_product<true, true>(a.dtype, dy, x, sw, plan, to, s);
-          launch_after(k_finish_dw<G>, flat_grid(a.out * a.in, 256), 256, s, part, a.out, (int)a.in, g);
+          launch_after(k_finish_dw<G>, flat_grid(a.out * (part.ld / 4), 256), 256, s, part, a.out, (int)a.in, g);
         }
       });
     if (err != cudaSuccess) return err;

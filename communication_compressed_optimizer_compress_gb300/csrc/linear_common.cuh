@@ -105,6 +105,17 @@ struct Partials {
     for (int i = 1; i < splits; ++i) s += p[i * split_stride + r * ld + c];
     return s;
   }
+  // columns c to c + 3, c a multiple of 4 (a row's end is padded to that)
+  __device__ __forceinline__ void at4(int64_t r, int c, float (&s)[4]) const {
+    const float* q = p + r * ld + c;
+    float4 t = *reinterpret_cast<const float4*>(q);
+#pragma unroll 4
+    for (int i = 1; i < splits; ++i) {
+      const float4 u = *reinterpret_cast<const float4*>(q + i * split_stride);
+      t.x += u.x, t.y += u.y, t.z += u.z, t.w += u.w;
+    }
+    s[0] = t.x, s[1] = t.y, s[2] = t.z, s[3] = t.w;
+  }
 };
 inline Partials take_partials(Space& ws, const ProductPlan& plan, int64_t rows, int64_t cols) {
   Partials q{};
