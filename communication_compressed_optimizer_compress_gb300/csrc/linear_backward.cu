@@ -64,7 +64,8 @@ __global__ void __launch_bounds__(256) k_finish_dw(Partials c, int64_t rows, int
 // Column sums of dy over runs of kRun rows: a block has 256 columns, eight threads (one of each warp) to
 // every eight columns.  Behind a product of the same call it starts at once and reads dy on the SMs that
 // the product's tiles leave idle (dy was complete before the product began); one block then waits for the
-// product, so that this kernel ends after it.  As the call's first kernel it waits before it reads.
+// product, so that this kernel ends after it.  As the call's first kernel it waits before it reads.  Bound by the bytes
+// of dy and the SMs that are idle: 16384 x 1024 in 23 us alone, under dw's 92.
 constexpr int kRun = 512;
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) k_colsum_part(const T* __restrict__ dy, int64_t lddy, int64_t rows, int cols, bool wait_first,
