@@ -666,7 +666,7 @@ void with_backward_form(int64_t cols, F&& f) {
     if (cols <= 1280) return f(integral_constant<int, 160>{}, One{});
     if (cols <= 1536) return f(integral_constant<int, 192>{}, One{});
     if (cols <= 2048) return f(integral_constant<int, 256>{}, One{});
-    if (cols <= 3072) return f(integral_constant<int, 384>{}, One{});
+    if (cols <= 384 * 8) return f(integral_constant<int, 384>{}, One{});
     if (cols <= 4096) return f(integral_constant<int, 512>{}, One{});
   }
   f(integral_constant<int, 512>{}, Two{});
