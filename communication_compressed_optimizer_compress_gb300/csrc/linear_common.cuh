@@ -37,7 +37,9 @@ struct Space {
 };
 
 // Rows of any alignment into rows of ld = pad8(cols) on 16 bytes (the columns past the end are not read).  Up to
-// three matrices in one launch, one to each blockIdx.y.  Latency of a launch: 3 us for 1237 x 1001 and 777 x 1001.
+// three matrices in one launch, one to each blockIdx.y.  Inside a row by whole words, shifted where the columns lie across
+// them (linear of 4144 x 3136 x 416 in odd rows 24.8 us, 28.8 by single elements).  Latency of a launch for small
+// matrices: 3 us for 1237 x 1001 and 777 x 1001.
 struct Realign {
   const uint16_t* x;
   int64_t ldx, rows, ld;
@@ -55,10 +57,22 @@ static __global__ void __launch_bounds__(256) k_realign(const Realigns all) {
     const int64_t r = i / per;
     const int c = (int)(i - r * per) * 8;
     uint32_t v[4];
+    const uint16_t* const x = a.x + r * a.ldx + c;
+    if (c > 0 && c + 8 < a.cols) {  // whole words, which hold columns c - 1 to c + 8 where the columns lie across them
+      const bool across = reinterpret_cast<uintptr_t>(x) & 2;
+      const uint32_t* const w = reinterpret_cast<const uint32_t*>(x - across);
+      uint32_t t[5];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint32_t lo = c + 2 * q < a.cols ? a.x[r * a.ldx + c + 2 * q] : 0, hi = c + 2 * q + 1 < a.cols ? a.x[r * a.ldx + c + 2 * q + 1] : 0;
-      v[q] = lo | hi << 16;
+      for (int q = 0; q < 4; ++q) t[q] = w[q];
+      t[4] = across ? w[4] : 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = across ? __funnelshift_r(t[q], t[q + 1], 16) : t[q];
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t lo = c + 2 * q < a.cols ? x[2 * q] : 0, hi = c + 2 * q + 1 < a.cols ? x[2 * q + 1] : 0;
+        v[q] = lo | hi << 16;
+      }
     }
     *reinterpret_cast<uint4*>(a.out + r * a.ld + c) = make_uint4(v[0], v[1], v[2], v[3]);
   }
