@@ -13,8 +13,8 @@ namespace {
 // the same columns of every row that it meets, so that the parameters' gradients add up in registers too).  Widths are
 // served by the narrowest of the forms below; a wider row than the widest takes the re-reading kernels.
 //
-// In the wide form (VEC: rows on 16 bytes, a multiple of eight columns) a group is eight columns that lie
-// together; otherwise it is columns lane and lane + 32 of four runs of 64, so that single-element accesses
+// In the wide form (VEC: rows, gamma and beta on 16 bytes, a multiple of eight columns) a group is eight columns that
+// lie together; otherwise it is columns lane and lane + 32 of four runs of 64, so that single-element accesses
 // of a warp are contiguous and a run is still one block of the 8-bit checkpoint.
 template <int TPR, bool VEC>
 struct Columns {
@@ -696,7 +696,8 @@ void launch_backward(const BackwardArgs& a, int parts, cudaStream_t s) {
 template <typename T>
 cudaError_t launch_backward(const BackwardArgs& a, cudaStream_t s) {
   auto on16 = [](const void* p, int64_t ld) { return aligned(p, 16) && (ld * (int64_t)sizeof(T)) % 16 == 0; };
-  const bool vec = a.cols % 8 == 0 && on16(a.dy, a.lddy) && on16(a.x, a.ldx) && on16(a.add, a.ldadd) && on16(a.dx, a.lddx) && aligned(a.codes, 8);
+  const bool vec = a.cols % 8 == 0 && on16(a.dy, a.lddy) && on16(a.x, a.ldx) && on16(a.add, a.ldadd) && on16(a.dx, a.lddx) && aligned(a.codes, 8) &&
+                   aligned(a.gamma, 16);
   const int parts = vec ? backward_parts<kTwoGroups<T, true>>(a.rows, a.cols) : backward_parts<false>(a.rows, a.cols);
   if (parts == 0) {  // no rows
   } else if (a.cols > kBackwardCols) {
@@ -747,7 +748,8 @@ extern "C" onebit_status_t onebit_layer_norm_forward(const void* x, int64_t ldx,
     return fail(ONEBIT_ERR_INVALID_ARG, "an output overlaps another buffer");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const ForwardArgs a{x, ldx, rows, (int)cols, (int)blocks, 1.0f / (float)cols, eps, gamma, beta, y, ldy, mean, rstd, codes, scales};
-  const bool vec = cols % 8 == 0 && aligned(x, 16) && aligned(y, 16) && (ldx * e) % 16 == 0 && (ldy * e) % 16 == 0 && aligned(codes, 8);
+  const bool vec = cols % 8 == 0 && aligned(x, 16) && aligned(y, 16) && (ldx * e) % 16 == 0 && (ldy * e) % 16 == 0 && aligned(codes, 8) &&
+                   aligned(gamma, 16) && aligned(beta, 16);
   auto go = [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
     if (vec) launch_forward<T, true>(a, s);

@@ -1,0 +1,54 @@
+"""Arguments that the layer operators accept and have to get right: parameters that lie anywhere in a flat fp32
+buffer, as an optimizer's often do."""
+import pytest
+import torch
+
+import test_gpu_layers as base
+from communication_compressed_optimizer_compress_gb300 import layers as L
+
+pytestmark = pytest.mark.gpu
+
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+
+
+def _in_flat(t, offset):
+    """The same values as a view that starts `offset` elements into a flat buffer."""
+    flat = torch.full((t.numel() + 8,), 77.0, device="cuda")
+    flat[offset: offset + t.numel()] = t
+    view = flat[offset: offset + t.numel()]
+    assert view.data_ptr() % 16 == 4 * offset % 16
+    return view
+
+
+@pytest.mark.parametrize("offset", [1, 2, 3, 4])
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=base.ids)
+@pytest.mark.parametrize("shape", [(3, 8), (33, 768), (300, 1024), (5, 4096), (2, 20000)], ids=str)
+def test_layer_norm_parameters_inside_a_flat_buffer(shape, dtype, offset):
+    """gamma and beta need no more than their own type's alignment: the results are within the tolerances of
+    test_gpu_layers, whatever their offset, with and without checkpoints and a second gradient."""
+    rows, cols = shape
+    gen = base._gen(rows + cols + offset)
+    x, dy, add = (base._randn(gen, rows, cols, dtype=dtype, scale=s, shift=m) for s, m in ((1.0, 0.5), (0.1, 0.0), (0.1, 0.0)))
+    gamma, beta = base._randn(gen, cols, shift=1.0), base._randn(gen, cols)
+    want, wmean, wrstd = base.ln64(x.double(), gamma.double(), beta.double())
+    n, top = min(cols, 64) + 16, x.double().abs().amax(1)
+    norm = (n * 2.0 ** -22 * (1 + top * wrstd))[:, None] * (1 + (x.double() - wmean[:, None]).abs() * wrstd[:, None])
+    tol = base._rounding(want, dtype) + norm * gamma.double().abs() + 2.0 ** -22 * beta.double().abs()
+    for g, b in ((_in_flat(gamma, offset), beta), (gamma, _in_flat(beta, offset)), (_in_flat(gamma, offset), _in_flat(beta, offset))):
+        for ck in (False, True):
+            y, mean, rstd, *kept = L.layer_norm(x, g, b, base.EPS, checkpoint=ck)
+            base._within(y, want, tol, "y")
+            if ck:
+                base._check_checkpoint(kept[0], x.double())
+    g = _in_flat(gamma, offset)
+    for src, x64 in ((x, x.double()), (kept[0], base.values64(kept[0]))):
+        for ad in (None, add):
+            dx, dg, db = L.layer_norm_backward(dy, src, g, mean, rstd, add=ad)
+            w, wg, wb, xh, gg = base._ln_grads64(dy.double(), x64, gamma.double(), mean.double(), rstd.double(), None if ad is None else ad.double())
+            # the sums of one row over its columns, of one column over the rows, and a few roundings of each term
+            size = rstd.double()[:, None] * (gg.abs() + gg.abs().mean(1, keepdim=True) + xh.abs() * (gg * xh).abs().mean(1, keepdim=True))
+            spread = 1 + (x64.abs().amax(1) * rstd.double())[:, None]
+            base._within(dx, w, base._rounding(w, dtype) + n * 2.0 ** -21 * spread * size + 2.0 ** -22 * add.double().abs(), "dx")
+            m = min(rows, 512) + 32
+            base._within(dg, wg, (m * 2.0 ** -24 * (dy.double() * xh).abs() + 2.0 ** -21 * spread * dy.double().abs()).sum(0), "dgamma")
+            base._within(db, wb, m * 2.0 ** -24 * dy.double().abs().sum(0), "dbeta")
