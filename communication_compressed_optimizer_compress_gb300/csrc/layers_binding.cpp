@@ -2,7 +2,8 @@
 //
 // A small call (16 tokens) spends 3 us on the GPU; through ctypes and Python's allocation calls the host needed
 // 15 us for it.  Here the common case of each operator of layers.py (2-D CUDA tensors, unit column stride,
-// matching types, at least one row) is checked, its outputs allocated and the C entry called in one step.
+// matching types, at least one row) is checked, its outputs allocated and the C entry called in one step, with the
+// tensors' device made current for that time.
 // Whatever else it meets -- another layout, an argument that does not fit, a status that is not OK -- it leaves
 // to layers.py by returning None: that path then does the call, or says what is wrong with it.  Nothing has
 // been enqueued when None is returned, as a call with a failed check enqueues nothing.
@@ -10,6 +11,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -178,6 +180,7 @@ void with_workspace(Run run, Size size, const Args& a, const at::Tensor& like) {
 PyObject* compress(PyObject* const* a) {
   const at::Tensor& x = tensor(a[0]);
   const Matrix m = matrix(x);
+  const c10::cuda::CUDAGuard guard(x.device());
   const int code = dtype_code(x.scalar_type());
   const NewCheckpoint ck(m.rows, m.cols, x);
   require(g_entry.compress(m.p, m.ld, code, m.rows, m.cols, ck.c(), ck.s(), stream(x)) == ONEBIT_OK);
@@ -188,6 +191,7 @@ PyObject* compress(PyObject* const* a) {
 PyObject* restore(PyObject* const* a) {
   require(Py_TYPE(a[0]) == g_checkpoint);
   const Kept k = kept(a[0]);
+  const c10::cuda::CUDAGuard guard(k.on->device());
   const int code = dtype_code(k.type), act = integer(a[1]);
   at::Tensor x = empty({k.rows, k.cols}, k.type, *k.on);
   require(g_entry.restore(k.codes, k.scales, k.rows, k.cols, act, x.data_ptr(), k.cols, code, stream(x)) == ONEBIT_OK);
@@ -198,6 +202,7 @@ PyObject* restore(PyObject* const* a) {
 PyObject* layer_norm(PyObject* const* a) {
   const at::Tensor& x = tensor(a[0]);
   const Matrix m = matrix(x);
+  const c10::cuda::CUDAGuard guard(x.device());
   const int code = dtype_code(x.scalar_type());
   const float *gamma = vector(a[1], m.cols, x), *beta = vector(a[2], m.cols, x);
   require(PyFloat_Check(a[3]));
@@ -221,6 +226,7 @@ PyObject* layer_norm(PyObject* const* a) {
 PyObject* layer_norm_backward(PyObject* const* a) {
   const at::Tensor& dy = tensor(a[0]);
   const Matrix m = matrix(dy);
+  const c10::cuda::CUDAGuard guard(dy.device());
   const int code = dtype_code(dy.scalar_type());
   const Kept k = kept(a[1], dy, m.rows, m.cols);
   const float *gamma = vector(a[2], m.cols, dy), *mean = vector(a[3], m.rows, dy), *rstd = vector(a[4], m.rows, dy);
@@ -242,6 +248,7 @@ PyObject* linear(PyObject* const* a) {
   const at::Tensor& x = tensor(a[0]);
   const at::Tensor& w = tensor(a[1]);
   const Matrix mx = matrix(x), mw = matrix(w);
+  const c10::cuda::CUDAGuard guard(x.device());
   require(mw.cols == mx.cols && w.scalar_type() == x.scalar_type() && w.device() == x.device());
   onebit_linear_t p{};
   p.dtype = dtype_code(x.scalar_type());
@@ -272,6 +279,7 @@ PyObject* linear_backward(PyObject* const* a) {
   const at::Tensor& dy = tensor(a[0]);
   const at::Tensor& w = tensor(a[2]);
   const Matrix md = matrix(dy), mw = matrix(w);
+  const c10::cuda::CUDAGuard guard(dy.device());
   require(mw.rows == md.cols && w.scalar_type() == dy.scalar_type() && w.device() == dy.device());
   onebit_linear_grad_t p{};
   p.dtype = dtype_code(dy.scalar_type());

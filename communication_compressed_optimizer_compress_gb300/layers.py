@@ -22,6 +22,7 @@ configured with, and may be written into the caller's tensors (``dw=``, ``db=``)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import importlib.util
 import os
@@ -213,13 +214,28 @@ def _workspace(nbytes: int, device):
     return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
+# The C entries launch on the current device, so the tensors' (or the stream's) is made current around each call;
+# the binding does the same.
+def _device_of(stream):
+    return contextlib.nullcontext() if stream is None else torch.cuda.device(stream.device)
+
+
+def _on(stream, t):
+    """The context in which an operator that was given `stream` calls itself."""
+    if t.device != stream.device:
+        raise ValueError(f"stream: expected one of {t.device}, got one of {stream.device}")
+    return torch.cuda.stream(stream)
+
+
 def get_status(stream=None) -> int:
-    """Waits for the stream; OK, or ERR_CUDA when a product gave up waiting for its copies."""
-    return int(_functions().onebit_layers_get_status(_stream_ptr(stream)))
+    """Waits for the stream; OK, or ERR_CUDA when a product of its device gave up waiting for its copies."""
+    with _device_of(stream):
+        return int(_functions().onebit_layers_get_status(_stream_ptr(stream)))
 
 
 def clear_status(stream=None):
-    _check(_functions().onebit_layers_clear_status(_stream_ptr(stream)), "onebit_layers_clear_status")
+    with _device_of(stream):
+        _check(_functions().onebit_layers_clear_status(_stream_ptr(stream)), "onebit_layers_clear_status")
 
 
 def set_fault_injection(kind: int, value: int = 0):
@@ -234,7 +250,7 @@ def set_fault_injection(kind: int, value: int = 0):
 def compress(x, stream=None) -> Checkpoint:
     """The 8-bit checkpoint of x."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, x):
             return compress(x)
     if _fn is None:
         _functions()
@@ -243,9 +259,10 @@ def compress(x, stream=None) -> Checkpoint:
         return fast
     rows, cols, ld = _matrix(x, "x")
     code, device = _code(x.dtype, "x"), x.device
-    ck = _new_checkpoint(x, rows, cols, x.dtype, device)
-    st = _functions().onebit_checkpoint_compress(x.data_ptr(), ld, code, rows, cols, ck[0].data_ptr(), ck[1].data_ptr(),
-                                                 _stream(device))
+    with torch.cuda.device(device):
+        ck = _new_checkpoint(x, rows, cols, x.dtype, device)
+        st = _functions().onebit_checkpoint_compress(x.data_ptr(), ld, code, rows, cols, ck[0].data_ptr(), ck[1].data_ptr(),
+                                                     _stream(device))
     if st:
         _check(st, "onebit_checkpoint_compress")
     return ck
@@ -254,7 +271,7 @@ def compress(x, stream=None) -> Checkpoint:
 def restore(ck: Checkpoint, activation=ACT_NONE, stream=None):
     """activation(the values a checkpoint stands for), in the checkpoint's dtype."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, ck[0]):
             return restore(ck, activation)
     if _fn is None:
         _functions()
@@ -262,9 +279,10 @@ def restore(ck: Checkpoint, activation=ACT_NONE, stream=None):
     if fast is not None:
         return fast
     _, _, codes, scales, rows, cols, dtype, device = _kept(ck, "ck")
-    x = torch.empty_like(ck[0], dtype=dtype)
-    st = _functions().onebit_checkpoint_restore(codes, scales, rows, cols, activation, x.data_ptr(), cols, _code(dtype, "ck"),
-                                                _stream(device))
+    with torch.cuda.device(device):
+        x = torch.empty_like(ck[0], dtype=dtype)
+        st = _functions().onebit_checkpoint_restore(codes, scales, rows, cols, activation, x.data_ptr(), cols, _code(dtype, "ck"),
+                                                    _stream(device))
     if st:
         _check(st, "onebit_checkpoint_restore")
     return x
@@ -273,7 +291,7 @@ def restore(ck: Checkpoint, activation=ACT_NONE, stream=None):
 def layer_norm(x, gamma, beta, eps=1e-5, checkpoint=False, stream=None):
     """(y, mean, rstd), and the 8-bit checkpoint of x where asked for."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, x):
             return layer_norm(x, gamma, beta, eps, checkpoint)
     if _fn is None:
         _functions()
@@ -283,12 +301,13 @@ def layer_norm(x, gamma, beta, eps=1e-5, checkpoint=False, stream=None):
     rows, cols, ld = _matrix(x, "x")
     code, device = _code(x.dtype, "x"), x.device
     g, b = _vector(gamma, "gamma", cols, device), _vector(beta, "beta", cols, device)
-    y = _like(x)
-    mean, rstd = _rows_of(x, rows, device), _rows_of(x, rows, device)
-    ck = _new_checkpoint(x, rows, cols, x.dtype, device) if checkpoint else None
-    st = _functions().onebit_layer_norm_forward(
-        x.data_ptr(), ld, code, rows, cols, g, b, eps, y.data_ptr(), cols, mean.data_ptr(), rstd.data_ptr(),
-        ck[0].data_ptr() if checkpoint else None, ck[1].data_ptr() if checkpoint else None, _stream(device))
+    with torch.cuda.device(device):
+        y = _like(x)
+        mean, rstd = _rows_of(x, rows, device), _rows_of(x, rows, device)
+        ck = _new_checkpoint(x, rows, cols, x.dtype, device) if checkpoint else None
+        st = _functions().onebit_layer_norm_forward(
+            x.data_ptr(), ld, code, rows, cols, g, b, eps, y.data_ptr(), cols, mean.data_ptr(), rstd.data_ptr(),
+            ck[0].data_ptr() if checkpoint else None, ck[1].data_ptr() if checkpoint else None, _stream(device))
     if st:
         _check(st, "onebit_layer_norm_forward")
     return (y, mean, rstd, ck) if checkpoint else (y, mean, rstd)
@@ -297,7 +316,7 @@ def layer_norm(x, gamma, beta, eps=1e-5, checkpoint=False, stream=None):
 def layer_norm_backward(dy, x, gamma, mean, rstd, add=None, grad_dtype=torch.float32, stream=None):
     """(dx, dgamma, dbeta) from the layer's input x, a tensor or its Checkpoint; ``add`` joins dx."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, dy):
             return layer_norm_backward(dy, x, gamma, mean, rstd, add, grad_dtype)
     if _fn is None:
         _functions()
@@ -312,15 +331,16 @@ def layer_norm_backward(dy, x, gamma, mean, rstd, add=None, grad_dtype=torch.flo
     mu, rs = _vector(mean, "mean", rows, device), _vector(rstd, "rstd", rows, device)
     ap, lda = (add.data_ptr(), _matrix(add, "add", cols, rows, dtype, device)[2]) if add is not None else (None, 0)
     fn, need = _functions(), ctypes.c_size_t()
-    dx = _like(dy)
-    dgamma, dbeta = torch.empty(cols, dtype=grad_dtype, device=device), torch.empty(cols, dtype=grad_dtype, device=device)
-    st = fn.onebit_layer_norm_backward_workspace(rows, cols, need)
-    if st:
-        _check(st, "onebit_layer_norm_backward_workspace")
-    ws = _workspace(need.value, device)
-    st = fn.onebit_layer_norm_backward(
-        dy.data_ptr(), lddy, xp, ldx, codes, scales, code, rows, cols, g, mu, rs, ap, lda, dx.data_ptr(), cols,
-        dgamma.data_ptr(), dbeta.data_ptr(), gcode, ws.data_ptr() if ws is not None else None, need.value, _stream(device))
+    with torch.cuda.device(device):
+        dx = _like(dy)
+        dgamma, dbeta = torch.empty(cols, dtype=grad_dtype, device=device), torch.empty(cols, dtype=grad_dtype, device=device)
+        st = fn.onebit_layer_norm_backward_workspace(rows, cols, need)
+        if st:
+            _check(st, "onebit_layer_norm_backward_workspace")
+        ws = _workspace(need.value, device)
+        st = fn.onebit_layer_norm_backward(
+            dy.data_ptr(), lddy, xp, ldx, codes, scales, code, rows, cols, g, mu, rs, ap, lda, dx.data_ptr(), cols,
+            dgamma.data_ptr(), dbeta.data_ptr(), gcode, ws.data_ptr() if ws is not None else None, need.value, _stream(device))
     if st:
         _check(st, "onebit_layer_norm_backward")
     return dx, dgamma, dbeta
@@ -344,7 +364,7 @@ def _with_workspace(run, size, args, device, where):
 def linear(x, w, bias=None, activation=ACT_NONE, residual=None, checkpoint=False, stream=None):
     """y = activation(x w^T + bias) + residual; with ``checkpoint`` (y, the 8-bit checkpoint of x w^T + bias)."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, x):
             return linear(x, w, bias, activation, residual, checkpoint)
     if _fn is None:
         _functions()
@@ -359,13 +379,14 @@ def linear(x, w, bias=None, activation=ACT_NONE, residual=None, checkpoint=False
     out, _, ldw = _matrix(w, "w", cols, None, dtype, device)
     bp = _vector(bias, "bias", out, device)
     rp, ldr = (residual.data_ptr(), _matrix(residual, "residual", out, rows, dtype, device)[2]) if residual is not None else (None, 0)
-    y = _rows_by(x, rows, out, dtype, device)
-    ck = _new_checkpoint(x, rows, out, dtype, device) if checkpoint else None
-    a = LinearArgs(x.data_ptr(), ldx, w.data_ptr(), ldw, bp, rp, ldr, y.data_ptr(), out,
-                   ck[0].data_ptr() if checkpoint else None, ck[1].data_ptr() if checkpoint else None, rows, cols, out, code,
-                   activation)
-    fn = _functions()
-    _with_workspace(fn.onebit_linear_forward, fn.onebit_linear_forward_workspace, a, device, "onebit_linear_forward")
+    with torch.cuda.device(device):
+        y = _rows_by(x, rows, out, dtype, device)
+        ck = _new_checkpoint(x, rows, out, dtype, device) if checkpoint else None
+        a = LinearArgs(x.data_ptr(), ldx, w.data_ptr(), ldw, bp, rp, ldr, y.data_ptr(), out,
+                       ck[0].data_ptr() if checkpoint else None, ck[1].data_ptr() if checkpoint else None, rows, cols, out, code,
+                       activation)
+        fn = _functions()
+        _with_workspace(fn.onebit_linear_forward, fn.onebit_linear_forward_workspace, a, device, "onebit_linear_forward")
     return (y, ck) if checkpoint else y
 
 
@@ -376,7 +397,7 @@ def linear_backward(dy, x, w, activation=ACT_NONE, add=None, grad_dtype=None, dw
     dx.  grad_dtype (default dy's) is the type of dw (out x in) and db; ``dw`` and ``db`` may be the
     caller's contiguous tensors.  What ``need`` leaves out is None."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, dy):
             return linear_backward(dy, x, w, activation, add, grad_dtype, dw, db, need)
     if _fn is None:
         _functions()
@@ -396,18 +417,19 @@ def linear_backward(dy, x, w, activation=ACT_NONE, add=None, grad_dtype=None, dw
         xp, ldx, codes, scales, *_ = _kept(x, "x", cols, rows, dtype, device)
     ap, lda = (add.data_ptr(), _matrix(add, "add", cols, rows, dtype, device)[2]) if add is not None else (None, 0)
     want_dx, want_dw, want_db = "dx" in need, "dw" in need, "db" in need
-    dx = _rows_by(dy, rows, cols, dtype, device) if want_dx else None
-    if not want_dw:
-        dw = None
-    elif dw is None:
-        dw = torch.empty(out, cols, dtype=grad_dtype, device=device)
-    if not want_db:
-        db = None
-    elif db is None:
-        db = torch.empty(out, dtype=grad_dtype, device=device)
-    a = LinearGradArgs(dy.data_ptr(), lddy, xp, ldx, codes, scales, w.data_ptr(), ldw, ap, lda,
-                       dx.data_ptr() if want_dx else None, cols, _vector(dw, "dw", out * cols, device, grad_dtype),
-                       _vector(db, "db", out, device, grad_dtype), rows, cols, out, code, activation, gcode)
-    fn = _functions()
-    _with_workspace(fn.onebit_linear_backward, fn.onebit_linear_backward_workspace, a, device, "onebit_linear_backward")
+    with torch.cuda.device(device):
+        dx = _rows_by(dy, rows, cols, dtype, device) if want_dx else None
+        if not want_dw:
+            dw = None
+        elif dw is None:
+            dw = torch.empty(out, cols, dtype=grad_dtype, device=device)
+        if not want_db:
+            db = None
+        elif db is None:
+            db = torch.empty(out, dtype=grad_dtype, device=device)
+        a = LinearGradArgs(dy.data_ptr(), lddy, xp, ldx, codes, scales, w.data_ptr(), ldw, ap, lda,
+                           dx.data_ptr() if want_dx else None, cols, _vector(dw, "dw", out * cols, device, grad_dtype),
+                           _vector(db, "db", out, device, grad_dtype), rows, cols, out, code, activation, gcode)
+        fn = _functions()
+        _with_workspace(fn.onebit_linear_backward, fn.onebit_linear_backward_workspace, a, device, "onebit_linear_backward")
     return dx, dw, db

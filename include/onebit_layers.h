@@ -10,6 +10,7 @@
  *   - `stream` is a cudaStream_t (NULL = legacy default stream).  Calls enqueue work on it and return
  *     without synchronising; every buffer must stay valid until the stream has passed the call.
  *     Calls on different streams are independent as long as their outputs and workspaces are.
+ *   - Calls run on the calling thread's current device, which has to be the buffers' and the stream's.
  *   - A matrix is row-major with unit column stride: element (r, c) is at base + r*ld + c, with the
  *     row stride ld >= columns in elements.  Bases may have any alignment that the type needs, and
  *     ld any value; rows that start on 16-byte boundaries take the wide loads (layer norm: where gamma

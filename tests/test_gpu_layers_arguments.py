@@ -52,3 +52,28 @@ def test_layer_norm_parameters_inside_a_flat_buffer(shape, dtype, offset):
             m = min(rows, 512) + 32
             base._within(dg, wg, (m * 2.0 ** -24 * (dy.double() * xh).abs() + 2.0 ** -21 * spread * dy.double().abs()).sum(0), "dgamma")
             base._within(db, wb, m * 2.0 ** -24 * dy.double().abs().sum(0), "dbeta")
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs two devices")
+def test_tensors_of_a_device_that_is_not_current():
+    """The same results, bit for bit, as with the tensors' device current, and the current device stays."""
+    gen = base._gen(4)
+    x, w, dy = (base._randn(gen, *s, dtype=BF16, scale=0.3) for s in ((300, 264), (136, 264), (300, 136)))
+    g = base._randn(gen, 264, shift=1.0)
+
+    def run(x, w, dy, g):
+        y, z = L.linear(x, w, activation=L.ACT_GELU, checkpoint=True)
+        n, mean, rstd, ck = L.layer_norm(x, g, g, checkpoint=True)
+        got = [y, *z[:2], n, mean, rstd, L.restore(ck), *L.layer_norm_backward(x, ck, g, mean, rstd), *L.linear_backward(dy, ck, w, L.ACT_GELU)]
+        got += list(L.linear_backward(dy[None], x[None], w))  # not the binding's case
+        return got
+
+    want = run(x, w, dy, g)
+    with torch.cuda.device(1):
+        other = [t.to("cuda:1") for t in (x, w, dy, g)]
+        torch.cuda.synchronize()
+    assert torch.cuda.current_device() == 0
+    got = run(*other)
+    assert torch.cuda.current_device() == 0 and L.get_status(torch.cuda.default_stream(1)) == 0
+    for a, b in zip(want, got):
+        assert b.device.index == 1 and torch.equal(a, b.to("cuda:0"))
