@@ -1,0 +1,72 @@
+"""How many digits the layer operators keep where another order of the same operations would lose some.
+
+Each tolerance is that of the operations as the formulas name them, every one rounded to fp32 (2^-24)."""
+import math
+
+import pytest
+import torch
+
+import test_gpu_layers as base
+from communication_compressed_optimizer_compress_gb300 import layers as L
+
+pytestmark = pytest.mark.gpu
+
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+
+
+@pytest.mark.parametrize("kept", ["x", "checkpoint"])
+@pytest.mark.parametrize("layout", ["dense", "odd"])
+@pytest.mark.parametrize("shape", [(5, 31), (300, 256), (40, 520), (200, 1024), (60, 1155), (20, 2048), (9, 4096), (5, 8192), (3, 9000)], ids=str)
+@pytest.mark.parametrize("shift", [0.0, 10.0, 100.0, 1000.0])
+def test_normalised_values_of_rows_far_from_zero(shift, shape, layout, kept):
+    """x - mean is exact or off by 2^-24 of itself however large the mean is, so that dx and dgamma lose nothing to it.
+    (A row of more than 8192 columns reads values of a checkpoint, code times scale, which are rounded themselves.)"""
+    rows, cols = shape
+    gen = base._gen(rows + cols)
+    x = base._lay(base._randn(gen, rows, cols, shift=shift), layout)
+    gamma, dy = base._randn(gen, cols, shift=1.0), base._lay(base._randn(gen, rows, cols, scale=0.1), layout)
+    _, mean, rstd = L.layer_norm(x, gamma, torch.zeros_like(gamma), base.EPS)
+    src, x64 = x, x.double()
+    if kept == "checkpoint":
+        src = L.compress(x)
+        x64 = base.values64(src)
+    dx, dg, db = L.layer_norm_backward(dy, src, gamma, mean, rstd)
+    d64, r64 = dy.double(), rstd.double()[:, None]
+    want, wg, _, xh, g = base._ln_grads64(d64, x64, gamma.double(), mean.double(), rstd.double(), None)
+    xe = 2.0 ** -22 * xh.abs()  # of a normalised value
+    if kept == "checkpoint" and cols > 8192:
+        xe = xe + 2.0 ** -23 * x64.abs() * r64
+    base._within(dg, wg, ((min(rows, 512) + 32) * 2.0 ** -24 * (d64 * xh).abs() + d64.abs() * xe).sum(0), "dgamma")
+    n = min(cols, 64) + 16  # additions one after another, and of the trees over them
+    mean_gx = (g * xh).mean(1, keepdim=True)
+    e2 = n * 2.0 ** -23 * (g * xh).abs().mean(1, keepdim=True) + (g.abs() * xe).mean(1, keepdim=True)
+    tol = r64 * (2.0 ** -21 * (g.abs() + (xh * mean_gx).abs()) + n * 2.0 ** -23 * g.abs().mean(1, keepdim=True) + xh.abs() * e2 + xe * mean_gx.abs())
+    base._within(dx, want, tol + base._rounding(want, F32), "dx")
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=base.ids)
+@pytest.mark.parametrize("cols", [64, 1024, 1001, 9000])
+def test_constant_rows_are_normalised_to_zero(cols, dtype):
+    """x - mean is 0, so dgamma is 0 and dx is what is left of the mean's own term; eps alone decides rstd."""
+    x = torch.full((40, cols), 1000.0, device="cuda").to(dtype)
+    mean, rstd = x[:, 0].float().contiguous(), torch.full((40,), base.EPS ** -0.5, device="cuda")
+    gamma, dy = base._randn(base._gen(1), cols, shift=1.0), base._randn(base._gen(2), 40, cols, dtype=dtype)
+    for src in (x, L.compress(x)):
+        dx, dg, db = L.layer_norm_backward(dy, src, gamma, mean, rstd)
+        if torch.is_tensor(src):
+            assert torch.equal(dg, torch.zeros_like(dg))
+        else:  # the checkpoint's value of 1000 is off by at most 2^-23 of it
+            assert float(dg.abs().max()) <= 40 * 1000 * 2.0 ** -23 * float(rstd[0]) * float(dy.abs().max())
+
+
+def test_checkpoint_of_the_largest_values_in_fp32():
+    """A code times its scale would round past the largest value: 127 (a / 127) with a just below it."""
+    top = torch.finfo(F32).max
+    x = torch.full((6, 128), top, device="cuda")
+    x[:, 1::2] *= 0.5
+    ck = L.compress(x)
+    mean, rstd = torch.full((6,), top / 2, device="cuda"), torch.full((6,), 2.0 ** -127, device="cuda")
+    dy, gamma = base._randn(base._gen(3), 6, 128), torch.ones(128, device="cuda")
+    dx, dg, db = L.layer_norm_backward(dy, ck, gamma, mean, rstd)
+    _, wg, _, xh, _ = base._ln_grads64(dy.double(), base.values64(ck), gamma.double(), mean.double(), rstd.double(), None)
+    base._within(dg, wg, 2.0 ** -20 * (dy.double() * xh).abs().sum(0) + 1e-30, "dgamma")
