@@ -202,8 +202,8 @@ struct BlockScale {
   float inv;    // what a value is multiplied by before it is rounded to a code
 };
 // Both quotients by one correction of an approximate one (Markstein 1990): q += r (n - d q), which leaves
-// them within an ulp.  A division of the language is several times as long, and every eight columns of a
-// layer norm's row need two.
+// them rounded as a division would (compared for every mantissa).  A division of the language is several times as
+// long, and every eight columns of a layer norm's row need two.
 __device__ __forceinline__ BlockScale block_scale(float most) {
   if (!(most <= 3.4028234663852886e38f)) return {CUDART_NAN_F, 0.0f};
   if (most < 7.52316384526264e-37f) return {0.0f, 0.0f};  // 2^-120
@@ -247,9 +247,11 @@ __device__ __forceinline__ void values4(uint32_t word, float scale, f2* v) {
   }
 }
 // four values to a word of codes; inv is 0 only for blocks whose codes are all 0.  The product is rounded
-// before 1.5*2^23 is added, as in code_of().
+// before 1.5*2^23 is added, as in code_of(): the additions go one by one, as a packed product and a packed sum behind it
+// are compiled to one fused operation, whatever rounding they name (codes at ties then differed between the layouts).
 __device__ __forceinline__ uint32_t codes4(f2 ab, f2 cd, float inv) {
-  const float2 x = halves(add2(mul2(ab, splat(inv)), splat(12582912.0f))), y = halves(add2(mul2(cd, splat(inv)), splat(12582912.0f)));
+  const float2 p = halves(mul2(ab, splat(inv))), q = halves(mul2(cd, splat(inv)));
+  const float2 x = make_float2(__fadd_rn(p.x, 12582912.0f), __fadd_rn(p.y, 12582912.0f)), y = make_float2(__fadd_rn(q.x, 12582912.0f), __fadd_rn(q.y, 12582912.0f));
   const uint32_t r = __byte_perm(__byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x0040),
                                  __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x0040), 0x5410);
   return inv == 0.0f ? 0u : r;  // inf and NaN times 0 would leave other bits

@@ -70,3 +70,49 @@ def test_checkpoint_of_the_largest_values_in_fp32():
     dx, dg, db = L.layer_norm_backward(dy, ck, gamma, mean, rstd)
     _, wg, _, xh, _ = base._ln_grads64(dy.double(), base.values64(ck), gamma.double(), mean.double(), rstd.double(), None)
     base._within(dg, wg, 2.0 ** -20 * (dy.double() * xh).abs().sum(0) + 1e-30, "dgamma")
+
+
+def _checkpoint_by_definition(x):
+    """Codes and scales of an fp32 matrix of whole blocks, operation by operation in fp32: a / 127 and 127 / a rounded,
+    x times the latter rounded, and that to the nearest integer, ties to even."""
+    v = x.view(x.shape[0], -1, 64)
+    a = v.abs().amax(2)
+    full = torch.full_like(a, 127.0)  # a tensor: a quotient by a number may be a product with its reciprocal
+    zero = a < 2.0 ** -120
+    scales = torch.where(zero, 0.0, a / full)
+    codes = torch.where(zero[:, :, None], 0.0, torch.round(v * (full / a)[:, :, None]))
+    return codes.to(torch.int8).view_as(x), scales
+
+
+@pytest.mark.parametrize("exponent", [-120, -60, 0, 126])
+def test_block_scales_of_every_mantissa(exponent):
+    """Both quotients are the rounded ones for every a of a binade: the scale is seen as it is, the factor of the
+    codes in values that lie on both sides of a rounding boundary."""
+    n, step = 1 << 23, 1 << 18
+    k = torch.arange(63, device="cuda") + 0.5 + 64.0 * (torch.arange(63, device="cuda") % 2)
+    for first in range(0, n, step):
+        m = torch.arange(first, first + step, device="cuda")
+        a = ((m + n).double() * 2.0 ** (exponent - 23)).float()[:, None]
+        edge = (k[None] * a.double() / 127).float().clamp(max=torch.finfo(F32).max)
+        edge = torch.minimum(edge, a)
+        side = (m % 3 - 1)[:, None]  # the boundary itself, or a value beside it
+        edge = torch.where(side < 0, torch.nextafter(edge, torch.zeros_like(edge)), edge)
+        x = torch.cat([a, edge], 1).contiguous()
+        ck = L.compress(x)
+        codes, scales = _checkpoint_by_definition(x)
+        assert torch.equal(ck.scales, scales) and torch.equal(ck.codes, codes), first
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=base.ids)
+@pytest.mark.parametrize("shape", [(20000, 256), (3000, 1024), (700, 4096), (90, 20032), (5, 64)], ids=str)
+def test_codes_are_the_definitions_in_every_layout(shape, dtype):
+    """Products that the rounding to fp32 puts on a tie among them (about one of a thousand codes of random bf16)."""
+    rows, cols = shape
+    x = base._randn(base._gen(rows), rows, cols, dtype=dtype)
+    codes, scales = _checkpoint_by_definition(x.float())
+    g = torch.ones(cols, device="cuda")
+    for layout in ("dense", "wide", "odd"):
+        t = base._lay(x, layout)
+        for ck in (L.compress(t), L.layer_norm(t, g, g, checkpoint=True)[3]):
+            assert torch.equal(ck.scales, scales)
+            assert torch.equal(ck.codes, codes), (layout, int((ck.codes != codes).sum()))
