@@ -246,24 +246,19 @@ __device__ __forceinline__ void values4(uint32_t word, float scale, f2* v) {
     }
   }
 }
-// four values to a word of codes; inv is 0 only for blocks whose codes are all 0.  The product is rounded
-// before 1.5*2^23 is added, as in code_of(): the additions go one by one, as a packed product and a packed sum behind it
-// are compiled to one fused operation, whatever rounding they name (codes at ties then differed between the layouts).
-__device__ __forceinline__ uint32_t codes4(f2 ab, f2 cd, float inv) {
+// four values to a word of codes.  The product is rounded before 1.5*2^23 is added, as in code_of(): the additions go
+// one by one, as a packed product and a packed sum behind it are compiled to one fused operation, whatever rounding they
+// name (codes at ties then differed between the layouts).  The caller sees to inv = 0 where values may be inf or NaN.
+__device__ __forceinline__ uint32_t codes4_finite(f2 ab, f2 cd, float inv) {
   const float2 p = halves(mul2(ab, splat(inv))), q = halves(mul2(cd, splat(inv)));
   const float2 x = make_float2(__fadd_rn(p.x, 12582912.0f), __fadd_rn(p.y, 12582912.0f)), y = make_float2(__fadd_rn(q.x, 12582912.0f), __fadd_rn(q.y, 12582912.0f));
-  const uint32_t r = __byte_perm(__byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x0040),
-                                 __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x0040), 0x5410);
-  return inv == 0.0f ? 0u : r;  // inf and NaN times 0 would leave other bits
-}
-
-// The same where the values are a product's own sums: the multiplication and the addition in one, rounded once,
-// which is half the work and no less exact (a tie of the twice rounded form may fall the other way).  The
-// caller sees to blocks with infinities and NaN.
-__device__ __forceinline__ uint32_t codes4_rounded_once(f2 ab, f2 cd, float inv) {
-  const float2 x = halves(fma2(ab, splat(inv), splat(12582912.0f))), y = halves(fma2(cd, splat(inv), splat(12582912.0f)));
   return __byte_perm(__byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x0040),
                      __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x0040), 0x5410);
+}
+// inv is 0 only for blocks whose codes are all 0
+__device__ __forceinline__ uint32_t codes4(f2 ab, f2 cd, float inv) {
+  const uint32_t r = codes4_finite(ab, cd, inv);
+  return inv == 0.0f ? 0u : r;  // inf and NaN times 0 would leave other bits
 }
 
 // ------------------------------------------------------------------------------------------------

@@ -574,7 +574,7 @@ struct ForwardEpilogue {
       add_bias(z, half, staging);
       if (keeps()) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = codes4_rounded_once(z[2 * i], z[2 * i + 1], inv);
+        for (int i = 0; i < 8; ++i) c[i] = codes4_finite(z[2 * i], z[2 * i + 1], inv);
         if (!plain && inv == 0.0f) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) c[i] = 0;

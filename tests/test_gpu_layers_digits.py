@@ -116,3 +116,23 @@ def test_codes_are_the_definitions_in_every_layout(shape, dtype):
         for ck in (L.compress(t), L.layer_norm(t, g, g, checkpoint=True)[3]):
             assert torch.equal(ck.scales, scales)
             assert torch.equal(ck.codes, codes), (layout, int((ck.codes != codes).sum()))
+
+
+@pytest.mark.parametrize("shape", [(65536, 256), (4096, 1024), (8192, 192), (300, 2048), (40, 4096), (33000, 136), (20000, 203)], ids=str)
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=base.ids)
+def test_codes_of_a_product_are_those_of_its_values(dtype, shape):
+    """With the identity as the weight z is x + bias, rounded once, whatever the product's form: its checkpoint is that of
+    the same fp32 matrix by compress(), code by code."""
+    rows, cols = shape
+    gen = base._gen(cols)
+    x, w = base._randn(gen, rows, cols, dtype=dtype), torch.eye(cols, device="cuda", dtype=dtype)
+    for bias in (None, base._randn(gen, cols)):
+        z = x.float() if bias is None else x.float() + bias
+        want = L.compress(z)
+        if cols % 64 == 0:
+            codes, scales = _checkpoint_by_definition(z)
+            assert torch.equal(want.codes, codes) and torch.equal(want.scales, scales)
+        for act, residual in ((L.ACT_NONE, None), (L.ACT_GELU, None), (L.ACT_GELU_TANH, x)):
+            _, ck = L.linear(x, w, bias, act, residual, checkpoint=True)
+            assert torch.equal(ck.scales, want.scales)
+            assert torch.equal(ck.codes, want.codes), int((ck.codes != want.codes).sum())
