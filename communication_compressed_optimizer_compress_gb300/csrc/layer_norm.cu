@@ -129,12 +129,13 @@ constexpr int kForwardThreads = TPR < 128 ? 128 / TPR * TPR : TPR;
 template <typename T, int TPR, int CH, bool VEC>
 constexpr int kForwardRoom = VEC && sizeof(T) == 2 && CH == 1 && TPR > 64 ? 1024 : TPR < 256 ? 640 : 512;  // threads an SM
 
-// NR rows at a time: their sums go through the shuffles and the barrier together.  gamma and beta stay in registers
+// NR rows at a time (1 or 2): their sums go through the shuffles and the barrier together.  gamma and beta stay in registers
 // where they fit beside the rows; elsewhere they are read (from L1) once for the NR rows.  16384 x 1024 bf16 with the
 // checkpoint: a warp a row, which reads them for every row, 18.6 us (62% of the L1's cycles), 128 threads a row that hold
 // them 17.2, at 1024 threads an SM (18.5 at 640); 33 rows 2.7 and 2.1 us.
 template <typename T, int TPR, int CH, int NR, bool VEC, bool FULL>
 __global__ void __launch_bounds__(kForwardThreads<TPR>, kForwardRoom<T, TPR, CH, VEC> / kForwardThreads<TPR>) k_ln_forward(const ForwardArgs A) {
+  static_assert(NR == 1 || NR == 2, "rows at a time");
   in_turn();
   constexpr int kGroups = kForwardThreads<TPR> / TPR;
   const int cols = FULL ? TPR * CH * 8 : A.cols;
@@ -237,8 +238,12 @@ __global__ void __launch_bounds__(kForwardThreads<TPR>, kForwardRoom<T, TPR, CH,
     }
     row_sums<TPR>(rstd, red[group], turn, 1 + group);
 #pragma unroll
+    for (int n = 0; n < NR; n += 2) {
+      const float2 v = halves(rsqrt_rounded(fma2(pair(rstd[n], rstd[NR - 1]), splat(A.inv_cols), splat(A.eps))));
+      rstd[n] = v.x, rstd[NR - 1] = NR > 1 ? v.y : v.x;
+    }
+#pragma unroll
     for (int n = 0; n < NR; ++n) {
-      rstd[n] = rsqrtf(fmaf(rstd[n], A.inv_cols, A.eps));
       if (t == 0 && r + n < A.rows) {
         A.mean[r + n] = mean[n];
         A.rstd[r + n] = rstd[n];
@@ -537,7 +542,7 @@ __global__ void __launch_bounds__(kLnThreads) k_ln_forward_wide(const ForwardArg
       const float d = to_f(xr[c]) - mean;
       s = fmaf(d, d, s);
     }
-    const float rstd = rsqrtf(fmaf(block_sum(s, red), A.inv_cols, A.eps));
+    const float rstd = halves(rsqrt_rounded(splat(fmaf(block_sum(s, red), A.inv_cols, A.eps)))).x;
     for (int c = threadIdx.x; c < A.cols; c += kLnThreads)
       yr[c] = from_f<T>(fmaf((to_f(xr[c]) - mean) * rstd, A.gamma[c], A.beta[c]));
     if (threadIdx.x == 0) {

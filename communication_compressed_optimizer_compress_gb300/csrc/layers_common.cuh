@@ -376,6 +376,15 @@ __device__ __forceinline__ float warp_max_nan(float v) {
   return v;
 }
 
+// 1/sqrt(v) of two values, rounded: one Newton step on CUDA's, which is within two ulps, with what v y rounds off taken
+// along (1 - v y^2 = 1 - s y + (s - v y) y).  The step of 0 and of infinity is NaN: their reciprocals are there before it.
+__device__ __forceinline__ f2 rsqrt_rounded(f2 v) {
+  const float2 w = halves(v), y = make_float2(rsqrtf(w.x), rsqrtf(w.y));
+  const f2 y2 = pair(y.x, y.y), n2 = pair(-y.x, -y.y), s = mul2(v, y2);
+  const float2 r = halves(fma2(mul2(y2, splat(0.5f)), fma2(fma2(v, n2, s), y2, fma2(s, n2, splat(1.0f))), y2));
+  return pair(r.x == r.x ? r.x : y.x, r.y == r.y ? r.y : y.y);
+}
+
 // ------------------------------------------------------------------------------------------------
 // All kernels of the layers are launched programmatically: a kernel's blocks may be brought up when every block of
 // the one before has called launch_next() or ended, beside its last blocks, and wait_previous() holds them until it is

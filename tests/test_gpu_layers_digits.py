@@ -136,3 +136,27 @@ def test_codes_of_a_product_are_those_of_its_values(dtype, shape):
             _, ck = L.linear(x, w, bias, act, residual, checkpoint=True)
             assert torch.equal(ck.scales, want.scales)
             assert torch.equal(ck.codes, want.codes), int((ck.codes != want.codes).sum())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=base.ids)
+@pytest.mark.parametrize("cols", [64, 256, 1024, 4096, 16384, 32768])
+def test_reciprocal_deviations_are_rounded(cols, dtype):
+    """Rows of +-c with whole c have the variance c^2 without any rounding, so that rstd is 1/sqrt(c^2 + eps) rounded:
+    within half a unit in the last place, and a thousandth of one for the steps that lead there."""
+    c = torch.arange(128, 256, device="cuda", dtype=dtype)
+    sign = 1 - 2 * (torch.arange(cols, device="cuda") % 2)
+    g = torch.ones(cols, device="cuda")
+    for eps in range(40):
+        _, mean, rstd = L.layer_norm(c[:, None] * sign.to(dtype), g, g, float(eps))
+        assert not mean.any()
+        want = (c.double().square() + eps) ** -0.5
+        unit = 2.0 ** (torch.floor(torch.log2(want)) - 23)
+        base._within(rstd, want, 0.501 * unit, f"rstd, eps {eps}")
+
+
+def test_reciprocal_deviations_at_the_ends():
+    """No variance and no eps, a variance past fp32, one below the normal range."""
+    g = torch.ones(64, device="cuda")
+    sign = (1 - 2 * (torch.arange(64, device="cuda") % 2)).float()
+    x = torch.stack([3.0 * torch.ones_like(sign), 2.0 ** 100 * sign, 2.0 ** -65 * sign])
+    assert L.layer_norm(x, g, g, 0.0)[2].tolist() == [math.inf, 0.0, 2.0 ** 65]
