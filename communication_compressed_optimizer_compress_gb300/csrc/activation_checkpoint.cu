@@ -22,7 +22,10 @@ onebit_status_t fail(onebit_status_t status, const char* what) {
   }
   return status;
 }
+// A call's errors are its launches' own results, so that one that earlier code has left pending is not taken for it; its
+// own is not left pending for the next caller either.
 onebit_status_t cuda_fail(cudaError_t e, const char* where) {
+  cudaGetLastError();
   char buf[256];
   snprintf(buf, sizeof buf, "%s: %s", where, cudaGetErrorString(e));
   return fail(ONEBIT_ERR_CUDA, buf);
@@ -158,30 +161,28 @@ unsigned ck_grid(int64_t units) {
 }
 
 template <typename T>
-void compress(const void* x, int64_t ldx, int32_t dtype, int64_t rows, int cols, int8_t* codes, float* scales, cudaStream_t s) {
+cudaError_t compress(const void* x, int64_t ldx, int32_t dtype, int64_t rows, int cols, int8_t* codes, float* scales, cudaStream_t s) {
   const int blocks = (int)ceil_div(cols, kBlock);
   const T* p = static_cast<const T*>(x);
   if (wide_ok(x, ldx, dtype, cols, codes)) {
     const Wide w{rows, cols, blocks, cols < kCkRun ? kCkRun / cols : 1};
-    launch_after(k_compress_wide<T>, ck_grid(ceil_div(rows, w.run_rows)), kCkThreads, s, p, ldx, w, codes, scales);
-  } else {
-    launch_after(k_compress<T>, ck_grid(ceil_div(rows * blocks, kCkThreads / 32)), kCkThreads, s, p, ldx, rows, cols, blocks, codes, scales);
+    return launch_after(k_compress_wide<T>, ck_grid(ceil_div(rows, w.run_rows)), kCkThreads, s, p, ldx, w, codes, scales);
   }
+  return launch_after(k_compress<T>, ck_grid(ceil_div(rows * blocks, kCkThreads / 32)), kCkThreads, s, p, ldx, rows, cols, blocks, codes, scales);
 }
 template <typename T>
-void restore(const int8_t* codes, const float* scales, int64_t rows, int cols, int act, void* x, int64_t ldx, int32_t dtype, cudaStream_t s) {
+cudaError_t restore(const int8_t* codes, const float* scales, int64_t rows, int cols, int act, void* x, int64_t ldx, int32_t dtype, cudaStream_t s) {
   const int blocks = (int)ceil_div(cols, kBlock);
   T* p = static_cast<T*>(x);
   if (wide_ok(x, ldx, dtype, cols, codes)) {
     const Wide w{rows, cols, blocks, cols < kCkRun ? kCkRun / cols : 1};
     const unsigned grid = ck_grid(ceil_div(rows, w.run_rows));
-    if (act == ONEBIT_ACT_NONE) launch_after(k_restore_wide<T, ONEBIT_ACT_NONE>, grid, kCkThreads, s, codes, scales, w, p, ldx);
-    else if (act == ONEBIT_ACT_RELU) launch_after(k_restore_wide<T, ONEBIT_ACT_RELU>, grid, kCkThreads, s, codes, scales, w, p, ldx);
-    else if (act == ONEBIT_ACT_GELU) launch_after(k_restore_wide<T, ONEBIT_ACT_GELU>, grid, kCkThreads, s, codes, scales, w, p, ldx);
-    else launch_after(k_restore_wide<T, ONEBIT_ACT_GELU_TANH>, grid, kCkThreads, s, codes, scales, w, p, ldx);
-  } else {
-    launch_after(k_restore<T>, ck_grid(ceil_div(rows * blocks, kCkThreads / 32)), kCkThreads, s, codes, scales, rows, cols, blocks, act, p, ldx);
+    if (act == ONEBIT_ACT_NONE) return launch_after(k_restore_wide<T, ONEBIT_ACT_NONE>, grid, kCkThreads, s, codes, scales, w, p, ldx);
+    if (act == ONEBIT_ACT_RELU) return launch_after(k_restore_wide<T, ONEBIT_ACT_RELU>, grid, kCkThreads, s, codes, scales, w, p, ldx);
+    if (act == ONEBIT_ACT_GELU) return launch_after(k_restore_wide<T, ONEBIT_ACT_GELU>, grid, kCkThreads, s, codes, scales, w, p, ldx);
+    return launch_after(k_restore_wide<T, ONEBIT_ACT_GELU_TANH>, grid, kCkThreads, s, codes, scales, w, p, ldx);
   }
+  return launch_after(k_restore<T>, ck_grid(ceil_div(rows * blocks, kCkThreads / 32)), kCkThreads, s, codes, scales, rows, cols, blocks, act, p, ldx);
 }
 
 }  // namespace
@@ -212,10 +213,9 @@ extern "C" onebit_status_t onebit_checkpoint_compress(const void* x, int64_t ldx
   if (!disjoint({matrix(x, rows, ldx, cols, dtype_size(dtype))}, {span_of(codes, rows * cols), span_of(scales, rows * blocks * 4)}))
     return fail(ONEBIT_ERR_INVALID_ARG, "an output overlaps another buffer");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dtype == ONEBIT_F32) compress<float>(x, ldx, dtype, rows, (int)cols, codes, scales, s);
-  else if (dtype == ONEBIT_F16) compress<__half>(x, ldx, dtype, rows, (int)cols, codes, scales, s);
-  else compress<__nv_bfloat16>(x, ldx, dtype, rows, (int)cols, codes, scales, s);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = dtype == ONEBIT_F32   ? compress<float>(x, ldx, dtype, rows, (int)cols, codes, scales, s)
+                        : dtype == ONEBIT_F16 ? compress<__half>(x, ldx, dtype, rows, (int)cols, codes, scales, s)
+                                              : compress<__nv_bfloat16>(x, ldx, dtype, rows, (int)cols, codes, scales, s);
   return e == cudaSuccess ? ONEBIT_OK : cuda_fail(e, "onebit_checkpoint_compress");
 }
 
@@ -231,9 +231,8 @@ extern "C" onebit_status_t onebit_checkpoint_restore(const int8_t* codes, const 
   if (!disjoint({span_of(codes, rows * cols), span_of(scales, rows * blocks * 4)}, {matrix(x, rows, ldx, cols, dtype_size(dtype))}))
     return fail(ONEBIT_ERR_INVALID_ARG, "the output overlaps an input");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dtype == ONEBIT_F32) restore<float>(codes, scales, rows, (int)cols, activation, x, ldx, dtype, s);
-  else if (dtype == ONEBIT_F16) restore<__half>(codes, scales, rows, (int)cols, activation, x, ldx, dtype, s);
-  else restore<__nv_bfloat16>(codes, scales, rows, (int)cols, activation, x, ldx, dtype, s);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = dtype == ONEBIT_F32   ? restore<float>(codes, scales, rows, (int)cols, activation, x, ldx, dtype, s)
+                        : dtype == ONEBIT_F16 ? restore<__half>(codes, scales, rows, (int)cols, activation, x, ldx, dtype, s)
+                                              : restore<__nv_bfloat16>(codes, scales, rows, (int)cols, activation, x, ldx, dtype, s);
   return e == cudaSuccess ? ONEBIT_OK : cuda_fail(e, "onebit_checkpoint_restore");
 }

@@ -116,17 +116,15 @@ cudaError_t run_few_rows(const onebit_linear_t& a, cudaStream_t s) {
   const int64_t groups = ceil_div(a.out, 8), sms = sm_count();
   auto go = [&](auto m, auto g) {
     constexpr int kM = decltype(m)::value, kG = decltype(g)::value;
-    launch_after(k_few_rows<T, kM, kG>, (unsigned)ceil_div(groups, kG), kFewThreads, s, f);
+    return launch_after(k_few_rows<T, kM, kG>, (unsigned)ceil_div(groups, kG), kFewThreads, s, f);
   };
   using std::integral_constant;
   auto by_rows = [&](auto g) {
-    if (a.rows <= 16) go(integral_constant<int, 1>{}, g);
-    else go(integral_constant<int, 2>{}, g);
+    return a.rows <= 16 ? go(integral_constant<int, 1>{}, g) : go(integral_constant<int, 2>{}, g);
   };
-  if (groups >= 8 * sms) by_rows(integral_constant<int, 8>{});
-  else if (groups >= 3 * sms) by_rows(integral_constant<int, 2>{});
-  else by_rows(integral_constant<int, 1>{});
-  return cudaGetLastError();
+  if (groups >= 8 * sms) return by_rows(integral_constant<int, 8>{});
+  if (groups >= 3 * sms) return by_rows(integral_constant<int, 2>{});
+  return by_rows(integral_constant<int, 1>{});
 }
 
 }  // namespace layers

@@ -617,12 +617,12 @@ unsigned at_most(int64_t want, int64_t per_sm) {
 constexpr int kForwardCols = 512 * 4 * 8, kBackwardCols = 512 * 2 * 8;
 
 template <typename T, bool VEC>
-void launch_forward(const ForwardArgs& a, cudaStream_t s) {
+cudaError_t launch_forward(const ForwardArgs& a, cudaStream_t s) {
   auto go = [&](auto tpr, auto ch, auto nr, int per_sm) {
     constexpr int kTpr = decltype(tpr)::value, kCh = decltype(ch)::value, kNr = decltype(nr)::value, kThreads = kForwardThreads<kTpr>;
     const unsigned grid = at_most(ceil_div(a.rows, kThreads / kTpr * kNr), per_sm);
-    if (VEC && a.cols == kTpr * kCh * 8) launch_after(k_ln_forward<T, kTpr, kCh, kNr, VEC, VEC>, grid, kThreads, s, a);  // no bounds to test
-    else launch_after(k_ln_forward<T, kTpr, kCh, kNr, VEC, false>, grid, kThreads, s, a);
+    if (VEC && a.cols == kTpr * kCh * 8) return launch_after(k_ln_forward<T, kTpr, kCh, kNr, VEC, VEC>, grid, kThreads, s, a);  // no bounds to test
+    return launch_after(k_ln_forward<T, kTpr, kCh, kNr, VEC, false>, grid, kThreads, s, a);
   };
   using std::integral_constant;
   using One = integral_constant<int, 1>;
@@ -642,18 +642,18 @@ void launch_forward(const ForwardArgs& a, cudaStream_t s) {
       if (a.cols <= 1024) return go(integral_constant<int, 128>{}, One{}, Two{}, 5);
     }
     if constexpr (VEC) {
-      go(integral_constant<int, 128>{}, Two{}, Two{}, 5);
+      return go(integral_constant<int, 128>{}, Two{}, Two{}, 5);
     } else {
-      if (a.cols <= 1280) go(integral_constant<int, 160>{}, One{}, Two{}, 4);
-      else if (a.cols <= 1536) go(integral_constant<int, 192>{}, One{}, Two{}, 3);
-      else go(integral_constant<int, 256>{}, One{}, Two{}, 2);
+      if (a.cols <= 1280) return go(integral_constant<int, 160>{}, One{}, Two{}, 4);
+      if (a.cols <= 1536) return go(integral_constant<int, 192>{}, One{}, Two{}, 3);
+      return go(integral_constant<int, 256>{}, One{}, Two{}, 2);
     }
   };
-  if (a.cols <= 256) go(integral_constant<int, 32>{}, One{}, Two{}, 5);
-  else if (a.cols <= 2048) up_to_2048();
-  else if (a.cols <= 4096) go(integral_constant<int, 256>{}, Two{}, Two{}, 2);
-  else if (a.cols <= kForwardCols) go(integral_constant<int, 512>{}, Four{}, One{}, 1);
-  else launch_after(k_ln_forward_wide<T>, at_most(a.rows, 8), kLnThreads, s, a);
+  if (a.cols <= 256) return go(integral_constant<int, 32>{}, One{}, Two{}, 5);
+  if (a.cols <= 2048) return up_to_2048();
+  if (a.cols <= 4096) return go(integral_constant<int, 256>{}, Two{}, Two{}, 2);
+  if (a.cols <= kForwardCols) return go(integral_constant<int, 512>{}, Four{}, One{}, 1);
+  return launch_after(k_ln_forward_wide<T>, at_most(a.rows, 8), kLnThreads, s, a);
 }
 
 // The backward form for a width: threads a row, groups of eight columns a thread.  In 16 bits, read wide, a row of
@@ -664,7 +664,7 @@ void launch_forward(const ForwardArgs& a, cudaStream_t s) {
 template <typename T, bool VEC>
 constexpr bool kTwoGroups = VEC && sizeof(T) == 2;
 template <bool TWO, typename F>
-void with_backward_form(int64_t cols, F&& f) {
+auto with_backward_form(int64_t cols, F&& f) {
   using std::integral_constant;
   using One = integral_constant<int, 1>;
   using Two = integral_constant<int, 2>;
@@ -682,27 +682,25 @@ void with_backward_form(int64_t cols, F&& f) {
     if (cols <= 384 * 8) return f(integral_constant<int, 384>{}, One{});
     if (cols <= 4096) return f(integral_constant<int, 512>{}, One{});
   }
-  f(integral_constant<int, 512>{}, Two{});
+  return f(integral_constant<int, 512>{}, Two{});
 }
 // Blocks of the backward kernel, which are the parts that the parameters' gradients are summed from.
 template <bool TWO>
 int backward_parts(int64_t rows, int64_t cols) {
   if (rows == 0) return 0;
   if (cols > kBackwardCols) return (int)ceil_div(rows, ceil_div(rows, 64));
-  int parts = 0;
-  with_backward_form<TWO>(cols, [&](auto tpr, auto ch) {
+  return with_backward_form<TWO>(cols, [&](auto tpr, auto ch) {
     constexpr int kCh = decltype(ch)::value, kThreads = kBackThreads<decltype(tpr)::value, kCh>;
-    parts = (int)at_most(rows, kBackRoom<kCh> / kThreads);
+    return (int)at_most(rows, kBackRoom<kCh> / kThreads);
   });
-  return parts;
 }
 
 template <typename T, bool VEC, bool CODES>
-void launch_backward(const BackwardArgs& a, int parts, cudaStream_t s) {
-  with_backward_form<kTwoGroups<T, VEC>>(a.cols, [&](auto tpr, auto ch) {
+cudaError_t launch_backward(const BackwardArgs& a, int parts, cudaStream_t s) {
+  return with_backward_form<kTwoGroups<T, VEC>>(a.cols, [&](auto tpr, auto ch) {
     constexpr int kTpr = decltype(tpr)::value, kCh = decltype(ch)::value;
-    if (a.add) launch_after(k_ln_backward<T, kTpr, kCh, VEC, CODES, true>, parts, kBackThreads<kTpr, kCh>, s, a);
-    else launch_after(k_ln_backward<T, kTpr, kCh, VEC, CODES, false>, parts, kBackThreads<kTpr, kCh>, s, a);
+    if (a.add) return launch_after(k_ln_backward<T, kTpr, kCh, VEC, CODES, true>, parts, kBackThreads<kTpr, kCh>, s, a);
+    return launch_after(k_ln_backward<T, kTpr, kCh, VEC, CODES, false>, parts, kBackThreads<kTpr, kCh>, s, a);
   });
 }
 
@@ -712,18 +710,17 @@ cudaError_t launch_backward(const BackwardArgs& a, cudaStream_t s) {
   const bool vec = a.cols % 8 == 0 && on16(a.dy, a.lddy) && on16(a.x, a.ldx) && on16(a.add, a.ldadd) && on16(a.dx, a.lddx) && aligned(a.codes, 8) &&
                    aligned(a.gamma, 16);
   const int parts = vec ? backward_parts<kTwoGroups<T, true>>(a.rows, a.cols) : backward_parts<false>(a.rows, a.cols);
+  cudaError_t e = cudaSuccess;
   if (parts == 0) {  // no rows
   } else if (a.cols > kBackwardCols) {
-    launch_after(k_ln_backward_wide<T>, at_most(a.rows, 8), kLnThreads, s, a);
-    launch_after(k_ln_param_wide<T>, dim3((unsigned)ceil_div(a.cols, kLnThreads), (unsigned)parts), kLnThreads, s, a, ceil_div(a.rows, 64));
+    e = launch_after(k_ln_backward_wide<T>, at_most(a.rows, 8), kLnThreads, s, a);
+    if (e == cudaSuccess)
+      e = launch_after(k_ln_param_wide<T>, dim3((unsigned)ceil_div(a.cols, kLnThreads), (unsigned)parts), kLnThreads, s, a, ceil_div(a.rows, 64));
   } else if (vec) {
-    if (a.codes) launch_backward<T, true, true>(a, parts, s);
-    else launch_backward<T, true, false>(a, parts, s);
+    e = a.codes ? launch_backward<T, true, true>(a, parts, s) : launch_backward<T, true, false>(a, parts, s);
   } else {
-    if (a.codes) launch_backward<T, false, true>(a, parts, s);
-    else launch_backward<T, false, false>(a, parts, s);
+    e = a.codes ? launch_backward<T, false, true>(a, parts, s) : launch_backward<T, false, false>(a, parts, s);
   }
-  const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? sum_parts(a.grad_dtype, a.part, parts, 2 * (int64_t)a.cols, a.cols, a.dgamma, a.dbeta, s) : e;
 }
 
@@ -765,13 +762,9 @@ extern "C" onebit_status_t onebit_layer_norm_forward(const void* x, int64_t ldx,
                    aligned(gamma, 16) && aligned(beta, 16);
   auto go = [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
-    if (vec) launch_forward<T, true>(a, s);
-    else launch_forward<T, false>(a, s);
+    return vec ? launch_forward<T, true>(a, s) : launch_forward<T, false>(a, s);
   };
-  if (dtype == ONEBIT_F32) go((float*)nullptr);
-  else if (dtype == ONEBIT_F16) go((__half*)nullptr);
-  else go((__nv_bfloat16*)nullptr);
-  const cudaError_t ce = cudaGetLastError();
+  const cudaError_t ce = dtype == ONEBIT_F32 ? go((float*)nullptr) : dtype == ONEBIT_F16 ? go((__half*)nullptr) : go((__nv_bfloat16*)nullptr);
   return ce == cudaSuccess ? ONEBIT_OK : cuda_fail(ce, "onebit_layer_norm_forward");
 }
 

@@ -5,8 +5,9 @@
 // matching types, at least one row) is checked, its outputs allocated and the C entry called in one step, with the
 // tensors' device made current for that time.
 // Whatever else it meets -- another layout, an argument that does not fit, a status that is not OK -- it leaves
-// to layers.py by returning None: that path then does the call, or says what is wrong with it.  Nothing has
-// been enqueued when None is returned, as a call with a failed check enqueues nothing.
+// to layers.py by returning None: that path then does the call, or says what is wrong with it.  A call with a
+// failed check has enqueued nothing by then; one whose launch failed is enqueued again from its start, into new outputs
+// (or the caller's dw and db), and fails again.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>

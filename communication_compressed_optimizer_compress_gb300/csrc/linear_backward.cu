@@ -171,12 +171,14 @@ cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, b
       PlainEpilogue<float> to{};
       err = to_partials(&to, part, a.in);
       if (err == cudaSuccess) err = run_product<false, true>(a.dtype, dy, w, sx, plan, to, s);
-      launch_after(k_finish_dx<T>, flat_grid(a.rows * (part.ld / 4), 256), 256, s, part, a.rows, (int)a.in, v, a.activation, add, a.ldadd,
-                                                                   static_cast<T*>(a.dx), a.lddx, h, ldh);
+      if (err == cudaSuccess)
+        err = launch_after(k_finish_dx<T>, flat_grid(a.rows * (part.ld / 4), 256), 256, s, part, a.rows, (int)a.in, v, a.activation, add, a.ldadd,
+                           static_cast<T*>(a.dx), a.lddx, h, ldh);
     }
     if (err != cudaSuccess) return err;
   } else if (computed && run) {
-    launch_after(k_operand<T>, flat_grid(a.rows * a.in, 256), 256, s, v, a.rows, (int)a.in, a.activation, h, ldh);
+    err = launch_after(k_operand<T>, flat_grid(a.rows * a.in, 256), 256, s, v, a.rows, (int)a.in, a.activation, h, ldh);
+    if (err != cudaSuccess) return err;
   }
   if (a.dw) {
     const ProductPlan plan = plan_product(sw, sms);
@@ -192,7 +194,7 @@ cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, b
           PlainEpilogue<float> to{};
           err = to_partials(&to, part, a.in);
           if (err == cudaSuccess) err = run_product<true, true>(a.dtype, dy, x, sw, plan, to, s);
-          launch_after(k_finish_dw<G>, flat_grid(a.out * (part.ld / 4), 256), 256, s, part, a.out, (int)a.in, g);
+          if (err == cudaSuccess) err = launch_after(k_finish_dw<G>, flat_grid(a.out * (part.ld / 4), 256), 256, s, part, a.out, (int)a.in, g);
         }
       });
     if (err != cudaSuccess) return err;
@@ -213,7 +215,7 @@ cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, b
       if (err != cudaSuccess) return err;
     }
   }
-  return cudaGetLastError();
+  return err;
 }
 cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, bool run) {
   return a.dtype == ONEBIT_F16 ? backward<__half>(a, ws, s, run) : backward<__nv_bfloat16>(a, ws, s, run);

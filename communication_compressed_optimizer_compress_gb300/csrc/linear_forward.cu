@@ -85,8 +85,7 @@ cudaError_t forward(const onebit_linear_t& a, Space& ws, cudaStream_t s, bool ru
   err = to_partials(&to, part, a.out);
   if (err == cudaSuccess) err = run_product<false, false>(a.dtype, x, w, shape, plan, to, s);
   if (err != cudaSuccess) return err;
-  launch_after(k_finish_forward<T>, flat_grid(a.rows * e.blocks * 32, 256), 256, s, part, a.rows, (int)a.out, e);
-  return cudaGetLastError();
+  return launch_after(k_finish_forward<T>, flat_grid(a.rows * e.blocks * 32, 256), 256, s, part, a.rows, (int)a.out, e);
 }
 cudaError_t forward(const onebit_linear_t& a, Space& ws, cudaStream_t s, bool run) {
   return a.dtype == ONEBIT_F16 ? forward<__half>(a, ws, s, run) : forward<__nv_bfloat16>(a, ws, s, run);

@@ -1,8 +1,11 @@
-"""Arguments that the layer operators accept and have to get right: parameters that lie anywhere in a flat fp32
-buffer, as an optimizer's often do."""
+"""What the layer operators meet around their values: parameters that lie anywhere in a flat fp32 buffer, as an
+optimizer's often do, tensors of a device that is not current, errors of earlier calls."""
+import ctypes
+
 import pytest
 import torch
 
+import communication_compressed_optimizer_compress_gb300 as ob
 import test_gpu_layers as base
 from communication_compressed_optimizer_compress_gb300 import layers as L
 
@@ -77,3 +80,44 @@ def test_tensors_of_a_device_that_is_not_current():
     assert torch.cuda.current_device() == 0 and L.get_status(torch.cuda.default_stream(1)) == 0
     for a, b in zip(want, got):
         assert b.device.index == 1 and torch.equal(a, b.to("cuda:0"))
+
+
+def test_errors_of_earlier_code_are_not_reported_again():
+    """A call of the optimizer that fails on a capturing stream leaves its error pending in the runtime.  The layer
+    operators, through the binding, which would hand a failed call on, and layers.py, do their work all the same."""
+    cuda = ctypes.CDLL("libcuda.so.1")
+    opt = ob.OneBitAdam([torch.zeros(64, device="cuda")], n_workers=1, warmup_steps=1)
+    side = torch.cuda.Stream()
+
+    def fail():
+        torch.cuda.synchronize()
+        assert cuda.cuStreamBeginCapture_v2(ctypes.c_void_p(side.cuda_stream), 2) == 0
+        with pytest.raises(ob.OneBitError):
+            ob._check(ob.lib().onebit_adam_get_status(opt.h, ctypes.c_void_p(side.cuda_stream)), "onebit_adam_get_status")
+        graph = ctypes.c_void_p()
+        assert cuda.cuStreamEndCapture(ctypes.c_void_p(side.cuda_stream), ctypes.byref(graph)) != 0 and not graph
+
+    L._functions()
+    b = L._layers_binding
+    gen = base._gen(8)
+    x, w, dy = (base._randn(gen, *s, dtype=BF16, scale=0.3) for s in ((300, 264), (136, 264), (300, 136)))
+    few, v = x[:16], base._randn(gen, 264, shift=1.0)
+    ck, (_, mean, rstd) = L.compress(x), L.layer_norm(x, v, v)
+    need = ("dx", "dw", "db")
+    for call in (lambda: b.compress(x), lambda: b.compress(x[:, :9]), lambda: b.restore(ck, 0), lambda: b.layer_norm(x, v, v, 1e-5, True),
+                 lambda: b.layer_norm_backward(x, ck, v, mean, rstd, None, F32), lambda: b.linear(x, w, None, L.ACT_GELU, None, True),
+                 lambda: b.linear(few, w, None, 0, None, False), lambda: b.linear_backward(dy, ck, w, L.ACT_GELU, None, None, None, None, need)):
+        want = call()
+        fail()
+        got = call()
+        assert got is not None
+        flat = _tensors(got)
+        assert flat and all(torch.equal(p, q) for p, q in zip(flat, _tensors(want)))
+    fail()
+    assert L.compress(x[None]).codes.shape == (1, 300, 264)  # layers.py's own path
+    opt.free()
+    assert L.get_status() == ob.OK
+
+
+def _tensors(v):
+    return [v] if torch.is_tensor(v) else [t for p in v for t in _tensors(p)] if isinstance(v, (tuple, list)) else []
