@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -54,12 +55,15 @@ const at::Tensor& tensor(PyObject* o) {
   return THPVariable_Unpack(o);
 }
 
+// would it be detached in silence?  (layers.py says so)
+bool has_history(const at::Tensor& t) { return t.requires_grad() && at::GradMode::is_enabled(); }
+
 struct Matrix {
   const void* p;
   int64_t rows, cols, ld;
 };
 Matrix matrix(const at::Tensor& t) {
-  require(t.is_cuda() && t.dim() == 2);
+  require(t.is_cuda() && t.dim() == 2 && !has_history(t));
   const int64_t r = t.size(0), c = t.size(1), ld = t.stride(0);
   require(r > 0 && c > 0 && t.stride(1) == 1 && (ld >= c || r == 1));
   return {t.data_ptr(), r, c, r == 1 ? c : ld};
@@ -71,7 +75,7 @@ Matrix matrix(const at::Tensor& t, const at::Tensor& like, int64_t rows, int64_t
 }
 const float* vector(PyObject* o, int64_t n, const at::Tensor& like) {
   const at::Tensor& t = tensor(o);
-  require(t.scalar_type() == at::kFloat && t.numel() == n && t.is_contiguous() && t.device() == like.device());
+  require(t.scalar_type() == at::kFloat && t.numel() == n && t.is_contiguous() && t.device() == like.device() && !has_history(t));
   return static_cast<const float*>(t.data_ptr());
 }
 
@@ -312,7 +316,7 @@ PyObject* linear_backward(PyObject* const* a) {
   }
   auto given = [&](PyObject* o, int64_t n) {
     const at::Tensor& t = tensor(o);
-    require(t.scalar_type() == grad && t.numel() == n && t.is_contiguous() && t.device() == dy.device());
+    require(t.scalar_type() == grad && t.numel() == n && t.is_contiguous() && t.device() == dy.device() && !has_history(t));
     return t.data_ptr();
   };
   if (want[1]) {

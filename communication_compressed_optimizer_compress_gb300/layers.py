@@ -8,7 +8,8 @@ and every complaint, comes from here.
 
 Matrices are CUDA tensors whose last dimension is the features and has unit stride.  A 2-D tensor may
 have any row stride (a column slice of a wider buffer); one of more dimensions must be contiguous and
-counts as its leading dimensions' rows.  Gradients come in ``grad_dtype``, the type ``OneBitAdam`` was
+counts as its leading dimensions' rows.  Nothing is recorded for autograd: the backward pass is the
+operators' own, and with gradient mode on a tensor that requires a gradient is refused.  Gradients come in ``grad_dtype``, the type ``OneBitAdam`` was
 configured with, and may be written into the caller's tensors (``dw=``, ``db=``).
 
     y = W2 gelu(W1 x + b1) + b2 + x, then layer norm, with 8-bit checkpoints:
@@ -128,10 +129,18 @@ def _code(dtype, what: str) -> int:
         raise ValueError(f"{what}: dtype {dtype} is not float32, float16 or bfloat16") from None
 
 
+def _no_history(t, name: str):
+    """The operators record nothing for autograd: with gradient mode on, an input that requires a gradient would be
+    detached without a word, so it is refused."""
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name}: requires a gradient, which these operators do not record: call under torch.no_grad(), or detach it")
+
+
 def _matrix(t, name: str, cols=None, rows=None, dtype=None, device=None):
     """(rows, columns, row stride) of a tensor whose last dimension is the features."""
     if not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA tensor")
+    _no_history(t, name)
     shape = t.shape
     if len(shape) == 2:
         r, c = shape
@@ -162,6 +171,7 @@ def _vector(t, name: str, n: int, device, dtype=torch.float32):
         return None
     if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name}: expected {n} contiguous {dtype} values on {device}")
+    _no_history(t, name)
     return t.data_ptr()
 
 

@@ -121,3 +121,33 @@ def test_errors_of_earlier_code_are_not_reported_again():
 
 def _tensors(v):
     return [v] if torch.is_tensor(v) else [t for p in v for t in _tensors(p)] if isinstance(v, (tuple, list)) else []
+
+
+def test_tensors_that_require_a_gradient():
+    """Refused with gradient mode on, where the result would silently have no history; taken with it off."""
+    gen = base._gen(9)
+    make = lambda: {"x": base._randn(gen, 40, 64, dtype=BF16), "w": base._randn(gen, 32, 64, dtype=BF16),  # noqa: E731
+                    "dy": base._randn(gen, 40, 32, dtype=BF16), "res": base._randn(gen, 40, 32, dtype=BF16),
+                    "v": base._randn(gen, 64), "b": base._randn(gen, 32), "dw": torch.zeros(32, 64, device="cuda"),
+                    "mean": base._randn(gen, 40), "codes": torch.zeros(40, 1, device="cuda")}
+    ck8 = torch.zeros(40, 64, dtype=torch.int8, device="cuda")
+    calls = {
+        "x": [lambda t: L.compress(t["x"]), lambda t: L.layer_norm(t["x"], t["v"], t["v"]), lambda t: L.linear(t["x"], t["w"]),
+              lambda t: L.linear_backward(t["dy"], t["x"], t["w"]), lambda t: L.layer_norm_backward(t["x"], t["x"], t["v"], t["mean"], t["mean"]),
+              lambda t: L.compress(t["x"][None])],
+        "w": [lambda t: L.linear(t["x"], t["w"]), lambda t: L.linear_backward(t["dy"], t["x"], t["w"])],
+        "dy": [lambda t: L.linear_backward(t["dy"], t["x"], t["w"])], "res": [lambda t: L.linear(t["x"], t["w"], residual=t["res"])],
+        "v": [lambda t: L.layer_norm(t["x"], t["v"], t["v"]), lambda t: L.layer_norm_backward(t["x"], t["x"], t["v"], t["mean"], t["mean"])],
+        "b": [lambda t: L.linear(t["x"], t["w"], t["b"])], "dw": [lambda t: L.linear_backward(t["dy"], t["x"], t["w"], dw=t["dw"], grad_dtype=F32)],
+        "codes": [lambda t: L.restore(L.Checkpoint(ck8, t["codes"], BF16))],
+    }
+    for name, fs in calls.items():
+        for f in fs:
+            t = make()
+            f(t)
+            t[name].requires_grad_()
+            with pytest.raises(ValueError, match="requires a gradient"):
+                f(t)
+            with torch.no_grad():
+                f(t)
+            f({k: v.detach() for k, v in t.items()})
