@@ -120,7 +120,10 @@ cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, b
   const int sms = sm_count();
   const ProductShape sx{a.rows, a.in, a.out}, sw{a.out, a.in, a.rows};
   const Kept<T> v{static_cast<const T*>(a.x), a.ldx, a.codes, a.scales, (int)a.in, (int)ceil_div(a.in, kBlock)};
-  const bool computed = a.dw && (a.codes || a.activation != ONEBIT_ACT_NONE);  // act(v) is not in memory yet
+  // act(v) is not in memory yet.  It is rounded to 16 bits for dw's product: the tensor cores take 16-bit operands, and the
+  // forward pass rounded the h = act(v) that it multiplied w with the same way, so that this is dw at that h; a second
+  // product with what the rounding leaves off would double dw's time for digits that the forward pass did not have.
+  const bool computed = a.dw && (a.codes || a.activation != ONEBIT_ACT_NONE);
   const int64_t ldh = pad8(a.in);
   T* h = computed ? ws.take<T>(a.rows * ldh) : nullptr;
   Readable copies;

@@ -405,7 +405,8 @@ def linear_backward(dy, x, w, activation=ACT_NONE, add=None, grad_dtype=None, dw
     """(dx, dw, db) of y = activation(x) w^T + bias, given dy: x is the value before the activation that
     precedes the product (with ACT_NONE the product's input), a tensor or its Checkpoint; ``add`` joins
     dx.  grad_dtype (default dy's) is the type of dw (out x in) and db; ``dw`` and ``db`` may be the
-    caller's contiguous tensors.  What ``need`` leaves out is None."""
+    caller's contiguous tensors.  What ``need`` leaves out is None.  Whatever grad_dtype, dw is
+    summed in fp32 from dy and activation(x) rounded to 16 bits, as the forward product takes it."""
     if stream is not None:
         with _on(stream, dy):
             return linear_backward(dy, x, w, activation, add, grad_dtype, dw, db, need)

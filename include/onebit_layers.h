@@ -114,8 +114,10 @@ onebit_status_t onebit_linear_forward(const onebit_linear_t* a, void* workspace,
 /* Backward of y = activation(v) w^T + bias with respect to v, w and bias, given dy:
  *   dx = (dy w) * activation'(v) [+ add];  dw = dy^T activation(v);  db = sum over rows of dy
  * v, the value before the activation that precedes the product, is x (codes = scales = NULL) or its
- * 8-bit checkpoint (x = NULL); with ONEBIT_ACT_NONE v is the product's input itself.  A 16-bit
- * activation(v) that has to be computed is rounded to dtype before it enters the product for dw.
+ * 8-bit checkpoint (x = NULL); with ONEBIT_ACT_NONE v is the product's input itself.  An
+ * activation(v) or a value of a checkpoint that has to be computed is rounded to dtype before it enters
+ * the product for dw, as the forward pass rounded what it multiplied w with: dw in fp32 is the fp32 sum
+ * of those products, and good to dtype's digits as the derivative at an unrounded activation(v).
  * dy: rows x out, dx and add: rows x in, of dtype; dw: out x in contiguous, db: out, of grad_dtype.
  * dx, dw and db may each be NULL (not wanted); x and codes may both be NULL when only dx without an
  * activation, or only db, is wanted. */

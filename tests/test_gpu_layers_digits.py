@@ -160,3 +160,31 @@ def test_reciprocal_deviations_at_the_ends():
     sign = (1 - 2 * (torch.arange(64, device="cuda") % 2)).float()
     x = torch.stack([3.0 * torch.ones_like(sign), 2.0 ** 100 * sign, 2.0 ** -65 * sign])
     assert L.layer_norm(x, g, g, 0.0)[2].tolist() == [math.inf, 0.0, 2.0 ** 65]
+
+
+@pytest.mark.parametrize("kept", ["x", "checkpoint"])
+@pytest.mark.parametrize("act", list(L.ACTIVATIONS.values()), ids=list(L.ACTIVATIONS))
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=base.ids)
+@pytest.mark.parametrize("shape,need", [((300, 264, 136), ("dx", "dw", "db")), ((333, 520, 1030), ("dw", "db")), ((4096, 512, 256), ("dx", "dw", "db")),
+                                        ((9000, 200, 203), ("dx", "dw", "db"))], ids=str)
+def test_fp32_gradients_through_an_activation(shape, need, dtype, act, kept):
+    """dw in fp32 is dy^T h in fp32 for the h that the forward pass multiplied the weight with: act(v), rounded once to 16
+    bits.  Elements of h that lie closer to the middle of two 16-bit values than act(v) is computed may be either of them."""
+    rows, cols, out = shape
+    gen = base._gen(rows + cols)
+    v = base._randn(gen, rows, cols, dtype=dtype, shift=0.1)
+    w, dy = base._randn(gen, out, cols, dtype=dtype, scale=0.1), base._randn(gen, rows, out, dtype=dtype, scale=0.1)
+    src, v64 = v, v.double()
+    if kept == "checkpoint":
+        src = L.compress(v)
+        v64 = base.values64(src)
+    dx, dw, db = L.linear_backward(dy, src, w, act, grad_dtype=F32, need=need)
+    assert dw.dtype == F32 and db.dtype == F32 and (dx is None) == ("dx" not in need)
+    h = base.act64(act, v64)
+    err = 2.0 ** -20 * (1 + v64.abs()) * (act > 1) + 2.0 ** -22 * v64.abs() * (kept == "checkpoint")
+    low, high = ((h + s * err).float().to(dtype).double() for s in (-1, 1))
+    size = dy.double().abs()
+    want = dy.double().t() @ ((low + high) / 2)
+    tol = size.t() @ ((high - low).abs() / 2) + (rows + 2) * 2.0 ** -23 * (size.t() @ h.abs())
+    base._within(dw, want, tol + base._rounding(want, F32), "dw")
+    base._within(db, dy.double().sum(0), (min(rows, 512) + 32) * 2.0 ** -24 * size.sum(0), "db")
