@@ -127,7 +127,7 @@ struct ForwardArgs {
 template <int TPR>
 constexpr int kForwardThreads = TPR < 128 ? 128 / TPR * TPR : TPR;
 template <typename T, int TPR, int CH, bool VEC>
-constexpr int kForwardRoom = VEC && sizeof(T) == 2 && CH == 1 && TPR > 64 ? 1024 : TPR < 256 ? 640 : 512;  // threads an SM
+constexpr int kForwardRoom = VEC && sizeof(T) == 2 && CH == 1 && TPR > 64 ? 1024 : TPR < 256 && !(TPR == 32 && CH == 2) ? 640 : 512;  // threads an SM
 
 // NR rows at a time (1 or 2): their sums go through the shuffles and the barrier together.  gamma and beta stay in registers
 // where they fit beside the rows; elsewhere they are read (from L1) once for the NR rows.  16384 x 1024 bf16 with the
@@ -632,9 +632,11 @@ cudaError_t launch_forward(const ForwardArgs& a, cudaStream_t s) {
   // Single elements and fp32 need more registers a column: up to 2048 (wide fp32: 1024) columns a thread has eight and
   // a row the fewest warps that hold it (4099 x 1155 fp32 by single elements: 9.6 us with 160 threads, 19.8 with 128 and
   // sixteen columns each; 16384 x 1024 wide fp32: 23.9 with 128, 28.1 with a warp, but 8192 x 2048 28.5 and 24.5).
+  // A warp has a 16-bit row of up to 512 columns, at 128 registers a thread (16384 x 512 6.5 us; at 96, where it spills,
+  // 7.2; one row at a time 8.0; two warps a row 9.7).
   auto up_to_2048 = [&] {
     if constexpr (kLean) {
-      if (a.cols <= 512) return go(integral_constant<int, 32>{}, Four{}, One{}, 5);
+      if (a.cols <= 512) return go(integral_constant<int, 32>{}, Two{}, Two{}, 4);
       if (a.cols <= 768) return go(integral_constant<int, 96>{}, One{}, Two{}, 10);
       if (a.cols <= 1024) return go(integral_constant<int, 128>{}, One{}, Two{}, 8);
     } else {
@@ -652,6 +654,8 @@ cudaError_t launch_forward(const ForwardArgs& a, cudaStream_t s) {
   if (a.cols <= 256) return go(integral_constant<int, 32>{}, One{}, Two{}, 5);
   if (a.cols <= 2048) return up_to_2048();
   if (a.cols <= 4096) return go(integral_constant<int, 256>{}, Two{}, Two{}, 2);
+  // (8192 x 8192 bf16: 54 us, with 512 threads and half the columns each 73, in the form of 16384 columns 81)
+  if (a.cols <= 8192) return go(integral_constant<int, 256>{}, Four{}, One{}, 2);
   if (a.cols <= kForwardCols) return go(integral_constant<int, 512>{}, Four{}, One{}, 1);
   return launch_after(k_ln_forward_wide<T>, at_most(a.rows, 8), kLnThreads, s, a);
 }
