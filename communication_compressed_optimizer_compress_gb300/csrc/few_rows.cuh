@@ -4,8 +4,8 @@
 // and by the latency of a launch.  A tile of the products' kernel would be 128 rows of which 16 are there, and
 // 32 blocks would pull the weight; here every warp of the GPU pulls a part of it at once.  A block has 8*G
 // columns; its eight warps share them G ways and the contraction 8/G ways, and add up in shared memory, in
-// order.  Each lane keeps kAhead 16-byte pieces of the weight in flight.  16 x 1024 x 4096 with gelu: 5.0 us back to
-// back, 10.3 by the products' kernel.
+// order.  Each lane keeps kAhead 16-byte pieces of the weight in flight.  16 x 1024 x 4096: the kernel takes 4.3 us with the
+// weight in HBM, 3.4 with it in L2; with gelu, called from Python back to back, 4.9 us, 10.3 by the products' kernel.
 //
 // The products are 16x8x16 warp instructions.  The contraction index is dealt to them in an order of its own:
 // lane (n, q) of a column group holds eight neighbouring k of column n, which are the four pairs that it owes to two
@@ -108,8 +108,12 @@ __global__ void __launch_bounds__(kFewThreads) k_few_rows(const FewRowsArgs A) {
 inline bool few_rows(const onebit_linear_t& a) {
   return a.rows <= kFewRows && !a.codes && a.in % 8 == 0 && vec16(a.x, a.ldx) && vec16(a.w, a.ldw);
 }
-// Columns a block: as many as still leave two blocks for most SMs, as more warps a column shorten the
-// contraction's chain (1024 -> 4096: G = 2; 4096 -> 1024: G = 1).
+// Groups a block: the fewest with which a warp's part of the contraction fills most of its kAhead pieces in flight, as
+// more warps a column shorten its chain; a short contraction leaves them room for more columns, which read x less often.
+// us by 1, 2, 4, 8 groups, one row, weights from HBM: 4096 -> 4096 9.0 14.9 23.0 28.8, 1024 -> 4096 3.8 4.7 6.6 8.4,
+// 768 -> 4096 3.5 4.3 5.2 6.6, 512 -> 4096 2.9 2.8 3.8 4.8, 256 -> 4096 2.6 2.1 2.1 2.2, 256 -> 8192 4.2 3.3 2.6 2.9,
+// 512 -> 1024 1.9 2.1 2.9 3.2.  Very many columns and a small x end that: eight groups (16 rows of 1024 -> 32768 19.3 and
+// 16.9, of 1024 -> 20480 13.2 and 15.7; 32 rows of 1024 -> 32768 30.3 and 43.3).
 template <typename T>
 cudaError_t run_few_rows(const onebit_linear_t& a, cudaStream_t s) {
   const FewRowsArgs f{a.x, a.ldx, a.w, a.ldw, a.bias, a.residual, a.ldr, a.y, a.ldy, (int)a.rows, (int)a.in, (int)a.out, a.activation};
@@ -122,8 +126,9 @@ cudaError_t run_few_rows(const onebit_linear_t& a, cudaStream_t s) {
   auto by_rows = [&](auto g) {
     return a.rows <= 16 ? go(integral_constant<int, 1>{}, g) : go(integral_constant<int, 2>{}, g);
   };
-  if (groups >= 8 * sms) return by_rows(integral_constant<int, 8>{});
-  if (groups >= 3 * sms) return by_rows(integral_constant<int, 2>{});
+  if (groups >= 24 * sms && a.rows <= 16) return by_rows(integral_constant<int, 8>{});
+  if (a.in < 384 && groups >= 2 * sms) return by_rows(integral_constant<int, 4>{});
+  if (a.in < 640 && groups >= sms) return by_rows(integral_constant<int, 2>{});
   return by_rows(integral_constant<int, 1>{});
 }
 

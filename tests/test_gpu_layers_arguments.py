@@ -151,3 +151,17 @@ def test_tensors_that_require_a_gradient():
             with torch.no_grad():
                 f(t)
             f({k: v.detach() for k, v in t.items()})
+
+
+@pytest.mark.parametrize("rows", [1, 16, 17, 32])
+@pytest.mark.parametrize("cols", [8, 136, 376, 384, 632, 640])
+@pytest.mark.parametrize("groups", [151, 152, 303, 304, 3647, 3648])
+def test_few_rows_on_both_sides_of_the_block_widths(groups, cols, rows):
+    """Outputs of 8 columns a group, less three, where the columns of a block change on 152 SMs."""
+    out = 8 * groups - 3
+    gen = base._gen(groups + rows)
+    x, w, b = base._randn(gen, rows, cols, dtype=BF16), base._randn(gen, out, cols, dtype=BF16, scale=0.1), base._randn(gen, out)
+    res = base._randn(gen, rows, out, dtype=BF16)
+    z, want, size = base._forward64(x, w, b, L.ACT_GELU, res)
+    tol = base._rounding(want, BF16) + 1.13 * (cols + 2) * 2.0 ** -23 * size + 2.0 ** -20 * (1 + z.abs()) + 2.0 ** -23 * res.double().abs()
+    base._within(L.linear(x, w, b, L.ACT_GELU, res), want, tol, "y")
