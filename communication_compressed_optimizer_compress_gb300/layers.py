@@ -197,10 +197,10 @@ def _stream(device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-# Outputs.  An allocation is most of what a small call costs the host, and one from plain integers costs
-# half of one from a shape, so the 2-D case is written out.
-def _like(t):
-    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+# Outputs, always of rows without gaps.  An allocation is most of what a small call costs the host, and one from plain
+# integers costs half of one from a shape, so the 2-D case is written out.
+def _like(t, dtype=None):
+    return torch.empty(t.shape, dtype=dtype or t.dtype, device=t.device)
 
 
 def _rows_of(t, rows, device):
@@ -290,7 +290,7 @@ def restore(ck: Checkpoint, activation=ACT_NONE, stream=None):
         return fast
     _, _, codes, scales, rows, cols, dtype, device = _kept(ck, "ck")
     with torch.cuda.device(device):
-        x = torch.empty_like(ck[0], dtype=dtype)
+        x = _like(ck[0], dtype)
         st = _functions().onebit_checkpoint_restore(codes, scales, rows, cols, activation, x.data_ptr(), cols, _code(dtype, "ck"),
                                                     _stream(device))
     if st:

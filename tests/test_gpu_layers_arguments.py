@@ -8,6 +8,7 @@ import torch
 import communication_compressed_optimizer_compress_gb300 as ob
 import test_gpu_layers as base
 from communication_compressed_optimizer_compress_gb300 import layers as L
+from test_gpu_layers_binding import both  # noqa: F401  (a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -165,3 +166,22 @@ def test_few_rows_on_both_sides_of_the_block_widths(groups, cols, rows):
     z, want, size = base._forward64(x, w, b, L.ACT_GELU, res)
     tol = base._rounding(want, BF16) + 1.13 * (cols + 2) * 2.0 ** -23 * size + 2.0 ** -20 * (1 + z.abs()) + 2.0 ** -23 * res.double().abs()
     base._within(L.linear(x, w, b, L.ACT_GELU, res), want, tol, "y")
+
+
+@pytest.mark.parametrize("rows,cols,out", [(1, 8, 8), (16, 1024, 136), (33, 72, 200), (700, 264, 520), (257, 63, 1), (2500, 520, 264)])
+@pytest.mark.parametrize("pad", [0, 8, 3])
+def test_both_ways_from_python_agree(both, rows, cols, out, pad):
+    """The binding and layers.py, bit for bit, where the kernels behind a call differ: few rows, single and paired blocks, cut
+    contractions, aligned and odd rows."""
+    gen = base._gen(rows + cols + out)
+    lay = lambda r, c: base._randn(gen, r, c + pad, dtype=BF16, scale=0.3)[:, :c]  # noqa: E731
+    x, w, dy, res = lay(rows, cols), lay(out, cols), lay(rows, out), lay(rows, out)
+    b, v = base._randn(gen, out), base._randn(gen, cols)
+    both(lambda: L.linear(x, w, b, L.ACT_GELU, res))
+    both(lambda: L.linear(x, w, None, L.ACT_RELU, checkpoint=True))
+    kept = both(lambda: L.compress(x))
+    both(lambda: L.restore(kept, L.ACT_GELU_TANH))
+    _, mean, rstd, ck = both(lambda: L.layer_norm(x, v, v, 1e-5, checkpoint=True))
+    both(lambda: L.layer_norm_backward(x, ck, v, mean, rstd, add=x, grad_dtype=BF16))
+    for src, act in ((x, L.ACT_NONE), (kept, L.ACT_GELU)):
+        both(lambda: L.linear_backward(dy, src, w, act, add=x, grad_dtype=F32))

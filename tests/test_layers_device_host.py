@@ -68,7 +68,7 @@ def machine(monkeypatch):
         return Tensor(*shape, dtype=dtype, device=device)
 
     fake = types.SimpleNamespace(
-        empty=empty, empty_like=lambda t, dtype=None: empty(*t.shape, dtype=dtype or t.dtype, device=t.device),
+        empty=empty,
         cuda=types.SimpleNamespace(device=device, stream=stream),
         is_grad_enabled=lambda: False,
         _C=types.SimpleNamespace(_cuda_getCurrentRawStream=lambda index: 1000 + index),
