@@ -1,8 +1,9 @@
 """Compile the CUDA library in-tree for sm_103a (nvcc only, no cmake).
 
 build() makes libonebit_adam.so.  build(checked=True) makes libonebit_adam_checked.so, the same
-library compiled with -DONEBIT_CHECKS: every kernel checks its units of work against its buffers
-before touching them, skips any that fail and reports them through onebit_adam_get_status().  The
+library compiled with -DONEBIT_CHECKS: every kernel of the optimizer's steps checks its units of work
+against its buffers before touching them, skips any that fail and reports them through
+onebit_adam_get_status() (the layer operators have no such checks and are the same in it).  The
 package loads the checked library when the environment variable ONEBIT_LIBRARY is "checked".
 """
 from __future__ import annotations

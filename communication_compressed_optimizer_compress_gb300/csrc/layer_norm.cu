@@ -384,11 +384,11 @@ struct KeptRow<T, TPR, CH, false, true> {
 };
 
 // dx of every row, and this block's share of dgamma and dbeta.  Each thread adds up its own columns over
-// the rows that it meets; at the end the block's row groups are joined in shared memory, in a fixed order.  Bound by
-// instruction issue with four warps to a row of 1024 columns (62% of the slots, 1370 instructions a row,
-// 29.6 us at 16384 rows from the checkpoint with `add`), so two warps have it, sixteen columns a thread: 27.6 us.
-// Single elements wait for their loads, gamma's among them: 4099 x 1155 fp32 21.1 us with gamma read for every
-// row (36% of the issue slots), 16.2 with gamma in registers.
+// the rows that it meets; at the end the block's row groups are joined in shared memory, in a fixed order.  16384 x 1024
+// bf16 from the checkpoint with `add`: 26.7 us with the sums of the parts behind it, 118 MB at 4.4 TB/s; 49% of the issue
+// slots, 16 warps an SM by their registers.  Four warps to a row were bound by issue (on one earlier build 29.6 us, 62%
+// of the slots, where two warps took 27.6).  Single elements wait for their loads: 4099 x 1155 fp32 13.6 us (on one earlier
+// build 21.1 with gamma read for every row, 16.2 with gamma in registers).
 template <typename T, int TPR, int CH, bool VEC, bool CODES, bool ADD>
 __global__ void __launch_bounds__(kBackThreads<TPR, CH>, kBackRoom<CH> / kBackThreads<TPR, CH>) k_ln_backward(const BackwardArgs A) {
   in_turn();
@@ -613,7 +613,8 @@ unsigned at_most(int64_t want, int64_t per_sm) {
   return (unsigned)(want < most ? want : most);
 }
 
-// the widest row of the forward and backward forms that hold rows in registers
+// the widest row of the forward and backward forms that hold rows in registers; wider ones are read again for each step
+// (backward of 4096 x 8192 bf16 52 us, of 4096 x 8200 143)
 constexpr int kForwardCols = 512 * 4 * 8, kBackwardCols = 512 * 2 * 8;
 
 template <typename T, bool VEC>
@@ -661,8 +662,8 @@ cudaError_t launch_forward(const ForwardArgs& a, cudaStream_t s) {
 }
 
 // The backward form for a width: threads a row, groups of eight columns a thread.  In 16 bits, read wide, a row of
-// more than 512 columns has few threads with two groups each (16384 x 1024 bf16 24.6 us, 27.4 with one; x 512 18.7 and
-// 16.8); single elements and fp32 need more registers a column, so there a thread has one
+// more than 512 columns has few threads with two groups each (whole calls on one build, from x: 16384 x 1024 bf16 24.6 us,
+// 27.4 with one; x 512 18.7 and 16.8); single elements and fp32 need more registers a column, so there a thread has one
 // group and a row the fewest warps that hold it (16384 x 1024 fp32 with two groups a thread spilled; 4099 x 1155 fp32
 // by single elements 20.8 us with 160 threads a row, 23.3 with 256).
 template <typename T, bool VEC>

@@ -13,13 +13,13 @@
 // rows and half of B's, and the even block's instructions use both halves: each SM's shared memory
 // then feeds a 256x256 tile with the traffic of a 128x128 one.
 //
-// Bound by the tensor cores where the epilogue is short (16384 x 4096 x 1024: 87 us, 1580 TFLOP/s of the 1878 measured
-// for the library's products), by epilogue and tensor cores together with gelu and codes (8.5 us a pair's tile of 1024
-// terms, of which the products alone take 5.0 and the epilogue alone 4.8), and by 64 bytes a clock into an SM where single
+// Bound by the tensor cores where the epilogue is short (16384 x 4096 x 1024: 84 us, 1630 TFLOP/s of the 1878 measured
+// for the library's products), by epilogue and tensor cores together with gelu and codes (16384 x 1024 x 4096 103 us, with
+// gelu alone 90, where its 14 waves of tiles need 70 for the products by themselves), and by 64 bytes a clock into an SM where single
 // blocks have a tile each (0.26 us a slab).
 //
-// A product that is stored in fp32 (dw over many tokens, partial sums) is accumulated in chunks of
-// kFoldSlabs slabs, whose sums the epilogue warps add up in registers: the tensor cores' own running
+// A product without an activation epilogue (dw in any type, whose contraction is all tokens, and partial sums) is
+// accumulated in chunks of kFoldSlabs slabs, whose sums the epilogue warps add up in registers: the tensor cores' own running
 // sum loses about 2^-26 of its size a step (measured: 1.9e-6 of the result's norm after 2048 terms).
 #pragma once
 
@@ -492,7 +492,9 @@ __device__ __forceinline__ ActConsts shared_consts(const f2* consts) {
 
 // The activation, and what the kept value is, are template parameters of the epilogues of pairs: with them
 // decided at run time inside the loop the register allocation of the alternatives met in copies, 100 to 300 of
-// a unit's 700 to 1700 instructions.  kAny decides at run time (the single blocks of small products).
+// a unit's 700 to 1700 instructions.  kAny decides at run time: the single blocks of small products, and in pairs a
+// residual together with an activation or a checkpoint (16384 x 1024 x 4096 with gelu, residual and checkpoint 130 us,
+// without the residual, in its own form, 103; 88 bytes of its registers spill).
 constexpr int kAny = -1;
 enum Kept16 { kKeptNone = 0, kKeptValue = 1, kKeptCodes = 2 };
 

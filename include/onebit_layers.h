@@ -106,7 +106,9 @@ typedef struct {
   int32_t activation;
 } onebit_linear_t;
 
-/* Bytes of device workspace (256-byte aligned; 0 is usual) that this call needs. */
+/* Bytes of device workspace (256-byte aligned) that this call needs: 0 where rows lie on 16 bytes and the contraction
+ * is not cut.  (onebit_linear_backward needs some also for an activation or a checkpoint behind dw, and for db of more
+ * than 512 rows.) */
 onebit_status_t onebit_linear_forward_workspace(const onebit_linear_t* a, size_t* bytes);
 onebit_status_t onebit_linear_forward(const onebit_linear_t* a, void* workspace, size_t workspace_bytes,
                                       onebit_stream_t stream);
