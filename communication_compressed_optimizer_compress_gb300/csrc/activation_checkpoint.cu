@@ -47,8 +47,8 @@ namespace {
 // Both kernels move every byte once and are bound by that.  Wide form: a thread has 16 columns (32 or 64
 // bytes in, 16 bytes of codes out), so that four threads share a scale and find the block's largest
 // magnitude with two shuffles; a block takes runs of about kCkRun elements of whole rows.  It needs rows
-// that start on 16 bytes and a multiple of 16 columns.  Any other matrix takes the narrow form: one warp
-// per 64 columns, a lane with two of them.  16384 x 4096 bf16: 36 us each way back to back, 205 MB at 5.7 TB/s (84% of
+// that start on 32 bytes, codes on 16 and a multiple of 16 columns.  Any other matrix takes the narrow form: one warp
+// per 64 columns, a lane with two of them.  16384 x 4096 bf16: 36 us each way back to back, 205 MB at 5.7 TB/s (83% of
 // a plain copy's rate).
 constexpr int kCkThreads = 256;
 constexpr int kCkRun = 16384;

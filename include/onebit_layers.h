@@ -13,8 +13,8 @@
  *   - Calls run on the calling thread's current device, which has to be the buffers' and the stream's.
  *   - A matrix is row-major with unit column stride: element (r, c) is at base + r*ld + c, with the
  *     row stride ld >= columns in elements.  Bases may have any alignment that the type needs, and
- *     ld any value; rows that start on 16-byte boundaries take the wide loads (layer norm: where gamma
- *     and beta lie on 16 bytes too).
+ *     ld any value; rows that start on 16-byte boundaries take the wide accesses (checkpoints: on 32-byte
+ *     boundaries; layer norm: where gamma and beta lie on 16 bytes too).
  *   - dtype is onebit_dtype_t and names the type of x, y, dy, dx, residual and add.  Parameters that
  *     the optimizer holds in fp32 (gamma, beta, bias) are read in fp32; the linear layer's weight is
  *     read in dtype, as the 16-bit copy that a mixed-precision step makes of it.
