@@ -10,6 +10,8 @@
 // (or the caller's dw and db), and fails again.
 #include <Python.h>
 
+#include <string.h>
+
 #include <ATen/core/Tensor.h>
 #include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
@@ -32,8 +34,18 @@ struct Entries {
   decltype(&onebit_linear_forward) forward;
   decltype(&onebit_linear_backward_workspace) backward_workspace;
   decltype(&onebit_linear_backward) backward;
+  decltype(&onebit_gated_linear_forward_workspace) gated_forward_workspace;
+  decltype(&onebit_gated_linear_forward) gated_forward;
+  decltype(&onebit_gated_linear_backward_workspace) gated_backward_workspace;
+  decltype(&onebit_gated_linear_backward) gated_backward;
+  decltype(&onebit_dropout) dropout;
+  decltype(&onebit_residual_norm_forward) rn_forward;
+  decltype(&onebit_residual_norm_backward_workspace) rn_workspace;
+  decltype(&onebit_residual_norm_backward) rn_backward;
 } g_entry;
+constexpr int kEntries = 17;
 PyTypeObject* g_checkpoint = nullptr;  // layers.Checkpoint
+PyTypeObject *g_gated = nullptr, *g_norm = nullptr, *g_norm_grads = nullptr;  // layers.Gated, ResidualNorm, ResidualNormGrads
 
 struct Decline {};  // to layers.py
 
@@ -332,6 +344,230 @@ PyObject* linear_backward(PyObject* const* a) {
                !want[2] ? none() : a[7] != Py_None ? Py_NewRef(a[7]) : wrap(std::move(db))});
 }
 
+// an instance of one of the named tuples
+PyObject* named(PyTypeObject* type, std::initializer_list<PyObject*> items) {
+  PyObject* args = pack(items);
+  if (!args) return nullptr;
+  PyObject* r = PyObject_CallObject(reinterpret_cast<PyObject*>(type), args);
+  Py_DECREF(args);
+  return r;
+}
+PyObject* wrap_or_none(at::Tensor t) { return t.defined() ? wrap(std::move(t)) : none(); }
+bool is(PyObject* o, const char* text) { return PyUnicode_Check(o) && PyUnicode_CompareWithASCIIString(o, text) == 0; }
+
+// The names in the tuple `need`, of three.
+void wanted(PyObject* need, const char* const (&names)[3], bool (&want)[3]) {
+  require(PyTuple_Check(need));
+  for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(need); ++i)
+    for (int k = 0; k < 3; ++k)
+      if (is(PyTuple_GET_ITEM(need, i), names[k])) want[k] = true;
+}
+
+// gated_linear(x, w, bias, activation, keep)
+PyObject* gated_linear(PyObject* const* a) {
+  const at::Tensor& x = tensor(a[0]);
+  const at::Tensor& w = tensor(a[1]);
+  const Matrix mx = matrix(x), mw = matrix(w);
+  const c10::cuda::CUDAGuard guard(x.device());
+  require(mw.cols == mx.cols && mw.rows % 2 == 0 && w.scalar_type() == x.scalar_type() && w.device() == x.device());
+  onebit_gated_linear_t p{};
+  p.dtype = dtype_code(x.scalar_type());
+  p.x = mx.p, p.ldx = mx.ld, p.w = mw.p, p.ldw = mw.ld;
+  p.rows = mx.rows, p.in = mx.cols, p.inner = mw.rows / 2;
+  if (a[2] != Py_None) p.bias = vector(a[2], mw.rows, x);
+  p.activation = integer(a[3]);
+  at::Tensor h = empty({p.rows, p.inner}, x.scalar_type(), x);
+  p.h = h.data_ptr(), p.ldh = p.inner;
+  if (a[4] == Py_None) {
+    with_workspace(g_entry.gated_forward, g_entry.gated_forward_workspace, p, x);
+    return wrap(std::move(h));
+  }
+  if (is(a[4], "values")) {
+    at::Tensor z = empty({p.rows, mw.rows}, x.scalar_type(), x);
+    p.z = z.data_ptr(), p.ldz = mw.rows;
+    with_workspace(g_entry.gated_forward, g_entry.gated_forward_workspace, p, x);
+    return pack({wrap(std::move(h)), wrap(std::move(z))});
+  }
+  require(is(a[4], "checkpoint"));
+  const NewCheckpoint gate(p.rows, p.inner, x), up(p.rows, p.inner, x);
+  p.gate_codes = gate.c(), p.gate_scales = gate.s(), p.up_codes = up.c(), p.up_scales = up.s();
+  with_workspace(g_entry.gated_forward, g_entry.gated_forward_workspace, p, x);
+  return pack({wrap(std::move(h)), named(g_gated, {gate.object(x.scalar_type()), up.object(x.scalar_type())})});
+}
+
+// gated_linear_backward(dy, z, w, activation, grad_dtype, dw, db, need)
+PyObject* gated_linear_backward(PyObject* const* a) {
+  const at::Tensor& dy = tensor(a[0]);
+  const at::Tensor& w = tensor(a[2]);
+  const Matrix md = matrix(dy), mw = matrix(w);
+  const c10::cuda::CUDAGuard guard(dy.device());
+  require(mw.rows == md.cols && w.scalar_type() == dy.scalar_type() && w.device() == dy.device());
+  onebit_gated_linear_grad_t p{};
+  p.dtype = dtype_code(dy.scalar_type());
+  p.dy = md.p, p.lddy = md.ld, p.w = mw.p, p.ldw = mw.ld;
+  p.rows = md.rows, p.inner = mw.cols, p.out = mw.rows;
+  if (Py_TYPE(a[1]) == g_gated) {
+    require(PyTuple_GET_SIZE(a[1]) == 2);
+    PyObject *gate = PyTuple_GET_ITEM(a[1], 0), *up = PyTuple_GET_ITEM(a[1], 1);
+    require(Py_TYPE(gate) == g_checkpoint && Py_TYPE(up) == g_checkpoint);
+    const Kept g = kept(gate, dy, p.rows, p.inner), u = kept(up, dy, p.rows, p.inner);
+    p.gate_codes = g.codes, p.gate_scales = g.scales, p.up_codes = u.codes, p.up_scales = u.scales;
+  } else if (a[1] != Py_None) {
+    const Matrix z = matrix(tensor(a[1]), dy, p.rows, 2 * p.inner);
+    p.z = z.p, p.ldz = z.ld;
+  }
+  p.activation = integer(a[3]);
+  const at::ScalarType grad = a[4] == Py_None ? dy.scalar_type() : scalar_type(a[4]);
+  p.grad_dtype = dtype_code(grad);
+  bool want[3] = {false, false, false};
+  wanted(a[7], {"dz", "dw", "db"}, want);
+  at::Tensor dz, dw, db;
+  if (want[0]) {
+    dz = empty({p.rows, 2 * p.inner}, dy.scalar_type(), dy);
+    p.dz = dz.data_ptr(), p.lddz = 2 * p.inner;
+  }
+  auto given = [&](PyObject* o, int64_t n) {
+    const at::Tensor& t = tensor(o);
+    require(t.scalar_type() == grad && t.numel() == n && t.is_contiguous() && t.device() == dy.device() && !has_history(t));
+    return t.data_ptr();
+  };
+  if (want[1]) {
+    if (a[5] != Py_None) p.dw = given(a[5], p.out * p.inner);
+    else dw = empty({p.out, p.inner}, grad, dy), p.dw = dw.data_ptr();
+  }
+  if (want[2]) {
+    if (a[6] != Py_None) p.db = given(a[6], p.out);
+    else db = empty({p.out}, grad, dy), p.db = db.data_ptr();
+  }
+  with_workspace(g_entry.gated_backward, g_entry.gated_backward_workspace, p, dy);
+  return pack({wrap_or_none(std::move(dz)), want[1] && a[5] != Py_None ? Py_NewRef(a[5]) : wrap_or_none(std::move(dw)),
+               want[2] && a[6] != Py_None ? Py_NewRef(a[6]) : wrap_or_none(std::move(db))});
+}
+
+// a Python float (whole numbers: layers.py)
+float real(PyObject* o) {
+  require(PyFloat_Check(o));
+  return (float)PyFloat_AS_DOUBLE(o);
+}
+struct DropoutArgs {
+  float p;
+  const int64_t* key = nullptr;
+  uint32_t site;
+  DropoutArgs(PyObject* p_, PyObject* key_, PyObject* site_, const at::Tensor& like) : p(real(p_)) {
+    if (key_ != Py_None) {
+      const at::Tensor& t = tensor(key_);
+      require(t.scalar_type() == at::kLong && t.numel() == 2 && t.is_contiguous() && t.device() == like.device());
+      key = static_cast<const int64_t*>(t.data_ptr());
+    }
+    const int s = integer(site_);  // (larger ones: layers.py)
+    require(s >= 0);
+    site = (uint32_t)s;
+  }
+};
+
+// dropout(x, p, key, site)
+PyObject* dropout(PyObject* const* a) {
+  const at::Tensor& x = tensor(a[0]);
+  const Matrix m = matrix(x);
+  const c10::cuda::CUDAGuard guard(x.device());
+  const int code = dtype_code(x.scalar_type());
+  const DropoutArgs d(a[1], a[2], a[3], x);
+  at::Tensor y = empty({m.rows, m.cols}, x.scalar_type(), x);
+  require(g_entry.dropout(m.p, m.ld, code, m.rows, m.cols, d.p, d.key, d.site, y.data_ptr(), m.cols, stream(x)) == ONEBIT_OK);
+  return wrap(std::move(y));
+}
+
+const float* vector_or_null(PyObject* o, int64_t n, const at::Tensor& like) { return o == Py_None ? nullptr : vector(o, n, like); }
+float* floats(const at::Tensor& t) { return t.defined() ? static_cast<float*>(t.data_ptr()) : nullptr; }
+void* bytes(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
+
+// residual_norm(x, block, gamma, beta, eps, norm, block_gamma, block_beta, gate, scale, p, key, site)
+PyObject* residual_norm(PyObject* const* a) {
+  const at::Tensor& x = tensor(a[0]);
+  const Matrix m = matrix(x);
+  const c10::cuda::CUDAGuard guard(x.device());
+  onebit_residual_norm_t p{};
+  p.dtype = dtype_code(x.scalar_type());
+  p.rows = m.rows, p.cols = m.cols;
+  p.x = m.p, p.ldx = m.ld;
+  if (a[1] != Py_None) {
+    const Matrix b = matrix(tensor(a[1]), x, m.rows, m.cols);
+    p.block = b.p, p.ldblock = b.ld;
+  }
+  p.gamma = vector_or_null(a[2], m.cols, x), p.beta = vector_or_null(a[3], m.cols, x);
+  p.block_gamma = vector_or_null(a[6], m.cols, x), p.block_beta = vector_or_null(a[7], m.cols, x), p.gate = vector_or_null(a[8], m.cols, x);
+  p.eps = real(a[4]), p.norm = integer(a[5]), p.scale = real(a[9]);
+  const DropoutArgs d(a[10], a[11], a[12], x);
+  p.p = d.p, p.key = d.key, p.site = d.site;
+  at::Tensor s, y, mean, rstd, block_mean, block_rstd;
+  const bool layer = p.norm == ONEBIT_NORM_LAYER;
+  if (p.block) s = empty({m.rows, m.cols}, x.scalar_type(), x);
+  if (p.gamma) {
+    y = empty({m.rows, m.cols}, x.scalar_type(), x);
+    if (layer) mean = empty({m.rows}, at::kFloat, x);
+    rstd = empty({m.rows}, at::kFloat, x);
+  }
+  if (p.block_gamma) {
+    if (layer) block_mean = empty({m.rows}, at::kFloat, x);
+    block_rstd = empty({m.rows}, at::kFloat, x);
+  }
+  p.s = bytes(s), p.y = bytes(y), p.lds = p.ldy = m.cols;
+  p.mean = floats(mean), p.rstd = floats(rstd), p.block_mean = floats(block_mean), p.block_rstd = floats(block_rstd);
+  require(g_entry.rn_forward(&p, stream(x)) == ONEBIT_OK);
+  return named(g_norm, {wrap_or_none(std::move(y)), s.defined() ? wrap(std::move(s)) : Py_NewRef(a[0]), wrap_or_none(std::move(mean)),
+                        wrap_or_none(std::move(rstd)), wrap_or_none(std::move(block_mean)), wrap_or_none(std::move(block_rstd))});
+}
+
+// residual_norm_backward(dy, ds, s, block, gamma, mean, rstd, norm, block_gamma, block_beta, block_mean, block_rstd, gate, scale, p, key, site,
+//                        has_block, grad_dtype)
+PyObject* residual_norm_backward(PyObject* const* a) {
+  const at::Tensor& first = tensor(a[0] != Py_None ? a[0] : a[1]);
+  const Matrix m = matrix(first);
+  const c10::cuda::CUDAGuard guard(first.device());
+  const int64_t rows = m.rows, cols = m.cols;
+  onebit_residual_norm_grad_t p{};
+  p.dtype = dtype_code(first.scalar_type());
+  p.rows = rows, p.cols = cols;
+  auto input = [&](PyObject* o, const void*& q, int64_t& ld) {
+    if (o == Py_None) return;
+    const Matrix t = matrix(tensor(o), first, rows, cols);
+    q = t.p, ld = t.ld;
+  };
+  const bool has_block = a[17] == Py_True;
+  require(has_block || a[17] == Py_False);
+  input(a[0], p.dy, p.lddy);
+  input(a[1], p.ds, p.ldds);
+  if (a[4] != Py_None) input(a[2], p.s, p.lds);
+  if (has_block) input(a[3], p.block, p.ldblock);
+  p.gamma = vector_or_null(a[4], cols, first);
+  p.mean = vector_or_null(a[5], rows, first), p.rstd = vector_or_null(a[6], rows, first);
+  p.norm = integer(a[7]);
+  p.block_gamma = vector_or_null(a[8], cols, first), p.block_beta = vector_or_null(a[9], cols, first);
+  p.block_mean = vector_or_null(a[10], rows, first), p.block_rstd = vector_or_null(a[11], rows, first);
+  p.gate = vector_or_null(a[12], cols, first);
+  p.scale = real(a[13]);
+  const DropoutArgs d(a[14], a[15], a[16], first);
+  p.p = d.p, p.key = d.key, p.site = d.site;
+  const at::ScalarType grad = scalar_type(a[18]);
+  p.grad_dtype = dtype_code(grad);
+  const bool layer = p.norm == ONEBIT_NORM_LAYER;
+  at::Tensor dx = empty({rows, cols}, first.scalar_type(), first), dblock, dgamma, dbeta, dblock_gamma, dblock_beta, dgate;
+  if (has_block) dblock = empty({rows, cols}, first.scalar_type(), first);
+  if (p.gamma) dgamma = empty({cols}, grad, first);
+  if (p.gamma && layer) dbeta = empty({cols}, grad, first);
+  if (p.block_gamma) dblock_gamma = empty({cols}, grad, first);
+  if (p.block_gamma && layer) dblock_beta = empty({cols}, grad, first);
+  if (p.gate) dgate = empty({cols}, grad, first);
+  p.dx = dx.data_ptr(), p.dblock = bytes(dblock), p.lddx = p.lddblock = cols;
+  p.dgamma = bytes(dgamma), p.dbeta = bytes(dbeta), p.dblock_gamma = bytes(dblock_gamma), p.dblock_beta = bytes(dblock_beta), p.dgate = bytes(dgate);
+  size_t need = 0;
+  require(g_entry.rn_workspace(&p, &need) == ONEBIT_OK);
+  const at::Tensor ws = empty({(int64_t)need}, at::kByte, first);
+  require(g_entry.rn_backward(&p, ws.data_ptr(), need, stream(first)) == ONEBIT_OK);
+  return named(g_norm_grads, {wrap(std::move(dx)), wrap_or_none(std::move(dblock)), wrap_or_none(std::move(dgamma)), wrap_or_none(std::move(dbeta)),
+                              wrap_or_none(std::move(dblock_gamma)), wrap_or_none(std::move(dblock_beta)), wrap_or_none(std::move(dgate))});
+}
+
 // Runs f on the arguments; None where it declines.  No C++ exception passes into Python.
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -348,30 +584,28 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   }
 }
 
-// setup(addresses of the C entries, Checkpoint)
+// setup(addresses of the C entries, Checkpoint, Gated, ResidualNorm, ResidualNormGrads)
 PyObject* setup(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  if (n != 2 || !PyTuple_Check(args[0]) || PyTuple_GET_SIZE(args[0]) != 9 || !PyType_Check(args[1])) {
-    PyErr_SetString(PyExc_TypeError, "setup(nine addresses, Checkpoint)");
+  bool ok = n == 5 && PyTuple_Check(args[0]) && PyTuple_GET_SIZE(args[0]) == kEntries;
+  for (int i = 1; i < 5 && ok; ++i) ok = PyType_Check(args[i]);
+  if (!ok) {
+    PyErr_SetString(PyExc_TypeError, "setup(seventeen addresses, Checkpoint, Gated, ResidualNorm, ResidualNormGrads)");
     return nullptr;
   }
-  void* p[9];
-  for (int i = 0; i < 9; ++i) {
+  static_assert(sizeof(Entries) == kEntries * sizeof(void*), "one address each");
+  void* p[kEntries];
+  for (int i = 0; i < kEntries; ++i) {
     p[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(args[0], i));
     if (!p[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a NULL address");
       return nullptr;
     }
   }
-  g_entry.compress = reinterpret_cast<decltype(g_entry.compress)>(p[0]);
-  g_entry.restore = reinterpret_cast<decltype(g_entry.restore)>(p[1]);
-  g_entry.ln_forward = reinterpret_cast<decltype(g_entry.ln_forward)>(p[2]);
-  g_entry.ln_workspace = reinterpret_cast<decltype(g_entry.ln_workspace)>(p[3]);
-  g_entry.ln_backward = reinterpret_cast<decltype(g_entry.ln_backward)>(p[4]);
-  g_entry.forward_workspace = reinterpret_cast<decltype(g_entry.forward_workspace)>(p[5]);
-  g_entry.forward = reinterpret_cast<decltype(g_entry.forward)>(p[6]);
-  g_entry.backward_workspace = reinterpret_cast<decltype(g_entry.backward_workspace)>(p[7]);
-  g_entry.backward = reinterpret_cast<decltype(g_entry.backward)>(p[8]);
+  memcpy(&g_entry, p, sizeof p);  // in the order of Entries
   g_checkpoint = reinterpret_cast<PyTypeObject*>(Py_NewRef(args[1]));
+  g_gated = reinterpret_cast<PyTypeObject*>(Py_NewRef(args[2]));
+  g_norm = reinterpret_cast<PyTypeObject*>(Py_NewRef(args[3]));
+  g_norm_grads = reinterpret_cast<PyTypeObject*>(Py_NewRef(args[4]));
   return none();
 }
 
@@ -386,6 +620,11 @@ PyMethodDef g_methods[] = {
     {"layer_norm_backward", as_method(call<layer_norm_backward, 7>), METH_FASTCALL, nullptr},
     {"linear", as_method(call<linear, 6>), METH_FASTCALL, nullptr},
     {"linear_backward", as_method(call<linear_backward, 9>), METH_FASTCALL, nullptr},
+    {"gated_linear", as_method(call<gated_linear, 5>), METH_FASTCALL, nullptr},
+    {"gated_linear_backward", as_method(call<gated_linear_backward, 8>), METH_FASTCALL, nullptr},
+    {"dropout", as_method(call<dropout, 4>), METH_FASTCALL, nullptr},
+    {"residual_norm", as_method(call<residual_norm, 13>), METH_FASTCALL, nullptr},
+    {"residual_norm_backward", as_method(call<residual_norm_backward, 19>), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_layers_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

@@ -90,6 +90,11 @@ __device__ __forceinline__ float held40(float z) {
   asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(z), "f"(40.0f));
   return r;
 }
+__device__ __forceinline__ float held87(float z) {
+  float r;
+  asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(z), "f"(87.0f));
+  return r;
+}
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -111,7 +116,8 @@ __device__ __forceinline__ float rcp_fast(float x) {
 // second exponential: 22).  Beyond 6 the product a (1 - Phi(a)) is 6e-9 and stays there.  The derivative
 // Phi(z) + z phi(z) = 1/2 + sign(z) (1/2 - tail + a phi(a)) needs one exponential more.
 //
-// The tanh form is z times the logistic function of 2 sqrt(2/pi) (z + 0.044715 z^3).
+// The tanh form is z times the logistic function of 2 sqrt(2/pi) (z + 0.044715 z^3), silu z times that of z.  silu's
+// argument is held to 87, where exp(87) and its reciprocal are still normal numbers: below -87 silu stays at -1.4e-36.
 //
 // The constants come as register pairs: as literals they would be set up again for each pair, which was
 // a third of the instructions of the products' epilogues.
@@ -127,7 +133,8 @@ __host__ __device__ constexpr float act_const(int act, int i) {
                                       0.5f};
   // -2 sqrt(2/pi) / ln 2 times 0.044715 and 1; 2 sqrt(2/pi) times 3 * 0.044715 and 1
   constexpr float tanh[kActConsts] = {-0.10294324f, -2.3022082f, 1.0f, 0.21406445f, 1.5957691f};
-  return act == ONEBIT_ACT_GELU ? gelu[i] : act == ONEBIT_ACT_GELU_TANH ? tanh[i] : 0.0f;
+  constexpr float silu[kActConsts] = {-1.4426950f, 1.0f};  // -1/ln 2
+  return act == ONEBIT_ACT_GELU ? gelu[i] : act == ONEBIT_ACT_GELU_TANH ? tanh[i] : act == ONEBIT_ACT_SILU ? silu[i] : 0.0f;
 }
 template <int ACT>
 __device__ __forceinline__ ActConsts literal_consts() {
@@ -160,6 +167,16 @@ __device__ __forceinline__ void activate(const ActConsts& c, f2 z2, f2& value, f
       const float2 g = halves(mul2(mul2(a2, a2), k[7]));
       const float2 m = halves(fma2(mul2(a2, k[8]), pair(exp2_fast(g.x), exp2_fast(g.y)), add2(k[9], pair(-tail.x, -tail.y))));
       slope = add2(pair(copysignf(m.x, z.x), copysignf(m.y, z.y)), k[9]);
+    }
+  } else if (ACT == ONEBIT_ACT_SILU) {
+    const f2 c2 = pair(held87(z.x), held87(z.y));
+    const float2 g = halves(mul2(c2, k[0]));
+    const float2 u = halves(add2(pair(exp2_fast(g.x), exp2_fast(g.y)), k[1]));
+    const f2 s = pair(rcp_fast(u.x), rcp_fast(u.y));
+    if (VALUE) value = mul2(pair(max_nan(z.x, -87.0f), max_nan(z.y, -87.0f)), s);
+    if (SLOPE) {
+      const float2 h = halves(s);
+      slope = fma2(mul2(c2, s), add2(k[1], pair(-h.x, -h.y)), s);
     }
   } else {
     const f2 c2 = pair(held40(z.x), held40(z.y)), zz = mul2(c2, c2);

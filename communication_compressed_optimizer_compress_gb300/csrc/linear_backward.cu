@@ -220,10 +220,6 @@ cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, b
   }
   return err;
 }
-cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, bool run) {
-  return a.dtype == ONEBIT_F16 ? backward<__half>(a, ws, s, run) : backward<__nv_bfloat16>(a, ws, s, run);
-}
-
 onebit_status_t backward_ok(const onebit_linear_grad_t* a) {
   if (!a) return fail(ONEBIT_ERR_INVALID_ARG, "the arguments are NULL");
   onebit_status_t st = linear_shape_ok(a->rows, a->in, a->out, a->dtype, a->activation);
@@ -247,6 +243,11 @@ onebit_status_t backward_ok(const onebit_linear_grad_t* a) {
 }
 
 }  // namespace
+
+cudaError_t linear_backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, bool run) {
+  return a.dtype == ONEBIT_F16 ? backward<__half>(a, ws, s, run) : backward<__nv_bfloat16>(a, ws, s, run);
+}
+
 }  // namespace layers
 }  // namespace onebit
 
@@ -257,7 +258,7 @@ extern "C" onebit_status_t onebit_linear_backward_workspace(const onebit_linear_
   if (st != ONEBIT_OK) return st;
   if (!bytes) return fail(ONEBIT_ERR_INVALID_ARG, "bytes is NULL");
   Space ws{nullptr};
-  if (a->rows > 0) backward(*a, ws, nullptr, false);
+  if (a->rows > 0) linear_backward(*a, ws, nullptr, false);
   *bytes = (size_t)ws.used;
   return ONEBIT_OK;
 }
@@ -280,7 +281,7 @@ extern "C" onebit_status_t onebit_linear_backward(const onebit_linear_grad_t* a,
   cudaError_t e = cudaSuccess;
   if (a->rows > 0) {
     Space ws{static_cast<char*>(workspace)};
-    e = backward(*a, ws, s, true);
+    e = linear_backward(*a, ws, s, true);
   } else {  // no tokens: the parameters' gradients are 0
     if (a->dw) e = cudaMemsetAsync(a->dw, 0, (size_t)(a->out * a->in * g), s);
     if (a->db && e == cudaSuccess) e = cudaMemsetAsync(a->db, 0, (size_t)(a->out * g), s);

@@ -131,14 +131,16 @@ struct Partials {
     s[0] = t.x, s[1] = t.y, s[2] = t.z, s[3] = t.w;
   }
 };
-inline Partials take_partials(Space& ws, const ProductPlan& plan, int64_t rows, int64_t cols) {
+inline Partials take_sums(Space& ws, const ProductPlan& plan, int64_t rows, int64_t cols) {
   Partials q{};
-  if (plan.splits == 1) return q;
   q.ld = (cols + 3) & ~(int64_t)3;
   q.split_stride = ((rows + 31) & ~(int64_t)31) * q.ld;
   q.splits = plan.splits;
   q.p = ws.take<float>(q.split_stride * plan.splits);
   return q;
+}
+inline Partials take_partials(Space& ws, const ProductPlan& plan, int64_t rows, int64_t cols) {
+  return plan.splits == 1 ? Partials{} : take_sums(ws, plan, rows, cols);
 }
 // Each split's tile rows are a multiple of the store boxes' (32): a box never reaches into the next split.
 inline cudaError_t to_partials(PlainEpilogue<float>* e, const Partials& q, int64_t cols) {
@@ -162,6 +164,9 @@ inline onebit_status_t linear_shape_ok(int64_t rows, int64_t in, int64_t out, in
   if (act < ONEBIT_ACT_NONE || act > ONEBIT_ACT_GELU_TANH) return fail(ONEBIT_ERR_INVALID_ARG, "unknown activation");
   return ONEBIT_OK;
 }
+
+// The linear layer's backward pass: takes the workspace; with `run`, enqueues the work too.
+cudaError_t linear_backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, bool run);
 
 }  // namespace layers
 }  // namespace onebit

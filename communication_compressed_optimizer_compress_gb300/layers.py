@@ -1,5 +1,6 @@
 """Layer operators that produce the gradients the optimizer exchanges: layer norm, the linear layer with
-a fused epilogue, and activation checkpoints held in 8 bits, forward and backward.
+a fused epilogue, the gated linear layer, dropout, the residual sum with the norms around it, and activation
+checkpoints held in 8 bits, forward and backward.
 
 Thin Python binding over the C ABI in ``include/onebit_layers.h`` (the formulas are stated there); every
 operator runs in the library's CUDA kernels on the current torch stream, or on ``stream``.  The common case
@@ -20,6 +21,16 @@ configured with, and may be written into the caller's tensors (``dw=``, ``db=``)
     ds, dgamma, dbeta = layers.layer_norm_backward(dy, s8, gamma, mean, rstd)
     dz, dw2, db2 = layers.linear_backward(ds, z8, w2, layers.ACT_GELU)
     dx, dw1, db1 = layers.linear_backward(dz, x, w1, add=ds)
+
+    s = x + dropout(W2 (silu(Wg x) * (Wu x))), then an RMS norm, W1 holding Wg's rows and then Wu's:
+
+    key = torch.tensor([seed, step], device="cuda")
+    h, z8 = layers.gated_linear(x, w1, keep="checkpoint")
+    f = layers.linear(h, w2)
+    r = layers.residual_norm(x, f, gamma, norm=layers.NORM_RMS, p=0.1, key=key)
+    g = layers.residual_norm_backward(dy, ds, r.s, None, gamma, None, r.rstd, norm=layers.NORM_RMS, p=0.1, key=key)
+    dz, dw2, _ = layers.gated_linear_backward(g.dblock, z8, w2, need=("dz", "dw"))
+    dx, dw1, _ = layers.linear_backward(dz, x, w1, add=g.dx, need=("dx", "dw"))
 """
 from __future__ import annotations
 
@@ -33,8 +44,10 @@ import torch
 
 from . import BF16, ERR_WORKSPACE, F16, F32, OK, OneBitError, _stream_ptr, lib
 
-ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH = range(4)
-ACTIVATIONS = {"none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH}
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = range(5)  # silu: of the gated linear layer alone
+ACTIVATIONS = {"none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH, "silu": ACT_SILU}
+NORM_LAYER, NORM_RMS = range(2)
+NORMS = {"layer": NORM_LAYER, "rms": NORM_RMS}
 CHECKPOINT_BLOCK = 64  # columns of a row that share one scale
 
 _DTYPE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
@@ -47,6 +60,36 @@ class Checkpoint(NamedTuple):
     codes: torch.Tensor
     scales: torch.Tensor
     dtype: torch.dtype
+
+
+class Gated(NamedTuple):
+    """The checkpoints of a gated linear layer's two halves before the gating."""
+
+    gate: Checkpoint
+    up: Checkpoint
+
+
+class ResidualNorm(NamedTuple):
+    """What residual_norm returns; None for what a call does not have."""
+
+    y: torch.Tensor | None
+    s: torch.Tensor
+    mean: torch.Tensor | None
+    rstd: torch.Tensor | None
+    block_mean: torch.Tensor | None
+    block_rstd: torch.Tensor | None
+
+
+class ResidualNormGrads(NamedTuple):
+    """What residual_norm_backward returns; None for what a call does not have."""
+
+    dx: torch.Tensor
+    dblock: torch.Tensor | None
+    dgamma: torch.Tensor | None
+    dbeta: torch.Tensor | None
+    dblock_gamma: torch.Tensor | None
+    dblock_beta: torch.Tensor | None
+    dgate: torch.Tensor | None
 
 
 class LinearArgs(ctypes.Structure):
@@ -64,6 +107,37 @@ class LinearGradArgs(ctypes.Structure):
                 ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64), ("dw", ctypes.c_void_p), ("db", ctypes.c_void_p),
                 ("rows", ctypes.c_int64), ("in_", ctypes.c_int64), ("out", ctypes.c_int64),
                 ("dtype", ctypes.c_int32), ("activation", ctypes.c_int32), ("grad_dtype", ctypes.c_int32)]
+
+
+def _fields(spec):
+    """ctypes fields from "name name:type ..." (pointers where no type is given; ld* are strides)."""
+    types = {"i64": ctypes.c_int64, "i32": ctypes.c_int32, "u32": ctypes.c_uint32, "f32": ctypes.c_float}
+    out = []
+    for word in spec.split():
+        name, _, kind = word.partition(":")
+        out.append((name, types[kind] if kind else ctypes.c_int64 if name.startswith("ld") else ctypes.c_void_p))
+    return out
+
+
+class GatedLinearArgs(ctypes.Structure):
+    _fields_ = _fields("x ldx w ldw bias h ldh z ldz gate_codes gate_scales up_codes up_scales rows:i64 in_:i64 inner:i64 "
+                       "dtype:i32 activation:i32")
+
+
+class GatedLinearGradArgs(ctypes.Structure):
+    _fields_ = _fields("dy lddy z ldz gate_codes gate_scales up_codes up_scales w ldw dz lddz dw db rows:i64 inner:i64 out:i64 "
+                       "dtype:i32 activation:i32 grad_dtype:i32")
+
+
+class ResidualNormArgs(ctypes.Structure):
+    _fields_ = _fields("x ldx block ldblock gamma beta block_gamma block_beta gate key s lds y ldy mean rstd block_mean block_rstd "
+                       "rows:i64 cols:i64 dtype:i32 norm:i32 eps:f32 scale:f32 p:f32 site:u32")
+
+
+class ResidualNormGradArgs(ctypes.Structure):
+    _fields_ = _fields("dy lddy ds ldds s lds block ldblock gamma block_gamma block_beta gate key mean rstd block_mean block_rstd "
+                       "dx lddx dblock lddblock dgamma dbeta dblock_gamma dblock_beta dgate rows:i64 cols:i64 dtype:i32 norm:i32 "
+                       "grad_dtype:i32 scale:f32 p:f32 site:u32")
 
 
 _fn = None
@@ -99,6 +173,14 @@ def _functions():
             "onebit_linear_forward": [ctypes.POINTER(LinearArgs), vp, sz, vp],
             "onebit_linear_backward_workspace": [ctypes.POINTER(LinearGradArgs), ctypes.POINTER(sz)],
             "onebit_linear_backward": [ctypes.POINTER(LinearGradArgs), vp, sz, vp],
+            "onebit_gated_linear_forward_workspace": [ctypes.POINTER(GatedLinearArgs), ctypes.POINTER(sz)],
+            "onebit_gated_linear_forward": [ctypes.POINTER(GatedLinearArgs), vp, sz, vp],
+            "onebit_gated_linear_backward_workspace": [ctypes.POINTER(GatedLinearGradArgs), ctypes.POINTER(sz)],
+            "onebit_gated_linear_backward": [ctypes.POINTER(GatedLinearGradArgs), vp, sz, vp],
+            "onebit_dropout": [vp, i64, i32, i64, i64, ctypes.c_float, vp, ctypes.c_uint32, vp, i64, vp],
+            "onebit_residual_norm_forward": [ctypes.POINTER(ResidualNormArgs), vp],
+            "onebit_residual_norm_backward_workspace": [ctypes.POINTER(ResidualNormGradArgs), ctypes.POINTER(sz)],
+            "onebit_residual_norm_backward": [ctypes.POINTER(ResidualNormGradArgs), vp, sz, vp],
             "onebit_layers_get_status": [vp],
             "onebit_layers_clear_status": [vp],
             "onebit_layers_set_fault_injection": [i32, i64],
@@ -111,8 +193,12 @@ def _functions():
         L.onebit_layers_last_error.restype = ctypes.c_char_p
         names = ("onebit_checkpoint_compress", "onebit_checkpoint_restore", "onebit_layer_norm_forward",
                  "onebit_layer_norm_backward_workspace", "onebit_layer_norm_backward", "onebit_linear_forward_workspace",
-                 "onebit_linear_forward", "onebit_linear_backward_workspace", "onebit_linear_backward")
-        _layers_binding.setup(tuple(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names), Checkpoint)
+                 "onebit_linear_forward", "onebit_linear_backward_workspace", "onebit_linear_backward",
+                 "onebit_gated_linear_forward_workspace", "onebit_gated_linear_forward",
+                 "onebit_gated_linear_backward_workspace", "onebit_gated_linear_backward", "onebit_dropout",
+                 "onebit_residual_norm_forward", "onebit_residual_norm_backward_workspace", "onebit_residual_norm_backward")
+        _layers_binding.setup(tuple(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names), Checkpoint, Gated,
+                              ResidualNorm, ResidualNormGrads)
         _fn = L
     return _fn
 
@@ -444,3 +530,207 @@ def linear_backward(dy, x, w, activation=ACT_NONE, add=None, grad_dtype=None, dw
         fn = _functions()
         _with_workspace(fn.onebit_linear_backward, fn.onebit_linear_backward_workspace, a, device, "onebit_linear_backward")
     return dx, dw, db
+
+
+def gated_linear(x, w, bias=None, activation=ACT_SILU, keep=None, stream=None):
+    """h = activation(g) * u with [g | u] = z = x w^T + bias; w holds the gate's rows and then as many of the up
+    projection.  ``keep``: "values" returns (h, z), "checkpoint" (h, the 8-bit checkpoints of g and u, a Gated)."""
+    if stream is not None:
+        with _on(stream, x):
+            return gated_linear(x, w, bias, activation, keep)
+    if _fn is None:
+        _functions()
+    fast = _layers_binding.gated_linear(x, w, bias, activation, keep)
+    if fast is not None:
+        return fast
+    rows, cols, ldx = _matrix(x, "x")
+    dtype, device = x.dtype, x.device
+    code = _code(dtype, "x")
+    if w.dim() != 2 or w.shape[0] % 2:
+        raise ValueError("w: expected 2 inner x in")
+    if keep not in (None, "values", "checkpoint"):
+        raise ValueError('keep: expected None, "values" or "checkpoint"')
+    out, _, ldw = _matrix(w, "w", cols, None, dtype, device)
+    inner = out // 2
+    bp = _vector(bias, "bias", out, device)
+    with torch.cuda.device(device):
+        h = _rows_by(x, rows, inner, dtype, device)
+        z = _rows_by(x, rows, out, dtype, device) if keep == "values" else None
+        if keep == "checkpoint":
+            z = Gated(_new_checkpoint(x, rows, inner, dtype, device), _new_checkpoint(x, rows, inner, dtype, device))
+        a = GatedLinearArgs(x.data_ptr(), ldx, w.data_ptr(), ldw, bp, h.data_ptr(), inner, z.data_ptr() if keep == "values" else None, out,
+                            *([t.data_ptr() for ck in z for t in ck[:2]] if keep == "checkpoint" else [None] * 4), rows, cols, inner, code,
+                            activation)
+        fn = _functions()
+        _with_workspace(fn.onebit_gated_linear_forward, fn.onebit_gated_linear_forward_workspace, a, device, "onebit_gated_linear_forward")
+    return h if keep is None else (h, z)
+
+
+def gated_linear_backward(dy, z, w, activation=ACT_SILU, grad_dtype=None, dw=None, db=None, need=("dz", "dw", "db"), stream=None):
+    """(dz, dw, db) of y = (activation(g) * u) w^T + bias, given dy: z = [g | u] is what gated_linear kept, a tensor or a
+    Gated; dz is the dy of linear_backward for the gated layer's own weight.  grad_dtype (default dy's) is the type of dw (out x
+    inner) and db; ``dw`` and ``db`` may be the caller's contiguous tensors.  What ``need`` leaves out is None.  dw is summed
+    in fp32 from dy and activation(g) * u rounded to 16 bits, as the forward product takes it."""
+    if stream is not None:
+        with _on(stream, dy):
+            return gated_linear_backward(dy, z, w, activation, grad_dtype, dw, db, need)
+    if _fn is None:
+        _functions()
+    fast = _layers_binding.gated_linear_backward(dy, z, w, activation, grad_dtype, dw, db, need)
+    if fast is not None:
+        return fast
+    rows, out, lddy = _matrix(dy, "dy")
+    dtype, device = dy.dtype, dy.device
+    code = _code(dtype, "dy")
+    grad_dtype = dtype if grad_dtype is None else grad_dtype
+    gcode = _code(grad_dtype, "grad_dtype")
+    if w.dim() != 2:
+        raise ValueError("w: expected out x inner")
+    _, inner, ldw = _matrix(w, "w", None, out, dtype, device)
+    zp, ldz, halves = None, 0, [None] * 4
+    if isinstance(z, Gated):
+        halves = [p for name, ck in zip(("z.gate", "z.up"), z) for p in _kept(_checkpoint(ck, name), name, inner, rows, dtype, device)[2:4]]
+    elif z is not None:
+        ldz = _matrix(z, "z", 2 * inner, rows, dtype, device)[2]
+        zp = z.data_ptr()
+    want_dz, want_dw, want_db = "dz" in need, "dw" in need, "db" in need
+    with torch.cuda.device(device):
+        dz = _rows_by(dy, rows, 2 * inner, dtype, device) if want_dz else None
+        if not want_dw:
+            dw = None
+        elif dw is None:
+            dw = torch.empty(out, inner, dtype=grad_dtype, device=device)
+        if not want_db:
+            db = None
+        elif db is None:
+            db = torch.empty(out, dtype=grad_dtype, device=device)
+        a = GatedLinearGradArgs(dy.data_ptr(), lddy, zp, ldz, *halves, w.data_ptr(), ldw, dz.data_ptr() if want_dz else None, 2 * inner,
+                                _vector(dw, "dw", out * inner, device, grad_dtype), _vector(db, "db", out, device, grad_dtype), rows, inner,
+                                out, code, activation, gcode)
+        fn = _functions()
+        _with_workspace(fn.onebit_gated_linear_backward, fn.onebit_gated_linear_backward_workspace, a, device, "onebit_gated_linear_backward")
+    return dz, dw, db
+
+
+def _checkpoint(ck, name):
+    if not isinstance(ck, Checkpoint):
+        raise ValueError(f"{name}: expected a Checkpoint")
+    return ck
+
+
+def _dropout_key(p, key, site, device):
+    """The key's pointer (None: no dropout)."""
+    if not 0 <= site < 1 << 32:
+        raise ValueError("site: expected a whole number below 2^32")
+    if key is None:
+        if p > 0:
+            raise ValueError("key: dropout needs two int64 values, seed and step")
+        return None
+    return _vector(key, "key", 2, device, torch.int64)
+
+
+def dropout(x, p, key, site=0, stream=None):
+    """x with each element set to 0 with probability p (in steps of 1/65536), the others divided by 1 - p.  ``key`` is a CUDA
+    tensor of two int64 values, seed and step, read when the kernel runs; ``site`` tells the places of a model apart that use one
+    key.  The backward pass is the same call on the gradient."""
+    if stream is not None:
+        with _on(stream, x):
+            return dropout(x, p, key, site)
+    if _fn is None:
+        _functions()
+    fast = _layers_binding.dropout(x, p, key, site)
+    if fast is not None:
+        return fast
+    rows, cols, ld = _matrix(x, "x")
+    code, device = _code(x.dtype, "x"), x.device
+    kp = _dropout_key(p, key, site, device)
+    with torch.cuda.device(device):
+        y = _like(x)
+        st = _functions().onebit_dropout(x.data_ptr(), ld, code, rows, cols, p, kp, site, y.data_ptr(), cols, _stream(device))
+    if st:
+        _check(st, "onebit_dropout")
+    return y
+
+
+def residual_norm(x, block=None, gamma=None, beta=None, eps=1e-5, norm=NORM_LAYER, block_gamma=None, block_beta=None, gate=None, scale=1.0,
+                  p=0.0, key=None, site=0, stream=None) -> ResidualNorm:
+    """s = x + scale * gate * dropout(n) and y = norm(s) * gamma + beta, where n is ``block``, a block's output, or with
+    ``block_gamma`` norm(block) * block_gamma + block_beta.  Without a block s is x itself; without gamma there is no y.  ``norm`` is
+    that of both places: NORM_LAYER, with beta and block_beta, or NORM_RMS, without.  p, key and site as for dropout().  s, mean,
+    rstd, block_mean and block_rstd are what the backward pass needs beside the call's arguments."""
+    if stream is not None:
+        with _on(stream, x):
+            return residual_norm(x, block, gamma, beta, eps, norm, block_gamma, block_beta, gate, scale, p, key, site)
+    if _fn is None:
+        _functions()
+    fast = _layers_binding.residual_norm(x, block, gamma, beta, eps, norm, block_gamma, block_beta, gate, scale, p, key, site)
+    if fast is not None:
+        return fast
+    rows, cols, ldx = _matrix(x, "x")
+    dtype, device = x.dtype, x.device
+    code = _code(dtype, "x")
+    bp, ldb = (block.data_ptr(), _matrix(block, "block", cols, rows, dtype, device)[2]) if block is not None else (None, 0)
+    vectors = [_vector(v, name, cols, device) for v, name in ((gamma, "gamma"), (beta, "beta"), (block_gamma, "block_gamma"),
+                                                              (block_beta, "block_beta"), (gate, "gate"))]
+    kp = _dropout_key(p, key, site, device)
+    layer = norm == NORM_LAYER
+    with torch.cuda.device(device):
+        s = _like(x) if block is not None else None
+        y = _like(x) if gamma is not None else None
+        stats = [_rows_of(x, rows, device) if there else None for there in
+                 (gamma is not None and layer, gamma is not None, block_gamma is not None and layer, block_gamma is not None)]
+        at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        a = ResidualNormArgs(x.data_ptr(), ldx, bp, ldb, *vectors, kp, at(s), cols, at(y), cols, *[at(t) for t in stats], rows, cols, code,
+                             norm, eps, scale, p, site)
+        st = _functions().onebit_residual_norm_forward(a, _stream(device))
+    if st:
+        _check(st, "onebit_residual_norm_forward")
+    return ResidualNorm(y, x if s is None else s, *stats)
+
+
+def residual_norm_backward(dy, ds, s, block, gamma, mean, rstd, norm=NORM_LAYER, block_gamma=None, block_beta=None, block_mean=None,
+                           block_rstd=None, gate=None, scale=1.0, p=0.0, key=None, site=0, has_block=True, grad_dtype=torch.float32,
+                           stream=None) -> ResidualNormGrads:
+    """The gradients of residual_norm's call with these arguments, given dy (of y; None without gamma) and ds, the gradient of
+    s from the residual path (or None).  ``block`` may be None where neither block_gamma nor gate is there; ``has_block=False`` stands
+    for a call without a block, whose dblock is None.  The parameters' gradients come in grad_dtype."""
+    first = ds if dy is None else dy
+    if first is None:
+        raise ValueError("dy, ds: one of them is needed")
+    if stream is not None:
+        with _on(stream, first):
+            return residual_norm_backward(dy, ds, s, block, gamma, mean, rstd, norm, block_gamma, block_beta, block_mean, block_rstd, gate,
+                                          scale, p, key, site, has_block, grad_dtype)
+    if _fn is None:
+        _functions()
+    fast = _layers_binding.residual_norm_backward(dy, ds, s, block, gamma, mean, rstd, norm, block_gamma, block_beta, block_mean, block_rstd,
+                                                  gate, scale, p, key, site, has_block, grad_dtype)
+    if fast is not None:
+        return fast
+    rows, cols, _ = _matrix(first, "ds" if dy is None else "dy")
+    dtype, device = first.dtype, first.device
+    code, gcode = _code(dtype, "dy"), _code(grad_dtype, "grad_dtype")
+    inputs = []
+    for t, name in ((dy, "dy"), (ds, "ds"), (s if gamma is not None else None, "s"), (block if has_block else None, "block")):
+        inputs += [t.data_ptr(), _matrix(t, name, cols, rows, dtype, device)[2]] if t is not None else [None, 0]
+    vectors = [_vector(v, name, cols, device) for v, name in ((gamma, "gamma"), (block_gamma, "block_gamma"), (block_beta, "block_beta"),
+                                                              (gate, "gate"))]
+    kp = _dropout_key(p, key, site, device)
+    stats = [_vector(v, name, rows, device) for v, name in ((mean, "mean"), (rstd, "rstd"), (block_mean, "block_mean"), (block_rstd, "block_rstd"))]
+    layer = norm == NORM_LAYER
+    need, fn = ctypes.c_size_t(), _functions()
+    with torch.cuda.device(device):
+        dx, dblock = _like(first), _like(first) if has_block else None
+        grads = [torch.empty(cols, dtype=grad_dtype, device=device) if there else None for there in
+                 (gamma is not None, gamma is not None and layer, block_gamma is not None, block_gamma is not None and layer, gate is not None)]
+        at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        a = ResidualNormGradArgs(*inputs, *vectors, kp, *stats, dx.data_ptr(), cols, at(dblock), cols, *[at(t) for t in grads], rows, cols, code,
+                                 norm, gcode, scale, p, site)
+        st = fn.onebit_residual_norm_backward_workspace(a, need)
+        if st:
+            _check(st, "onebit_residual_norm_backward_workspace")
+        ws = _workspace(need.value, device)
+        st = fn.onebit_residual_norm_backward(a, at(ws), need.value, _stream(device))
+    if st:
+        _check(st, "onebit_residual_norm_backward")
+    return ResidualNormGrads(dx, dblock, *grads)
