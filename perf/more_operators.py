@@ -338,7 +338,7 @@ def _own(s):
     if op == "dropout":
         return layers.dropout(s["x"], s["p"], s["key"], s["site"])
     if op.startswith("gated"):
-        act = layers.ACTIVATIONS[s["act"]]
+        act = layers.GATE_ACTIVATIONS[s["act"]]
         if op == "gated_bwd":
             if s["keep"] == "checkpoint":
                 z = layers.Gated(layers.Checkpoint(s["gate_codes"], s["gate_scales"], dtype),
