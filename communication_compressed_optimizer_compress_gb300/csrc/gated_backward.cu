@@ -49,18 +49,48 @@ cudaError_t backward(const onebit_gated_linear_grad_t& a, Space& ws, cudaStream_
   cudaError_t err = run ? copies.run(s) : cudaSuccess;
   if (err != cudaSuccess) return err;
   Partials part{};
+  bool done = false;  // dz and h
   if (a.dz) {
     const ProductShape shape{a.rows, a.inner, a.out};
     const ProductPlan plan = plan_product(shape, sm_count());
-    part = take_sums(ws, plan, a.rows, a.inner);
-    if (run) {
+    part = take_partials(ws, plan, a.rows, a.inner);
+    if (run && plan.splits == 1) {
+      auto go = [&](auto ctas, auto act, auto what) {
+        GatedGradEpilogue<T, decltype(act)::value, decltype(what)::value> e{};
+        e.gate = make_input<T>(kept.gate.x, a.ldz), e.up = make_input<T>(kept.up.x, a.ldz);
+        e.gate_codes = a.gate_codes, e.up_codes = a.up_codes, e.gate_scales = a.gate_scales, e.up_scales = a.up_scales;
+        e.blocks = blocks, e.act = a.activation, e.kept = a.z ? kKeptValue : kKeptCodes;
+        e.wide_codes = aligned(a.gate_codes, 32) && aligned(a.up_codes, 32) && n % 32 == 0;
+        e.vec_codes = aligned(a.gate_codes, 16) && aligned(a.up_codes, 16) && n % 16 == 0;
+        T* dz = static_cast<T*>(a.dz);
+        cudaError_t r = make_output(&e.dgate, dz, a.rows, a.inner, a.lddz);
+        if (r == cudaSuccess) r = make_output(&e.dup, dz + n, a.rows, a.inner, a.lddz);
+        if (r == cudaSuccess) r = make_output(&e.h, h, a.rows, a.inner, ldh);
+        return r == cudaSuccess ? run_product_by<decltype(ctas)::value, false, true>(a.dtype, dy, w, shape, plan, e, s) : r;
+      };
+      using std::integral_constant;
+      using Any = integral_constant<int, kAny>;
+      auto by_act = [&](auto what) {
+        integral_constant<int, 2> two;
+        switch (a.activation) {
+          case ONEBIT_ACT_GELU: return go(two, integral_constant<int, ONEBIT_ACT_GELU>{}, what);
+          case ONEBIT_ACT_GELU_TANH: return go(two, integral_constant<int, ONEBIT_ACT_GELU_TANH>{}, what);
+          case ONEBIT_ACT_SILU: return go(two, integral_constant<int, ONEBIT_ACT_SILU>{}, what);
+          default: return go(two, Any{}, what);
+        }
+      };
+      err = plan.ctas == 1 ? go(integral_constant<int, 1>{}, Any{}, Any{})
+            : a.z          ? by_act(integral_constant<int, kKeptValue>{}) : by_act(integral_constant<int, kKeptCodes>{});
+      if (err != cudaSuccess) return err;
+      done = true;
+    } else if (run) {
       PlainEpilogue<float> to{};
       err = to_partials(&to, part, a.inner);
       if (err == cudaSuccess) err = run_product<false, true>(a.dtype, dy, w, shape, plan, to, s);
       if (err != cudaSuccess) return err;
     }
   }
-  if (run && (a.dz || h)) {
+  if (run && !done && (a.dz || h)) {
     err = launch_after(k_finish_dz<T>, flat_grid(a.rows * ceil_div(a.inner, 4), 256), 256, s, part, a.rows, n, kept, a.activation, static_cast<T*>(a.dz),
                        a.lddz, h, ldh);
     if (err != cudaSuccess) return err;

@@ -1,5 +1,6 @@
 // gated_forward.cu -- the gated linear layer's forward pass: both projections in one matrix product, activation,
 // gating and what is kept.  See include/onebit_layers.h for the formulas.
+#include "few_rows.cuh"
 #include "gated_common.cuh"
 
 namespace onebit {
@@ -53,22 +54,134 @@ __global__ void __launch_bounds__(256) k_finish_gated(Partials c, int64_t rows, 
   }
 }
 
+// Up to 32 rows, as generation meets them: the few-rows product (few_rows.cuh) with two weights to a column, the gate's and
+// the up projection's, whose sums meet in shared memory.
+struct FewGatedArgs {
+  const void* x;
+  int64_t ldx;
+  const void* w;
+  int64_t ldw;
+  const float* bias;
+  void* h;
+  int64_t ldh;
+  int rows, in, inner, act;
+};
+template <typename T, int M>
+__global__ void __launch_bounds__(kFewThreads) k_few_rows_gated(const FewGatedArgs A) {
+  in_turn();
+  constexpr int kSplits = 8, kAhead = 4;
+  __shared__ float part[kSplits][2][M * 16][9];
+  const int lane = threadIdx.x & 31, split = threadIdx.x >> 5;
+  const int n = lane >> 2, q = lane & 3;
+  const int col = blockIdx.x * 8 + n;
+  const int steps = (A.in + 31) / 32, per = (steps + kSplits - 1) / kSplits;
+  const int s0 = split * per, s1 = s0 + per < steps ? s0 + per : steps;
+  const T* w = static_cast<const T*>(A.w) + (int64_t)(col < A.inner ? col : 0) * A.ldw;
+  const int64_t up = (int64_t)A.inner * A.ldw;
+  const T* x = static_cast<const T*>(A.x);
+  float d[2][M][4] = {};
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  auto piece = [&](int s, int64_t half) {
+    const int k = s * 32 + q * 8;
+    return col < A.inner && s < s1 && k < A.in ? __ldg(reinterpret_cast<const uint4*>(w + half + k)) : zero;
+  };
+  uint4 ahead[kAhead][2];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) ahead[i][0] = piece(s0 + i, 0), ahead[i][1] = piece(s0 + i, up);
+  for (int s = s0; s < s1; s += kAhead) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const uint4 b[2] = {ahead[i][0], ahead[i][1]};
+      ahead[i][0] = piece(s + kAhead + i, 0), ahead[i][1] = piece(s + kAhead + i, up);
+      const int k = (s + i) * 32 + q * 8;
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        const int r0 = m * 16 + n, r1 = r0 + 8;
+        const bool in = s + i < s1 && k < A.in;
+        const uint4 a = in && r0 < A.rows ? __ldg(reinterpret_cast<const uint4*>(x + r0 * A.ldx + k)) : zero;
+        const uint4 c = in && r1 < A.rows ? __ldg(reinterpret_cast<const uint4*>(x + r1 * A.ldx + k)) : zero;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          mma_16x8x16<T>(d[p][m], a.x, c.x, a.y, c.y, b[p].x, b[p].y);
+          mma_16x8x16<T>(d[p][m], a.z, c.z, a.w, c.w, b[p].z, b[p].w);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) part[split][p][m * 16 + n + 8 * (i / 2)][2 * q + (i & 1)] = d[p][m][i];
+  __syncthreads();
+  for (int i = threadIdx.x; i < M * 16 * 8; i += kFewThreads) {
+    const int r = i / 8, j = i % 8, c = blockIdx.x * 8 + j;
+    if (r >= A.rows || c >= A.inner) continue;
+    float g = part[0][0][r][j], u = part[0][1][r][j];
+#pragma unroll
+    for (int s = 1; s < kSplits; ++s) g += part[s][0][r][j], u += part[s][1][r][j];
+    if (A.bias) g += __ldg(A.bias + c), u += __ldg(A.bias + A.inner + c);
+    static_cast<T*>(A.h)[r * A.ldh + c] = from_f<T>(gate_both(A.act, g).x * u);
+  }
+}
+// Few rows, on 16 bytes, and nothing kept.
+inline bool few_rows(const onebit_gated_linear_t& a) {
+  return a.rows <= kFewRows && !a.z && !a.gate_codes && a.in % 8 == 0 && vec16(a.x, a.ldx) && vec16(a.w, a.ldw);
+}
+template <typename T>
+cudaError_t run_few_rows(const onebit_gated_linear_t& a, cudaStream_t s) {
+  const FewGatedArgs f{a.x, a.ldx, a.w, a.ldw, a.bias, a.h, a.ldh, (int)a.rows, (int)a.in, (int)a.inner, a.activation};
+  const unsigned grid = (unsigned)ceil_div(a.inner, 8);
+  return a.rows <= 16 ? launch_after(k_few_rows_gated<T, 1>, grid, kFewThreads, s, f) : launch_after(k_few_rows_gated<T, 2>, grid, kFewThreads, s, f);
+}
+
 // Takes the workspace; with `run`, enqueues the work too.
 template <typename T>
 cudaError_t forward(const onebit_gated_linear_t& a, Space& ws, cudaStream_t s, bool run) {
+  if (few_rows(a)) return run ? run_few_rows<T>(a, s) : cudaSuccess;
   const ProductShape shape{a.rows, 2 * a.inner, a.in};
-  ProductPlan plan = plan_product(shape, sm_count());
+  const ProductPlan plan = plan_product(shape, sm_count());
   Readable copies;
   const Operand x = copies.take(ws, a.x, a.ldx, a.rows, a.in), w = copies.take(ws, a.w, a.ldw, 2 * a.inner, a.in);
-  const Partials part = take_sums(ws, plan, a.rows, 2 * a.inner);
+  const Partials part = take_partials(ws, plan, a.rows, 2 * a.inner);
   if (!run) return cudaSuccess;
   cudaError_t err = copies.run(s);
   if (err != cudaSuccess) return err;
+  const int64_t blocks = ceil_div(a.inner, kBlock);
+  if (plan.splits == 1) {
+    auto go = [&](auto ctas, auto act, auto keep) {
+      GatedEpilogue<T, decltype(act)::value, decltype(keep)::value> e{};
+      T* z = static_cast<T*>(a.z);
+      e.bias = a.bias;
+      e.gate_scales = a.gate_scales, e.up_scales = a.up_scales;
+      e.blocks = (int)blocks, e.act = a.activation, e.keep = a.z ? kKeptValue : a.gate_codes ? kKeptCodes : kKeptNone;
+      cudaError_t r = make_output(&e.h, static_cast<T*>(a.h), a.rows, a.inner, a.ldh);
+      if (r == cudaSuccess) r = make_output(&e.gate, z, a.rows, a.inner, a.ldz);
+      if (r == cudaSuccess) r = make_output(&e.up, z ? z + a.inner : nullptr, a.rows, a.inner, a.ldz);
+      if (r == cudaSuccess) r = make_output(&e.gate_codes, a.gate_codes, a.rows, a.inner, a.inner);
+      if (r == cudaSuccess) r = make_output(&e.up_codes, a.up_codes, a.rows, a.inner, a.inner);
+      return r == cudaSuccess ? run_product_by<decltype(ctas)::value, false, false>(a.dtype, x, w, shape, plan, e, s) : r;
+    };
+    using std::integral_constant;
+    using Any = integral_constant<int, kAny>;
+    if (plan.ctas == 1) return go(integral_constant<int, 1>{}, Any{}, Any{});
+    auto by_act = [&](auto keep) {
+      integral_constant<int, 2> two;
+      switch (a.activation) {
+        case ONEBIT_ACT_GELU: return go(two, integral_constant<int, ONEBIT_ACT_GELU>{}, keep);
+        case ONEBIT_ACT_GELU_TANH: return go(two, integral_constant<int, ONEBIT_ACT_GELU_TANH>{}, keep);
+        case ONEBIT_ACT_SILU: return go(two, integral_constant<int, ONEBIT_ACT_SILU>{}, keep);
+        default: return go(two, Any{}, keep);
+      }
+    };
+    return a.z ? by_act(integral_constant<int, kKeptValue>{})
+           : a.gate_codes ? by_act(integral_constant<int, kKeptCodes>{}) : by_act(integral_constant<int, kKeptNone>{});
+  }
   PlainEpilogue<float> to{};
   err = to_partials(&to, part, 2 * a.inner);
   if (err == cudaSuccess) err = run_product<false, false>(a.dtype, x, w, shape, plan, to, s);
   if (err != cudaSuccess) return err;
-  const int64_t blocks = ceil_div(a.inner, kBlock);
   const GatedOut<T> o{a.bias, static_cast<T*>(a.h), a.ldh, static_cast<T*>(a.z), a.ldz, a.gate_codes, a.up_codes, a.gate_scales, a.up_scales,
                       (int)blocks, a.activation};
   return launch_after(k_finish_gated<T>, flat_grid(a.rows * blocks * 32, 256), 256, s, part, a.rows, (int)a.inner, o);

@@ -65,6 +65,7 @@ struct ProductArgs {
   int32_t slabs;             // of the whole contraction
   int32_t tiles_m, tiles_n;
   int32_t splits, split_slabs;
+  int32_t half;              // (gated epilogues) rows of B between a column's two halves
   uint32_t units;            // tiles times splits
   uint32_t group_mul, group_shift;  // reciprocal of the tiles in a group of kGroupTiles tile rows
   uint32_t idesc;
@@ -279,11 +280,11 @@ __device__ __forceinline__ void stage_rows(char* staging, const uint32_t (&v)[16
   for (int j = 0; j < 4; ++j)
     *reinterpret_cast<uint4*>(staging + lane * 64 + (j ^ swap) * 16) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
 }
-__device__ __forceinline__ void stage_codes(char* staging, const uint32_t (&v)[8]) {
+__device__ __forceinline__ void stage_codes(char* to, const uint32_t (&v)[8]) {
   const int lane = threadIdx.x & 31, swap = lane >> 2 & 1;  // 32-byte swizzle: chunk j of row r lies at j ^ (r / 4 % 2)
 #pragma unroll
   for (int j = 0; j < 2; ++j)
-    *reinterpret_cast<uint4*>(staging + kCodeStaging + lane * 32 + (j ^ swap) * 16) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    *reinterpret_cast<uint4*>(to + lane * 32 + (j ^ swap) * 16) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
 }
 
 // 64 bytes of a lane's row.  (With ordinary stores the way through shared memory and back to registers
@@ -390,7 +391,7 @@ __device__ __forceinline__ void store_codes(char* staging, const uint32_t (&v)[8
   const int lane = threadIdx.x & 31;
   staging_free();
   if (out.by_tma) {
-    stage_codes(staging, v);
+    stage_codes(staging + kCodeStaging, v);
     store_box(&out.map, smem_addr(staging + kCodeStaging), col0, (int32_t)row0);
     return;
   }
@@ -418,7 +419,7 @@ __device__ __forceinline__ void store_rows_and_codes(char* staging, const uint32
   if (y.by_tma && codes.by_tma) {
     staging_free();
     stage_rows<T>(staging, v);
-    stage_codes(staging, c);
+    stage_codes(staging + kCodeStaging, c);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if ((threadIdx.x & 31) == 0) {
@@ -482,9 +483,9 @@ __device__ __forceinline__ void load_codes(char* staging, uint32_t (&v)[8], cons
 template <int ACT>
 __device__ __forceinline__ ActConsts shared_consts(const f2* consts) {
   ActConsts k;
-  if (ACT == ONEBIT_ACT_GELU || ACT == ONEBIT_ACT_GELU_TANH) {
+  if (ACT == ONEBIT_ACT_GELU || ACT == ONEBIT_ACT_GELU_TANH || ACT == ONEBIT_ACT_SILU) {
 #pragma unroll
-    for (int i = 0; i < kActConsts; i += 2)
+    for (int i = 0; i < (ACT == ONEBIT_ACT_SILU ? 2 : kActConsts); i += 2)
       asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(k.k[i]), "=l"(k.k[i + 1]) : "r"(smem_addr(consts + i)));
   }
   return k;
@@ -502,6 +503,7 @@ template <typename T, int ACT, int CK, int RES>
 struct ForwardEpilogue {
   // y = act(d + bias) + residual, and the 8-bit checkpoint of d + bias
   static constexpr bool kFold = false;
+  static constexpr bool kGated = false;
   const float* bias;
   Input16<T> residual;
   Output<T> y;
@@ -602,6 +604,7 @@ template <typename T, int ACT, int KEPT>
 struct InputGradEpilogue {
   // dx = d * act'(v) [+ add], and h = act(v) for the product of dw
   static constexpr bool kFold = false;
+  static constexpr bool kGated = false;
   Input16<T> x;          // the value before the activation,
   const int8_t* codes;   // or its checkpoint
   const float* scales;
@@ -731,10 +734,328 @@ struct InputGradEpilogue {
   }
 };
 
+// The gated epilogues have several outputs, whose rows lie in the staging buffer's two halves of 2048 bytes in the stores' own
+// (swizzled) order.
+
+// chunk j of 16 bytes of this lane's row
+__device__ __forceinline__ void stage_chunk(char* to, int j, const uint32_t* v) {
+  const int lane = threadIdx.x & 31;
+  *reinterpret_cast<uint4*>(to + lane * 64 + (j ^ (lane >> 1 & 3)) * 16) = make_uint4(v[0], v[1], v[2], v[3]);
+}
+// A staged box to its matrix, element by element where TMA cannot store it.
+template <typename T>
+__device__ __forceinline__ void send_rows(const char* from, const Output<T>& out, int64_t row0, int64_t rows, int col0, int cols) {
+  const int lane = threadIdx.x & 31;
+  if (out.by_tma) {
+    if (lane == 0) copy_out(&out.map, smem_addr(from), col0, (int32_t)row0);
+    return;
+  }
+  T* p = out.p + row0 * out.ld + col0 + lane;
+  const int last = col0 + lane < cols && row0 < rows ? (int)(rows - row0 < 32 ? rows - row0 : 32) : 0;
+#pragma unroll 1
+  for (int i = 0; i < 32; i += 16) {
+    T t[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) t[k] = *reinterpret_cast<const T*>(from + (i + k) * 64 + (((lane >> 3) ^ ((i + k) >> 1 & 3)) << 4) + (lane & 7) * 2);
+#pragma unroll
+    for (int k = 0; k < 16; ++k, p += out.ld)
+      if (i + k < last) *p = t[k];
+  }
+}
+// before a staged box is sent, and behind the boxes that are sent together (an empty group where none goes by TMA, so that
+// groups and boxes stay in step)
+__device__ __forceinline__ void staged() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+}
+__device__ __forceinline__ void sent() {
+  if ((threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  __syncwarp();
+}
+// One matrix's rows; the halves of the buffer take turns, so that one is filled while the other's store reads.
+template <typename T>
+__device__ __forceinline__ void put_rows(char* staging, int& turn, const uint32_t (&v)[16], const Output<T>& out, int64_t row0, int64_t rows, int col0,
+                                         int cols) {
+  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+  __syncwarp();
+  char* to = staging + turn * 2048;
+  turn ^= 1;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) stage_chunk(to, j, v + 4 * j);
+  staged();
+  send_rows(to, out, row0, rows, col0, cols);
+  sent();
+}
+
+// h = act(g) u with [g | u] = d + bias, and what is kept of g and u.  A tile's accumulator holds the gate's columns in its
+// first half and the same columns of the up projection in its second, so that a lane has both; a warp has 32 columns of h.  For
+// the checkpoints' blocks of 64 columns it reads its neighbour's 32 too: once more out of tensor memory, which is cheaper than
+// two warps waiting for each other.
+template <typename T, int ACT, int KEEP>
+struct GatedEpilogue {
+  static constexpr bool kFold = false;
+  static constexpr bool kGated = true;
+  const float* bias;
+  Output<T> h, gate, up;  // gate, up: z's halves (kKeptValue)
+  Output<int8_t> gate_codes, up_codes;
+  float *gate_scales, *up_scales;
+  int blocks;
+  int act;
+  int keep;
+
+  __device__ __forceinline__ int keeps() const { return KEEP == kAny ? keep : KEEP; }
+  // 16 pairs of columns, from column c of the layer on, `from` in tensor memory
+  template <int PAIRS>
+  __device__ __forceinline__ void load(uint32_t from, const float* b, int c, int cols, f2 (&z)[PAIRS]) const {
+    float v[2 * PAIRS];
+    if constexpr (PAIRS == 16) tmem_load32(from, v);
+    else tmem_load16(from, v);
+    tmem_wait_load();
+    if constexpr (PAIRS == 16) tmem_hold32(v);
+    else tmem_hold16(v);
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) z[i] = pair(v[2 * i], v[2 * i + 1]);
+    if (bias) {  // (the same address in every lane)
+#pragma unroll
+      for (int i = 0; i < PAIRS; ++i)
+        z[i] = add2(z[i], pair(c + 2 * i < cols ? __ldg(b + c + 2 * i) : 0.0f, c + 2 * i + 1 < cols ? __ldg(b + c + 2 * i + 1) : 0.0f));
+    }
+  }
+  __device__ __forceinline__ BlockScale scale_of(uint32_t from, const float* b, int c, int cols) const {
+    float most = 0.0f;
+#pragma unroll 1
+    for (int q = 0; q < 2; ++q, c += 32, from += 32) {
+      f2 z[16];
+      load(from, b, c, cols, z);
+      if (c + 32 > cols) {  // behind the gate's last column lie the up projection's first
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 v = halves(z[i]);
+          z[i] = pair(c + 2 * i < cols ? v.x : 0.0f, c + 2 * i + 1 < cols ? v.y : 0.0f);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) most = max_abs(most, z[i]);
+    }
+    return block_scale(most);
+  }
+  // act(g) u of eight pairs, u's in z; out h
+  template <int A>
+  __device__ __forceinline__ void gated(const f2* consts, const f2 (&g)[8], const f2* u, uint32_t* v) const {
+    const ActConsts k = shared_consts<A>(consts);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = narrow<T>(mul2(act2<A>(k, g[i]), u[i]));
+  }
+  template <int HALF, class Release>
+  __device__ __forceinline__ void run(uint32_t at, int group, Release&& release, const f2* consts, int64_t row0, int64_t rows, int col0, int cols,
+                                      char* staging, int& turn) const {
+    const uint32_t mine = at + group * 32;
+    const float *bg = bias, *bu = bias + cols;
+    uint32_t v[16], cu[8], cg[8];
+    float inv_g = 0.0f, inv_u = 0.0f;
+    bool plain = true;  // no value of the warp's blocks is infinite or NaN
+    if (keeps() == kKeptCodes) {
+      const uint32_t both = at + (group & ~1) * 32;
+      const int c = col0 & ~(kBlock - 1);
+      const BlockScale sg = scale_of(both, bg, c, cols), su = scale_of(both + HALF, bu, c, cols);
+      const int64_t row = row0 + (threadIdx.x & 31);
+      if (row < rows && c == col0) gate_scales[row * blocks + c / kBlock] = sg.scale, up_scales[row * blocks + c / kBlock] = su.scale;
+      inv_g = sg.inv, inv_u = su.inv;
+      plain = __all_sync(0xffffffffu, sg.scale == sg.scale && su.scale == su.scale);
+    }
+    if (keeps() == kKeptValue) {
+      f2 g[16];
+      load(mine, bg, col0, cols, g);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = narrow<T>(g[i]);
+      put_rows(staging, turn, v, gate, row0, rows, col0, cols);
+    }
+    f2 u[16];
+    load(mine + HALF, bu, col0, cols, u);
+    if (keeps() == kKeptValue) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = narrow<T>(u[i]);
+      put_rows(staging, turn, v, up, row0, rows, col0, cols);
+    } else if (keeps() == kKeptCodes) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) cu[i] = codes4_finite(u[2 * i], u[2 * i + 1], inv_u);
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      f2 g[8];
+      load(mine + 16 * q, bg, col0 + 16 * q, cols, g);
+      if (q) release();
+      if (keeps() == kKeptCodes) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cg[4 * q + i] = codes4_finite(g[2 * i], g[2 * i + 1], inv_g);
+      }
+      if constexpr (ACT != kAny) gated<ACT>(consts, g, u + 8 * q, v + 8 * q);
+      else if (act == ONEBIT_ACT_NONE) gated<ONEBIT_ACT_NONE>(consts, g, u + 8 * q, v + 8 * q);
+      else if (act == ONEBIT_ACT_RELU) gated<ONEBIT_ACT_RELU>(consts, g, u + 8 * q, v + 8 * q);
+      else if (act == ONEBIT_ACT_GELU) gated<ONEBIT_ACT_GELU>(consts, g, u + 8 * q, v + 8 * q);
+      else if (act == ONEBIT_ACT_GELU_TANH) gated<ONEBIT_ACT_GELU_TANH>(consts, g, u + 8 * q, v + 8 * q);
+      else gated<ONEBIT_ACT_SILU>(consts, g, u + 8 * q, v + 8 * q);
+    }
+    if (keeps() != kKeptCodes) {
+      put_rows(staging, turn, v, h, row0, rows, col0, cols);
+      return;
+    }
+    if (!plain) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) cg[i] = inv_g == 0.0f ? 0u : cg[i], cu[i] = inv_u == 0.0f ? 0u : cu[i];
+    }
+    if (h.by_tma && gate_codes.by_tma && up_codes.by_tma) {  // one fence between staging and copies
+      staging_free();
+      stage_rows<T>(staging, v);
+      stage_codes(staging + 2048, cg);
+      stage_codes(staging + 3072, cu);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) {
+        copy_out(&h.map, smem_addr(staging), col0, (int32_t)row0);
+        copy_out(&gate_codes.map, smem_addr(staging + 2048), col0, (int32_t)row0);
+        copy_out(&up_codes.map, smem_addr(staging + 3072), col0, (int32_t)row0);
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      }
+    } else {
+      store_codes(staging, cg, gate_codes, row0, rows, col0, cols);
+      store_codes(staging, cu, up_codes, row0, rows, col0, cols);
+      store_rows(staging, v, h, row0, rows, col0, cols);
+    }
+  }
+};
+
+// dz = [d u act'(g) | d act(g)], and h = act(g) u for the product of dw.  The kept halves come as InputGradEpilogue's value does:
+// a lane reads its row's 32 columns of both ahead, the first before the product is waited for.  d is read sixteen columns at
+// a time, and what becomes of them goes to the staging buffer at once: 32 columns of d, g, u and three results do not fit the
+// registers (240 bytes of spilled stores).
+template <typename T, int ACT, int KEPT>
+struct GatedGradEpilogue {
+  static constexpr bool kFold = false;
+  static constexpr bool kGated = false;
+  Input16<T> gate, up;                     // the kept values,
+  const int8_t *gate_codes, *up_codes;     // or their checkpoints
+  const float *gate_scales, *up_scales;
+  int blocks;
+  Output<T> dgate, dup, h;  // h.p NULL: not wanted
+  int act;
+  int kept;                 // Kept16: values or codes
+  bool wide_codes, vec_codes;
+
+  static constexpr int kWords = KEPT == kKeptCodes ? 8 : 16;
+  struct Ahead {
+    uint32_t g[kWords], u[kWords];
+  };
+  __device__ __forceinline__ bool by_codes() const { return (KEPT == kAny ? kept : KEPT) == kKeptCodes; }
+  __device__ __forceinline__ bool reads_ahead(int c0, int cols) const { return c0 + 32 <= cols && (by_codes() ? wide_codes : gate.wide && up.wide); }
+  __device__ __forceinline__ void fetch(Ahead& a, int64_t row, int64_t rows, int c0, int cols) const {
+    if (!reads_ahead(c0, cols) || row >= rows) return;
+    if (by_codes()) {
+      load32(gate_codes + row * cols + c0, a.g);
+      load32(up_codes + row * cols + c0, a.u);
+    } else if constexpr (KEPT != kKeptCodes) {
+      gate.ahead(row, rows, c0, cols, a.g);
+      up.ahead(row, rows, c0, cols, a.u);
+    }
+  }
+  __device__ __forceinline__ void prepare(Ahead& a, int64_t row0, int64_t rows, int col0, int cols, char*) const {
+    fetch(a, row0 + (threadIdx.x & 31), rows, col0, cols);
+  }
+  // sixteen columns: the kept ones in cg and cu (8 words of values or 4 of codes); out dgate, dup, h
+  template <int A>
+  __device__ __forceinline__ void part(const f2* consts, const f2 (&d)[8], const uint32_t* cg, const uint32_t* cu, float sg, float su, uint32_t (&vg)[8],
+                                       uint32_t (&vu)[8], uint32_t* vh) const {
+    const ActConsts k = shared_consts<A>(consts);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      f2 g[2], u[2];
+      if (by_codes()) {
+        values4<T>(cg[i / 2], sg, g);
+        values4<T>(cu[i / 2], su, u);
+      } else {
+        g[0] = widen<T>(cg[i]), g[1] = widen<T>(cg[i + 1]);
+        u[0] = widen<T>(cu[i]), u[1] = widen<T>(cu[i + 1]);
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        f2 a, s;
+        activate<A, true, true>(k, g[q], a, s);
+        vh[i + q] = narrow<T>(mul2(a, u[q]));
+        vu[i + q] = narrow<T>(mul2(d[i + q], a));
+        vg[i + q] = narrow<T>(mul2(mul2(d[i + q], u[q]), s));
+      }
+    }
+  }
+  template <class Load, class Release>
+  __device__ __forceinline__ void run(Ahead& a, Load&& load, Release&& release, const f2* consts, int64_t row0, int64_t rows, int col0, int cols,
+                                      char* staging) const {
+    const int64_t row = row0 + (threadIdx.x & 31);
+    float sg = 0.0f, su = 0.0f;
+    if (by_codes() && row < rows) sg = __ldg(gate_scales + row * blocks + col0 / kBlock), su = __ldg(up_scales + row * blocks + col0 / kBlock);
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      const int c0 = col0 + 32 * half;
+      if (c0 >= cols) {
+        release();
+        break;
+      }
+      if (!reads_ahead(c0, cols)) {
+        if (by_codes()) {
+          uint32_t c[8];
+          load_codes(staging, c, gate_codes, row0, rows, c0, cols, vec_codes);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) a.g[i] = c[i];
+          load_codes(staging, c, up_codes, row0, rows, c0, cols, vec_codes);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) a.u[i] = c[i];
+        } else if constexpr (KEPT != kKeptCodes) {
+          load_rows(staging, a.g, gate.p, gate.ld, row0, rows, c0, cols, gate.vec);
+          load_rows(staging, a.u, up.p, up.ld, row0, rows, c0, cols, up.vec);
+        }
+      }
+      uint32_t vh[16];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        f2 d[8];
+        uint32_t vg[8], vu[8];
+        load(2 * half + q, d);
+        if (q && half) release();
+        const int w = by_codes() ? 4 * q : 8 * q;
+        if constexpr (ACT != kAny) part<ACT>(consts, d, a.g + w, a.u + w, sg, su, vg, vu, vh + 8 * q);
+        else if (act == ONEBIT_ACT_NONE) part<ONEBIT_ACT_NONE>(consts, d, a.g + w, a.u + w, sg, su, vg, vu, vh + 8 * q);
+        else if (act == ONEBIT_ACT_RELU) part<ONEBIT_ACT_RELU>(consts, d, a.g + w, a.u + w, sg, su, vg, vu, vh + 8 * q);
+        else if (act == ONEBIT_ACT_GELU) part<ONEBIT_ACT_GELU>(consts, d, a.g + w, a.u + w, sg, su, vg, vu, vh + 8 * q);
+        else if (act == ONEBIT_ACT_GELU_TANH) part<ONEBIT_ACT_GELU_TANH>(consts, d, a.g + w, a.u + w, sg, su, vg, vu, vh + 8 * q);
+        else part<ONEBIT_ACT_SILU>(consts, d, a.g + w, a.u + w, sg, su, vg, vu, vh + 8 * q);
+        if (q == 0) staging_free();
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          stage_chunk(staging, 2 * q + j, vg + 4 * j);
+          stage_chunk(staging + 2048, 2 * q + j, vu + 4 * j);
+        }
+      }
+      staged();
+      send_rows(staging, dgate, row0, rows, c0, cols);
+      send_rows(staging + 2048, dup, row0, rows, c0, cols);
+      sent();
+      if (!half) fetch(a, row, rows, c0 + 32, cols);
+      if (h.p) {
+        staging_free();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) stage_chunk(staging, j, vh + 4 * j);
+        staged();
+        send_rows(staging, h, row0, rows, c0, cols);
+        sent();
+      }
+    }
+  }
+};
+
 template <typename G>
 struct PlainEpilogue {
   // the product itself in G; split s of a cut contraction goes to rows s * split_rows and on
   static constexpr bool kFold = true;
+  static constexpr bool kGated = false;
   static constexpr int act = ONEBIT_ACT_NONE;
   Output<G> out;
   int64_t split_rows;
@@ -819,7 +1140,9 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
     *gave_up = 0;
 #pragma unroll
     for (int i = 0; i < kActConsts; ++i)
-      consts[i] = splat(E.act == ONEBIT_ACT_GELU ? act_const(ONEBIT_ACT_GELU, i) : act_const(ONEBIT_ACT_GELU_TANH, i));
+      consts[i] = splat(E.act == ONEBIT_ACT_GELU   ? act_const(ONEBIT_ACT_GELU, i)
+                        : E.act == ONEBIT_ACT_SILU ? act_const(ONEBIT_ACT_SILU, i)
+                                                   : act_const(ONEBIT_ACT_GELU_TANH, i));
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc<CTAS>(smem_addr((const void*)tmem_ptr), kTmemCols);
@@ -852,12 +1175,18 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
       return ok;
     };
     bool ok = true;
+    int turn = 0;  // (gated epilogues) which half of the staging buffer comes next
     for (uint32_t u = first_unit; u < units && ok; u += unit_step) {
       const Tile t = tile_of<CTAS>(P, u);
       const int64_t row0 = t.m0 + rank * kRowsPerBlock + quad * 32;
-      const int col0 = t.n0 + group * 64;
+      const int col0 = Epilogue::kGated ? t.n0 / 2 + group * 32 : t.n0 + group * 64;
       const bool inside = row0 < P.m && col0 < P.n;
-      if constexpr (Epilogue::kFold) {
+      if constexpr (Epilogue::kGated) {
+        if (!(ok = ready())) break;
+        const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + acc * kTileN;
+        if (inside) E.template run<kTileN / 2>(at, group, release, consts, row0, P.m, col0, P.n, staging, turn);
+        else release();
+      } else if constexpr (Epilogue::kFold) {
         f2 c[2][16];
         for (int k0 = 0; k0 < t.slabs; k0 += kFoldSlabs) {
           if (!(ok = ready())) break;
@@ -885,13 +1214,16 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
         if (inside) E.prepare(ahead, row0, P.m, col0, P.n, staging);
         if (!(ok = ready())) break;
         const uint32_t at = lanes + acc * kTileN;
-        auto load = [&](int half, f2(&z)[16]) {
-          float v[32];
-          tmem_load32(at + 32 * half, v);
+        auto load = [&](int part, auto& z) {  // 32 or 16 columns
+          constexpr int kPairs = sizeof(z) / sizeof(f2);
+          float v[2 * kPairs];
+          if constexpr (kPairs == 16) tmem_load32(at + 32 * part, v);
+          else tmem_load16(at + 16 * part, v);
           tmem_wait_load();
-          tmem_hold32(v);
+          if constexpr (kPairs == 16) tmem_hold32(v);
+          else tmem_hold16(v);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) z[i] = pair(v[2 * i], v[2 * i + 1]);
+          for (int i = 0; i < kPairs; ++i) z[i] = pair(v[2 * i], v[2 * i + 1]);
         };
         if (inside) E.run(ahead, load, release, consts, row0, P.m, col0, P.n, staging);
         else release();
@@ -927,7 +1259,15 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
           } else {
             copy_box<CTAS>(da, &P.a, kk, ma, bar);
           }
-          if (B_MN) {
+          if (Epilogue::kGated) {  // the tile's first half of columns is the gate's, the second the up projection's
+            const int32_t n0 = t.n0 / 2;
+            if (CTAS == 2) {
+              copy_box<CTAS>(db, &P.b, kk, n0 + (int)rank * P.half, bar);
+            } else {
+              copy_box<CTAS>(db, &P.b, kk, n0, bar);
+              copy_box<CTAS>(db + kOperandBytes / 2, &P.b, kk, n0 + P.half, bar);
+            }
+          } else if (B_MN) {
             copy_box<CTAS>(db, &P.b, nb, kk, bar);
             copy_box<CTAS>(db + kOperandBytes / 2, &P.b, nb + 64, kk, bar);
           } else {
@@ -1056,13 +1396,15 @@ cudaError_t run_product_by(int32_t dtype, const Operand& a, const Operand& b, co
                            cudaStream_t stream) {
   ProductArgs P{};
   cudaError_t e = make_map(&P.a, dtype, a.p, A_MN ? s.k : s.m, A_MN ? s.m : s.k, a.ld, A_MN ? 64 : 128);
-  if (e == cudaSuccess) e = make_map(&P.b, dtype, b.p, B_MN ? s.k : s.n, B_MN ? s.n : s.k, b.ld, B_MN ? 64 : 128);
+  if (e == cudaSuccess)
+    e = make_map(&P.b, dtype, b.p, B_MN ? s.k : s.n, B_MN ? s.n : s.k, b.ld, B_MN || (Epilogue::kGated && CTAS == 1) ? 64 : 128);
   if (e != cudaSuccess) return e;
   P.m = s.m;
-  P.n = (int32_t)s.n;
+  P.n = (int32_t)(Epilogue::kGated ? s.n / 2 : s.n);
+  P.half = (int32_t)(s.n / 2);
   P.slabs = (int32_t)ceil_div(s.k, kSlabK);
   P.tiles_m = (int32_t)ceil_div(s.m, kRowsPerBlock * plan.ctas);
-  P.tiles_n = (int32_t)ceil_div(s.n, kRowsPerBlock * plan.ctas);
+  P.tiles_n = Epilogue::kGated ? (int32_t)ceil_div(s.n / 2, kRowsPerBlock * plan.ctas / 2) : (int32_t)ceil_div(s.n, kRowsPerBlock * plan.ctas);
   P.splits = plan.splits;
   P.split_slabs = plan.split_slabs;
   const int64_t units = (int64_t)P.tiles_m * P.tiles_n * P.splits;

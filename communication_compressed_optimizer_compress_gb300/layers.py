@@ -44,8 +44,9 @@ import torch
 
 from . import BF16, ERR_WORKSPACE, F16, F32, OK, OneBitError, _stream_ptr, lib
 
-ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = range(5)  # silu: of the gated linear layer alone
-ACTIVATIONS = {"none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH, "silu": ACT_SILU}
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = range(5)
+ACTIVATIONS = {"none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH}
+GATE_ACTIVATIONS = {**ACTIVATIONS, "silu": ACT_SILU}  # those of the gated linear layer
 NORM_LAYER, NORM_RMS = range(2)
 NORMS = {"layer": NORM_LAYER, "rms": NORM_RMS}
 CHECKPOINT_BLOCK = 64  # columns of a row that share one scale

@@ -196,6 +196,7 @@ def test_structures_match_the_header():
                     pointer = "*" in n or "*" in words[0]
                     fields.append((n.strip(" *").replace("in", "in_") if n.strip() == "in" else n.strip(" *"), ctypes.c_void_p if pointer else kinds[words[0]]))
         assert fields == list(kind._fields_), name
+    assert L.GATE_ACTIVATIONS == {**L.ACTIVATIONS, "silu": L.ACT_SILU} and f"ONEBIT_ACT_SILU = {L.ACT_SILU}" in src
     assert re.search(r"ONEBIT_NORM_LAYER = 0, ONEBIT_NORM_RMS = 1", src) and L.NORMS == {"layer": 0, "rms": 1}
 
 
