@@ -60,7 +60,6 @@ cudaError_t backward(const onebit_gated_linear_grad_t& a, Space& ws, cudaStream_
         e.gate = make_input<T>(kept.gate.x, a.ldz), e.up = make_input<T>(kept.up.x, a.ldz);
         e.gate_codes = a.gate_codes, e.up_codes = a.up_codes, e.gate_scales = a.gate_scales, e.up_scales = a.up_scales;
         e.blocks = blocks, e.act = a.activation, e.kept = a.z ? kKeptValue : kKeptCodes;
-        e.wide_codes = aligned(a.gate_codes, 32) && aligned(a.up_codes, 32) && n % 32 == 0;
         e.vec_codes = aligned(a.gate_codes, 16) && aligned(a.up_codes, 16) && n % 16 == 0;
         T* dz = static_cast<T*>(a.dz);
         cudaError_t r = make_output(&e.dgate, dz, a.rows, a.inner, a.lddz);
@@ -76,7 +75,8 @@ cudaError_t backward(const onebit_gated_linear_grad_t& a, Space& ws, cudaStream_
           case ONEBIT_ACT_GELU: return go(two, integral_constant<int, ONEBIT_ACT_GELU>{}, what);
           case ONEBIT_ACT_GELU_TANH: return go(two, integral_constant<int, ONEBIT_ACT_GELU_TANH>{}, what);
           case ONEBIT_ACT_SILU: return go(two, integral_constant<int, ONEBIT_ACT_SILU>{}, what);
-          default: return go(two, Any{}, what);
+          case ONEBIT_ACT_RELU: return go(two, integral_constant<int, ONEBIT_ACT_RELU>{}, what);
+          default: return go(two, integral_constant<int, ONEBIT_ACT_NONE>{}, what);
         }
       };
       err = plan.ctas == 1 ? go(integral_constant<int, 1>{}, Any{}, Any{})

@@ -155,6 +155,7 @@ cudaError_t forward(const onebit_gated_linear_t& a, Space& ws, cudaStream_t s, b
       T* z = static_cast<T*>(a.z);
       e.bias = a.bias;
       e.gate_scales = a.gate_scales, e.up_scales = a.up_scales;
+      e.vec_bias = aligned(a.bias, 16) && a.inner % 4 == 0;
       e.blocks = (int)blocks, e.act = a.activation, e.keep = a.z ? kKeptValue : a.gate_codes ? kKeptCodes : kKeptNone;
       cudaError_t r = make_output(&e.h, static_cast<T*>(a.h), a.rows, a.inner, a.ldh);
       if (r == cudaSuccess) r = make_output(&e.gate, z, a.rows, a.inner, a.ldz);

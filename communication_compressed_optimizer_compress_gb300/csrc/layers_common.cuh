@@ -190,6 +190,26 @@ __device__ __forceinline__ void activate(const ActConsts& c, f2 z2, f2& value, f
     }
   }
 }
+// The same without registers for the constants, for an epilogue that has none left: literals, and gelu's ten pairs as those of
+// single operations (seven instructions a pair more).
+__device__ __forceinline__ float2 gelu_single(float z) {  // value and slope
+  constexpr int A = ONEBIT_ACT_GELU;
+  const float a = magnitude6(z);
+  float p = act_const(A, 6);
+#pragma unroll
+  for (int i = 5; i >= 0; --i) p = fmaf(p, a, act_const(A, i));
+  const float tail = exp2_fast(p), m = fmaf(a * act_const(A, 8), exp2_fast(a * a * act_const(A, 7)), act_const(A, 9) - tail);
+  return make_float2(fmaf(-a, tail, fmaxf(z, 0.0f)), copysignf(m, z) + act_const(A, 9));
+}
+template <int ACT>
+__device__ __forceinline__ void activate_lean(f2 z2, f2& value, f2& slope) {
+  if constexpr (ACT == ONEBIT_ACT_GELU) {
+    const float2 z = halves(z2), lo = gelu_single(z.x), hi = gelu_single(z.y);
+    value = pair(lo.x, hi.x), slope = pair(lo.y, hi.y);
+  } else {
+    activate<ACT, true, true>(literal_consts<ACT>(), z2, value, slope);
+  }
+}
 template <int ACT>
 __device__ __forceinline__ f2 act2(const ActConsts& c, f2 z) {
   f2 v, s;

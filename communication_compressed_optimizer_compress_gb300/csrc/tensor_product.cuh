@@ -42,7 +42,7 @@ constexpr int kEpilogueWarps = 8 * CTAS;      // 128 rows are 4 quarters of the 
 template <int CTAS>
 constexpr int kProductThreads = 128 + 32 * kEpilogueWarps<CTAS>;
 // A pair's block is launched with 640 * 96 registers; 128 * 56 + 512 * 104 of them are used.
-constexpr int kControlRegs = 56, kEpilogueRegs = 104;
+constexpr int kControlRegs = 64, kEpilogueRegs = 104;
 // A warp's staging buffer: 32 rows of 64 bytes (2048, swizzled, what TMA stores; padded to 80 bytes a row
 // where single elements are stored), behind it 32 rows of 32 codes, and 64 columns' bias.
 constexpr int kStagingRow = 80;
@@ -50,9 +50,12 @@ constexpr int kCodeStaging = 32 * kStagingRow;
 constexpr int kBiasStaging = kCodeStaging + 1024;
 constexpr int kStagingBytes = kBiasStaging + 512;
 constexpr int kBarrierBytes = 256;
-template <int CTAS>
-constexpr int kProductSmem = 1024 + kStages * kStageBytes + kEpilogueWarps<CTAS> * kStagingBytes + kBarrierBytes + kActConsts * 8;
 static_assert(kStagingBytes % 512 == 0, "the swizzle's period");
+// An epilogue's staging bytes a warp, and the stages that they leave room for beside a pair's sixteen warps.
+template <int CTAS, class Epilogue>
+constexpr int kStagesWith = CTAS == 2 && Epilogue::kStaging > kStagingBytes ? kStages - 1 : kStages;
+template <int CTAS, class Epilogue>
+constexpr int kProductSmem = 1024 + kStagesWith<CTAS, Epilogue> * kStageBytes + kEpilogueWarps<CTAS> * Epilogue::kStaging + kBarrierBytes + kActConsts * 8;
 constexpr int kFoldSlabs = 8;                 // slabs that an accumulator of a folded product sums up
 constexpr int kGroupTiles = 8;                // tile rows that are walked together, for the L2
 
@@ -162,6 +165,15 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, float* v) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
                : "r"(addr));
+}
+__device__ __forceinline__ void tmem_load8(uint32_t addr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(addr));
+}
+__device__ __forceinline__ void tmem_hold8(float* v) {
+  asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]));
 }
 __device__ __forceinline__ void tmem_hold16(float* v) {
   asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
@@ -503,7 +515,9 @@ template <typename T, int ACT, int CK, int RES>
 struct ForwardEpilogue {
   // y = act(d + bias) + residual, and the 8-bit checkpoint of d + bias
   static constexpr bool kFold = false;
+  static constexpr bool kPrefetch = false;
   static constexpr bool kGated = false;
+  static constexpr int kStaging = kStagingBytes;
   const float* bias;
   Input16<T> residual;
   Output<T> y;
@@ -604,7 +618,9 @@ template <typename T, int ACT, int KEPT>
 struct InputGradEpilogue {
   // dx = d * act'(v) [+ add], and h = act(v) for the product of dw
   static constexpr bool kFold = false;
+  static constexpr bool kPrefetch = false;
   static constexpr bool kGated = false;
+  static constexpr int kStaging = kStagingBytes;
   Input16<T> x;          // the value before the activation,
   const int8_t* codes;   // or its checkpoint
   const float* scales;
@@ -753,12 +769,12 @@ __device__ __forceinline__ void send_rows(const char* from, const Output<T>& out
   T* p = out.p + row0 * out.ld + col0 + lane;
   const int last = col0 + lane < cols && row0 < rows ? (int)(rows - row0 < 32 ? rows - row0 : 32) : 0;
 #pragma unroll 1
-  for (int i = 0; i < 32; i += 16) {
-    T t[16];
+  for (int i = 0; i < 32; i += 8) {  // (sixteen at a time spill in the kernels of pairs, on their way by TMA too)
+    T t[8];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) t[k] = *reinterpret_cast<const T*>(from + (i + k) * 64 + (((lane >> 3) ^ ((i + k) >> 1 & 3)) << 4) + (lane & 7) * 2);
+    for (int k = 0; k < 8; ++k) t[k] = *reinterpret_cast<const T*>(from + (i + k) * 64 + (((lane >> 3) ^ (k >> 1 & 3)) << 4) + (lane & 7) * 2);
 #pragma unroll
-    for (int k = 0; k < 16; ++k, p += out.ld)
+    for (int k = 0; k < 8; ++k, p += out.ld)
       if (i + k < last) *p = t[k];
   }
 }
@@ -795,6 +811,7 @@ template <typename T, int ACT, int KEEP>
 struct GatedEpilogue {
   static constexpr bool kFold = false;
   static constexpr bool kGated = true;
+  static constexpr int kStaging = kStagingBytes;
   const float* bias;
   Output<T> h, gate, up;  // gate, up: z's halves (kKeptValue)
   Output<int8_t> gate_codes, up_codes;
@@ -802,6 +819,7 @@ struct GatedEpilogue {
   int blocks;
   int act;
   int keep;
+  bool vec_bias;  // on 16 bytes, and a multiple of four columns
 
   __device__ __forceinline__ int keeps() const { return KEEP == kAny ? keep : KEEP; }
   // 16 pairs of columns, from column c of the layer on, `from` in tensor memory
@@ -815,10 +833,17 @@ struct GatedEpilogue {
     else tmem_hold16(v);
 #pragma unroll
     for (int i = 0; i < PAIRS; ++i) z[i] = pair(v[2 * i], v[2 * i + 1]);
-    if (bias) {  // (the same address in every lane)
+    if (!bias) return;
+    // (the same address in every lane)
+    if (vec_bias) {
 #pragma unroll
-      for (int i = 0; i < PAIRS; ++i)
-        z[i] = add2(z[i], pair(c + 2 * i < cols ? __ldg(b + c + 2 * i) : 0.0f, c + 2 * i + 1 < cols ? __ldg(b + c + 2 * i + 1) : 0.0f));
+      for (int i = 0; i < PAIRS; i += 2) {
+        const float4 t = c + 2 * i < cols ? __ldg(reinterpret_cast<const float4*>(b + c + 2 * i)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        z[i] = add2(z[i], pair(t.x, t.y)), z[i + 1] = add2(z[i + 1], pair(t.z, t.w));
+      }
+    } else {  // past the last column nothing is kept: any value does
+#pragma unroll
+      for (int i = 0; i < PAIRS; ++i) z[i] = add2(z[i], pair(__ldg(b + min(c + 2 * i, cols - 1)), __ldg(b + min(c + 2 * i + 1, cols - 1))));
     }
   }
   __device__ __forceinline__ BlockScale scale_of(uint32_t from, const float* b, int c, int cols) const {
@@ -842,9 +867,12 @@ struct GatedEpilogue {
   // act(g) u of eight pairs, u's in z; out h
   template <int A>
   __device__ __forceinline__ void gated(const f2* consts, const f2 (&g)[8], const f2* u, uint32_t* v) const {
-    const ActConsts k = shared_consts<A>(consts);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = narrow<T>(mul2(act2<A>(k, g[i]), u[i]));
+    for (int i = 0; i < 8; ++i) {
+      f2 a, s;
+      activate_lean<A>(g[i], a, s);
+      v[i] = narrow<T>(mul2(a, u[i]));
+    }
   }
   template <int HALF, class Release>
   __device__ __forceinline__ void run(uint32_t at, int group, Release&& release, const f2* consts, int64_t row0, int64_t rows, int col0, int cols,
@@ -925,14 +953,37 @@ struct GatedEpilogue {
   }
 };
 
-// dz = [d u act'(g) | d act(g)], and h = act(g) u for the product of dw.  The kept halves come as InputGradEpilogue's value does:
-// a lane reads its row's 32 columns of both ahead, the first before the product is waited for.  d is read sixteen columns at
-// a time, and what becomes of them goes to the staging buffer at once: 32 columns of d, g, u and three results do not fit the
-// registers (240 bytes of spilled stores).
+// `WORDS` words of elements from any address, of which `left` are there; the sectors stay in L1 from one to the next.  A call:
+// in line its loads would take the registers of the kernel's ordinary way.
+template <int WORDS>
+struct Words {
+  uint32_t v[WORDS];
+};
+template <int WORDS, typename E>
+__device__ __noinline__ Words<WORDS> read_single(const E* p, int left) {
+  using Bits = std::conditional_t<sizeof(E) == 2, uint16_t, uint8_t>;
+  constexpr int kPer = 4 / sizeof(E);
+  const Bits* q = reinterpret_cast<const Bits*>(p);
+  Words<WORDS> w;
+#pragma unroll
+  for (int i = 0; i < WORDS; ++i) {
+    w.v[i] = 0;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e)
+      if (i * kPer + e < left) w.v[i] |= (uint32_t)__ldg(q + i * kPer + e) << (32 / kPer * e);
+  }
+  return w;
+}
+// dz = [d u act'(g) | d act(g)], and h = act(g) u for the product of dw.  A lane has its row's 64 columns, sixteen at a time: it
+// reads g and u ahead (out of the L2, where they were sent for under the tile before), and what becomes of them goes to the staging
+// buffer at once, a box of 32 columns for each of the three results.  With 32 columns at a time the registers spill, and a
+// kernel that spills takes 150 to 165 us for 16384 x 4096 x 1024 from checkpoints, one that does not 130 (silu and gelu, either way round).
 template <typename T, int ACT, int KEPT>
 struct GatedGradEpilogue {
   static constexpr bool kFold = false;
   static constexpr bool kGated = false;
+  static constexpr int kStaging = 3 * 2048;
+  static constexpr bool kPrefetch = true;
   Input16<T> gate, up;                     // the kept values,
   const int8_t *gate_codes, *up_codes;     // or their checkpoints
   const float *gate_scales, *up_scales;
@@ -940,51 +991,106 @@ struct GatedGradEpilogue {
   Output<T> dgate, dup, h;  // h.p NULL: not wanted
   int act;
   int kept;                 // Kept16: values or codes
-  bool wide_codes, vec_codes;
+  bool vec_codes;
 
-  static constexpr int kWords = KEPT == kKeptCodes ? 8 : 16;
+  static constexpr int kCols = 16;  // at a time
+  static constexpr int kWords = KEPT == kKeptCodes ? kCols / 4 : kCols / 2;  // of their codes or values
   struct Ahead {
     uint32_t g[kWords], u[kWords];
   };
   __device__ __forceinline__ bool by_codes() const { return (KEPT == kAny ? kept : KEPT) == kKeptCodes; }
-  __device__ __forceinline__ bool reads_ahead(int c0, int cols) const { return c0 + 32 <= cols && (by_codes() ? wide_codes : gate.wide && up.wide); }
-  __device__ __forceinline__ void fetch(Ahead& a, int64_t row, int64_t rows, int c0, int cols) const {
-    if (!reads_ahead(c0, cols) || row >= rows) return;
-    if (by_codes()) {
-      load32(gate_codes + row * cols + c0, a.g);
-      load32(up_codes + row * cols + c0, a.u);
-    } else if constexpr (KEPT != kKeptCodes) {
-      gate.ahead(row, rows, c0, cols, a.g);
-      up.ahead(row, rows, c0, cols, a.u);
+  // kCols values of a row: at once where they lie on their own size, else in pieces of 16 bytes or one by one; 0 past the end
+  __device__ __forceinline__ static void values(const Input16<T>& in, int64_t row, int c, int cols, uint32_t (&v)[kWords]) {
+    if constexpr (KEPT != kKeptCodes) {
+      const T* p = in.p + row * in.ld + c;
+      if (kCols == 16 && in.wide && c + 16 <= cols) {
+        uint32_t t[8];
+        load32(p, t);
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) v[i] = t[i];
+      } else if (in.vec && cols % 8 == 0) {
+#pragma unroll
+        for (int j = 0; j < kCols / 8; ++j) {
+          const uint4 t = c + 8 * j < cols ? __ldg(reinterpret_cast<const uint4*>(p) + j) : make_uint4(0, 0, 0, 0);
+          v[4 * j] = t.x, v[4 * j + 1] = t.y, v[4 * j + 2] = t.z, v[4 * j + 3] = t.w;
+        }
+      } else {
+        const auto w = read_single<kWords>(p, cols - c);
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) v[i] = w.v[i];
+      }
     }
+  }
+  __device__ __forceinline__ void codes(const int8_t* p, int c, int cols, uint32_t (&v)[kWords]) const {
+    if (vec_codes) {  // rows of whole sixteens
+      if constexpr (kCols == 16) {
+        const uint4 t = __ldg(reinterpret_cast<const uint4*>(p));
+        v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
+      } else {
+        const uint2 t = __ldg(reinterpret_cast<const uint2*>(p));
+        v[0] = t.x, v[1] = t.y;
+      }
+    } else {
+      const auto w = read_single<kCols / 4>(p, cols - c);
+#pragma unroll
+      for (int i = 0; i < kCols / 4; ++i) v[i] = w.v[i];
+    }
+  }
+  __device__ __forceinline__ void fetch(Ahead& a, int64_t row, int64_t rows, int c, int cols) const {
+    if (row >= rows) return;
+    if (by_codes()) {
+      codes(gate_codes + row * cols + c, c, cols, a.g);
+      codes(up_codes + row * cols + c, c, cols, a.u);
+    } else {
+      values(gate, row, c, cols, a.g);
+      values(up, row, c, cols, a.u);
+    }
+  }
+  // 64 columns of a row of both halves: a line of values, half a line of codes
+  __device__ __forceinline__ void prefetch(int64_t row, int64_t rows, int col0, int cols) const {
+    if (row >= rows || col0 >= cols) return;
+    const void *g, *u;
+    if (by_codes()) g = gate_codes + row * cols + col0, u = up_codes + row * cols + col0;
+    else g = gate.p + row * gate.ld + col0, u = up.p + row * up.ld + col0;
+    asm volatile("prefetch.global.L2 [%0];\n\tprefetch.global.L2 [%1];" ::"l"(g), "l"(u));
   }
   __device__ __forceinline__ void prepare(Ahead& a, int64_t row0, int64_t rows, int col0, int cols, char*) const {
     fetch(a, row0 + (threadIdx.x & 31), rows, col0, cols);
   }
-  // sixteen columns: the kept ones in cg and cu (8 words of values or 4 of codes); out dgate, dup, h
+  // eight columns of the three results to the staging buffer's chunk, the j-th eight of what was read ahead
   template <int A>
-  __device__ __forceinline__ void part(const f2* consts, const f2 (&d)[8], const uint32_t* cg, const uint32_t* cu, float sg, float su, uint32_t (&vg)[8],
-                                       uint32_t (&vu)[8], uint32_t* vh) const {
-    const ActConsts k = shared_consts<A>(consts);
+  __device__ __forceinline__ void part(const f2* d, const Ahead& a, int j, int chunk, float sg, float su, char* staging) const {
+    uint32_t vg[4], vu[4], vh[4];
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
+    for (int i = 0; i < 4; i += 2) {
       f2 g[2], u[2];
       if (by_codes()) {
-        values4<T>(cg[i / 2], sg, g);
-        values4<T>(cu[i / 2], su, u);
+        values4<T>(a.g[2 * j + i / 2], sg, g);
+        values4<T>(a.u[2 * j + i / 2], su, u);
       } else {
-        g[0] = widen<T>(cg[i]), g[1] = widen<T>(cg[i + 1]);
-        u[0] = widen<T>(cu[i]), u[1] = widen<T>(cu[i + 1]);
+        constexpr int kLast = kWords - 1;
+        g[0] = widen<T>(a.g[(4 * j + i) & kLast]), g[1] = widen<T>(a.g[(4 * j + i + 1) & kLast]);
+        u[0] = widen<T>(a.u[(4 * j + i) & kLast]), u[1] = widen<T>(a.u[(4 * j + i + 1) & kLast]);
       }
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        f2 a, s;
-        activate<A, true, true>(k, g[q], a, s);
-        vh[i + q] = narrow<T>(mul2(a, u[q]));
-        vu[i + q] = narrow<T>(mul2(d[i + q], a));
-        vg[i + q] = narrow<T>(mul2(mul2(d[i + q], u[q]), s));
+      for (int p = 0; p < 2; ++p) {
+        f2 v, s;
+        activate_lean<A>(g[p], v, s);
+        const f2 dh = d[4 * j + i + p];
+        vh[i + p] = narrow<T>(mul2(v, u[p]));
+        vu[i + p] = narrow<T>(mul2(dh, v));
+        vg[i + p] = narrow<T>(mul2(mul2(dh, u[p]), s));
       }
     }
+    if (j == 0 && chunk == 0) staging_free();  // the boxes sent last have left
+    stage_chunk(staging, chunk, vg);
+    stage_chunk(staging + 2048, chunk, vu);
+    if (h.p) stage_chunk(staging + 4096, chunk, vh);
+  }
+  template <int A>
+  __device__ __forceinline__ void parts(const f2 (&d)[kCols / 2], const Ahead& a, int chunk, float sg, float su, char* staging) const {
+#pragma unroll
+    for (int j = 0; j < kCols / 8; ++j) part<A>(d, a, j, chunk + j, sg, su, staging);
   }
   template <class Load, class Release>
   __device__ __forceinline__ void run(Ahead& a, Load&& load, Release&& release, const f2* consts, int64_t row0, int64_t rows, int col0, int cols,
@@ -992,61 +1098,28 @@ struct GatedGradEpilogue {
     const int64_t row = row0 + (threadIdx.x & 31);
     float sg = 0.0f, su = 0.0f;
     if (by_codes() && row < rows) sg = __ldg(gate_scales + row * blocks + col0 / kBlock), su = __ldg(up_scales + row * blocks + col0 / kBlock);
+    const int end = cols - col0 < 64 ? cols - col0 : 64;
 #pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-      const int c0 = col0 + 32 * half;
-      if (c0 >= cols) {
-        release();
-        break;
-      }
-      if (!reads_ahead(c0, cols)) {
-        if (by_codes()) {
-          uint32_t c[8];
-          load_codes(staging, c, gate_codes, row0, rows, c0, cols, vec_codes);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) a.g[i] = c[i];
-          load_codes(staging, c, up_codes, row0, rows, c0, cols, vec_codes);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) a.u[i] = c[i];
-        } else if constexpr (KEPT != kKeptCodes) {
-          load_rows(staging, a.g, gate.p, gate.ld, row0, rows, c0, cols, gate.vec);
-          load_rows(staging, a.u, up.p, up.ld, row0, rows, c0, cols, up.vec);
-        }
-      }
-      uint32_t vh[16];
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        f2 d[8];
-        uint32_t vg[8], vu[8];
-        load(2 * half + q, d);
-        if (q && half) release();
-        const int w = by_codes() ? 4 * q : 8 * q;
-        if constexpr (ACT != kAny) part<ACT>(consts, d, a.g + w, a.u + w, sg, su, vg, vu, vh + 8 * q);
-        else if (act == ONEBIT_ACT_NONE) part<ONEBIT_ACT_NONE>(consts, d, a.g + w, a.u + w, sg, su, vg, vu, vh + 8 * q);
-        else if (act == ONEBIT_ACT_RELU) part<ONEBIT_ACT_RELU>(consts, d, a.g + w, a.u + w, sg, su, vg, vu, vh + 8 * q);
-        else if (act == ONEBIT_ACT_GELU) part<ONEBIT_ACT_GELU>(consts, d, a.g + w, a.u + w, sg, su, vg, vu, vh + 8 * q);
-        else if (act == ONEBIT_ACT_GELU_TANH) part<ONEBIT_ACT_GELU_TANH>(consts, d, a.g + w, a.u + w, sg, su, vg, vu, vh + 8 * q);
-        else part<ONEBIT_ACT_SILU>(consts, d, a.g + w, a.u + w, sg, su, vg, vu, vh + 8 * q);
-        if (q == 0) staging_free();
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          stage_chunk(staging, 2 * q + j, vg + 4 * j);
-          stage_chunk(staging + 2048, 2 * q + j, vu + 4 * j);
-        }
-      }
+    for (int c = 0; c < end; c += kCols) {
+      f2 d[kCols / 2];
+      load(c / kCols, d);
+      const bool last = c + kCols >= end;
+      if (last) release();
+      const int chunk = c / 8 & 3;
+      if constexpr (ACT != kAny) parts<ACT>(d, a, chunk, sg, su, staging);
+      else if (act == ONEBIT_ACT_NONE) parts<ONEBIT_ACT_NONE>(d, a, chunk, sg, su, staging);
+      else if (act == ONEBIT_ACT_RELU) parts<ONEBIT_ACT_RELU>(d, a, chunk, sg, su, staging);
+      else if (act == ONEBIT_ACT_GELU) parts<ONEBIT_ACT_GELU>(d, a, chunk, sg, su, staging);
+      else if (act == ONEBIT_ACT_GELU_TANH) parts<ONEBIT_ACT_GELU_TANH>(d, a, chunk, sg, su, staging);
+      else parts<ONEBIT_ACT_SILU>(d, a, chunk, sg, su, staging);
+      if (!last) fetch(a, row, rows, col0 + c + kCols, cols);
+      if (!last && chunk + kCols / 8 < 4) continue;
+      const int c0 = col0 + (c & 32);
       staged();
       send_rows(staging, dgate, row0, rows, c0, cols);
       send_rows(staging + 2048, dup, row0, rows, c0, cols);
+      if (h.p) send_rows(staging + 4096, h, row0, rows, c0, cols);
       sent();
-      if (!half) fetch(a, row, rows, c0 + 32, cols);
-      if (h.p) {
-        staging_free();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) stage_chunk(staging, j, vh + 4 * j);
-        staged();
-        send_rows(staging, h, row0, rows, c0, cols);
-        sent();
-      }
     }
   }
 };
@@ -1056,6 +1129,7 @@ struct PlainEpilogue {
   // the product itself in G; split s of a cut contraction goes to rows s * split_rows and on
   static constexpr bool kFold = true;
   static constexpr bool kGated = false;
+  static constexpr int kStaging = kStagingBytes;
   static constexpr int act = ONEBIT_ACT_NONE;
   Output<G> out;
   int64_t split_rows;
@@ -1112,21 +1186,22 @@ __device__ __forceinline__ Tile tile_of(const ProductArgs& P, uint32_t unit) {
 template <int CTAS, bool A_MN, bool B_MN, class Epilogue>
 __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __grid_constant__ ProductArgs P, const __grid_constant__ Epilogue E) {
   constexpr int kTileN = kRowsPerBlock * CTAS;
+  constexpr int kRing = kStagesWith<CTAS, Epilogue>;
   constexpr uint32_t kTmemCols = 2 * kTileN;    // two accumulators
   extern __shared__ char smem_raw[];
   // (an offset, not a rounded pointer: the compiler has to see that this is shared memory)
   char* smem = smem_raw + (-(int)smem_addr(smem_raw) & 1023);
-  char* staging_base = smem + kStages * kStageBytes;
-  char* bars = staging_base + kEpilogueWarps<CTAS> * kStagingBytes;
+  char* staging_base = smem + kRing * kStageBytes;
+  char* bars = staging_base + kEpilogueWarps<CTAS> * Epilogue::kStaging;
   f2* consts = reinterpret_cast<f2*>(bars + kBarrierBytes);  // on 16 bytes
   const uint32_t bar0 = smem_addr(bars);
   auto full = [&](int s) { return bar0 + 8 * s; };
-  auto empty = [&](int s) { return bar0 + 8 * (kStages + s); };
-  auto acc_full = [&](int s) { return bar0 + 8 * (2 * kStages + s); };
-  auto acc_empty = [&](int s) { return bar0 + 8 * (2 * kStages + 2 + s); };
-  const uint32_t drained = bar0 + 8 * (2 * kStages + 4);
-  volatile uint32_t* tmem_ptr = reinterpret_cast<volatile uint32_t*>(bars + 8 * (2 * kStages + 5));
-  volatile int* gave_up = reinterpret_cast<volatile int*>(bars + 8 * (2 * kStages + 6));
+  auto empty = [&](int s) { return bar0 + 8 * (kRing + s); };
+  auto acc_full = [&](int s) { return bar0 + 8 * (2 * kRing + s); };
+  auto acc_empty = [&](int s) { return bar0 + 8 * (2 * kRing + 2 + s); };
+  const uint32_t drained = bar0 + 8 * (2 * kRing + 4);
+  volatile uint32_t* tmem_ptr = reinterpret_cast<volatile uint32_t*>(bars + 8 * (2 * kRing + 5));
+  volatile int* gave_up = reinterpret_cast<volatile int*>(bars + 8 * (2 * kRing + 6));
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CTAS == 2 ? cluster_rank() : 0;
@@ -1134,7 +1209,7 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
   const Wait wait{gave_up, P.status};
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) bar_init(full(s), 1), bar_init(empty(s), 1);
+    for (int s = 0; s < kRing; ++s) bar_init(full(s), 1), bar_init(empty(s), 1);
     for (int s = 0; s < 2; ++s) bar_init(acc_full(s), 1), bar_init(acc_empty(s), CTAS * kEpilogueWarps<CTAS>);
     bar_init(drained, 1);
     *gave_up = 0;
@@ -1158,7 +1233,7 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
     // ---- epilogue
     if (CTAS == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpilogueRegs));
     const int quad = warp & 3, group = (warp - 4) >> 2;
-    char* staging = staging_base + (warp - 4) * kStagingBytes;
+    char* staging = staging_base + (warp - 4) * Epilogue::kStaging;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + group * 64;
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -1211,17 +1286,26 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
           if (inside && col0 + 32 * q < P.n) E.run(c[q], row0, P.m, col0 + 32 * q, P.n, t.split, staging);
       } else {
         typename Epilogue::Ahead ahead;
+        if constexpr (Epilogue::kPrefetch) {  // the next tile's, from DRAM to the L2 under this one
+          const uint32_t v = u + unit_step;
+          if (v < units) {
+            const Tile n = tile_of<CTAS>(P, v);
+            E.prefetch(n.m0 + rank * kRowsPerBlock + quad * 32 + lane, P.m, n.n0 + group * 64, P.n);
+          }
+        }
         if (inside) E.prepare(ahead, row0, P.m, col0, P.n, staging);
         if (!(ok = ready())) break;
         const uint32_t at = lanes + acc * kTileN;
-        auto load = [&](int part, auto& z) {  // 32 or 16 columns
+        auto load = [&](int part, auto& z) {  // 32, 16 or 8 columns
           constexpr int kPairs = sizeof(z) / sizeof(f2);
           float v[2 * kPairs];
           if constexpr (kPairs == 16) tmem_load32(at + 32 * part, v);
-          else tmem_load16(at + 16 * part, v);
+          else if constexpr (kPairs == 8) tmem_load16(at + 16 * part, v);
+          else tmem_load8(at + 8 * part, v);
           tmem_wait_load();
           if constexpr (kPairs == 16) tmem_hold32(v);
-          else tmem_hold16(v);
+          else if constexpr (kPairs == 8) tmem_hold16(v);
+          else tmem_hold8(v);
 #pragma unroll
           for (int i = 0; i < kPairs; ++i) z[i] = pair(v[2 * i], v[2 * i + 1]);
         };
@@ -1274,14 +1358,14 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
             copy_box<CTAS>(db, &P.b, kk, nb, bar);
           }
           ++issued;
-          if (++st == kStages) st = 0, phase ^= 1;
+          if (++st == kRing) st = 0, phase ^= 1;
         }
       }
       if (!ok && rank == 0) {
         // gave up: the copies in flight land before the block leaves (a limited wait for each stage's)
-        for (int64_t q = issued > kStages ? issued - kStages : 0; q < issued; ++q) {
+        for (int64_t q = issued > kRing ? issued - kRing : 0; q < issued; ++q) {
           const long long t0 = clock64();
-          while (!bar_try(full((int)(q % kStages)), (uint32_t)(q / kStages) & 1) && clock64() - t0 < 20000000ll) {
+          while (!bar_try(full((int)(q % kRing)), (uint32_t)(q / kRing) & 1) && clock64() - t0 < 20000000ll) {
           }
         }
       }
@@ -1304,7 +1388,7 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
             if (!(ok = wait(full(st), phase))) break;
             mma_slab<CTAS, A_MN, B_MN>(d, desc_a + st * (kStageBytes >> 4), desc_b + st * (kStageBytes >> 4), P.idesc, k > k0);
             mma_commit<CTAS>(empty(st));
-            if (++st == kStages) st = 0, phase ^= 1;
+            if (++st == kRing) st = 0, phase ^= 1;
           }
           if (!ok) break;
           mma_commit<CTAS>(acc_full(acc));
@@ -1369,7 +1453,7 @@ cudaError_t launch_product(const ProductArgs& P, const Epilogue& E, int sms, cud
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem<CTAS>);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem<CTAS, Epilogue>);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
@@ -1377,7 +1461,7 @@ cudaError_t launch_product(const ProductArgs& P, const Epilogue& E, int sms, cud
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((units < most ? units : most) * CTAS));
   cfg.blockDim = dim3(kProductThreads<CTAS>);
-  cfg.dynamicSmemBytes = kProductSmem<CTAS>;
+  cfg.dynamicSmemBytes = kProductSmem<CTAS, Epilogue>;
   cfg.stream = s;
   cudaLaunchAttribute attr[2]{};
   attr[0].id = cudaLaunchAttributeClusterDimension;
