@@ -1,0 +1,869 @@
+// residual_norm.cuh -- kernels of the residual sum with the norms around it, forward and backward with the parameters'
+// gradients.  See include/onebit_layers.h for the formulas.
+#pragma once
+
+#include <atomic>
+#include <type_traits>
+
+#include "dropout.cuh"
+
+namespace onebit {
+namespace layers {
+
+struct ResidualForward {
+  const void* x;
+  int64_t ldx;
+  const void* block;  // NULL: s = x
+  int64_t ldblock;
+  const float *gamma, *beta, *block_gamma, *block_beta, *gate;
+  Dropout drop;
+  void* s;
+  int64_t lds;
+  void* y;
+  int64_t ldy;
+  float *mean, *rstd, *block_mean, *block_rstd;
+  int64_t rows;
+  int cols, groups;
+  bool layer;
+  float inv_cols, eps, scale;
+};
+
+struct ResidualBackward {
+  const void* dy;
+  int64_t lddy;
+  const void* ds;
+  int64_t ldds;
+  const void* s;
+  int64_t lds;
+  const void* block;
+  int64_t ldblock;
+  const float *gamma, *block_gamma, *block_beta, *gate;
+  Dropout drop;
+  const float *mean, *rstd, *block_mean, *block_rstd;
+  void* dx;
+  int64_t lddx;
+  void* dblock;
+  int64_t lddblock;
+  int64_t rows;
+  int cols, groups;
+  bool layer;
+  float inv_cols, scale;
+  float* part;  // the parameters' partial sums
+  float* sums;  // (rows read again:) each row's two sums behind the norm before the next block
+};
+
+// ------------------------------------------------------------------------------------------------
+// Rows held in registers between their statistics and their outputs, so that they are read once: TPR threads have a row, a
+// thread CH groups of eight neighbouring columns (and the same columns of every row that it meets, so that parameters stay
+// in registers and their gradients add up there).  Both passes are bound by the bytes of the rows: what the next rows need is
+// copied ahead into shared memory, each thread's own columns into a slot of its own, which takes no registers and no
+// barrier (backward reads four rows for each one: ahead in registers it would have 16 warps an SM and one row in flight).
+template <typename T, bool VEC>
+constexpr int kVectors = (int)sizeof(T) / 2;  // 16-byte vectors of a group
+
+__device__ __forceinline__ void copy16(void* to, const void* from, int bytes) {  // the rest of 16 is zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <typename T, int TPR, int CH, bool VEC, int IN, int STAGES, int THREADS>
+struct RowRing {
+  static constexpr int kSlot = CH * kVectors<T, VEC>;
+  static constexpr int kBytes = VEC ? STAGES * IN * kSlot * THREADS * 16 : 0;
+  uint4* mine;  // this thread's first slot
+  __device__ __forceinline__ explicit RowRing(char* smem) : mine(reinterpret_cast<uint4*>(smem) + threadIdx.x) {}
+  __device__ __forceinline__ uint4* at(int stage, int in, int j, int v) const { return mine + (((stage * IN + in) * CH + j) * kVectors<T, VEC> + v) * THREADS; }
+  // row r of one input, from p, its first element, on; nothing where there is no such row
+  __device__ __forceinline__ void ahead(int stage, int in, const T* p, int64_t ld, int64_t r, bool there, int t, int cols) const {
+    if (!VEC) return;
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      const int c = (j * TPR + t) * 8;
+      const bool some = there && c < cols;
+#pragma unroll
+      for (int v = 0; v < kVectors<T, VEC>; ++v) copy16(at(stage, in, j, v), some ? p + r * ld + c + v * (16 / (int)sizeof(T)) : p, some ? 16 : 0);
+    }
+  }
+  // eight columns, 0 past the end
+  __device__ __forceinline__ void take(int stage, int in, const T* p, int64_t ld, int64_t r, bool there, int t, int cols, int j, f2 (&f)[4]) const {
+    const int c = (j * TPR + t) * 8;
+    if (VEC) {
+      Raw8<T> raw;
+#pragma unroll
+      for (int v = 0; v < kVectors<T, VEC>; ++v) raw.v[v] = *at(stage, in, j, v);
+      expand8(raw, f);
+    } else {
+      load_group<T, false>(p + r * ld + c, there ? cols - c : 0, f);
+    }
+  }
+};
+
+// a parameter's eight columns, `none` where there is no parameter, 0 past the end
+__device__ __forceinline__ void held8(const float* p, int c, int cols, float none, f2 (&f)[4]) {
+  if (!p) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = pair(c + 2 * e < cols ? none : 0.0f, c + 2 * e + 1 < cols ? none : 0.0f);
+  } else if ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && c + 8 <= cols) {
+    expand8(load8(p + c), f);
+  } else {
+    load_group<float, false>(p + c, cols - c, f);
+  }
+}
+
+// Sums over the TPR threads of a row, the same order on every call; every thread gets them.  `red` has room for two sets,
+// used alternately, so that one barrier a call is enough.
+template <int TPR, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[N * (TPR < 32 ? 1 : TPR / 32)], int& turn, int bar) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int o = (TPR < 32 ? TPR : 32) / 2; o; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  if constexpr (TPR > 32) {
+    constexpr int kWarps = TPR / 32;
+    float* r = red[turn];
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) r[(threadIdx.x % TPR >> 5) * N + i] = v[i];
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(TPR) : "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) v[i] += r[w * N + i];
+    }
+  }
+}
+
+// (v - mean, its squares' sum): one row's distance from its mean; columns past the end stay 0
+template <int TPR, int CH>
+__device__ __forceinline__ float centre(f2 (&v)[CH][4], float mean, int t, int cols) {
+  f2 s = 0;
+#pragma unroll
+  for (int j = 0; j < CH; ++j) {
+    const int c = (j * TPR + t) * 8;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[j][e] = add2(v[j][e], pair(c + 2 * e < cols ? -mean : 0.0f, c + 2 * e + 1 < cols ? -mean : 0.0f));
+      s = fma2(v[j][e], v[j][e], s);
+    }
+  }
+  return sum_of(s);
+}
+template <int CH>
+__device__ __forceinline__ float total(const f2 (&v)[CH][4]) {
+  f2 s = 0;
+#pragma unroll
+  for (int j = 0; j < CH; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s = add2(s, v[j][e]);
+  return sum_of(s);
+}
+
+template <int TPR>
+constexpr int kForwardThreads = TPR > 256 ? TPR : 256;
+// blocks an SM: 64 registers a thread where one group of columns and no norm behind the block are held, 80 with it, else 128
+template <int TPR, int CH, bool POST>
+constexpr int kForwardBlocks = (CH > 1 ? 512 : POST ? 768 : 1024) / kForwardThreads<TPR>;
+template <typename T>
+constexpr int kForwardStages = sizeof(T) == 2 ? 4 : 3;
+
+template <typename T, int TPR, int CH, bool VEC, bool POST>
+static __global__ void __launch_bounds__(kForwardThreads<TPR>, kForwardBlocks<TPR, CH, POST>) k_rn_forward(const ResidualForward A) {
+  constexpr int kThreads = kForwardThreads<TPR>, kGroups = kThreads / TPR, kStages = kForwardStages<T>;
+  extern __shared__ __align__(16) char dynamic[];
+  __shared__ float red[kGroups][2][TPR < 32 ? 1 : TPR / 32];
+  const int t = threadIdx.x % TPR, group = threadIdx.x / TPR, cols = A.cols;
+  const RowRing<T, TPR, CH, VEC, 2, kStages, kThreads> ring(dynamic);
+  const T *x = static_cast<const T*>(A.x), *b = static_cast<const T*>(A.block);
+  const int64_t step = (int64_t)gridDim.x * kGroups, first = (int64_t)blockIdx.x * kGroups;
+  in_turn();
+  auto ahead = [&](int stage, int64_t r) {
+    ring.ahead(stage, 0, x, A.ldx, r, r < A.rows, t, cols);
+    if (b) ring.ahead(stage, 1, b, A.ldblock, r, r < A.rows, t, cols);
+    copies_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) ahead(i, first + group + i * step);
+  const Generator gen(A.drop);
+  // what the block's values are multiplied by and what is added behind its norm, gamma, beta
+  f2 pa[CH][4], pb[CH][4], gamma[CH][4], beta[CH][4];
+#pragma unroll
+  for (int j = 0; j < CH; ++j) {
+    const int c = (j * TPR + t) * 8;
+    held8(A.gate, c, cols, 1.0f, pa[j]);
+    if (POST) {
+      f2 g[4];
+      held8(A.block_beta, c, cols, 0.0f, pb[j]);
+      held8(A.block_gamma, c, cols, 1.0f, g);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) pb[j][e] = mul2(mul2(pb[j][e], pa[j][e]), splat(A.scale)), pa[j][e] = mul2(pa[j][e], g[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) pa[j][e] = mul2(pa[j][e], splat(A.scale));
+    held8(A.gamma, c, cols, 0.0f, gamma[j]);
+    held8(A.beta, c, cols, 0.0f, beta[j]);
+  }
+  int turn = 0, stage = 0;
+  for (int64_t base = first; base < A.rows; base += step) {  // (whole warps stay together, whatever rows are left)
+    const int64_t r = base + group;
+    const bool there = r < A.rows;
+    copies_wait<kStages - 2>();
+    ahead(stage == 0 ? kStages - 1 : stage - 1, r + (kStages - 1) * step);
+    f2 s[CH][4];
+#pragma unroll
+    for (int j = 0; j < CH; ++j) ring.take(stage, 0, x, A.ldx, r, there, t, cols, j, s[j]);
+    if (b) {
+      f2 n[CH][4];
+#pragma unroll
+      for (int j = 0; j < CH; ++j) ring.take(stage, 1, b, A.ldblock, r, there, t, cols, j, n[j]);
+      if (POST) {
+        float v[1], mean = 0.0f;
+        if (A.layer) {
+          v[0] = total(n);
+          row_sums<TPR>(v, red[group], turn, 1 + group);
+          mean = v[0] * A.inv_cols;
+        }
+        v[0] = centre<TPR>(n, mean, t, cols);
+        row_sums<TPR>(v, red[group], turn, 1 + group);
+        const float rstd = halves(rsqrt_rounded(splat(fmaf(v[0], A.inv_cols, A.eps)))).x;
+        if (t == 0 && there) {
+          if (A.layer) A.block_mean[r] = mean;
+          A.block_rstd[r] = rstd;
+        }
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) n[j][e] = fma2(mul2(n[j][e], splat(rstd)), pa[j][e], pb[j][e]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) n[j][e] = mul2(n[j][e], pa[j][e]);
+      }
+#pragma unroll
+      for (int j = 0; j < CH; ++j) {
+        const int c = (j * TPR + t) * 8;
+        if (gen.threshold) gen.apply8(r * A.groups + c / 8, n[j]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[j][e] = add2(s[j][e], n[j][e]);
+        if (there && c < cols) store_group8<T, VEC>(static_cast<T*>(A.s) + r * A.lds + c, cols - c, s[j]);
+      }
+    }
+    if (A.gamma) {
+      float v[1], mean = 0.0f;
+      if (A.layer) {
+        v[0] = total(s);
+        row_sums<TPR>(v, red[group], turn, 1 + group);
+        mean = v[0] * A.inv_cols;
+      }
+      v[0] = centre<TPR>(s, mean, t, cols);
+      row_sums<TPR>(v, red[group], turn, 1 + group);
+      const float rstd = halves(rsqrt_rounded(splat(fmaf(v[0], A.inv_cols, A.eps)))).x;
+      if (t == 0 && there) {
+        if (A.layer) A.mean[r] = mean;
+        A.rstd[r] = rstd;
+      }
+#pragma unroll
+      for (int j = 0; j < CH; ++j) {
+        const int c = (j * TPR + t) * 8;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[j][e] = fma2(mul2(s[j][e], splat(rstd)), gamma[j][e], beta[j][e]);
+        if (there && c < cols) store_group8<T, VEC>(static_cast<T*>(A.y) + r * A.ldy + c, cols - c, s[j]);
+      }
+    }
+    if (++stage == kStages) stage = 0;
+  }
+  copies_wait<0>();
+}
+
+constexpr int kBackwardThreads = 512;  // of 128 registers: all that an SM has room for, so that it leaves one part
+template <typename T>
+constexpr int kBackwardStages = sizeof(T) == 2 ? 4 : 3;
+
+template <typename T, int TPR, bool VEC, bool POST>
+static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(const ResidualBackward A) {
+  constexpr int kGroups = kBackwardThreads / TPR, kStages = kBackwardStages<T>;
+  constexpr int kKinds = POST ? 4 : 3;  // sums of dy shat, dy, d bhat, d (the last for the norm behind the block)
+  extern __shared__ __align__(16) char dynamic[];
+  __shared__ float red[kGroups][2][2 * (TPR < 32 ? 1 : TPR / 32)];
+  const int t = threadIdx.x % TPR, group = threadIdx.x / TPR, cols = A.cols, c = t * 8;
+  const RowRing<T, TPR, 1, VEC, 4, kStages, kBackwardThreads> ring(dynamic);
+  const T *dy = static_cast<const T*>(A.dy), *ds = static_cast<const T*>(A.ds), *s = static_cast<const T*>(A.s), *b = static_cast<const T*>(A.block);
+  const int64_t step = (int64_t)gridDim.x * kGroups, first = (int64_t)blockIdx.x * kGroups;
+  const bool pre = A.gamma != nullptr, needs_block = POST || A.gate;
+  in_turn();
+  auto ahead = [&](int stage, int64_t r) {
+    const bool there = r < A.rows;
+    if (pre) ring.ahead(stage, 0, dy, A.lddy, r, there, t, cols), ring.ahead(stage, 1, s, A.lds, r, there, t, cols);
+    if (ds) ring.ahead(stage, 2, ds, A.ldds, r, there, t, cols);
+    if (needs_block) ring.ahead(stage, 3, b, A.ldblock, r, there, t, cols);
+    copies_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) ahead(i, first + group + i * step);
+  const Generator gen(A.drop);
+  f2 gamma[4], pa[4], sum[kKinds][4];
+  held8(A.gamma, c, cols, 0.0f, gamma);
+  held8(A.gate, c, cols, 1.0f, pa);
+  if (POST) {
+    f2 g[4];
+    held8(A.block_gamma, c, cols, 1.0f, g);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) pa[e] = mul2(pa[e], g[e]);
+  }
+#pragma unroll
+  for (int k = 0; k < kKinds; ++k)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[k][e] = 0;
+  float mean = 0.0f, rstd = 0.0f, block_mean = 0.0f, block_rstd = 0.0f;  // of the next row
+  auto statistics = [&](int64_t r) {
+    if (r >= A.rows) return;
+    if (pre) {
+      if (A.layer) mean = __ldg(A.mean + r);
+      rstd = __ldg(A.rstd + r);
+    }
+    if (POST) {
+      if (A.layer) block_mean = __ldg(A.block_mean + r);
+      block_rstd = __ldg(A.block_rstd + r);
+    }
+  };
+  statistics(first + group);
+  int turn = 0, stage = 0;
+  for (int64_t base = first; base < A.rows; base += step) {
+    const int64_t r = base + group;
+    const bool there = r < A.rows;
+    const float mu = mean, rs = rstd, bmu = block_mean, brs = block_rstd;
+    copies_wait<kStages - 2>();
+    ahead(stage == 0 ? kStages - 1 : stage - 1, r + (kStages - 1) * step);
+    statistics(r + step);
+    f2 d[4];  // t, then d, then what is left of it before the block
+    if (ds) {
+      ring.take(stage, 2, ds, A.ldds, r, there, t, cols, 0, d);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[e] = 0;
+    }
+    if (pre) {
+      f2 q[4], hat[4], s0 = 0, s1 = 0;
+      ring.take(stage, 0, dy, A.lddy, r, there, t, cols, 0, q);
+      ring.take(stage, 1, s, A.lds, r, there, t, cols, 0, hat);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {  // columns past the end have dy = gamma = 0 and add nothing
+        hat[e] = mul2(add2(hat[e], splat(-mu)), splat(rs));
+        sum[0][e] = fma2(q[e], hat[e], sum[0][e]);
+        sum[1][e] = add2(sum[1][e], q[e]);
+        q[e] = mul2(q[e], gamma[e]);
+        s0 = add2(s0, q[e]);
+        s1 = fma2(q[e], hat[e], s1);
+      }
+      float v[2] = {sum_of(s0), sum_of(s1)};
+      row_sums<TPR>(v, red[group], turn, 1 + group);
+      const f2 m0 = splat(A.layer ? -v[0] * A.inv_cols * rs : 0.0f), m1 = splat(-v[1] * A.inv_cols * rs);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[e] = add2(fma2(hat[e], m1, fma2(q[e], splat(rs), m0)), d[e]);
+    }
+    const bool inside = there && c < cols;
+    if (inside) store_group8<T, VEC>(static_cast<T*>(A.dx) + r * A.lddx + c, cols - c, d);
+    if (A.dblock) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[e] = mul2(d[e], splat(A.scale));
+      if (gen.threshold) gen.apply8(r * A.groups + t, d);
+      if (needs_block) {
+        f2 hat[4];
+        ring.take(stage, 3, b, A.ldblock, r, there, t, cols, 0, hat);
+        if (POST) {
+          f2 s0 = 0, s1 = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            hat[e] = mul2(add2(hat[e], splat(-bmu)), splat(brs));
+            // (t is not 0 past the end, and a row that is not there has no statistics of its own)
+            const f2 v = inside ? d[e] : 0;
+            sum[2][e] = fma2(v, hat[e], sum[2][e]);
+            sum[kKinds - 1][e] = add2(sum[kKinds - 1][e], v);
+            d[e] = mul2(v, pa[e]);
+            s0 = add2(s0, d[e]);
+            s1 = fma2(d[e], hat[e], s1);
+          }
+          float v[2] = {sum_of(s0), sum_of(s1)};
+          row_sums<TPR>(v, red[group], turn, 1 + group);
+          const f2 m0 = splat(A.layer ? -v[0] * A.inv_cols * brs : 0.0f), m1 = splat(-v[1] * A.inv_cols * brs);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) d[e] = fma2(hat[e], m1, fma2(d[e], splat(brs), m0));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            sum[2][e] = fma2(inside ? d[e] : 0, hat[e], sum[2][e]);
+            d[e] = mul2(d[e], pa[e]);
+          }
+        }
+      }
+      if (inside) store_group8<T, VEC>(static_cast<T*>(A.dblock) + r * A.lddblock + c, cols - c, d);
+    }
+    if (++stage == kStages) stage = 0;
+  }
+  copies_wait<0>();
+  if (!A.part) return;
+  // the upper half of the row groups hand their sums to the lower, until one has them
+  constexpr int kSums = kKinds * 4;
+  f2* const join = reinterpret_cast<f2*>(dynamic);
+#pragma unroll 1
+  for (int n = kGroups; n > 1; n /= 2) {
+    const int low = n / 2;
+    __syncthreads();
+    if (group >= low && group < n) {
+#pragma unroll
+      for (int i = 0; i < kSums; ++i) join[((group - low) * kSums + i) * TPR + t] = sum[i / 4][i % 4];
+    }
+    __syncthreads();
+    if (group < low) {
+#pragma unroll
+      for (int i = 0; i < kSums; ++i) sum[i / 4][i % 4] = add2(sum[i / 4][i % 4], join[(group * kSums + i) * TPR + t]);
+    }
+  }
+  if (group == 0 && c < cols) {
+    float* p = A.part + (int64_t)blockIdx.x * 4 * cols + c;
+#pragma unroll
+    for (int k = 0; k < kKinds; ++k) store_group8<float, false>(p + k * cols, cols - c, sum[k]);
+  }
+}
+template <typename T, int TPR, bool VEC, bool POST>
+constexpr int kBackwardSmem = [] {
+  constexpr int ring = RowRing<T, TPR, 1, VEC, 4, kBackwardStages<T>, kBackwardThreads>::kBytes, join = kBackwardThreads / 2 * (POST ? 4 : 3) * 4 * 8;
+  return ring > join ? ring : join;
+}();
+
+// ------------------------------------------------------------------------------------------------
+// Rows of any width, read again for each step: one block a row, a thread eight columns at a time.
+constexpr int kWideThreads = 256;
+constexpr int kWideWarps = kWideThreads / 32;
+template <int N>
+__device__ __forceinline__ void block_sums(float (&v)[N], float (*red)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+  __syncthreads();  // red may still be read from the sums before
+  if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) red[threadIdx.x >> 5][i] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWideWarps; ++w) v[i] += red[w][i];
+  }
+}
+// (mean, rstd) of eight columns at a time from get(column, values), which gives 0 past the end
+template <typename Get>
+__device__ __forceinline__ float2 row_statistics(Get&& get, int cols, bool layer, float inv_cols, float eps, float (*red)[1]) {
+  float v[1], mean = 0.0f;
+  if (layer) {
+    f2 t = 0;
+    for (int c = threadIdx.x * 8; c < cols; c += kWideThreads * 8) {
+      f2 f[4];
+      get(c, f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t = add2(t, f[e]);
+    }
+    v[0] = sum_of(t);
+    block_sums(v, red);
+    mean = v[0] * inv_cols;
+  }
+  f2 t = 0;
+  for (int c = threadIdx.x * 8; c < cols; c += kWideThreads * 8) {
+    f2 f[4];
+    get(c, f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const f2 d = add2(f[e], pair(c + 2 * e < cols ? -mean : 0.0f, c + 2 * e + 1 < cols ? -mean : 0.0f));
+      t = fma2(d, d, t);
+    }
+  }
+  v[0] = sum_of(t);
+  block_sums(v, red);
+  return make_float2(mean, halves(rsqrt_rounded(splat(fmaf(v[0], inv_cols, eps)))).x);
+}
+
+// a parameter's eight columns, `none` where there is no parameter
+__device__ __forceinline__ void param8(const float* p, int c, int cols, float none, f2 (&f)[4]) {
+  if (!p) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = splat(none);
+  } else {
+    load_group<float, false>(p + c, cols - c, f);
+  }
+}
+
+template <typename T>
+static __global__ void __launch_bounds__(kWideThreads) k_rn_forward_wide(const ResidualForward A) {
+  in_turn();
+  __shared__ float red[kWideWarps][1];
+  const Generator gen(A.drop);
+  for (int64_t r = blockIdx.x; r < A.rows; r += gridDim.x) {
+    const T* x = static_cast<const T*>(A.x) + r * A.ldx;
+    const T* b = static_cast<const T*>(A.block) + r * A.ldblock;
+    float2 bst = make_float2(0.0f, 1.0f);
+    auto block = [&](int c, f2(&f)[4]) { load_group<T, false>(b + c, A.cols - c, f); };
+    if (A.block_gamma) {
+      bst = row_statistics(block, A.cols, A.layer, A.inv_cols, A.eps, red);
+      if (threadIdx.x == 0) {
+        if (A.block_mean) A.block_mean[r] = bst.x;
+        A.block_rstd[r] = bst.y;
+      }
+    }
+    auto sum = [&](int c, f2(&f)[4]) {
+      load_group<T, false>(x + c, A.cols - c, f);
+      if (!A.block) return;
+      f2 n[4], p[4], q[4];
+      block(c, n);
+      if (A.block_gamma) {
+        param8(A.block_gamma, c, A.cols, 0.0f, p);
+        param8(A.block_beta, c, A.cols, 0.0f, q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) n[e] = fma2(mul2(add2(n[e], splat(-bst.x)), splat(bst.y)), p[e], q[e]);
+      }
+      if (A.drop.threshold) gen.apply8(r * A.groups + c / 8, n);
+      param8(A.gate, c, A.cols, 1.0f, p);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f[e] = fma2(mul2(n[e], splat(A.scale)), p[e], f[e]);
+        const float2 h = halves(f[e]);  // past the end there is no column (without a gate there is no parameter to be 0 there)
+        f[e] = pair(c + 2 * e < A.cols ? h.x : 0.0f, c + 2 * e + 1 < A.cols ? h.y : 0.0f);
+      }
+    };
+    float2 st = make_float2(0.0f, 1.0f);
+    if (A.gamma) {
+      st = row_statistics(sum, A.cols, A.layer, A.inv_cols, A.eps, red);
+      if (threadIdx.x == 0) {
+        if (A.mean) A.mean[r] = st.x;
+        A.rstd[r] = st.y;
+      }
+    }
+    for (int c = threadIdx.x * 8; c < A.cols; c += kWideThreads * 8) {
+      f2 f[4], p[4], q[4];
+      sum(c, f);
+      if (A.block) store_group8<T, false>(static_cast<T*>(A.s) + r * A.lds + c, A.cols - c, f);
+      if (A.gamma) {
+        param8(A.gamma, c, A.cols, 0.0f, p);
+        param8(A.beta, c, A.cols, 0.0f, q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = fma2(mul2(add2(f[e], splat(-st.x)), splat(st.y)), p[e], q[e]);
+        store_group8<T, false>(static_cast<T*>(A.y) + r * A.ldy + c, A.cols - c, f);
+      }
+    }
+  }
+}
+
+// What a row's columns pass on backward, eight of them: shat, dy and t, the gradient of s; d and n behind it.
+template <typename T>
+struct RowBackward {
+  const ResidualBackward& A;
+  const Generator& gen;
+  int64_t r;
+  float mean, rstd, block_mean, block_rstd;
+  __device__ __forceinline__ RowBackward(const ResidualBackward& a, const Generator& g, int64_t row)
+      : A(a), gen(g), r(row), mean(a.mean ? a.mean[row] : 0.0f), rstd(a.rstd ? a.rstd[row] : 0.0f), block_mean(a.block_mean ? a.block_mean[row] : 0.0f),
+        block_rstd(a.block_rstd ? a.block_rstd[row] : 0.0f) {}
+  __device__ __forceinline__ void load(const void* p, int64_t ld, int c, f2 (&f)[4]) const {
+    load_group<T, false>(static_cast<const T*>(p) + r * ld + c, A.cols - c, f);
+  }
+  __device__ __forceinline__ void before(int c, f2 (&dy)[4], f2 (&shat)[4]) const {  // with gamma
+    load(A.dy, A.lddy, c, dy);
+    load(A.s, A.lds, c, shat);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) shat[e] = mul2(add2(shat[e], splat(-mean)), splat(rstd));
+  }
+  // t, from the row's means of q and q shat
+  __device__ __forceinline__ void t(int c, float m0, float m1, f2 (&out)[4]) const {
+    f2 ds[4];
+    if (A.ds) load(A.ds, A.ldds, c, ds);
+    if (A.gamma) {
+      f2 dy[4], shat[4], g[4];
+      before(c, dy, shat);
+      param8(A.gamma, c, A.cols, 0.0f, g);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        out[e] = mul2(fma2(shat[e], splat(-m1), fma2(dy[e], g[e], splat(-m0))), splat(rstd));
+        if (A.ds) out[e] = add2(out[e], ds[e]);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[e] = ds[e];
+    }
+  }
+  // d = scale t mask, from t
+  __device__ __forceinline__ void through(int c, f2 (&v)[4]) const {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = mul2(v[e], splat(A.scale));
+    if (A.drop.threshold) gen.apply8(r * A.groups + c / 8, v);
+  }
+  __device__ __forceinline__ void bhat(int c, f2 (&b)[4]) const {  // normalised behind a norm, else the block itself
+    load(A.block, A.ldblock, c, b);
+    if (A.block_gamma) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b[e] = mul2(add2(b[e], splat(-block_mean)), splat(block_rstd));
+    }
+  }
+  // f = d gate block_gamma, from d; 0 past the end
+  __device__ __forceinline__ void gated(int c, f2 (&v)[4]) const {
+    f2 p[4], q[4];
+    param8(A.gate, c, A.cols, 1.0f, p);
+    param8(A.block_gamma, c, A.cols, 1.0f, q);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = mul2(mul2(v[e], p[e]), q[e]);
+  }
+};
+
+template <typename T>
+static __global__ void __launch_bounds__(kWideThreads) k_rn_backward_wide(const ResidualBackward A) {
+  in_turn();
+  __shared__ float red[kWideWarps][2];
+  const Generator gen(A.drop);
+  for (int64_t r = blockIdx.x; r < A.rows; r += gridDim.x) {
+    const RowBackward<T> row(A, gen, r);
+    float m[2] = {0.0f, 0.0f};
+    if (A.gamma) {
+      f2 s0 = 0, s1 = 0;
+      for (int c = threadIdx.x * 8; c < A.cols; c += kWideThreads * 8) {
+        f2 dy[4], shat[4], g[4];
+        row.before(c, dy, shat);
+        param8(A.gamma, c, A.cols, 0.0f, g);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const f2 q = mul2(dy[e], g[e]);
+          s0 = add2(s0, q);
+          s1 = fma2(q, shat[e], s1);
+        }
+      }
+      m[0] = sum_of(s0), m[1] = sum_of(s1);
+      block_sums(m, red);
+      m[0] = A.layer ? m[0] * A.inv_cols : 0.0f;
+      m[1] *= A.inv_cols;
+      if (threadIdx.x == 0) A.sums[2 * r] = m[0], A.sums[2 * r + 1] = m[1];
+    }
+    float n[2] = {0.0f, 0.0f};
+    if (A.block_gamma) {
+      f2 s0 = 0, s1 = 0;
+      for (int c = threadIdx.x * 8; c < A.cols; c += kWideThreads * 8) {
+        f2 v[4], b[4];
+        row.t(c, m[0], m[1], v);
+        row.through(c, v);
+        row.gated(c, v);
+        row.bhat(c, b);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s0 = add2(s0, v[e]);
+          s1 = fma2(v[e], b[e], s1);
+        }
+      }
+      n[0] = sum_of(s0), n[1] = sum_of(s1);
+      block_sums(n, red);
+      n[0] = A.layer ? n[0] * A.inv_cols : 0.0f;
+      n[1] *= A.inv_cols;
+    }
+    for (int c = threadIdx.x * 8; c < A.cols; c += kWideThreads * 8) {
+      f2 v[4], b[4];
+      row.t(c, m[0], m[1], v);
+      store_group8<T, false>(static_cast<T*>(A.dx) + r * A.lddx + c, A.cols - c, v);
+      if (!A.dblock) continue;
+      row.through(c, v);
+      row.gated(c, v);
+      if (A.block_gamma) {
+        row.bhat(c, b);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = mul2(fma2(b[e], splat(-n[1]), add2(v[e], splat(-n[0]))), splat(row.block_rstd));
+      }
+      store_group8<T, false>(static_cast<T*>(A.dblock) + r * A.lddblock + c, A.cols - c, v);
+    }
+  }
+}
+
+// The parameters' gradients of one run of rows follow from four sums over them: of dy shat and dy, and of d bhat and d.
+template <typename T>
+static __global__ void __launch_bounds__(kWideThreads) k_rn_param_wide(const ResidualBackward A, int64_t run) {
+  in_turn();
+  const int c = (blockIdx.x * kWideThreads + threadIdx.x) * 8;
+  if (c >= A.cols) return;
+  const Generator gen(A.drop);
+  const int64_t r0 = blockIdx.y * run, r1 = r0 + run < A.rows ? r0 + run : A.rows;
+  f2 sum[4][4] = {};
+  for (int64_t r = r0; r < r1; ++r) {
+    const RowBackward<T> row(A, gen, r);
+    f2 v[4], b[4];
+    if (A.gamma) {
+      row.before(c, v, b);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[0][e] = fma2(v[e], b[e], sum[0][e]), sum[1][e] = add2(sum[1][e], v[e]);
+    }
+    if (A.block_gamma || A.gate) {
+      row.t(c, A.gamma ? A.sums[2 * r] : 0.0f, A.gamma ? A.sums[2 * r + 1] : 0.0f, v);
+      row.through(c, v);
+      row.bhat(c, b);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[2][e] = fma2(v[e], b[e], sum[2][e]), sum[3][e] = add2(sum[3][e], v[e]);
+    }
+  }
+  float* p = A.part + (int64_t)blockIdx.y * 4 * A.cols + c;
+#pragma unroll
+  for (int k = 0; k < 4; ++k, p += A.cols) store_group8<float, false>(p, A.cols - c, sum[k]);
+}
+
+// The parameters' gradients from the four sums of each part, added in a fixed order: a block has eight columns (a sector of a
+// part's row), 128 threads to each of them.
+struct ParamGrads {
+  void *dgamma, *dbeta, *dblock_gamma, *dblock_beta, *dgate;
+};
+template <typename G>
+static __global__ void __launch_bounds__(1024) k_rn_params(const float* __restrict__ part, int64_t parts, int cols, const float* __restrict__ block_gamma,
+                                                           const float* __restrict__ block_beta, const float* __restrict__ gate, const ParamGrads out) {
+  __shared__ float red[4][8][129], sums[4][8];
+  const int col = threadIdx.x & 7, row = threadIdx.x >> 3, c = blockIdx.x * 8 + col;
+  const bool need[4] = {out.dgamma != nullptr, out.dbeta != nullptr, out.dblock_gamma || out.dgate, out.dblock_beta || (out.dgate && block_beta)};
+  in_turn();
+  float s[4] = {};
+  if (c < cols) {
+    for (int64_t p = row; p < parts; p += 128) {
+      const float* q = part + p * 4 * cols + c;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (need[k]) s[k] += q[(int64_t)k * cols];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) red[k][col][row] = s[k];
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;  // a warp's kind and column
+  const float* q = red[warp >> 3][warp & 7];
+  const float total = warp_sum(q[lane] + q[lane + 32] + (q[lane + 64] + q[lane + 96]));
+  if (lane == 0) sums[warp >> 3][warp & 7] = total;
+  __syncthreads();
+  const int o = blockIdx.x * 8 + threadIdx.x;
+  if (threadIdx.x >= 8 || o >= cols) return;
+  const float a = sums[2][threadIdx.x], b = sums[3][threadIdx.x], at = gate ? gate[o] : 1.0f;
+  if (out.dgamma) static_cast<G*>(out.dgamma)[o] = from_f<G>(sums[0][threadIdx.x]);
+  if (out.dbeta) static_cast<G*>(out.dbeta)[o] = from_f<G>(sums[1][threadIdx.x]);
+  if (out.dblock_gamma) static_cast<G*>(out.dblock_gamma)[o] = from_f<G>(a * at);
+  if (out.dblock_beta) static_cast<G*>(out.dblock_beta)[o] = from_f<G>(b * at);
+  if (out.dgate) static_cast<G*>(out.dgate)[o] = from_f<G>(block_gamma ? fmaf(a, block_gamma[o], block_beta ? b * block_beta[o] : 0.0f) : a);
+}
+
+// ------------------------------------------------------------------------------------------------
+// host side
+
+inline unsigned at_most(int64_t want, int64_t per_sm) {
+  const int64_t most = (int64_t)sm_count() * per_sm;
+  return (unsigned)(want < most ? want : most);
+}
+// With `bytes` of dynamic shared memory, which a kernel is allowed once for each device.
+template <typename Args>
+inline cudaError_t launch_rows(void (*kernel)(const Args), std::atomic<uint64_t>& ready, unsigned grid, int threads, int bytes, cudaStream_t s,
+                               const Args& a) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+// the widest rows that are held in registers; wider ones are read again for each step
+constexpr int kForwardCols = 512 * 2 * 8, kBackwardCols = 512 * 8;
+
+// f(threads a row): the fewest that hold `cols` columns, eight each
+template <typename F>
+auto with_threads(int64_t cols, F&& f) {
+  using std::integral_constant;
+  if (cols <= 64) return f(integral_constant<int, 8>{});
+  if (cols <= 128) return f(integral_constant<int, 16>{});
+  if (cols <= 256) return f(integral_constant<int, 32>{});
+  if (cols <= 512) return f(integral_constant<int, 64>{});
+  if (cols <= 1024) return f(integral_constant<int, 128>{});
+  if (cols <= 2048) return f(integral_constant<int, 256>{});
+  return f(integral_constant<int, 512>{});
+}
+
+template <typename T, int TPR, int CH, bool VEC, bool POST>
+cudaError_t run_forward(const ResidualForward& a, cudaStream_t s) {
+  static std::atomic<uint64_t> ready{0};
+  constexpr int kThreads = kForwardThreads<TPR>, kBytes = RowRing<T, TPR, CH, VEC, 2, kForwardStages<T>, kThreads>::kBytes;
+  return launch_rows(k_rn_forward<T, TPR, CH, VEC, POST>, ready, at_most(ceil_div(a.rows, kThreads / TPR), kForwardBlocks<TPR, CH, POST>), kThreads,
+                     kBytes, s, a);
+}
+template <typename T>
+cudaError_t rn_forward(const ResidualForward& a, cudaStream_t s) {
+  if (a.cols > kForwardCols) return launch_after(k_rn_forward_wide<T>, at_most(a.rows, 8), kWideThreads, s, a);
+  auto on16 = [](const void* p, int64_t ld) { return aligned(p, 16) && (ld * (int64_t)sizeof(T)) % 16 == 0; };
+  const bool vec = a.cols % 8 == 0 && on16(a.x, a.ldx) && on16(a.block, a.ldblock) && on16(a.s, a.lds) && on16(a.y, a.ldy);
+  auto by = [&](auto tpr, auto ch) {
+    constexpr int kTpr = decltype(tpr)::value, kCh = decltype(ch)::value;
+    if (vec) return a.block_gamma ? run_forward<T, kTpr, kCh, true, true>(a, s) : run_forward<T, kTpr, kCh, true, false>(a, s);
+    return a.block_gamma ? run_forward<T, kTpr, kCh, false, true>(a, s) : run_forward<T, kTpr, kCh, false, false>(a, s);
+  };
+  using std::integral_constant;
+  if (a.cols > 4096) return by(integral_constant<int, 512>{}, integral_constant<int, 2>{});
+  return with_threads(a.cols, [&](auto tpr) { return by(tpr, integral_constant<int, 1>{}); });
+}
+
+template <typename T, int TPR, bool VEC, bool POST>
+cudaError_t run_backward(const ResidualBackward& a, unsigned parts, cudaStream_t s) {
+  static std::atomic<uint64_t> ready{0};
+  return launch_rows(k_rn_backward<T, TPR, VEC, POST>, ready, parts, kBackwardThreads, kBackwardSmem<T, TPR, VEC, POST>, s, a);
+}
+// Takes the workspace; with `run`, enqueues the work too.
+template <typename T>
+cudaError_t rn_backward(ResidualBackward a, const ParamGrads& g, int32_t grad_dtype, char* workspace, int64_t* used, cudaStream_t s, bool run) {
+  const bool params = g.dgamma || g.dbeta || g.dblock_gamma || g.dblock_beta || g.dgate, wide = a.cols > kBackwardCols;
+  const int64_t run_rows = a.rows ? ceil_div(a.rows, 64) : 1;  // of a wide kernel's part
+  const int64_t parts = a.rows == 0 ? 0
+                        : wide      ? ceil_div(a.rows, run_rows)
+                                    : with_threads(a.cols, [&](auto tpr) { return (int64_t)at_most(ceil_div(a.rows, kBackwardThreads / decltype(tpr)::value), 1); });
+  const int64_t part_bytes = params ? (parts * 4 * a.cols * 4 + 15) & ~(int64_t)15 : 0;
+  *used = part_bytes + (wide && a.gamma ? a.rows * 8 : 0);
+  if (!run) return cudaSuccess;
+  a.part = params ? reinterpret_cast<float*>(workspace) : nullptr;
+  a.sums = reinterpret_cast<float*>(workspace + part_bytes);
+  cudaError_t e = cudaSuccess;
+  if (a.rows == 0) {
+  } else if (wide) {
+    e = launch_after(k_rn_backward_wide<T>, at_most(a.rows, 8), kWideThreads, s, a);
+    if (e == cudaSuccess && params)
+      e = launch_after(k_rn_param_wide<T>, dim3((unsigned)ceil_div(a.cols, kWideThreads * 8), (unsigned)parts), kWideThreads, s, a, run_rows);
+  } else {
+    auto on16 = [](const void* p, int64_t ld) { return aligned(p, 16) && (ld * (int64_t)sizeof(T)) % 16 == 0; };
+    const bool vec = a.cols % 8 == 0 && on16(a.dy, a.lddy) && on16(a.ds, a.ldds) && on16(a.s, a.lds) && on16(a.block, a.ldblock) && on16(a.dx, a.lddx) &&
+                     on16(a.dblock, a.lddblock);
+    e = with_threads(a.cols, [&](auto tpr) {
+      constexpr int kTpr = decltype(tpr)::value;
+      if (vec) return a.block_gamma ? run_backward<T, kTpr, true, true>(a, (unsigned)parts, s) : run_backward<T, kTpr, true, false>(a, (unsigned)parts, s);
+      return a.block_gamma ? run_backward<T, kTpr, false, true>(a, (unsigned)parts, s) : run_backward<T, kTpr, false, false>(a, (unsigned)parts, s);
+    });
+  }
+  if (e != cudaSuccess || !params) return e;
+  auto finish = [&](auto* kernel) {
+    return launch_after(kernel, (unsigned)ceil_div(a.cols, 8), 1024, s, a.part, parts, a.cols, a.block_gamma, a.block_beta, a.gate, g);
+  };
+  return grad_dtype == ONEBIT_F32 ? finish(k_rn_params<float>) : grad_dtype == ONEBIT_F16 ? finish(k_rn_params<__half>) : finish(k_rn_params<__nv_bfloat16>);
+}
+
+}  // namespace layers
+}  // namespace onebit
