@@ -43,14 +43,20 @@ struct Generator {
   __device__ __forceinline__ uint4 draw(int64_t group) const {
     return philox(make_uint4((uint32_t)(uint64_t)group, (uint32_t)((uint64_t)group >> 32), step, site), k0, k1);
   }
-  // a pair of columns (2 q and 2 q + 1 of the group) times the factor, or 0
-  __device__ __forceinline__ f2 apply(uint32_t word, f2 v) const {
-    const float2 h = halves(mul2(v, splat(factor)));
-    return pair((word & 0xffffu) >= threshold ? h.x : 0.0f, (word >> 16) >= threshold ? h.y : 0.0f);
+  // a group's values, 0 where they are dropped (the upper half of a word is compared in place: what lies below it decides nothing)
+  __device__ __forceinline__ void keep8(int64_t group, f2 (&v)[4]) const {
+    const uint4 w = draw(group);
+    const uint32_t words[4] = {w.x, w.y, w.z, w.w}, least = threshold << 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 h = halves(v[i]);
+      v[i] = pair((words[i] << 16) >= least ? h.x : 0.0f, words[i] >= least ? h.y : 0.0f);
+    }
   }
   __device__ __forceinline__ void apply8(int64_t group, f2 (&v)[4]) const {
-    const uint4 w = draw(group);
-    v[0] = apply(w.x, v[0]), v[1] = apply(w.y, v[1]), v[2] = apply(w.z, v[2]), v[3] = apply(w.w, v[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], splat(factor));
+    keep8(group, v);
   }
 };
 

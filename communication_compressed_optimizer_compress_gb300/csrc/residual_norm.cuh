@@ -55,14 +55,107 @@ struct ResidualBackward {
 // ------------------------------------------------------------------------------------------------
 // Rows held in registers between their statistics and their outputs, so that they are read once: TPR threads have a row, a
 // thread CH groups of eight neighbouring columns (and the same columns of every row that it meets, so that parameters stay
-// in registers and their gradients add up there).  Both passes are bound by the bytes of the rows: what the next rows need is
-// copied ahead into shared memory, each thread's own columns into a slot of its own, which takes no registers and no
-// barrier (backward reads four rows for each one: ahead in registers it would have 16 warps an SM and one row in flight).
-template <typename T, bool VEC>
-constexpr int kVectors = (int)sizeof(T) / 2;  // 16-byte vectors of a group
+// in registers and their gradients add up there).  What the next rows need is copied ahead into shared memory, each
+// thread's own columns into slots of its own, which takes no registers and no barrier (backward reads four rows for each one:
+// ahead in registers it would have 16 warps an SM and one row in flight).
+//
+// Rows that lie on 16 bytes and are whole groups (VEC) are copied and stored as they lie.  Of others a thread copies the aligned
+// vectors that its columns touch, one more than they fill, and shifts; their outputs are put together from its own and its
+// neighbour's values into aligned vectors, single elements where a warp's columns or the row begin and end.
 
-__device__ __forceinline__ void copy16(void* to, const void* from, int bytes) {  // the rest of 16 is zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from), "r"(bytes) : "memory");
+__device__ __forceinline__ uint32_t lanes_of(int width) {  // the lanes of this lane's group of `width`
+  return width == 32 ? 0xffffffffu : ((1u << width) - 1) << (threadIdx.x & 31 & ~(width - 1));
+}
+
+// One input's rows on their way: IN inputs share the ring, this is the `in`-th.
+template <typename T, int TPR, int CH, bool VEC, int IN, int STAGES, int THREADS>
+struct RowStream {
+  static constexpr int kOwn = (int)sizeof(T) / 2, kVectors = kOwn + (VEC ? 0 : 1);  // 16-byte vectors of a group
+  static constexpr int kBytes = STAGES * IN * CH * kVectors * THREADS * 16;
+  const T* base;  // the matrix
+  const T* next;  // the row to copy next
+  int64_t hop;
+  uint32_t slot;
+  __device__ __forceinline__ RowStream(char* smem, int in, const void* p, int64_t ld, int64_t first, int64_t step, int t, int cols)
+      : base(static_cast<const T*>(p)), next(base + first * ld), hop(step * ld),
+        slot((uint32_t)__cvta_generic_to_shared(smem) + ((uint32_t)in * CH * kVectors * THREADS + threadIdx.x) * 16) {
+#pragma unroll
+    for (int j = 0; j < CH; ++j)
+      if ((j * TPR + t) * 8 >= cols) {  // nothing is ever copied there: zeros
+#pragma unroll
+        for (int i = 0; i < STAGES; ++i)
+#pragma unroll
+          for (int v = 0; v < kVectors; ++v) asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at(i, j, v)), "r"(0) : "memory");
+      }
+  }
+  __device__ __forceinline__ uint32_t at(int stage, int j, int v) const {
+    return slot + (uint32_t)(stage * (IN * CH * kVectors * THREADS) + (j * kVectors + v) * THREADS) * 16;
+  }
+  __device__ __forceinline__ void ahead(int stage, int t, int cols) {
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      const int c = (j * TPR + t) * 8;
+      if (c >= cols) continue;
+      if (VEC) {
+#pragma unroll
+        for (int v = 0; v < kVectors; ++v)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at(stage, j, v)), "l"(next + c + v * (16 / (int)sizeof(T))) : "memory");
+      } else {
+        const char* const row = reinterpret_cast<const char*>(next);
+        const int m = (int)(reinterpret_cast<uintptr_t>(row) & 15);
+        const int left = m + (cols - c) * (int)sizeof(T);  // from the first vector to the row's end
+#pragma unroll
+        for (int v = 0; v < kVectors; ++v) {
+          const int bytes = left - 16 * v < 16 ? left - 16 * v : 16;  // the rest is zeros
+          if (v == 0 && c == 0 && m > 0 && next == base) {  // what lies before the matrix's first row is left alone
+#pragma unroll 1
+            for (int e = 0; e < 16; e += (int)sizeof(T)) {
+              uint32_t bits = 0;
+              if (e >= m && e < bytes) {
+                if (sizeof(T) == 2) bits = *reinterpret_cast<const uint16_t*>(row - m + e);
+                else bits = *reinterpret_cast<const uint32_t*>(row - m + e);
+              }
+              if (sizeof(T) == 2) asm volatile("st.shared.b16 [%0], %1;" ::"r"(at(stage, j, v) + e), "h"((uint16_t)bits) : "memory");
+              else asm volatile("st.shared.b32 [%0], %1;" ::"r"(at(stage, j, v) + e), "r"(bits) : "memory");
+            }
+          } else {
+            const bool some = bytes > 0;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(at(stage, j, v)), "l"(some ? row - m + (int64_t)c * (int)sizeof(T) + 16 * v : row - m),
+                         "r"(some ? bytes : 0)
+                         : "memory");
+          }
+        }
+      }
+    }
+    next += hop;
+  }
+  // eight columns of a row, 0 past the end; m: the row's distance from 16 bytes (VEC: any)
+  __device__ __forceinline__ void take(int stage, int j, int m, f2 (&f)[4]) const {
+    uint32_t w[4 * kVectors];
+#pragma unroll
+    for (int v = 0; v < kVectors; ++v)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[4 * v]), "=r"(w[4 * v + 1]), "=r"(w[4 * v + 2]), "=r"(w[4 * v + 3]) : "r"(at(stage, j, v)) : "memory");
+    if (!VEC) {
+      constexpr int n = 4 * kOwn;
+#pragma unroll
+      for (int i = 0; i < n + 2; ++i) w[i] = m & 8 ? w[i + 2] : w[i];
+#pragma unroll
+      for (int i = 0; i < n + 1; ++i) w[i] = m & 4 ? w[i + 1] : w[i];
+      if (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < n; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (m & 2) * 8);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 2) f[i] = widen<T>(w[i]);
+      else f[i] = pair(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    }
+  }
+};
+template <typename T>
+__device__ __forceinline__ int off16(const void* p, int64_t ld, int64_t r) {  // a row's distance from 16 bytes
+  return (int)((uint32_t)reinterpret_cast<uintptr_t>(p) + (uint32_t)r * (uint32_t)ld * (uint32_t)sizeof(T)) & 15;
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -70,37 +163,71 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <typename T, int TPR, int CH, bool VEC, int IN, int STAGES, int THREADS>
-struct RowRing {
-  static constexpr int kSlot = CH * kVectors<T, VEC>;
-  static constexpr int kBytes = VEC ? STAGES * IN * kSlot * THREADS * 16 : 0;
-  uint4* mine;  // this thread's first slot
-  __device__ __forceinline__ explicit RowRing(char* smem) : mine(reinterpret_cast<uint4*>(smem) + threadIdx.x) {}
-  __device__ __forceinline__ uint4* at(int stage, int in, int j, int v) const { return mine + (((stage * IN + in) * CH + j) * kVectors<T, VEC> + v) * THREADS; }
-  // row r of one input, from p, its first element, on; nothing where there is no such row
-  __device__ __forceinline__ void ahead(int stage, int in, const T* p, int64_t ld, int64_t r, bool there, int t, int cols) const {
-    if (!VEC) return;
-#pragma unroll
-    for (int j = 0; j < CH; ++j) {
-      const int c = (j * TPR + t) * 8;
-      const bool some = there && c < cols;
-#pragma unroll
-      for (int v = 0; v < kVectors<T, VEC>; ++v) copy16(at(stage, in, j, v), some ? p + r * ld + c + v * (16 / (int)sizeof(T)) : p, some ? 16 : 0);
-    }
+// Eight columns from c on of a row of an output.  All lanes of a row's group come here together.
+template <typename T, int TPR, bool VEC>
+__device__ __forceinline__ void store_columns(T* row, int c, int cols, const f2 (&f)[4]) {
+  if (VEC) {
+    if (c < cols) store8(row + c, f);
+    return;
   }
-  // eight columns, 0 past the end
-  __device__ __forceinline__ void take(int stage, int in, const T* p, int64_t ld, int64_t r, bool there, int t, int cols, int j, f2 (&f)[4]) const {
-    const int c = (j * TPR + t) * 8;
-    if (VEC) {
-      Raw8<T> raw;
+  constexpr int kSize = (int)sizeof(T), n = kSize * 2, kWidth = TPR < 32 ? TPR : 32;  // n: words
+  uint32_t w[n + 4];  // the last four words of the lane before, then this lane's
 #pragma unroll
-      for (int v = 0; v < kVectors<T, VEC>; ++v) raw.v[v] = *at(stage, in, j, v);
-      expand8(raw, f);
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kSize == 2) {
+      w[4 + i] = narrow<T>(f[i]);
     } else {
-      load_group<T, false>(p + r * ld + c, there ? cols - c : 0, f);
+      const float2 h = halves(f[i]);
+      w[4 + 2 * i] = __float_as_uint(h.x), w[5 + 2 * i] = __float_as_uint(h.y);
     }
   }
-};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = __shfl_up_sync(lanes_of(kWidth), w[n + i], 1, kWidth);
+  if (c >= cols) return;
+  const int lane = threadIdx.x & (kWidth - 1), m = (int)(reinterpret_cast<uintptr_t>(row) & 15), left = cols - c;
+  // vector v has this lane's elements before (16 v + 16 - m) / kSize; the last m / kSize go with the next lane's
+  bool whole[n / 4];
+  uint32_t x[n + 4];
+#pragma unroll
+  for (int i = 0; i < n + 4; ++i) x[i] = w[i];
+  const int sh = 16 - m;
+#pragma unroll
+  for (int i = 0; i < n; ++i) x[i] = sh & 16 ? x[i + 4] : x[i];
+  if (!(sh & 16)) {
+#pragma unroll
+    for (int i = 0; i < n + 2; ++i) x[i] = sh & 8 ? x[i + 2] : x[i];
+#pragma unroll
+    for (int i = 0; i < n + 1; ++i) x[i] = sh & 4 ? x[i + 1] : x[i];
+    if (kSize == 2) {
+#pragma unroll
+      for (int i = 0; i < n; ++i) x[i] = __funnelshift_r(x[i], x[i + 1], (sh & 2) * 8);
+    }
+  }
+  char* const to = reinterpret_cast<char*>(row + c) - m;
+#pragma unroll
+  for (int v = 0; v < n / 4; ++v) {
+    whole[v] = left * kSize >= 16 * v + 16 - m && (v > 0 || lane > 0 || m == 0);
+    if (whole[v]) *reinterpret_cast<uint4*>(to + 16 * v) = make_uint4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
+  }
+  const bool last = lane == kWidth - 1 || c + 8 >= cols;  // no lane behind takes this one's last elements
+  if ((last && m > 0) || !whole[0] || !whole[n / 4 - 1]) {
+    auto put = [&](int at, uint32_t word, int e) {  // element e of a word's two or one
+      if constexpr (kSize == 2) reinterpret_cast<uint16_t*>(row)[at] = (uint16_t)(e ? word >> 16 : word);
+      else reinterpret_cast<uint32_t*>(row)[at] = word;
+    };
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int v = (e * kSize + m) / 16;
+      const bool vector = v < n / 4 ? (v == 0 ? whole[0] : whole[n / 4 - 1]) : !last;
+      if (e < left && !vector) put(c + e, w[4 + e * kSize / 4], kSize == 2 ? e & 1 : 0);
+    }
+    if (!whole[0] && lane > 0) {  // the row ends inside the vector that the lane before counts on
+#pragma unroll
+      for (int e = 8 - 16 / kSize < 0 ? 0 : 8 - 16 / kSize; e < 8; ++e)
+        if ((8 - e) * kSize <= m) put(c + e - 8, w[4 + e * kSize / 4 - n], kSize == 2 ? e & 1 : 0);
+    }
+  }
+}
 
 // a parameter's eight columns, `none` where there is no parameter, 0 past the end
 __device__ __forceinline__ void held8(const float* p, int c, int cols, float none, f2 (&f)[4]) {
@@ -117,42 +244,63 @@ __device__ __forceinline__ void held8(const float* p, int c, int cols, float non
 // Sums over the TPR threads of a row, the same order on every call; every thread gets them.  `red` has room for two sets,
 // used alternately, so that one barrier a call is enough.
 template <int TPR, int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[N * (TPR < 32 ? 1 : TPR / 32)], int& turn, int bar) {
+constexpr int kRedWords = TPR > 32 ? N * TPR / 32 : 4;
+template <int TPR, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[kRedWords<TPR, N>], int& turn, int bar) {
+  constexpr int kWidth = TPR < 32 ? TPR : 32;
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int o = (TPR < 32 ? TPR : 32) / 2; o; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    for (int o = kWidth / 2; o; o >>= 1) v[i] += __shfl_xor_sync(lanes_of(kWidth), v[i], o);
   if constexpr (TPR > 32) {
     constexpr int kWarps = TPR / 32;
     float* r = red[turn];
     turn ^= 1;
     if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) r[(threadIdx.x % TPR >> 5) * N + i] = v[i];
+      for (int i = 0; i < N; ++i) r[i * kWarps + (threadIdx.x % TPR >> 5)] = v[i];
     }
     asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(TPR) : "memory");
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      v[i] = 0.0f;
+      if constexpr (kWarps % 4 == 0) {
+        v[i] = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) v[i] += r[w * N + i];
+        for (int w = 0; w < kWarps; w += 4) {
+          const float4 q = *reinterpret_cast<const float4*>(r + i * kWarps + w);
+          v[i] += (q.x + q.y) + (q.z + q.w);
+        }
+      } else {
+        const float2 q = *reinterpret_cast<const float2*>(r + i * kWarps);
+        v[i] = q.x + q.y;
+      }
     }
   }
 }
 
-// (v - mean, its squares' sum): one row's distance from its mean; columns past the end stay 0
-template <int TPR, int CH>
+// v becomes its distance from the mean, columns past the end stay 0; returns its squares' sum
+template <int TPR, int CH, bool VEC>
 __device__ __forceinline__ float centre(f2 (&v)[CH][4], float mean, int t, int cols) {
   f2 s = 0;
 #pragma unroll
   for (int j = 0; j < CH; ++j) {
     const int c = (j * TPR + t) * 8;
+    const f2 shift = splat(c < cols ? -mean : 0.0f);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      v[j][e] = add2(v[j][e], pair(c + 2 * e < cols ? -mean : 0.0f, c + 2 * e + 1 < cols ? -mean : 0.0f));
+      v[j][e] = add2(v[j][e], VEC ? shift : pair(c + 2 * e < cols ? -mean : 0.0f, c + 2 * e + 1 < cols ? -mean : 0.0f));
       s = fma2(v[j][e], v[j][e], s);
     }
   }
+  return sum_of(s);
+}
+template <int CH>
+__device__ __forceinline__ float squares(const f2 (&v)[CH][4]) {
+  f2 s = 0;
+#pragma unroll
+  for (int j = 0; j < CH; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s = fma2(v[j][e], v[j][e], s);
   return sum_of(s);
 }
 template <int CH>
@@ -167,79 +315,89 @@ __device__ __forceinline__ float total(const f2 (&v)[CH][4]) {
 
 template <int TPR>
 constexpr int kForwardThreads = TPR > 256 ? TPR : 256;
-// blocks an SM: 64 registers a thread where one group of columns and no norm behind the block are held, 80 with it, else 128
+// blocks an SM: 80 registers a thread where one group of columns is held, else 128
 template <int TPR, int CH, bool POST>
-constexpr int kForwardBlocks = (CH > 1 ? 512 : POST ? 768 : 1024) / kForwardThreads<TPR>;
+constexpr int kForwardBlocks = (CH > 1 ? 512 : 768) / kForwardThreads<TPR>;
 template <typename T>
-constexpr int kForwardStages = sizeof(T) == 2 ? 4 : 3;
+constexpr int kForwardStages = sizeof(T) == 2 ? 3 : 2;
 
 template <typename T, int TPR, int CH, bool VEC, bool POST>
 static __global__ void __launch_bounds__(kForwardThreads<TPR>, kForwardBlocks<TPR, CH, POST>) k_rn_forward(const ResidualForward A) {
   constexpr int kThreads = kForwardThreads<TPR>, kGroups = kThreads / TPR, kStages = kForwardStages<T>;
   extern __shared__ __align__(16) char dynamic[];
-  __shared__ float red[kGroups][2][TPR < 32 ? 1 : TPR / 32];
+  __shared__ __align__(16) float red[kGroups][2][kRedWords<TPR, 1>];
   const int t = threadIdx.x % TPR, group = threadIdx.x / TPR, cols = A.cols;
-  const RowRing<T, TPR, CH, VEC, 2, kStages, kThreads> ring(dynamic);
-  const T *x = static_cast<const T*>(A.x), *b = static_cast<const T*>(A.block);
-  const int64_t step = (int64_t)gridDim.x * kGroups, first = (int64_t)blockIdx.x * kGroups;
+  const int64_t step = (int64_t)gridDim.x * kGroups, first = (int64_t)blockIdx.x * kGroups + group;
+  using Stream = RowStream<T, TPR, CH, VEC, 2, kStages, kThreads>;
+  Stream x(dynamic, 0, A.x, A.ldx, first, step, t, cols), b(dynamic, 1, A.block, A.ldblock, first, step, t, cols);
+  const bool block = A.block != nullptr;
   in_turn();
+  if (first >= A.rows) return;  // (no barrier is the whole block's)
   auto ahead = [&](int stage, int64_t r) {
-    ring.ahead(stage, 0, x, A.ldx, r, r < A.rows, t, cols);
-    if (b) ring.ahead(stage, 1, b, A.ldblock, r, r < A.rows, t, cols);
+    if (r < A.rows) {
+      x.ahead(stage, t, cols);
+      if (block) b.ahead(stage, t, cols);
+    }
     copies_commit();
   };
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) ahead(i, first + group + i * step);
+  for (int i = 0; i < kStages - 1; ++i) ahead(i, first + i * step);
   const Generator gen(A.drop);
-  // what the block's values are multiplied by and what is added behind its norm, gamma, beta
+  // what the block's values are multiplied by (dropout's factor included) and what is added behind its norm, gamma, beta
   f2 pa[CH][4], pb[CH][4], gamma[CH][4], beta[CH][4];
+  const f2 scale = splat(A.scale * (gen.threshold ? gen.factor : 1.0f));
 #pragma unroll
   for (int j = 0; j < CH; ++j) {
     const int c = (j * TPR + t) * 8;
     held8(A.gate, c, cols, 1.0f, pa[j]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) pa[j][e] = mul2(pa[j][e], scale);
     if (POST) {
       f2 g[4];
       held8(A.block_beta, c, cols, 0.0f, pb[j]);
       held8(A.block_gamma, c, cols, 1.0f, g);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) pb[j][e] = mul2(mul2(pb[j][e], pa[j][e]), splat(A.scale)), pa[j][e] = mul2(pa[j][e], g[e]);
+      for (int e = 0; e < 4; ++e) pb[j][e] = mul2(pb[j][e], pa[j][e]), pa[j][e] = mul2(pa[j][e], g[e]);
     }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) pa[j][e] = mul2(pa[j][e], splat(A.scale));
     held8(A.gamma, c, cols, 0.0f, gamma[j]);
     held8(A.beta, c, cols, 0.0f, beta[j]);
   }
   int turn = 0, stage = 0;
-  for (int64_t base = first; base < A.rows; base += step) {  // (whole warps stay together, whatever rows are left)
-    const int64_t r = base + group;
-    const bool there = r < A.rows;
+  T *ps = static_cast<T*>(A.s) + first * A.lds, *py = static_cast<T*>(A.y) + first * A.ldy;
+  // (v - mean) and 1/sqrt of its mean square
+  auto normal = [&](f2(&v)[CH][4], float* means, float* rstds, int64_t r) {
+    float q[1];
+    if (A.layer) {
+      q[0] = total(v);
+      row_sums<TPR>(q, red[group], turn, 1 + group);
+      const float mean = q[0] * A.inv_cols;
+      if (t == 0) means[r] = mean;
+      q[0] = centre<TPR, CH, VEC>(v, mean, t, cols);
+    } else {
+      q[0] = squares(v);
+    }
+    row_sums<TPR>(q, red[group], turn, 1 + group);
+    const float rstd = halves(rsqrt_rounded(splat(fmaf(q[0], A.inv_cols, A.eps)))).x;
+    if (t == 0) rstds[r] = rstd;
+    return splat(rstd);
+  };
+  for (int64_t r = first; r < A.rows; r += step) {
     copies_wait<kStages - 2>();
     ahead(stage == 0 ? kStages - 1 : stage - 1, r + (kStages - 1) * step);
     f2 s[CH][4];
+    const int mx = VEC ? 0 : off16<T>(A.x, A.ldx, r), mb = VEC ? 0 : off16<T>(A.block, A.ldblock, r);
 #pragma unroll
-    for (int j = 0; j < CH; ++j) ring.take(stage, 0, x, A.ldx, r, there, t, cols, j, s[j]);
-    if (b) {
+    for (int j = 0; j < CH; ++j) x.take(stage, j, mx, s[j]);
+    if (block) {
       f2 n[CH][4];
 #pragma unroll
-      for (int j = 0; j < CH; ++j) ring.take(stage, 1, b, A.ldblock, r, there, t, cols, j, n[j]);
+      for (int j = 0; j < CH; ++j) b.take(stage, j, mb, n[j]);
       if (POST) {
-        float v[1], mean = 0.0f;
-        if (A.layer) {
-          v[0] = total(n);
-          row_sums<TPR>(v, red[group], turn, 1 + group);
-          mean = v[0] * A.inv_cols;
-        }
-        v[0] = centre<TPR>(n, mean, t, cols);
-        row_sums<TPR>(v, red[group], turn, 1 + group);
-        const float rstd = halves(rsqrt_rounded(splat(fmaf(v[0], A.inv_cols, A.eps)))).x;
-        if (t == 0 && there) {
-          if (A.layer) A.block_mean[r] = mean;
-          A.block_rstd[r] = rstd;
-        }
+        const f2 rstd = normal(n, A.block_mean, A.block_rstd, r);
 #pragma unroll
         for (int j = 0; j < CH; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) n[j][e] = fma2(mul2(n[j][e], splat(rstd)), pa[j][e], pb[j][e]);
+          for (int e = 0; e < 4; ++e) n[j][e] = fma2(mul2(n[j][e], rstd), pa[j][e], pb[j][e]);
       } else {
 #pragma unroll
         for (int j = 0; j < CH; ++j)
@@ -249,33 +407,22 @@ static __global__ void __launch_bounds__(kForwardThreads<TPR>, kForwardBlocks<TP
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
         const int c = (j * TPR + t) * 8;
-        if (gen.threshold) gen.apply8(r * A.groups + c / 8, n[j]);
+        if (gen.threshold) gen.keep8(r * A.groups + c / 8, n[j]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[j][e] = add2(s[j][e], n[j][e]);
-        if (there && c < cols) store_group8<T, VEC>(static_cast<T*>(A.s) + r * A.lds + c, cols - c, s[j]);
+        store_columns<T, TPR, VEC>(ps, c, cols, s[j]);
       }
+      ps += step * A.lds;
     }
     if (A.gamma) {
-      float v[1], mean = 0.0f;
-      if (A.layer) {
-        v[0] = total(s);
-        row_sums<TPR>(v, red[group], turn, 1 + group);
-        mean = v[0] * A.inv_cols;
-      }
-      v[0] = centre<TPR>(s, mean, t, cols);
-      row_sums<TPR>(v, red[group], turn, 1 + group);
-      const float rstd = halves(rsqrt_rounded(splat(fmaf(v[0], A.inv_cols, A.eps)))).x;
-      if (t == 0 && there) {
-        if (A.layer) A.mean[r] = mean;
-        A.rstd[r] = rstd;
-      }
+      const f2 rstd = normal(s, A.mean, A.rstd, r);
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
-        const int c = (j * TPR + t) * 8;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[j][e] = fma2(mul2(s[j][e], splat(rstd)), gamma[j][e], beta[j][e]);
-        if (there && c < cols) store_group8<T, VEC>(static_cast<T*>(A.y) + r * A.ldy + c, cols - c, s[j]);
+        for (int e = 0; e < 4; ++e) s[j][e] = fma2(mul2(s[j][e], rstd), gamma[j][e], beta[j][e]);
+        store_columns<T, TPR, VEC>(py, (j * TPR + t) * 8, cols, s[j]);
       }
+      py += step * A.ldy;
     }
     if (++stage == kStages) stage = 0;
   }
@@ -283,30 +430,32 @@ static __global__ void __launch_bounds__(kForwardThreads<TPR>, kForwardBlocks<TP
 }
 
 constexpr int kBackwardThreads = 512;  // of 128 registers: all that an SM has room for, so that it leaves one part
-template <typename T>
-constexpr int kBackwardStages = sizeof(T) == 2 ? 4 : 3;
+template <typename T, bool VEC>
+constexpr int kBackwardStages = sizeof(T) == 2 ? 3 : VEC ? 3 : 2;
 
 template <typename T, int TPR, bool VEC, bool POST>
 static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(const ResidualBackward A) {
-  constexpr int kGroups = kBackwardThreads / TPR, kStages = kBackwardStages<T>;
+  constexpr int kGroups = kBackwardThreads / TPR, kStages = kBackwardStages<T, VEC>;
   constexpr int kKinds = POST ? 4 : 3;  // sums of dy shat, dy, d bhat, d (the last for the norm behind the block)
   extern __shared__ __align__(16) char dynamic[];
-  __shared__ float red[kGroups][2][2 * (TPR < 32 ? 1 : TPR / 32)];
+  __shared__ __align__(16) float red[kGroups][2][kRedWords<TPR, 2>];
   const int t = threadIdx.x % TPR, group = threadIdx.x / TPR, cols = A.cols, c = t * 8;
-  const RowRing<T, TPR, 1, VEC, 4, kStages, kBackwardThreads> ring(dynamic);
-  const T *dy = static_cast<const T*>(A.dy), *ds = static_cast<const T*>(A.ds), *s = static_cast<const T*>(A.s), *b = static_cast<const T*>(A.block);
-  const int64_t step = (int64_t)gridDim.x * kGroups, first = (int64_t)blockIdx.x * kGroups;
-  const bool pre = A.gamma != nullptr, needs_block = POST || A.gate;
+  const int64_t step = (int64_t)gridDim.x * kGroups, first = (int64_t)blockIdx.x * kGroups + group;
+  using Stream = RowStream<T, TPR, 1, VEC, 4, kStages, kBackwardThreads>;
+  Stream dy(dynamic, 0, A.dy, A.lddy, first, step, t, cols), s(dynamic, 1, A.s, A.lds, first, step, t, cols),
+      ds(dynamic, 2, A.ds, A.ldds, first, step, t, cols), b(dynamic, 3, A.block, A.ldblock, first, step, t, cols);
+  const bool pre = A.gamma != nullptr, path = A.ds != nullptr, block = POST || A.gate;
   in_turn();
   auto ahead = [&](int stage, int64_t r) {
-    const bool there = r < A.rows;
-    if (pre) ring.ahead(stage, 0, dy, A.lddy, r, there, t, cols), ring.ahead(stage, 1, s, A.lds, r, there, t, cols);
-    if (ds) ring.ahead(stage, 2, ds, A.ldds, r, there, t, cols);
-    if (needs_block) ring.ahead(stage, 3, b, A.ldblock, r, there, t, cols);
+    if (r < A.rows) {
+      if (pre) dy.ahead(stage, t, cols), s.ahead(stage, t, cols);
+      if (path) ds.ahead(stage, t, cols);
+      if (block) b.ahead(stage, t, cols);
+    }
     copies_commit();
   };
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) ahead(i, first + group + i * step);
+  for (int i = 0; i < kStages - 1; ++i) ahead(i, first + i * step);
   const Generator gen(A.drop);
   f2 gamma[4], pa[4], sum[kKinds][4];
   held8(A.gamma, c, cols, 0.0f, gamma);
@@ -317,6 +466,7 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
 #pragma unroll
     for (int e = 0; e < 4; ++e) pa[e] = mul2(pa[e], g[e]);
   }
+  const f2 scale = splat(A.scale * (gen.threshold ? gen.factor : 1.0f));
 #pragma unroll
   for (int k = 0; k < kKinds; ++k)
 #pragma unroll
@@ -333,26 +483,25 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
       block_rstd = __ldg(A.block_rstd + r);
     }
   };
-  statistics(first + group);
+  statistics(first);
   int turn = 0, stage = 0;
-  for (int64_t base = first; base < A.rows; base += step) {
-    const int64_t r = base + group;
-    const bool there = r < A.rows;
+  T *pdx = static_cast<T*>(A.dx) + first * A.lddx, *pdb = static_cast<T*>(A.dblock) + first * A.lddblock;
+  for (int64_t r = first; r < A.rows; r += step) {
     const float mu = mean, rs = rstd, bmu = block_mean, brs = block_rstd;
     copies_wait<kStages - 2>();
     ahead(stage == 0 ? kStages - 1 : stage - 1, r + (kStages - 1) * step);
     statistics(r + step);
     f2 d[4];  // t, then d, then what is left of it before the block
-    if (ds) {
-      ring.take(stage, 2, ds, A.ldds, r, there, t, cols, 0, d);
+    if (path) {
+      ds.take(stage, 0, VEC ? 0 : off16<T>(A.ds, A.ldds, r), d);
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e) d[e] = 0;
     }
     if (pre) {
       f2 q[4], hat[4], s0 = 0, s1 = 0;
-      ring.take(stage, 0, dy, A.lddy, r, there, t, cols, 0, q);
-      ring.take(stage, 1, s, A.lds, r, there, t, cols, 0, hat);
+      dy.take(stage, 0, VEC ? 0 : off16<T>(A.dy, A.lddy, r), q);
+      s.take(stage, 0, VEC ? 0 : off16<T>(A.s, A.lds, r), hat);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {  // columns past the end have dy = gamma = 0 and add nothing
         hat[e] = mul2(add2(hat[e], splat(-mu)), splat(rs));
@@ -368,25 +517,23 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
 #pragma unroll
       for (int e = 0; e < 4; ++e) d[e] = add2(fma2(hat[e], m1, fma2(q[e], splat(rs), m0)), d[e]);
     }
-    const bool inside = there && c < cols;
-    if (inside) store_group8<T, VEC>(static_cast<T*>(A.dx) + r * A.lddx + c, cols - c, d);
+    store_columns<T, TPR, VEC>(pdx, c, cols, d);
+    pdx += step * A.lddx;
     if (A.dblock) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) d[e] = mul2(d[e], splat(A.scale));
-      if (gen.threshold) gen.apply8(r * A.groups + t, d);
-      if (needs_block) {
+      for (int e = 0; e < 4; ++e) d[e] = mul2(d[e], scale);
+      if (gen.threshold) gen.keep8(r * A.groups + t, d);
+      if (block) {
         f2 hat[4];
-        ring.take(stage, 3, b, A.ldblock, r, there, t, cols, 0, hat);
+        b.take(stage, 0, VEC ? 0 : off16<T>(A.block, A.ldblock, r), hat);
         if (POST) {
           f2 s0 = 0, s1 = 0;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
+          for (int e = 0; e < 4; ++e) {  // d is not 0 past the end, where pa is, and its sums there go nowhere
             hat[e] = mul2(add2(hat[e], splat(-bmu)), splat(brs));
-            // (t is not 0 past the end, and a row that is not there has no statistics of its own)
-            const f2 v = inside ? d[e] : 0;
-            sum[2][e] = fma2(v, hat[e], sum[2][e]);
-            sum[kKinds - 1][e] = add2(sum[kKinds - 1][e], v);
-            d[e] = mul2(v, pa[e]);
+            sum[2][e] = fma2(d[e], hat[e], sum[2][e]);
+            sum[kKinds - 1][e] = add2(sum[kKinds - 1][e], d[e]);
+            d[e] = mul2(d[e], pa[e]);
             s0 = add2(s0, d[e]);
             s1 = fma2(d[e], hat[e], s1);
           }
@@ -398,12 +545,13 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            sum[2][e] = fma2(inside ? d[e] : 0, hat[e], sum[2][e]);
+            sum[2][e] = fma2(d[e], hat[e], sum[2][e]);
             d[e] = mul2(d[e], pa[e]);
           }
         }
       }
-      if (inside) store_group8<T, VEC>(static_cast<T*>(A.dblock) + r * A.lddblock + c, cols - c, d);
+      store_columns<T, TPR, VEC>(pdb, c, cols, d);
+      pdb += step * A.lddblock;
     }
     if (++stage == kStages) stage = 0;
   }
@@ -434,7 +582,7 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
 }
 template <typename T, int TPR, bool VEC, bool POST>
 constexpr int kBackwardSmem = [] {
-  constexpr int ring = RowRing<T, TPR, 1, VEC, 4, kBackwardStages<T>, kBackwardThreads>::kBytes, join = kBackwardThreads / 2 * (POST ? 4 : 3) * 4 * 8;
+  constexpr int ring = RowStream<T, TPR, 1, VEC, 4, kBackwardStages<T, VEC>, kBackwardThreads>::kBytes, join = kBackwardThreads / 2 * (POST ? 4 : 3) * 4 * 8;
   return ring > join ? ring : join;
 }();
 
@@ -805,7 +953,7 @@ auto with_threads(int64_t cols, F&& f) {
 template <typename T, int TPR, int CH, bool VEC, bool POST>
 cudaError_t run_forward(const ResidualForward& a, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
-  constexpr int kThreads = kForwardThreads<TPR>, kBytes = RowRing<T, TPR, CH, VEC, 2, kForwardStages<T>, kThreads>::kBytes;
+  constexpr int kThreads = kForwardThreads<TPR>, kBytes = RowStream<T, TPR, CH, VEC, 2, kForwardStages<T>, kThreads>::kBytes;
   return launch_rows(k_rn_forward<T, TPR, CH, VEC, POST>, ready, at_most(ceil_div(a.rows, kThreads / TPR), kForwardBlocks<TPR, CH, POST>), kThreads,
                      kBytes, s, a);
 }
