@@ -27,7 +27,7 @@ BINDING = os.path.join(HERE, "_layers_binding.so")
 SOURCES = ["onebit_adam.cu", "onebit_noalloc.cu", "activation_checkpoint.cu", "layer_norm.cu", "tensor_product.cu",
            "linear_forward.cu", "linear_backward.cu", "gated_forward.cu", "gated_backward.cu", "dropout.cu", "residual_norm.cu",
            "residual_norm_f32.cu", "residual_norm_f16.cu", "residual_norm_bf16.cu"]
-HEADERS = ["onebit_kernels.cuh", "layers_common.cuh", "tensor_product.cuh", "linear_common.cuh", "few_rows.cuh", "gated_common.cuh", "dropout.cuh", "residual_norm.cuh",
+HEADERS = ["onebit_kernels.cuh", "layers_common.cuh", "tensor_product.cuh", "linear_common.cuh", "few_rows.cuh", "gated_common.cuh", "dropout.cuh", "unaligned.cuh", "residual_norm.cuh",
            os.path.join("..", "..", "include", "onebit_adam.h"),
            os.path.join("..", "..", "include", "onebit_layers.h")]
 

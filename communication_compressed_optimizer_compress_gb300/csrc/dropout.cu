@@ -1,35 +1,64 @@
 // dropout.cu -- dropout of a matrix from a counter-based generator.  See include/onebit_layers.h for the definition.
-#include "dropout.cuh"
+#include "unaligned.cuh"
 
 namespace onebit {
 namespace layers {
 namespace {
 
-// A thread has a group of eight columns at a time.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) k_dropout(const T* __restrict__ x, int64_t ldx, int64_t rows, int cols, const Dropout d, T* __restrict__ y,
-                                                 int64_t ldy) {
+// Dense rows on 32 bytes, of whole groups: a thread has 16 columns, two groups, at a time, whatever row they are in.  Bound by
+// DRAM and, with ten rounds of two products a group, by instruction issue.
+template <typename T>
+__global__ void __launch_bounds__(256) k_dropout_dense(const T* __restrict__ x, int64_t pairs, const Dropout d, T* __restrict__ y) {
   in_turn();
   const Generator gen(d);
-  const int64_t groups = (cols + 7) / 8, total = rows * groups;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / groups;
-    const int c = (int)(i - r * groups) * 8;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < pairs; i += (int64_t)gridDim.x * 256) {
+    f2 v[2][4];
+    load16(x + i * 16, &v[0][0]);
+    if (d.threshold) gen.apply8(2 * i, v[0]), gen.apply8(2 * i + 1, v[1]);
+    store16(y + i * 16, &v[0][0]);
+  }
+}
+
+// Rows of any layout: WIDTH lanes have WIDTH groups of a row at a time.
+template <typename T, int WIDTH, bool VEC>
+__global__ void __launch_bounds__(256) k_dropout_rows(const T* __restrict__ x, int64_t ldx, int64_t rows, int cols, const Dropout d, T* __restrict__ y,
+                                                      int64_t ldy) {
+  in_turn();
+  const Generator gen(d);
+  const int64_t groups = (cols + 7) / 8;
+  const int parts = (int)((groups + WIDTH - 1) / WIDTH), lane = threadIdx.x % WIDTH;
+  // part p of row r, and as far as all lanes together go at a step
+  const int64_t first = ((int64_t)blockIdx.x * 256 + threadIdx.x) / WIDTH, all = (int64_t)gridDim.x * (256 / WIDTH), dr = all / parts;
+  int64_t r = first / parts;
+  int p = (int)(first - r * parts);
+  const int dp = (int)(all - dr * parts);
+  while (r < rows) {
+    const int c = (p * WIDTH + lane) * 8;
     f2 v[4];
-    load_group<T, VEC>(x + r * ldx + c, cols - c, v);
-    if (d.threshold) gen.apply8(i, v);
-    store_group8<T, VEC>(y + r * ldy + c, cols - c, v);
+    load_columns<T, VEC>(x + r * ldx, c, cols, v);
+    if (d.threshold) gen.apply8(r * groups + c / 8, v);
+    store_columns<T, WIDTH, VEC>(y + r * ldy, c, cols, v);
+    r += dr, p += dp;
+    if (p >= parts) p -= parts, ++r;
   }
 }
 
 template <typename T>
-cudaError_t run(const void* x, int64_t ldx, int64_t rows, int64_t cols, const Dropout& d, void* y, int64_t ldy, cudaStream_t s) {
+cudaError_t run(const void* px, int64_t ldx, int64_t rows, int64_t cols, const Dropout& d, void* py, int64_t ldy, cudaStream_t s) {
+  const T* x = static_cast<const T*>(px);
+  T* y = static_cast<T*>(py);
+  const int64_t most = (int64_t)sm_count() * 8, total = rows * cols;
+  auto grid = [&](int64_t threads) { return (unsigned)(ceil_div(threads, 256) < most ? ceil_div(threads, 256) : most); };
+  if (cols % 8 == 0 && total % 16 == 0 && aligned(x, 32) && aligned(y, 32) && (rows == 1 || (ldx == cols && ldy == cols)))
+    return launch_after(k_dropout_dense<T>, grid(total / 16), 256, s, x, total / 16, d, y);
   auto on16 = [](const void* p, int64_t ld) { return aligned(p, 16) && (ld * (int64_t)sizeof(T)) % 16 == 0; };
-  const int64_t want = ceil_div(rows * ceil_div(cols, 8), 256), most = (int64_t)sm_count() * 8;
-  auto go = [&](auto* kernel) {
-    return launch_after(kernel, (unsigned)(want < most ? want : most), 256, s, static_cast<const T*>(x), ldx, rows, (int)cols, d, static_cast<T*>(y), ldy);
+  const bool vec = cols % 8 == 0 && on16(x, ldx) && on16(y, ldy);
+  const int64_t groups = ceil_div(cols, 8);
+  auto go = [&](auto* kernel, int64_t width) {
+    return launch_after(kernel, grid(rows * ceil_div(groups, width) * width), 256, s, x, ldx, rows, (int)cols, d, y, ldy);
   };
-  return cols % 8 == 0 && on16(x, ldx) && on16(y, ldy) ? go(k_dropout<T, true>) : go(k_dropout<T, false>);
+  if (groups <= 8) return vec ? go(k_dropout_rows<T, 8, true>, 8) : go(k_dropout_rows<T, 8, false>, 8);
+  return vec ? go(k_dropout_rows<T, 32, true>, 32) : go(k_dropout_rows<T, 32, false>, 32);
 }
 
 }  // namespace

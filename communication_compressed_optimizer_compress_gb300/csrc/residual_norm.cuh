@@ -5,7 +5,7 @@
 #include <atomic>
 #include <type_traits>
 
-#include "dropout.cuh"
+#include "unaligned.cuh"
 
 namespace onebit {
 namespace layers {
@@ -62,10 +62,6 @@ struct ResidualBackward {
 // Rows that lie on 16 bytes and are whole groups (VEC) are copied and stored as they lie.  Of others a thread copies the aligned
 // vectors that its columns touch, one more than they fill, and shifts; their outputs are put together from its own and its
 // neighbour's values into aligned vectors, single elements where a warp's columns or the row begin and end.
-
-__device__ __forceinline__ uint32_t lanes_of(int width) {  // the lanes of this lane's group of `width`
-  return width == 32 ? 0xffffffffu : ((1u << width) - 1) << (threadIdx.x & 31 & ~(width - 1));
-}
 
 // One input's rows on their way: IN inputs share the ring, this is the `in`-th.
 template <typename T, int TPR, int CH, bool VEC, int IN, int STAGES, int THREADS>
@@ -135,17 +131,7 @@ struct RowStream {
 #pragma unroll
     for (int v = 0; v < kVectors; ++v)
       asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[4 * v]), "=r"(w[4 * v + 1]), "=r"(w[4 * v + 2]), "=r"(w[4 * v + 3]) : "r"(at(stage, j, v)) : "memory");
-    if (!VEC) {
-      constexpr int n = 4 * kOwn;
-#pragma unroll
-      for (int i = 0; i < n + 2; ++i) w[i] = m & 8 ? w[i + 2] : w[i];
-#pragma unroll
-      for (int i = 0; i < n + 1; ++i) w[i] = m & 4 ? w[i + 1] : w[i];
-      if (sizeof(T) == 2) {
-#pragma unroll
-        for (int i = 0; i < n; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (m & 2) * 8);
-      }
-    }
+    if constexpr (!VEC) shift_words<T>(w, m);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (sizeof(T) == 2) f[i] = widen<T>(w[i]);
@@ -161,72 +147,6 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 template <int N>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// Eight columns from c on of a row of an output.  All lanes of a row's group come here together.
-template <typename T, int TPR, bool VEC>
-__device__ __forceinline__ void store_columns(T* row, int c, int cols, const f2 (&f)[4]) {
-  if (VEC) {
-    if (c < cols) store8(row + c, f);
-    return;
-  }
-  constexpr int kSize = (int)sizeof(T), n = kSize * 2, kWidth = TPR < 32 ? TPR : 32;  // n: words
-  uint32_t w[n + 4];  // the last four words of the lane before, then this lane's
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (kSize == 2) {
-      w[4 + i] = narrow<T>(f[i]);
-    } else {
-      const float2 h = halves(f[i]);
-      w[4 + 2 * i] = __float_as_uint(h.x), w[5 + 2 * i] = __float_as_uint(h.y);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = __shfl_up_sync(lanes_of(kWidth), w[n + i], 1, kWidth);
-  if (c >= cols) return;
-  const int lane = threadIdx.x & (kWidth - 1), m = (int)(reinterpret_cast<uintptr_t>(row) & 15), left = cols - c;
-  // vector v has this lane's elements before (16 v + 16 - m) / kSize; the last m / kSize go with the next lane's
-  bool whole[n / 4];
-  uint32_t x[n + 4];
-#pragma unroll
-  for (int i = 0; i < n + 4; ++i) x[i] = w[i];
-  const int sh = 16 - m;
-#pragma unroll
-  for (int i = 0; i < n; ++i) x[i] = sh & 16 ? x[i + 4] : x[i];
-  if (!(sh & 16)) {
-#pragma unroll
-    for (int i = 0; i < n + 2; ++i) x[i] = sh & 8 ? x[i + 2] : x[i];
-#pragma unroll
-    for (int i = 0; i < n + 1; ++i) x[i] = sh & 4 ? x[i + 1] : x[i];
-    if (kSize == 2) {
-#pragma unroll
-      for (int i = 0; i < n; ++i) x[i] = __funnelshift_r(x[i], x[i + 1], (sh & 2) * 8);
-    }
-  }
-  char* const to = reinterpret_cast<char*>(row + c) - m;
-#pragma unroll
-  for (int v = 0; v < n / 4; ++v) {
-    whole[v] = left * kSize >= 16 * v + 16 - m && (v > 0 || lane > 0 || m == 0);
-    if (whole[v]) *reinterpret_cast<uint4*>(to + 16 * v) = make_uint4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
-  }
-  const bool last = lane == kWidth - 1 || c + 8 >= cols;  // no lane behind takes this one's last elements
-  if ((last && m > 0) || !whole[0] || !whole[n / 4 - 1]) {
-    auto put = [&](int at, uint32_t word, int e) {  // element e of a word's two or one
-      if constexpr (kSize == 2) reinterpret_cast<uint16_t*>(row)[at] = (uint16_t)(e ? word >> 16 : word);
-      else reinterpret_cast<uint32_t*>(row)[at] = word;
-    };
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int v = (e * kSize + m) / 16;
-      const bool vector = v < n / 4 ? (v == 0 ? whole[0] : whole[n / 4 - 1]) : !last;
-      if (e < left && !vector) put(c + e, w[4 + e * kSize / 4], kSize == 2 ? e & 1 : 0);
-    }
-    if (!whole[0] && lane > 0) {  // the row ends inside the vector that the lane before counts on
-#pragma unroll
-      for (int e = 8 - 16 / kSize < 0 ? 0 : 8 - 16 / kSize; e < 8; ++e)
-        if ((8 - e) * kSize <= m) put(c + e - 8, w[4 + e * kSize / 4 - n], kSize == 2 ? e & 1 : 0);
-    }
-  }
 }
 
 // a parameter's eight columns, `none` where there is no parameter, 0 past the end
@@ -248,18 +168,23 @@ constexpr int kRedWords = TPR > 32 ? N * TPR / 32 : 4;
 template <int TPR, int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[kRedWords<TPR, N>], int& turn, int bar) {
   constexpr int kWidth = TPR < 32 ? TPR : 32;
+  if constexpr (N == 2 && TPR > 32) {  // each half of the warp goes on with one of the two: five exchanges for ten
+    const bool upper = threadIdx.x & 16;
+    float u = (upper ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, upper ? v[0] : v[1], 16);
 #pragma unroll
-  for (int i = 0; i < N; ++i)
+    for (int o = 8; o; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+    v[0] = u;
+  } else {
 #pragma unroll
-    for (int o = kWidth / 2; o; o >>= 1) v[i] += __shfl_xor_sync(lanes_of(kWidth), v[i], o);
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int o = kWidth / 2; o; o >>= 1) v[i] += __shfl_xor_sync(lanes_of(kWidth), v[i], o);
+  }
   if constexpr (TPR > 32) {
     constexpr int kWarps = TPR / 32;
     float* r = red[turn];
     turn ^= 1;
-    if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) r[i * kWarps + (threadIdx.x % TPR >> 5)] = v[i];
-    }
+    if ((threadIdx.x & (32 / N - 1)) == 0) r[(threadIdx.x & 31) / (32 / N) * kWarps + (threadIdx.x % TPR >> 5)] = v[0];
     asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(TPR) : "memory");
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -433,10 +358,13 @@ constexpr int kBackwardThreads = 512;  // of 128 registers: all that an SM has r
 template <typename T, bool VEC>
 constexpr int kBackwardStages = sizeof(T) == 2 ? 3 : VEC ? 3 : 2;
 
-template <typename T, int TPR, bool VEC, bool POST>
+// What the block's side has: nothing but dropout and a scale, a gate, or a norm (and a gate).
+enum BlockSide { kBlockPlain = 0, kBlockGate = 1, kBlockNorm = 2 };
+template <typename T, int TPR, bool VEC, int SIDE>
 static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(const ResidualBackward A) {
   constexpr int kGroups = kBackwardThreads / TPR, kStages = kBackwardStages<T, VEC>;
-  constexpr int kKinds = POST ? 4 : 3;  // sums of dy shat, dy, d bhat, d (the last for the norm behind the block)
+  constexpr bool POST = SIDE == kBlockNorm, block = SIDE != kBlockPlain;
+  constexpr int kKinds = 2 + SIDE;  // sums of dy shat, dy, d bhat, d
   extern __shared__ __align__(16) char dynamic[];
   __shared__ __align__(16) float red[kGroups][2][kRedWords<TPR, 2>];
   const int t = threadIdx.x % TPR, group = threadIdx.x / TPR, cols = A.cols, c = t * 8;
@@ -444,7 +372,7 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
   using Stream = RowStream<T, TPR, 1, VEC, 4, kStages, kBackwardThreads>;
   Stream dy(dynamic, 0, A.dy, A.lddy, first, step, t, cols), s(dynamic, 1, A.s, A.lds, first, step, t, cols),
       ds(dynamic, 2, A.ds, A.ldds, first, step, t, cols), b(dynamic, 3, A.block, A.ldblock, first, step, t, cols);
-  const bool pre = A.gamma != nullptr, path = A.ds != nullptr, block = POST || A.gate;
+  const bool pre = A.gamma != nullptr, path = A.ds != nullptr;
   in_turn();
   auto ahead = [&](int stage, int64_t r) {
     if (r < A.rows) {
@@ -459,7 +387,7 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
   const Generator gen(A.drop);
   f2 gamma[4], pa[4], sum[kKinds][4];
   held8(A.gamma, c, cols, 0.0f, gamma);
-  held8(A.gate, c, cols, 1.0f, pa);
+  if (block) held8(A.gate, c, cols, 1.0f, pa);
   if (POST) {
     f2 g[4];
     held8(A.block_gamma, c, cols, 1.0f, g);
@@ -531,7 +459,7 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
 #pragma unroll
           for (int e = 0; e < 4; ++e) {  // d is not 0 past the end, where pa is, and its sums there go nowhere
             hat[e] = mul2(add2(hat[e], splat(-bmu)), splat(brs));
-            sum[2][e] = fma2(d[e], hat[e], sum[2][e]);
+            sum[kKinds - 2][e] = fma2(d[e], hat[e], sum[kKinds - 2][e]);
             sum[kKinds - 1][e] = add2(sum[kKinds - 1][e], d[e]);
             d[e] = mul2(d[e], pa[e]);
             s0 = add2(s0, d[e]);
@@ -545,7 +473,7 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            sum[2][e] = fma2(d[e], hat[e], sum[2][e]);
+            sum[kKinds - 1][e] = fma2(d[e], hat[e], sum[kKinds - 1][e]);
             d[e] = mul2(d[e], pa[e]);
           }
         }
@@ -580,9 +508,9 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
     for (int k = 0; k < kKinds; ++k) store_group8<float, false>(p + k * cols, cols - c, sum[k]);
   }
 }
-template <typename T, int TPR, bool VEC, bool POST>
+template <typename T, int TPR, bool VEC, int SIDE>
 constexpr int kBackwardSmem = [] {
-  constexpr int ring = RowStream<T, TPR, 1, VEC, 4, kBackwardStages<T, VEC>, kBackwardThreads>::kBytes, join = kBackwardThreads / 2 * (POST ? 4 : 3) * 4 * 8;
+  constexpr int ring = RowStream<T, TPR, 1, VEC, 4, kBackwardStages<T, VEC>, kBackwardThreads>::kBytes, join = kBackwardThreads / 2 * (2 + SIDE) * 4 * 8;
   return ring > join ? ring : join;
 }();
 
@@ -972,10 +900,10 @@ cudaError_t rn_forward(const ResidualForward& a, cudaStream_t s) {
   return with_threads(a.cols, [&](auto tpr) { return by(tpr, integral_constant<int, 1>{}); });
 }
 
-template <typename T, int TPR, bool VEC, bool POST>
+template <typename T, int TPR, bool VEC, int SIDE>
 cudaError_t run_backward(const ResidualBackward& a, unsigned parts, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
-  return launch_rows(k_rn_backward<T, TPR, VEC, POST>, ready, parts, kBackwardThreads, kBackwardSmem<T, TPR, VEC, POST>, s, a);
+  return launch_rows(k_rn_backward<T, TPR, VEC, SIDE>, ready, parts, kBackwardThreads, kBackwardSmem<T, TPR, VEC, SIDE>, s, a);
 }
 // Takes the workspace; with `run`, enqueues the work too.
 template <typename T>
@@ -1002,8 +930,12 @@ cudaError_t rn_backward(ResidualBackward a, const ParamGrads& g, int32_t grad_dt
                      on16(a.dblock, a.lddblock);
     e = with_threads(a.cols, [&](auto tpr) {
       constexpr int kTpr = decltype(tpr)::value;
-      if (vec) return a.block_gamma ? run_backward<T, kTpr, true, true>(a, (unsigned)parts, s) : run_backward<T, kTpr, true, false>(a, (unsigned)parts, s);
-      return a.block_gamma ? run_backward<T, kTpr, false, true>(a, (unsigned)parts, s) : run_backward<T, kTpr, false, false>(a, (unsigned)parts, s);
+      auto by = [&](auto v) {
+        constexpr bool kVec = decltype(v)::value;
+        if (a.block_gamma) return run_backward<T, kTpr, kVec, kBlockNorm>(a, (unsigned)parts, s);
+        return a.gate ? run_backward<T, kTpr, kVec, kBlockGate>(a, (unsigned)parts, s) : run_backward<T, kTpr, kVec, kBlockPlain>(a, (unsigned)parts, s);
+      };
+      return vec ? by(std::true_type{}) : by(std::false_type{});
     });
   }
   if (e != cudaSuccess || !params) return e;
