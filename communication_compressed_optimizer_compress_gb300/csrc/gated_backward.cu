@@ -12,25 +12,34 @@ struct KeptPair {
   Kept<T> gate, up;
 };
 
-// dz from the sums dh (partial ones of a cut contraction), and h = act(g) u.  Without dz: h alone.
+// dz from the sums dh (partial ones of a cut contraction), and h = act(g) u, a warp for 128 columns of a row, single elements side
+// by side.  Without dz: h alone.
 template <typename T>
 __global__ void __launch_bounds__(256) k_finish_dz(Partials c, int64_t rows, int n, KeptPair<T> kept, int act, T* __restrict__ dz, int64_t lddz,
                                                    T* __restrict__ h, int64_t ldh) {
   in_turn();
-  const int64_t per = (n + 3) / 4, total = rows * per;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+  const int lane = threadIdx.x & 31;
+  const int64_t per = (n + 127) / 128, units = rows * per, step = (int64_t)gridDim.x * 8;
+  for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < units; i += step) {
     const int64_t r = i / per;
-    const int c0 = (int)(i - r * per) * 4;
-    float d[4] = {};
-    if (dz) c.at4(r, c0, d);
+    const int c0 = (int)(i - r * per) * 128 + lane;
+    float d[4], g[4], u[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int col = c0 + q;
+      const int col = c0 + 32 * q;
+      d[q] = g[q] = u[q] = 0.0f;
+      if (col < n) {
+        g[q] = kept.gate.at(r, col), u[q] = kept.up.at(r, col);
+        if (dz) d[q] = c.at(r, col);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int col = c0 + 32 * q;
       if (col >= n) break;
-      const float u = kept.up.at(r, col);
-      const float2 p = gate_both(act, kept.gate.at(r, col));
-      if (h) h[r * ldh + col] = from_f<T>(p.x * u);
-      if (dz) dz[r * lddz + col] = from_f<T>(d[q] * u * p.y), dz[r * lddz + n + col] = from_f<T>(d[q] * p.x);
+      const float2 p = gate_both(act, g[q]);
+      if (h) h[r * ldh + col] = from_f<T>(p.x * u[q]);
+      if (dz) dz[r * lddz + col] = from_f<T>(d[q] * u[q] * p.y), dz[r * lddz + n + col] = from_f<T>(d[q] * p.x);
     }
   }
 }
@@ -49,18 +58,21 @@ cudaError_t backward(const onebit_gated_linear_grad_t& a, Space& ws, cudaStream_
   cudaError_t err = run ? copies.run(s) : cudaSuccess;
   if (err != cudaSuccess) return err;
   Partials part{};
-  bool done = false;  // dz and h
+  bool done = false;  // dz and h, in the epilogue
   if (a.dz) {
     const ProductShape shape{a.rows, a.inner, a.out};
     const ProductPlan plan = plan_product(shape, sm_count());
-    part = take_partials(ws, plan, a.rows, a.inner);
-    if (run && plan.splits == 1) {
+    // Single blocks that cannot store dz by TMA leave it to the kernel over the sums: their few warps write it element by element
+    // (333 x 1030 x 520: 19.8 us from values in the epilogue, 13.0 that way; pairs have more work each: 16384 x 4090 x 1024 432 and 531).
+    const bool whole = aligned(a.dz, 16) && a.lddz % 8 == 0 && a.inner % 8 == 0, fused = plan.splits == 1 && (whole || plan.ctas == 2);
+    if (!fused) part = take_sums(ws, plan, a.rows, a.inner);
+    if (run && fused) {
       auto go = [&](auto ctas, auto act, auto what) {
         GatedGradEpilogue<T, decltype(act)::value, decltype(what)::value> e{};
         e.gate = make_input<T>(kept.gate.x, a.ldz), e.up = make_input<T>(kept.up.x, a.ldz);
         e.gate_codes = a.gate_codes, e.up_codes = a.up_codes, e.gate_scales = a.gate_scales, e.up_scales = a.up_scales;
         e.blocks = blocks, e.act = a.activation, e.kept = a.z ? kKeptValue : kKeptCodes;
-        e.vec_codes = aligned(a.gate_codes, 16) && aligned(a.up_codes, 16) && n % 16 == 0;
+        e.code_bytes = aligned(a.gate_codes, 16) && aligned(a.up_codes, 16) && n % 16 == 0 ? 16 : aligned(a.gate_codes, 8) && aligned(a.up_codes, 8) && n % 8 == 0 ? 8 : 1;
         T* dz = static_cast<T*>(a.dz);
         cudaError_t r = make_output(&e.dgate, dz, a.rows, a.inner, a.lddz);
         if (r == cudaSuccess) r = make_output(&e.dup, dz + n, a.rows, a.inner, a.lddz);
@@ -91,7 +103,7 @@ cudaError_t backward(const onebit_gated_linear_grad_t& a, Space& ws, cudaStream_
     }
   }
   if (run && !done && (a.dz || h)) {
-    err = launch_after(k_finish_dz<T>, flat_grid(a.rows * ceil_div(a.inner, 4), 256), 256, s, part, a.rows, n, kept, a.activation, static_cast<T*>(a.dz),
+    err = launch_after(k_finish_dz<T>, flat_grid(a.rows * ceil_div(a.inner, 128) * 32, 256), 256, s, part, a.rows, n, kept, a.activation, static_cast<T*>(a.dz),
                        a.lddz, h, ldh);
     if (err != cudaSuccess) return err;
   }

@@ -344,11 +344,12 @@ PyObject* linear_backward(PyObject* const* a) {
                !want[2] ? none() : a[7] != Py_None ? Py_NewRef(a[7]) : wrap(std::move(db))});
 }
 
-// an instance of one of the named tuples
+// an instance of one of the named tuples: as tuple makes it of its items (through the class's own __new__, a Python function, it
+// takes the host as long as two allocations)
 PyObject* named(PyTypeObject* type, std::initializer_list<PyObject*> items) {
-  PyObject* args = pack(items);
+  PyObject* args = pack({pack(items)});
   if (!args) return nullptr;
-  PyObject* r = PyObject_CallObject(reinterpret_cast<PyObject*>(type), args);
+  PyObject* r = PyTuple_Type.tp_new(type, args, nullptr);
   Py_DECREF(args);
   return r;
 }

@@ -991,7 +991,7 @@ struct GatedGradEpilogue {
   Output<T> dgate, dup, h;  // h.p NULL: not wanted
   int act;
   int kept;                 // Kept16: values or codes
-  bool vec_codes;
+  int code_bytes;           // what every row of codes is a multiple of: 16, 8 or 1
 
   static constexpr int kCols = 16;  // at a time
   static constexpr int kWords = KEPT == kKeptCodes ? kCols / 4 : kCols / 2;  // of their codes or values
@@ -999,15 +999,12 @@ struct GatedGradEpilogue {
     uint32_t g[kWords], u[kWords];
   };
   __device__ __forceinline__ bool by_codes() const { return (KEPT == kAny ? kept : KEPT) == kKeptCodes; }
-  // kCols values of a row: at once where they lie on their own size, else in pieces of 16 bytes or one by one; 0 past the end
+  // sixteen values of a row: at once where they lie on 32 bytes, else in pieces of 16 or one by one; 0 past the end
   __device__ __forceinline__ static void values(const Input16<T>& in, int64_t row, int c, int cols, uint32_t (&v)[kWords]) {
     if constexpr (KEPT != kKeptCodes) {
       const T* p = in.p + row * in.ld + c;
-      if (kCols == 16 && in.wide && c + 16 <= cols) {
-        uint32_t t[8];
-        load32(p, t);
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) v[i] = t[i];
+      if (in.wide && c + 16 <= cols) {
+        load32(p, v);
       } else if (in.vec && cols % 8 == 0) {
 #pragma unroll
         for (int j = 0; j < kCols / 8; ++j) {
@@ -1022,18 +1019,19 @@ struct GatedGradEpilogue {
     }
   }
   __device__ __forceinline__ void codes(const int8_t* p, int c, int cols, uint32_t (&v)[kWords]) const {
-    if (vec_codes) {  // rows of whole sixteens
-      if constexpr (kCols == 16) {
-        const uint4 t = __ldg(reinterpret_cast<const uint4*>(p));
-        v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
-      } else {
-        const uint2 t = __ldg(reinterpret_cast<const uint2*>(p));
-        v[0] = t.x, v[1] = t.y;
+    if (code_bytes == 16) {
+      const uint4 t = __ldg(reinterpret_cast<const uint4*>(p));
+      v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
+    } else if (code_bytes == 8) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint2 t = c + 8 * j < cols ? __ldg(reinterpret_cast<const uint2*>(p) + j) : make_uint2(0, 0);
+        v[2 * j] = t.x, v[2 * j + 1] = t.y;
       }
     } else {
-      const auto w = read_single<kCols / 4>(p, cols - c);
+      const auto w = read_single<4>(p, cols - c);
 #pragma unroll
-      for (int i = 0; i < kCols / 4; ++i) v[i] = w.v[i];
+      for (int i = 0; i < 4; ++i) v[i] = w.v[i];
     }
   }
   __device__ __forceinline__ void fetch(Ahead& a, int64_t row, int64_t rows, int c, int cols) const {
