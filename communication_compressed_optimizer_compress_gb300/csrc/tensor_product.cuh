@@ -515,7 +515,6 @@ template <typename T, int ACT, int CK, int RES>
 struct ForwardEpilogue {
   // y = act(d + bias) + residual, and the 8-bit checkpoint of d + bias
   static constexpr bool kFold = false;
-  static constexpr bool kPrefetch = false;
   static constexpr bool kGated = false;
   static constexpr int kStaging = kStagingBytes;
   const float* bias;
@@ -618,7 +617,6 @@ template <typename T, int ACT, int KEPT>
 struct InputGradEpilogue {
   // dx = d * act'(v) [+ add], and h = act(v) for the product of dw
   static constexpr bool kFold = false;
-  static constexpr bool kPrefetch = false;
   static constexpr bool kGated = false;
   static constexpr int kStaging = kStagingBytes;
   Input16<T> x;          // the value before the activation,
@@ -975,15 +973,14 @@ __device__ __noinline__ Words<WORDS> read_single(const E* p, int left) {
   return w;
 }
 // dz = [d u act'(g) | d act(g)], and h = act(g) u for the product of dw.  A lane has its row's 64 columns, sixteen at a time: it
-// reads g and u ahead (out of the L2, where they were sent for under the tile before), and what becomes of them goes to the staging
-// buffer at once, a box of 32 columns for each of the three results.  With 32 columns at a time the registers spill, and a
+// reads g and u ahead, and what becomes of them goes to the staging buffer at once, a box of 32 columns for each of the three
+// results.  (Sent for into the L2 a tile before, they are read from DRAM twice: 159 us from values, 150 without.)  With 32 columns at a time the registers spill, and a
 // kernel that spills takes 150 to 165 us for 16384 x 4096 x 1024 from checkpoints, one that does not 130 (silu and gelu, either way round).
 template <typename T, int ACT, int KEPT>
 struct GatedGradEpilogue {
   static constexpr bool kFold = false;
   static constexpr bool kGated = false;
   static constexpr int kStaging = 3 * 2048;
-  static constexpr bool kPrefetch = true;
   Input16<T> gate, up;                     // the kept values,
   const int8_t *gate_codes, *up_codes;     // or their checkpoints
   const float *gate_scales, *up_scales;
@@ -1043,14 +1040,6 @@ struct GatedGradEpilogue {
       values(gate, row, c, cols, a.g);
       values(up, row, c, cols, a.u);
     }
-  }
-  // 64 columns of a row of both halves: a line of values, half a line of codes
-  __device__ __forceinline__ void prefetch(int64_t row, int64_t rows, int col0, int cols) const {
-    if (row >= rows || col0 >= cols) return;
-    const void *g, *u;
-    if (by_codes()) g = gate_codes + row * cols + col0, u = up_codes + row * cols + col0;
-    else g = gate.p + row * gate.ld + col0, u = up.p + row * up.ld + col0;
-    asm volatile("prefetch.global.L2 [%0];\n\tprefetch.global.L2 [%1];" ::"l"(g), "l"(u));
   }
   __device__ __forceinline__ void prepare(Ahead& a, int64_t row0, int64_t rows, int col0, int cols, char*) const {
     fetch(a, row0 + (threadIdx.x & 31), rows, col0, cols);
@@ -1284,13 +1273,6 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
           if (inside && col0 + 32 * q < P.n) E.run(c[q], row0, P.m, col0 + 32 * q, P.n, t.split, staging);
       } else {
         typename Epilogue::Ahead ahead;
-        if constexpr (Epilogue::kPrefetch) {  // the next tile's, from DRAM to the L2 under this one
-          const uint32_t v = u + unit_step;
-          if (v < units) {
-            const Tile n = tile_of<CTAS>(P, v);
-            E.prefetch(n.m0 + rank * kRowsPerBlock + quad * 32 + lane, P.m, n.n0 + group * 64, P.n);
-          }
-        }
         if (inside) E.prepare(ahead, row0, P.m, col0, P.n, staging);
         if (!(ok = ready())) break;
         const uint32_t at = lanes + acc * kTileN;
