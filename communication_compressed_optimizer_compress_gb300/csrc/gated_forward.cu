@@ -55,7 +55,10 @@ __global__ void __launch_bounds__(256) k_finish_gated(Partials c, int64_t rows, 
 }
 
 // Up to 32 rows, as generation meets them: the few-rows product (few_rows.cuh) with two weights to a column, the gate's and
-// the up projection's, whose sums meet in shared memory.
+// the up projection's, whose sums meet in shared memory.  Bound by the weights' bytes and a launch's latency: a warp asks for kAhead
+// steps of both weights, and of x where it is up to eight rows, before it multiplies any; 128 registers a thread hold them (with 64
+// they spill: one row of 4096 -> 11008 35 us, 31 with 128, where the weights alone are 27).  One row of 1024 -> 4096, weights in HBM:
+// 4.5 us a call, 5.2 without sending for them before the turn.
 struct FewGatedArgs {
   const void* x;
   int64_t ldx;
@@ -66,44 +69,47 @@ struct FewGatedArgs {
   int64_t ldh;
   int rows, in, inner, act;
 };
-template <typename T, int M>
-__global__ void __launch_bounds__(kFewThreads) k_few_rows_gated(const FewGatedArgs A) {
-  in_turn();
-  constexpr int kSplits = 8, kAhead = 4;
-  __shared__ float part[kSplits][2][M * 16][9];
+// HALVES of eight rows: 1, 2 or 4
+template <typename T, int HALVES>
+__global__ void __launch_bounds__(kFewThreads, 2) k_few_rows_gated(const FewGatedArgs A) {
+  constexpr int kSplits = 8, kAhead = 4, M = HALVES == 4 ? 2 : 1;
+  __shared__ float part[kSplits][2][HALVES * 8][9];
   const int lane = threadIdx.x & 31, split = threadIdx.x >> 5;
   const int n = lane >> 2, q = lane & 3;
   const int col = blockIdx.x * 8 + n;
   const int steps = (A.in + 31) / 32, per = (steps + kSplits - 1) / kSplits;
-  const int s0 = split * per, s1 = s0 + per < steps ? s0 + per : steps;
-  const T* w = static_cast<const T*>(A.w) + (int64_t)(col < A.inner ? col : 0) * A.ldw;
+  const int s1 = split * per + per < steps ? split * per + per : steps;
+  const T* w = static_cast<const T*>(A.w) + (int64_t)(col < A.inner ? col : 0) * A.ldw + q * 8;
+  const T* x = static_cast<const T*>(A.x) + (int64_t)n * A.ldx + q * 8;
   const int64_t up = (int64_t)A.inner * A.ldw;
-  const T* x = static_cast<const T*>(A.x);
   float d[2][M][4] = {};
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  auto piece = [&](int s, int64_t half) {
-    const int k = s * 32 + q * 8;
-    return col < A.inner && s < s1 && k < A.in ? __ldg(reinterpret_cast<const uint4*>(w + half + k)) : zero;
-  };
-  uint4 ahead[kAhead][2];
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) ahead[i][0] = piece(s0 + i, 0), ahead[i][1] = piece(s0 + i, up);
-  for (int s = s0; s < s1; s += kAhead) {
+  // the first steps' weights (two lines of a row) on their way to the L2 beside the kernel before, whatever it writes
+  const int k0 = split * per * 32 + (q & 1) * 64;
+  if (col < A.inner && k0 < A.in) asm volatile("prefetch.global.L2 [%0];" ::"l"(w - q * 8 + (q & 2 ? up : 0) + k0));
+  in_turn();
+  for (int s = split * per; s < s1; s += kAhead) {
+    uint4 b[kAhead][2], a[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const uint4 b[2] = {ahead[i][0], ahead[i][1]};
-      ahead[i][0] = piece(s + kAhead + i, 0), ahead[i][1] = piece(s + kAhead + i, up);
-      const int k = (s + i) * 32 + q * 8;
+      const int k = (s + i) * 32;
+      const bool in = s + i < s1 && k + q * 8 < A.in;
+      b[i][0] = in && col < A.inner ? __ldg(reinterpret_cast<const uint4*>(w + k)) : zero;
+      b[i][1] = in && col < A.inner ? __ldg(reinterpret_cast<const uint4*>(w + up + k)) : zero;
+      if (HALVES == 1) a[i] = in && n < A.rows ? __ldg(reinterpret_cast<const uint4*>(x + k)) : zero;
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int k = (s + i) * 32;
+      const bool in = s + i < s1 && k + q * 8 < A.in;
 #pragma unroll
       for (int m = 0; m < M; ++m) {
-        const int r0 = m * 16 + n, r1 = r0 + 8;
-        const bool in = s + i < s1 && k < A.in;
-        const uint4 a = in && r0 < A.rows ? __ldg(reinterpret_cast<const uint4*>(x + r0 * A.ldx + k)) : zero;
-        const uint4 c = in && r1 < A.rows ? __ldg(reinterpret_cast<const uint4*>(x + r1 * A.ldx + k)) : zero;
+        auto row = [&](int r) { return in && r + n < A.rows ? __ldg(reinterpret_cast<const uint4*>(x + r * A.ldx + k)) : zero; };
+        const uint4 lo = HALVES == 1 ? a[i] : row(16 * m), hi = HALVES == 1 ? zero : row(16 * m + 8);
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          mma_16x8x16<T>(d[p][m], a.x, c.x, a.y, c.y, b[p].x, b[p].y);
-          mma_16x8x16<T>(d[p][m], a.z, c.z, a.w, c.w, b[p].z, b[p].w);
+          mma_16x8x16<T>(d[p][m], lo.x, hi.x, lo.y, hi.y, b[i][p].x, b[i][p].y);
+          mma_16x8x16<T>(d[p][m], lo.z, hi.z, lo.w, hi.w, b[i][p].z, b[i][p].w);
         }
       }
     }
@@ -113,17 +119,15 @@ __global__ void __launch_bounds__(kFewThreads) k_few_rows_gated(const FewGatedAr
 #pragma unroll
     for (int m = 0; m < M; ++m)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) part[split][p][m * 16 + n + 8 * (i / 2)][2 * q + (i & 1)] = d[p][m][i];
+      for (int i = 0; i < (HALVES == 1 ? 2 : 4); ++i) part[split][p][m * 16 + n + 8 * (i / 2)][2 * q + (i & 1)] = d[p][m][i];
   __syncthreads();
-  for (int i = threadIdx.x; i < M * 16 * 8; i += kFewThreads) {
-    const int r = i / 8, j = i % 8, c = blockIdx.x * 8 + j;
-    if (r >= A.rows || c >= A.inner) continue;
-    float g = part[0][0][r][j], u = part[0][1][r][j];
+  const int r = threadIdx.x / 8, j = threadIdx.x % 8, c = blockIdx.x * 8 + j;
+  if (r >= A.rows || c >= A.inner) return;  // (at most 32 rows: a thread has one value)
+  float g = part[0][0][r][j], u = part[0][1][r][j];
 #pragma unroll
-    for (int s = 1; s < kSplits; ++s) g += part[s][0][r][j], u += part[s][1][r][j];
-    if (A.bias) g += __ldg(A.bias + c), u += __ldg(A.bias + A.inner + c);
-    static_cast<T*>(A.h)[r * A.ldh + c] = from_f<T>(gate_both(A.act, g).x * u);
-  }
+  for (int s = 1; s < kSplits; ++s) g += part[s][0][r][j], u += part[s][1][r][j];
+  if (A.bias) g += __ldg(A.bias + c), u += __ldg(A.bias + A.inner + c);
+  static_cast<T*>(A.h)[r * A.ldh + c] = from_f<T>(gate_both(A.act, g).x * u);
 }
 // Few rows, on 16 bytes, and nothing kept.
 inline bool few_rows(const onebit_gated_linear_t& a) {
@@ -133,7 +137,8 @@ template <typename T>
 cudaError_t run_few_rows(const onebit_gated_linear_t& a, cudaStream_t s) {
   const FewGatedArgs f{a.x, a.ldx, a.w, a.ldw, a.bias, a.h, a.ldh, (int)a.rows, (int)a.in, (int)a.inner, a.activation};
   const unsigned grid = (unsigned)ceil_div(a.inner, 8);
-  return a.rows <= 16 ? launch_after(k_few_rows_gated<T, 1>, grid, kFewThreads, s, f) : launch_after(k_few_rows_gated<T, 2>, grid, kFewThreads, s, f);
+  if (a.rows <= 8) return launch_after(k_few_rows_gated<T, 1>, grid, kFewThreads, s, f);
+  return a.rows <= 16 ? launch_after(k_few_rows_gated<T, 2>, grid, kFewThreads, s, f) : launch_after(k_few_rows_gated<T, 4>, grid, kFewThreads, s, f);
 }
 
 // Takes the workspace; with `run`, enqueues the work too.

@@ -193,6 +193,16 @@ void with_workspace(Run run, Size size, const Args& a, const at::Tensor& like) {
   require(st == ONEBIT_OK);
 }
 
+// The same for calls that need one most of the time: the size first.
+template <typename Run, typename Size, typename Args>
+void with_sized_workspace(Run run, Size size, const Args& a, const at::Tensor& like) {
+  size_t need = 0;
+  require(size(&a, &need) == ONEBIT_OK);
+  at::Tensor ws;
+  if (need > 0) ws = empty({(int64_t)need}, at::kByte, like);
+  require(run(&a, need > 0 ? ws.data_ptr() : nullptr, need, stream(like)) == ONEBIT_OK);
+}
+
 // compress(x)
 PyObject* compress(PyObject* const* a) {
   const at::Tensor& x = tensor(a[0]);
@@ -380,19 +390,19 @@ PyObject* gated_linear(PyObject* const* a) {
   at::Tensor h = empty({p.rows, p.inner}, x.scalar_type(), x);
   p.h = h.data_ptr(), p.ldh = p.inner;
   if (a[4] == Py_None) {
-    with_workspace(g_entry.gated_forward, g_entry.gated_forward_workspace, p, x);
+    with_sized_workspace(g_entry.gated_forward, g_entry.gated_forward_workspace, p, x);
     return wrap(std::move(h));
   }
   if (is(a[4], "values")) {
     at::Tensor z = empty({p.rows, mw.rows}, x.scalar_type(), x);
     p.z = z.data_ptr(), p.ldz = mw.rows;
-    with_workspace(g_entry.gated_forward, g_entry.gated_forward_workspace, p, x);
+    with_sized_workspace(g_entry.gated_forward, g_entry.gated_forward_workspace, p, x);
     return pack({wrap(std::move(h)), wrap(std::move(z))});
   }
   require(is(a[4], "checkpoint"));
   const NewCheckpoint gate(p.rows, p.inner, x), up(p.rows, p.inner, x);
   p.gate_codes = gate.c(), p.gate_scales = gate.s(), p.up_codes = up.c(), p.up_scales = up.s();
-  with_workspace(g_entry.gated_forward, g_entry.gated_forward_workspace, p, x);
+  with_sized_workspace(g_entry.gated_forward, g_entry.gated_forward_workspace, p, x);
   return pack({wrap(std::move(h)), named(g_gated, {gate.object(x.scalar_type()), up.object(x.scalar_type())})});
 }
 
@@ -440,7 +450,7 @@ PyObject* gated_linear_backward(PyObject* const* a) {
     if (a[6] != Py_None) p.db = given(a[6], p.out);
     else db = empty({p.out}, grad, dy), p.db = db.data_ptr();
   }
-  with_workspace(g_entry.gated_backward, g_entry.gated_backward_workspace, p, dy);
+  with_sized_workspace(g_entry.gated_backward, g_entry.gated_backward_workspace, p, dy);
   return pack({wrap_or_none(std::move(dz)), want[1] && a[5] != Py_None ? Py_NewRef(a[5]) : wrap_or_none(std::move(dw)),
                want[2] && a[6] != Py_None ? Py_NewRef(a[6]) : wrap_or_none(std::move(db))});
 }
@@ -478,6 +488,23 @@ PyObject* dropout(PyObject* const* a) {
   return wrap(std::move(y));
 }
 
+// `count` vectors of n values out of one allocation (each one would take the host as long as a third of a launch), on 256 bytes
+struct Vectors {
+  at::Tensor all;
+  int64_t n, each;
+  int used = 0;
+  Vectors(int count, int64_t n_, at::ScalarType type, const at::Tensor& like) : n(n_) {
+    const int64_t per = 256 / (int64_t)c10::elementSize(type);
+    each = (n + per - 1) / per * per;
+    if (count > 0) all = empty({count * each}, type, like);
+  }
+  at::Tensor next() {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+    t.unsafeGetTensorImpl()->set_storage_offset(used++ * each);
+    t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+    return t;
+  }
+};
 const float* vector_or_null(PyObject* o, int64_t n, const at::Tensor& like) { return o == Py_None ? nullptr : vector(o, n, like); }
 float* floats(const at::Tensor& t) { return t.defined() ? static_cast<float*>(t.data_ptr()) : nullptr; }
 void* bytes(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
@@ -503,15 +530,12 @@ PyObject* residual_norm(PyObject* const* a) {
   at::Tensor s, y, mean, rstd, block_mean, block_rstd;
   const bool layer = p.norm == ONEBIT_NORM_LAYER;
   if (p.block) s = empty({m.rows, m.cols}, x.scalar_type(), x);
-  if (p.gamma) {
-    y = empty({m.rows, m.cols}, x.scalar_type(), x);
-    if (layer) mean = empty({m.rows}, at::kFloat, x);
-    rstd = empty({m.rows}, at::kFloat, x);
-  }
-  if (p.block_gamma) {
-    if (layer) block_mean = empty({m.rows}, at::kFloat, x);
-    block_rstd = empty({m.rows}, at::kFloat, x);
-  }
+  if (p.gamma) y = empty({m.rows, m.cols}, x.scalar_type(), x);
+  Vectors stats((1 + layer) * ((p.gamma != nullptr) + (p.block_gamma != nullptr)), m.rows, at::kFloat, x);
+  if (p.gamma && layer) mean = stats.next();
+  if (p.gamma) rstd = stats.next();
+  if (p.block_gamma && layer) block_mean = stats.next();
+  if (p.block_gamma) block_rstd = stats.next();
   p.s = bytes(s), p.y = bytes(y), p.lds = p.ldy = m.cols;
   p.mean = floats(mean), p.rstd = floats(rstd), p.block_mean = floats(block_mean), p.block_rstd = floats(block_rstd);
   require(g_entry.rn_forward(&p, stream(x)) == ONEBIT_OK);
@@ -554,11 +578,12 @@ PyObject* residual_norm_backward(PyObject* const* a) {
   const bool layer = p.norm == ONEBIT_NORM_LAYER;
   at::Tensor dx = empty({rows, cols}, first.scalar_type(), first), dblock, dgamma, dbeta, dblock_gamma, dblock_beta, dgate;
   if (has_block) dblock = empty({rows, cols}, first.scalar_type(), first);
-  if (p.gamma) dgamma = empty({cols}, grad, first);
-  if (p.gamma && layer) dbeta = empty({cols}, grad, first);
-  if (p.block_gamma) dblock_gamma = empty({cols}, grad, first);
-  if (p.block_gamma && layer) dblock_beta = empty({cols}, grad, first);
-  if (p.gate) dgate = empty({cols}, grad, first);
+  Vectors grads((1 + layer) * ((p.gamma != nullptr) + (p.block_gamma != nullptr)) + (p.gate != nullptr), cols, grad, first);
+  if (p.gamma) dgamma = grads.next();
+  if (p.gamma && layer) dbeta = grads.next();
+  if (p.block_gamma) dblock_gamma = grads.next();
+  if (p.block_gamma && layer) dblock_beta = grads.next();
+  if (p.gate) dgate = grads.next();
   p.dx = dx.data_ptr(), p.dblock = bytes(dblock), p.lddx = p.lddblock = cols;
   p.dgamma = bytes(dgamma), p.dbeta = bytes(dbeta), p.dblock_gamma = bytes(dblock_gamma), p.dblock_beta = bytes(dblock_beta), p.dgate = bytes(dgate);
   size_t need = 0;
