@@ -2,6 +2,7 @@
 // gradients.  See include/onebit_layers.h for the formulas.
 #pragma once
 
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 
@@ -203,6 +204,39 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[kRedWords<T
   }
 }
 
+// Rows of more columns than a block holds are a cluster's: each block has a part of the columns.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_blocks() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() { asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+constexpr int kClusterMost = 8;
+// The blocks' sums of a row to its sum: each block hands its own to all, added in the blocks' order.  All threads of all blocks come
+// here as often as each other, as they have the same rows.
+template <int N>
+__device__ __forceinline__ void cluster_sums(float (&v)[N], float (*shared)[N * kClusterMost], int turn, uint32_t rank, uint32_t blocks) {
+  float* const mine = shared[turn];
+  if (threadIdx.x < blocks) {
+    uint32_t to;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"((uint32_t)__cvta_generic_to_shared(mine + rank * N)), "r"(threadIdx.x));
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4 * i), "f"(v[i]) : "memory");
+  }
+  __syncwarp();  // whole warps arrive
+  cluster_barrier();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = mine[i];
+    for (uint32_t b = 1; b < blocks; ++b) v[i] += mine[b * N + i];
+  }
+}
+
 // v becomes its distance from the mean, columns past the end stay 0; returns its squares' sum
 template <int TPR, int CH, bool VEC>
 __device__ __forceinline__ float centre(f2 (&v)[CH][4], float mean, int t, int cols) {
@@ -246,18 +280,21 @@ constexpr int kForwardBlocks = (CH > 1 ? 512 : 768) / kForwardThreads<TPR>;
 template <typename T>
 constexpr int kForwardStages = sizeof(T) == 2 ? 3 : 2;
 
-template <typename T, int TPR, int CH, bool VEC, bool POST>
+template <typename T, int TPR, int CH, bool VEC, bool POST, bool CLUSTER>
 static __global__ void __launch_bounds__(kForwardThreads<TPR>, kForwardBlocks<TPR, CH, POST>) k_rn_forward(const ResidualForward A) {
   constexpr int kThreads = kForwardThreads<TPR>, kGroups = kThreads / TPR, kStages = kForwardStages<T>;
   extern __shared__ __align__(16) char dynamic[];
   __shared__ __align__(16) float red[kGroups][2][kRedWords<TPR, 1>];
-  const int t = threadIdx.x % TPR, group = threadIdx.x / TPR, cols = A.cols;
-  const int64_t step = (int64_t)gridDim.x * kGroups, first = (int64_t)blockIdx.x * kGroups + group;
+  __shared__ float across[CLUSTER ? 2 : 1][kClusterMost];
+  const uint32_t rank = CLUSTER ? cluster_rank() : 0, blocks = CLUSTER ? cluster_blocks() : 1;
+  const int t = threadIdx.x % TPR + rank * TPR * CH, group = threadIdx.x / TPR, cols = A.cols;
+  const int64_t step = (int64_t)(gridDim.x / blocks) * kGroups, first = (int64_t)(blockIdx.x / blocks) * kGroups + group;
   using Stream = RowStream<T, TPR, CH, VEC, 2, kStages, kThreads>;
   Stream x(dynamic, 0, A.x, A.ldx, first, step, t, cols), b(dynamic, 1, A.block, A.ldblock, first, step, t, cols);
   const bool block = A.block != nullptr;
   in_turn();
-  if (first >= A.rows) return;  // (no barrier is the whole block's)
+  if (CLUSTER) cluster_barrier();  // the other blocks are there to be written to
+  if (first >= A.rows) return;     // (no barrier is the whole block's, and a cluster's blocks have the same rows)
   auto ahead = [&](int stage, int64_t r) {
     if (r < A.rows) {
       x.ahead(stage, t, cols);
@@ -292,16 +329,21 @@ static __global__ void __launch_bounds__(kForwardThreads<TPR>, kForwardBlocks<TP
   // (v - mean) and 1/sqrt of its mean square
   auto normal = [&](f2(&v)[CH][4], float* means, float* rstds, int64_t r) {
     float q[1];
+    auto sums = [&] {
+      const int now = turn;
+      row_sums<TPR>(q, red[group], turn, 1 + group);
+      if (CLUSTER) cluster_sums(q, across, now, rank, blocks);
+    };
     if (A.layer) {
       q[0] = total(v);
-      row_sums<TPR>(q, red[group], turn, 1 + group);
+      sums();
       const float mean = q[0] * A.inv_cols;
       if (t == 0) means[r] = mean;
       q[0] = centre<TPR, CH, VEC>(v, mean, t, cols);
     } else {
       q[0] = squares(v);
     }
-    row_sums<TPR>(q, red[group], turn, 1 + group);
+    sums();
     const float rstd = halves(rsqrt_rounded(splat(fmaf(q[0], A.inv_cols, A.eps)))).x;
     if (t == 0) rstds[r] = rstd;
     return splat(rstd);
@@ -360,20 +402,23 @@ constexpr int kBackwardStages = sizeof(T) == 2 ? 3 : VEC ? 3 : 2;
 
 // What the block's side has: nothing but dropout and a scale, a gate, or a norm (and a gate).
 enum BlockSide { kBlockPlain = 0, kBlockGate = 1, kBlockNorm = 2 };
-template <typename T, int TPR, bool VEC, int SIDE>
+template <typename T, int TPR, bool VEC, int SIDE, bool CLUSTER>
 static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(const ResidualBackward A) {
   constexpr int kGroups = kBackwardThreads / TPR, kStages = kBackwardStages<T, VEC>;
   constexpr bool POST = SIDE == kBlockNorm, block = SIDE != kBlockPlain;
   constexpr int kKinds = 2 + SIDE;  // sums of dy shat, dy, d bhat, d
   extern __shared__ __align__(16) char dynamic[];
   __shared__ __align__(16) float red[kGroups][2][kRedWords<TPR, 2>];
-  const int t = threadIdx.x % TPR, group = threadIdx.x / TPR, cols = A.cols, c = t * 8;
-  const int64_t step = (int64_t)gridDim.x * kGroups, first = (int64_t)blockIdx.x * kGroups + group;
+  __shared__ float across[CLUSTER ? 2 : 1][2 * kClusterMost];
+  const uint32_t rank = CLUSTER ? cluster_rank() : 0, blocks = CLUSTER ? cluster_blocks() : 1;
+  const int t = threadIdx.x % TPR + rank * TPR, group = threadIdx.x / TPR, cols = A.cols, c = t * 8;
+  const int64_t step = (int64_t)(gridDim.x / blocks) * kGroups, first = (int64_t)(blockIdx.x / blocks) * kGroups + group;
   using Stream = RowStream<T, TPR, 1, VEC, 4, kStages, kBackwardThreads>;
   Stream dy(dynamic, 0, A.dy, A.lddy, first, step, t, cols), s(dynamic, 1, A.s, A.lds, first, step, t, cols),
       ds(dynamic, 2, A.ds, A.ldds, first, step, t, cols), b(dynamic, 3, A.block, A.ldblock, first, step, t, cols);
   const bool pre = A.gamma != nullptr, path = A.ds != nullptr;
   in_turn();
+  if (CLUSTER) cluster_barrier();  // the other blocks are there to be written to
   auto ahead = [&](int stage, int64_t r) {
     if (r < A.rows) {
       if (pre) dy.ahead(stage, t, cols), s.ahead(stage, t, cols);
@@ -413,6 +458,11 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
   };
   statistics(first);
   int turn = 0, stage = 0;
+  auto sums = [&](float(&v)[2]) {
+    const int now = turn;
+    row_sums<TPR>(v, red[group], turn, 1 + group);
+    if (CLUSTER) cluster_sums(v, across, now, rank, blocks);
+  };
   T *pdx = static_cast<T*>(A.dx) + first * A.lddx, *pdb = static_cast<T*>(A.dblock) + first * A.lddblock;
   for (int64_t r = first; r < A.rows; r += step) {
     const float mu = mean, rs = rstd, bmu = block_mean, brs = block_rstd;
@@ -440,7 +490,7 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
         s1 = fma2(q[e], hat[e], s1);
       }
       float v[2] = {sum_of(s0), sum_of(s1)};
-      row_sums<TPR>(v, red[group], turn, 1 + group);
+      sums(v);
       const f2 m0 = splat(A.layer ? -v[0] * A.inv_cols * rs : 0.0f), m1 = splat(-v[1] * A.inv_cols * rs);
 #pragma unroll
       for (int e = 0; e < 4; ++e) d[e] = add2(fma2(hat[e], m1, fma2(q[e], splat(rs), m0)), d[e]);
@@ -466,7 +516,7 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
             s1 = fma2(d[e], hat[e], s1);
           }
           float v[2] = {sum_of(s0), sum_of(s1)};
-          row_sums<TPR>(v, red[group], turn, 1 + group);
+          sums(v);
           const f2 m0 = splat(A.layer ? -v[0] * A.inv_cols * brs : 0.0f), m1 = splat(-v[1] * A.inv_cols * brs);
 #pragma unroll
           for (int e = 0; e < 4; ++e) d[e] = fma2(hat[e], m1, fma2(d[e], splat(brs), m0));
@@ -494,16 +544,16 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
     __syncthreads();
     if (group >= low && group < n) {
 #pragma unroll
-      for (int i = 0; i < kSums; ++i) join[((group - low) * kSums + i) * TPR + t] = sum[i / 4][i % 4];
+      for (int i = 0; i < kSums; ++i) join[((group - low) * kSums + i) * TPR + threadIdx.x % TPR] = sum[i / 4][i % 4];
     }
     __syncthreads();
     if (group < low) {
 #pragma unroll
-      for (int i = 0; i < kSums; ++i) sum[i / 4][i % 4] = add2(sum[i / 4][i % 4], join[(group * kSums + i) * TPR + t]);
+      for (int i = 0; i < kSums; ++i) sum[i / 4][i % 4] = add2(sum[i / 4][i % 4], join[(group * kSums + i) * TPR + threadIdx.x % TPR]);
     }
   }
   if (group == 0 && c < cols) {
-    float* p = A.part + (int64_t)blockIdx.x * 4 * cols + c;
+    float* p = A.part + (int64_t)(blockIdx.x / blocks) * 4 * cols + c;
 #pragma unroll
     for (int k = 0; k < kKinds; ++k) store_group8<float, false>(p + k * cols, cols - c, sum[k]);
   }
@@ -836,9 +886,9 @@ inline unsigned at_most(int64_t want, int64_t per_sm) {
   const int64_t most = (int64_t)sm_count() * per_sm;
   return (unsigned)(want < most ? want : most);
 }
-// With `bytes` of dynamic shared memory, which a kernel is allowed once for each device.
+// With `bytes` of dynamic shared memory, which a kernel is allowed once for each device, in clusters of `blocks`.
 template <typename Args>
-inline cudaError_t launch_rows(void (*kernel)(const Args), std::atomic<uint64_t>& ready, unsigned grid, int threads, int bytes, cudaStream_t s,
+inline cudaError_t launch_rows(void (*kernel)(const Args), std::atomic<uint64_t>& ready, unsigned grid, int threads, int bytes, int blocks, cudaStream_t s,
                                const Args& a) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -850,20 +900,28 @@ inline cudaError_t launch_rows(void (*kernel)(const Args), std::atomic<uint64_t>
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = dim3(grid * (unsigned)blocks);
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)bytes;
   cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)blocks;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = blocks > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-// the widest rows that are held in registers; wider ones are read again for each step
+// the widest rows that one block holds in registers, up to eight of them as a cluster; wider ones are read again for each step
 constexpr int kForwardCols = 512 * 2 * 8, kBackwardCols = 512 * 8;
+inline int cluster_for(int64_t cols, int held) {
+  int blocks = 1;
+  while (cols > (int64_t)blocks * held) blocks *= 2;
+  return blocks;
+}
 
 // f(threads a row): the fewest that hold `cols` columns, eight each
 template <typename F>
@@ -878,40 +936,46 @@ auto with_threads(int64_t cols, F&& f) {
   return f(integral_constant<int, 512>{});
 }
 
-template <typename T, int TPR, int CH, bool VEC, bool POST>
+template <typename T, int TPR, int CH, bool VEC, bool POST, bool CLUSTER>
 cudaError_t run_forward(const ResidualForward& a, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
+  const int blocks = CLUSTER ? cluster_for(a.cols, kForwardCols) : 1;
+  const int64_t most = (int64_t)sm_count() * kForwardBlocks<TPR, CH, POST> / blocks, want = ceil_div(a.rows, kForwardThreads<TPR> / TPR);
   constexpr int kThreads = kForwardThreads<TPR>, kBytes = RowStream<T, TPR, CH, VEC, 2, kForwardStages<T>, kThreads>::kBytes;
-  return launch_rows(k_rn_forward<T, TPR, CH, VEC, POST>, ready, at_most(ceil_div(a.rows, kThreads / TPR), kForwardBlocks<TPR, CH, POST>), kThreads,
-                     kBytes, s, a);
+  return launch_rows(k_rn_forward<T, TPR, CH, VEC, POST, CLUSTER>, ready, (unsigned)(want < most ? want : most), kThreads, kBytes, blocks, s, a);
 }
 template <typename T>
 cudaError_t rn_forward(const ResidualForward& a, cudaStream_t s) {
-  if (a.cols > kForwardCols) return launch_after(k_rn_forward_wide<T>, at_most(a.rows, 8), kWideThreads, s, a);
+  if (a.cols > kForwardCols * kClusterMost) return launch_after(k_rn_forward_wide<T>, at_most(a.rows, 8), kWideThreads, s, a);
   auto on16 = [](const void* p, int64_t ld) { return aligned(p, 16) && (ld * (int64_t)sizeof(T)) % 16 == 0; };
   const bool vec = a.cols % 8 == 0 && on16(a.x, a.ldx) && on16(a.block, a.ldblock) && on16(a.s, a.lds) && on16(a.y, a.ldy);
-  auto by = [&](auto tpr, auto ch) {
+  auto by = [&](auto tpr, auto ch, auto cluster) {
     constexpr int kTpr = decltype(tpr)::value, kCh = decltype(ch)::value;
-    if (vec) return a.block_gamma ? run_forward<T, kTpr, kCh, true, true>(a, s) : run_forward<T, kTpr, kCh, true, false>(a, s);
-    return a.block_gamma ? run_forward<T, kTpr, kCh, false, true>(a, s) : run_forward<T, kTpr, kCh, false, false>(a, s);
+    constexpr bool kCluster = decltype(cluster)::value;
+    if (vec) return a.block_gamma ? run_forward<T, kTpr, kCh, true, true, kCluster>(a, s) : run_forward<T, kTpr, kCh, true, false, kCluster>(a, s);
+    return a.block_gamma ? run_forward<T, kTpr, kCh, false, true, kCluster>(a, s) : run_forward<T, kTpr, kCh, false, false, kCluster>(a, s);
   };
   using std::integral_constant;
-  if (a.cols > 4096) return by(integral_constant<int, 512>{}, integral_constant<int, 2>{});
-  return with_threads(a.cols, [&](auto tpr) { return by(tpr, integral_constant<int, 1>{}); });
+  using Two = integral_constant<int, 2>;
+  if (a.cols > kForwardCols) return by(integral_constant<int, 512>{}, Two{}, std::true_type{});
+  if (a.cols > 4096) return by(integral_constant<int, 512>{}, Two{}, std::false_type{});
+  return with_threads(a.cols, [&](auto tpr) { return by(tpr, integral_constant<int, 1>{}, std::false_type{}); });
 }
 
-template <typename T, int TPR, bool VEC, int SIDE>
+template <typename T, int TPR, bool VEC, int SIDE, bool CLUSTER>
 cudaError_t run_backward(const ResidualBackward& a, unsigned parts, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
-  return launch_rows(k_rn_backward<T, TPR, VEC, SIDE>, ready, parts, kBackwardThreads, kBackwardSmem<T, TPR, VEC, SIDE>, s, a);
+  return launch_rows(k_rn_backward<T, TPR, VEC, SIDE, CLUSTER>, ready, parts, kBackwardThreads, kBackwardSmem<T, TPR, VEC, SIDE>,
+                     CLUSTER ? cluster_for(a.cols, kBackwardCols) : 1, s, a);
 }
 // Takes the workspace; with `run`, enqueues the work too.
 template <typename T>
 cudaError_t rn_backward(ResidualBackward a, const ParamGrads& g, int32_t grad_dtype, char* workspace, int64_t* used, cudaStream_t s, bool run) {
-  const bool params = g.dgamma || g.dbeta || g.dblock_gamma || g.dblock_beta || g.dgate, wide = a.cols > kBackwardCols;
+  const bool params = g.dgamma || g.dbeta || g.dblock_gamma || g.dblock_beta || g.dgate, wide = a.cols > kBackwardCols * kClusterMost;
   const int64_t run_rows = a.rows ? ceil_div(a.rows, 64) : 1;  // of a wide kernel's part
   const int64_t parts = a.rows == 0 ? 0
                         : wide      ? ceil_div(a.rows, run_rows)
+                        : a.cols > kBackwardCols ? std::min(a.rows, (int64_t)std::max(sm_count() / cluster_for(a.cols, kBackwardCols), 1))
                                     : with_threads(a.cols, [&](auto tpr) { return (int64_t)at_most(ceil_div(a.rows, kBackwardThreads / decltype(tpr)::value), 1); });
   const int64_t part_bytes = params ? (parts * 4 * a.cols * 4 + 15) & ~(int64_t)15 : 0;
   *used = part_bytes + (wide && a.gamma ? a.rows * 8 : 0);
@@ -928,15 +992,18 @@ cudaError_t rn_backward(ResidualBackward a, const ParamGrads& g, int32_t grad_dt
     auto on16 = [](const void* p, int64_t ld) { return aligned(p, 16) && (ld * (int64_t)sizeof(T)) % 16 == 0; };
     const bool vec = a.cols % 8 == 0 && on16(a.dy, a.lddy) && on16(a.ds, a.ldds) && on16(a.s, a.lds) && on16(a.block, a.ldblock) && on16(a.dx, a.lddx) &&
                      on16(a.dblock, a.lddblock);
-    e = with_threads(a.cols, [&](auto tpr) {
+    auto by = [&](auto tpr, auto cluster) {
       constexpr int kTpr = decltype(tpr)::value;
-      auto by = [&](auto v) {
+      constexpr bool kCluster = decltype(cluster)::value;
+      auto go = [&](auto v) {
         constexpr bool kVec = decltype(v)::value;
-        if (a.block_gamma) return run_backward<T, kTpr, kVec, kBlockNorm>(a, (unsigned)parts, s);
-        return a.gate ? run_backward<T, kTpr, kVec, kBlockGate>(a, (unsigned)parts, s) : run_backward<T, kTpr, kVec, kBlockPlain>(a, (unsigned)parts, s);
+        if (a.block_gamma) return run_backward<T, kTpr, kVec, kBlockNorm, kCluster>(a, (unsigned)parts, s);
+        return a.gate ? run_backward<T, kTpr, kVec, kBlockGate, kCluster>(a, (unsigned)parts, s)
+                      : run_backward<T, kTpr, kVec, kBlockPlain, kCluster>(a, (unsigned)parts, s);
       };
-      return vec ? by(std::true_type{}) : by(std::false_type{});
-    });
+      return vec ? go(std::true_type{}) : go(std::false_type{});
+    };
+    e = a.cols > kBackwardCols ? by(std::integral_constant<int, 512>{}, std::true_type{}) : with_threads(a.cols, [&](auto tpr) { return by(tpr, std::false_type{}); });
   }
   if (e != cudaSuccess || !params) return e;
   auto finish = [&](auto* kernel) {

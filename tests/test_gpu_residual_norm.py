@@ -40,7 +40,7 @@ def _call(gen, rows, cols, dtype, layout, layer, option, size=1.0):
 
 
 SHAPES = [(1, 1), (1, 8), (3, 40), (33, 72), (5, 200), (16, 256), (300, 264), (17, 512), (9, 768), (40, 1024), (150, 1155), (7, 1600), (1300, 520), (12, 2048), (6, 3001),
-          (5, 4096), (4, 5000), (4, 8192), (3, 8200), (2, 20000)]
+          (5, 4096), (4, 5000), (4, 8192), (3, 8200), (2, 20000), (5, 33000), (2, 70001), (1, 65544)]
 
 
 @pytest.mark.parametrize("layout", ["dense", "wide", "odd"])
@@ -83,7 +83,7 @@ def test_forward_and_backward(shape, layer, layout):
                     ref.check(got, wg[name], dtype if name in ("dx", "dblock") else grad, (name, *what))
 
 
-@pytest.mark.parametrize("cols", [264, 1155, 9000])
+@pytest.mark.parametrize("cols", [264, 1155, 9000, 40000])
 def test_values_of_all_sizes(cols):
     """Rows a million apart in size, a large mean, zero rows: statistics as good as for ordinary rows."""
     gen = base._gen(cols)
@@ -126,7 +126,7 @@ def test_no_rows():
     assert g.dx.shape == (0, 64) and all(t.shape == (64,) and not t.any() for t in g[2:])
 
 
-@pytest.mark.parametrize("shape", [(1, 8), (33, 200), (300, 1155), (20, 9000)], ids=str)
+@pytest.mark.parametrize("shape", [(1, 8), (33, 200), (300, 1155), (20, 9000), (3, 66000)], ids=str)
 @pytest.mark.parametrize("pad", [0, 8, 3])
 def test_both_ways_from_python_agree(both, shape, pad):  # noqa: F811
     for i, (option, layer) in enumerate(itertools.product(OPTIONS, (True, False))):
