@@ -472,6 +472,9 @@ static __global__ void __launch_bounds__(1024) k_sum_parts(const float* __restri
 onebit_status_t fail(onebit_status_t status, const char* what);
 onebit_status_t cuda_fail(cudaError_t e, const char* where);
 int sm_count();  // of the current device
+// What a kernel that gave up waiting leaves, in the current device's status word (NULL: a CUDA error).
+constexpr unsigned kStatusGaveUp = 1u;
+unsigned int* status_word();
 
 inline int dtype_size(int32_t dtype) { return dtype == ONEBIT_F32 ? 4 : 2; }
 inline bool dtype_ok(int32_t dtype) { return dtype >= ONEBIT_F32 && dtype <= ONEBIT_BF16; }

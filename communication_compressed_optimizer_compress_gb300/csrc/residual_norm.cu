@@ -7,11 +7,11 @@ namespace onebit {
 namespace layers {
 
 // (in files of their own)
-extern template cudaError_t rn_forward<float>(const ResidualForward&, cudaStream_t);
+extern template cudaError_t rn_forward<float>(ResidualForward, cudaStream_t);
 extern template cudaError_t rn_backward<float>(ResidualBackward, const ParamGrads&, int32_t, char*, int64_t*, cudaStream_t, bool);
-extern template cudaError_t rn_forward<__half>(const ResidualForward&, cudaStream_t);
+extern template cudaError_t rn_forward<__half>(ResidualForward, cudaStream_t);
 extern template cudaError_t rn_backward<__half>(ResidualBackward, const ParamGrads&, int32_t, char*, int64_t*, cudaStream_t, bool);
-extern template cudaError_t rn_forward<__nv_bfloat16>(const ResidualForward&, cudaStream_t);
+extern template cudaError_t rn_forward<__nv_bfloat16>(ResidualForward, cudaStream_t);
 extern template cudaError_t rn_backward<__nv_bfloat16>(ResidualBackward, const ParamGrads&, int32_t, char*, int64_t*, cudaStream_t, bool);
 
 namespace {

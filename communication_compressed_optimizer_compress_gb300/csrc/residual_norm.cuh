@@ -27,6 +27,7 @@ struct ResidualForward {
   int cols, groups;
   bool layer;
   float inv_cols, eps, scale;
+  unsigned int* status;
 };
 
 struct ResidualBackward {
@@ -50,6 +51,7 @@ struct ResidualBackward {
   bool layer;
   float inv_cols, scale;
   float* part;  // the parameters' partial sums
+  unsigned int* status;
   float* sums;  // (rows read again:) each row's two sums behind the norm before the next block
 };
 
@@ -216,26 +218,82 @@ __device__ __forceinline__ uint32_t cluster_blocks() {
   return r;
 }
 __device__ __forceinline__ void cluster_barrier() { asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-constexpr int kClusterMost = 8;
-// The blocks' sums of a row to its sum: each block hands its own to all, added in the blocks' order.  All threads of all blocks come
-// here as often as each other, as they have the same rows.
-template <int N>
-__device__ __forceinline__ void cluster_sums(float (&v)[N], float (*shared)[N * kClusterMost], int turn, uint32_t rank, uint32_t blocks) {
-  float* const mine = shared[turn];
-  if (threadIdx.x < blocks) {
-    uint32_t to;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"((uint32_t)__cvta_generic_to_shared(mine + rank * N)), "r"(threadIdx.x));
-#pragma unroll
-    for (int i = 0; i < N; ++i) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4 * i), "f"(v[i]) : "memory");
-  }
-  __syncwarp();  // whole warps arrive
-  cluster_barrier();
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    v[i] = mine[i];
-    for (uint32_t b = 1; b < blocks; ++b) v[i] += mine[b * N + i];
-  }
+// no block leaves while another may still send to it
+__device__ __forceinline__ void cluster_end() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
+constexpr int kClusterMost = 8;
+
+// The blocks' sums of a row to its sum, added in the blocks' order: each block sends its own to all, who wait for the bytes.  (With
+// the cluster's barrier instead, whose release waits for the rows that were stored before it, a row of 8192 columns took 2 us a sum.)
+// Two sets of places take turns: a block sends to one of them again only after it has had what the others sent behind their reading it.
+// A wait ends after about a second, and all that follow at once; the status word says so.
+template <int N>
+struct ClusterSums {
+  struct Shared {
+    float from[2][kClusterMost][N];
+    uint64_t bar[2];
+    int gave_up;
+  };
+  Shared& m;
+  unsigned int* status;
+  uint32_t rank, blocks, phase;
+  // by all threads, before the cluster's first barrier
+  __device__ __forceinline__ ClusterSums(Shared& shared, unsigned int* status_) : m(shared), status(status_), rank(cluster_rank()), blocks(cluster_blocks()), phase(0) {
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < 2; ++i) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(at(&m.bar[i])) : "memory");
+      *(volatile int*)&m.gave_up = 0;
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
+  }
+  __device__ __forceinline__ static uint32_t at(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+  __device__ __forceinline__ bool here(uint32_t bar, uint32_t parity) const {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+  }
+  __device__ __forceinline__ void operator()(float (&v)[N], int turn) {
+    const uint32_t bar = at(&m.bar[turn]);
+    if (threadIdx.x == 0) asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(blocks * N * 4) : "memory");
+    if (threadIdx.x < blocks) {
+      uint32_t to, its;
+      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(at(&m.from[turn][rank][0])), "r"(threadIdx.x));
+      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(its) : "r"(bar), "r"(threadIdx.x));
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(to + 4 * i), "r"(__float_as_uint(v[i])), "r"(its) : "memory");
+    }
+    __syncwarp();
+    const uint32_t parity = phase >> turn & 1;
+    phase ^= 1u << turn;
+    if (!here(bar, parity)) {
+      const long long t0 = clock64();
+      while (!here(bar, parity)) {
+        if (*(volatile int*)&m.gave_up) break;
+        if (clock64() - t0 > 2000000000ll) {
+          *(volatile int*)&m.gave_up = 1;
+          atomicOr(status, kStatusGaveUp);
+          break;
+        }
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i] = *(volatile float*)&m.from[turn][0][i];
+      for (uint32_t b = 1; b < blocks; ++b) v[i] += *(volatile float*)&m.from[turn][b][i];
+    }
+  }
+};
+
+struct OneBlock {
+  template <class Shared>
+  __device__ __forceinline__ OneBlock(Shared&, unsigned int*) {}
+  template <int N>
+  __device__ __forceinline__ void operator()(float (&)[N], int) const {}
+};
 
 // v becomes its distance from the mean, columns past the end stay 0; returns its squares' sum
 template <int TPR, int CH, bool VEC>
@@ -285,15 +343,16 @@ static __global__ void __launch_bounds__(kForwardThreads<TPR>, kForwardBlocks<TP
   constexpr int kThreads = kForwardThreads<TPR>, kGroups = kThreads / TPR, kStages = kForwardStages<T>;
   extern __shared__ __align__(16) char dynamic[];
   __shared__ __align__(16) float red[kGroups][2][kRedWords<TPR, 1>];
-  __shared__ float across[CLUSTER ? 2 : 1][kClusterMost];
+  __shared__ typename ClusterSums<1>::Shared places;
   const uint32_t rank = CLUSTER ? cluster_rank() : 0, blocks = CLUSTER ? cluster_blocks() : 1;
   const int t = threadIdx.x % TPR + rank * TPR * CH, group = threadIdx.x / TPR, cols = A.cols;
   const int64_t step = (int64_t)(gridDim.x / blocks) * kGroups, first = (int64_t)(blockIdx.x / blocks) * kGroups + group;
   using Stream = RowStream<T, TPR, CH, VEC, 2, kStages, kThreads>;
   Stream x(dynamic, 0, A.x, A.ldx, first, step, t, cols), b(dynamic, 1, A.block, A.ldblock, first, step, t, cols);
   const bool block = A.block != nullptr;
+  std::conditional_t<CLUSTER, ClusterSums<1>, OneBlock> across(places, A.status);
+  if (CLUSTER) cluster_barrier();  // the other blocks are there to be sent to
   in_turn();
-  if (CLUSTER) cluster_barrier();  // the other blocks are there to be written to
   if (first >= A.rows) return;     // (no barrier is the whole block's, and a cluster's blocks have the same rows)
   auto ahead = [&](int stage, int64_t r) {
     if (r < A.rows) {
@@ -332,7 +391,7 @@ static __global__ void __launch_bounds__(kForwardThreads<TPR>, kForwardBlocks<TP
     auto sums = [&] {
       const int now = turn;
       row_sums<TPR>(q, red[group], turn, 1 + group);
-      if (CLUSTER) cluster_sums(q, across, now, rank, blocks);
+      across(q, now);
     };
     if (A.layer) {
       q[0] = total(v);
@@ -394,6 +453,7 @@ static __global__ void __launch_bounds__(kForwardThreads<TPR>, kForwardBlocks<TP
     if (++stage == kStages) stage = 0;
   }
   copies_wait<0>();
+  if (CLUSTER) cluster_end();
 }
 
 constexpr int kBackwardThreads = 512;  // of 128 registers: all that an SM has room for, so that it leaves one part
@@ -409,7 +469,7 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
   constexpr int kKinds = 2 + SIDE;  // sums of dy shat, dy, d bhat, d
   extern __shared__ __align__(16) char dynamic[];
   __shared__ __align__(16) float red[kGroups][2][kRedWords<TPR, 2>];
-  __shared__ float across[CLUSTER ? 2 : 1][2 * kClusterMost];
+  __shared__ typename ClusterSums<2>::Shared places;
   const uint32_t rank = CLUSTER ? cluster_rank() : 0, blocks = CLUSTER ? cluster_blocks() : 1;
   const int t = threadIdx.x % TPR + rank * TPR, group = threadIdx.x / TPR, cols = A.cols, c = t * 8;
   const int64_t step = (int64_t)(gridDim.x / blocks) * kGroups, first = (int64_t)(blockIdx.x / blocks) * kGroups + group;
@@ -417,8 +477,9 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
   Stream dy(dynamic, 0, A.dy, A.lddy, first, step, t, cols), s(dynamic, 1, A.s, A.lds, first, step, t, cols),
       ds(dynamic, 2, A.ds, A.ldds, first, step, t, cols), b(dynamic, 3, A.block, A.ldblock, first, step, t, cols);
   const bool pre = A.gamma != nullptr, path = A.ds != nullptr;
+  std::conditional_t<CLUSTER, ClusterSums<2>, OneBlock> across(places, A.status);
+  if (CLUSTER) cluster_barrier();  // the other blocks are there to be sent to
   in_turn();
-  if (CLUSTER) cluster_barrier();  // the other blocks are there to be written to
   auto ahead = [&](int stage, int64_t r) {
     if (r < A.rows) {
       if (pre) dy.ahead(stage, t, cols), s.ahead(stage, t, cols);
@@ -461,7 +522,7 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
   auto sums = [&](float(&v)[2]) {
     const int now = turn;
     row_sums<TPR>(v, red[group], turn, 1 + group);
-    if (CLUSTER) cluster_sums(v, across, now, rank, blocks);
+    across(v, now);
   };
   T *pdx = static_cast<T*>(A.dx) + first * A.lddx, *pdb = static_cast<T*>(A.dblock) + first * A.lddblock;
   for (int64_t r = first; r < A.rows; r += step) {
@@ -534,6 +595,7 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
     if (++stage == kStages) stage = 0;
   }
   copies_wait<0>();
+  if (CLUSTER) cluster_end();
   if (!A.part) return;
   // the upper half of the row groups hand their sums to the lower, until one has them
   constexpr int kSums = kKinds * 4;
@@ -945,7 +1007,7 @@ cudaError_t run_forward(const ResidualForward& a, cudaStream_t s) {
   return launch_rows(k_rn_forward<T, TPR, CH, VEC, POST, CLUSTER>, ready, (unsigned)(want < most ? want : most), kThreads, kBytes, blocks, s, a);
 }
 template <typename T>
-cudaError_t rn_forward(const ResidualForward& a, cudaStream_t s) {
+cudaError_t rn_forward(ResidualForward a, cudaStream_t s) {
   if (a.cols > kForwardCols * kClusterMost) return launch_after(k_rn_forward_wide<T>, at_most(a.rows, 8), kWideThreads, s, a);
   auto on16 = [](const void* p, int64_t ld) { return aligned(p, 16) && (ld * (int64_t)sizeof(T)) % 16 == 0; };
   const bool vec = a.cols % 8 == 0 && on16(a.x, a.ldx) && on16(a.block, a.ldblock) && on16(a.s, a.lds) && on16(a.y, a.ldy);
@@ -957,7 +1019,8 @@ cudaError_t rn_forward(const ResidualForward& a, cudaStream_t s) {
   };
   using std::integral_constant;
   using Two = integral_constant<int, 2>;
-  if (a.cols > kForwardCols) return by(integral_constant<int, 512>{}, Two{}, std::true_type{});
+  if (a.cols > kForwardCols && !(a.status = status_word())) return cudaErrorUnknown;
+  if (a.cols > kForwardCols) return by(integral_constant<int, 512>{}, Two{}, std::true_type{}); 
   if (a.cols > 4096) return by(integral_constant<int, 512>{}, Two{}, std::false_type{});
   return with_threads(a.cols, [&](auto tpr) { return by(tpr, integral_constant<int, 1>{}, std::false_type{}); });
 }
@@ -1003,6 +1066,7 @@ cudaError_t rn_backward(ResidualBackward a, const ParamGrads& g, int32_t grad_dt
       };
       return vec ? go(std::true_type{}) : go(std::false_type{});
     };
+    if (a.cols > kBackwardCols && !(a.status = status_word())) return cudaErrorUnknown;
     e = a.cols > kBackwardCols ? by(std::integral_constant<int, 512>{}, std::true_type{}) : with_threads(a.cols, [&](auto tpr) { return by(tpr, std::false_type{}); });
   }
   if (e != cudaSuccess || !params) return e;

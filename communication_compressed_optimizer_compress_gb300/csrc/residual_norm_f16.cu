@@ -4,7 +4,7 @@
 namespace onebit {
 namespace layers {
 
-template cudaError_t rn_forward<__half>(const ResidualForward&, cudaStream_t);
+template cudaError_t rn_forward<__half>(ResidualForward, cudaStream_t);
 template cudaError_t rn_backward<__half>(ResidualBackward, const ParamGrads&, int32_t, char*, int64_t*, cudaStream_t, bool);
 
 }  // namespace layers

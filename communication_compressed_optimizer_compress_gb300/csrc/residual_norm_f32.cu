@@ -4,7 +4,7 @@
 namespace onebit {
 namespace layers {
 
-template cudaError_t rn_forward<float>(const ResidualForward&, cudaStream_t);
+template cudaError_t rn_forward<float>(ResidualForward, cudaStream_t);
 template cudaError_t rn_backward<float>(ResidualBackward, const ParamGrads&, int32_t, char*, int64_t*, cudaStream_t, bool);
 
 }  // namespace layers

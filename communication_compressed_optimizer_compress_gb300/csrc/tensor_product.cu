@@ -108,7 +108,7 @@ extern "C" onebit_status_t onebit_layers_get_status(onebit_stream_t stream) {
   cudaError_t e = cudaMemcpyAsync(&v, p, sizeof v, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_fail(e, "onebit_layers_get_status");
-  return v & kStatusGaveUp ? fail(ONEBIT_ERR_CUDA, "a product gave up waiting for its copies and stopped early") : ONEBIT_OK;
+  return v & kStatusGaveUp ? fail(ONEBIT_ERR_CUDA, "a kernel gave up waiting for its copies or its cluster") : ONEBIT_OK;
 }
 
 extern "C" onebit_status_t onebit_layers_clear_status(onebit_stream_t stream) {

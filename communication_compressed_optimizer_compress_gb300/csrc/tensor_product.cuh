@@ -59,8 +59,6 @@ constexpr int kProductSmem = 1024 + kStagesWith<CTAS, Epilogue> * kStageBytes + 
 constexpr int kFoldSlabs = 8;                 // slabs that an accumulator of a folded product sums up
 constexpr int kGroupTiles = 8;                // tile rows that are walked together, for the L2
 
-constexpr unsigned kStatusGaveUp = 1u;
-
 struct ProductArgs {
   CUtensorMap a, b;
   int64_t m;
@@ -1407,7 +1405,6 @@ cudaError_t make_output(Output<T>* out, T* p, int64_t rows, int64_t cols, int64_
   out->by_tma = true;
   return make_output_map(&out->map, (int)sizeof(T), p, rows, cols, ld);
 }
-unsigned int* status_word();   // of the current device (NULL: a CUDA error)
 uint32_t stall_bytes();        // the test hook's
 
 struct ProductShape {

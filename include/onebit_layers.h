@@ -329,8 +329,9 @@ onebit_status_t onebit_residual_norm_backward(const onebit_residual_norm_grad_t*
 /* ---- Status ----
  *
  * Synchronise `stream` and report the device's sticky flag: ONEBIT_OK, or ONEBIT_ERR_CUDA when some
- * product gave up waiting (about one second) for its own asynchronous copies and stopped early; its
- * outputs are then not meaningful.  The CUDA context stays usable. */
+ * product gave up waiting (about one second) for its own asynchronous copies and stopped early, or a residual norm of
+ * a row that several blocks share for a block's part of a sum; its outputs are then not meaningful.  The CUDA context
+ * stays usable. */
 onebit_status_t onebit_layers_get_status(onebit_stream_t stream);
 /* Clear the flag (enqueued on `stream`). */
 onebit_status_t onebit_layers_clear_status(onebit_stream_t stream);
