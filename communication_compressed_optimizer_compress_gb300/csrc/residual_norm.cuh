@@ -331,10 +331,10 @@ __device__ __forceinline__ float total(const f2 (&v)[CH][4]) {
 }
 
 template <int TPR>
-constexpr int kForwardThreads = TPR > 256 ? TPR : 256;
+constexpr int kForwardThreads = TPR > 128 ? TPR : 128;
 // blocks an SM: 80 registers a thread where one group of columns is held, else 128
 template <int TPR, int CH, bool POST>
-constexpr int kForwardBlocks = (CH > 1 ? 512 : 768) / kForwardThreads<TPR>;
+constexpr int kForwardBlocks = (CH > 1 ? 512 : POST ? 768 : 896) / kForwardThreads<TPR>;
 template <typename T>
 constexpr int kForwardStages = sizeof(T) == 2 ? 3 : 2;
 
