@@ -488,20 +488,21 @@ PyObject* dropout(PyObject* const* a) {
   return wrap(std::move(y));
 }
 
-// `count` vectors of n values out of one allocation (each one would take the host as long as a third of a launch), on 256 bytes
-struct Vectors {
+// Several results out of one allocation, each on 256 bytes: an allocation takes the host as long as a third of a launch.  For
+// vectors, and for matrices so small that nothing is lost when one of them outlives the others.
+constexpr int64_t kSmall = 1 << 17;  // bytes
+int64_t padded(int64_t count, at::ScalarType type) { return (count * (int64_t)c10::elementSize(type) + 255) / 256 * 256; }
+struct Pieces {
   at::Tensor all;
-  int64_t n, each;
-  int used = 0;
-  Vectors(int count, int64_t n_, at::ScalarType type, const at::Tensor& like) : n(n_) {
-    const int64_t per = 256 / (int64_t)c10::elementSize(type);
-    each = (n + per - 1) / per * per;
-    if (count > 0) all = empty({count * each}, type, like);
+  int64_t used = 0;
+  Pieces(int64_t bytes, const at::Tensor& like) {
+    if (bytes > 0) all = empty({bytes}, at::kByte, like);
   }
-  at::Tensor next() {
-    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
-    t.unsafeGetTensorImpl()->set_storage_offset(used++ * each);
-    t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+  at::Tensor next(at::IntArrayRef size, at::ScalarType type) {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), c10::scalarTypeToTypeMeta(type));
+    t.unsafeGetTensorImpl()->set_storage_offset(used / (int64_t)c10::elementSize(type));
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(size);
+    used += padded(t.numel(), type);
     return t;
   }
 };
@@ -529,13 +530,18 @@ PyObject* residual_norm(PyObject* const* a) {
   p.p = d.p, p.key = d.key, p.site = d.site;
   at::Tensor s, y, mean, rstd, block_mean, block_rstd;
   const bool layer = p.norm == ONEBIT_NORM_LAYER;
-  if (p.block) s = empty({m.rows, m.cols}, x.scalar_type(), x);
-  if (p.gamma) y = empty({m.rows, m.cols}, x.scalar_type(), x);
-  Vectors stats((1 + layer) * ((p.gamma != nullptr) + (p.block_gamma != nullptr)), m.rows, at::kFloat, x);
-  if (p.gamma && layer) mean = stats.next();
-  if (p.gamma) rstd = stats.next();
-  if (p.block_gamma && layer) block_mean = stats.next();
-  if (p.block_gamma) block_rstd = stats.next();
+  const at::ScalarType type = x.scalar_type();
+  const int64_t matrices = ((p.block != nullptr) + (p.gamma != nullptr)) * padded(m.rows * m.cols, type);
+  const int statistics = (1 + layer) * ((p.gamma != nullptr) + (p.block_gamma != nullptr));
+  const bool small = matrices <= kSmall;
+  Pieces pieces((small ? matrices : 0) + statistics * padded(m.rows, at::kFloat), x);
+  auto matrix_out = [&] { return small ? pieces.next({m.rows, m.cols}, type) : empty({m.rows, m.cols}, type, x); };
+  if (p.block) s = matrix_out();
+  if (p.gamma) y = matrix_out();
+  if (p.gamma && layer) mean = pieces.next({m.rows}, at::kFloat);
+  if (p.gamma) rstd = pieces.next({m.rows}, at::kFloat);
+  if (p.block_gamma && layer) block_mean = pieces.next({m.rows}, at::kFloat);
+  if (p.block_gamma) block_rstd = pieces.next({m.rows}, at::kFloat);
   p.s = bytes(s), p.y = bytes(y), p.lds = p.ldy = m.cols;
   p.mean = floats(mean), p.rstd = floats(rstd), p.block_mean = floats(block_mean), p.block_rstd = floats(block_rstd);
   require(g_entry.rn_forward(&p, stream(x)) == ONEBIT_OK);
@@ -578,12 +584,12 @@ PyObject* residual_norm_backward(PyObject* const* a) {
   const bool layer = p.norm == ONEBIT_NORM_LAYER;
   at::Tensor dx = empty({rows, cols}, first.scalar_type(), first), dblock, dgamma, dbeta, dblock_gamma, dblock_beta, dgate;
   if (has_block) dblock = empty({rows, cols}, first.scalar_type(), first);
-  Vectors grads((1 + layer) * ((p.gamma != nullptr) + (p.block_gamma != nullptr)) + (p.gate != nullptr), cols, grad, first);
-  if (p.gamma) dgamma = grads.next();
-  if (p.gamma && layer) dbeta = grads.next();
-  if (p.block_gamma) dblock_gamma = grads.next();
-  if (p.block_gamma && layer) dblock_beta = grads.next();
-  if (p.gate) dgate = grads.next();
+  Pieces grads(((1 + layer) * ((p.gamma != nullptr) + (p.block_gamma != nullptr)) + (p.gate != nullptr)) * padded(cols, grad), first);
+  if (p.gamma) dgamma = grads.next({cols}, grad);
+  if (p.gamma && layer) dbeta = grads.next({cols}, grad);
+  if (p.block_gamma) dblock_gamma = grads.next({cols}, grad);
+  if (p.block_gamma && layer) dblock_beta = grads.next({cols}, grad);
+  if (p.gate) dgate = grads.next({cols}, grad);
   p.dx = dx.data_ptr(), p.dblock = bytes(dblock), p.lddx = p.lddblock = cols;
   p.dgamma = bytes(dgamma), p.dbeta = bytes(dbeta), p.dblock_gamma = bytes(dblock_gamma), p.dblock_beta = bytes(dblock_beta), p.dgate = bytes(dgate);
   size_t need = 0;
