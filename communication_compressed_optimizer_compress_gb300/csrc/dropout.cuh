@@ -44,8 +44,7 @@ struct Generator {
     return philox(make_uint4((uint32_t)(uint64_t)group, (uint32_t)((uint64_t)group >> 32), step, site), k0, k1);
   }
   // a group's values, 0 where they are dropped (the upper half of a word is compared in place: what lies below it decides nothing)
-  __device__ __forceinline__ void keep8(int64_t group, f2 (&v)[4]) const {
-    const uint4 w = draw(group);
+  __device__ __forceinline__ void keep8(const uint4& w, f2 (&v)[4]) const {
     const uint32_t words[4] = {w.x, w.y, w.z, w.w}, least = threshold << 16;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -56,7 +55,7 @@ struct Generator {
   __device__ __forceinline__ void apply8(int64_t group, f2 (&v)[4]) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], splat(factor));
-    keep8(group, v);
+    keep8(draw(group), v);
   }
 };
 

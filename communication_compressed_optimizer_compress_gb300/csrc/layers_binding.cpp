@@ -112,11 +112,31 @@ PyObject* pack(std::initializer_list<PyObject*> items) {
 PyObject* wrap(at::Tensor t) { return THPVariable_Wrap(std::move(t)); }
 PyObject* none() { return Py_NewRef(Py_None); }
 
+// Several results out of one allocation, each on 256 bytes: an allocation takes the host as long as a third of a launch.  For
+// vectors, for what is needed together, and for matrices so small that nothing is lost when one of them outlives the others.
+constexpr int64_t kSmall = 1 << 17;  // bytes
+int64_t padded(int64_t count, at::ScalarType type) { return (count * (int64_t)c10::elementSize(type) + 255) / 256 * 256; }
+struct Pieces {
+  at::Tensor all;
+  int64_t used = 0;
+  Pieces(int64_t bytes, const at::Tensor& like) {
+    if (bytes > 0) all = empty({bytes}, at::kByte, like);
+  }
+  at::Tensor next(at::IntArrayRef size, at::ScalarType type) {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), c10::scalarTypeToTypeMeta(type));
+    t.unsafeGetTensorImpl()->set_storage_offset(used / (int64_t)c10::elementSize(type));
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(size);
+    used += padded(t.numel(), type);
+    return t;
+  }
+};
 struct NewCheckpoint {
   at::Tensor codes, scales;
   NewCheckpoint(int64_t rows, int64_t cols, const at::Tensor& like)
       : codes(empty({rows, cols}, at::kChar, like)),
-        scales(empty({rows, (cols + ONEBIT_CHECKPOINT_BLOCK - 1) / ONEBIT_CHECKPOINT_BLOCK}, at::kFloat, like)) {}
+        scales(empty({rows, blocks(cols)}, at::kFloat, like)) {}
+  NewCheckpoint(int64_t rows, int64_t cols, Pieces& from) : codes(from.next({rows, cols}, at::kChar)), scales(from.next({rows, blocks(cols)}, at::kFloat)) {}
+  static int64_t blocks(int64_t cols) { return (cols + ONEBIT_CHECKPOINT_BLOCK - 1) / ONEBIT_CHECKPOINT_BLOCK; }
   int8_t* c() const { return static_cast<int8_t*>(codes.data_ptr()); }
   float* s() const { return static_cast<float*>(scales.data_ptr()); }
   PyObject* object(at::ScalarType type) const {
@@ -400,7 +420,9 @@ PyObject* gated_linear(PyObject* const* a) {
     return pack({wrap(std::move(h)), wrap(std::move(z))});
   }
   require(is(a[4], "checkpoint"));
-  const NewCheckpoint gate(p.rows, p.inner, x), up(p.rows, p.inner, x);
+  // (both halves are kept and needed together)
+  Pieces pieces(2 * (padded(p.rows * p.inner, at::kChar) + padded(p.rows * NewCheckpoint::blocks(p.inner), at::kFloat)), x);
+  const NewCheckpoint gate(p.rows, p.inner, pieces), up(p.rows, p.inner, pieces);
   p.gate_codes = gate.c(), p.gate_scales = gate.s(), p.up_codes = up.c(), p.up_scales = up.s();
   with_sized_workspace(g_entry.gated_forward, g_entry.gated_forward_workspace, p, x);
   return pack({wrap(std::move(h)), named(g_gated, {gate.object(x.scalar_type()), up.object(x.scalar_type())})});
@@ -488,24 +510,6 @@ PyObject* dropout(PyObject* const* a) {
   return wrap(std::move(y));
 }
 
-// Several results out of one allocation, each on 256 bytes: an allocation takes the host as long as a third of a launch.  For
-// vectors, and for matrices so small that nothing is lost when one of them outlives the others.
-constexpr int64_t kSmall = 1 << 17;  // bytes
-int64_t padded(int64_t count, at::ScalarType type) { return (count * (int64_t)c10::elementSize(type) + 255) / 256 * 256; }
-struct Pieces {
-  at::Tensor all;
-  int64_t used = 0;
-  Pieces(int64_t bytes, const at::Tensor& like) {
-    if (bytes > 0) all = empty({bytes}, at::kByte, like);
-  }
-  at::Tensor next(at::IntArrayRef size, at::ScalarType type) {
-    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), c10::scalarTypeToTypeMeta(type));
-    t.unsafeGetTensorImpl()->set_storage_offset(used / (int64_t)c10::elementSize(type));
-    t.unsafeGetTensorImpl()->set_sizes_contiguous(size);
-    used += padded(t.numel(), type);
-    return t;
-  }
-};
 const float* vector_or_null(PyObject* o, int64_t n, const at::Tensor& like) { return o == Py_None ? nullptr : vector(o, n, like); }
 float* floats(const at::Tensor& t) { return t.defined() ? static_cast<float*>(t.data_ptr()) : nullptr; }
 void* bytes(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }

@@ -412,6 +412,9 @@ static __global__ void __launch_bounds__(kForwardThreads<TPR>, kForwardBlocks<TP
     ahead(stage == 0 ? kStages - 1 : stage - 1, r + (kStages - 1) * step);
     f2 s[CH][4];
     const int mx = VEC ? 0 : off16<T>(A.x, A.ldx, r), mb = VEC ? 0 : off16<T>(A.block, A.ldblock, r);
+    uint4 bits[CH];
+#pragma unroll
+    for (int j = 0; j < CH; ++j) bits[j] = gen.threshold ? gen.draw(r * A.groups + j * TPR + t) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int j = 0; j < CH; ++j) x.take(stage, j, mx, s[j]);
     if (block) {
@@ -433,7 +436,7 @@ static __global__ void __launch_bounds__(kForwardThreads<TPR>, kForwardBlocks<TP
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
         const int c = (j * TPR + t) * 8;
-        if (gen.threshold) gen.keep8(r * A.groups + c / 8, n[j]);
+        if (gen.threshold) gen.keep8(bits[j], n[j]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[j][e] = add2(s[j][e], n[j][e]);
         store_columns<T, TPR, VEC>(ps, c, cols, s[j]);
@@ -530,6 +533,7 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
     copies_wait<kStages - 2>();
     ahead(stage == 0 ? kStages - 1 : stage - 1, r + (kStages - 1) * step);
     statistics(r + step);
+    const uint4 bits = gen.threshold ? gen.draw(r * A.groups + t) : make_uint4(0, 0, 0, 0);  // (beside the first sums' exchanges)
     f2 d[4];  // t, then d, then what is left of it before the block
     if (path) {
       ds.take(stage, 0, VEC ? 0 : off16<T>(A.ds, A.ldds, r), d);
@@ -561,7 +565,7 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
     if (A.dblock) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) d[e] = mul2(d[e], scale);
-      if (gen.threshold) gen.keep8(r * A.groups + t, d);
+      if (gen.threshold) gen.keep8(bits, d);
       if (block) {
         f2 hat[4];
         b.take(stage, 0, VEC ? 0 : off16<T>(A.block, A.ldblock, r), hat);
