@@ -106,7 +106,7 @@ struct RowStream {
 #pragma unroll
         for (int v = 0; v < kVectors; ++v) {
           const int bytes = left - 16 * v < 16 ? left - 16 * v : 16;  // the rest is zeros
-          if (v == 0 && c == 0 && m > 0 && next == base) {  // what lies before the matrix's first row is left alone
+          if (v == 0 && c == 0 && row - m < reinterpret_cast<const char*>(base)) {  // what lies before the matrix is left alone
 #pragma unroll 1
             for (int e = 0; e < 16; e += (int)sizeof(T)) {
               uint32_t bits = 0;

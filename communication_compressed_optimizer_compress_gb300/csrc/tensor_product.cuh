@@ -41,7 +41,7 @@ template <int CTAS>
 constexpr int kEpilogueWarps = 8 * CTAS;      // 128 rows are 4 quarters of the tensor memory; 64 columns a warp
 template <int CTAS>
 constexpr int kProductThreads = 128 + 32 * kEpilogueWarps<CTAS>;
-// A pair's block is launched with 640 * 96 registers; 128 * 56 + 512 * 104 of them are used.
+// A pair's block is launched with 640 * 96 registers, which are 128 * 64 + 512 * 104.
 constexpr int kControlRegs = 64, kEpilogueRegs = 104;
 // A warp's staging buffer: 32 rows of 64 bytes (2048, swizzled, what TMA stores; padded to 80 bytes a row
 // where single elements are stored), behind it 32 rows of 32 codes, and 64 columns' bias.

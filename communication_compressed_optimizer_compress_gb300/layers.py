@@ -325,7 +325,8 @@ def _on(stream, t):
 
 
 def get_status(stream=None) -> int:
-    """Waits for the stream; OK, or ERR_CUDA when a product of its device gave up waiting for its copies."""
+    """Waits for the stream; OK, or ERR_CUDA when a kernel of its device gave up waiting for its copies (a product) or for
+    another block's part of a row (a residual norm of rows that several blocks share)."""
     with _device_of(stream):
         return int(_functions().onebit_layers_get_status(_stream_ptr(stream)))
 
