@@ -465,14 +465,16 @@ constexpr int kBackwardStages = sizeof(T) == 2 ? 3 : VEC ? 3 : 2;
 
 // What the block's side has: nothing but dropout and a scale, a gate, or a norm (and a gate).
 enum BlockSide { kBlockPlain = 0, kBlockGate = 1, kBlockNorm = 2 };
-template <typename T, int TPR, bool VEC, int SIDE, bool CLUSTER>
+// RMS: the norms are known to be without means (else A.layer says so), which saves their sums and a tenth of the instructions.
+template <typename T, int TPR, bool VEC, int SIDE, bool CLUSTER, bool RMS>
 static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(const ResidualBackward A) {
   constexpr int kGroups = kBackwardThreads / TPR, kStages = kBackwardStages<T, VEC>;
   constexpr bool POST = SIDE == kBlockNorm, block = SIDE != kBlockPlain;
-  constexpr int kKinds = 2 + SIDE;  // sums of dy shat, dy, d bhat, d
+  constexpr int kSums = RMS ? 1 : 2;                                   // of a row behind each norm
+  constexpr int kKinds = kSums + (SIDE == kBlockGate ? 1 : SIDE / 2 * kSums);  // over the rows: of dy shat, dy, d bhat, d; without the means' none of dy and d
   extern __shared__ __align__(16) char dynamic[];
-  __shared__ __align__(16) float red[kGroups][2][kRedWords<TPR, 2>];
-  __shared__ typename ClusterSums<2>::Shared places;
+  __shared__ __align__(16) float red[kGroups][2][kRedWords<TPR, kSums>];
+  __shared__ typename ClusterSums<kSums>::Shared places;
   const uint32_t rank = CLUSTER ? cluster_rank() : 0, blocks = CLUSTER ? cluster_blocks() : 1;
   const int t = threadIdx.x % TPR + rank * TPR, group = threadIdx.x / TPR, cols = A.cols, c = t * 8;
   const int64_t step = (int64_t)(gridDim.x / blocks) * kGroups, first = (int64_t)(blockIdx.x / blocks) * kGroups + group;
@@ -480,7 +482,7 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
   Stream dy(dynamic, 0, A.dy, A.lddy, first, step, t, cols), s(dynamic, 1, A.s, A.lds, first, step, t, cols),
       ds(dynamic, 2, A.ds, A.ldds, first, step, t, cols), b(dynamic, 3, A.block, A.ldblock, first, step, t, cols);
   const bool pre = A.gamma != nullptr, path = A.ds != nullptr;
-  std::conditional_t<CLUSTER, ClusterSums<2>, OneBlock> across(places, A.status);
+  std::conditional_t<CLUSTER, ClusterSums<kSums>, OneBlock> across(places, A.status);
   if (CLUSTER) cluster_barrier();  // the other blocks are there to be sent to
   in_turn();
   auto ahead = [&](int stage, int64_t r) {
@@ -508,21 +510,22 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
   for (int k = 0; k < kKinds; ++k)
 #pragma unroll
     for (int e = 0; e < 4; ++e) sum[k][e] = 0;
+  const bool layer = !RMS && A.layer;
   float mean = 0.0f, rstd = 0.0f, block_mean = 0.0f, block_rstd = 0.0f;  // of the next row
   auto statistics = [&](int64_t r) {
     if (r >= A.rows) return;
     if (pre) {
-      if (A.layer) mean = __ldg(A.mean + r);
+      if (layer) mean = __ldg(A.mean + r);
       rstd = __ldg(A.rstd + r);
     }
     if (POST) {
-      if (A.layer) block_mean = __ldg(A.block_mean + r);
+      if (layer) block_mean = __ldg(A.block_mean + r);
       block_rstd = __ldg(A.block_rstd + r);
     }
   };
   statistics(first);
   int turn = 0, stage = 0;
-  auto sums = [&](float(&v)[2]) {
+  auto sums = [&](float(&v)[kSums]) {
     const int now = turn;
     row_sums<TPR>(v, red[group], turn, 1 + group);
     across(v, now);
@@ -547,18 +550,22 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
       s.take(stage, 0, VEC ? 0 : off16<T>(A.s, A.lds, r), hat);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {  // columns past the end have dy = gamma = 0 and add nothing
-        hat[e] = mul2(add2(hat[e], splat(-mu)), splat(rs));
+        hat[e] = mul2(RMS ? hat[e] : add2(hat[e], splat(-mu)), splat(rs));
         sum[0][e] = fma2(q[e], hat[e], sum[0][e]);
-        sum[1][e] = add2(sum[1][e], q[e]);
+        if (!RMS) sum[kSums - 1][e] = add2(sum[kSums - 1][e], q[e]);
         q[e] = mul2(q[e], gamma[e]);
-        s0 = add2(s0, q[e]);
+        if (!RMS) s0 = add2(s0, q[e]);
         s1 = fma2(q[e], hat[e], s1);
       }
-      float v[2] = {sum_of(s0), sum_of(s1)};
+      float v[kSums];
+      v[0] = sum_of(s0), v[kSums - 1] = sum_of(s1);
       sums(v);
-      const f2 m0 = splat(A.layer ? -v[0] * A.inv_cols * rs : 0.0f), m1 = splat(-v[1] * A.inv_cols * rs);
+      const f2 m0 = splat(layer ? -v[0] * A.inv_cols * rs : 0.0f), m1 = splat(-v[kSums - 1] * A.inv_cols * rs);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) d[e] = add2(fma2(hat[e], m1, fma2(q[e], splat(rs), m0)), d[e]);
+      for (int e = 0; e < 4; ++e) {
+        const f2 scaled = RMS ? mul2(q[e], splat(rs)) : fma2(q[e], splat(rs), m0);
+        d[e] = add2(fma2(hat[e], m1, scaled), d[e]);
+      }
     }
     store_columns<T, TPR, VEC>(pdx, c, cols, d);
     pdx += step * A.lddx;
@@ -573,22 +580,23 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
           f2 s0 = 0, s1 = 0;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {  // d is not 0 past the end, where pa is, and its sums there go nowhere
-            hat[e] = mul2(add2(hat[e], splat(-bmu)), splat(brs));
-            sum[kKinds - 2][e] = fma2(d[e], hat[e], sum[kKinds - 2][e]);
-            sum[kKinds - 1][e] = add2(sum[kKinds - 1][e], d[e]);
+            hat[e] = mul2(RMS ? hat[e] : add2(hat[e], splat(-bmu)), splat(brs));
+            sum[kSums][e] = fma2(d[e], hat[e], sum[kSums][e]);
+            if (!RMS) sum[kKinds - 1][e] = add2(sum[kKinds - 1][e], d[e]);
             d[e] = mul2(d[e], pa[e]);
-            s0 = add2(s0, d[e]);
+            if (!RMS) s0 = add2(s0, d[e]);
             s1 = fma2(d[e], hat[e], s1);
           }
-          float v[2] = {sum_of(s0), sum_of(s1)};
+          float v[kSums];
+          v[0] = sum_of(s0), v[kSums - 1] = sum_of(s1);
           sums(v);
-          const f2 m0 = splat(A.layer ? -v[0] * A.inv_cols * brs : 0.0f), m1 = splat(-v[1] * A.inv_cols * brs);
+          const f2 m0 = splat(layer ? -v[0] * A.inv_cols * brs : 0.0f), m1 = splat(-v[kSums - 1] * A.inv_cols * brs);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) d[e] = fma2(hat[e], m1, fma2(d[e], splat(brs), m0));
+          for (int e = 0; e < 4; ++e) d[e] = fma2(hat[e], m1, RMS ? mul2(d[e], splat(brs)) : fma2(d[e], splat(brs), m0));
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            sum[kKinds - 1][e] = fma2(d[e], hat[e], sum[kKinds - 1][e]);
+            sum[kSums][e] = fma2(d[e], hat[e], sum[kSums][e]);
             d[e] = mul2(d[e], pa[e]);
           }
         }
@@ -602,7 +610,7 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
   if (CLUSTER) cluster_end();
   if (!A.part) return;
   // the upper half of the row groups hand their sums to the lower, until one has them
-  constexpr int kSums = kKinds * 4;
+  constexpr int kPairs = kKinds * 4;
   f2* const join = reinterpret_cast<f2*>(dynamic);
 #pragma unroll 1
   for (int n = kGroups; n > 1; n /= 2) {
@@ -610,18 +618,18 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
     __syncthreads();
     if (group >= low && group < n) {
 #pragma unroll
-      for (int i = 0; i < kSums; ++i) join[((group - low) * kSums + i) * TPR + threadIdx.x % TPR] = sum[i / 4][i % 4];
+      for (int i = 0; i < kPairs; ++i) join[((group - low) * kPairs + i) * TPR + threadIdx.x % TPR] = sum[i / 4][i % 4];
     }
     __syncthreads();
     if (group < low) {
 #pragma unroll
-      for (int i = 0; i < kSums; ++i) sum[i / 4][i % 4] = add2(sum[i / 4][i % 4], join[(group * kSums + i) * TPR + threadIdx.x % TPR]);
+      for (int i = 0; i < kPairs; ++i) sum[i / 4][i % 4] = add2(sum[i / 4][i % 4], join[(group * kPairs + i) * TPR + threadIdx.x % TPR]);
     }
   }
   if (group == 0 && c < cols) {
     float* p = A.part + (int64_t)(blockIdx.x / blocks) * 4 * cols + c;
 #pragma unroll
-    for (int k = 0; k < kKinds; ++k) store_group8<float, false>(p + k * cols, cols - c, sum[k]);
+    for (int k = 0; k < kKinds; ++k) store_group8<float, false>(p + (RMS ? 2 * k : k) * cols, cols - c, sum[k]);
   }
 }
 template <typename T, int TPR, bool VEC, int SIDE>
@@ -1029,10 +1037,10 @@ cudaError_t rn_forward(ResidualForward a, cudaStream_t s) {
   return with_threads(a.cols, [&](auto tpr) { return by(tpr, integral_constant<int, 1>{}, std::false_type{}); });
 }
 
-template <typename T, int TPR, bool VEC, int SIDE, bool CLUSTER>
+template <typename T, int TPR, bool VEC, int SIDE, bool CLUSTER, bool RMS>
 cudaError_t run_backward(const ResidualBackward& a, unsigned parts, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
-  return launch_rows(k_rn_backward<T, TPR, VEC, SIDE, CLUSTER>, ready, parts, kBackwardThreads, kBackwardSmem<T, TPR, VEC, SIDE>,
+  return launch_rows(k_rn_backward<T, TPR, VEC, SIDE, CLUSTER, RMS>, ready, parts, kBackwardThreads, kBackwardSmem<T, TPR, VEC, SIDE>,
                      CLUSTER ? cluster_for(a.cols, kBackwardCols) : 1, s, a);
 }
 // Takes the workspace; with `run`, enqueues the work too.
@@ -1062,13 +1070,14 @@ cudaError_t rn_backward(ResidualBackward a, const ParamGrads& g, int32_t grad_dt
     auto by = [&](auto tpr, auto cluster) {
       constexpr int kTpr = decltype(tpr)::value;
       constexpr bool kCluster = decltype(cluster)::value;
-      auto go = [&](auto v) {
-        constexpr bool kVec = decltype(v)::value;
-        if (a.block_gamma) return run_backward<T, kTpr, kVec, kBlockNorm, kCluster>(a, (unsigned)parts, s);
-        return a.gate ? run_backward<T, kTpr, kVec, kBlockGate, kCluster>(a, (unsigned)parts, s)
-                      : run_backward<T, kTpr, kVec, kBlockPlain, kCluster>(a, (unsigned)parts, s);
+      auto go = [&](auto v, auto rms) {
+        constexpr bool kVec = decltype(v)::value, kRms = decltype(rms)::value;
+        if (a.block_gamma) return run_backward<T, kTpr, kVec, kBlockNorm, kCluster, kRms>(a, (unsigned)parts, s);
+        return a.gate ? run_backward<T, kTpr, kVec, kBlockGate, kCluster, kRms>(a, (unsigned)parts, s)
+                      : run_backward<T, kTpr, kVec, kBlockPlain, kCluster, kRms>(a, (unsigned)parts, s);
       };
-      return vec ? go(std::true_type{}) : go(std::false_type{});
+      if (!vec) return go(std::false_type{}, std::false_type{});
+      return a.layer ? go(std::true_type{}, std::false_type{}) : go(std::true_type{}, std::true_type{});
     };
     if (a.cols > kBackwardCols && !(a.status = status_word())) return cudaErrorUnknown;
     e = a.cols > kBackwardCols ? by(std::integral_constant<int, 512>{}, std::true_type{}) : with_threads(a.cols, [&](auto tpr) { return by(tpr, std::false_type{}); });
