@@ -66,8 +66,8 @@ struct ResidualBackward {
 // vectors that its columns touch, one more than they fill, and shifts; their outputs are put together from its own and its
 // neighbour's values into aligned vectors, single elements where a warp's columns or the row begin and end.
 
-// One input's rows on their way: IN inputs share the ring, this is the `in`-th.
-template <typename T, int TPR, int CH, bool VEC, int IN, int STAGES, int THREADS>
+// One input's rows on their way: IN rows share a stage of the ring, this input has the `in`-th (of two rows at a time: and the one behind it).
+template <typename T, int TPR, int CH, bool VEC, int IN, int STAGES, int THREADS, int ROWS = 1>
 struct RowStream {
   static constexpr int kOwn = (int)sizeof(T) / 2, kVectors = kOwn + (VEC ? 0 : 1);  // 16-byte vectors of a group
   static constexpr int kBytes = STAGES * IN * CH * kVectors * THREADS * 16;
@@ -84,13 +84,16 @@ struct RowStream {
 #pragma unroll
         for (int i = 0; i < STAGES; ++i)
 #pragma unroll
-          for (int v = 0; v < kVectors; ++v) asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at(i, j, v)), "r"(0) : "memory");
+          for (int v = 0; v < kVectors; ++v)
+#pragma unroll
+            for (int n = 0; n < ROWS; ++n) asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at(i, j, v, n)), "r"(0) : "memory");
       }
   }
-  __device__ __forceinline__ uint32_t at(int stage, int j, int v) const {
-    return slot + (uint32_t)(stage * (IN * CH * kVectors * THREADS) + (j * kVectors + v) * THREADS) * 16;
+  __device__ __forceinline__ uint32_t at(int stage, int j, int v, int n = 0) const {
+    return slot + (uint32_t)(stage * (IN * CH * kVectors * THREADS) + ((n * CH + j) * kVectors + v) * THREADS) * 16;
   }
-  __device__ __forceinline__ void ahead(int stage, int t, int cols) {
+  // the n-th row, n rows (`offset` elements) behind the next one
+  __device__ __forceinline__ void ahead(int stage, int t, int cols, int n = 0, int64_t offset = 0) {
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
       const int c = (j * TPR + t) * 8;
@@ -98,7 +101,7 @@ struct RowStream {
       if (VEC) {
 #pragma unroll
         for (int v = 0; v < kVectors; ++v)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at(stage, j, v)), "l"(next + c + v * (16 / (int)sizeof(T))) : "memory");
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at(stage, j, v, n)), "l"(next + offset + c + v * (16 / (int)sizeof(T))) : "memory");
       } else {
         const char* const row = reinterpret_cast<const char*>(next);
         const int m = (int)(reinterpret_cast<uintptr_t>(row) & 15);
@@ -126,14 +129,14 @@ struct RowStream {
         }
       }
     }
-    next += hop;
+    if (ROWS == 1) next += hop;
   }
   // eight columns of a row, 0 past the end; m: the row's distance from 16 bytes (VEC: any)
-  __device__ __forceinline__ void take(int stage, int j, int m, f2 (&f)[4]) const {
+  __device__ __forceinline__ void take(int stage, int j, int m, f2 (&f)[4], int n = 0) const {
     uint32_t w[4 * kVectors];
 #pragma unroll
     for (int v = 0; v < kVectors; ++v)
-      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[4 * v]), "=r"(w[4 * v + 1]), "=r"(w[4 * v + 2]), "=r"(w[4 * v + 3]) : "r"(at(stage, j, v)) : "memory");
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[4 * v]), "=r"(w[4 * v + 1]), "=r"(w[4 * v + 2]), "=r"(w[4 * v + 3]) : "r"(at(stage, j, v, n)) : "memory");
     if constexpr (!VEC) shift_words<T>(w, m);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -332,32 +335,40 @@ __device__ __forceinline__ float total(const f2 (&v)[CH][4]) {
 
 template <int TPR>
 constexpr int kForwardThreads = TPR > 128 ? TPR : 128;
-// blocks an SM: 80 registers a thread where one group of columns is held, else 128
-template <int TPR, int CH, bool POST>
-constexpr int kForwardBlocks = (CH > 1 ? 512 : POST ? 768 : 896) / kForwardThreads<TPR>;
+// Blocks an SM: 72 registers a thread where one group of columns of one row is held, 80 with a norm behind the block, 96 for two rows (a
+// norm behind the block: 128), else 128.
+template <int TPR, int CH, int NR, bool POST>
+constexpr int kForwardBlocks = (CH > 1 ? 512 : NR > 1 ? (POST ? 512 : 640) : POST ? 768 : 896) / kForwardThreads<TPR>;
 template <typename T>
 constexpr int kForwardStages = sizeof(T) == 2 ? 3 : 2;
 
-template <typename T, int TPR, int CH, bool VEC, bool POST, bool CLUSTER>
-static __global__ void __launch_bounds__(kForwardThreads<TPR>, kForwardBlocks<TPR, CH, POST>) k_rn_forward(const ResidualForward A) {
+// NR rows at a time: two share the exchanges of their sums, the barrier behind them and the reciprocal roots.
+template <typename T, int TPR, int CH, int NR, bool VEC, bool POST, bool CLUSTER>
+static __global__ void __launch_bounds__(kForwardThreads<TPR>, kForwardBlocks<TPR, CH, NR, POST>) k_rn_forward(const ResidualForward A) {
+  static_assert(NR == 1 || (VEC && !CLUSTER), "two rows at a time: dense ones of one block");
   constexpr int kThreads = kForwardThreads<TPR>, kGroups = kThreads / TPR, kStages = kForwardStages<T>;
   extern __shared__ __align__(16) char dynamic[];
-  __shared__ __align__(16) float red[kGroups][2][kRedWords<TPR, 1>];
-  __shared__ typename ClusterSums<1>::Shared places;
+  __shared__ __align__(16) float red[kGroups][2][kRedWords<TPR, NR>];
+  __shared__ typename ClusterSums<NR>::Shared places;
   const uint32_t rank = CLUSTER ? cluster_rank() : 0, blocks = CLUSTER ? cluster_blocks() : 1;
   const int t = threadIdx.x % TPR + rank * TPR * CH, group = threadIdx.x / TPR, cols = A.cols;
-  const int64_t step = (int64_t)(gridDim.x / blocks) * kGroups, first = (int64_t)(blockIdx.x / blocks) * kGroups + group;
-  using Stream = RowStream<T, TPR, CH, VEC, 2, kStages, kThreads>;
-  Stream x(dynamic, 0, A.x, A.ldx, first, step, t, cols), b(dynamic, 1, A.block, A.ldblock, first, step, t, cols);
+  const int64_t step = (int64_t)(gridDim.x / blocks) * kGroups * NR, first = ((int64_t)(blockIdx.x / blocks) * kGroups + group) * NR;
+  using Stream = RowStream<T, TPR, CH, VEC, 2 * NR, kStages, kThreads, NR>;
+  Stream x(dynamic, 0, A.x, A.ldx, first, step, t, cols), b(dynamic, NR, A.block, A.ldblock, first, step, t, cols);
   const bool block = A.block != nullptr;
-  std::conditional_t<CLUSTER, ClusterSums<1>, OneBlock> across(places, A.status);
+  std::conditional_t<CLUSTER, ClusterSums<NR>, OneBlock> across(places, A.status);
   if (CLUSTER) cluster_barrier();  // the other blocks are there to be sent to
   in_turn();
   if (first >= A.rows) return;     // (no barrier is the whole block's, and a cluster's blocks have the same rows)
   auto ahead = [&](int stage, int64_t r) {
     if (r < A.rows) {
-      x.ahead(stage, t, cols);
-      if (block) b.ahead(stage, t, cols);
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+        if (n == 0 || r + n < A.rows) {
+          x.ahead(stage, t, cols, n, n * A.ldx);
+          if (block) b.ahead(stage, t, cols, n, n * A.ldblock);
+        }
+      if (NR > 1) x.next += x.hop, b.next += b.hop;
     }
     copies_commit();
   };
@@ -385,72 +396,81 @@ static __global__ void __launch_bounds__(kForwardThreads<TPR>, kForwardBlocks<TP
   }
   int turn = 0, stage = 0;
   T *ps = static_cast<T*>(A.s) + first * A.lds, *py = static_cast<T*>(A.y) + first * A.ldy;
-  // (v - mean) and 1/sqrt of its mean square
-  auto normal = [&](f2(&v)[CH][4], float* means, float* rstds, int64_t r) {
-    float q[1];
+  // v becomes v - mean; out 1/sqrt of its mean square
+  auto normal = [&](f2(&v)[NR][CH][4], float* means, float* rstds, int64_t r, float(&rstd)[NR]) {
+    float q[NR];
     auto sums = [&] {
       const int now = turn;
       row_sums<TPR>(q, red[group], turn, 1 + group);
       across(q, now);
     };
     if (A.layer) {
-      q[0] = total(v);
+#pragma unroll
+      for (int n = 0; n < NR; ++n) q[n] = total(v[n]);
       sums();
-      const float mean = q[0] * A.inv_cols;
-      if (t == 0) means[r] = mean;
-      q[0] = centre<TPR, CH, VEC>(v, mean, t, cols);
+#pragma unroll
+      for (int n = 0; n < NR; ++n) {
+        const float mean = q[n] * A.inv_cols;
+        if (t == 0 && (n == 0 || r + n < A.rows)) means[r + n] = mean;
+        q[n] = centre<TPR, CH, VEC>(v[n], mean, t, cols);
+      }
     } else {
-      q[0] = squares(v);
+#pragma unroll
+      for (int n = 0; n < NR; ++n) q[n] = squares(v[n]);
     }
     sums();
-    const float rstd = halves(rsqrt_rounded(splat(fmaf(q[0], A.inv_cols, A.eps)))).x;
-    if (t == 0) rstds[r] = rstd;
-    return splat(rstd);
+    const float2 root = halves(rsqrt_rounded(fma2(pair(q[0], q[NR - 1]), splat(A.inv_cols), splat(A.eps))));
+    rstd[0] = root.x, rstd[NR - 1] = root.y;
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+      if (t == 0 && (n == 0 || r + n < A.rows)) rstds[r + n] = rstd[n];
   };
-  for (int64_t r = first; r < A.rows; r += step) {
+  for (int64_t r = first; r < A.rows; r += step) {  // (a second row that is not there has no outputs)
     copies_wait<kStages - 2>();
     ahead(stage == 0 ? kStages - 1 : stage - 1, r + (kStages - 1) * step);
-    f2 s[CH][4];
+    f2 s[NR][CH][4];
     const int mx = VEC ? 0 : off16<T>(A.x, A.ldx, r), mb = VEC ? 0 : off16<T>(A.block, A.ldblock, r);
-    uint4 bits[CH];
+    uint4 bits[NR][CH];
 #pragma unroll
-    for (int j = 0; j < CH; ++j) bits[j] = gen.threshold ? gen.draw(r * A.groups + j * TPR + t) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int j = 0; j < CH; ++j) x.take(stage, j, mx, s[j]);
-    if (block) {
-      f2 n[CH][4];
-#pragma unroll
-      for (int j = 0; j < CH; ++j) b.take(stage, j, mb, n[j]);
-      if (POST) {
-        const f2 rstd = normal(n, A.block_mean, A.block_rstd, r);
-#pragma unroll
-        for (int j = 0; j < CH; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) n[j][e] = fma2(mul2(n[j][e], rstd), pa[j][e], pb[j][e]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < CH; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) n[j][e] = mul2(n[j][e], pa[j][e]);
-      }
+    for (int n = 0; n < NR; ++n)
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
-        const int c = (j * TPR + t) * 8;
-        if (gen.threshold) gen.keep8(bits[j], n[j]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[j][e] = add2(s[j][e], n[j][e]);
-        store_columns<T, TPR, VEC>(ps, c, cols, s[j]);
+        bits[n][j] = gen.threshold ? gen.draw((r + n) * A.groups + j * TPR + t) : make_uint4(0, 0, 0, 0);
+        x.take(stage, j, mx, s[n][j], n);
       }
+    if (block) {
+      f2 v[NR][CH][4];
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int j = 0; j < CH; ++j) b.take(stage, j, mb, v[n][j], n);
+      float rstd[NR];
+      if (POST) normal(v, A.block_mean, A.block_rstd, r, rstd);
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+          const int c = (j * TPR + t) * 8;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[n][j][e] = POST ? fma2(mul2(v[n][j][e], splat(rstd[n])), pa[j][e], pb[j][e]) : mul2(v[n][j][e], pa[j][e]);
+          if (gen.threshold) gen.keep8(bits[n][j], v[n][j]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][j][e] = add2(s[n][j][e], v[n][j][e]);
+          if (n == 0 || r + n < A.rows) store_columns<T, TPR, VEC>(ps + n * A.lds, c, cols, s[n][j]);
+        }
       ps += step * A.lds;
     }
     if (A.gamma) {
-      const f2 rstd = normal(s, A.mean, A.rstd, r);
+      float rstd[NR];
+      normal(s, A.mean, A.rstd, r, rstd);
 #pragma unroll
-      for (int j = 0; j < CH; ++j) {
+      for (int n = 0; n < NR; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[j][e] = fma2(mul2(s[j][e], rstd), gamma[j][e], beta[j][e]);
-        store_columns<T, TPR, VEC>(py, (j * TPR + t) * 8, cols, s[j]);
-      }
+        for (int j = 0; j < CH; ++j) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][j][e] = fma2(mul2(s[n][j][e], splat(rstd[n])), gamma[j][e], beta[j][e]);
+          if (n == 0 || r + n < A.rows) store_columns<T, TPR, VEC>(py + n * A.ldy, (j * TPR + t) * 8, cols, s[n][j]);
+        }
       py += step * A.ldy;
     }
     if (++stage == kStages) stage = 0;
@@ -1010,29 +1030,39 @@ auto with_threads(int64_t cols, F&& f) {
   return f(integral_constant<int, 512>{});
 }
 
-template <typename T, int TPR, int CH, bool VEC, bool POST, bool CLUSTER>
+template <typename T, int TPR, int CH, int NR, bool VEC, bool POST, bool CLUSTER>
 cudaError_t run_forward(const ResidualForward& a, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
   const int blocks = CLUSTER ? cluster_for(a.cols, kForwardCols) : 1;
-  const int64_t most = (int64_t)sm_count() * kForwardBlocks<TPR, CH, POST> / blocks, want = ceil_div(a.rows, kForwardThreads<TPR> / TPR);
-  constexpr int kThreads = kForwardThreads<TPR>, kBytes = RowStream<T, TPR, CH, VEC, 2, kForwardStages<T>, kThreads>::kBytes;
-  return launch_rows(k_rn_forward<T, TPR, CH, VEC, POST, CLUSTER>, ready, (unsigned)(want < most ? want : most), kThreads, kBytes, blocks, s, a);
+  const int64_t most = (int64_t)sm_count() * kForwardBlocks<TPR, CH, NR, POST> / blocks, want = ceil_div(a.rows, kForwardThreads<TPR> / TPR * NR);
+  constexpr int kThreads = kForwardThreads<TPR>, kBytes = RowStream<T, TPR, CH, VEC, 2 * NR, kForwardStages<T>, kThreads, NR>::kBytes;
+  return launch_rows(k_rn_forward<T, TPR, CH, NR, VEC, POST, CLUSTER>, ready, (unsigned)(want < most ? want : most), kThreads, kBytes, blocks, s, a);
 }
 template <typename T>
 cudaError_t rn_forward(ResidualForward a, cudaStream_t s) {
   if (a.cols > kForwardCols * kClusterMost) return launch_after(k_rn_forward_wide<T>, at_most(a.rows, 8), kWideThreads, s, a);
   auto on16 = [](const void* p, int64_t ld) { return aligned(p, 16) && (ld * (int64_t)sizeof(T)) % 16 == 0; };
   const bool vec = a.cols % 8 == 0 && on16(a.x, a.ldx) && on16(a.block, a.ldblock) && on16(a.s, a.lds) && on16(a.y, a.ldy);
+  // Two rows at a time where there are enough for all SMs and arithmetic, not bytes, bounds: with dropout or a norm behind the block (us
+  // for 16384 x 1024 bf16, one and two: layer norm with dropout 28.6, 25.4, with layer norms on both sides 30.7, 26.1, alone 22.9, 24.8).
+  const bool two = a.drop.threshold || a.block_gamma;
   auto by = [&](auto tpr, auto ch, auto cluster) {
     constexpr int kTpr = decltype(tpr)::value, kCh = decltype(ch)::value;
     constexpr bool kCluster = decltype(cluster)::value;
-    if (vec) return a.block_gamma ? run_forward<T, kTpr, kCh, true, true, kCluster>(a, s) : run_forward<T, kTpr, kCh, true, false, kCluster>(a, s);
-    return a.block_gamma ? run_forward<T, kTpr, kCh, false, true, kCluster>(a, s) : run_forward<T, kTpr, kCh, false, false, kCluster>(a, s);
+    auto go = [&](auto post) {
+      constexpr bool kPost = decltype(post)::value;
+      if (!vec) return run_forward<T, kTpr, kCh, 1, false, kPost, kCluster>(a, s);
+      if constexpr (sizeof(T) == 2 && kCh == 1 && !kCluster) {
+        if (two && a.rows * kTpr >= (int64_t)sm_count() * 1280) return run_forward<T, kTpr, kCh, 2, true, kPost, kCluster>(a, s);
+      }
+      return run_forward<T, kTpr, kCh, 1, true, kPost, kCluster>(a, s);
+    };
+    return a.block_gamma ? go(std::true_type{}) : go(std::false_type{});
   };
   using std::integral_constant;
   using Two = integral_constant<int, 2>;
   if (a.cols > kForwardCols && !(a.status = status_word())) return cudaErrorUnknown;
-  if (a.cols > kForwardCols) return by(integral_constant<int, 512>{}, Two{}, std::true_type{}); 
+  if (a.cols > kForwardCols) return by(integral_constant<int, 512>{}, Two{}, std::true_type{});
   if (a.cols > 4096) return by(integral_constant<int, 512>{}, Two{}, std::false_type{});
   return with_threads(a.cols, [&](auto tpr) { return by(tpr, integral_constant<int, 1>{}, std::false_type{}); });
 }

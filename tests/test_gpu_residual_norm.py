@@ -40,7 +40,8 @@ def _call(gen, rows, cols, dtype, layout, layer, option, size=1.0):
 
 
 SHAPES = [(1, 1), (1, 8), (50, 3), (41, 7), (3, 40), (33, 72), (5, 200), (16, 256), (300, 264), (17, 512), (9, 768), (40, 1024), (150, 1155), (7, 1600), (1300, 520), (12, 2048), (6, 3001),
-          (5, 4096), (4, 5000), (4, 8192), (3, 8200), (2, 20000), (5, 33000), (2, 70001), (1, 65544)]
+          (5, 4096), (4, 5000), (4, 8192), (3, 8200), (2, 20000), (5, 33000), (2, 70001), (1, 65544), (1601, 1000), (3101, 512), (801, 2048), (401, 4096), (25001, 64),
+          (12301, 120), (6203, 256)]
 
 
 @pytest.mark.parametrize("layout", ["dense", "wide", "odd"])
