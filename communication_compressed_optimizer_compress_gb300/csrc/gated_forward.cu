@@ -20,7 +20,8 @@ struct GatedOut {
   int blocks, act;
 };
 
-// The epilogue over the sums z (partial ones of a cut contraction), one warp per 64 columns of a row of h.
+// The epilogue over the sums z of a cut contraction, one warp per 64 columns of a row of h (a checkpoint's block), elements side by side.
+// Bound by the sums' bytes, out of the L2: 512 x 4096 x 256 in four parts.
 template <typename T>
 __global__ void __launch_bounds__(256) k_finish_gated(Partials c, int64_t rows, int n, const GatedOut<T> o) {
   in_turn();
@@ -56,9 +57,9 @@ __global__ void __launch_bounds__(256) k_finish_gated(Partials c, int64_t rows, 
 
 // Up to 32 rows, as generation meets them: the few-rows product (few_rows.cuh) with two weights to a column, the gate's and
 // the up projection's, whose sums meet in shared memory.  Bound by the weights' bytes and a launch's latency: a warp asks for kAhead
-// steps of both weights, and of x where it is up to eight rows, before it multiplies any; 128 registers a thread hold them (with 64
-// they spill: one row of 4096 -> 11008 35 us, 31 with 128, where the weights alone are 27).  One row of 1024 -> 4096, weights in HBM:
-// 4.5 us a call, 5.2 without sending for them before the turn.
+// steps of both weights, and of x where it is up to eight rows, before it multiplies any; 128 registers a thread hold them.  One row of
+// 4096 -> 12288 35 us, where the weights alone are 30 (with 64 registers, which spill, a sixth longer); of 1024 -> 4096, weights in HBM, 4.5 us a
+// call, 5.2 without sending for them before the turn.
 struct FewGatedArgs {
   const void* x;
   int64_t ldx;
