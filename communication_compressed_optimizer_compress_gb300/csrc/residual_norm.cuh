@@ -943,42 +943,49 @@ static __global__ void __launch_bounds__(kWideThreads) k_rn_param_wide(const Res
 }
 
 // The parameters' gradients from the four sums of each part, added in a fixed order: a block has eight columns (a sector of a
-// part's row), 128 threads to each of them.  Bound by latency: 3 us of a call behind the rows' kernel.
+// part's row), an eighth of its threads to each of them.  Bound by latency: 1024 threads read 152 parts in two steps where every block has an SM,
+// 256 in five where there are more (a call of 8192 x 2048: 47.9 us with 1024, 46.6 with 256; of 16384 x 1024: 36.5 and 38.3).
 struct ParamGrads {
   void *dgamma, *dbeta, *dblock_gamma, *dblock_beta, *dgate;
 };
-template <typename G>
-static __global__ void __launch_bounds__(1024) k_rn_params(const float* __restrict__ part, int64_t parts, int cols, const float* __restrict__ block_gamma,
-                                                           const float* __restrict__ block_beta, const float* __restrict__ gate, const ParamGrads out) {
-  __shared__ float red[4][8][129], sums[4][8];
+template <typename G, int THREADS>
+static __global__ void __launch_bounds__(THREADS) k_rn_params(const float* __restrict__ part, int64_t parts, int cols, const float* __restrict__ block_gamma,
+                                                              const float* __restrict__ block_beta, const float* __restrict__ gate, const ParamGrads out) {
+  constexpr int kRows = THREADS / 8;
+  __shared__ float red[THREADS / 32][32];
   const int col = threadIdx.x & 7, row = threadIdx.x >> 3, c = blockIdx.x * 8 + col;
   const bool need[4] = {out.dgamma != nullptr, out.dbeta != nullptr, out.dblock_gamma || out.dgate, out.dblock_beta || (out.dgate && block_beta)};
   in_turn();
   float s[4] = {};
   if (c < cols) {
-    for (int64_t p = row; p < parts; p += 128) {
+#pragma unroll 2
+    for (int64_t p = row; p < parts; p += kRows) {
       const float* q = part + p * 4 * cols + c;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (need[k]) s[k] += q[(int64_t)k * cols];
     }
   }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) red[k][col][row] = s[k];
+  for (int k = 0; k < 4; ++k) {
+    s[k] += __shfl_xor_sync(0xffffffffu, s[k], 8);
+    s[k] += __shfl_xor_sync(0xffffffffu, s[k], 16);
+  }
+  red[warp][lane] = lane < 16 ? (lane < 8 ? s[0] : s[1]) : (lane < 24 ? s[2] : s[3]);  // eight columns of each kind
   __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;  // a warp's kind and column
-  const float* q = red[warp >> 3][warp & 7];
-  const float total = warp_sum(q[lane] + q[lane + 32] + (q[lane + 64] + q[lane + 96]));
-  if (lane == 0) sums[warp >> 3][warp & 7] = total;
-  __syncthreads();
-  const int o = blockIdx.x * 8 + threadIdx.x;
-  if (threadIdx.x >= 8 || o >= cols) return;
-  const float a = sums[2][threadIdx.x], b = sums[3][threadIdx.x], at = gate ? gate[o] : 1.0f;
-  if (out.dgamma) static_cast<G*>(out.dgamma)[o] = from_f<G>(sums[0][threadIdx.x]);
-  if (out.dbeta) static_cast<G*>(out.dbeta)[o] = from_f<G>(sums[1][threadIdx.x]);
-  if (out.dblock_gamma) static_cast<G*>(out.dblock_gamma)[o] = from_f<G>(a * at);
-  if (out.dblock_beta) static_cast<G*>(out.dblock_beta)[o] = from_f<G>(b * at);
-  if (out.dgate) static_cast<G*>(out.dgate)[o] = from_f<G>(block_gamma ? fmaf(a, block_gamma[o], block_beta ? b * block_beta[o] : 0.0f) : a);
+  if (warp != 0) return;
+  float total = 0.0f;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) total += red[w][lane];
+  const float dbeta = __shfl_sync(0xffffffffu, total, 8 + col), a = __shfl_sync(0xffffffffu, total, 16 + col), b = __shfl_sync(0xffffffffu, total, 24 + col);
+  if (lane >= 8 || c >= cols) return;
+  const float at = gate ? gate[c] : 1.0f;
+  if (out.dgamma) static_cast<G*>(out.dgamma)[c] = from_f<G>(total);
+  if (out.dbeta) static_cast<G*>(out.dbeta)[c] = from_f<G>(dbeta);
+  if (out.dblock_gamma) static_cast<G*>(out.dblock_gamma)[c] = from_f<G>(a * at);
+  if (out.dblock_beta) static_cast<G*>(out.dblock_beta)[c] = from_f<G>(b * at);
+  if (out.dgate) static_cast<G*>(out.dgate)[c] = from_f<G>(block_gamma ? fmaf(a, block_gamma[c], block_beta ? b * block_beta[c] : 0.0f) : a);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -1121,10 +1128,13 @@ cudaError_t rn_backward(ResidualBackward a, const ParamGrads& g, int32_t grad_dt
     e = a.cols > kBackwardCols ? by(std::integral_constant<int, 512>{}, std::true_type{}) : with_threads(a.cols, [&](auto tpr) { return by(tpr, std::false_type{}); });
   }
   if (e != cudaSuccess || !params) return e;
-  auto finish = [&](auto* kernel) {
-    return launch_after(kernel, (unsigned)ceil_div(a.cols, 8), 1024, s, a.part, parts, a.cols, a.block_gamma, a.block_beta, a.gate, g);
+  auto finish = [&](auto g0) {
+    using G = decltype(g0);
+    const unsigned blocks = (unsigned)ceil_div(a.cols, 8);
+    if ((int)blocks <= sm_count()) return launch_after(k_rn_params<G, 1024>, blocks, 1024, s, a.part, parts, a.cols, a.block_gamma, a.block_beta, a.gate, g);
+    return launch_after(k_rn_params<G, 256>, blocks, 256, s, a.part, parts, a.cols, a.block_gamma, a.block_beta, a.gate, g);
   };
-  return grad_dtype == ONEBIT_F32 ? finish(k_rn_params<float>) : grad_dtype == ONEBIT_F16 ? finish(k_rn_params<__half>) : finish(k_rn_params<__nv_bfloat16>);
+  return grad_dtype == ONEBIT_F32 ? finish(float{}) : grad_dtype == ONEBIT_F16 ? finish(__half{}) : finish(__nv_bfloat16{});
 }
 
 }  // namespace layers
