@@ -150,6 +150,9 @@ cudaError_t forward(const onebit_gated_linear_t& a, Space& ws, cudaStream_t s, b
   const ProductPlan plan = plan_product(shape, sm_count());
   Readable copies;
   const Operand x = copies.take(ws, a.x, a.ldx, a.rows, a.in), w = copies.take(ws, a.w, a.ldw, 2 * a.inner, a.in);
+  // the bias's halves as rows of 16-bit words: they start on 16 bytes, or their realigned copies do
+  const bool in_epilogue = plan.splits == 1 && a.bias;
+  const Operand bias = in_epilogue ? copies.take(ws, a.bias, 2 * a.inner, 2, 2 * a.inner) : Operand{};
   const Partials part = take_partials(ws, plan, a.rows, 2 * a.inner);
   if (!run) return cudaSuccess;
   cudaError_t err = copies.run(s);
@@ -159,9 +162,8 @@ cudaError_t forward(const onebit_gated_linear_t& a, Space& ws, cudaStream_t s, b
     auto go = [&](auto ctas, auto act, auto keep) {
       GatedEpilogue<T, decltype(act)::value, decltype(keep)::value> e{};
       T* z = static_cast<T*>(a.z);
-      e.bias = a.bias;
+      if (in_epilogue) e.gate_bias = static_cast<const float*>(bias.p), e.up_bias = e.gate_bias + bias.ld / 2;
       e.gate_scales = a.gate_scales, e.up_scales = a.up_scales;
-      e.vec_bias = aligned(a.bias, 16) && a.inner % 4 == 0;
       e.blocks = (int)blocks, e.act = a.activation, e.keep = a.z ? kKeptValue : a.gate_codes ? kKeptCodes : kKeptNone;
       cudaError_t r = make_output(&e.h, static_cast<T*>(a.h), a.rows, a.inner, a.ldh);
       if (r == cudaSuccess) r = make_output(&e.gate, z, a.rows, a.inner, a.ldz);

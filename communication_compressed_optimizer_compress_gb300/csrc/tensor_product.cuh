@@ -493,9 +493,9 @@ __device__ __forceinline__ void load_codes(char* staging, uint32_t (&v)[8], cons
 template <int ACT>
 __device__ __forceinline__ ActConsts shared_consts(const f2* consts) {
   ActConsts k;
-  if (ACT == ONEBIT_ACT_GELU || ACT == ONEBIT_ACT_GELU_TANH || ACT == ONEBIT_ACT_SILU) {
+  if (ACT == ONEBIT_ACT_GELU || ACT == ONEBIT_ACT_GELU_TANH) {
 #pragma unroll
-    for (int i = 0; i < (ACT == ONEBIT_ACT_SILU ? 2 : kActConsts); i += 2)
+    for (int i = 0; i < kActConsts; i += 2)
       asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(k.k[i]), "=l"(k.k[i + 1]) : "r"(smem_addr(consts + i)));
   }
   return k;
@@ -809,14 +809,13 @@ struct GatedEpilogue {
   static constexpr bool kFold = false;
   static constexpr bool kGated = true;
   static constexpr int kStaging = kStagingBytes;
-  const float* bias;
+  const float *gate_bias, *up_bias;  // on 16 bytes, read by four columns; NULL: none
   Output<T> h, gate, up;  // gate, up: z's halves (kKeptValue)
   Output<int8_t> gate_codes, up_codes;
   float *gate_scales, *up_scales;
   int blocks;
   int act;
   int keep;
-  bool vec_bias;  // on 16 bytes, and a multiple of four columns
 
   __device__ __forceinline__ int keeps() const { return KEEP == kAny ? keep : KEEP; }
   // 16 pairs of columns, from column c of the layer on, `from` in tensor memory
@@ -830,17 +829,11 @@ struct GatedEpilogue {
     else tmem_hold16(v);
 #pragma unroll
     for (int i = 0; i < PAIRS; ++i) z[i] = pair(v[2 * i], v[2 * i + 1]);
-    if (!bias) return;
-    // (the same address in every lane)
-    if (vec_bias) {
+    if (!b) return;
 #pragma unroll
-      for (int i = 0; i < PAIRS; i += 2) {
-        const float4 t = c + 2 * i < cols ? __ldg(reinterpret_cast<const float4*>(b + c + 2 * i)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        z[i] = add2(z[i], pair(t.x, t.y)), z[i + 1] = add2(z[i + 1], pair(t.z, t.w));
-      }
-    } else {  // past the last column nothing is kept: any value does
-#pragma unroll
-      for (int i = 0; i < PAIRS; ++i) z[i] = add2(z[i], pair(__ldg(b + min(c + 2 * i, cols - 1)), __ldg(b + min(c + 2 * i + 1, cols - 1))));
+    for (int i = 0; i < PAIRS; i += 2) {  // (the same address in every lane)
+      const float4 t = c + 2 * i < cols ? __ldg(reinterpret_cast<const float4*>(b + c + 2 * i)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      z[i] = add2(z[i], pair(t.x, t.y)), z[i + 1] = add2(z[i + 1], pair(t.z, t.w));
     }
   }
   __device__ __forceinline__ BlockScale scale_of(uint32_t from, const float* b, int c, int cols) const {
@@ -863,7 +856,7 @@ struct GatedEpilogue {
   }
   // act(g) u of eight pairs, u's in z; out h
   template <int A>
-  __device__ __forceinline__ void gated(const f2* consts, const f2 (&g)[8], const f2* u, uint32_t* v) const {
+  __device__ __forceinline__ void gated(const f2 (&g)[8], const f2* u, uint32_t* v) const {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       f2 a, s;
@@ -872,10 +865,9 @@ struct GatedEpilogue {
     }
   }
   template <int HALF, class Release>
-  __device__ __forceinline__ void run(uint32_t at, int group, Release&& release, const f2* consts, int64_t row0, int64_t rows, int col0, int cols,
-                                      char* staging, int& turn) const {
+  __device__ __forceinline__ void run(uint32_t at, int group, Release&& release, int64_t row0, int64_t rows, int col0, int cols, char* staging, int& turn) const {
     const uint32_t mine = at + group * 32;
-    const float *bg = bias, *bu = bias + cols;
+    const float *const bg = gate_bias, *const bu = up_bias;
     uint32_t v[16], cu[8], cg[8];
     float inv_g = 0.0f, inv_u = 0.0f;
     bool plain = true;  // no value of the warp's blocks is infinite or NaN
@@ -914,12 +906,12 @@ struct GatedEpilogue {
 #pragma unroll
         for (int i = 0; i < 4; ++i) cg[4 * q + i] = codes4_finite(g[2 * i], g[2 * i + 1], inv_g);
       }
-      if constexpr (ACT != kAny) gated<ACT>(consts, g, u + 8 * q, v + 8 * q);
-      else if (act == ONEBIT_ACT_NONE) gated<ONEBIT_ACT_NONE>(consts, g, u + 8 * q, v + 8 * q);
-      else if (act == ONEBIT_ACT_RELU) gated<ONEBIT_ACT_RELU>(consts, g, u + 8 * q, v + 8 * q);
-      else if (act == ONEBIT_ACT_GELU) gated<ONEBIT_ACT_GELU>(consts, g, u + 8 * q, v + 8 * q);
-      else if (act == ONEBIT_ACT_GELU_TANH) gated<ONEBIT_ACT_GELU_TANH>(consts, g, u + 8 * q, v + 8 * q);
-      else gated<ONEBIT_ACT_SILU>(consts, g, u + 8 * q, v + 8 * q);
+      if constexpr (ACT != kAny) gated<ACT>(g, u + 8 * q, v + 8 * q);
+      else if (act == ONEBIT_ACT_NONE) gated<ONEBIT_ACT_NONE>(g, u + 8 * q, v + 8 * q);
+      else if (act == ONEBIT_ACT_RELU) gated<ONEBIT_ACT_RELU>(g, u + 8 * q, v + 8 * q);
+      else if (act == ONEBIT_ACT_GELU) gated<ONEBIT_ACT_GELU>(g, u + 8 * q, v + 8 * q);
+      else if (act == ONEBIT_ACT_GELU_TANH) gated<ONEBIT_ACT_GELU_TANH>(g, u + 8 * q, v + 8 * q);
+      else gated<ONEBIT_ACT_SILU>(g, u + 8 * q, v + 8 * q);
     }
     if (keeps() != kKeptCodes) {
       put_rows(staging, turn, v, h, row0, rows, col0, cols);
@@ -1081,7 +1073,7 @@ struct GatedGradEpilogue {
     for (int j = 0; j < kCols / 8; ++j) part<A>(d, a, j, chunk + j, sg, su, staging);
   }
   template <class Load, class Release>
-  __device__ __forceinline__ void run(Ahead& a, Load&& load, Release&& release, const f2* consts, int64_t row0, int64_t rows, int col0, int cols,
+  __device__ __forceinline__ void run(Ahead& a, Load&& load, Release&& release, const f2*, int64_t row0, int64_t rows, int col0, int cols,
                                       char* staging) const {
     const int64_t row = row0 + (threadIdx.x & 31);
     float sg = 0.0f, su = 0.0f;
@@ -1203,9 +1195,7 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
     *gave_up = 0;
 #pragma unroll
     for (int i = 0; i < kActConsts; ++i)
-      consts[i] = splat(E.act == ONEBIT_ACT_GELU   ? act_const(ONEBIT_ACT_GELU, i)
-                        : E.act == ONEBIT_ACT_SILU ? act_const(ONEBIT_ACT_SILU, i)
-                                                   : act_const(ONEBIT_ACT_GELU_TANH, i));
+      consts[i] = splat(E.act == ONEBIT_ACT_GELU ? act_const(ONEBIT_ACT_GELU, i) : act_const(ONEBIT_ACT_GELU_TANH, i));
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc<CTAS>(smem_addr((const void*)tmem_ptr), kTmemCols);
@@ -1247,7 +1237,7 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
       if constexpr (Epilogue::kGated) {
         if (!(ok = ready())) break;
         const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + acc * kTileN;
-        if (inside) E.template run<kTileN / 2>(at, group, release, consts, row0, P.m, col0, P.n, staging, turn);
+        if (inside) E.template run<kTileN / 2>(at, group, release, row0, P.m, col0, P.n, staging, turn);
         else release();
       } else if constexpr (Epilogue::kFold) {
         f2 c[2][16];

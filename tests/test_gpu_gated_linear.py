@@ -184,3 +184,21 @@ def test_tensors_that_require_a_gradient():
         with torch.no_grad():
             call()
         t.requires_grad_(False)
+
+
+@pytest.mark.parametrize("offset", [1, 2, 3, 4])
+@pytest.mark.parametrize("shape", [(8, 64, 40), (300, 264, 136), (300, 264, 130), (2500, 264, 520), (512, 4096, 256)], ids=str)
+def test_a_bias_inside_a_flat_buffer(shape, offset):
+    """The bias needs no more than its own type's alignment, whatever its offset, and nothing around it enters a result."""
+    rows, k, n = shape
+    gen = base._gen(rows + n)
+    x, w = base._randn(gen, rows, k, dtype=BF16), base._randn(gen, 2 * n, k, dtype=BF16, scale=0.1)
+    flat = torch.full((2 * n + 8,), float("nan"), device="cuda")
+    b = flat[offset: offset + 2 * n]
+    b.copy_(base._randn(gen, 2 * n))
+    h, g, u = ref.gated(x, w, b, L.ACT_SILU)
+    for keep in KEEP:
+        got = L.gated_linear(x, w, b, L.ACT_SILU, keep=keep)
+        ref.check(got if keep is None else got[0], h, BF16, "h")
+        if keep == "checkpoint":
+            _check_checkpoints(got[1], g[0], u[0], g[1], u[1])
