@@ -492,8 +492,13 @@ struct DropoutArgs {
       require(t.scalar_type() == at::kLong && t.numel() == 2 && t.is_contiguous() && t.device() == like.device());
       key = static_cast<const int64_t*>(t.data_ptr());
     }
-    const int s = integer(site_);  // (larger ones: layers.py)
-    require(s >= 0);
+    require(PyLong_Check(site_));
+    const unsigned long s = PyLong_AsUnsignedLong(site_);
+    if (s == (unsigned long)-1 && PyErr_Occurred()) {
+      PyErr_Clear();
+      throw Decline{};
+    }
+    require(s <= 0xffffffffu);
     site = (uint32_t)s;
   }
 };

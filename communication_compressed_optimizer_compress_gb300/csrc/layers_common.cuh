@@ -190,8 +190,8 @@ __device__ __forceinline__ void activate(const ActConsts& c, f2 z2, f2& value, f
     }
   }
 }
-// The same without registers for the constants, for an epilogue that has none left: literals, and gelu's ten pairs as those of
-// single operations (seven instructions a pair more).
+// The same without registers for the constants, for an epilogue that has none left: literals, and gelu's ten pairs (where that is the
+// form that does not spill, the tanh form's five too) as those of single operations, seven instructions a pair more.
 __device__ __forceinline__ float2 gelu_single(float z) {  // value and slope
   constexpr int A = ONEBIT_ACT_GELU;
   const float a = magnitude6(z);
@@ -201,10 +201,16 @@ __device__ __forceinline__ float2 gelu_single(float z) {  // value and slope
   const float tail = exp2_fast(p), m = fmaf(a * act_const(A, 8), exp2_fast(a * a * act_const(A, 7)), act_const(A, 9) - tail);
   return make_float2(fmaf(-a, tail, fmaxf(z, 0.0f)), copysignf(m, z) + act_const(A, 9));
 }
-template <int ACT>
+__device__ __forceinline__ float2 gelu_tanh_single(float z) {
+  constexpr int A = ONEBIT_ACT_GELU_TANH;
+  const float c = held40(z), zz = c * c, s = rcp_fast(exp2_fast(c * fmaf(zz, act_const(A, 0), act_const(A, 1))) + 1.0f);
+  return make_float2(max_nan(z, -40.0f) * s, fmaf(c * s * (1.0f - s), fmaf(zz, act_const(A, 3), act_const(A, 4)), s));
+}
+template <int ACT, bool SINGLE_TANH = false>
 __device__ __forceinline__ void activate_lean(f2 z2, f2& value, f2& slope) {
-  if constexpr (ACT == ONEBIT_ACT_GELU) {
-    const float2 z = halves(z2), lo = gelu_single(z.x), hi = gelu_single(z.y);
+  if constexpr (ACT == ONEBIT_ACT_GELU || (ACT == ONEBIT_ACT_GELU_TANH && SINGLE_TANH)) {
+    const float2 z = halves(z2), lo = ACT == ONEBIT_ACT_GELU ? gelu_single(z.x) : gelu_tanh_single(z.x),
+                 hi = ACT == ONEBIT_ACT_GELU ? gelu_single(z.y) : gelu_tanh_single(z.y);
     value = pair(lo.x, hi.x), slope = pair(lo.y, hi.y);
   } else {
     activate<ACT, true, true>(literal_consts<ACT>(), z2, value, slope);

@@ -1043,23 +1043,21 @@ struct GatedGradEpilogue {
     uint32_t vg[4], vu[4], vh[4];
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {
-      f2 g[2], u[2];
-      if (by_codes()) {
-        values4<T>(a.g[2 * j + i / 2], sg, g);
-        values4<T>(a.u[2 * j + i / 2], su, u);
-      } else {
-        constexpr int kLast = kWords - 1;
-        g[0] = widen<T>(a.g[(4 * j + i) & kLast]), g[1] = widen<T>(a.g[(4 * j + i + 1) & kLast]);
-        u[0] = widen<T>(a.u[(4 * j + i) & kLast]), u[1] = widen<T>(a.u[(4 * j + i + 1) & kLast]);
-      }
+      constexpr int kLast = kWords - 1;
+      f2 g[2], v[2], s[2];
+      if (by_codes()) values4<T>(a.g[2 * j + i / 2], sg, g);
+      else g[0] = widen<T>(a.g[(4 * j + i) & kLast]), g[1] = widen<T>(a.g[(4 * j + i + 1) & kLast]);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) activate_lean<A, KEPT == kKeptCodes>(g[p], v[p], s[p]);
+      f2 u[2];  // (not before it is needed)
+      if (by_codes()) values4<T>(a.u[2 * j + i / 2], su, u);
+      else u[0] = widen<T>(a.u[(4 * j + i) & kLast]), u[1] = widen<T>(a.u[(4 * j + i + 1) & kLast]);
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        f2 v, s;
-        activate_lean<A>(g[p], v, s);
         const f2 dh = d[4 * j + i + p];
-        vh[i + p] = narrow<T>(mul2(v, u[p]));
-        vu[i + p] = narrow<T>(mul2(dh, v));
-        vg[i + p] = narrow<T>(mul2(mul2(dh, u[p]), s));
+        vh[i + p] = narrow<T>(mul2(v[p], u[p]));
+        vu[i + p] = narrow<T>(mul2(dh, v[p]));
+        vg[i + p] = narrow<T>(mul2(mul2(dh, u[p]), s[p]));
       }
     }
     if (j == 0 && chunk == 0) staging_free();  // the boxes sent last have left

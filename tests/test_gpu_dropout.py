@@ -122,7 +122,10 @@ def test_both_ways_from_python_agree(both, pad):  # noqa: F811
         x = base._randn(gen, 33, 264 + pad, dtype=dtype)[:, :264]
         both(lambda: L.dropout(x, 0.2, key, 3))
         both(lambda: L.dropout(x, 0.0, None))
-    big = L.dropout(x, 0.2, key, 2 ** 31)  # not the binding's case
+    big = both(lambda: L.dropout(x, 0.2, key, 2 ** 31))
+    for site in (-1, 2 ** 32, 2 ** 70):  # the binding leaves them to layers.py
+        with pytest.raises(ValueError, match="site"):
+            L.dropout(x, 0.2, key, site)
     assert torch.equal(big != 0, ref.stays(33, 264, 0.2, key, 2 ** 31) & (x != 0))
     y = L.dropout(x.contiguous()[None], 0.2, key, 3)
     assert y.shape == (1, 33, 264) and torch.equal(y[0], L.dropout(x, 0.2, key, 3))
