@@ -492,7 +492,7 @@ enum BlockSide { kBlockPlain = 0, kBlockGate = 1, kBlockNorm = 2 };
 // One pass over the rows: what comes through the norm before the next block joins ds to t, which goes on through mask, gate and the norm
 // behind the block; a thread adds up its columns' part of the parameters' gradients.  Bound by latency, 16 warps an SM: 16384 x 1024 bf16 36.5
 // us with layer norm and dropout, parameters' sums included (168 MB at 4.6 TB/s), 33 with RMS norm; 8192 x 2048 f16 with RMS norms on both sides,
-// gate and dropout 47.9 (62.6 with the means' sums).  640 threads of 96 registers are no faster.
+// gate and dropout 46.3 (the means' sums cost 15 more).  640 threads of 96 registers are no faster.
 template <typename T, int TPR, bool VEC, int SIDE, bool CLUSTER, bool RMS>
 static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(const ResidualBackward A) {
   constexpr int kGroups = kBackwardThreads / TPR, kStages = kBackwardStages<T, VEC>;
