@@ -809,6 +809,7 @@ struct GatedEpilogue {
   static constexpr bool kFold = false;
   static constexpr bool kGated = true;
   static constexpr int kStaging = kStagingBytes;
+  static constexpr int kGateCodes = 32 * 32 * sizeof(T), kUpCodes = kGateCodes + 32 * 32;  // boxes behind that of h
   const float *gate_bias, *up_bias;  // on 16 bytes, read by four columns; NULL: none
   Output<T> h, gate, up;  // gate, up: z's halves (kKeptValue)
   Output<int8_t> gate_codes, up_codes;
@@ -924,14 +925,14 @@ struct GatedEpilogue {
     if (h.by_tma && gate_codes.by_tma && up_codes.by_tma) {  // one fence between staging and copies
       staging_free();
       stage_rows<T>(staging, v);
-      stage_codes(staging + 2048, cg);
-      stage_codes(staging + 3072, cu);
+      stage_codes(staging + kGateCodes, cg);
+      stage_codes(staging + kUpCodes, cu);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if ((threadIdx.x & 31) == 0) {
         copy_out(&h.map, smem_addr(staging), col0, (int32_t)row0);
-        copy_out(&gate_codes.map, smem_addr(staging + 2048), col0, (int32_t)row0);
-        copy_out(&up_codes.map, smem_addr(staging + 3072), col0, (int32_t)row0);
+        copy_out(&gate_codes.map, smem_addr(staging + kGateCodes), col0, (int32_t)row0);
+        copy_out(&up_codes.map, smem_addr(staging + kUpCodes), col0, (int32_t)row0);
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       }
     } else {
