@@ -481,6 +481,7 @@ int sm_count();  // of the current device
 // What a kernel that gave up waiting leaves, in the current device's status word (NULL: a CUDA error).
 constexpr unsigned kStatusGaveUp = 1u;
 unsigned int* status_word();
+uint32_t stall_bytes();  // the test hook's
 
 inline int dtype_size(int32_t dtype) { return dtype == ONEBIT_F32 ? 4 : 2; }
 inline bool dtype_ok(int32_t dtype) { return dtype >= ONEBIT_F32 && dtype <= ONEBIT_BF16; }

@@ -28,6 +28,7 @@ struct ResidualForward {
   bool layer;
   float inv_cols, eps, scale;
   unsigned int* status;
+  uint32_t stall_tx;  // (clusters) test hook: bytes that every sum waits for and no block sends (normally 0)
 };
 
 struct ResidualBackward {
@@ -52,6 +53,7 @@ struct ResidualBackward {
   float inv_cols, scale;
   float* part;  // the parameters' partial sums
   unsigned int* status;
+  uint32_t stall_tx;
   float* sums;  // (rows read again:) each row's two sums behind the norm before the next block
 };
 
@@ -221,32 +223,35 @@ __device__ __forceinline__ uint32_t cluster_blocks() {
   return r;
 }
 __device__ __forceinline__ void cluster_barrier() { asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// no block leaves while another may still send to it
-__device__ __forceinline__ void cluster_end() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
 constexpr int kClusterMost = 8;
 
 // The blocks' sums of a row to its sum, added in the blocks' order: each block sends its own to all, who wait for the bytes.  (With
 // the cluster's barrier instead, whose release waits for the rows that were stored before it, a row of 8192 columns took 2 us a sum.)
 // Two sets of places take turns: a block sends to one of them again only after it has had what the others sent behind their reading it.
-// A wait ends after about a second, and all that follow at once; the status word says so.
+//
+// A wait ends after about a second, or as soon as another thread of the block has given up the same one; the status word says so.  The
+// phase that was waited for stays open, so its barrier is not touched again: behind the barrier of the block's next sums every thread sees
+// which wait was given up, and from there on none arrives, sends or waits: what is left of the rows is done on sums that say nothing.
+// The other blocks of the cluster then miss what this one would have sent, and their next wait ends the same way.  (Each of the three
+// has the condition to itself: behind one branch around them, or with the rows left, backward's loads for the next row no longer overlap
+// the sums, and 4096 x 8192 with RMS norms on both sides takes 160 us for 111.)
 template <int N>
 struct ClusterSums {
   struct Shared {
     float from[2][kClusterMost][N];
     uint64_t bar[2];
-    int gave_up;
+    uint32_t gave_up;  // 0, or the number of the wait that ran out, from 1 on
   };
   Shared& m;
   unsigned int* status;
-  uint32_t rank, blocks, phase;
+  uint32_t stall, rank, blocks, count;
+  bool mine;  // this thread's wait ran out
   // by all threads, before the cluster's first barrier
-  __device__ __forceinline__ ClusterSums(Shared& shared, unsigned int* status_) : m(shared), status(status_), rank(cluster_rank()), blocks(cluster_blocks()), phase(0) {
+  __device__ __forceinline__ ClusterSums(Shared& shared, unsigned int* status_, uint32_t stall_)
+      : m(shared), status(status_), stall(stall_), rank(cluster_rank()), blocks(cluster_blocks()), count(0), mine(false) {
     if (threadIdx.x == 0) {
       for (int i = 0; i < 2; ++i) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(at(&m.bar[i])) : "memory");
-      *(volatile int*)&m.gave_up = 0;
+      *(volatile uint32_t*)&m.gave_up = 0;
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncwarp();
@@ -257,10 +262,15 @@ struct ClusterSums {
     asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
   }
+  // Behind the block's own sums, whose barrier all threads have just passed: all see the same wait before this one given up, or none.
+  // `turn` is the set of places, alternating from 0.
   __device__ __forceinline__ void operator()(float (&v)[N], int turn) {
-    const uint32_t bar = at(&m.bar[turn]);
-    if (threadIdx.x == 0) asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(blocks * N * 4) : "memory");
-    if (threadIdx.x < blocks) {
+    const uint32_t parity = count >> 1 & 1, bar = at(&m.bar[turn]);
+    ++count;
+    const uint32_t lost = *(volatile uint32_t*)&m.gave_up;
+    const bool live = lost == 0 || lost == count;  // (another thread may be giving up this very wait already)
+    if (live && threadIdx.x == 0) asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(blocks * N * 4 + stall) : "memory");
+    if (live && threadIdx.x < blocks) {
       uint32_t to, its;
       asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(at(&m.from[turn][rank][0])), "r"(threadIdx.x));
       asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(its) : "r"(bar), "r"(threadIdx.x));
@@ -269,15 +279,17 @@ struct ClusterSums {
         asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(to + 4 * i), "r"(__float_as_uint(v[i])), "r"(its) : "memory");
     }
     __syncwarp();
-    const uint32_t parity = phase >> turn & 1;
-    phase ^= 1u << turn;
-    if (!here(bar, parity)) {
+    if (live && !here(bar, parity)) {
       const long long t0 = clock64();
       while (!here(bar, parity)) {
-        if (*(volatile int*)&m.gave_up) break;
+        if (*(volatile uint32_t*)&m.gave_up) {
+          mine = true;
+          break;
+        }
         if (clock64() - t0 > 2000000000ll) {
-          *(volatile int*)&m.gave_up = 1;
+          *(volatile uint32_t*)&m.gave_up = count;
           atomicOr(status, kStatusGaveUp);
+          mine = true;
           break;
         }
       }
@@ -289,13 +301,25 @@ struct ClusterSums {
       for (uint32_t b = 1; b < blocks; ++b) v[i] += *(volatile float*)&m.from[turn][b][i];
     }
   }
+  // No block leaves while another may still send to it.  One that has had all that it waited for has nothing more coming; one
+  // that gave up stays for some ten milliseconds more behind all the cluster's last sends.
+  __device__ __forceinline__ void end() const {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+    if (mine) {
+      const long long t0 = clock64();
+      while (clock64() - t0 < 20000000ll) {
+      }
+    }
+  }
 };
 
 struct OneBlock {
   template <class Shared>
-  __device__ __forceinline__ OneBlock(Shared&, unsigned int*) {}
+  __device__ __forceinline__ OneBlock(Shared&, unsigned int*, uint32_t) {}
   template <int N>
   __device__ __forceinline__ void operator()(float (&)[N], int) const {}
+  __device__ __forceinline__ void end() const {}
 };
 
 // v becomes its distance from the mean, columns past the end stay 0; returns its squares' sum
@@ -359,7 +383,7 @@ static __global__ void __launch_bounds__(kForwardThreads<TPR>, kForwardBlocks<TP
   using Stream = RowStream<T, TPR, CH, VEC, 2 * NR, kStages, kThreads, NR>;
   Stream x(dynamic, 0, A.x, A.ldx, first, step, t, cols), b(dynamic, NR, A.block, A.ldblock, first, step, t, cols);
   const bool block = A.block != nullptr;
-  std::conditional_t<CLUSTER, ClusterSums<NR>, OneBlock> across(places, A.status);
+  std::conditional_t<CLUSTER, ClusterSums<NR>, OneBlock> across(places, A.status, A.stall_tx);
   if (CLUSTER) cluster_barrier();  // the other blocks are there to be sent to
   in_turn();
   if (first >= A.rows) return;     // (no barrier is the whole block's, and a cluster's blocks have the same rows)
@@ -479,7 +503,7 @@ static __global__ void __launch_bounds__(kForwardThreads<TPR>, kForwardBlocks<TP
     if (++stage == kStages) stage = 0;
   }
   copies_wait<0>();
-  if (CLUSTER) cluster_end();
+  across.end();
 }
 
 constexpr int kBackwardThreads = 512;  // of 128 registers: all that an SM has room for, so that it leaves one part
@@ -509,7 +533,7 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
   Stream dy(dynamic, 0, A.dy, A.lddy, first, step, t, cols), s(dynamic, 1, A.s, A.lds, first, step, t, cols),
       ds(dynamic, 2, A.ds, A.ldds, first, step, t, cols), b(dynamic, 3, A.block, A.ldblock, first, step, t, cols);
   const bool pre = A.gamma != nullptr, path = A.ds != nullptr;
-  std::conditional_t<CLUSTER, ClusterSums<kSums>, OneBlock> across(places, A.status);
+  std::conditional_t<CLUSTER, ClusterSums<kSums>, OneBlock> across(places, A.status, A.stall_tx);
   if (CLUSTER) cluster_barrier();  // the other blocks are there to be sent to
   in_turn();
   auto ahead = [&](int stage, int64_t r) {
@@ -634,7 +658,7 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
     if (++stage == kStages) stage = 0;
   }
   copies_wait<0>();
-  if (CLUSTER) cluster_end();
+  across.end();
   if (!A.part) return;
   // the upper half of the row groups hand their sums to the lower, until one has them
   constexpr int kPairs = kKinds * 4;
@@ -1077,6 +1101,7 @@ cudaError_t rn_forward(ResidualForward a, cudaStream_t s) {
   using std::integral_constant;
   using Two = integral_constant<int, 2>;
   if (a.cols > kForwardCols && !(a.status = status_word())) return cudaErrorUnknown;
+  a.stall_tx = stall_bytes();
   if (a.cols > kForwardCols) return by(integral_constant<int, 512>{}, Two{}, std::true_type{});
   if (a.cols > 4096) return by(integral_constant<int, 512>{}, Two{}, std::false_type{});
   return with_threads(a.cols, [&](auto tpr) { return by(tpr, integral_constant<int, 1>{}, std::false_type{}); });
@@ -1125,6 +1150,7 @@ cudaError_t rn_backward(ResidualBackward a, const ParamGrads& g, int32_t grad_dt
       return a.layer ? go(std::true_type{}, std::false_type{}) : go(std::true_type{}, std::true_type{});
     };
     if (a.cols > kBackwardCols && !(a.status = status_word())) return cudaErrorUnknown;
+    a.stall_tx = stall_bytes();
     e = a.cols > kBackwardCols ? by(std::integral_constant<int, 512>{}, std::true_type{}) : with_threads(a.cols, [&](auto tpr) { return by(tpr, std::false_type{}); });
   }
   if (e != cudaSuccess || !params) return e;

@@ -1397,7 +1397,6 @@ cudaError_t make_output(Output<T>* out, T* p, int64_t rows, int64_t cols, int64_
   out->by_tma = true;
   return make_output_map(&out->map, (int)sizeof(T), p, rows, cols, ld);
 }
-uint32_t stall_bytes();        // the test hook's
 
 struct ProductShape {
   int64_t m;

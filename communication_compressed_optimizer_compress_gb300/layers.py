@@ -337,7 +337,8 @@ def clear_status(stream=None):
 
 
 def set_fault_injection(kind: int, value: int = 0):
-    """Test hook of the whole process: FAULT_STALL_COPIES makes the following products' waits run out."""
+    """Test hook of the whole process: FAULT_STALL_COPIES makes the waits of the following products, and of residual norms of rows
+    that several blocks share, run out."""
     _check(_functions().onebit_layers_set_fault_injection(int(kind), int(value)), "onebit_layers_set_fault_injection")
 
 

@@ -335,8 +335,9 @@ onebit_status_t onebit_residual_norm_backward(const onebit_residual_norm_grad_t*
 onebit_status_t onebit_layers_get_status(onebit_stream_t stream);
 /* Clear the flag (enqueued on `stream`). */
 onebit_status_t onebit_layers_clear_status(onebit_stream_t stream);
-/* Test hook, of the whole process: with ONEBIT_FAULT_STALL_COPIES the products of the following calls
- * wait for `value` bytes (1..2^19) that no copy delivers, so that their limited waits run out.
+/* Test hook, of the whole process: with ONEBIT_FAULT_STALL_COPIES the products of the following calls, and their
+ * residual norms of rows that several blocks share, wait for `value` bytes (1..2^19) that nothing delivers, so
+ * that their limited waits run out.
  * ONEBIT_FAULT_NONE turns it off.  Nothing here makes the GPU fault. */
 onebit_status_t onebit_layers_set_fault_injection(int32_t kind, int64_t value);
 
