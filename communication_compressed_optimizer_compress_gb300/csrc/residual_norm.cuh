@@ -645,6 +645,7 @@ static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(cons
 #pragma unroll
           for (int e = 0; e < 4; ++e) d[e] = fma2(hat[e], m1, RMS ? mul2(d[e], splat(brs)) : fma2(d[e], splat(brs), m0));
         } else {
+          if (gen.threshold) gen.keep8(bits, hat);  // what forward dropped enters nothing, whatever it was
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             sum[kSums][e] = fma2(d[e], hat[e], sum[kSums][e]);
@@ -855,11 +856,14 @@ struct RowBackward {
     for (int e = 0; e < 4; ++e) v[e] = mul2(v[e], splat(A.scale));
     if (A.drop.threshold) gen.apply8(r * A.groups + c / 8, v);
   }
-  __device__ __forceinline__ void bhat(int c, f2 (&b)[4]) const {  // normalised behind a norm, else the block itself
+  // the block normalised, or without a norm behind it what stays of it: what forward dropped enters nothing, whatever it was
+  __device__ __forceinline__ void bhat(int c, f2 (&b)[4]) const {
     load(A.block, A.ldblock, c, b);
     if (A.block_gamma) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) b[e] = mul2(add2(b[e], splat(-block_mean)), splat(block_rstd));
+    } else if (gen.threshold) {
+      gen.keep8(gen.draw(r * A.groups + c / 8), b);
     }
   }
   // f = d gate block_gamma, from d; 0 past the end

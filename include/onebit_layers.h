@@ -279,7 +279,7 @@ onebit_status_t onebit_residual_norm_forward(const onebit_residual_norm_t* a, on
  *   dblock = e, or behind a norm with bhat = (block - block_mean) * block_rstd and f = e * block_gamma:
  *            block_rstd * (f [- sum(f)/cols] - bhat * sum(f*bhat)/cols);
  *   dgamma = sum over rows of dy*shat;  dbeta = sum of dy;  dblock_gamma = sum of e*bhat;  dblock_beta = sum of e;
- *   dgate = sum of d*n
+ *   dgate = sum of d*n                          (an element that dropout set to 0 adds nothing, whatever it was)
  * [..] with ONEBIT_NORM_LAYER.  s may be NULL without gamma, block without both block_gamma and gate.  dx: always.
  * dblock: NULL where there was no block (block, block_gamma, gate are then NULL and p is 0).  Each parameter's gradient,
  * cols values of grad_dtype, is there exactly where the parameter is: dgamma with gamma, dbeta with gamma and
