@@ -359,7 +359,7 @@ __device__ __forceinline__ float total(const f2 (&v)[CH][4]) {
 
 template <int TPR>
 constexpr int kForwardThreads = TPR > 128 ? TPR : 128;
-// Blocks an SM: 72 registers a thread where one group of columns of one row is held, 80 with a norm behind the block, 96 for two rows (a
+// Blocks that an SM has room for at least: 72 registers a thread where one group of columns of one row is held, 80 with a norm behind the block, 96 for two rows (a
 // norm behind the block: 128), else 128.
 template <int TPR, int CH, int NR, bool POST>
 constexpr int kForwardBlocks = (CH > 1 ? 512 : NR > 1 ? (POST ? 512 : 640) : POST ? 768 : 896) / kForwardThreads<TPR>;
@@ -368,8 +368,8 @@ constexpr int kForwardStages = sizeof(T) == 2 ? 3 : 2;
 
 // One pass over the rows: the block's statistics (where a norm stands behind it), its masked and gated values onto x, s's statistics, y.
 // Variances are summed about the mean, a second exchange behind the first.  NR rows at a time: two share the exchanges of their sums,
-// the barrier behind them and the reciprocal roots.  Bound by bytes where little is done (16384 x 1024 bf16 layer norm 22.9 us, RMS norm 22.1, 134
-// MB at 5.9 and 6.1 TB/s), else by issue (with dropout 25.4 to 29, with RMS norms on both sides, gate and dropout 26.1; odd rows of 1001 61).
+// the barrier behind them and the reciprocal roots.  16384 x 1024 bf16, over twelve placements in memory: layer norm 23.1 us and RMS norm
+// 22.4, 134 MB at 5.8 and 6.0 TB/s; with dropout 25.9 and 23.3, with RMS norms on both sides, gate and dropout 26.2; odd rows of 1001 61.6.
 template <typename T, int TPR, int CH, int NR, bool VEC, bool POST, bool CLUSTER>
 static __global__ void __launch_bounds__(kForwardThreads<TPR>, kForwardBlocks<TPR, CH, NR, POST>) k_rn_forward(const ResidualForward A) {
   static_assert(NR == 1 || (VEC && !CLUSTER), "two rows at a time: dense ones of one block");
@@ -1023,6 +1023,21 @@ inline unsigned at_most(int64_t want, int64_t per_sm) {
   const int64_t most = (int64_t)sm_count() * per_sm;
   return (unsigned)(want < most ? want : most);
 }
+// The blocks of a kernel that an SM holds at once, asked once for each device; `least` are what its launch bounds leave room for.
+struct Held {
+  std::atomic<int> blocks[64];
+  template <typename Kernel>
+  int operator()(Kernel* kernel, int threads, int bytes, int least) {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return least;
+    if ((n = blocks[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, bytes) != cudaSuccess || n < least)
+      return least;
+    blocks[dev].store(n, std::memory_order_relaxed);
+    return n;
+  }
+};
 // With `bytes` of dynamic shared memory, which a kernel is allowed once for each device, in clusters of `blocks`.
 template <typename Args>
 inline cudaError_t launch_rows(void (*kernel)(const Args), std::atomic<uint64_t>& ready, unsigned grid, int threads, int bytes, int blocks, cudaStream_t s,
@@ -1076,9 +1091,14 @@ auto with_threads(int64_t cols, F&& f) {
 template <typename T, int TPR, int CH, int NR, bool VEC, bool POST, bool CLUSTER>
 cudaError_t run_forward(const ResidualForward& a, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
-  const int blocks = CLUSTER ? cluster_for(a.cols, kForwardCols) : 1;
-  const int64_t most = (int64_t)sm_count() * kForwardBlocks<TPR, CH, NR, POST> / blocks, want = ceil_div(a.rows, kForwardThreads<TPR> / TPR * NR);
+  // As many blocks as the SMs hold, and no fewer: blocks come up while those of the kernel before leave, six to one SM then and four to another
+  // where six fit and the grid has five for each (16384 x 1024 bf16 layer norm with dropout, two rows at a time: 25.5 us or 30 from one
+  // call to the next).
+  static Held held{};
   constexpr int kThreads = kForwardThreads<TPR>, kBytes = RowStream<T, TPR, CH, VEC, 2 * NR, kForwardStages<T>, kThreads, NR>::kBytes;
+  const int blocks = CLUSTER ? cluster_for(a.cols, kForwardCols) : 1;
+  const int64_t per_sm = held(k_rn_forward<T, TPR, CH, NR, VEC, POST, CLUSTER>, kThreads, kBytes, kForwardBlocks<TPR, CH, NR, POST>);
+  const int64_t most = (int64_t)sm_count() * per_sm / blocks, want = ceil_div(a.rows, kForwardThreads<TPR> / TPR * NR);
   return launch_rows(k_rn_forward<T, TPR, CH, NR, VEC, POST, CLUSTER>, ready, (unsigned)(want < most ? want : most), kThreads, kBytes, blocks, s, a);
 }
 template <typename T>
@@ -1086,8 +1106,10 @@ cudaError_t rn_forward(ResidualForward a, cudaStream_t s) {
   if (a.cols > kForwardCols * kClusterMost) return launch_after(k_rn_forward_wide<T>, at_most(a.rows, 8), kWideThreads, s, a);
   auto on16 = [](const void* p, int64_t ld) { return aligned(p, 16) && (ld * (int64_t)sizeof(T)) % 16 == 0; };
   const bool vec = a.cols % 8 == 0 && on16(a.x, a.ldx) && on16(a.block, a.ldblock) && on16(a.s, a.lds) && on16(a.y, a.ldy);
-  // Two rows at a time where there are enough for all SMs and arithmetic, not bytes, bounds: with dropout or a norm behind the block (us
-  // for 16384 x 1024 bf16, one and two: layer norm with dropout 28.6, 25.4, with layer norms on both sides 30.7, 26.1, alone 22.9, 24.8).
+  // Two rows at a time where there are enough for all SMs and it gains, with dropout or a norm behind the block (us for bf16, one and two,
+  // medians over placements that differ by 1%: 16384 x 1024 with dropout, layer norm 28.7, 26.0, RMS norm 25.3, 23.4; layer norms on both sides
+  // 30.9, 26.1, RMS norms 23.3, 23.0; 8192 x 2048 layer norm with dropout 30.7, 24.6).  Not where it does not, alone (layer norm 23.2, 23.3, RMS
+  // norm 22.4, 22.2; 8192 x 2048 layer norm 23.3, 22.5).
   const bool two = a.drop.threshold || a.block_gamma;
   auto by = [&](auto tpr, auto ch, auto cluster) {
     constexpr int kTpr = decltype(tpr)::value, kCh = decltype(ch)::value;
