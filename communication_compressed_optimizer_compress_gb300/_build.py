@@ -98,7 +98,7 @@ def build(force: bool = False, verbose: bool = False, checked: bool = False) -> 
         o = os.path.join(bdir, src.replace(".cu", ".o"))
         objs.append(o)
         if force or _stale(o, [s, *hdrs, __file__]):
-            jobs.append([nvcc(), *flags, "-c", s, "-o", o])
+            jobs.append([nvcc(), *flags, "-Xptxas", "-v", "-c", s, "-o", o])
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -106,6 +106,9 @@ def build(force: bool = False, verbose: bool = False, checked: bool = False) -> 
             raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
         if verbose:
             print(r.stdout + r.stderr)
+        if cmd[-1].endswith(".o") and "-c" in cmd:  # each kernel's registers and spills, beside its object
+            with open(cmd[-1][:-2] + ".ptxas", "w") as f:
+                f.write(r.stdout + r.stderr)
 
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
         binding = ex.submit(build_binding, force)
