@@ -112,7 +112,7 @@ cudaError_t backward(const onebit_gated_linear_grad_t& a, Space& ws, cudaStream_
   onebit_linear_grad_t b{};
   b.dy = dy.p, b.lddy = dy.ld, b.x = h, b.ldx = ldh, b.dw = a.dw, b.db = a.db;
   b.rows = a.rows, b.in = a.inner, b.out = a.out, b.dtype = a.dtype, b.grad_dtype = a.grad_dtype;
-  return linear_backward(b, ws, s, run);
+  return linear_backward(b, ws, s, run, dy.p != a.dy);
 }
 cudaError_t backward(const onebit_gated_linear_grad_t& a, Space& ws, cudaStream_t s, bool run) {
   return a.dtype == ONEBIT_F16 ? backward<__half>(a, ws, s, run) : backward<__nv_bfloat16>(a, ws, s, run);

@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(256) k_colsum_part(const T* __restrict__ dy, i
 
 // Takes the workspace; with `run`, enqueues the work too.
 template <typename T>
-cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, bool run) {
+cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, bool run, bool padded) {
   const int sms = sm_count();
   const ProductShape sx{a.rows, a.in, a.out}, sw{a.out, a.in, a.rows};
   const Kept<T> v{static_cast<const T*>(a.x), a.ldx, a.codes, a.scales, (int)a.in, (int)ceil_div(a.in, kBlock)};
@@ -211,7 +211,7 @@ cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, b
       const dim3 grid((unsigned)ceil_div(a.out, 256), (unsigned)(chunks < 65535 ? chunks : 65535));
       const bool first = !a.dx && !a.dw;
       // eight columns at a time where the last eight lie inside the row (a realigned copy is padded to them)
-      err = vec16(p, dy.ld) && (a.out % 8 == 0 || p != a.dy)
+      err = vec16(p, dy.ld) && (a.out % 8 == 0 || padded || p != a.dy)
                 ? launch_after(k_colsum_part<T, true>, grid, 256, s, p, dy.ld, a.rows, (int)a.out, first, part, whole, a.grad_dtype)
                 : launch_after(k_colsum_part<T, false>, grid, 256, s, p, dy.ld, a.rows, (int)a.out, first, part, whole, a.grad_dtype);
       if (err == cudaSuccess && chunks > 1) err = sum_parts(a.grad_dtype, part, chunks, a.out, a.out, a.db, nullptr, s);
@@ -244,8 +244,8 @@ onebit_status_t backward_ok(const onebit_linear_grad_t* a) {
 
 }  // namespace
 
-cudaError_t linear_backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, bool run) {
-  return a.dtype == ONEBIT_F16 ? backward<__half>(a, ws, s, run) : backward<__nv_bfloat16>(a, ws, s, run);
+cudaError_t linear_backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, bool run, bool padded) {
+  return a.dtype == ONEBIT_F16 ? backward<__half>(a, ws, s, run, padded) : backward<__nv_bfloat16>(a, ws, s, run, padded);
 }
 
 }  // namespace layers

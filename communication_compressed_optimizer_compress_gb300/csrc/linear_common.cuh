@@ -165,8 +165,9 @@ inline onebit_status_t linear_shape_ok(int64_t rows, int64_t in, int64_t out, in
   return ONEBIT_OK;
 }
 
-// The linear layer's backward pass: takes the workspace; with `run`, enqueues the work too.
-cudaError_t linear_backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, bool run);
+// The linear layer's backward pass: takes the workspace; with `run`, enqueues the work too.  `padded`: dy is a realigned copy, whose
+// rows go on to whole groups of eight columns.
+cudaError_t linear_backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, bool run, bool padded = false);
 
 }  // namespace layers
 }  // namespace onebit
