@@ -27,7 +27,8 @@ __global__ void __launch_bounds__(256, kDenseBlocks) k_dropout_dense(const T* __
 }
 
 // Rows of any layout: WIDTH lanes have WIDTH groups of a row at a time, so that odd rows' vectors are put together from neighbouring
-// lanes' values.  Bound by latency and the shifts: 4099 x 1155 fp32 10.1 us (18.5 by single elements), 16384 x 1001 bf16 29.2 (45.4).
+// lanes' values.  Bound by the instructions of the shifts and the generator (65% of the issue slots, the ALU 59% in fp32 and 69% in 16 bits): 4099 x
+// 1155 fp32 10.1 us (18.5 by single elements), 16384 x 1001 bf16 29.3 (45.4).
 template <typename T, int WIDTH, bool VEC>
 __global__ void __launch_bounds__(256) k_dropout_rows(const T* __restrict__ x, int64_t ldx, int64_t rows, int cols, const Dropout d, T* __restrict__ y,
                                                       int64_t ldy) {

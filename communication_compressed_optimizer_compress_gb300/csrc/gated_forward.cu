@@ -58,8 +58,9 @@ __global__ void __launch_bounds__(256) k_finish_gated(Partials c, int64_t rows, 
 // Up to 32 rows, as generation meets them: the few-rows product (few_rows.cuh) with two weights to a column, the gate's and
 // the up projection's, whose sums meet in shared memory.  Bound by the weights' bytes and a launch's latency: a warp asks for kAhead
 // steps of both weights, and of x where it is up to eight rows, before it multiplies any; 128 registers a thread hold them.  One row of
-// 4096 -> 12288 35 us, where the weights alone are 30 (with 64 registers, which spill, a sixth longer); of 1024 -> 4096, weights in HBM, 4.5 us a
-// call, 5.2 without sending for them before the turn.
+// 4096 -> 12288 34 us, where the weights alone are 30 (with 64 registers, which spill, a sixth longer); of 1024 -> 4096, weights in HBM, 4.4 us a
+// call, 5.2 without sending for them before the turn.  Nine rows and more are bound by x, all of which every block of eight columns reads: 32 rows
+// of 4096 -> 12288 take 50 us, 403 MB out of the L2 beside the weights' 201, with L1's data pipe at 64% (one row 32%); sixteen 39.
 struct FewGatedArgs {
   const void* x;
   int64_t ldx;

@@ -369,7 +369,10 @@ constexpr int kForwardStages = sizeof(T) == 2 ? 3 : 2;
 // One pass over the rows: the block's statistics (where a norm stands behind it), its masked and gated values onto x, s's statistics, y.
 // Variances are summed about the mean, a second exchange behind the first.  NR rows at a time: two share the exchanges of their sums,
 // the barrier behind them and the reciprocal roots.  16384 x 1024 bf16, over twelve placements in memory: layer norm 23.1 us and RMS norm
-// 22.4, 134 MB at 5.8 and 6.0 TB/s; with dropout 25.9 and 23.3, with RMS norms on both sides, gate and dropout 26.2; odd rows of 1001 61.6.
+// 22.4, 134 MB at 5.8 and 6.0 TB/s; with dropout 25.9 and 23.3, with RMS norms on both sides, gate and dropout 26.2.  Then bound by
+// latency, with the 16 to 24 warps an SM that registers leave: 56 to 61% of the issue slots, no pipe above 45%.  Odd rows (1001: 61.5) are bound by
+// their shifts' instructions, 2.7 times as many: 68% of the issue slots, the ALU 59%.  fp32 (layer norms, gate, dropout: 62, floor 40) by latency
+// too (issue 40%): a copy of 16 of a thread's 32 bytes asks for half a sector, so that the L2 has three times the requests for twice the bytes.
 template <typename T, int TPR, int CH, int NR, bool VEC, bool POST, bool CLUSTER>
 static __global__ void __launch_bounds__(kForwardThreads<TPR>, kForwardBlocks<TPR, CH, NR, POST>) k_rn_forward(const ResidualForward A) {
   static_assert(NR == 1 || (VEC && !CLUSTER), "two rows at a time: dense ones of one block");
@@ -514,9 +517,11 @@ constexpr int kBackwardStages = sizeof(T) == 2 ? 3 : VEC ? 3 : 2;
 enum BlockSide { kBlockPlain = 0, kBlockGate = 1, kBlockNorm = 2 };
 // RMS: the norms are known to be without means (else A.layer says so), which saves their sums.
 // One pass over the rows: what comes through the norm before the next block joins ds to t, which goes on through mask, gate and the norm
-// behind the block; a thread adds up its columns' part of the parameters' gradients.  Bound by latency, 16 warps an SM: 16384 x 1024 bf16 36.5
-// us with layer norm and dropout, parameters' sums included (168 MB at 4.6 TB/s), 33 with RMS norm; 8192 x 2048 f16 with RMS norms on both sides,
-// gate and dropout 46.3 (the means' sums cost 15 more).  640 threads of 96 registers are no faster.
+// behind the block; a thread adds up its columns' part of the parameters' gradients.  Bound by latency, 16 warps an SM (49 to 59% of the issue
+// slots, no pipe above 49%): 16384 x 1024 bf16 36.2 us with layer norm and dropout, parameters' sums included (168 MB at 4.6 TB/s), 32.8 with RMS norm; 8192 x 2048
+// f16 with RMS norms on both sides, gate and dropout 46.1 (the means' sums cost 15 more).  640 threads of 96 registers are no faster.  Odd rows
+// (1001: 69) by their shifts' instructions, as forward; fp32 (RMS norm 80.5, floor 50; everything 105, floor 60) waits for its copies, issue 15 to
+// 29%, with four times the L2 requests of 16 bits for twice the bytes.
 template <typename T, int TPR, bool VEC, int SIDE, bool CLUSTER, bool RMS>
 static __global__ void __launch_bounds__(kBackwardThreads, 1) k_rn_backward(const ResidualBackward A) {
   constexpr int kGroups = kBackwardThreads / TPR, kStages = kBackwardStages<T, VEC>;
@@ -692,7 +697,7 @@ constexpr int kBackwardSmem = [] {
 
 // ------------------------------------------------------------------------------------------------
 // Rows wider than a cluster holds (65536 columns, backward 32768), read again for each step: one block a row, a thread eight columns at a
-// time by single elements.  Right at any width, not fast: as the form for all rows it took 135 us where forward now takes 25.
+// time by single elements.  Right at any width, not fast: as the form for all rows it took 135 us where forward now takes 26.
 constexpr int kWideThreads = 256;
 constexpr int kWideWarps = kWideThreads / 32;
 template <int N>

@@ -802,8 +802,10 @@ __device__ __forceinline__ void put_rows(char* staging, int& turn, const uint32_
 // h = act(g) u with [g | u] = d + bias, and what is kept of g and u.  A tile's accumulator holds the gate's columns in its
 // first half and the same columns of the up projection in its second, so that a lane has both; a warp has 32 columns of h.  For
 // the checkpoints' blocks of 64 columns it reads its neighbour's 32 too: once more out of tensor memory, which is cheaper than
-// two warps waiting for each other.  16384 x 1024 x 4096 bf16 with silu, us: nothing kept 146 (the library's product alone 143), values 179,
-// checkpoints 175: a tile's outputs pass through shared memory, whose bandwidth the products' operands nearly fill.
+// two warps waiting for each other.  16384 x 1024 x 4096 bf16 with silu, us, medians of three placements in memory that differ by 1%: nothing
+// kept 145 (the library's product alone 140), values 178, checkpoints 170.  With what is kept no unit is near its limit (values: tensor 67%,
+// reads and writes of shared memory's banks 20% each, the way to the L2 43%, DRAM 31%, issue 23%; nothing kept: tensor 82%): a warp's own chain, out of tensor memory,
+// through a box and away, once for each output, is then longer than the products of a tile.
 template <typename T, int ACT, int KEEP>
 struct GatedEpilogue {
   static constexpr bool kFold = false;
@@ -967,9 +969,10 @@ __device__ __noinline__ Words<WORDS> read_single(const E* p, int left) {
 // dz = [d u act'(g) | d act(g)], and h = act(g) u for the product of dw.  A lane has its row's 64 columns, sixteen at a time: it
 // reads g and u ahead, and what becomes of them goes to the staging buffer at once, a box of 32 columns for each of the three
 // results.  (Sent for into the L2 a tile before, they are read from DRAM twice: 159 us from values, 150 without.)  With 32 columns at a
-// time the registers spill, and a kernel that spills takes 150 to 165 us for 16384 x 4096 x 1024 from checkpoints, one that does not 130 to 140
-// (silu and gelu, either way round).  Bound by the latency of its reads and boxes: 37% tensor, 33% issue, 4 TB/s.  By 32-byte stores from
-// the registers instead of boxes it takes 175 us.
+// time the registers spill.  16384 x 4096 x 1024 bf16, us, medians of three placements in memory that differ by 1%: from checkpoints 131 (silu) to
+// 138 (gelu), from values 149 to 153; with h and from checkpoints 148.  No unit is near its limit (that form: tensor 38%, issue 34%, DRAM 48%, reads
+// and writes of shared memory's banks 15% each, the way to the L2 66%): bound by the latency of its reads, each lane's out of a row of its own, and of its boxes.
+// By 32-byte stores from the registers instead of boxes it takes 175 us from checkpoints.
 template <typename T, int ACT, int KEPT>
 struct GatedGradEpilogue {
   static constexpr bool kFold = false;
