@@ -77,7 +77,7 @@ cudaError_t backward(const onebit_gated_linear_grad_t& a, Space& ws, cudaStream_
         T* dz = static_cast<T*>(a.dz);
         cudaError_t r = make_output(&e.dgate, dz, a.rows, a.inner, a.lddz);
         if (r == cudaSuccess) r = make_output(&e.dup, dz + n, a.rows, a.inner, a.lddz);
-        if (r == cudaSuccess) r = make_output(&e.h, h, a.rows, a.inner, ldh);
+        if (r == cudaSuccess) r = make_output(&e.h, h, a.rows, a.inner, ldh, true);
         return r == cudaSuccess ? run_product_by<decltype(ctas)::value, false, true>(a.dtype, dy, w, shape, plan, e, s) : r;
       };
       using std::integral_constant;

@@ -151,7 +151,7 @@ cudaError_t backward(const onebit_linear_grad_t& a, Space& ws, cudaStream_t s, b
         e.wide_codes = aligned(a.codes, 32) && a.in % 32 == 0;
         e.vec_codes = aligned(a.codes, 16) && a.in % 16 == 0;
         cudaError_t r = make_output(&e.dx, static_cast<T*>(a.dx), a.rows, a.in, a.lddx);
-        if (r == cudaSuccess) r = make_output(&e.h, h, a.rows, a.in, ldh);
+        if (r == cudaSuccess) r = make_output(&e.h, h, a.rows, a.in, ldh, true);
         return r == cudaSuccess ? run_product_by<decltype(ctas)::value, false, true>(a.dtype, dy, w, sx, plan, e, s) : r;
       };
       using std::integral_constant;

@@ -145,7 +145,7 @@ inline Partials take_partials(Space& ws, const ProductPlan& plan, int64_t rows, 
 // Each split's tile rows are a multiple of the store boxes' (32): a box never reaches into the next split.
 inline cudaError_t to_partials(PlainEpilogue<float>* e, const Partials& q, int64_t cols) {
   e->split_rows = q.split_stride / q.ld;
-  return make_output(&e->out, const_cast<float*>(q.p), e->split_rows * q.splits, cols, q.ld);
+  return make_output(&e->out, const_cast<float*>(q.p), e->split_rows * q.splits, cols, q.ld, true);
 }
 
 template <typename F>

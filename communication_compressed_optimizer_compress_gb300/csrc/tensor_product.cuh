@@ -274,7 +274,7 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t src, 
   }
 }
 
-// A matrix that an epilogue writes: by TMA where its rows start on 16 bytes, element by element elsewhere.
+// A matrix that an epilogue writes: by TMA where its rows start and end on 16 bytes, element by element elsewhere.
 template <typename T>
 struct Output {
   CUtensorMap map;
@@ -1391,12 +1391,14 @@ __global__ void __launch_bounds__(kProductThreads<CTAS>, 1) k_product(const __gr
 cudaError_t make_map(CUtensorMap* map, int32_t dtype, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows);
 // An output matrix of elements of `size` bytes (1: codes), stored in boxes of 32 rows of 64 bytes (codes: 32).
 cudaError_t make_output_map(CUtensorMap* map, int size, const void* p, int64_t rows, int64_t cols, int64_t ld);
+// By TMA where rows start on 16 bytes and end on 16, too: a store writes the last 16 bytes of a row whole, also where the matrix ends
+// inside them.  `padded`: what lies there is the row's own padding, and may be written.
 template <typename T>
-cudaError_t make_output(Output<T>* out, T* p, int64_t rows, int64_t cols, int64_t ld) {
+cudaError_t make_output(Output<T>* out, T* p, int64_t rows, int64_t cols, int64_t ld, bool padded = false) {
   *out = Output<T>{};
   out->p = p;
   out->ld = ld;
-  if (!p || !aligned(p, 16) || ld * (int64_t)sizeof(T) % 16 != 0) return cudaSuccess;
+  if (!p || !aligned(p, 16) || ld * (int64_t)sizeof(T) % 16 != 0 || (!padded && cols * (int64_t)sizeof(T) % 16 != 0)) return cudaSuccess;
   out->by_tma = true;
   return make_output_map(&out->map, (int)sizeof(T), p, rows, cols, ld);
 }
