@@ -46,7 +46,7 @@ def _bounded(g, most):
 
 
 # few rows, single blocks, a cut contraction, pairs; on 16 bytes and off
-@pytest.mark.parametrize("rows,k,n", [(5, 64, 136), (20, 64, 136), (70, 64, 136), (70, 64, 131), (512, 4096, 256), (5000, 256, 1024), (5000, 256, 1027)], ids=str)
+@pytest.mark.parametrize("rows,k,n", [(5, 64, 136), (20, 64, 136), (70, 64, 136), (70, 64, 131), (512, 4096, 256), (2500, 264, 520), (2500, 264, 523)], ids=str)
 @pytest.mark.parametrize("dtype", [F16, BF16], ids=base.ids)
 def test_forward(rows, k, n, dtype):
     """x is 0, so that the bias alone is g and u."""
@@ -70,7 +70,7 @@ def test_forward(rows, k, n, dtype):
     assert L.get_status() == ob.OK
 
 
-@pytest.mark.parametrize("rows,n,out", [(70, 136, 64), (70, 131, 64), (512, 256, 4096), (5000, 1024, 256), (5000, 1027, 256)], ids=str)
+@pytest.mark.parametrize("rows,n,out", [(70, 136, 64), (70, 131, 64), (512, 256, 4096), (2500, 520, 264), (2500, 523, 264)], ids=str)
 @pytest.mark.parametrize("dtype", [F16, BF16], ids=base.ids)
 def test_backward(rows, n, out, dtype):
     gen = base._gen(rows + n)
